@@ -80,7 +80,7 @@ def draw(rng):
         P = rng.choice([1, 8, 32, 64])
         T = _log(rng, 1, 8192)
         H = 128 * rng.choice([2, 4, 5, 8, 11, 16, 20, 32, 40])
-        T = max(1, min(_odd(T), 6000 * 2048 // H))
+        T = max(1, min(_odd(T), 4900 * 2048 // H))
         c = _norm("", T, H, P, rng.choice(["f32", "bf16"]), rng.choice(["bf16", "bf16", "f32"]), rng.random() < 0.8,
                   rng.random() < 0.8)
         del c["name"]
