@@ -255,6 +255,98 @@ int block_decode_loop(const moestep_dims* dims, int R, int n_layers, const moest
                       float threshold, int max_rounds, int32_t* tokens, uint8_t* masked, int32_t* rounds,
                       void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention side of a layer.  The pages leave the token mixers' weights and
+ * controls unspecified; what follows are the operators that any such layer needs
+ * around the MoE step: a paged key-value cache, attention of a block of new
+ * tokens over it (bidirectional inside the block, [AIT 四], or causal), and the
+ * residual update with the norms before and after a block.
+ *
+ * Shape of a paged cache.  Supported: D 64 or 128; page 16, 32, 64 or 128 tokens;
+ * Hq a multiple of Hkv; Hq <= 1024; n_pages * Hkv * page < 2^31; max_pages * page <= 2^31 - 256.
+ * dtype is the cache's element type; queries, new keys and values, and outputs are
+ * fp32 with MOESTEP_F32 and bf16 otherwise. */
+typedef struct {
+    int Hq;        /* query heads; query head i reads key-value head i / (Hq / Hkv) */
+    int Hkv;       /* key-value heads */
+    int D;         /* head size */
+    int page;      /* tokens per page */
+    int n_pages;   /* pages in the pool */
+    int max_pages; /* entries of one request's page table */
+    int dtype;     /* MOESTEP_BF16, MOESTEP_F32 or MOESTEP_FP8 (E4M3 codes) */
+} moestep_kv_dims;
+
+/* A paged cache (host struct of device pointers, all 16-byte aligned).
+ *   k, v   [n_pages][Hkv][page][D]
+ *   k_exp, v_exp [n_pages][Hkv][page] uint8, MOESTEP_FP8 only (NULL otherwise):
+ *          an element is its E4M3 value times 2^(exp - 127)
+ *   table  [R][max_pages] int32: page of positions page*i .. page*i + page - 1 of
+ *          request r.  Only entries that a call's positions need are read; one
+ *          outside [0, n_pages) is never followed (MOESTEP_EDEVINPUT in the error
+ *          word; the call's results for that request are unspecified). */
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_exp;
+    uint8_t* v_exp;
+    const int32_t* table;
+} moestep_kv_cache;
+
+/* Bytes of workspace for the three cache calls below with R requests of n_q query
+ * tokens each (kv_cache_write and kv_cache_read need only its 512-byte header, for
+ * the error word, whatever R and n are).  moestep_workspace_init() prepares it. */
+int moestep_kv_workspace_size(const moestep_kv_dims* kd, int R, int n_q, size_t* bytes);
+
+/* Stores the keys and values of n new tokens of each of R requests.
+ *   k, v [R*n][Hkv][D], rows ld elements apart (ld >= Hkv*D; rows 16-byte aligned)
+ *   pos [R][n] int32: position of each token in its request; negative: not stored.
+ *   Two tokens of a call must not have the same place.
+ * MOESTEP_FP8: each (token, head) vector is stored as code = e4m3(x * 2^-e), rounded to
+ * nearest even, with e the smallest integer in [-100, 119] for which max|x| <= 448 * 2^e
+ * (-100 for a vector of zeros); infinities and what passes 448 * 2^119 saturate, NaN
+ * stays NaN and does not count for e. */
+int kv_cache_write(const moestep_kv_dims* kd, int R, int n, const void* k, const void* v, long long ld,
+                   const int32_t* pos, const moestep_kv_cache* cache, void* ws, size_t ws_bytes, void* stream);
+
+/* Reads the cached keys and values at pos [R][n] back into k, v [R*n][Hkv][D] (dense;
+ * zeros where pos is negative).  FP8 values times their power of two are exact in bf16
+ * except where they fall below its smallest subnormal. */
+int kv_cache_read(const moestep_kv_dims* kd, int R, int n, const int32_t* pos, const moestep_kv_cache* cache,
+                  void* k, void* v, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of n_q new tokens of each request over its first L = kv_len[r] cached
+ * positions; query i stands at position p_i = L - n_q + i (the new tokens' own keys and
+ * values are written first).  It sees the positions j < L, with causal != 0 only j <= p_i,
+ * with window > 0 only j > p_i - window.
+ *   out = sum_j softmax_j(scale * q . k_j) v_j;  lse = log sum_j exp(scale * q . k_j)
+ * A row that sees nothing has out = 0 and lse = -inf.  Keys and values at positions that
+ * no query of the request sees are never used, whatever they hold; a non-finite value at
+ * a position that some of the request's rows see may reach its other rows.
+ *   q [R*n_q][Hq][D], rows q_ld elements apart (q_ld >= Hq*D; rows 16-byte aligned)
+ *   kv_len [R] int32 in [0, max_pages * page] (others are clamped, MOESTEP_EDEVINPUT)
+ *   out [R*n_q][Hq][D]; lse [R*n_q][Hq] fp32 (may be NULL); scale > 0; n_q <= 1024
+ * Products accumulate in fp32; the softmax weights are rounded to bf16 before they
+ * multiply V, except with MOESTEP_F32.  Results do not depend on timing, only on the
+ * arguments and the device. */
+int block_attention(const moestep_kv_dims* kd, int R, int n_q, const void* q, long long q_ld,
+                    const int32_t* kv_len, const moestep_kv_cache* cache, float scale, int causal, int window,
+                    void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* The residual update after a block and the norm before the next one, for T tokens:
+ *   h_out = h_in + res_scale * gate * (w_post * y / rms(y)),   x = w_pre * h_out / rms(h_out)
+ * with rms(a) = sqrt(mean(a^2) + eps) over a token's H values.
+ *   y [T][H], bf16 or fp32 (y_dtype MOESTEP_BF16 / MOESTEP_F32): the block's output
+ *   w_post [H]: norm after the block; NULL: y itself, not normalised
+ *   gate fp32, gate_ld elements between the rows of consecutive requests (token t reads row
+ *   t / dims.P): 0 for one vector [H], else >= H and a multiple of 4; NULL: 1
+ *   h_in, h_out [T][H] fp32 (may be the same buffer)
+ *   w_pre [H] (NULL: 1); x [T][H] (NULL: not wanted); w_post, w_pre and x in the
+ *   activations' type (fp32 with MOESTEP_F32, else bf16)
+ * All pointers 16-byte aligned; eps > 0. */
+int block_residual_norm(const moestep_dims* dims, int T, const void* y, int y_dtype, const void* w_post,
+                        const float* gate, long long gate_ld, float res_scale, const float* h_in, float* h_out,
+                        const void* w_pre, void* x, float eps, void* stream);
+
 /* Synchronously reads and clears the workspace's device error word (host *word:
  * 0 or a MOESTEP_E* code).  Waits for `stream`. */
 int moestep_read_device_error(void* ws, size_t ws_bytes, void* stream, int* word);

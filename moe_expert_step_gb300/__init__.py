@@ -36,6 +36,7 @@ EXPORTS = [
     "moestep_error_string", "moestep_last_cuda_error", "moestep_prof_enable", "moestep_prof_read",
     "moestep_set_wait_timeout_ns", "moestep_set_route_fusion", "moestep_route_fusion", "moestep_launch_count",
     "moe_block_route_noalloc",
+    "moestep_kv_workspace_size", "kv_cache_write", "kv_cache_read", "block_attention", "block_residual_norm",
 ]
 
 
@@ -60,6 +61,14 @@ class Trace(ctypes.Structure):
                 ("sel", ctypes.c_void_p), ("x", ctypes.c_void_p), ("h", ctypes.c_void_p)]
 
 
+class KvDimsC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("Hq", "Hkv", "D", "page", "n_pages", "max_pages", "dtype")]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp", "table")]
+
+
 _LIB = None
 
 
@@ -76,6 +85,7 @@ def lib():
         L = ctypes.CDLL(_build.LIB)
         vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
         D = ctypes.POINTER(Dims)
+        ll, KD, KC = ctypes.c_longlong, ctypes.POINTER(KvDimsC), ctypes.POINTER(KvCache)
         sig = {
             "moestep_workspace_size": [D, i, ctypes.POINTER(sz)],
             "moestep_workspace_init": [vp, sz, vp],
@@ -99,6 +109,11 @@ def lib():
             "moestep_set_route_fusion": [ctypes.c_int],
             "moestep_route_fusion": [],
             "moestep_launch_count": [],
+            "moestep_kv_workspace_size": [KD, i, i, ctypes.POINTER(sz)],
+            "kv_cache_write": [KD, i, i, vp, vp, ll, vp, KC, vp, sz, vp],
+            "kv_cache_read": [KD, i, i, vp, KC, vp, vp, vp, sz, vp],
+            "block_attention": [KD, i, i, vp, ll, vp, KC, f, i, i, vp, vp, vp, sz, vp],
+            "block_residual_norm": [D, i, vp, i, vp, vp, ll, f, vp, vp, vp, vp, f, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -246,6 +261,138 @@ def block_decode_loop(d: ModelDims, R: int, layers, Wlm, emb, pos, mask_id: int,
     _check(lib().block_decode_loop(ctypes.byref(d.c()), R, len(layers), arr, _p(Wlm), _p(emb), _p(pos), int(mask_id),
                                    _p(top_p), float(logit_scale), float(threshold), mr, _p(tokens), _p(masked),
                                    _p(rounds), _p(ws), ws.numel(), _s(stream)), "block_decode_loop")
+
+
+# ------------------------------------------------------------------------------ the attention side of a layer
+
+
+@dataclass(frozen=True)
+class KvDims:
+    """Shape of a paged key-value cache and of the heads that read it (moestep_kv_dims)."""
+    Hq: int
+    Hkv: int
+    D: int
+    page: int
+    n_pages: int
+    max_pages: int
+    dtype: int = BF16
+
+    def __post_init__(self):
+        c = KvDimsC(self.Hq, self.Hkv, self.D, self.page, self.n_pages, self.max_pages, self.dtype)
+        object.__setattr__(self, "_c", ctypes.byref(c))  # kept: single-token calls are short
+
+
+def kv_cache(k, v, table, k_exp=None, v_exp=None) -> KvCache:
+    """Device pointers of one paged cache: k, v [n_pages, Hkv, page, D], table [R, max_pages] int32, and with
+    MOESTEP_FP8 k_exp, v_exp [n_pages, Hkv, page] uint8.  The struct keeps the tensors alive."""
+    for t in (k, v, table, k_exp, v_exp):
+        if t is not None and not t.is_contiguous():
+            raise MoeStepError(EINVAL, "kv_cache: tensors must be contiguous")
+    c = KvCache(_p(k), _p(v), _p(k_exp), _p(v_exp), _p(table))
+    c._tensors = (k, v, table, k_exp, v_exp)
+    return c
+
+
+def kv_workspace_size(kd: KvDims, R: int, n_q: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moestep_kv_workspace_size(kd._c, R, n_q, ctypes.byref(n)), "moestep_kv_workspace_size")
+    return n.value
+
+
+def kv_workspace(kd: KvDims, R: int, n_q: int, device="cuda", stream=None):
+    """Allocate (through torch) and initialise a workspace for the cache calls."""
+    import torch
+    ws = torch.empty(kv_workspace_size(kd, R, n_q), dtype=torch.uint8, device=device)
+    workspace_init(ws, stream)
+    return ws
+
+
+def _rows(t, heads: int, kd: KvDims, what: str) -> int:
+    """Distance between the rows of t [tokens, heads, D], which may be part of a wider row."""
+    st = t.stride()
+    if (len(st) != 3 or st[2] != 1 or (heads > 1 and st[1] != kd.D) or t.shape[1] != heads or t.shape[2] != kd.D
+            or t.element_size() != (4 if kd.dtype == F32 else 2)):
+        raise MoeStepError(EINVAL, f"{what} must be [tokens, {heads}, {kd.D}] in the activations' type, heads dense")
+    if not t.is_cuda:
+        raise MoeStepError(EINVAL, f"{what} must be on the GPU")
+    return st[0] if t.shape[0] > 1 else max(st[0], heads * kd.D)
+
+
+def _dense(t, shape, size: int, what: str) -> None:
+    """t is a contiguous GPU tensor of the shape, `size` bytes an element."""
+    if tuple(t.shape) != shape or t.element_size() != size or not t.is_contiguous():
+        raise MoeStepError(EINVAL, f"{what} must be contiguous, of shape {list(shape)} and {size} bytes an element")
+    if not t.is_cuda:
+        raise MoeStepError(EINVAL, f"{what} must be on the GPU")
+
+
+def kv_cache_write(kd: KvDims, R: int, k, v, pos, cache: KvCache, ws, stream=None) -> None:
+    """Store the keys and values k, v [R * n, Hkv, D] (rows may be parts of wider rows) at positions
+    pos [R, n] int32; a negative position is not stored."""
+    n = pos.shape[1]
+    _dense(pos, (R, n), 4, "kv_cache_write: pos")
+    ld = _rows(k, kd.Hkv, kd, "kv_cache_write: k")
+    if _rows(v, kd.Hkv, kd, "kv_cache_write: v") != ld or k.shape[0] != R * n or v.shape[0] != R * n:
+        raise MoeStepError(EINVAL, "kv_cache_write: k and v must have R * n rows, equally far apart")
+    _check(lib().kv_cache_write(kd._c, R, n, k.data_ptr(), v.data_ptr(), ld, pos.data_ptr(), cache, ws.data_ptr(),
+                                ws.numel(), _s(stream)), "kv_cache_write")
+
+
+def kv_cache_read(kd: KvDims, R: int, pos, cache: KvCache, k, v, ws, stream=None) -> None:
+    """Read the cached vectors at positions pos [R, n] back into k, v [R * n, Hkv, D] (zeros where negative)."""
+    n = pos.shape[1]
+    _dense(pos, (R, n), 4, "kv_cache_read: pos")
+    size = 4 if kd.dtype == F32 else 2
+    _dense(k, (R * n, kd.Hkv, kd.D), size, "kv_cache_read: k")
+    _dense(v, (R * n, kd.Hkv, kd.D), size, "kv_cache_read: v")
+    _check(lib().kv_cache_read(kd._c, R, n, pos.data_ptr(), cache, k.data_ptr(), v.data_ptr(), ws.data_ptr(),
+                               ws.numel(), _s(stream)), "kv_cache_read")
+
+
+def block_attention(kd: KvDims, R: int, q, kv_len, cache: KvCache, out, ws, scale: float, causal: bool = False,
+                    window: int = 0, lse=None, stream=None) -> None:
+    """Attention of q [R * n_q, Hq, D] (rows may be parts of wider rows) over the first kv_len [R] cached
+    positions of each request, the last n_q of which are the queries' own; see block_attention in moestep.h."""
+    T = q.shape[0]
+    n_q = T // R if R > 0 else 0
+    ld = _rows(q, kd.Hq, kd, "block_attention: q")
+    _dense(out, (R * n_q, kd.Hq, kd.D), 4 if kd.dtype == F32 else 2, "block_attention: out")
+    _dense(kv_len, (R,), 4, "block_attention: kv_len")
+    if R * n_q != T:
+        raise MoeStepError(EINVAL, "block_attention: q must have R * n_q rows")
+    if lse is not None:
+        _dense(lse, (T, kd.Hq), 4, "block_attention: lse")
+    _check(lib().block_attention(kd._c, R, n_q, q.data_ptr(), ld, kv_len.data_ptr(), cache, scale, int(causal),
+                                 int(window), out.data_ptr(), _p(lse), ws.data_ptr(), ws.numel(), _s(stream)),
+           "block_attention")
+
+
+def block_residual_norm(d: ModelDims, y, h_in, h_out, x, w_pre=None, w_post=None, gate=None, res_scale: float = 1.0,
+                        eps: float = 1e-6, stream=None) -> None:
+    """h_out = h_in + res_scale * gate * (w_post * y / rms(y)); x = w_pre * h_out / rms(h_out).  y [T, H] fp32 or
+    bf16; gate fp32 [H], or [requests, H] with one row for each d.P tokens; see block_residual_norm in moestep.h."""
+    T = y.shape[0]
+    shape = (T, d.H)
+    size, act = y.element_size(), 4 if d.dtype == F32 else 2
+    if size not in (2, 4):
+        raise MoeStepError(EINVAL, "block_residual_norm: y must be bf16 or fp32")
+    _dense(y, shape, size, "block_residual_norm: y")
+    _dense(h_in, shape, 4, "block_residual_norm: h_in")
+    _dense(h_out, shape, 4, "block_residual_norm: h_out")
+    if x is not None:
+        _dense(x, shape, act, "block_residual_norm: x")
+    for w in (w_pre, w_post):
+        if w is not None:
+            _dense(w, (d.H,), act, "block_residual_norm: w_pre, w_post")
+    gate_ld = 0
+    if gate is not None:
+        if (gate.shape[-1] != d.H or gate.stride(-1) != 1 or gate.element_size() != 4 or not gate.is_cuda
+                or gate.dim() > 2 or (gate.dim() == 2 and gate.shape[0] < -(-T // d.P))):
+            raise MoeStepError(EINVAL, "block_residual_norm: gate must be fp32 on the GPU, [H] or [requests, H]")
+        gate_ld = gate.stride(0) if gate.dim() == 2 and gate.shape[0] > 1 else 0
+    _check(lib().block_residual_norm(ctypes.byref(d.c()), T, y.data_ptr(), F32 if size == 4 else BF16, _p(w_post),
+                                     _p(gate), gate_ld, res_scale, h_in.data_ptr(), h_out.data_ptr(), _p(w_pre),
+                                     _p(x), eps, _s(stream)), "block_residual_norm")
 
 
 def read_device_error(ws, stream=None) -> int:

@@ -9,7 +9,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmoestep.so")
-SOURCES = ["api.cu", "route.cu", "misc.cu", "expert_gemm.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "route.cu", "misc.cu", "expert_gemm.cu", "noalloc.cu", "kv_cache.cu",
+           "residual_norm.cu", "attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

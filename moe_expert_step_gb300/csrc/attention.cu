@@ -1,0 +1,413 @@
+// Attention of a block of new tokens over a paged key-value cache (see attn.cuh for how the
+// work is divided): the CUDA-core kernel, the join of shared segments, and the C entry.
+#include "attn.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "kv.h"
+#include "launch.cuh"
+
+#include <cmath>
+#include <type_traits>
+
+namespace moestep {
+namespace {
+
+// ---------------------------------------------------------------------------- CUDA cores
+// Tiles of 16 query rows and 64 keys, 128 threads.  Each thread computes a 2 x 4 block of the
+// tile's scores, the 16 rows' statistics are kept by 8 lanes each, and each thread accumulates
+// 4 rows x (D / 32) columns of the output.
+constexpr int kRT = 16, kKT = 64, kSimpleThreads = 128;
+template <int D>
+constexpr int simple_smem() {
+    return (kRT * D + 2 * kKT * (D + 4) + kRT * (kKT + 4) + 3 * kRT) * 4;
+}
+
+__device__ __forceinline__ float pow2i(int e) {  // 2^e for any e of a byte's exponent, in two factors
+    const int h = e >> 1;
+    return __uint_as_float(static_cast<uint32_t>(h + 127) << 23) * __uint_as_float(static_cast<uint32_t>(e - h + 127) << 23);
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnArgs a) {
+    using T = typename std::conditional<DT == MOESTEP_F32, float, bf16>::type;
+    extern __shared__ float smf[];
+    __shared__ long long plan_sm[64];
+    float* sq = smf;                       // [16][D]
+    float* sk = sq + kRT * D;              // [64][D + 4]
+    float* sv = sk + kKT * (D + 4);        // [64][D + 4]
+    float* sp = sv + kKT * (D + 4);        // [16][68]: scores, then weights
+    float* s_m = sp + kRT * (kKT + 4);     // [16] running maximum
+    float* s_l = s_m + kRT;                // [16] running sum
+    float* s_f = s_l + kRT;                // [16] factor of this tile's rescaling
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x;
+    const AttnPlan plan = attn_plan<kKT, kSimpleThreads>(a, plan_sm);
+    constexpr int CW = D / 32;             // output columns of a thread
+    AttnWalk w = attn_begin<kKT>(plan);
+    while (attn_next<kKT>(a, w)) {
+        const int h = w.seg / a.row_tiles, row0 = (w.seg - h * a.row_tiles) * kRT;
+        const int nrows = min(kRT, a.rows - row0);
+        __syncthreads();
+        for (int i = tid; i < kRT * D; i += kSimpleThreads) {
+            const int rr = i / D, d = i - rr * D, row = row0 + rr;
+            float x = 0.f;
+            if (rr < nrows) {
+                const int qi = row / a.G, g = row - qi * a.G;
+                x = to_f32<T>(static_cast<const T*>(a.q)[(static_cast<long long>(w.r) * a.n_q + qi) * a.q_ld +
+                                                         (h * a.G + g) * D + d]);
+            }
+            sq[i] = x;
+        }
+        if (tid < kRT) {
+            s_m[tid] = -INFINITY;
+            s_l[tid] = 0.f;
+        }
+        float acc[4][CW] = {};
+        const int vr = tid >> 5, vc = tid & 31;  // output: rows 4 vr .., columns vc + 32 j
+        const int lo = attn_lo(a, w.L);
+        for (int t = w.tile; t < w.tile + w.tiles; ++t) {
+            const int j0 = t * kKT;
+            __syncthreads();
+            for (int i = tid; i < kKT * (D / 4); i += kSimpleThreads) {
+                const int key = i / (D / 4), d = 4 * (i - key * (D / 4)), j = j0 + key;
+                float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+                if (j >= lo && j < w.L) {
+                    const int id = __ldg(&a.table[static_cast<long long>(w.r) * a.max_pages + (j >> a.page_log2)]);
+                    if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_pages)) {
+                        record_error(a.err, kErrBadInput);
+                    } else {
+                        const long long row = ((static_cast<long long>(id) * a.Hkv + h) << a.page_log2) +
+                                              (j & ((1 << a.page_log2) - 1));
+                        if (DT == MOESTEP_F32) {
+                            kx = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + row * D + d);
+                            vx = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + row * D + d);
+                        } else if (DT == MOESTEP_BF16) {
+                            const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.k) + row * D + d);
+                            const uint2 y = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.v) + row * D + d);
+                            kx = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                                             __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+                            vx = make_float4(__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u),
+                                             __uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u));
+                        } else {
+                            const float ks = pow2i(__ldg(&a.k_exp[row]) - 127), vs = pow2i(__ldg(&a.v_exp[row]) - 127);
+                            const uint32_t x = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.k) + row * D + d);
+                            const uint32_t y = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + row * D + d);
+                            float f[8];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const uint32_t src = u < 2 ? x : y;
+                                uint32_t r;
+                                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(src >> (16 * (u & 1)))));
+                                const float2 p = __half22float2(*reinterpret_cast<__half2*>(&r));
+                                f[2 * u] = p.x;
+                                f[2 * u + 1] = p.y;
+                            }
+                            kx = make_float4(f[0] * ks, f[1] * ks, f[2] * ks, f[3] * ks);
+                            vx = make_float4(f[4] * vs, f[5] * vs, f[6] * vs, f[7] * vs);
+                        }
+                    }
+                }
+                *reinterpret_cast<float4*>(sk + key * (D + 4) + d) = kx;
+                *reinterpret_cast<float4*>(sv + key * (D + 4) + d) = vx;
+            }
+            __syncthreads();
+            {   // scores: rows 2 sr, 2 sr + 1; keys sc + 16 j
+                const int sr = tid >> 4, sc = tid & 15;
+                float s[2][4] = {};
+                for (int d = 0; d < D; d += 4) {
+                    const float4 q0 = *reinterpret_cast<const float4*>(sq + (2 * sr) * D + d);
+                    const float4 q1 = *reinterpret_cast<const float4*>(sq + (2 * sr + 1) * D + d);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 kx = *reinterpret_cast<const float4*>(sk + (sc + 16 * j) * (D + 4) + d);
+                        s[0][j] += q0.x * kx.x + q0.y * kx.y + q0.z * kx.z + q0.w * kx.w;
+                        s[1][j] += q1.x * kx.x + q1.y * kx.y + q1.z * kx.z + q1.w * kx.w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rr = 2 * sr + i;
+                    const int2 see = attn_sees(a, w.L, (row0 + min(rr, nrows - 1)) / a.G);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int jj = j0 + sc + 16 * j;
+                        sp[rr * (kKT + 4) + sc + 16 * j] =
+                            (jj >= see.x && jj < see.y) ? s[i][j] * a.scale_log2 : -INFINITY;
+                    }
+                }
+            }
+            __syncthreads();
+            {   // eight lanes a row: statistics and weights
+                const int rr = tid >> 3, l8 = tid & 7;
+                float* row = sp + rr * (kKT + 4) + l8 * 8;
+                float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx = fmaxf(mx, row[i]);  // passes over NaN, which the weights keep
+#pragma unroll
+                for (int o = 4; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float m0 = s_m[rr], m1 = fmaxf(m0, mx), ms = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p = exp2f(row[i] - ms);
+                    row[i] = p;
+                    sum += p;
+                }
+#pragma unroll
+                for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                __syncwarp();
+                if (l8 == 0) {
+                    const float f = exp2f(m0 - ms);
+                    s_f[rr] = f;
+                    s_l[rr] = s_l[rr] * f + sum;
+                    s_m[rr] = m1;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = s_f[4 * vr + i];
+#pragma unroll
+                for (int c = 0; c < CW; ++c) acc[i][c] *= f;
+            }
+            for (int key = 0; key < kKT; key += 4) {
+                float4 p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (4 * vr + i) * (kKT + 4) + key);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) {
+                        const float x = sv[(key + u) * (D + 4) + vc + 32 * c];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[i][c] += (u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w) * x;
+                    }
+            }
+        }
+        __syncthreads();
+        const int slot = 2 * blockIdx.x + (w.k > 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int rr = 4 * vr + i;
+            if (rr >= nrows) continue;
+            const float m = s_m[rr], l = s_l[rr];
+            if (w.whole) {
+                const int row = row0 + rr, qi = row / a.G, g = row - qi * a.G;
+                const size_t o = (static_cast<size_t>(w.r) * a.n_q + qi) * a.Hq + h * a.G + g;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int c = 0; c < CW; ++c) static_cast<T*>(a.out)[o * D + vc + 32 * c] = from_f32<T>(acc[i][c] * inv);
+                if (a.lse && vc == 0) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            } else {
+                const size_t at = static_cast<size_t>(slot) * a.slot_rows + rr;
+#pragma unroll
+                for (int c = 0; c < CW; ++c) a.part_o[at * D + vc + 32 * c] = acc[i][c];
+                if (vc == 0) a.part_ml[at] = make_float2(m, l);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------- join
+// Rows of a shared segment: m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m) / l over
+// its CTAs c in order.  Eight warps a block; WPR of them share a row (each every WPR-th part).
+template <typename T, int D, int WPR>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+    __shared__ float s_f[8 / WPR][2 * kAttnMaxCtas];
+    __shared__ float s_o[8][D];
+    pdl_trigger();
+    pdl_wait();
+    const int4 j = a.joins[blockIdx.x];
+    if (j.x < 0) return;
+    const int h = j.y / a.row_tiles, row0 = (j.y - h * a.row_tiles) * a.slot_rows;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / WPR, part = warp % WPR;
+    const int rr = blockIdx.y * (8 / WPR) + team;
+    const bool on = rr < a.slot_rows && row0 + rr < a.rows;
+    const int c0 = j.z >> 1, n = j.w - c0 + 1;
+    float m = -INFINITY, l = 0.f;
+    auto slot = [&](int i) { return i == 0 ? j.z : 2 * (c0 + i); };
+    if (on) {
+        for (int i = lane; i < n; i += 32) {
+            const float2 ml = __ldcg(&a.part_ml[static_cast<size_t>(slot(i)) * a.slot_rows + rr]);
+            const float m1 = fmaxf(m, ml.x), ms = m1 == -INFINITY ? 0.f : m1;
+            l = l * exp2f(m - ms) + ml.y * exp2f(ml.x - ms);
+            m = m1;
+        }
+        const float mm = warp_max(m), ms = mm == -INFINITY ? 0.f : mm;
+        l = warp_sum(l * exp2f(m - ms));
+        m = mm;
+        for (int i = lane; i < n; i += 32) {
+            const float2 ml = __ldcg(&a.part_ml[static_cast<size_t>(slot(i)) * a.slot_rows + rr]);
+            s_f[team][i] = exp2f(ml.x - ms);  // each of the team's warps writes the same values
+        }
+        __syncwarp();
+    }
+    constexpr int W = D / 32;
+    float acc[W] = {};
+    if (on) {
+#pragma unroll 4
+        for (int i = part; i < n; i += WPR) {
+            const float* p = a.part_o + (static_cast<size_t>(slot(i)) * a.slot_rows + rr) * D + lane * W;
+            const float f = s_f[team][i];
+            if (W == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+                acc[0] += f * x.x, acc[1] += f * x.y, acc[W > 2 ? 2 : 0] += f * x.z, acc[W > 2 ? 3 : 0] += f * x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+                acc[0] += f * x.x, acc[1] += f * x.y;
+            }
+        }
+    }
+    if (WPR > 1) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) s_o[warp][lane * W + i] = acc[i];
+        __syncthreads();
+        if (part != 0) return;
+#pragma unroll
+        for (int k = 1; k < WPR; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] += s_o[warp + k][lane * W + i];
+    }
+    if (!on) return;
+    const int row = row0 + rr, qi = row / a.G, g = row - qi * a.G;
+    const size_t o = (static_cast<size_t>(j.x) * a.n_q + qi) * a.Hq + h * a.G + g;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* out = static_cast<T*>(a.out) + o * D + lane * W;
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = from_f32<T>(acc[i] * inv);
+    if (a.lse && lane == 0) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+template <int DT, int D>
+cudaError_t launch_simple(const AttnArgs& a, int grid, cudaStream_t s) {
+    static int done[64] = {};
+    cudaError_t e = ensure_smem(attn_simple_kernel<DT, D>, simple_smem<D>(), done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_simple_kernel<DT, D>, dim3(grid), dim3(kSimpleThreads), simple_smem<D>(), s, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const AttnArgs& a, int grid, cudaStream_t s) {
+    const int rows = a.slot_rows < a.rows ? a.slot_rows : a.rows;
+    return launch_pdl(attn_join_kernel<T, D, 8>, dim3(grid, rows), dim3(256), 0, s, a);
+}
+
+struct KvLayout {
+    size_t joins, ml, o, total;
+    int slot_rows;
+};
+KvLayout kv_layout(const moestep_kv_dims& d, int n_q) {
+    (void)n_q;
+    KvLayout L{};
+    L.slot_rows = kRT;
+    size_t at = kKvHeader;
+    auto take = [&](size_t bytes) {
+        const size_t p = at;
+        at = (at + bytes + 255) / 256 * 256;
+        return p;
+    };
+    L.joins = take(sizeof(int4) * kAttnMaxCtas);
+    L.ml = take(sizeof(float2) * 2 * kAttnMaxCtas * L.slot_rows);
+    L.o = take(sizeof(float) * 2 * kAttnMaxCtas * L.slot_rows * d.D);
+    L.total = at;
+    return L;
+}
+
+int check_attn(const moestep_kv_dims* kd, int R, int n_q) {
+    const int rc = check_kv_dims(kd);
+    if (rc != MOESTEP_OK) return rc;
+    if (R <= 0 || n_q <= 0) return MOESTEP_EINVAL;
+    if (n_q > 1024 || R > (1 << 20)) return MOESTEP_EUNSUPPORTED;
+    // units and rows are counted in 31 bits
+    const long long row_tiles = (1ll * n_q * (kd->Hq / kd->Hkv) + kRT - 1) / kRT;
+    const long long tiles = (1ll * kd->max_pages * kd->page + kKT - 1) / kKT;
+    if (tiles * kd->Hkv > ((1ll << 31) - 1) / row_tiles) return MOESTEP_EUNSUPPORTED;
+    if (1ll * R * n_q > ((1ll << 31) - 1) / kd->Hq) return MOESTEP_EUNSUPPORTED;
+    return MOESTEP_OK;
+}
+
+}  // namespace
+}  // namespace moestep
+
+extern "C" int moestep_kv_workspace_size(const moestep_kv_dims* kd, int R, int n_q, size_t* bytes) {
+    using namespace moestep;
+    const int rc = check_attn(kd, R, n_q);
+    if (rc != MOESTEP_OK) return rc;
+    if (bytes == nullptr) return MOESTEP_EINVAL;
+    *bytes = kv_layout(*kd, n_q).total;
+    return MOESTEP_OK;
+}
+
+extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const void* q, long long q_ld,
+                               const int32_t* kv_len, const moestep_kv_cache* cache, float scale, int causal,
+                               int window, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    using namespace moestep;
+    int rc = check_attn(kd, R, n_q);
+    if (rc != MOESTEP_OK) return rc;
+    if (!kv_len || !out || window < 0 || !std::isfinite(scale) || !(scale > 0.f)) return MOESTEP_EINVAL;
+    if ((rc = check_kv_cache(kd, cache)) != MOESTEP_OK) return rc;
+    if ((rc = check_kv_rows(q, q_ld, 1ll * kd->Hq * kd->D, kd->dtype)) != MOESTEP_OK) return rc;
+    if (!kv_aligned16(out)) return MOESTEP_EALIGN;
+    const KvLayout L = kv_layout(*kd, n_q);
+    if ((rc = check_kv_ws(ws, ws_bytes, L.total)) != MOESTEP_OK) return rc;
+    int sms = 0;
+    if ((rc = device_ok(&sms)) != MOESTEP_OK) return rc;
+    char* w = static_cast<char*>(ws);
+    AttnArgs a{};
+    a.q = q;
+    a.q_ld = q_ld;
+    a.kv_len = kv_len;
+    a.table = cache->table;
+    a.k = cache->k;
+    a.v = cache->v;
+    a.k_exp = cache->k_exp;
+    a.v_exp = cache->v_exp;
+    a.out = out;
+    a.lse = lse;
+    a.joins = reinterpret_cast<int4*>(w + L.joins);
+    a.part_ml = reinterpret_cast<float2*>(w + L.ml);
+    a.part_o = reinterpret_cast<float*>(w + L.o);
+    a.err = reinterpret_cast<int*>(w);
+    a.R = R;
+    a.n_q = n_q;
+    a.Hq = kd->Hq;
+    a.Hkv = kd->Hkv;
+    a.G = kd->Hq / kd->Hkv;
+    a.rows = n_q * a.G;
+    a.slot_rows = L.slot_rows;
+    a.row_tiles = (a.rows + kRT - 1) / kRT;
+    a.page_log2 = kd->page == 16 ? 4 : kd->page == 32 ? 5 : kd->page == 64 ? 6 : 7;
+    a.max_pages = kd->max_pages;
+    a.n_pages = kd->n_pages;
+    a.causal = causal != 0;
+    // a window as long as the cache hides nothing (and stays out of 32-bit overflow)
+    a.window = window >= kd->max_pages * kd->page ? 0 : window;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    const int grid = 2 * sms < kAttnMaxCtas ? 2 * sms : kAttnMaxCtas;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool wide = kd->D == 128;
+    prof_begin(8, s);
+    cudaError_t e;
+    if (kd->dtype == MOESTEP_F32)
+        e = wide ? launch_simple<MOESTEP_F32, 128>(a, grid, s) : launch_simple<MOESTEP_F32, 64>(a, grid, s);
+    else if (kd->dtype == MOESTEP_BF16)
+        e = wide ? launch_simple<MOESTEP_BF16, 128>(a, grid, s) : launch_simple<MOESTEP_BF16, 64>(a, grid, s);
+    else
+        e = wide ? launch_simple<MOESTEP_FP8, 128>(a, grid, s) : launch_simple<MOESTEP_FP8, 64>(a, grid, s);
+    prof_end(8, s);
+    if (e == cudaSuccess) {
+        count_launch();
+        prof_begin(8, s);
+        if (kd->dtype == MOESTEP_F32)
+            e = wide ? launch_join<float, 128>(a, grid, s) : launch_join<float, 64>(a, grid, s);
+        else
+            e = wide ? launch_join<bf16, 128>(a, grid, s) : launch_join<bf16, 64>(a, grid, s);
+        prof_end(8, s);
+        if (e == cudaSuccess) count_launch();
+    }
+    if (e != cudaSuccess) {
+        set_last_cuda(static_cast<int>(e));
+        return MOESTEP_ECUDA;
+    }
+    return MOESTEP_OK;
+}

@@ -1,0 +1,197 @@
+// What the attention kernels share: the arguments, the division of the work among CTAs, and
+// the rows a query sees.
+//
+// The work is a list of units: one tile of keys for one tile of query rows of one
+// (request, key-value head).  Units are numbered request by request, then head, then row tile, then key
+// tile, and CTA c of A takes units [W c / A, W (c+1) / A): every CTA streams the same number
+// of key tiles whatever the requests' lengths are.  The lengths are on the device, so every
+// CTA works the division out from kv_len itself (a block-wide scan over the requests; an
+// empty request counts one unit, whose only effect is to write its empty rows).
+//
+// The units of one (request, head, row tile) are a segment.  A segment inside one CTA is
+// written out directly; of one that CTAs share, each leaves its rows' (m, l, o) in a slot of
+// the workspace (a CTA has at most two such: the one it begins in and the one it ends in) and
+// the join launch adds them up in CTA order, so the result does not depend on timing.
+#pragma once
+#include "common.cuh"
+#include "moestep.h"
+
+namespace moestep {
+
+constexpr int kAttnMaxCtas = 304;  // CTAs that the workspace has slots for
+
+struct AttnArgs {
+    const void* q;
+    long long q_ld;
+    const int32_t* kv_len;
+    const int32_t* table;
+    const void* k;
+    const void* v;
+    const uint8_t* k_exp;
+    const uint8_t* v_exp;
+    void* out;
+    float* lse;
+    float* part_o;    // [2 * CTAs][slot_rows][D]
+    float2* part_ml;  // [2 * CTAs][slot_rows]: maximum (times scale * log2 e), sum
+    int4* joins;      // [CTAs]: {request or -1, head * row tiles + row tile, first CTA, last CTA}
+    int* err;
+    int R, n_q, Hq, Hkv, G;
+    int rows;        // n_q * G: query rows of one (request, key-value head)
+    int row_tiles;
+    int slot_rows;
+    int page_log2, max_pages, n_pages;
+    int causal, window;
+    float scale_log2;  // scale * log2(e): the kernels take exponentials to base 2
+    unsigned long long timeout_ns;
+};
+
+// Cached positions of a request (clamped; a bad length is recorded by CTA 0)
+__device__ __forceinline__ int attn_len(const AttnArgs& a, int r) {
+    const int L = __ldg(&a.kv_len[r]), most = a.max_pages << a.page_log2;
+    return min(max(L, 0), most);
+}
+
+// Positions [lo, hi) that some query of the request sees
+__device__ __forceinline__ int attn_lo(const AttnArgs& a, int L) {
+    return a.window > 0 ? max(0, L - a.n_q - a.window + 1) : 0;
+}
+
+// Positions [lo, hi) that query i sees
+__device__ __forceinline__ int2 attn_sees(const AttnArgs& a, int L, int i) {
+    const int p = L - a.n_q + i;
+    return make_int2(a.window > 0 ? max(0, p - a.window + 1) : 0, a.causal ? min(L, max(0, p + 1)) : L);
+}
+
+template <int KT>
+__device__ __forceinline__ int2 attn_tiles(const AttnArgs& a, int L) {  // first tile, number of tiles
+    const int t0 = attn_lo(a, L) / KT;
+    return make_int2(t0, max(1, (L + KT - 1) / KT - t0));
+}
+
+// First unit of CTA c, and the CTA that holds unit u, of W units over A CTAs
+__device__ __forceinline__ long long attn_first(long long W, int A, int c) { return W * c / A; }
+__device__ __forceinline__ int attn_owner(long long W, int A, long long u) {
+    return static_cast<int>(((u + 1) * A - 1) / W);
+}
+
+// One CTA's place in the list
+struct AttnPlan {
+    long long W;  // units in all
+    int A;        // CTAs that have some
+    int begin_r;  // request of the CTA's first unit
+    int begin_o;  // that unit's number within the request
+    int count;    // the CTA's units
+};
+
+// Executed by every thread of the block (NT threads); `sm`: 64 long longs of shared memory.
+template <int KT, int NT>
+__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, long long* sm) {
+    const int tid = threadIdx.x, per = (a.R + NT - 1) / NT, heads = a.Hkv * a.row_tiles;
+    const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) {
+        const int L = attn_len(a, r);
+        if (blockIdx.x == 0 && L != __ldg(&a.kv_len[r])) record_error(a.err, kErrBadInput);
+        mine += static_cast<long long>(attn_tiles<KT>(a, L).y) * heads;
+    }
+    long long incl = mine;  // block-wide inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if ((tid & 31) >= o) incl += v;
+    }
+    if ((tid & 31) == 31) sm[tid >> 5] = incl;
+    __syncthreads();
+    long long before = 0, W = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w == (tid >> 5)) before = W;
+        W += sm[w];
+    }
+    incl += before;
+    AttnPlan p;
+    p.W = W;
+    p.A = static_cast<int>(min(W, static_cast<long long>(gridDim.x)));
+    const int c = blockIdx.x;
+    const long long first = c < p.A ? attn_first(W, p.A, c) : W;
+    p.count = c < p.A ? static_cast<int>(attn_first(W, p.A, c + 1) - first) : 0;
+    int* out = reinterpret_cast<int*>(sm + 40);
+    if (p.count > 0 && first >= incl - mine && first < incl) {
+        long long at = incl - mine;
+        for (int r = r0; r < r1; ++r) {
+            const long long n = static_cast<long long>(attn_tiles<KT>(a, attn_len(a, r)).y) * heads;
+            if (first < at + n) {
+                out[0] = r;
+                out[1] = static_cast<int>(first - at);
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    p.begin_r = p.count > 0 ? out[0] : 0;
+    p.begin_o = p.count > 0 ? out[1] : 0;
+    // the join of a segment is described by the CTA that is the second to work on it
+    if (tid == 0) {
+        int4 j = make_int4(-1, 0, 0, 0);
+        if (p.count > 0) {
+            const int nt = attn_tiles<KT>(a, attn_len(a, p.begin_r)).y, seg = p.begin_o / nt, t = p.begin_o - seg * nt;
+            if (t > 0) {
+                const int c0 = attn_owner(W, p.A, first - t);
+                if (c0 == c - 1) j = make_int4(p.begin_r, seg, c0, attn_owner(W, p.A, first - t + nt - 1));
+            }
+        }
+        a.joins[c] = j;
+        if (p.count > 0 && j.x >= 0) {
+            // whether the segment is the first CTA's own first one (its slot 0) or not (slot 1)
+            const int nt = attn_tiles<KT>(a, attn_len(a, p.begin_r)).y;
+            const int t = p.begin_o - (p.begin_o / nt) * nt;
+            const int slot1 = attn_first(W, p.A, j.z) != first - t;
+            a.joins[c].z = j.z * 2 + slot1;
+        }
+    }
+    return p;
+}
+
+// A CTA's walk over its segments.
+struct AttnWalk {
+    int r, o, left, k;   // request, unit within it, units left, segments done
+    int L, t0, nt, seg;  // of the current segment
+    int tile, tiles;     // its first key tile here (from t0) and how many
+    bool whole;
+};
+template <int KT>
+__device__ __forceinline__ AttnWalk attn_begin(const AttnPlan& p) {
+    AttnWalk w{};
+    w.r = p.begin_r;
+    w.o = p.begin_o;
+    w.left = p.count;
+    w.k = -1;
+    w.tiles = 0;
+    return w;
+}
+template <int KT>
+__device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnWalk& w) {
+    w.o += w.tiles;
+    w.left -= w.tiles;
+    if (w.left <= 0) return false;
+    w.L = attn_len(a, w.r);
+    int2 t = attn_tiles<KT>(a, w.L);
+    if (w.o >= t.y * a.Hkv * a.row_tiles) {
+        ++w.r;
+        w.o = 0;
+        w.L = attn_len(a, w.r);
+        t = attn_tiles<KT>(a, w.L);
+    }
+    w.t0 = t.x;
+    w.nt = t.y;
+    w.seg = w.o / w.nt;
+    const int in = w.o - w.seg * w.nt;
+    w.tile = w.t0 + in;
+    w.tiles = min(w.nt - in, w.left);
+    w.whole = w.tiles == w.nt;
+    ++w.k;
+    return true;
+}
+
+}  // namespace moestep

@@ -16,3 +16,4 @@ plain loops, zero-weight and one-token-block special cases, and request
 independence.  None is "parity unpinned".
 """
 from .moe_step import *  # noqa: F401,F403
+from . import kv_attention  # noqa: F401
