@@ -7,7 +7,6 @@
 #include "launch.cuh"
 
 #include <cmath>
-#include <type_traits>
 
 namespace moestep {
 namespace {
@@ -22,14 +21,8 @@ constexpr int simple_smem() {
     return (kRT * D + 2 * kKT * (D + 4) + kRT * (kKT + 4) + 3 * kRT) * 4;
 }
 
-__device__ __forceinline__ float pow2i(int e) {  // 2^e for any e of a byte's exponent, in two factors
-    const int h = e >> 1;
-    return __uint_as_float(static_cast<uint32_t>(h + 127) << 23) * __uint_as_float(static_cast<uint32_t>(e - h + 127) << 23);
-}
-
-template <int DT, int D>
-__global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnArgs a) {
-    using T = typename std::conditional<DT == MOESTEP_F32, float, bf16>::type;
+template <int D>
+__global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs a) {
     extern __shared__ float smf[];
     __shared__ long long plan_sm[64];
     float* sq = smf;                       // [16][D]
@@ -54,8 +47,8 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
             float x = 0.f;
             if (rr < nrows) {
                 const int qi = row / a.G, g = row - qi * a.G;
-                x = to_f32<T>(static_cast<const T*>(a.q)[(static_cast<long long>(w.r) * a.n_q + qi) * a.q_ld +
-                                                         (h * a.G + g) * D + d]);
+                x = static_cast<const float*>(a.q)[(static_cast<long long>(w.r) * a.n_q + qi) * a.q_ld +
+                                                   (h * a.G + g) * D + d];
             }
             sq[i] = x;
         }
@@ -79,33 +72,8 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
                     } else {
                         const long long row = ((static_cast<long long>(id) * a.Hkv + h) << a.page_log2) +
                                               (j & ((1 << a.page_log2) - 1));
-                        if (DT == MOESTEP_F32) {
-                            kx = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + row * D + d);
-                            vx = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + row * D + d);
-                        } else if (DT == MOESTEP_BF16) {
-                            const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.k) + row * D + d);
-                            const uint2 y = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.v) + row * D + d);
-                            kx = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
-                                             __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
-                            vx = make_float4(__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u),
-                                             __uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u));
-                        } else {
-                            const float ks = pow2i(__ldg(&a.k_exp[row]) - 127), vs = pow2i(__ldg(&a.v_exp[row]) - 127);
-                            const uint32_t x = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.k) + row * D + d);
-                            const uint32_t y = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + row * D + d);
-                            float f[8];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const uint32_t src = u < 2 ? x : y;
-                                uint32_t r;
-                                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(src >> (16 * (u & 1)))));
-                                const float2 p = __half22float2(*reinterpret_cast<__half2*>(&r));
-                                f[2 * u] = p.x;
-                                f[2 * u + 1] = p.y;
-                            }
-                            kx = make_float4(f[0] * ks, f[1] * ks, f[2] * ks, f[3] * ks);
-                            vx = make_float4(f[4] * vs, f[5] * vs, f[6] * vs, f[7] * vs);
-                        }
+                        kx = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + row * D + d);
+                        vx = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + row * D + d);
                     }
                 }
                 *reinterpret_cast<float4*>(sk + key * (D + 4) + d) = kx;
@@ -196,7 +164,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
                 const size_t o = (static_cast<size_t>(w.r) * a.n_q + qi) * a.Hq + h * a.G + g;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-                for (int c = 0; c < CW; ++c) static_cast<T*>(a.out)[o * D + vc + 32 * c] = from_f32<T>(acc[i][c] * inv);
+                for (int c = 0; c < CW; ++c) static_cast<float*>(a.out)[o * D + vc + 32 * c] = acc[i][c] * inv;
                 if (a.lse && vc == 0) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             } else {
                 const size_t at = static_cast<size_t>(slot) * a.slot_rows + rr;
@@ -278,12 +246,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
     if (a.lse && lane == 0) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-template <int DT, int D>
-cudaError_t launch_simple(const AttnArgs& a, int grid, cudaStream_t s) {
+template <int D>
+cudaError_t launch_f32(const AttnArgs& a, int grid, cudaStream_t s) {
     static int done[64] = {};
-    cudaError_t e = ensure_smem(attn_simple_kernel<DT, D>, simple_smem<D>(), done);
+    cudaError_t e = ensure_smem(attn_f32_kernel<D>, simple_smem<D>(), done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_simple_kernel<DT, D>, dim3(grid), dim3(kSimpleThreads), simple_smem<D>(), s, a);
+    return launch_pdl(attn_f32_kernel<D>, dim3(grid), dim3(kSimpleThreads), simple_smem<D>(), s, a);
 }
 
 template <typename T, int D>
@@ -292,23 +260,32 @@ cudaError_t launch_join(const AttnArgs& a, int grid, cudaStream_t s) {
     return launch_pdl(attn_join_kernel<T, D, 8>, dim3(grid, rows), dim3(256), 0, s, a);
 }
 
+// Row tile of the kernel that runs (attention_tc.cu), and the CTAs that it may have: rows that
+// fit 32, 64 or 128 lanes, else two tiles of 128
+int row_tile(const moestep_kv_dims& d, int n_q) {
+    if (d.dtype == MOESTEP_F32) return kRT;
+    const long long rows = 1ll * n_q * (d.Hq / d.Hkv);
+    return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+}
+int max_ctas(const moestep_kv_dims& d) { return d.dtype == MOESTEP_F32 ? kAttnMaxCtas : kAttnMaxCtasTc; }
+
 struct KvLayout {
     size_t joins, ml, o, total;
     int slot_rows;
 };
 KvLayout kv_layout(const moestep_kv_dims& d, int n_q) {
-    (void)n_q;
     KvLayout L{};
-    L.slot_rows = kRT;
+    L.slot_rows = row_tile(d, n_q);
+    const int ctas = max_ctas(d);
     size_t at = kKvHeader;
     auto take = [&](size_t bytes) {
         const size_t p = at;
         at = (at + bytes + 255) / 256 * 256;
         return p;
     };
-    L.joins = take(sizeof(int4) * kAttnMaxCtas);
-    L.ml = take(sizeof(float2) * 2 * kAttnMaxCtas * L.slot_rows);
-    L.o = take(sizeof(float) * 2 * kAttnMaxCtas * L.slot_rows * d.D);
+    L.joins = take(sizeof(int4) * ctas);
+    L.ml = take(sizeof(float2) * 2 * ctas * L.slot_rows);
+    L.o = take(sizeof(float) * 2 * ctas * L.slot_rows * d.D);
     L.total = at;
     return L;
 }
@@ -375,7 +352,7 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     a.G = kd->Hq / kd->Hkv;
     a.rows = n_q * a.G;
     a.slot_rows = L.slot_rows;
-    a.row_tiles = (a.rows + kRT - 1) / kRT;
+    a.row_tiles = (a.rows + L.slot_rows - 1) / L.slot_rows;
     a.page_log2 = kd->page == 16 ? 4 : kd->page == 32 ? 5 : kd->page == 64 ? 6 : 7;
     a.max_pages = kd->max_pages;
     a.n_pages = kd->n_pages;
@@ -383,22 +360,32 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     // a window as long as the cache hides nothing (and stays out of 32-bit overflow)
     a.window = window >= kd->max_pages * kd->page ? 0 : window;
     a.scale_log2 = scale * 1.4426950408889634f;
-    const int grid = 2 * sms < kAttnMaxCtas ? 2 * sms : kAttnMaxCtas;
+    a.timeout_ns = wait_timeout_ns();
+    const bool f32 = kd->dtype == MOESTEP_F32, f8 = kd->dtype == MOESTEP_FP8;
+    const int want = f32 ? 2 * sms : sms, grid = want < max_ctas(*kd) ? want : max_ctas(*kd);
+    CUtensorMap km, vm;
+    if (!f32) {
+        const uint64_t n = 1ull * kd->n_pages * kd->Hkv * kd->page;
+        for (int i = 0; i < 2; ++i) {
+            const void* p = i ? cache->v : cache->k;
+            rc = f8 ? encode_tile_map(i ? &vm : &km, 1, p, kd->D, n, kd->D, kd->page, false)
+                    : encode_tile_map(i ? &vm : &km, 2, p, kd->D, n, 64, kd->page, true);
+            if (rc != MOESTEP_OK) return rc;
+        }
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool wide = kd->D == 128;
     prof_begin(8, s);
     cudaError_t e;
-    if (kd->dtype == MOESTEP_F32)
-        e = wide ? launch_simple<MOESTEP_F32, 128>(a, grid, s) : launch_simple<MOESTEP_F32, 64>(a, grid, s);
-    else if (kd->dtype == MOESTEP_BF16)
-        e = wide ? launch_simple<MOESTEP_BF16, 128>(a, grid, s) : launch_simple<MOESTEP_BF16, 64>(a, grid, s);
+    if (f32)
+        e = wide ? launch_f32<128>(a, grid, s) : launch_f32<64>(a, grid, s);
     else
-        e = wide ? launch_simple<MOESTEP_FP8, 128>(a, grid, s) : launch_simple<MOESTEP_FP8, 64>(a, grid, s);
+        e = launch_attn_tc(kd->D, f8, km, vm, a, grid, s);
     prof_end(8, s);
     if (e == cudaSuccess) {
         count_launch();
         prof_begin(8, s);
-        if (kd->dtype == MOESTEP_F32)
+        if (f32)
             e = wide ? launch_join<float, 128>(a, grid, s) : launch_join<float, 64>(a, grid, s);
         else
             e = wide ? launch_join<bf16, 128>(a, grid, s) : launch_join<bf16, 64>(a, grid, s);

@@ -13,12 +13,15 @@
 // the workspace (a CTA has at most two such: the one it begins in and the one it ends in) and
 // the join launch adds them up in CTA order, so the result does not depend on timing.
 #pragma once
+#include <cuda.h>
+
 #include "common.cuh"
 #include "moestep.h"
 
 namespace moestep {
 
-constexpr int kAttnMaxCtas = 304;  // CTAs that the workspace has slots for
+constexpr int kAttnMaxCtas = 304;    // CTAs that the workspace has slots for: CUDA-core kernel,
+constexpr int kAttnMaxCtasTc = 160;  // tensor-core kernel
 
 struct AttnArgs {
     const void* q;
@@ -193,5 +196,9 @@ __device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnWalk& w) {
     ++w.k;
     return true;
 }
+
+// attention_tc.cu: bf16 or FP8 cache, row tiles of a.slot_rows (32, 64, 128 or 256)
+cudaError_t launch_attn_tc(int D, bool f8, const CUtensorMap& km, const CUtensorMap& vm, const AttnArgs& a, int grid,
+                           cudaStream_t s);
 
 }  // namespace moestep
