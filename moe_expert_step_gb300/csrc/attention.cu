@@ -24,7 +24,7 @@ constexpr int simple_smem() {
 template <int D>
 __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs a) {
     extern __shared__ float smf[];
-    __shared__ long long plan_sm[64];
+    __shared__ int plan_sm[40];
     float* sq = smf;                       // [16][D]
     float* sk = sq + kRT * D;              // [64][D + 4]
     float* sv = sk + kKT * (D + 4);        // [64][D + 4]
@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
     pdl_wait();
     const int tid = threadIdx.x;
     const AttnPlan plan = attn_plan<kKT, kSimpleThreads>(a, plan_sm);
+    if (tid == 0) attn_describe_join<kKT>(a, plan);
     constexpr int CW = D / 32;             // output columns of a thread
     AttnWalk w = attn_begin<kKT>(plan);
     while (attn_next<kKT>(a, w)) {
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
             const int rr = i / D, d = i - rr * D, row = row0 + rr;
             float x = 0.f;
             if (rr < nrows) {
-                const int qi = row / a.G, g = row - qi * a.G;
+                const int qi = attn_query(a, row), g = row - qi * a.G;
                 x = static_cast<const float*>(a.q)[(static_cast<long long>(w.r) * a.n_q + qi) * a.q_ld +
                                                    (h * a.G + g) * D + d];
             }
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int rr = 2 * sr + i;
-                    const int2 see = attn_sees(a, w.L, (row0 + min(rr, nrows - 1)) / a.G);
+                    const int2 see = attn_sees(a, w.L, attn_query(a, row0 + min(rr, nrows - 1)));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int jj = j0 + sc + 16 * j;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
             if (rr >= nrows) continue;
             const float m = s_m[rr], l = s_l[rr];
             if (w.whole) {
-                const int row = row0 + rr, qi = row / a.G, g = row - qi * a.G;
+                const int row = row0 + rr, qi = attn_query(a, row), g = row - qi * a.G;
                 const size_t o = (static_cast<size_t>(w.r) * a.n_q + qi) * a.Hq + h * a.G + g;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -178,72 +179,91 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
 
 // ---------------------------------------------------------------------------- join
 // Rows of a shared segment: m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m) / l over
-// its CTAs c in order.  Eight warps a block; WPR of them share a row (each every WPR-th part).
-template <typename T, int D, int WPR>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
-    __shared__ float s_f[8 / WPR][2 * kAttnMaxCtas];
+// its CTAs c in order.  What is read is what the attention launch just left in L2, so the time
+// is the latency of a row's parts: the launch's warps are spread over all rows of all joins, and
+// where there are more warps than rows, up to eight share a row, each taking every eighth part.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, int ctas) {
+    __shared__ int s_list[kAttnMaxCtas];  // CTAs that describe a join
+    __shared__ int s_n;
+    __shared__ float s_f[8][kAttnMaxCtas];
     __shared__ float s_o[8][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    const int4 j = a.joins[blockIdx.x];
-    if (j.x < 0) return;
-    const int h = j.y / a.row_tiles, row0 = (j.y - h * a.row_tiles) * a.slot_rows;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / WPR, part = warp % WPR;
-    const int rr = blockIdx.y * (8 / WPR) + team;
-    const bool on = rr < a.slot_rows && row0 + rr < a.rows;
-    const int c0 = j.z >> 1, n = j.w - c0 + 1;
-    float m = -INFINITY, l = 0.f;
-    auto slot = [&](int i) { return i == 0 ? j.z : 2 * (c0 + i); };
-    if (on) {
-        for (int i = lane; i < n; i += 32) {
-            const float2 ml = __ldcg(&a.part_ml[static_cast<size_t>(slot(i)) * a.slot_rows + rr]);
-            const float m1 = fmaxf(m, ml.x), ms = m1 == -INFINITY ? 0.f : m1;
-            l = l * exp2f(m - ms) + ml.y * exp2f(ml.x - ms);
-            m = m1;
+    if (warp == 0) {
+        int n = 0;
+        for (int i0 = 0; i0 < ctas; i0 += 32) {
+            const bool on = i0 + lane < ctas && __ldcg(&a.joins[i0 + lane].x) >= 0;
+            const unsigned b = __ballot_sync(0xffffffffu, on);
+            if (on) s_list[n + __popc(b & ((1u << lane) - 1))] = i0 + lane;
+            n += __popc(b);
         }
-        const float mm = warp_max(m), ms = mm == -INFINITY ? 0.f : mm;
-        l = warp_sum(l * exp2f(m - ms));
-        m = mm;
-        for (int i = lane; i < n; i += 32) {
-            const float2 ml = __ldcg(&a.part_ml[static_cast<size_t>(slot(i)) * a.slot_rows + rr]);
-            s_f[team][i] = exp2f(ml.x - ms);  // each of the team's warps writes the same values
-        }
-        __syncwarp();
+        if (lane == 0) s_n = n;
     }
-    constexpr int W = D / 32;
-    float acc[W] = {};
-    if (on) {
-#pragma unroll 4
-        for (int i = part; i < n; i += WPR) {
-            const float* p = a.part_o + (static_cast<size_t>(slot(i)) * a.slot_rows + rr) * D + lane * W;
-            const float f = s_f[team][i];
-            if (W == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
-                acc[0] += f * x.x, acc[1] += f * x.y, acc[W > 2 ? 2 : 0] += f * x.z, acc[W > 2 ? 3 : 0] += f * x.w;
-            } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
-                acc[0] += f * x.x, acc[1] += f * x.y;
+    __syncthreads();
+    const int rows = min(a.slot_rows, a.rows), work = s_n * rows;
+    int wpr = 8;  // warps per row
+    while (wpr > 1 && work * wpr > static_cast<int>(gridDim.x) * 8) wpr >>= 1;
+    const int team = warp / wpr, part = warp % wpr, teams = 8 / wpr;
+    for (int w0 = blockIdx.x * teams; w0 < work; w0 += gridDim.x * teams) {  // the same for the whole block
+        const int w = w0 + team, seg = w / rows, rr = w - seg * rows;
+        int4 j = make_int4(-1, 0, 0, 0);
+        if (w < work) j = __ldcg(&a.joins[s_list[seg]]);
+        const int h = j.y / a.row_tiles, row0 = (j.y - h * a.row_tiles) * a.slot_rows;
+        const bool on = j.x >= 0 && row0 + rr < a.rows;
+        const int c0 = j.z >> 1, n = j.w - c0 + 1;
+        auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? j.z : 2 * (c0 + i)) * a.slot_rows + rr; };
+        float m = -INFINITY, l = 0.f;
+        constexpr int W = D / 32;
+        float acc[W] = {};
+        if (on) {
+            for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(&a.part_ml[slot(i)]).x);
+            m = warp_max(m);
+            const float ms = m == -INFINITY ? 0.f : m;
+            for (int i = lane; i < n; i += 32) {
+                const float2 ml = __ldcg(&a.part_ml[slot(i)]);
+                const float f = exp2f(ml.x - ms);
+                l += ml.y * f;
+                s_f[warp][i] = f;
+            }
+            l = warp_sum(l);
+            __syncwarp();
+#pragma unroll 8
+            for (int i = part; i < n; i += wpr) {
+                const float* p = a.part_o + slot(i) * D + lane * W;
+                const float f = s_f[warp][i];
+                if constexpr (W == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+                    acc[0] += f * x.x, acc[1] += f * x.y, acc[2] += f * x.z, acc[3] += f * x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+                    acc[0] += f * x.x, acc[1] += f * x.y;
+                }
             }
         }
+        if (wpr > 1) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) s_o[warp][lane * W + i] = acc[i];
+            __syncthreads();
+            if (part == 0)
+                for (int k = 1; k < wpr; ++k)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) acc[i] += s_o[warp + k][lane * W + i];
+            __syncthreads();
+        }
+        __syncwarp();
+        if (!on || part != 0) continue;
+        const int row = row0 + rr, qi = attn_query(a, row), g = row - qi * a.G;
+        const size_t o = (static_cast<size_t>(j.x) * a.n_q + qi) * a.Hq + h * a.G + g;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* out = static_cast<T*>(a.out) + o * D + lane * W;
+#pragma unroll
+        for (int i = 0; i < W; ++i) out[i] = from_f32<T>(acc[i] * inv);
+        if (a.lse && lane == 0) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
-    if (WPR > 1) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) s_o[warp][lane * W + i] = acc[i];
-        __syncthreads();
-        if (part != 0) return;
-#pragma unroll
-        for (int k = 1; k < WPR; ++k)
-#pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] += s_o[warp + k][lane * W + i];
-    }
-    if (!on) return;
-    const int row = row0 + rr, qi = row / a.G, g = row - qi * a.G;
-    const size_t o = (static_cast<size_t>(j.x) * a.n_q + qi) * a.Hq + h * a.G + g;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* out = static_cast<T*>(a.out) + o * D + lane * W;
-#pragma unroll
-    for (int i = 0; i < W; ++i) out[i] = from_f32<T>(acc[i] * inv);
-    if (a.lse && lane == 0) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D>
@@ -255,9 +275,11 @@ cudaError_t launch_f32(const AttnArgs& a, int grid, cudaStream_t s) {
 }
 
 template <typename T, int D>
-cudaError_t launch_join(const AttnArgs& a, int grid, cudaStream_t s) {
-    const int rows = a.slot_rows < a.rows ? a.slot_rows : a.rows;
-    return launch_pdl(attn_join_kernel<T, D, 8>, dim3(grid, rows), dim3(256), 0, s, a);
+cudaError_t launch_join(const AttnArgs& a, int ctas, int sms, cudaStream_t s) {
+    // at most ctas - 1 segments are shared; eight blocks an SM are resident at once
+    const long long work = 1ll * ctas * (a.slot_rows < a.rows ? a.slot_rows : a.rows);
+    const int grid = work < 8ll * sms ? static_cast<int>(work) : 8 * sms;
+    return launch_pdl(attn_join_kernel<T, D>, dim3(grid), dim3(kJoinThreads), 0, s, a, ctas);
 }
 
 // Row tile of the kernel that runs (attention_tc.cu), and the CTAs that it may have: rows that
@@ -298,7 +320,7 @@ int check_attn(const moestep_kv_dims* kd, int R, int n_q) {
     // units and rows are counted in 31 bits
     const long long row_tiles = (1ll * n_q * (kd->Hq / kd->Hkv) + kRT - 1) / kRT;
     const long long tiles = (1ll * kd->max_pages * kd->page + kKT - 1) / kKT;
-    if (tiles * kd->Hkv > ((1ll << 31) - 1) / row_tiles) return MOESTEP_EUNSUPPORTED;
+    if (tiles * kd->Hkv > ((1ll << 31) - 1) / row_tiles / R) return MOESTEP_EUNSUPPORTED;
     if (1ll * R * n_q > ((1ll << 31) - 1) / kd->Hq) return MOESTEP_EUNSUPPORTED;
     return MOESTEP_OK;
 }
@@ -350,6 +372,7 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     a.Hq = kd->Hq;
     a.Hkv = kd->Hkv;
     a.G = kd->Hq / kd->Hkv;
+    a.g_magic = a.G > 1 ? static_cast<uint32_t>(((1ull << 32) + a.G - 1) / a.G) : 0;
     a.rows = n_q * a.G;
     a.slot_rows = L.slot_rows;
     a.row_tiles = (a.rows + L.slot_rows - 1) / L.slot_rows;
@@ -386,9 +409,9 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
         count_launch();
         prof_begin(8, s);
         if (f32)
-            e = wide ? launch_join<float, 128>(a, grid, s) : launch_join<float, 64>(a, grid, s);
+            e = wide ? launch_join<float, 128>(a, grid, sms, s) : launch_join<float, 64>(a, grid, sms, s);
         else
-            e = wide ? launch_join<bf16, 128>(a, grid, s) : launch_join<bf16, 64>(a, grid, s);
+            e = wide ? launch_join<bf16, 128>(a, grid, sms, s) : launch_join<bf16, 64>(a, grid, sms, s);
         prof_end(8, s);
         if (e == cudaSuccess) count_launch();
     }

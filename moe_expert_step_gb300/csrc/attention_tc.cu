@@ -19,8 +19,8 @@
 // than 8 (a factor 256, harmless in fp32 sums and bf16 weights): O is then rescaled in tensor
 // memory by the softmax warps, which is rare after the first tiles.
 //
-// Warps: 0-7 softmax (two warpgroups), 8 TMA producer, 9 MMA issuer (one lane), and with FP8
-// 10-13 converters (E4M3 code * 2^exp -> bf16, exact, into the swizzled operand buffers).
+// Warps: 0-7 softmax (two warpgroups), 8 TMA producer, 9-10 MMA issuers (one lane each, a
+// stream each), and with FP8 11-18 converters (E4M3 code * 2^exp -> bf16, exact, into the swizzled operand buffers).
 // Keys outside [lo, L) of the request reach no result: their scores are replaced by -inf, and
 // their V rows, which a zero weight would still multiply (NaN), are zeroed in shared memory.
 // Every wait is bounded (timeout -> error word, orderly teardown).
@@ -45,24 +45,57 @@ struct Cfg {
     static constexpr int kRows = 32 << MODE;
     static constexpr int kRep = MODE == 0 ? 4 : MODE == 1 ? 2 : 1;
     static constexpr int kCols = kKeys / kRep;            // keys of a tile that a lane handles
-    static constexpr int kParts = kTwo ? 1 : 2 * kRep;    // (m, l, O) of a row
-    static constexpr int kThreads = F8 ? 448 : 320;
+    static constexpr int kThreads = F8 ? 608 : 352;
     static constexpr int kTile = kKeys * D * 2;           // bytes of a bf16 operand tile
     static constexpr int kQ = 128 * D * 2;
-    static constexpr int kSide = kTwo ? kQ : 32768;       // second query tile, or the merge buffer
+    // query tile(s); with one row tile also the merge buffer, once the segment's scores are done
+    static constexpr int kFront = kTwo ? 2 * kQ : 32768;
     static constexpr int kRaw = kKeys * D;                // bytes of an FP8 tile
-    static constexpr int kBufs = F8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-    static constexpr int kRaws = F8 ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int kBufs = (F8 ? (kTwo ? 3 : 4) : (kTwo ? 5 : 6)) * (128 / D);
+    static constexpr int kRaws = F8 ? 4 * (128 / D) : 0;
     static constexpr int kMisc = 1024 + kRaws * kKeys;    // plan, barriers, exponents
-    static constexpr int kSmem = 1024 + kQ + kSide + kBufs * kTile + kRaws * kRaw + kMisc;
+    static constexpr int kSmem = 1024 + kFront + kBufs * kTile + kRaws * kRaw + kMisc;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
+// The FP8 converters leave every four columns in the order 0, 2, 1, 3 (see there): queries are put
+// into the same order, and the output's columns back.
+__device__ __forceinline__ uint4 to_fp8_order(uint4 x) {
+    return make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x5410),
+                      __byte_perm(x.z, x.w, 0x7632));
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool F8>
+__device__ __forceinline__ void load_output(uint32_t taddr, float* x) {
+    tc::tmem_ld32(taddr, x);
+    if (F8) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float t = x[i + 1];
+            x[i + 1] = x[i + 2];
+            x[i + 2] = t;
+        }
+    }
+}
+
+// A warp's bounded waits.  Lane 0 alone polls the barrier (a poll is served lane by lane: with all
+// 32 a wait on a phase long complete took 300 cycles).  Once one gave up, the rest return at once.
 struct Waits {
     volatile int* abort;
     uint64_t tmo;
-    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-        return tc::mbar_wait(bar, parity, abort, tmo);
+    bool ok;
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
+        if (ok) {
+            int r = 1;
+            if ((threadIdx.x & 31) == 0) r = tc::mbar_wait(bar, parity, abort, tmo);
+            ok = __shfl_sync(0xffffffffu, r, 0) != 0;
+            __syncwarp();
+        }
+        return ok;
     }
 };
 
@@ -93,12 +126,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sq = sm;
-    uint8_t* side = sq + C::kQ;
-    uint8_t* ring = side + C::kSide;
+    uint8_t* ring = sq + C::kFront;
     uint8_t* raw = ring + NB * C::kTile;
     uint8_t* exps = raw + C::kRaws * C::kRaw;              // [kRaws][128]
-    long long* plan_sm = reinterpret_cast<long long*>(exps + C::kRaws * kKeys);  // 64 x 8 bytes
-    uint64_t* full = reinterpret_cast<uint64_t*>(plan_sm + 64);
+    int* plan_sm = reinterpret_cast<int*>(exps + C::kRaws * kKeys);  // 40
+    uint64_t* full = reinterpret_cast<uint64_t*>(plan_sm + 40);
     uint64_t* empty = full + NB;
     uint64_t* rfull = empty + NB;
     uint64_t* rempty = rfull + C::kRaws;
@@ -107,21 +139,21 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     uint64_t* o_full = p_full + 2;
     uint64_t* q_full = o_full + 2;
     uint64_t* fin = q_full + 1;
-    uint64_t* meet = fin + 1;  // the eight softmax warps, between the steps of a merge
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(meet + 1);
+    uint64_t* go = fin + 1;  // the first stream has begun a segment (two row tiles)
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(go + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
     int* zero_flag = abort_flag + 1;
-    static_assert((2 * NB + 2 * C::kRaws + 9) * 8 + 12 + 512 <= 1024, "misc area");
+    static_assert((2 * NB + 2 * C::kRaws + 9) * 8 + 12 + 160 <= 1024, "misc area");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NB; ++i) {
-            tc::mbar_init(&full[i], F8 ? 4 : 1);
-            tc::mbar_init(&empty[i], 1);
+            tc::mbar_init(&full[i], F8 ? 8 : 1);
+            tc::mbar_init(&empty[i], 2);  // both MMA issuers
         }
         for (int i = 0; i < C::kRaws; ++i) {
             tc::mbar_init(&rfull[i], 1);
-            tc::mbar_init(&rempty[i], 4);
+            tc::mbar_init(&rempty[i], 8);
         }
         for (int g = 0; g < 2; ++g) {
             tc::mbar_init(&s_full[g], 1);
@@ -129,8 +161,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             tc::mbar_init(&o_full[g], 1);
         }
         tc::mbar_init(q_full, 8);
-        tc::mbar_init(fin, 1);
-        tc::mbar_init(meet, 8);
+        tc::mbar_init(fin, 2);
+        tc::mbar_init(go, 4);
         *abort_flag = 0;
         *zero_flag = 0;
         tc::fence_mbar_init();
@@ -148,8 +180,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     pdl_trigger();
     pdl_wait();
     const AttnPlan plan = attn_plan<kKeys, C::kThreads>(a, plan_sm);
-    const Waits wait{abort_flag, a.timeout_ns};
-    bool ok = true;
+    Waits wait{abort_flag, a.timeout_ns, true};
     int err_bits = 0;
 
     if (warp < 8) {
@@ -161,62 +192,71 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const int lrow = C::kTwo ? g * 128 + w * 32 + lane               // row within the row tile
                                  : (w * 32 + lane) & (C::kRows - 1);
         const int col0 = part * C::kCols;
-        uint32_t turns = 0, segs_g = 0, meets = 0;
-        auto sync8 = [&]() -> bool {  // all eight warps; false if the wait gave up
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(meet);
-            return __all_sync(0xffffffffu, wait(meet, meets++ & 1));
-        };
+        uint32_t turns = 0, segs_g = 0;
+        // The eight warps meet at a hardware barrier between the steps of a merge.  They pass it
+        // equally often whatever happens: after a wait that gave up they go through the rest of
+        // their segments without waiting (their results are then unspecified).
+        auto sync8 = [&]() { tc::named_bar_sync(1, 256); };
         AttnWalk s = attn_begin<kKeys>(plan);
-        while (ok && attn_next<kKeys>(a, s)) {
+        while (attn_next<kKeys>(a, s)) {
             const int h = s.seg / a.row_tiles, row0 = (s.seg - h * a.row_tiles) * C::kRows;
             const int nrows = min(C::kRows, a.rows - row0);
             {   // query rows into the swizzled operand tile(s), copies for lanes that repeat rows
-                constexpr int kChunks = D / 8, NT = C::kTwo ? 128 : 256;
-                uint8_t* dst = C::kTwo ? (g == 0 ? sq : side) : sq;
-                for (int i = (C::kTwo ? threadIdx.x & 127 : threadIdx.x); i < 128 * kChunks; i += NT) {
-                    const int m = i / kChunks, c = i - m * kChunks;
-                    const int row = C::kTwo ? g * 128 + m : m & (C::kRows - 1);
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row < nrows) {
-                        const int rr = row0 + row, qi = rr / a.G;
-                        x = __ldg(reinterpret_cast<const uint4*>(
-                            static_cast<const bf16*>(a.q) + (static_cast<long long>(s.r) * a.n_q + qi) * a.q_ld +
-                            (h * a.G + rr - qi * a.G) * D + c * 8));
+                constexpr int kChunks = D / 8, NT = C::kTwo ? 128 : 256, kBatch = 128 * kChunks / NT;
+                uint8_t* dst = sq + (C::kTwo ? g * C::kQ : 0);
+                const int c = threadIdx.x % kChunks, m0 = (threadIdx.x & (NT - 1)) / kChunks;
+                constexpr int kStep = NT / kChunks;  // rows apart
+                // (all loads in flight at once, ahead of the key and value copies that follow)
+                {
+                    uint4 x[kBatch];
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int m = m0 + b * kStep, row = C::kTwo ? g * 128 + m : m & (C::kRows - 1);
+                        x[b] = make_uint4(0, 0, 0, 0);
+                        if (row < nrows) {
+                            const int rr = row0 + row, qi = attn_query(a, rr);
+                            x[b] = __ldg(reinterpret_cast<const uint4*>(
+                                static_cast<const bf16*>(a.q) + (static_cast<long long>(s.r) * a.n_q + qi) * a.q_ld +
+                                (h * a.G + rr - qi * a.G) * D + c * 8));
+                            if (F8) x[b] = to_fp8_order(x[b]);
+                        }
                     }
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = x;
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int m = m0 + b * kStep;
+                        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = x[b];
+                    }
                 }
                 tc::fence_proxy_async_smem();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(q_full);
             }
-            const int2 see = attn_sees(a, s.L, (row0 + min(lrow, nrows - 1)) / a.G);
+            const int2 see = attn_sees(a, s.L, attn_query(a, row0 + min(lrow, nrows - 1)));
             float m = -INFINITY, l = 0.f;
             const int step = C::kTwo ? 1 : 2, first = s.tile + (C::kTwo ? 0 : g);
             int turn = 0;
             for (int t = first; t < s.tile + s.tiles; t += step, ++turn) {
-                if (!__all_sync(0xffffffffu, wait(&s_full[g], turns & 1))) {
-                    ok = false;
-                    break;
-                }
+                wait(&s_full[g], turns & 1);
                 ++turns;
                 tc::fence_after_sync();
                 const int lo = see.x - (t * kKeys + col0), hi = see.y - (t * kKeys + col0);
                 const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < C::kCols);
-                constexpr bool kKeep = C::kCols <= 64;  // scores held in registers between the two passes
-                float v[kKeep ? C::kCols : 32];
+                constexpr bool kKeep = C::kCols == 32;  // scores held in registers between the two passes
+                float v[32];
                 float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < C::kCols; c += 32) {
-                    float* x = v + (kKeep ? c : 0);
-                    tc::tmem_ld32(t_s + col0 + c, x);
+                auto fetch = [&](int c) {  // 32 of the lane's scores, the hidden ones replaced
+                    tc::tmem_ld32(t_s + col0 + c, v);
                     if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = (c + i >= lo && c + i < hi) ? x[i] : -INFINITY;
+                        for (int i = 0; i < 32; ++i) v[i] = (c + i >= lo && c + i < hi) ? v[i] : -INFINITY;
                     }
+                };
+#pragma unroll 1
+                for (int c = 0; c < C::kCols; c += 32) {
+                    fetch(c);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[i]);
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
                 }
                 mx *= a.scale_log2;
                 const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
@@ -238,187 +278,200 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     }
                 }
                 const float ms = m == -INFINITY ? 0.f : m;
-                if (C::kRep > 1) {  // the other copies' keys
-                    const uint32_t z[16] = {};
-#pragma unroll
-                    for (int c = 0; c < kKeys / 2; c += 16)
-                        if (c / (C::kCols / 2) != part) tc::tmem_st16_async(t_s + c, z);
-                }
-#pragma unroll
+                if (C::kTwo && g == 0 && turn == 0 && lane == 0) tc::mbar_arrive(go);
+#pragma unroll 1
                 for (int c = 0; c < C::kCols; c += 32) {
-                    float* x = v + (kKeep ? c : 0);
-                    if (!kKeep) {
-                        tc::tmem_ld32(t_s + col0 + c, x);
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = (c + i >= lo && c + i < hi) ? x[i] : -INFINITY;
-                        }
-                    }
+                    if (!kKeep) fetch(c);
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float p0 = tc::exp2_fast(fmaf(x[2 * i], a.scale_log2, -ms));
-                        const float p1 = tc::exp2_fast(fmaf(x[2 * i + 1], a.scale_log2, -ms));
+                        const float p0 = tc::exp2_fast(fmaf(v[2 * i], a.scale_log2, -ms));
+                        const float p1 = tc::exp2_fast(fmaf(v[2 * i + 1], a.scale_log2, -ms));
                         l += p0 + p1;
                         p[i] = tc::pack_bf16(p0, p1);
                     }
                     tc::tmem_st16_async(t_s + (col0 + c) / 2, p);
+                }
+                if (C::kRep > 1) {  // the other copies' keys (after the lane's own scores have been read)
+                    const uint32_t z[16] = {};
+#pragma unroll
+                    for (int c = 0; c < kKeys / 2; c += 16)
+                        if (c / (C::kCols / 2) != part) tc::tmem_st16_async(t_s + c, z);
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&p_full[g]);
             }
-            if (!ok) break;
             if (turn > 0) {
-                if (!__all_sync(0xffffffffu, wait(&o_full[g], segs_g & 1))) {
-                    ok = false;
-                    break;
-                }
+                wait(&o_full[g], segs_g & 1);
                 ++segs_g;
                 tc::fence_after_sync();
             }
             const int slot = 2 * blockIdx.x + (s.k > 0);
             // row `rr` of the row tile: where it goes
             auto where = [&](int rr) {
-                const int row = row0 + rr, qi = row / a.G;
+                const int row = row0 + rr, qi = attn_query(a, row);
                 return (static_cast<size_t>(s.r) * a.n_q + qi) * a.Hq + h * a.G + row - qi * a.G;
             };
             if constexpr (C::kTwo) {
+                // Each warp passes its 32 rows through its own part of the query tile, which is no
+                // longer read, so that whole lines are written.
                 const bool on = lrow < nrows;
-                const size_t o = on ? where(lrow) : 0, at = static_cast<size_t>(slot) * a.slot_rows + lrow;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                constexpr int kPart = 32 * D * 2;  // bytes: 32 rows of bf16, or half of their fp32 columns
+                uint8_t* mine = sq + g * C::kQ + w * kPart;
+                const int wrow0 = g * 128 + w * 32, wrows = min(32, nrows - wrow0);
+                constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;  // lanes of a row, 16 bytes each
+                const int sr = lane / kLanes, sc = lane % kLanes;
+                const int halves = s.whole ? 1 : 2;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float x[32];
+                for (int half = 0; half < halves; ++half) {
+#pragma unroll 1
+                    for (int c = 0; c < (s.whole ? D : D / 2); c += 32) {
+                        float x[32];
+                        __syncwarp();
+                        load_output<F8>(t_o + half * (D / 2) + c, x);
+                        uint8_t* r = mine + lane * D * 2;
+                        if (s.whole) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4*>(r + (((c / 8 + i) ^ (lane & 7)) << 4)) =
+                                    make_uint4(tc::pack_bf16(x[8 * i] * inv, x[8 * i + 1] * inv),
+                                               tc::pack_bf16(x[8 * i + 2] * inv, x[8 * i + 3] * inv),
+                                               tc::pack_bf16(x[8 * i + 4] * inv, x[8 * i + 5] * inv),
+                                               tc::pack_bf16(x[8 * i + 6] * inv, x[8 * i + 7] * inv));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<float4*>(r + (((c / 4 + i) ^ (lane & 7)) << 4)) =
+                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        }
+                    }
                     __syncwarp();
-                    tc::tmem_ld32(t_o + c, x);
-                    if (!on) continue;
-                    if (s.whole) {
-                        uint4* d = reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + o * D + c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            d[i] = make_uint4(tc::pack_bf16(x[8 * i] * inv, x[8 * i + 1] * inv),
-                                              tc::pack_bf16(x[8 * i + 2] * inv, x[8 * i + 3] * inv),
-                                              tc::pack_bf16(x[8 * i + 4] * inv, x[8 * i + 5] * inv),
-                                              tc::pack_bf16(x[8 * i + 6] * inv, x[8 * i + 7] * inv));
-                    } else {
-                        float4* d = reinterpret_cast<float4*>(a.part_o + at * D + c);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) d[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+#pragma unroll 4
+                    for (int i = 0; i < 32; i += kRowsAtOnce) {
+                        const int rr = i + sr;
+                        if (rr >= wrows) continue;
+                        const uint4 x = *reinterpret_cast<const uint4*>(mine + rr * D * 2 + ((sc ^ (rr & 7)) << 4));
+                        if (s.whole)
+                            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + where(wrow0 + rr) * D + sc * 8) = x;
+                        else
+                            *reinterpret_cast<uint4*>(a.part_o + (static_cast<size_t>(slot) * a.slot_rows + wrow0 + rr) * D +
+                                                      half * (D / 2) + sc * 4) = x;
                     }
                 }
-                if (on && s.whole && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-                if (on && !s.whole) a.part_ml[at] = make_float2(m, l);
+                __syncwarp();
+                if (on && s.whole && a.lse) a.lse[where(lrow)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                if (on && !s.whole) a.part_ml[static_cast<size_t>(slot) * a.slot_rows + lrow] = make_float2(m, l);
             } else {
-                // merge the row's parts: p = stream * copies + copy
+                // merge the row's (m, l, O): p = stream * copies + copy
+                constexpr int kParts = 2 * C::kRep;
                 const int p = g * C::kRep + part;
-                float2* ml = reinterpret_cast<float2*>(side);  // [parts][rows]
+                float2* ml = reinterpret_cast<float2*>(sq);  // [parts][rows]
+                sync8();  // neither stream reads the query tile any more
                 ml[p * C::kRows + lrow] = make_float2(m, l);
-                if (!sync8()) {
-                    ok = false;
-                    break;
-                }
+                sync8();
                 float M = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < C::kParts; ++i) M = fmaxf(M, ml[i * C::kRows + lrow].x);
+                for (int i = 0; i < kParts; ++i) M = fmaxf(M, ml[i * C::kRows + lrow].x);
                 const float Ms = M == -INFINITY ? 0.f : M;
                 const float f = tc::exp2_fast(m - Ms);
-                // the row that this thread puts together, and its sum
-                constexpr int kPer = C::kRows * 32 / 256;  // columns of a 32-wide slice, a multiple of 4
-                const int orow = threadIdx.x / (32 / kPer), ocol = (threadIdx.x % (32 / kPer)) * kPer;
+                // The buffer holds 32768 / (parts * rows * 4) columns of every part's valid rows, a
+                // multiple of 32: all of D at once where rows are few.  Threads of a group of
+                // 256 / rows put together a row's columns, four at a time.
+                const int wide = C::kRows == 32 && nrows <= 8 ? min(D, 128) : C::kRows == 32 && nrows <= 16 ? 64 : 32;
+                const int trow = C::kRows == 32 && nrows <= 8 ? 8 : C::kRows == 32 && nrows <= 16 ? 16 : C::kRows;
+                const int tpr = 256 / trow, orow = threadIdx.x / tpr, ocol = (threadIdx.x % tpr) * 4;
                 float OM = -INFINITY, ol = 0.f;
 #pragma unroll
-                for (int i = 0; i < C::kParts; ++i) OM = fmaxf(OM, ml[i * C::kRows + orow].x);
+                for (int i = 0; i < kParts; ++i) OM = fmaxf(OM, ml[i * C::kRows + orow].x);
                 const float OMs = OM == -INFINITY ? 0.f : OM;
 #pragma unroll
-                for (int i = 0; i < C::kParts; ++i) {
+                for (int i = 0; i < kParts; ++i) {
                     const float2 q = ml[i * C::kRows + orow];
                     ol += q.y * tc::exp2_fast(q.x - OMs);
                 }
                 const bool on = orow < nrows;
                 const size_t o = on ? where(orow) : 0, at = static_cast<size_t>(slot) * a.slot_rows + orow;
                 const float inv = ol == 0.f ? 0.f : 1.f / ol;
-                float* buf = reinterpret_cast<float*>(side);  // [parts][rows][32], 16-byte pieces swizzled by row
+                float* buf = reinterpret_cast<float*>(sq);  // [parts][trow][wide], 16-byte pieces swizzled by row
+                sync8();  // the statistics have been read
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float x[32];
-                    __syncwarp();
-                    if (turn > 0) {
-                        tc::tmem_ld32(t_o + c, x);
-                    } else {
+                for (int c = 0; c < D; c += wide) {
+                    float* b = buf + (p * trow + lrow) * wide;
+#pragma unroll 1
+                    for (int cc = 0; cc < wide; cc += 32) {
+                        float x[32];
+                        __syncwarp();
+                        if (turn > 0) {
+                            load_output<F8>(t_o + c + cc, x);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
-                    }
-                    if (!sync8()) {  // the statistics, or the slice before, have been read
-                        ok = false;
-                        break;
-                    }
-                    float* b = buf + (p * C::kRows + lrow) * 32;
-                    if (lrow < nrows) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<float4*>(b + ((i ^ (lrow & 7)) << 2)) =
-                                make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
-                    }
-                    if (!sync8()) {
-                        ok = false;
-                        break;
-                    }
-                    if (!on) continue;
-#pragma unroll
-                    for (int k = 0; k < kPer; k += 4) {
-                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int i = 0; i < C::kParts; ++i) {
-                            const float4 z = *reinterpret_cast<const float4*>(
-                                buf + (i * C::kRows + orow) * 32 + ((((ocol + k) >> 2) ^ (orow & 7)) << 2));
-                            y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
+                            for (int i = 0; i < 32; ++i) x[i] = 0.f;
                         }
-                        if (s.whole)
-                            *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + o * D + c + ocol + k) =
-                                make_uint2(tc::pack_bf16(y.x * inv, y.y * inv), tc::pack_bf16(y.z * inv, y.w * inv));
-                        else
-                            *reinterpret_cast<float4*>(a.part_o + at * D + c + ocol + k) = y;
+                        if (lrow < nrows) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<float4*>(b + cc + ((i ^ (lrow & 7)) << 2)) =
+                                    make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
+                        }
                     }
+                    sync8();
+                    if (on) {
+                        for (int k = ocol; k < wide; k += 4 * tpr) {
+                            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                            const int kk = (k & ~31) + ((((k & 31) >> 2) ^ (orow & 7)) << 2);
+#pragma unroll
+                            for (int i = 0; i < kParts; ++i) {
+                                const float4 z = *reinterpret_cast<const float4*>(buf + (i * trow + orow) * wide + kk);
+                                y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
+                            }
+                            if (s.whole)
+                                *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + o * D + c + k) = make_uint2(
+                                    tc::pack_bf16(y.x * inv, y.y * inv), tc::pack_bf16(y.z * inv, y.w * inv));
+                            else
+                                *reinterpret_cast<float4*>(a.part_o + at * D + c + k) = y;
+                        }
+                    }
+                    sync8();  // the slice has been read
                 }
-                if (!ok) break;
                 if (on && ocol == 0) {
                     if (!s.whole) a.part_ml[at] = make_float2(OM, ol);
                     else if (a.lse) a.lse[o] = ol == 0.f ? -INFINITY : (OM + log2f(ol)) * 0.69314718055994531f;
                 }
-                if (!sync8()) ok = false;  // the next segment's statistics reuse the buffer
             }
         }
-        if (!ok) err_bits = kErrTimeoutEpilogue;
+        if (!wait.ok) err_bits = kErrTimeoutEpilogue;
     } else if (warp == 8) {
         // ------------------------------------------------------------ TMA producer
         uint64_t* const bf = F8 ? rfull : full;
         uint64_t* const be = F8 ? rempty : empty;
         constexpr int N = F8 ? NR : NB;
         uint32_t it = 0;
-        const int page = 1 << a.page_log2;
+        const int page = 1 << a.page_log2, pages = kKeys >> a.page_log2;
         AttnWalk s = attn_begin<kKeys>(plan);
-        while (ok && attn_next<kKeys>(a, s)) {
+        while (wait.ok && attn_next<kKeys>(a, s)) {
             const int h = s.seg / a.row_tiles, lo = attn_lo(a, s.L);
             const int32_t* tab = a.table + static_cast<long long>(s.r) * a.max_pages;
-            ok = each_buffer<C::kTwo>(s.tiles, [&](bool is_v, int tt) -> bool {
-                const int p0 = (s.tile + tt) * kKeys + lane * page;  // this lane's page
-                int id = -1;
-                if (lane * page < kKeys && p0 < s.L && p0 + page > lo) {
-                    id = __ldg(&tab[p0 >> a.page_log2]);
-                    if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_pages)) {
-                        id = -1;
-                        record_error(a.err, kErrBadInput);
-                    }
+            // lane i: the first pool row of page i of key tile t, -1 for a page that is not loaded
+            auto rows_of = [&](int t) -> int {
+                const int p0 = (s.tile + t) * kKeys + lane * page;
+                if (t >= s.tiles || lane >= pages || p0 >= s.L || p0 + page <= lo) return -1;
+                const int id = __ldg(&tab[p0 >> a.page_log2]);
+                if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_pages)) {
+                    record_error(a.err, kErrBadInput);
+                    return -1;
                 }
-                const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                return (id * a.Hkv + h) << a.page_log2;
+            };
+            auto load = [&](bool is_v, int y) -> bool {
+                const unsigned on = __ballot_sync(0xffffffffu, y >= 0);
                 const int b = it % N;
-                if (!__all_sync(0xffffffffu, wait(&be[b], ((it / N) & 1) ^ 1u))) return false;
-                if (lane == 0) tc::mbar_arrive_expect_tx(&bf[b], n * page * (F8 ? D + 1 : 2 * D));
+                if (!wait(&be[b], ((it / N) & 1) ^ 1u)) return false;
+                if (lane == 0) tc::mbar_arrive_expect_tx(&bf[b], __popc(on) * page * (F8 ? D + 1 : 2 * D));
                 __syncwarp();
-                if (id >= 0) {
-                    const int y = (id * a.Hkv + h) << a.page_log2;
+                if (y >= 0) {
                     const CUtensorMap* map = is_v ? &vmap : &kmap;
                     if (F8) {
                         tc::tma_load_2d(raw + b * C::kRaw + lane * page * D, map, &bf[b], 0, y);
@@ -432,98 +485,123 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 }
                 ++it;
                 return true;
-            });
+            };
+            // the order of each_buffer, every page number read once and ahead of its use
+            int y0 = rows_of(0), y1 = rows_of(1), y2 = C::kTwo ? -1 : rows_of(2);
+            if (C::kTwo) {
+                for (int t = 0; t < s.tiles; ++t) {
+                    const int next = rows_of(t + 2);
+                    if (!load(false, y0) || !load(true, y0)) break;
+                    y0 = y1;
+                    y1 = next;
+                }
+            } else if (load(false, y0) && (s.tiles < 2 || load(false, y1))) {
+                for (int t = 0; t < s.tiles; ++t) {
+                    const int next = rows_of(t + 3);
+                    if (!load(true, y0) || (t + 2 < s.tiles && !load(false, y2))) break;
+                    y0 = y1;
+                    y1 = y2;
+                    y2 = next;
+                }
+            }
         }
-        if (!ok) err_bits = kErrTimeoutProducer;
+        if (!wait.ok) err_bits = kErrTimeoutProducer;
         // copies in flight land before the CTA ends
-        for (uint32_t i = it > N ? it - N : 0; i < it; ++i) tc::mbar_wait(&bf[i % N], (i / N) & 1, zero_flag, kTeardown);
-    } else if (warp == 9) {
-        // ------------------------------------------------------------ MMA issuer
-        const uint32_t idesc_s = tc::idesc_bf16(128, kKeys), idesc_o = tc::idesc_bf16(128, D) | tc::kIdescTransposeB;
-        uint32_t it = 0, segs = 0, p_cnt[2] = {0, 0};
-        int buf = 0;
-        auto acquire = [&]() -> bool {  // the next buffer in the ring
-            buf = it % NB;
-            const bool got = __all_sync(0xffffffffu, wait(&full[buf], (it / NB) & 1));
-            ++it;
-            return got;
+        for (uint32_t i = it > N ? it - N : 0; lane == 0 && i < it; ++i)
+            tc::mbar_wait(&bf[i % N], (i / N) & 1, zero_flag, kTeardown);
+        __syncwarp();
+    } else if (warp < 11) {
+        // ------------------------------------------------------------ MMA issuers, one a stream
+        // (An MMA costs its issuing thread about 85 cycles, the tensor cores 64.)  Lane 0 runs the
+        // role; the other lanes only help where V rows are zeroed.  With two row tiles the second
+        // stream's first scores wait until the first stream's weights are under way, so that one's MMAs
+        // run under the other's exponentials: in step with each other both waited for both.
+        // After a wait that gave up lane 0 goes through the rest without waiting or issuing.
+        const int g = warp - 9;
+        if (g == 1 && lane == 0) attn_describe_join<kKeys>(a, plan);
+        __syncwarp();
+        constexpr uint32_t idesc_s = tc::idesc_bf16(128, kKeys), idesc_o = tc::idesc_bf16(128, D) | tc::kIdescTransposeB;
+        const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128;
+        const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(sq + (C::kTwo ? g * C::kQ : 0)));
+        const uint64_t kd0 = tc::sdesc_k_sw128(tc::smem_addr(ring)), vd0 = tc::sdesc_mn_sw128(tc::smem_addr(ring), 16384);
+        uint32_t it = 0, segs = 0, turns = 0;
+        bool ok = true;
+        auto wait0 = [&](uint64_t* bar, uint32_t parity) {
+            if (lane == 0) ok = ok && tc::mbar_wait(bar, parity, abort_flag, a.timeout_ns);
         };
         AttnWalk s = attn_begin<kKeys>(plan);
-        while (ok && attn_next<kKeys>(a, s)) {
-            const int N = C::kTwo ? 2 * s.tiles : s.tiles, lo = attn_lo(a, s.L);
-            if (!__all_sync(0xffffffffu, wait(q_full, segs & 1))) {
-                ok = false;
-                break;
-            }
+        while (attn_next<kKeys>(a, s)) {
+            const int lo = attn_lo(a, s.L);
+            wait0(q_full, segs & 1);
+            if (C::kTwo && g == 1) wait0(go, segs & 1);
             ++segs;
-            int kb = 0, vb = 0;
-            auto scores = [&](int n) -> bool {  // S of turn n
-                const int g = n & 1;
-                if (!C::kTwo || g == 0) {
-                    if (!acquire()) return false;
-                    kb = buf;
+            // this stream's turns: every key tile, or every other one
+            const int last = C::kTwo ? s.tiles - 1 : s.tiles - 1 - ((s.tiles - 1 - g) & 1);
+            bool begun = false;
+            each_buffer<C::kTwo>(s.tiles, [&](bool is_v, int t) -> bool {
+                const int b = it % NB;
+                // Every buffer is waited for and released in order, the other stream's too: a parity
+                // names a phase only as long as nobody skips one or falls two behind.
+                wait0(&full[b], (it / NB) & 1);
+                ++it;
+                if (!C::kTwo && ((t ^ g) & 1)) {
+                    if (lane == 0) tc::mbar_arrive(&empty[b]);
+                    return true;
                 }
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t qa = tc::smem_addr(C::kTwo && g == 1 ? side : sq);
-                    const uint32_t ka = tc::smem_addr(ring + kb * C::kTile);
+                if (!is_v) {
+                    if (lane == 0 && ok) {
+                        tc::fence_after_sync();
+                        const uint64_t kd = kd0 + b * (C::kTile >> 4);  // (descriptors count in 16 bytes)
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                        tc::mma_bf16(tmem + g * 128, tc::sdesc_k_sw128(qa + off), tc::sdesc_k_sw128(ka + off), idesc_s,
-                                     k > 0);
-                    }
-                    tc::mma_commit(&s_full[g]);
-                    if (!C::kTwo || g == 1) tc::mma_commit(&empty[kb]);
-                }
-                __syncwarp();
-                return true;
-            };
-            ok = scores(0) && (N < 2 || scores(1));
-            for (int n = 0; ok && n < N; ++n) {
-                const int g = n & 1;
-                if (!C::kTwo || g == 0) {
-                    if (!acquire()) {
-                        ok = false;
-                        break;
-                    }
-                    vb = buf;
-                    if (!F8) {  // V rows that no query sees
-                        const int j0 = (s.tile + (C::kTwo ? n >> 1 : n)) * kKeys;
-                        const int za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
-                        if (za > 0 || zb < kKeys) {
-                            uint8_t* v = ring + vb * C::kTile;
-                            for (int i = lane; i < kKeys * (D / 8); i += 32) {
-                                const int row = (i >> 3) & (kKeys - 1);
-                                if (row < za || row >= zb)
-                                    *reinterpret_cast<uint4*>(v + (i >> 10) * 16384 + row * 128 + (i & 7) * 16) =
-                                        make_uint4(0, 0, 0, 0);
-                            }
-                            tc::fence_proxy_async_smem();
-                            __syncwarp();
+                        for (int k = 0; k < D / 16; ++k) {
+                            const int off = (k >> 2) * 1024 + (k & 3) * 2;
+                            tc::mma_bf16(t_s, qd + off, kd + off, idesc_s, k > 0);
                         }
+                        tc::mma_commit(&s_full[g]);
+                        tc::mma_commit(&empty[b]);
                     }
+                    return true;
                 }
-                if (!__all_sync(0xffffffffu, wait(&p_full[g], p_cnt[g] & 1))) {
-                    ok = false;
-                    break;
+                const int j0 = (s.tile + t) * kKeys, za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
+                // V's keys in steps of 16: those that some query sees, one step at least; the rows
+                // of the first and last step that none sees are zeroed (by both streams alike)
+                const int k0 = min(za >> 4, 7), k1 = max((zb + 15) >> 4, k0 + 1);
+                if (!F8 && ((za & 15) != 0 || (zb & 15) != 0 || zb <= 0)) {
+                    __syncwarp();
+                    uint8_t* v = ring + b * C::kTile;
+#pragma unroll 1
+                    for (int i = lane; i < 2 * 16 * (D / 8); i += 32) {
+                        const int r = (i >> 3) & 31, row = r < 16 ? k0 * 16 + r : k1 * 16 - 32 + r;
+                        if (row < za || row >= zb)
+                            *reinterpret_cast<uint4*>(v + (i >> 8) * 16384 + row * 128 + (i & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                ++p_cnt[g];
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t va = tc::smem_addr(ring + vb * C::kTile);
+                wait0(&p_full[g], turns++ & 1);
+                if (lane == 0 && ok) {
+                    tc::fence_after_sync();
+                    const uint64_t vd = vd0 + b * (C::kTile >> 4);
+                    if (k0 == 0 && k1 == 8) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        tc::mma_f16_tmem_a(tmem + 256 + g * 128, tmem + g * 128 + k * 8,
-                                           tc::sdesc_mn_sw128(va + k * 2048, 16384), idesc_o, n >= 2 || k > 0);
-                    if (!C::kTwo || g == 1) tc::mma_commit(&empty[vb]);
-                    if (n + 2 >= N) tc::mma_commit(&o_full[g]);
+                        for (int k = 0; k < 8; ++k)
+                            tc::mma_f16_tmem_a(t_o, t_s + k * 8, vd + k * 128, idesc_o, begun || k > 0);
+                    } else {
+#pragma unroll 1
+                        for (int k = k0; k < k1; ++k)
+                            tc::mma_f16_tmem_a(t_o, t_s + k * 8, vd + k * 128, idesc_o, begun || k > k0);
+                    }
+                    tc::mma_commit(&empty[b]);
+                    if (t == last) tc::mma_commit(&o_full[g]);
                 }
-                __syncwarp();
-                if (n + 2 < N) ok = scores(n + 2);
-            }
+                begun = true;
+                return true;
+            });
         }
-        if (!ok) err_bits = kErrTimeoutMma;
+        wait.ok = ok;
+        if (!wait.ok) err_bits = kErrTimeoutMma;
+        __syncwarp();
         if (lane == 0) {  // MMAs in flight complete before the tensor memory is freed
             tc::mma_commit(fin);
             tc::mbar_wait(fin, 0, zero_flag, kTeardown);
@@ -534,43 +612,70 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         // Eight (D = 128) or four lanes take a key's codes, 16 each, and write 32 bytes of the
         // 128-byte swizzled bf16 tile; the lanes of the second 64-column box store their two
         // 16-byte pieces in the other order, so that no two of a row's lanes meet in a bank.
-        const int cw = warp - 10;
+        // A code s eeee mmm placed as s 0000eeee mmm0000 is the bf16 value code * 2^-120,
+        // subnormals included, so one exact multiplication by 2^(exp - 127 + 120) dequantises two
+        // codes (two of them where that factor passes bf16's range).  The four codes of a word
+        // are placed as bytes 0 and 2, then 1 and 3, which is the column order 0, 2, 1, 3.  The
+        // conversion instruction would share its unit with the exponentials (2300 cycles a
+        // tile instead of ~1000); NaN codes, which the placement does not keep, are rare and patched.
+        const int cw = warp - 11;
         constexpr int L = D / 16, RPI = 32 / L;  // lanes a row, rows a step
         const int lr = lane / L, lc = lane % L;
         uint32_t it = 0;
         AttnWalk s = attn_begin<kKeys>(plan);
-        while (ok && attn_next<kKeys>(a, s)) {
+        while (wait.ok && attn_next<kKeys>(a, s)) {
             const int lo = attn_lo(a, s.L);
-            ok = each_buffer<C::kTwo>(s.tiles, [&](bool, int tt) -> bool {
+            each_buffer<C::kTwo>(s.tiles, [&](bool, int tt) -> bool {
                 const int rb = it % NR, b = it % NB;
-                if (!__all_sync(0xffffffffu, wait(&rfull[rb], (it / NR) & 1))) return false;
-                if (!__all_sync(0xffffffffu, wait(&empty[b], ((it / NB) & 1) ^ 1u))) return false;
+                if (!wait(&rfull[rb], (it / NR) & 1)) return false;
                 const int j0 = (s.tile + tt) * kKeys;
                 const int za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
-                const uint8_t* src = raw + rb * C::kRaw;
+                const uint8_t* src = raw + rb * C::kRaw + (cw * 16 + lr) * D + lc * 16;
+                const uint8_t* se = exps + rb * kKeys + cw * 16 + lr;
+                constexpr int STEPS = 16 / RPI;
+                if (!wait(&empty[b], ((it / NB) & 1) ^ 1u)) return false;
                 uint8_t* dst = ring + b * C::kTile + (lc >> 2) * 16384;
-#pragma unroll 4
-                for (int i = 0; i < 32 / RPI; ++i) {
-                    const int row = cw * 32 + i * RPI + lr;
-                    uint4 x = *reinterpret_cast<const uint4*>(src + row * D + lc * 16);
-                    const int e = exps[rb * kKeys + row];
-                    const float sc = e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 5.8774717541114375e-39f;
-                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[8];
+                const int c = (lc & 3) * 2;
+                const bool flip = lc >= 4;
+                uint4 xn = *reinterpret_cast<const uint4*>(src);
+                uint32_t en = se[0];
+                // (compact code: unrolled in full, this loop ran at the speed of its instruction fetches)
+#pragma unroll 1
+                for (int i = 0; i < STEPS; ++i) {
+                    const uint4 xi = xn;
+                    const uint32_t ei = en;
+                    if (i + 1 < STEPS) {
+                        xn = *reinterpret_cast<const uint4*>(src + (i + 1) * RPI * D);
+                        en = se[(i + 1) * RPI];
+                    }
+                    const int row = cw * 16 + i * RPI + lr, sw = row & 7;
+                    const uint32_t in[4] = {xi.x, xi.y, xi.z, xi.w};
+                    const uint32_t f1 = min(ei + 120u, 254u);  // exponent field of the factor
+                    const uint32_t s1 = f1 << 7 | f1 << 23;
+                    uint32_t y[8], odd_one = 0;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t h2 = tc::e4m3x2_to_f16x2(in[k >> 1], 2 * (k & 1));
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                        y[k] = tc::pack_bf16(f.x * sc, f.y * sc);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t w = in[k];
+                        y[2 * k] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), s1);
+                        y[2 * k + 1] = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s1);
+                        odd_one |= (w & 0x7f7f7f7fu) + 0x01010101u;  // bit 7 of a NaN code's byte
+                    }
+                    if ((odd_one & 0x80808080u) | (ei > 134u)) {
+                        const uint32_t f2 = ei > 134u ? ei - 134u + 127u : 127u, s2 = f2 << 7 | f2 << 23;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t w = in[k >> 1] >> (8 * (k & 1));
+                            y[k] = mul_bf16x2(y[k], s2);
+                            if ((w & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
+                            if ((w & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
+                        }
                     }
                     if (row < za || row >= zb) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) y[k] = 0;
                     }
                     uint8_t* d = dst + row * 128;
-                    const int c = (lc & 3) * 2, sw = row & 7;
                     const uint4 y0 = make_uint4(y[0], y[1], y[2], y[3]), y1 = make_uint4(y[4], y[5], y[6], y[7]);
-                    const bool flip = lc >= 4;
                     *reinterpret_cast<uint4*>(d + (((c + flip) ^ sw) << 4)) = flip ? y1 : y0;
                     *reinterpret_cast<uint4*>(d + (((c + !flip) ^ sw) << 4)) = flip ? y0 : y1;
                 }
@@ -584,7 +689,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 return true;
             });
         }
-        if (!ok) err_bits = kErrTimeoutProducer;
+        if (!wait.ok) err_bits = kErrTimeoutProducer;
     }
     if (err_bits) {
         *abort_flag = 1;

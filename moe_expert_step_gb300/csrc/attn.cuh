@@ -3,8 +3,8 @@
 //
 // The work is a list of units: one tile of keys for one tile of query rows of one
 // (request, key-value head).  Units are numbered request by request, then head, then row tile, then key
-// tile, and CTA c of A takes units [W c / A, W (c+1) / A): every CTA streams the same number
-// of key tiles whatever the requests' lengths are.  The lengths are on the device, so every
+// tile, and every CTA takes the same number of them in a row (one more or less): it streams as
+// many key tiles as any other whatever the requests' lengths are.  The lengths are on the device, so every
 // CTA works the division out from kv_len itself (a block-wide scan over the requests; an
 // empty request counts one unit, whose only effect is to write its empty rows).
 //
@@ -36,9 +36,10 @@ struct AttnArgs {
     float* lse;
     float* part_o;    // [2 * CTAs][slot_rows][D]
     float2* part_ml;  // [2 * CTAs][slot_rows]: maximum (times scale * log2 e), sum
-    int4* joins;      // [CTAs]: {request or -1, head * row tiles + row tile, first CTA, last CTA}
+    int4* joins;      // [CTAs]: {request or -1, head * row tiles + row tile, first CTA's slot, last CTA}
     int* err;
     int R, n_q, Hq, Hkv, G;
+    uint32_t g_magic;  // ceil(2^32 / G); 0 for G = 1
     int rows;        // n_q * G: query rows of one (request, key-value head)
     int row_tiles;
     int slot_rows;
@@ -52,6 +53,11 @@ struct AttnArgs {
 __device__ __forceinline__ int attn_len(const AttnArgs& a, int r) {
     const int L = __ldg(&a.kv_len[r]), most = a.max_pages << a.page_log2;
     return min(max(L, 0), most);
+}
+
+// Query of a row: row / G, exact while row * G < 2^32
+__device__ __forceinline__ int attn_query(const AttnArgs& a, int row) {
+    return a.g_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.g_magic)) : row;
 }
 
 // Positions [lo, hi) that some query of the request sees
@@ -71,89 +77,91 @@ __device__ __forceinline__ int2 attn_tiles(const AttnArgs& a, int L) {  // first
     return make_int2(t0, max(1, (L + KT - 1) / KT - t0));
 }
 
-// First unit of CTA c, and the CTA that holds unit u, of W units over A CTAs
-__device__ __forceinline__ long long attn_first(long long W, int A, int c) { return W * c / A; }
-__device__ __forceinline__ int attn_owner(long long W, int A, long long u) {
-    return static_cast<int>(((u + 1) * A - 1) / W);
-}
+// The division: of W units over A CTAs the first W % A take one more than the rest.
+struct AttnShare {
+    int A, base, extra;
+    __device__ __forceinline__ AttnShare(int W, int grid) : A(min(W, grid)), base(W / A), extra(W - base * A) {}
+    __device__ __forceinline__ int first(int c) const { return c * base + min(c, extra); }  // of CTA c
+    __device__ __forceinline__ int owner(int u) const {                                     // of unit u
+        const int cut = extra * (base + 1);
+        return u < cut ? u / (base + 1) : extra + (u - cut) / base;
+    }
+};
 
 // One CTA's place in the list
 struct AttnPlan {
-    long long W;  // units in all
-    int A;        // CTAs that have some
-    int begin_r;  // request of the CTA's first unit
-    int begin_o;  // that unit's number within the request
+    int W;        // units in all
+    int first;    // the CTA's first unit
+    int begin_r;  // that unit's request
+    int begin_o;  // and its number within the request
     int count;    // the CTA's units
 };
 
-// Executed by every thread of the block (NT threads); `sm`: 64 long longs of shared memory.
+// Executed by every thread of the block (NT threads); `sm`: 40 ints of shared memory.
 template <int KT, int NT>
-__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, long long* sm) {
+__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int* sm) {
     const int tid = threadIdx.x, per = (a.R + NT - 1) / NT, heads = a.Hkv * a.row_tiles;
     const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
-    long long mine = 0;
+    int mine = 0;
     for (int r = r0; r < r1; ++r) {
         const int L = attn_len(a, r);
         if (blockIdx.x == 0 && L != __ldg(&a.kv_len[r])) record_error(a.err, kErrBadInput);
-        mine += static_cast<long long>(attn_tiles<KT>(a, L).y) * heads;
+        mine += attn_tiles<KT>(a, L).y * heads;
     }
-    long long incl = mine;  // block-wide inclusive scan
+    int incl = mine;  // block-wide inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if ((tid & 31) >= o) incl += v;
     }
     if ((tid & 31) == 31) sm[tid >> 5] = incl;
     __syncthreads();
-    long long before = 0, W = 0;
+    int before = 0, W = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
         if (w == (tid >> 5)) before = W;
         W += sm[w];
     }
     incl += before;
+    const AttnShare sh(W, gridDim.x);
     AttnPlan p;
     p.W = W;
-    p.A = static_cast<int>(min(W, static_cast<long long>(gridDim.x)));
     const int c = blockIdx.x;
-    const long long first = c < p.A ? attn_first(W, p.A, c) : W;
-    p.count = c < p.A ? static_cast<int>(attn_first(W, p.A, c + 1) - first) : 0;
-    int* out = reinterpret_cast<int*>(sm + 40);
-    if (p.count > 0 && first >= incl - mine && first < incl) {
-        long long at = incl - mine;
+    p.first = c < sh.A ? sh.first(c) : W;
+    p.count = c < sh.A ? sh.first(c + 1) - p.first : 0;
+    if (p.count > 0 && p.first >= incl - mine && p.first < incl) {
+        int at = incl - mine;
         for (int r = r0; r < r1; ++r) {
-            const long long n = static_cast<long long>(attn_tiles<KT>(a, attn_len(a, r)).y) * heads;
-            if (first < at + n) {
-                out[0] = r;
-                out[1] = static_cast<int>(first - at);
+            const int n = attn_tiles<KT>(a, attn_len(a, r)).y * heads;
+            if (p.first < at + n) {
+                sm[32] = r;
+                sm[33] = p.first - at;
                 break;
             }
             at += n;
         }
     }
     __syncthreads();
-    p.begin_r = p.count > 0 ? out[0] : 0;
-    p.begin_o = p.count > 0 ? out[1] : 0;
-    // the join of a segment is described by the CTA that is the second to work on it
-    if (tid == 0) {
-        int4 j = make_int4(-1, 0, 0, 0);
-        if (p.count > 0) {
-            const int nt = attn_tiles<KT>(a, attn_len(a, p.begin_r)).y, seg = p.begin_o / nt, t = p.begin_o - seg * nt;
-            if (t > 0) {
-                const int c0 = attn_owner(W, p.A, first - t);
-                if (c0 == c - 1) j = make_int4(p.begin_r, seg, c0, attn_owner(W, p.A, first - t + nt - 1));
-            }
-        }
-        a.joins[c] = j;
-        if (p.count > 0 && j.x >= 0) {
-            // whether the segment is the first CTA's own first one (its slot 0) or not (slot 1)
-            const int nt = attn_tiles<KT>(a, attn_len(a, p.begin_r)).y;
-            const int t = p.begin_o - (p.begin_o / nt) * nt;
-            const int slot1 = attn_first(W, p.A, j.z) != first - t;
-            a.joins[c].z = j.z * 2 + slot1;
+    p.begin_r = p.count > 0 ? sm[32] : 0;
+    p.begin_o = p.count > 0 ? sm[33] : 0;
+    return p;
+}
+
+// Executed by one thread: the join of a segment is described by the second CTA that works on it.
+template <int KT>
+__device__ __forceinline__ void attn_describe_join(const AttnArgs& a, const AttnPlan& p) {
+    int4 j = make_int4(-1, 0, 0, 0);
+    const int c = blockIdx.x;
+    if (p.count > 0) {
+        const int nt = attn_tiles<KT>(a, attn_len(a, p.begin_r)).y, seg = p.begin_o / nt, t = p.begin_o - seg * nt;
+        if (t > 0) {
+            const AttnShare sh(p.W, gridDim.x);
+            const int start = p.first - t, c0 = sh.owner(start);
+            // the segment is the first one of CTA c0 (its slot 0) or not (slot 1)
+            if (c0 == c - 1) j = make_int4(p.begin_r, seg, 2 * c0 + (sh.first(c0) != start), sh.owner(start + nt - 1));
         }
     }
-    return p;
+    a.joins[c] = j;
 }
 
 // A CTA's walk over its segments.
