@@ -45,6 +45,7 @@ struct Cfg {
     static constexpr int kRows = 32 << MODE;
     static constexpr int kRep = MODE == 0 ? 4 : MODE == 1 ? 2 : 1;
     static constexpr int kCols = kKeys / kRep;            // keys of a tile that a lane handles
+    static constexpr int kSteps = kRep == 1 ? 2 : 1;      // parts in which its weights are handed to the MMAs
     static constexpr int kThreads = F8 ? 608 : 352;
     static constexpr int kTile = kKeys * D * 2;           // bytes of a bf16 operand tile
     static constexpr int kQ = 128 * D * 2;
@@ -86,12 +87,12 @@ __device__ __forceinline__ void load_output(uint32_t taddr, float* x) {
 // 32 a wait on a phase long complete took 300 cycles).  Once one gave up, the rest return at once.
 struct Waits {
     volatile int* abort;
-    uint64_t tmo;
+    long long limit;  // cycles
     bool ok;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
         if (ok) {
             int r = 1;
-            if ((threadIdx.x & 31) == 0) r = tc::mbar_wait(bar, parity, abort, tmo);
+            if ((threadIdx.x & 31) == 0) r = tc::mbar_poll(bar, parity, abort, limit);
             ok = __shfl_sync(0xffffffffu, r, 0) != 0;
             __syncwarp();
         }
@@ -136,14 +137,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     uint64_t* rempty = rfull + C::kRaws;
     uint64_t* s_full = rempty + C::kRaws;
     uint64_t* p_full = s_full + 2;
-    uint64_t* o_full = p_full + 2;
+    uint64_t* o_full = p_full + 4;  // p_full: [stream][half]
     uint64_t* q_full = o_full + 2;
     uint64_t* fin = q_full + 1;
     uint64_t* go = fin + 1;  // the first stream has begun a segment (two row tiles)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(go + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
     int* zero_flag = abort_flag + 1;
-    static_assert((2 * NB + 2 * C::kRaws + 9) * 8 + 12 + 160 <= 1024, "misc area");
+    static_assert((2 * NB + 2 * C::kRaws + 11) * 8 + 12 + 160 <= 1024, "misc area");
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         }
         for (int g = 0; g < 2; ++g) {
             tc::mbar_init(&s_full[g], 1);
-            tc::mbar_init(&p_full[g], 4);
+            for (int q = 0; q < C::kSteps; ++q) tc::mbar_init(&p_full[g * 2 + q], 4);
             tc::mbar_init(&o_full[g], 1);
         }
         tc::mbar_init(q_full, 8);
@@ -176,11 +177,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_holder;
+    // (from one lane, so that the compiler knows it for uniform: an MMA whose accumulator address is
+    // not issues in 97 cycles instead of 67)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     pdl_trigger();
     pdl_wait();
     const AttnPlan plan = attn_plan<kKeys, C::kThreads>(a, plan_sm);
-    Waits wait{abort_flag, a.timeout_ns, true};
+    // (two cycles a nanosecond: the SM clock stays below 2.1 GHz)
+    Waits wait{abort_flag, static_cast<long long>(a.timeout_ns < (1ull << 61) ? 2 * a.timeout_ns : 1ull << 62), true};
     int err_bits = 0;
 
     if (warp < 8) {
@@ -291,6 +295,12 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         p[i] = tc::pack_bf16(p0, p1);
                     }
                     tc::tmem_st16_async(t_s + (col0 + c) / 2, p);
+                    if (C::kSteps > 1 && (c & 32)) {  // the MMAs of these 64 keys can begin
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&p_full[g * 2 + (c >> 6)]);
+                    }
                 }
                 if (C::kRep > 1) {  // the other copies' keys (after the lane's own scores have been read)
                     const uint32_t z[16] = {};
@@ -298,10 +308,12 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     for (int c = 0; c < kKeys / 2; c += 16)
                         if (c / (C::kCols / 2) != part) tc::tmem_st16_async(t_s + c, z);
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&p_full[g]);
+                if (C::kSteps == 1) {
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&p_full[g * 2]);
+                }
             }
             if (turn > 0) {
                 wait(&o_full[g], segs_g & 1);
@@ -454,50 +466,69 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         while (wait.ok && attn_next<kKeys>(a, s)) {
             const int h = s.seg / a.row_tiles, lo = attn_lo(a, s.L);
             const int32_t* tab = a.table + static_cast<long long>(s.r) * a.max_pages;
-            // lane i: the first pool row of page i of key tile t, -1 for a page that is not loaded
-            auto rows_of = [&](int t) -> int {
-                const int p0 = (s.tile + t) * kKeys + lane * page;
-                if (t >= s.tiles || lane >= pages || p0 >= s.L || p0 + page <= lo) return -1;
-                const int id = __ldg(&tab[p0 >> a.page_log2]);
-                if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_pages)) {
-                    record_error(a.err, kErrBadInput);
-                    return -1;
-                }
-                return (id * a.Hkv + h) << a.page_log2;
+            // Page numbers come 32 at a time, a lane each, the next 32 while these are used: a
+            // table read behind the copies in flight takes as long as they do.
+            const int pg0 = (s.tile * kKeys) >> a.page_log2, pg_lo = lo >> a.page_log2;
+            const int pg_end = (min(s.L, (s.tile + s.tiles) * kKeys) + page - 1) >> a.page_log2;
+            auto table = [&](int at) -> int {  // entries at .. at + 31
+                const int pg = at + lane;
+                return pg >= pg_lo && pg < pg_end ? __ldg(&tab[pg]) : -2;
             };
-            auto load = [&](bool is_v, int y) -> bool {
-                const unsigned on = __ballot_sync(0xffffffffu, y >= 0);
+            int chunk = pg0, ids = table(chunk), ids_next = table(chunk + 32);
+            // lane i: page i of key tile t, -2 for one that is not loaded; tiles in ascending order
+            auto page_of = [&](int t) -> int {
+                const int at = pg0 + t * pages;
+                if (at >= chunk + 32) {
+                    chunk += 32;
+                    ids = ids_next;
+                    ids_next = table(chunk + 32);
+                }
+                const int id = __shfl_sync(0xffffffffu, ids, (at - chunk + lane) & 31);
+                return t < s.tiles && lane < pages ? id : -2;
+            };
+            auto load = [&](bool is_v, int id) -> bool {
                 const int b = it % N;
                 if (!wait(&be[b], ((it / N) & 1) ^ 1u)) return false;
+                const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages);
+                if (!good && id != -2) record_error(a.err, kErrBadInput);
+                const unsigned on = __ballot_sync(0xffffffffu, good);
+                const int y = good ? (id * a.Hkv + h) << a.page_log2 : 0;
                 if (lane == 0) tc::mbar_arrive_expect_tx(&bf[b], __popc(on) * page * (F8 ? D + 1 : 2 * D));
                 __syncwarp();
-                if (y >= 0) {
-                    const CUtensorMap* map = is_v ? &vmap : &kmap;
-                    if (F8) {
-                        tc::tma_load_2d(raw + b * C::kRaw + lane * page * D, map, &bf[b], 0, y);
-                        tc::bulk_load(exps + b * kKeys + lane * page, (is_v ? a.v_exp : a.k_exp) + y, page, &bf[b]);
-                    } else {
+                const CUtensorMap* map = is_v ? &vmap : &kmap;
+                const uint8_t* ex = is_v ? a.v_exp : a.k_exp;
+#pragma unroll 1
+                for (int p = 0; p < pages; ++p) {
+                    const int yp = __shfl_sync(0xffffffffu, y, p);
+                    if (!(on >> p & 1)) continue;
+                    if (tc::elect_one()) {
+                        if (F8) {
+                            tc::tma_load_2d(raw + b * C::kRaw + p * page * D, map, &bf[b], 0, yp);
+                            tc::bulk_load(exps + b * kKeys + p * page, ex + yp, page, &bf[b]);
+                        } else {
 #pragma unroll
-                        for (int half = 0; half < D / 64; ++half)
-                            tc::tma_load_2d(ring + b * C::kTile + half * 16384 + lane * page * 128, map, &bf[b],
-                                            half * 64, y);
+                            for (int half = 0; half < D / 64; ++half)
+                                tc::tma_load_2d(ring + b * C::kTile + half * 16384 + p * page * 128, map, &bf[b],
+                                                half * 64, yp);
+                        }
                     }
+                    __syncwarp();
                 }
                 ++it;
                 return true;
             };
-            // the order of each_buffer, every page number read once and ahead of its use
-            int y0 = rows_of(0), y1 = rows_of(1), y2 = C::kTwo ? -1 : rows_of(2);
+            // the order of each_buffer, every page number read once, ahead of its use
+            int y0 = page_of(0), y1 = page_of(1), y2 = C::kTwo ? -1 : page_of(2);
             if (C::kTwo) {
                 for (int t = 0; t < s.tiles; ++t) {
-                    const int next = rows_of(t + 2);
+                    const int next = page_of(t + 2);
                     if (!load(false, y0) || !load(true, y0)) break;
                     y0 = y1;
                     y1 = next;
                 }
             } else if (load(false, y0) && (s.tiles < 2 || load(false, y1))) {
                 for (int t = 0; t < s.tiles; ++t) {
-                    const int next = rows_of(t + 3);
+                    const int next = page_of(t + 3);
                     if (!load(true, y0) || (t + 2 < s.tiles && !load(false, y2))) break;
                     y0 = y1;
                     y1 = y2;
@@ -512,11 +543,9 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         __syncwarp();
     } else if (warp < 11) {
         // ------------------------------------------------------------ MMA issuers, one a stream
-        // (An MMA costs its issuing thread about 85 cycles, the tensor cores 64.)  Lane 0 runs the
-        // role; the other lanes only help where V rows are zeroed.  With two row tiles the second
-        // stream's first scores wait until the first stream's weights are under way, so that one's MMAs
-        // run under the other's exponentials: in step with each other both waited for both.
-        // After a wait that gave up lane 0 goes through the rest without waiting or issuing.
+        // With two row tiles the second stream's first scores wait until the first stream's weights
+        // are under way, so that one's MMAs run under the other's exponentials: in step with each
+        // other both waited for both.
         const int g = warp - 9;
         if (g == 1 && lane == 0) attn_describe_join<kKeys>(a, plan);
         __syncwarp();
@@ -525,33 +554,29 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(sq + (C::kTwo ? g * C::kQ : 0)));
         const uint64_t kd0 = tc::sdesc_k_sw128(tc::smem_addr(ring)), vd0 = tc::sdesc_mn_sw128(tc::smem_addr(ring), 16384);
         uint32_t it = 0, segs = 0, turns = 0;
-        bool ok = true;
-        auto wait0 = [&](uint64_t* bar, uint32_t parity) {
-            if (lane == 0) ok = ok && tc::mbar_wait(bar, parity, abort_flag, a.timeout_ns);
-        };
         AttnWalk s = attn_begin<kKeys>(plan);
-        while (attn_next<kKeys>(a, s)) {
+        while (wait.ok && attn_next<kKeys>(a, s)) {
             const int lo = attn_lo(a, s.L);
-            wait0(q_full, segs & 1);
-            if (C::kTwo && g == 1) wait0(go, segs & 1);
+            if (!wait(q_full, segs & 1)) break;
+            if (C::kTwo && g == 1 && !wait(go, segs & 1)) break;
             ++segs;
             // this stream's turns: every key tile, or every other one
             const int last = C::kTwo ? s.tiles - 1 : s.tiles - 1 - ((s.tiles - 1 - g) & 1);
-            bool begun = false;
+            uint32_t begun = 0;
             each_buffer<C::kTwo>(s.tiles, [&](bool is_v, int t) -> bool {
                 const int b = it % NB;
                 // Every buffer is waited for and released in order, the other stream's too: a parity
                 // names a phase only as long as nobody skips one or falls two behind.
-                wait0(&full[b], (it / NB) & 1);
+                if (!wait(&full[b], (it / NB) & 1)) return false;
                 ++it;
                 if (!C::kTwo && ((t ^ g) & 1)) {
                     if (lane == 0) tc::mbar_arrive(&empty[b]);
                     return true;
                 }
+                tc::fence_after_sync();
                 if (!is_v) {
-                    if (lane == 0 && ok) {
-                        tc::fence_after_sync();
-                        const uint64_t kd = kd0 + b * (C::kTile >> 4);  // (descriptors count in 16 bytes)
+                    const uint64_t kd = kd0 + b * (C::kTile >> 4);  // (descriptors count in 16 bytes)
+                    if (tc::elect_one()) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             const int off = (k >> 2) * 1024 + (k & 3) * 2;
@@ -560,6 +585,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         tc::mma_commit(&s_full[g]);
                         tc::mma_commit(&empty[b]);
                     }
+                    __syncwarp();
                     return true;
                 }
                 const int j0 = (s.tile + t) * kKeys, za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
@@ -567,7 +593,6 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 // of the first and last step that none sees are zeroed (by both streams alike)
                 const int k0 = min(za >> 4, 7), k1 = max((zb + 15) >> 4, k0 + 1);
                 if (!F8 && ((za & 15) != 0 || (zb & 15) != 0 || zb <= 0)) {
-                    __syncwarp();
                     uint8_t* v = ring + b * C::kTile;
 #pragma unroll 1
                     for (int i = lane; i < 2 * 16 * (D / 8); i += 32) {
@@ -579,39 +604,52 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                 }
-                wait0(&p_full[g], turns++ & 1);
-                if (lane == 0 && ok) {
-                    tc::fence_after_sync();
-                    const uint64_t vd = vd0 + b * (C::kTile >> 4);
-                    if (k0 == 0 && k1 == 8) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            tc::mma_f16_tmem_a(t_o, t_s + k * 8, vd + k * 128, idesc_o, begun || k > 0);
-                    } else {
+                const uint64_t vd = vd0 + b * (C::kTile >> 4);
+                constexpr int kPer = 8 / C::kSteps;
 #pragma unroll 1
-                        for (int k = k0; k < k1; ++k)
-                            tc::mma_f16_tmem_a(t_o, t_s + k * 8, vd + k * 128, idesc_o, begun || k > k0);
+                for (int q = 0; q < C::kSteps; ++q) {  // every part is waited for, so that none falls behind
+                    if (!wait(&p_full[g * 2 + q], turns & 1)) return false;
+                    tc::fence_after_sync();
+                    const uint32_t tp = t_s + q * kPer * 8;
+                    const uint64_t vq = vd + q * kPer * 128;
+                    if (tc::elect_one()) {
+                        if (k0 == 0 && k1 == 8) {
+#pragma unroll
+                            for (int k = 0; k < kPer; ++k) {
+                                tc::mma_f16_tmem_a(t_o, tp + k * 8, vq + k * 128, idesc_o, begun);
+                                begun = 1;
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int k = max(k0 - q * kPer, 0); k < min(k1 - q * kPer, kPer); ++k) {
+                                tc::mma_f16_tmem_a(t_o, tp + k * 8, vq + k * 128, idesc_o, begun);
+                                begun = 1;
+                            }
+                        }
+                        if (q == C::kSteps - 1) {
+                            tc::mma_commit(&empty[b]);
+                            if (t == last) tc::mma_commit(&o_full[g]);
+                        }
                     }
-                    tc::mma_commit(&empty[b]);
-                    if (t == last) tc::mma_commit(&o_full[g]);
+                    __syncwarp();
                 }
-                begun = true;
+                ++turns;
                 return true;
             });
         }
-        wait.ok = ok;
         if (!wait.ok) err_bits = kErrTimeoutMma;
         __syncwarp();
-        if (lane == 0) {  // MMAs in flight complete before the tensor memory is freed
+        if (tc::elect_one()) {  // MMAs in flight complete before the tensor memory is freed
             tc::mma_commit(fin);
             tc::mbar_wait(fin, 0, zero_flag, kTeardown);
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ FP8 converters
-        // Eight (D = 128) or four lanes take a key's codes, 16 each, and write 32 bytes of the
-        // 128-byte swizzled bf16 tile; the lanes of the second 64-column box store their two
-        // 16-byte pieces in the other order, so that no two of a row's lanes meet in a bank.
+        // Eight lanes take 64 codes of a key, 8 each, and write the 16-byte piece of the 128-byte
+        // swizzled bf16 tile that holds them; each lane does that twice a step (D = 128: the key's
+        // other half, the halves in the other order for odd keys, so that two keys' lanes read
+        // different banks; D = 64: four keys further on).
         // A code s eeee mmm placed as s 0000eeee mmm0000 is the bf16 value code * 2^-120,
         // subnormals included, so one exact multiplication by 2^(exp - 127 + 120) dequantises two
         // codes (two of them where that factor passes bf16's range).  The four codes of a word
@@ -619,8 +657,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         // conversion instruction would share its unit with the exponentials (2300 cycles a
         // tile instead of ~1000); NaN codes, which the placement does not keep, are rare and patched.
         const int cw = warp - 11;
-        constexpr int L = D / 16, RPI = 32 / L;  // lanes a row, rows a step
-        const int lr = lane / L, lc = lane % L;
+        constexpr int kStepRows = D == 128 ? 4 : 8, kStepsC = 16 / kStepRows;  // of a warp's 16 keys
+        const int lr = lane >> 3, lc = lane & 7;
         uint32_t it = 0;
         AttnWalk s = attn_begin<kKeys>(plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
@@ -628,56 +666,50 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             each_buffer<C::kTwo>(s.tiles, [&](bool, int tt) -> bool {
                 const int rb = it % NR, b = it % NB;
                 if (!wait(&rfull[rb], (it / NR) & 1)) return false;
+                if (!wait(&empty[b], ((it / NB) & 1) ^ 1u)) return false;
                 const int j0 = (s.tile + tt) * kKeys;
                 const int za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
-                const uint8_t* src = raw + rb * C::kRaw + (cw * 16 + lr) * D + lc * 16;
-                const uint8_t* se = exps + rb * kKeys + cw * 16 + lr;
-                constexpr int STEPS = 16 / RPI;
-                if (!wait(&empty[b], ((it / NB) & 1) ^ 1u)) return false;
-                uint8_t* dst = ring + b * C::kTile + (lc >> 2) * 16384;
-                const int c = (lc & 3) * 2;
-                const bool flip = lc >= 4;
-                uint4 xn = *reinterpret_cast<const uint4*>(src);
-                uint32_t en = se[0];
+                const bool partial = za > 0 || zb < kKeys;
                 // (compact code: unrolled in full, this loop ran at the speed of its instruction fetches)
-#pragma unroll 1
-                for (int i = 0; i < STEPS; ++i) {
-                    const uint4 xi = xn;
-                    const uint32_t ei = en;
-                    if (i + 1 < STEPS) {
-                        xn = *reinterpret_cast<const uint4*>(src + (i + 1) * RPI * D);
-                        en = se[(i + 1) * RPI];
-                    }
-                    const int row = cw * 16 + i * RPI + lr, sw = row & 7;
-                    const uint32_t in[4] = {xi.x, xi.y, xi.z, xi.w};
-                    const uint32_t f1 = min(ei + 120u, 254u);  // exponent field of the factor
-                    const uint32_t s1 = f1 << 7 | f1 << 23;
-                    uint32_t y[8], odd_one = 0;
+#pragma unroll 2
+                for (int i = 0; i < kStepsC; ++i) {
+                    uint2 x[2];
+                    uint32_t ex[2];
+                    int row[2], half[2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t w = in[k];
-                        y[2 * k] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), s1);
-                        y[2 * k + 1] = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s1);
-                        odd_one |= (w & 0x7f7f7f7fu) + 0x01010101u;  // bit 7 of a NaN code's byte
+                    for (int u = 0; u < 2; ++u) {
+                        half[u] = D == 128 ? u ^ (lr & 1) : 0;
+                        row[u] = cw * 16 + i * kStepRows + lr + (D == 128 ? 0 : 4 * u);
+                        x[u] = *reinterpret_cast<const uint2*>(raw + rb * C::kRaw + row[u] * D + half[u] * 64 + lc * 8);
+                        if (D == 64 || u == 0) ex[u] = exps[rb * kKeys + row[u]];
+                        if (D == 128 && u == 1) ex[1] = ex[0];
                     }
-                    if ((odd_one & 0x80808080u) | (ei > 134u)) {
-                        const uint32_t f2 = ei > 134u ? ei - 134u + 127u : 127u, s2 = f2 << 7 | f2 << 23;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t w = in[k >> 1] >> (8 * (k & 1));
-                            y[k] = mul_bf16x2(y[k], s2);
-                            if ((w & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
-                            if ((w & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t f1 = min(ex[u] + 120u, 254u);  // exponent field of the factor
+                        const uint32_t s1 = f1 * 0x00800080u;
+                        uint32_t y[4], nan = 0;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t w = k ? x[u].y : x[u].x;
+                            y[2 * k] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), s1);
+                            y[2 * k + 1] = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s1);
+                            nan |= (w & 0x7f7f7f7fu) + 0x01010101u;  // bit 7 of a NaN code's byte
                         }
-                    }
-                    if (row < za || row >= zb) {
+                        if ((nan & 0x80808080u) | (ex[u] > 134u)) {
+                            const uint32_t f2 = ex[u] > 134u ? ex[u] - 134u + 127u : 127u;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] = 0;
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t w = (k < 2 ? x[u].x : x[u].y) >> (8 * (k & 1));
+                                y[k] = mul_bf16x2(y[k], f2 * 0x00800080u);
+                                if ((w & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
+                                if ((w & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
+                            }
+                        }
+                        if (partial && (row[u] < za || row[u] >= zb)) y[0] = y[1] = y[2] = y[3] = 0;
+                        *reinterpret_cast<uint4*>(ring + b * C::kTile + half[u] * 16384 + row[u] * 128 +
+                                                  ((lc ^ (row[u] & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
-                    uint8_t* d = dst + row * 128;
-                    const uint4 y0 = make_uint4(y[0], y[1], y[2], y[3]), y1 = make_uint4(y[4], y[5], y[6], y[7]);
-                    *reinterpret_cast<uint4*>(d + (((c + flip) ^ sw) << 4)) = flip ? y1 : y0;
-                    *reinterpret_cast<uint4*>(d + (((c + !flip) ^ sw) << 4)) = flip ? y0 : y1;
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();

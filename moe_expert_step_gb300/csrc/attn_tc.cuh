@@ -18,6 +18,34 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lead
     d |= static_cast<uint64_t>(2) << 61;
     return d;
 }
+// mbar_wait by polling, its limit in SM clock cycles.  The blocking probe (try_wait) returned up to
+// 850 cycles after the phase was complete, longer than most of these waits; one lane's polls
+// take an issue slot every ~50 cycles.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, long long limit) {
+    if (mbar_test_wait(bar, parity)) return true;
+    if (limit <= 0) return false;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_test_wait(bar, parity)) return true;
+        if (*abort || clock64() - t0 >= limit) return false;
+    }
+}
+
+// True in one lane of a converged warp, the same one each time.  Asynchronous instructions whose
+// operands are uniform are issued under it rather than under a comparison of the lane number,
+// which tells the compiler nothing about how many lanes may arrive.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)::"memory");
+    return r != 0;
+}
+
 constexpr uint32_t kIdescTransposeB = 1u << 16;  // B is stored with N contiguous
 
 // 16 consecutive 32-bit columns of this thread's TMEM lane (no wait)
