@@ -45,7 +45,8 @@ struct Cfg {
     static constexpr int kRows = 32 << MODE;
     static constexpr int kRep = MODE == 0 ? 4 : MODE == 1 ? 2 : 1;
     static constexpr int kCols = kKeys / kRep;            // keys of a tile that a lane handles
-    static constexpr int kSteps = kRep == 1 ? 2 : 1;      // parts in which its weights are handed to the MMAs
+    static constexpr int kHalves = kRep == 1 ? 2 : 1;     // turns in which a tile's keys pass through a stream
+    static constexpr int kWide = kCols / kHalves;         // scores of a lane and turn: 32 or 64
     static constexpr int kThreads = F8 ? 608 : 352;
     static constexpr int kTile = kKeys * D * 2;           // bytes of a bf16 operand tile
     static constexpr int kQ = 128 * D * 2;
@@ -136,15 +137,16 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     uint64_t* rfull = empty + NB;
     uint64_t* rempty = rfull + C::kRaws;
     uint64_t* s_full = rempty + C::kRaws;
-    uint64_t* p_full = s_full + 2;
-    uint64_t* o_full = p_full + 4;  // p_full: [stream][half]
-    uint64_t* q_full = o_full + 2;
+    uint64_t* p_full = s_full + 4;  // both [stream][half]
+    uint64_t* o_full = p_full + 4;
+    uint64_t* pv_done = o_full + 2;  // [stream] each product of weights and values
+    uint64_t* q_full = pv_done + 2;
     uint64_t* fin = q_full + 1;
     uint64_t* go = fin + 1;  // the first stream has begun a segment (two row tiles)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(go + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
     int* zero_flag = abort_flag + 1;
-    static_assert((2 * NB + 2 * C::kRaws + 11) * 8 + 12 + 160 <= 1024, "misc area");
+    static_assert((2 * NB + 2 * C::kRaws + 15) * 8 + 12 + 160 <= 1024, "misc area");
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -157,9 +159,12 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             tc::mbar_init(&rempty[i], 8);
         }
         for (int g = 0; g < 2; ++g) {
-            tc::mbar_init(&s_full[g], 1);
-            for (int q = 0; q < C::kSteps; ++q) tc::mbar_init(&p_full[g * 2 + q], 4);
+            for (int q = 0; q < C::kHalves; ++q) {
+                tc::mbar_init(&s_full[g * 2 + q], 1);
+                tc::mbar_init(&p_full[g * 2 + q], 4);
+            }
             tc::mbar_init(&o_full[g], 1);
+            tc::mbar_init(&pv_done[g], 1);
         }
         tc::mbar_init(q_full, 8);
         tc::mbar_init(fin, 2);
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const int lrow = C::kTwo ? g * 128 + w * 32 + lane               // row within the row tile
                                  : (w * 32 + lane) & (C::kRows - 1);
         const int col0 = part * C::kCols;
-        uint32_t turns = 0, segs_g = 0;
+        uint32_t tiles_g = 0, turns_g = 0, segs_g = 0;
         // The eight warps meet at a hardware barrier between the steps of a merge.  They pass it
         // equally often whatever happens: after a wait that gave up they go through the rest of
         // their segments without waiting (their results are then unspecified).
@@ -237,38 +242,51 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 if (lane == 0) tc::mbar_arrive(q_full);
             }
             const int2 see = attn_sees(a, s.L, attn_query(a, row0 + min(lrow, nrows - 1)));
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f);
             const int step = C::kTwo ? 1 : 2, first = s.tile + (C::kTwo ? 0 : g);
             int turn = 0;
-            for (int t = first; t < s.tile + s.tiles; t += step, ++turn) {
-                wait(&s_full[g], turns & 1);
-                ++turns;
+            for (int t = first; t < s.tile + s.tiles; t += step, ++tiles_g)
+#pragma unroll 1
+            for (int half = 0; half < C::kHalves; ++half, ++turn) {
+                wait(&s_full[g * 2 + half], tiles_g & 1);
                 tc::fence_after_sync();
-                const int lo = see.x - (t * kKeys + col0), hi = see.y - (t * kKeys + col0);
-                const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < C::kCols);
-                constexpr bool kKeep = C::kCols == 32;  // scores held in registers between the two passes
-                float v[32];
+                const uint32_t t_x = t_s + half * 64;  // this turn's scores, then its weights
+                const int c0 = col0 + half * 64;
+                const int lo = see.x - (t * kKeys + c0), hi = see.y - (t * kKeys + c0);
+                const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < C::kWide);
+                // scores held in registers between the two passes (with FP8 the converters' registers
+                // leave room for 32)
+                constexpr bool kKeep = C::kWide == 32 || !F8;
+                constexpr int kHold = kKeep ? C::kWide : 32;
+                float v[kHold];
                 float mx = -INFINITY;
-                auto fetch = [&](int c) {  // 32 of the lane's scores, the hidden ones replaced
-                    tc::tmem_ld32(t_s + col0 + c, v);
+                auto fetch = [&](int c) {  // kHold of the lane's scores, the hidden ones replaced
+                    const uint32_t at = C::kRep == 1 ? t_x + c : t_s + col0 + c;
+                    if constexpr (kHold == 64) tc::tmem_ld64(at, v);
+                    else tc::tmem_ld32(at, v);
                     if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = (c + i >= lo && c + i < hi) ? v[i] : -INFINITY;
+                        for (int i = 0; i < kHold; ++i) v[i] = (c + i >= lo && c + i < hi) ? v[i] : -INFINITY;
                     }
                 };
 #pragma unroll 1
-                for (int c = 0; c < C::kCols; c += 32) {
+                for (int c = 0; c < C::kWide; c += kHold) {
                     fetch(c);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+                    for (int i = 0; i < kHold; i += 2) mx = fmaxf(mx, fmaxf(v[i], v[i + 1]));
                 }
                 mx *= a.scale_log2;
                 const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
                 if (__any_sync(0xffffffffu, move)) {
                     const float f = move ? tc::exp2_fast(m - mx) : 1.f;  // 0 from m = -inf
                     if (move) m = mx;
-                    l *= f;
+                    l2 = make_float2(l2.x * f, l2.y * f);
                     if (turn > 0) {
+                        if (C::kHalves > 1) {  // the half before is multiplied meanwhile
+                            wait(&pv_done[g], (turns_g + turn - 1) & 1);
+                            tc::fence_after_sync();
+                        }
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             float o[32];
@@ -283,23 +301,21 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 }
                 const float ms = m == -INFINITY ? 0.f : m;
                 if (C::kTwo && g == 0 && turn == 0 && lane == 0) tc::mbar_arrive(go);
+                const float2 c2 = make_float2(a.scale_log2, a.scale_log2), m2 = make_float2(-ms, -ms);
 #pragma unroll 1
-                for (int c = 0; c < C::kCols; c += 32) {
+                for (int c = 0; c < C::kWide; c += kHold) {
                     if (!kKeep) fetch(c);
-                    uint32_t p[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float p0 = tc::exp2_fast(fmaf(v[2 * i], a.scale_log2, -ms));
-                        const float p1 = tc::exp2_fast(fmaf(v[2 * i + 1], a.scale_log2, -ms));
-                        l += p0 + p1;
-                        p[i] = tc::pack_bf16(p0, p1);
-                    }
-                    tc::tmem_st16_async(t_s + (col0 + c) / 2, p);
-                    if (C::kSteps > 1 && (c & 32)) {  // the MMAs of these 64 keys can begin
-                        tc::tmem_wait_st();
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&p_full[g * 2 + (c >> 6)]);
+                    for (int j = 0; j < kHold; j += 32) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 x = tc::fma2(make_float2(v[j + 2 * i], v[j + 2 * i + 1]), c2, m2);
+                            x = make_float2(tc::exp2_fast(x.x), tc::exp2_fast(x.y));
+                            l2 = tc::add2(l2, x);
+                            p[i] = tc::pack_bf16(x.x, x.y);
+                        }
+                        tc::tmem_st16_async((C::kRep == 1 ? t_x : t_s + col0 / 2) + (c + j) / 2, p);
                     }
                 }
                 if (C::kRep > 1) {  // the other copies' keys (after the lane's own scores have been read)
@@ -308,13 +324,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     for (int c = 0; c < kKeys / 2; c += 16)
                         if (c / (C::kCols / 2) != part) tc::tmem_st16_async(t_s + c, z);
                 }
-                if (C::kSteps == 1) {
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&p_full[g * 2]);
-                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&p_full[g * 2 + half]);
             }
+            turns_g += turn;
+            const float l = l2.x + l2.y;
             if (turn > 0) {
                 wait(&o_full[g], segs_g & 1);
                 ++segs_g;
@@ -549,45 +565,59 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const int g = warp - 9;
         if (g == 1 && lane == 0) attn_describe_join<kKeys>(a, plan);
         __syncwarp();
-        constexpr uint32_t idesc_s = tc::idesc_bf16(128, kKeys), idesc_o = tc::idesc_bf16(128, D) | tc::kIdescTransposeB;
+        constexpr uint32_t idesc_s = tc::idesc_bf16(128, kKeys / C::kHalves), idesc_o = tc::idesc_bf16(128, D) | tc::kIdescTransposeB;
         const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128;
         const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(sq + (C::kTwo ? g * C::kQ : 0)));
         const uint64_t kd0 = tc::sdesc_k_sw128(tc::smem_addr(ring)), vd0 = tc::sdesc_mn_sw128(tc::smem_addr(ring), 16384);
+        // Every buffer is waited for and released in order, the other stream's too: a parity names
+        // a phase only as long as nobody skips one or falls two behind.
         uint32_t it = 0, segs = 0, turns = 0;
+        auto ready = [&](uint32_t i) -> bool { return wait(&full[i % NB], (i / NB) & 1); };
+        auto pass = [&]() -> bool {  // a buffer of the other stream's
+            if (!ready(it)) return false;
+            if (lane == 0) tc::mbar_arrive(&empty[it % NB]);
+            ++it;
+            return true;
+        };
+        auto scores = [&](uint32_t i, int half) {  // Q K^T of the keys in buffer i
+            const int b = i % NB;
+            const uint64_t kd = kd0 + b * (C::kTile >> 4) + half * 512;  // (descriptors count in 16 bytes)
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int off = (k >> 2) * 1024 + (k & 3) * 2;
+                    tc::mma_bf16(t_s + half * 64, qd + off, kd + off, idesc_s, k > 0);
+                }
+                tc::mma_commit(&s_full[g * 2 + half]);
+                if (half == C::kHalves - 1) tc::mma_commit(&empty[b]);
+            }
+            __syncwarp();
+        };
         AttnWalk s = attn_begin<kKeys>(plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
-            const int lo = attn_lo(a, s.L);
+            const int lo = attn_lo(a, s.L), n = s.tiles;
             if (!wait(q_full, segs & 1)) break;
             if (C::kTwo && g == 1 && !wait(go, segs & 1)) break;
             ++segs;
-            // this stream's turns: every key tile, or every other one
-            const int last = C::kTwo ? s.tiles - 1 : s.tiles - 1 - ((s.tiles - 1 - g) & 1);
+            for (int t = 0; t < (C::kTwo ? 1 : min(n, 2)); ++t) {  // the stream's first keys
+                if (!C::kTwo && t != g) {
+                    pass();
+                } else if (ready(it)) {
+                    for (int half = 0; half < C::kHalves; ++half) scores(it, half);
+                    ++it;
+                }
+            }
+            constexpr int kNext = C::kTwo ? 1 : 2;  // the stream's next key tile
             uint32_t begun = 0;
-            each_buffer<C::kTwo>(s.tiles, [&](bool is_v, int t) -> bool {
-                const int b = it % NB;
-                // Every buffer is waited for and released in order, the other stream's too: a parity
-                // names a phase only as long as nobody skips one or falls two behind.
-                if (!wait(&full[b], (it / NB) & 1)) return false;
-                ++it;
+            for (int t = 0; t < n && wait.ok; ++t) {
+                const bool more = t + kNext < n;
                 if (!C::kTwo && ((t ^ g) & 1)) {
-                    if (lane == 0) tc::mbar_arrive(&empty[b]);
-                    return true;
+                    if (pass() && more) pass();
+                    continue;
                 }
-                tc::fence_after_sync();
-                if (!is_v) {
-                    const uint64_t kd = kd0 + b * (C::kTile >> 4);  // (descriptors count in 16 bytes)
-                    if (tc::elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const int off = (k >> 2) * 1024 + (k & 3) * 2;
-                            tc::mma_bf16(t_s, qd + off, kd + off, idesc_s, k > 0);
-                        }
-                        tc::mma_commit(&s_full[g]);
-                        tc::mma_commit(&empty[b]);
-                    }
-                    __syncwarp();
-                    return true;
-                }
+                const int b = it % NB;
+                if (!ready(it)) break;
                 const int j0 = (s.tile + t) * kKeys, za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
                 // V's keys in steps of 16: those that some query sees, one step at least; the rows
                 // of the first and last step that none sees are zeroed (by both streams alike)
@@ -605,37 +635,43 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     __syncwarp();
                 }
                 const uint64_t vd = vd0 + b * (C::kTile >> 4);
-                constexpr int kPer = 8 / C::kSteps;
+                constexpr int kPer = 8 / C::kHalves;
 #pragma unroll 1
-                for (int q = 0; q < C::kSteps; ++q) {  // every part is waited for, so that none falls behind
-                    if (!wait(&p_full[g * 2 + q], turns & 1)) return false;
+                for (int half = 0; half < C::kHalves; ++half) {
+                    if (!wait(&p_full[g * 2 + half], turns & 1)) break;
                     tc::fence_after_sync();
-                    const uint32_t tp = t_s + q * kPer * 8;
-                    const uint64_t vq = vd + q * kPer * 128;
+                    const uint32_t tp = t_s + half * 64;
+                    const uint64_t vh = vd + half * kPer * 128;
                     if (tc::elect_one()) {
                         if (k0 == 0 && k1 == 8) {
 #pragma unroll
                             for (int k = 0; k < kPer; ++k) {
-                                tc::mma_f16_tmem_a(t_o, tp + k * 8, vq + k * 128, idesc_o, begun);
+                                tc::mma_f16_tmem_a(t_o, tp + k * 8, vh + k * 128, idesc_o, begun);
                                 begun = 1;
                             }
                         } else {
 #pragma unroll 1
-                            for (int k = max(k0 - q * kPer, 0); k < min(k1 - q * kPer, kPer); ++k) {
-                                tc::mma_f16_tmem_a(t_o, tp + k * 8, vq + k * 128, idesc_o, begun);
+                            for (int k = max(k0 - half * kPer, 0); k < min(k1 - half * kPer, kPer); ++k) {
+                                tc::mma_f16_tmem_a(t_o, tp + k * 8, vh + k * 128, idesc_o, begun);
                                 begun = 1;
                             }
                         }
-                        if (q == C::kSteps - 1) {
+                        if (C::kHalves > 1) tc::mma_commit(&pv_done[g]);
+                        if (half == C::kHalves - 1) {
                             tc::mma_commit(&empty[b]);
-                            if (t == last) tc::mma_commit(&o_full[g]);
+                            if (t + kNext >= n) tc::mma_commit(&o_full[g]);
                         }
                     }
                     __syncwarp();
+                    // the next tile's scores of this half take the place of the weights just used
+                    if (more) {
+                        if (half == 0 && !ready(it + 1)) break;
+                        scores(it + 1, half);
+                    }
                 }
                 ++turns;
-                return true;
-            });
+                it += more ? 2 : 1;
+            }
         }
         if (!wait.ok) err_bits = kErrTimeoutMma;
         __syncwarp();
