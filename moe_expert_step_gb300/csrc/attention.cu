@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
     const AttnPlan plan = attn_plan<kKT, kSimpleThreads>(a, plan_sm);
     if (tid == 0) attn_describe_join<kKT>(a, plan);
     constexpr int CW = D / 32;             // output columns of a thread
-    AttnWalk w = attn_begin<kKT>(plan);
+    AttnWalk w = attn_begin<kKT>(a, plan);
     while (attn_next<kKT>(a, w)) {
         const int h = w.seg / a.row_tiles, row0 = (w.seg - h * a.row_tiles) * kRT;
         const int nrows = min(kRT, a.rows - row0);

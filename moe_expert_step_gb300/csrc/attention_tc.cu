@@ -101,22 +101,21 @@ struct Waits {
     }
 };
 
-// The buffers of a segment of n key tiles in the order in which the MMAs use them:
-// f(is_v, tile) until it returns false.
-template <bool TWO, typename F>
-__device__ __forceinline__ bool each_buffer(int n, F f) {
-    if (TWO) {
-        for (int t = 0; t < n; ++t)
-            if (!f(false, t) || !f(true, t)) return false;
-        return true;
-    }
-    if (!f(false, 0)) return false;
-    if (n > 1 && !f(false, 1)) return false;
-    for (int t = 0; t < n; ++t) {
-        if (!f(true, t)) return false;
-        if (t + 2 < n && !f(false, t + 2)) return false;
-    }
-    return true;
+// The buffers of a segment of n key tiles in the order in which the MMAs use them: number i of
+// 2 n is the keys or the values of a tile.  Two row tiles: K0 V0 K1 V1 ..; else, with two key
+// tiles in work, K0 K1 V0 K2 V1 K3 .. V(n-2) V(n-1).  (One loop over i at every place that goes
+// through them: the code of all roles together has to stay small, or it runs at the speed of
+// its instruction fetches.)
+struct Buffer {
+    bool v;
+    int tile;
+};
+template <bool TWO>
+__device__ __forceinline__ Buffer buffer_of(int i, int n) {
+    if (TWO) return {(i & 1) != 0, i >> 1};
+    if (i == 2 * n - 1) return {true, n - 1};
+    if (i < 2) return {false, i};
+    return {(i & 1) == 0, (i & 1) == 0 ? (i >> 1) - 1 : (i + 1) >> 1};
 }
 
 template <int D, int MODE, bool F8>
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         // equally often whatever happens: after a wait that gave up they go through the rest of
         // their segments without waiting (their results are then unspecified).
         auto sync8 = [&]() { tc::named_bar_sync(1, 256); };
-        AttnWalk s = attn_begin<kKeys>(plan);
+        AttnWalk s = attn_begin<kKeys>(a, plan);
         while (attn_next<kKeys>(a, s)) {
             const int h = s.seg / a.row_tiles, row0 = (s.seg - h * a.row_tiles) * C::kRows;
             const int nrows = min(C::kRows, a.rows - row0);
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         constexpr int N = F8 ? NR : NB;
         uint32_t it = 0;
         const int page = 1 << a.page_log2, pages = kKeys >> a.page_log2;
-        AttnWalk s = attn_begin<kKeys>(plan);
+        AttnWalk s = attn_begin<kKeys>(a, plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
             const int h = s.seg / a.row_tiles, lo = attn_lo(a, s.L);
             const int32_t* tab = a.table + static_cast<long long>(s.r) * a.max_pages;
@@ -490,29 +489,31 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 const int pg = at + lane;
                 return pg >= pg_lo && pg < pg_end ? __ldg(&tab[pg]) : -2;
             };
-            int chunk = pg0, ids = table(chunk), ids_next = table(chunk + 32);
-            // lane i: page i of key tile t, -2 for one that is not loaded; tiles in ascending order
-            auto page_of = [&](int t) -> int {
-                const int at = pg0 + t * pages;
+            int chunk = pg0, ids_last = -2, ids = table(chunk), ids_next = table(chunk + 32);
+#pragma unroll 1
+            for (int i = 0; i < 2 * s.tiles; ++i, ++it) {
+                const Buffer buf = buffer_of<C::kTwo>(i, s.tiles);
+                // lane l: page l of the tile.  The keys' tiles ascend; the values' follow at most
+                // two tiles behind, so they are in these 32 pages or the last.
+                const int at = pg0 + buf.tile * pages;
                 if (at >= chunk + 32) {
                     chunk += 32;
+                    ids_last = ids;
                     ids = ids_next;
                     ids_next = table(chunk + 32);
                 }
-                const int id = __shfl_sync(0xffffffffu, ids, (at - chunk + lane) & 31);
-                return t < s.tiles && lane < pages ? id : -2;
-            };
-            auto load = [&](bool is_v, int id) -> bool {
+                const int id = __shfl_sync(0xffffffffu, at < chunk ? ids_last : ids, (at - chunk + lane) & 31);
                 const int b = it % N;
-                if (!wait(&be[b], ((it / N) & 1) ^ 1u)) return false;
-                const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages);
-                if (!good && id != -2) record_error(a.err, kErrBadInput);
+                if (!wait(&be[b], ((it / N) & 1) ^ 1u)) break;
+                const bool here = lane < pages && id != -2;
+                const bool good = here && static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages);
+                if (here && !good) record_error(a.err, kErrBadInput);
                 const unsigned on = __ballot_sync(0xffffffffu, good);
                 const int y = good ? (id * a.Hkv + h) << a.page_log2 : 0;
                 if (lane == 0) tc::mbar_arrive_expect_tx(&bf[b], __popc(on) * page * (F8 ? D + 1 : 2 * D));
                 __syncwarp();
-                const CUtensorMap* map = is_v ? &vmap : &kmap;
-                const uint8_t* ex = is_v ? a.v_exp : a.k_exp;
+                const CUtensorMap* map = buf.v ? &vmap : &kmap;
+                const uint8_t* ex = buf.v ? a.v_exp : a.k_exp;
 #pragma unroll 1
                 for (int p = 0; p < pages; ++p) {
                     const int yp = __shfl_sync(0xffffffffu, y, p);
@@ -529,26 +530,6 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         }
                     }
                     __syncwarp();
-                }
-                ++it;
-                return true;
-            };
-            // the order of each_buffer, every page number read once, ahead of its use
-            int y0 = page_of(0), y1 = page_of(1), y2 = C::kTwo ? -1 : page_of(2);
-            if (C::kTwo) {
-                for (int t = 0; t < s.tiles; ++t) {
-                    const int next = page_of(t + 2);
-                    if (!load(false, y0) || !load(true, y0)) break;
-                    y0 = y1;
-                    y1 = next;
-                }
-            } else if (load(false, y0) && (s.tiles < 2 || load(false, y1))) {
-                for (int t = 0; t < s.tiles; ++t) {
-                    const int next = page_of(t + 3);
-                    if (!load(true, y0) || (t + 2 < s.tiles && !load(false, y2))) break;
-                    y0 = y1;
-                    y1 = y2;
-                    y2 = next;
                 }
             }
         }
@@ -594,35 +575,31 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             }
             __syncwarp();
         };
-        AttnWalk s = attn_begin<kKeys>(plan);
+        AttnWalk s = attn_begin<kKeys>(a, plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
             const int lo = attn_lo(a, s.L), n = s.tiles;
             if (!wait(q_full, segs & 1)) break;
             if (C::kTwo && g == 1 && !wait(go, segs & 1)) break;
             ++segs;
-            for (int t = 0; t < (C::kTwo ? 1 : min(n, 2)); ++t) {  // the stream's first keys
-                if (!C::kTwo && t != g) {
-                    pass();
-                } else if (ready(it)) {
-                    for (int half = 0; half < C::kHalves; ++half) scores(it, half);
-                    ++it;
-                }
-            }
-            constexpr int kNext = C::kTwo ? 1 : 2;  // the stream's next key tile
+            constexpr int kNext = C::kTwo ? 1 : 2;  // from one of the stream's key tiles to the next
             uint32_t begun = 0;
-            for (int t = 0; t < n && wait.ok; ++t) {
-                const bool more = t + kNext < n;
+            // t = -kNext ..: the values of tile t, and the scores of the stream's next tile, each
+            // half taking the place of the weights just used
+#pragma unroll 1
+            for (int t = -kNext; t < n && wait.ok; ++t) {
+                const bool now = t >= 0, more = t + kNext < n;
                 if (!C::kTwo && ((t ^ g) & 1)) {
-                    if (pass() && more) pass();
+                    if ((!now || pass()) && more) pass();
                     continue;
                 }
-                const int b = it % NB;
-                if (!ready(it)) break;
+                const uint32_t iv = it, ik = it + now;
+                const int b = iv % NB;
+                if (now && !ready(iv)) break;
                 const int j0 = (s.tile + t) * kKeys, za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
                 // V's keys in steps of 16: those that some query sees, one step at least; the rows
                 // of the first and last step that none sees are zeroed (by both streams alike)
                 const int k0 = min(za >> 4, 7), k1 = max((zb + 15) >> 4, k0 + 1);
-                if (!F8 && ((za & 15) != 0 || (zb & 15) != 0 || zb <= 0)) {
+                if (!F8 && now && ((za & 15) != 0 || (zb & 15) != 0 || zb <= 0)) {
                     uint8_t* v = ring + b * C::kTile;
 #pragma unroll 1
                     for (int i = lane; i < 2 * 16 * (D / 8); i += 32) {
@@ -638,39 +615,33 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 constexpr int kPer = 8 / C::kHalves;
 #pragma unroll 1
                 for (int half = 0; half < C::kHalves; ++half) {
-                    if (!wait(&p_full[g * 2 + half], turns & 1)) break;
-                    tc::fence_after_sync();
-                    const uint32_t tp = t_s + half * 64;
-                    const uint64_t vh = vd + half * kPer * 128;
-                    if (tc::elect_one()) {
-                        if (k0 == 0 && k1 == 8) {
+                    if (now) {
+                        if (!wait(&p_full[g * 2 + half], turns & 1)) break;
+                        tc::fence_after_sync();
+                        const uint32_t tp = t_s + half * 64;
+                        const uint64_t vh = vd + half * kPer * 128;
+                        if (tc::elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < kPer; ++k) {
-                                tc::mma_f16_tmem_a(t_o, tp + k * 8, vh + k * 128, idesc_o, begun);
-                                begun = 1;
-                            }
-                        } else {
-#pragma unroll 1
-                            for (int k = max(k0 - half * kPer, 0); k < min(k1 - half * kPer, kPer); ++k) {
-                                tc::mma_f16_tmem_a(t_o, tp + k * 8, vh + k * 128, idesc_o, begun);
-                                begun = 1;
+                            for (int k = 0; k < kPer; ++k)
+                                if (k >= k0 - half * kPer && k < k1 - half * kPer) {
+                                    tc::mma_f16_tmem_a(t_o, tp + k * 8, vh + k * 128, idesc_o, begun);
+                                    begun = 1;
+                                }
+                            if (C::kHalves > 1) tc::mma_commit(&pv_done[g]);
+                            if (half == C::kHalves - 1) {
+                                tc::mma_commit(&empty[b]);
+                                if (!more) tc::mma_commit(&o_full[g]);
                             }
                         }
-                        if (C::kHalves > 1) tc::mma_commit(&pv_done[g]);
-                        if (half == C::kHalves - 1) {
-                            tc::mma_commit(&empty[b]);
-                            if (t + kNext >= n) tc::mma_commit(&o_full[g]);
-                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    // the next tile's scores of this half take the place of the weights just used
                     if (more) {
-                        if (half == 0 && !ready(it + 1)) break;
-                        scores(it + 1, half);
+                        if (half == 0 && !ready(ik)) break;
+                        scores(ik, half);
                     }
                 }
-                ++turns;
-                it += more ? 2 : 1;
+                if (now) ++turns;
+                it += now + more;
             }
         }
         if (!wait.ok) err_bits = kErrTimeoutMma;
@@ -696,26 +667,27 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         constexpr int kStepRows = D == 128 ? 4 : 8, kStepsC = 16 / kStepRows;  // of a warp's 16 keys
         const int lr = lane >> 3, lc = lane & 7;
         uint32_t it = 0;
-        AttnWalk s = attn_begin<kKeys>(plan);
+        AttnWalk s = attn_begin<kKeys>(a, plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
             const int lo = attn_lo(a, s.L);
-            each_buffer<C::kTwo>(s.tiles, [&](bool, int tt) -> bool {
+#pragma unroll 1
+            for (int i = 0; i < 2 * s.tiles; ++i, ++it) {
+                const int tt = buffer_of<C::kTwo>(i, s.tiles).tile;
                 const int rb = it % NR, b = it % NB;
-                if (!wait(&rfull[rb], (it / NR) & 1)) return false;
-                if (!wait(&empty[b], ((it / NB) & 1) ^ 1u)) return false;
+                if (!wait(&rfull[rb], (it / NR) & 1) || !wait(&empty[b], ((it / NB) & 1) ^ 1u)) break;
                 const int j0 = (s.tile + tt) * kKeys;
                 const int za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
                 const bool partial = za > 0 || zb < kKeys;
                 // (compact code: unrolled in full, this loop ran at the speed of its instruction fetches)
-#pragma unroll 2
-                for (int i = 0; i < kStepsC; ++i) {
+#pragma unroll 1
+                for (int st = 0; st < kStepsC; ++st) {
                     uint2 x[2];
                     uint32_t ex[2];
                     int row[2], half[2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         half[u] = D == 128 ? u ^ (lr & 1) : 0;
-                        row[u] = cw * 16 + i * kStepRows + lr + (D == 128 ? 0 : 4 * u);
+                        row[u] = cw * 16 + st * kStepRows + lr + (D == 128 ? 0 : 4 * u);
                         x[u] = *reinterpret_cast<const uint2*>(raw + rb * C::kRaw + row[u] * D + half[u] * 64 + lc * 8);
                         if (D == 64 || u == 0) ex[u] = exps[rb * kKeys + row[u]];
                         if (D == 128 && u == 1) ex[1] = ex[0];
@@ -753,9 +725,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     tc::mbar_arrive(&full[b]);
                     tc::mbar_arrive(&rempty[rb]);
                 }
-                ++it;
-                return true;
-            });
+            }
         }
         if (!wait.ok) err_bits = kErrTimeoutProducer;
     }

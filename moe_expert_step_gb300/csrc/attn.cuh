@@ -166,40 +166,44 @@ __device__ __forceinline__ void attn_describe_join(const AttnArgs& a, const Attn
 
 // A CTA's walk over its segments.
 struct AttnWalk {
-    int r, o, left, k;   // request, unit within it, units left, segments done
-    int L, t0, nt, seg;  // of the current segment
-    int tile, tiles;     // its first key tile here (from t0) and how many
+    int r, left, k;         // request, units left, segments done
+    int L, t0, nt, seg;     // of the current segment: length, first key tile, key tiles, head * row tiles + row tile
+    int tile, tiles;        // its first key tile here and how many
     bool whole;
 };
 template <int KT>
-__device__ __forceinline__ AttnWalk attn_begin(const AttnPlan& p) {
+__device__ __forceinline__ AttnWalk attn_begin(const AttnArgs& a, const AttnPlan& p) {
     AttnWalk w{};
     w.r = p.begin_r;
-    w.o = p.begin_o;
     w.left = p.count;
     w.k = -1;
-    w.tiles = 0;
+    if (p.count > 0) {
+        w.L = attn_len(a, w.r);
+        const int2 t = attn_tiles<KT>(a, w.L);
+        w.t0 = t.x;
+        w.nt = t.y;
+        w.seg = p.begin_o / t.y;
+        w.tile = t.x + (p.begin_o - w.seg * t.y);
+    }
     return w;
 }
 template <int KT>
 __device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnWalk& w) {
-    w.o += w.tiles;
-    w.left -= w.tiles;
-    if (w.left <= 0) return false;
-    w.L = attn_len(a, w.r);
-    int2 t = attn_tiles<KT>(a, w.L);
-    if (w.o >= t.y * a.Hkv * a.row_tiles) {
-        ++w.r;
-        w.o = 0;
-        w.L = attn_len(a, w.r);
-        t = attn_tiles<KT>(a, w.L);
+    if (w.k >= 0) {
+        w.left -= w.tiles;
+        ++w.seg;
+        if (w.left > 0 && w.seg == a.Hkv * a.row_tiles) {
+            w.seg = 0;
+            w.L = attn_len(a, ++w.r);
+            const int2 t = attn_tiles<KT>(a, w.L);
+            w.t0 = t.x;
+            w.nt = t.y;
+        }
+        w.tile = w.t0;
     }
-    w.t0 = t.x;
-    w.nt = t.y;
-    w.seg = w.o / w.nt;
-    const int in = w.o - w.seg * w.nt;
-    w.tile = w.t0 + in;
-    w.tiles = min(w.nt - in, w.left);
+    if (w.left <= 0) return false;
+    const int rest = w.t0 + w.nt - w.tile;
+    w.tiles = min(rest, w.left);
     w.whole = w.tiles == w.nt;
     ++w.k;
     return true;
