@@ -53,8 +53,8 @@ struct Cfg {
     // query tile(s); with one row tile also the merge buffer, once the segment's scores are done
     static constexpr int kFront = kTwo ? 2 * kQ : 32768;
     static constexpr int kRaw = kKeys * D;                // bytes of an FP8 tile
-    static constexpr int kBufs = (F8 ? (kTwo ? 3 : 4) : (kTwo ? 5 : 6)) * (128 / D);
-    static constexpr int kRaws = F8 ? 4 * (128 / D) : 0;
+    static constexpr int kBufs = (F8 ? 4 : kTwo ? 5 : 6) * (128 / D);
+    static constexpr int kRaws = F8 ? (kTwo ? 2 : 4) * (128 / D) : 0;
     static constexpr int kMisc = 1024 + kRaws * kKeys;    // plan, barriers, exponents
     static constexpr int kSmem = 1024 + kFront + kBufs * kTile + kRaws * kRaw + kMisc;
     static_assert(kSmem <= 232448, "shared memory");
@@ -95,6 +95,17 @@ struct Waits {
             int r = 1;
             if ((threadIdx.x & 31) == 0) r = tc::mbar_poll(bar, parity, abort, limit);
             ok = __shfl_sync(0xffffffffu, r, 0) != 0;
+            __syncwarp();
+        }
+        return ok;
+    }
+    // two barriers, polled by two lanes
+    __device__ __forceinline__ bool both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1) {
+        if (ok) {
+            const int l = threadIdx.x & 31;
+            int r = 1;
+            if (l < 2) r = tc::mbar_poll(l ? bar1 : bar0, l ? parity1 : parity0, abort, limit);
+            ok = __all_sync(0xffffffffu, r) != 0;
             __syncwarp();
         }
         return ok;
@@ -674,50 +685,48 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             for (int i = 0; i < 2 * s.tiles; ++i, ++it) {
                 const int tt = buffer_of<C::kTwo>(i, s.tiles).tile;
                 const int rb = it % NR, b = it % NB;
-                if (!wait(&rfull[rb], (it / NR) & 1) || !wait(&empty[b], ((it / NB) & 1) ^ 1u)) break;
+                if (!wait.both(&rfull[rb], (it / NR) & 1, &empty[b], ((it / NB) & 1) ^ 1u)) break;
                 const int j0 = (s.tile + tt) * kKeys;
                 const int za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
                 const bool partial = za > 0 || zb < kKeys;
-                // (compact code: unrolled in full, this loop ran at the speed of its instruction fetches)
-#pragma unroll 1
-                for (int st = 0; st < kStepsC; ++st) {
-                    uint2 x[2];
-                    uint32_t ex[2];
-                    int row[2], half[2];
+                uint2 x[2 * kStepsC];
+                uint32_t ex[2 * kStepsC];
+                auto row_of = [&](int i) { return cw * 16 + (i >> 1) * kStepRows + lr + (D == 128 ? 0 : 4 * (i & 1)); };
+                auto half_of = [&](int i) { return D == 128 ? (i ^ lr) & 1 : 0; };
+                const uint8_t* src = raw + rb * C::kRaw + lc * 8;
+                const uint8_t* se = exps + rb * kKeys;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        half[u] = D == 128 ? u ^ (lr & 1) : 0;
-                        row[u] = cw * 16 + st * kStepRows + lr + (D == 128 ? 0 : 4 * u);
-                        x[u] = *reinterpret_cast<const uint2*>(raw + rb * C::kRaw + row[u] * D + half[u] * 64 + lc * 8);
-                        if (D == 64 || u == 0) ex[u] = exps[rb * kKeys + row[u]];
-                        if (D == 128 && u == 1) ex[1] = ex[0];
+                for (int i = 0; i < 2 * kStepsC; ++i) {
+                    x[i] = *reinterpret_cast<const uint2*>(src + row_of(i) * D + half_of(i) * 64);
+                    ex[i] = D == 128 && (i & 1) ? ex[i - 1] : se[row_of(i)];
+                }
+                uint8_t* dst = ring + b * C::kTile;
+#pragma unroll
+                for (int i = 0; i < 2 * kStepsC; ++i) {
+                    const uint32_t f1 = min(ex[i] + 120u, 254u);  // exponent field of the factor
+                    const uint32_t s1 = f1 * 0x00800080u;
+                    uint32_t y[4], nan = 0;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t w = k ? x[i].y : x[i].x;
+                        y[2 * k] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), s1);
+                        y[2 * k + 1] = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s1);
+                        nan |= (w & 0x7f7f7f7fu) + 0x01010101u;  // bit 7 of a NaN code's byte
                     }
+                    if ((nan & 0x80808080u) | (ex[i] > 134u)) {
+                        const uint32_t f2 = ex[i] > 134u ? ex[i] - 134u + 127u : 127u;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t f1 = min(ex[u] + 120u, 254u);  // exponent field of the factor
-                        const uint32_t s1 = f1 * 0x00800080u;
-                        uint32_t y[4], nan = 0;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t w = k ? x[u].y : x[u].x;
-                            y[2 * k] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), s1);
-                            y[2 * k + 1] = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s1);
-                            nan |= (w & 0x7f7f7f7fu) + 0x01010101u;  // bit 7 of a NaN code's byte
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t w = (k < 2 ? x[i].x : x[i].y) >> (8 * (k & 1));
+                            y[k] = mul_bf16x2(y[k], f2 * 0x00800080u);
+                            if ((w & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
+                            if ((w & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
                         }
-                        if ((nan & 0x80808080u) | (ex[u] > 134u)) {
-                            const uint32_t f2 = ex[u] > 134u ? ex[u] - 134u + 127u : 127u;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t w = (k < 2 ? x[u].x : x[u].y) >> (8 * (k & 1));
-                                y[k] = mul_bf16x2(y[k], f2 * 0x00800080u);
-                                if ((w & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
-                                if ((w & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
-                            }
-                        }
-                        if (partial && (row[u] < za || row[u] >= zb)) y[0] = y[1] = y[2] = y[3] = 0;
-                        *reinterpret_cast<uint4*>(ring + b * C::kTile + half[u] * 16384 + row[u] * 128 +
-                                                  ((lc ^ (row[u] & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
+                    const int row = row_of(i);
+                    if (partial && (row < za || row >= zb)) y[0] = y[1] = y[2] = y[3] = 0;
+                    *reinterpret_cast<uint4*>(dst + half_of(i) * 16384 + row * 128 + ((lc ^ (row & 7)) << 4)) =
+                        make_uint4(y[0], y[1], y[2], y[3]);
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
