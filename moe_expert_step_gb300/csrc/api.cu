@@ -496,7 +496,7 @@ bool thr_ok(float t) { return t > 0.f && t <= 1.f; }
 }  // namespace
 
 int encode_tile_map(CUtensorMap* m, int elem_bytes, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
-                    uint32_t box_rows, bool swizzle128) {
+                    uint32_t box_rows, int swizzle) {
     if (get_encode() != MOESTEP_OK) return MOESTEP_ECUDA;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {cols * elem_bytes};
@@ -505,7 +505,10 @@ int encode_tile_map(CUtensorMap* m, int elem_bytes, const void* base, uint64_t c
     const CUresult r = g_encode(
         m, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+        : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                        : CU_TENSOR_MAP_SWIZZLE_NONE,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         g_last_cuda = static_cast<int>(r);

@@ -391,8 +391,9 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
         const uint64_t n = 1ull * kd->n_pages * kd->Hkv * kd->page;
         for (int i = 0; i < 2; ++i) {
             const void* p = i ? cache->v : cache->k;
-            rc = f8 ? encode_tile_map(i ? &vm : &km, 1, p, kd->D, n, kd->D, kd->page, false)
-                    : encode_tile_map(i ? &vm : &km, 2, p, kd->D, n, 64, kd->page, true);
+            // FP8 keys are an operand as they are, FP8 values go through the converters
+            rc = f8 ? encode_tile_map(i ? &vm : &km, 1, p, kd->D, n, kd->D, kd->page, i ? 0 : kd->D)
+                    : encode_tile_map(i ? &vm : &km, 2, p, kd->D, n, 64, kd->page, 128);
             if (rc != MOESTEP_OK) return rc;
         }
     }

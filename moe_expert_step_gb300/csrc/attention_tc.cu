@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kKeys = 128;                        // keys of a tile
 constexpr uint64_t kTeardown = 1000000000ull;     // limit for draining copies and MMAs in flight
+constexpr uint64_t kAbortedTile = 1000000ull;     // for FP8 key tiles whose scales an aborted CTA did not write
 constexpr float kSlack = 8.f;                     // how far a tile's maximum may pass m
 
 // MODE 0, 1, 2: row tiles of 32, 64, 128 (one tile, streams on alternate keys); 3: of 256 (two tiles)
@@ -49,22 +50,26 @@ struct Cfg {
     static constexpr int kWide = kCols / kHalves;         // scores of a lane and turn: 32 or 64
     static constexpr int kThreads = F8 ? 608 : 352;
     static constexpr int kTile = kKeys * D * 2;           // bytes of a bf16 operand tile
-    static constexpr int kQ = 128 * D * 2;
+    static constexpr int kKTile = F8 ? kKeys * D : kTile; // of keys, as they are multiplied
+    static constexpr int kRaw = kKeys * D;                // of FP8 values
+    static constexpr int kQ = 128 * D * 2;                // of queries (FP8: two E4M3 parts)
     // query tile(s); with one row tile also the merge buffer, once the segment's scores are done
     static constexpr int kFront = kTwo ? 2 * kQ : 32768;
-    static constexpr int kRaw = kKeys * D;                // bytes of an FP8 tile
-    static constexpr int kBufs = (F8 ? 4 : kTwo ? 5 : 6) * (128 / D);
-    static constexpr int kRaws = F8 ? (kTwo ? 2 : 4) * (128 / D) : 0;
-    static constexpr int kMisc = 1024 + kRaws * kKeys;    // plan, barriers, exponents
-    static constexpr int kSmem = 1024 + kFront + kBufs * kTile + kRaws * kRaw + kMisc;
+    static constexpr int kMul = 128 / D;
+    static constexpr int kNK = (F8 ? (kTwo ? 3 : 4) : 3) * kMul;             // key tiles
+    static constexpr int kNV = (F8 ? 2 : kTwo ? 2 : 3) * kMul;               // value tiles
+    static constexpr int kNR = F8 ? (kTwo ? 2 : 3) * kMul : 0;               // FP8 value tiles
+    static constexpr int kNS = F8 ? kNK + 2 : 0;  // key tiles' scales: a turn's are read while the tiles two ahead land
+    static constexpr int kMisc = 1024 + (F8 ? 1024 + (kNK + kNR) * kKeys + kNS * kKeys * 4 : 0);
+    static constexpr int kSmem = 1024 + kFront + kNK * kKTile + kNV * kTile + kNR * kRaw + kMisc;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// The FP8 converters leave every four columns in the order 0, 2, 1, 3 (see there): queries are put
-// into the same order, and the output's columns back.
-__device__ __forceinline__ uint4 to_fp8_order(uint4 x) {
-    return make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x5410),
-                      __byte_perm(x.z, x.w, 0x7632));
+// The FP8 converters leave every four columns of the values in the order 0, 2, 1, 3 (see there):
+// the output's columns are put back.
+// 2^(exp - 127) of an exponent byte
+__device__ __forceinline__ float exp_scale(uint32_t e) {
+    return e > 0 ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -134,19 +139,26 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const AttnArgs a) {
     using C = Cfg<D, MODE, F8>;
-    constexpr int NB = C::kBufs, NR = C::kRaws > 0 ? C::kRaws : 1;
+    constexpr int NK = C::kNK, NV = C::kNV, NR = F8 ? C::kNR : 1, NS = F8 ? C::kNS : 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sq = sm;
-    uint8_t* ring = sq + C::kFront;
-    uint8_t* raw = ring + NB * C::kTile;
-    uint8_t* exps = raw + C::kRaws * C::kRaw;              // [kRaws][128]
-    int* plan_sm = reinterpret_cast<int*>(exps + C::kRaws * kKeys);  // 40
-    uint64_t* full = reinterpret_cast<uint64_t*>(plan_sm + 40);
-    uint64_t* empty = full + NB;
-    uint64_t* rfull = empty + NB;
-    uint64_t* rempty = rfull + C::kRaws;
-    uint64_t* s_full = rempty + C::kRaws;
+    uint8_t* vring = sq + C::kFront;
+    uint8_t* kring = vring + NV * C::kTile;
+    uint8_t* raw = kring + NK * C::kKTile;
+    float* kscale = reinterpret_cast<float*>(raw + C::kNR * C::kRaw);        // FP8 [NS][128]: 2^(exp - 127) of keys
+    float* qscale = kscale + C::kNS * kKeys;                                 // FP8 [256]: powers of two of query rows
+    uint8_t* kexps = reinterpret_cast<uint8_t*>(qscale + (F8 ? 256 : 0));    // FP8 [NK][128]
+    uint8_t* exps = kexps + (F8 ? NK * kKeys : 0);                           // FP8 [NR][128] of values
+    int* plan_sm = reinterpret_cast<int*>(exps + C::kNR * kKeys);            // 40
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(plan_sm + 40);
+    uint64_t* kempty = kfull + NK;
+    uint64_t* vfull = kempty + NK;
+    uint64_t* vempty = vfull + NV;
+    uint64_t* rfull = vempty + NV;   // FP8 values as stored
+    uint64_t* rempty = rfull + C::kNR;
+    uint64_t* xfull = rempty + C::kNR;  // FP8 keys' exponents
+    uint64_t* s_full = xfull + (F8 ? NK : 0);
     uint64_t* p_full = s_full + 4;  // both [stream][half]
     uint64_t* o_full = p_full + 4;
     uint64_t* pv_done = o_full + 2;  // [stream] each product of weights and values
@@ -156,15 +168,20 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(go + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
     int* zero_flag = abort_flag + 1;
-    static_assert((2 * NB + 2 * C::kRaws + 15) * 8 + 12 + 160 <= 1024, "misc area");
+    static_assert((3 * NK + 2 * NV + 2 * C::kNR + 15) * 8 + 12 + 160 <= 1024, "misc area");
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NB; ++i) {
-            tc::mbar_init(&full[i], F8 ? 8 : 1);
-            tc::mbar_init(&empty[i], 2);  // both MMA issuers
+        for (int i = 0; i < NK; ++i) {
+            tc::mbar_init(&kfull[i], F8 ? 2 : 1);  // the copy, and the scales
+            tc::mbar_init(&kempty[i], 2);          // both MMA issuers
+            if (F8) tc::mbar_init(&xfull[i], 1);
         }
-        for (int i = 0; i < C::kRaws; ++i) {
+        for (int i = 0; i < NV; ++i) {
+            tc::mbar_init(&vfull[i], F8 ? 8 : 1);
+            tc::mbar_init(&vempty[i], 2);
+        }
+        for (int i = 0; i < C::kNR; ++i) {
             tc::mbar_init(&rfull[i], 1);
             tc::mbar_init(&rempty[i], 8);
         }
@@ -211,7 +228,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const int lrow = C::kTwo ? g * 128 + w * 32 + lane               // row within the row tile
                                  : (w * 32 + lane) & (C::kRows - 1);
         const int col0 = part * C::kCols;
-        uint32_t tiles_g = 0, turns_g = 0, segs_g = 0;
+        uint32_t tiles_g = 0, turns_g = 0, segs_g = 0, kt0 = 0;
         // The eight warps meet at a hardware barrier between the steps of a merge.  They pass it
         // equally often whatever happens: after a wait that gave up they go through the rest of
         // their segments without waiting (their results are then unspecified).
@@ -226,25 +243,63 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 const int c = threadIdx.x % kChunks, m0 = (threadIdx.x & (NT - 1)) / kChunks;
                 constexpr int kStep = NT / kChunks;  // rows apart
                 // (all loads in flight at once, ahead of the key and value copies that follow)
-                {
-                    uint4 x[kBatch];
+                uint4 x[kBatch];
 #pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-                        const int m = m0 + b * kStep, row = C::kTwo ? g * 128 + m : m & (C::kRows - 1);
-                        x[b] = make_uint4(0, 0, 0, 0);
-                        if (row < nrows) {
-                            const int rr = row0 + row, qi = attn_query(a, rr);
-                            x[b] = __ldg(reinterpret_cast<const uint4*>(
-                                static_cast<const bf16*>(a.q) + (static_cast<long long>(s.r) * a.n_q + qi) * a.q_ld +
-                                (h * a.G + rr - qi * a.G) * D + c * 8));
-                            if (F8) x[b] = to_fp8_order(x[b]);
-                        }
+                for (int b = 0; b < kBatch; ++b) {
+                    const int m = m0 + b * kStep, row = C::kTwo ? g * 128 + m : m & (C::kRows - 1);
+                    x[b] = make_uint4(0, 0, 0, 0);
+                    if (row < nrows) {
+                        const int rr = row0 + row, qi = attn_query(a, rr);
+                        x[b] = __ldg(reinterpret_cast<const uint4*>(
+                            static_cast<const bf16*>(a.q) + (static_cast<long long>(s.r) * a.n_q + qi) * a.q_ld +
+                            (h * a.G + rr - qi * a.G) * D + c * 8));
                     }
+                }
+                __syncwarp();
 #pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-                        const int m = m0 + b * kStep;
+                for (int b = 0; b < kBatch; ++b) {
+                    const int m = m0 + b * kStep;
+                    if (!F8) {
                         *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = x[b];
+                        continue;
                     }
+                    // A row times a power of two that brings it to at most 448, as the sum of two E4M3
+                    // parts: the first takes the leading 4 bits of a bf16's 8, the second the rest,
+                    // exactly but for elements 2000 times below the row's largest (error
+                    // below 2^-19 of that).  An infinite row gives NaN scores.
+                    const uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+                    float amax = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+#pragma unroll
+                    for (int o = kChunks / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    const uint32_t bits = __float_as_uint(amax);
+                    int e = static_cast<int>(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u);  // 448 = 0.875 * 2^9
+                    e = min(max(e, -100), 119);
+                    const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    if (c == 0)
+                        qscale[(C::kTwo ? g * 128 : 0) + m] = bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                                                                  : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t p[2], q[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float y0 = __uint_as_float(w[2 * i + j] << 16) * s, y1 = __uint_as_float(w[2 * i + j] & 0xffff0000u) * s;
+                            p[j] = tc::to_e4m3x2(y0, y1);
+                            const uint32_t h2 = tc::e4m3x2_to_f16x2(p[j], 0);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                            q[j] = tc::to_e4m3x2(y0 - f.x, y1 - f.y);
+                        }
+                        hi[i] = p[0] | p[1] << 16;
+                        lo[i] = q[0] | q[1] << 16;
+                    }
+                    const int piece = D == 128 ? (c >> 1) ^ (m & 7) : (c >> 1) ^ ((m >> 1) & 3);  // TMA's swizzles
+                    uint8_t* d = dst + m * D + (piece << 4) + (c & 1) * 8;
+                    *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(d + 128 * D) = make_uint2(lo[0], lo[1]);
                 }
                 tc::fence_proxy_async_smem();
                 tc::fence_before_sync();
@@ -252,15 +307,20 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 if (lane == 0) tc::mbar_arrive(q_full);
             }
             const int2 see = attn_sees(a, s.L, attn_query(a, row0 + min(lrow, nrows - 1)));
+            if (F8) __syncwarp();
+            float scl = a.scale_log2;  // of this row's scores; FP8: read once the queries are staged
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
             const int step = C::kTwo ? 1 : 2, first = s.tile + (C::kTwo ? 0 : g);
             int turn = 0;
-            for (int t = first; t < s.tile + s.tiles; t += step, ++tiles_g)
+            uint32_t kt = kt0 + first - s.tile;  // number of the key tile among all of the CTA's
+            kt0 += s.tiles;
+            for (int t = first; t < s.tile + s.tiles; t += step, ++tiles_g, kt += step)
 #pragma unroll 1
             for (int half = 0; half < C::kHalves; ++half, ++turn) {
                 wait(&s_full[g * 2 + half], tiles_g & 1);
                 tc::fence_after_sync();
+                if (F8 && turn == 0) scl = a.scale_log2 * qscale[C::kTwo ? lrow : w * 32 + lane];
                 const uint32_t t_x = t_s + half * 64;  // this turn's scores, then its weights
                 const int c0 = col0 + half * 64;
                 const int lo = see.x - (t * kKeys + c0), hi = see.y - (t * kKeys + c0);
@@ -275,6 +335,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     const uint32_t at = C::kRep == 1 ? t_x + c : t_s + col0 + c;
                     if constexpr (kHold == 64) tc::tmem_ld64(at, v);
                     else tc::tmem_ld32(at, v);
+                    if (F8) {
+                        const float* ks = kscale + (kt % NS) * kKeys + c0 + c;
+#pragma unroll
+                        for (int i = 0; i < kHold; i += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(ks + i);
+                            v[i] *= k4.x, v[i + 1] *= k4.y, v[i + 2] *= k4.z, v[i + 3] *= k4.w;
+                        }
+                    }
                     if (masked) {
 #pragma unroll
                         for (int i = 0; i < kHold; ++i) v[i] = (c + i >= lo && c + i < hi) ? v[i] : -INFINITY;
@@ -286,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kHold; i += 2) mx = fmaxf(mx, fmaxf(v[i], v[i + 1]));
                 }
-                mx *= a.scale_log2;
+                mx *= scl;
                 const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
                 if (__any_sync(0xffffffffu, move)) {
                     const float f = move ? tc::exp2_fast(m - mx) : 1.f;  // 0 from m = -inf
@@ -311,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 }
                 const float ms = m == -INFINITY ? 0.f : m;
                 if (C::kTwo && g == 0 && turn == 0 && lane == 0) tc::mbar_arrive(go);
-                const float2 c2 = make_float2(a.scale_log2, a.scale_log2), m2 = make_float2(-ms, -ms);
+                const float2 c2 = make_float2(scl, scl), m2 = make_float2(-ms, -ms);
 #pragma unroll 1
                 for (int c = 0; c < C::kWide; c += kHold) {
                     if (!kKeep) fetch(c);
@@ -483,10 +551,10 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         if (!wait.ok) err_bits = kErrTimeoutEpilogue;
     } else if (warp == 8) {
         // ------------------------------------------------------------ TMA producer
-        uint64_t* const bf = F8 ? rfull : full;
-        uint64_t* const be = F8 ? rempty : empty;
-        constexpr int N = F8 ? NR : NB;
-        uint32_t it = 0;
+        uint64_t* const vf = F8 ? rfull : vfull;
+        uint64_t* const ve = F8 ? rempty : vempty;
+        constexpr int N = F8 ? NR : NV;
+        uint32_t ik = 0, iv = 0;
         const int page = 1 << a.page_log2, pages = kKeys >> a.page_log2;
         AttnWalk s = attn_begin<kKeys>(a, plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
@@ -502,7 +570,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             };
             int chunk = pg0, ids_last = -2, ids = table(chunk), ids_next = table(chunk + 32);
 #pragma unroll 1
-            for (int i = 0; i < 2 * s.tiles; ++i, ++it) {
+            for (int i = 0; i < 2 * s.tiles; ++i) {
                 const Buffer buf = buffer_of<C::kTwo>(i, s.tiles);
                 // lane l: page l of the tile.  The keys' tiles ascend; the values' follow at most
                 // two tiles behind, so they are in these 32 pages or the last.
@@ -514,40 +582,56 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     ids_next = table(chunk + 32);
                 }
                 const int id = __shfl_sync(0xffffffffu, at < chunk ? ids_last : ids, (at - chunk + lane) & 31);
-                const int b = it % N;
-                if (!wait(&be[b], ((it / N) & 1) ^ 1u)) break;
+                const int b = buf.v ? iv % N : ik % NK;
+                if (!(buf.v ? wait(&ve[b], ((iv / N) & 1) ^ 1u) : wait(&kempty[b], ((ik / NK) & 1) ^ 1u))) break;
                 const bool here = lane < pages && id != -2;
                 const bool good = here && static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages);
                 if (here && !good) record_error(a.err, kErrBadInput);
                 const unsigned on = __ballot_sync(0xffffffffu, good);
                 const int y = good ? (id * a.Hkv + h) << a.page_log2 : 0;
-                if (lane == 0) tc::mbar_arrive_expect_tx(&bf[b], __popc(on) * page * (F8 ? D + 1 : 2 * D));
+                const int keys = __popc(on) * page;
+                uint64_t* bar = buf.v ? &vf[b] : &kfull[b];
+                if (lane == 0) {
+                    if (F8 && !buf.v) tc::mbar_arrive_expect_tx(&xfull[b], keys);
+                    tc::mbar_arrive_expect_tx(bar, keys * (F8 ? D + buf.v : 2 * D));
+                }
                 __syncwarp();
                 const CUtensorMap* map = buf.v ? &vmap : &kmap;
-                const uint8_t* ex = buf.v ? a.v_exp : a.k_exp;
+                uint8_t* dst = !buf.v ? kring + b * C::kKTile : F8 ? raw + b * C::kRaw : vring + b * C::kTile;
 #pragma unroll 1
                 for (int p = 0; p < pages; ++p) {
                     const int yp = __shfl_sync(0xffffffffu, y, p);
                     if (!(on >> p & 1)) continue;
                     if (tc::elect_one()) {
                         if (F8) {
-                            tc::tma_load_2d(raw + b * C::kRaw + p * page * D, map, &bf[b], 0, yp);
-                            tc::bulk_load(exps + b * kKeys + p * page, ex + yp, page, &bf[b]);
+                            if (buf.v)
+                                tc::bulk_load(exps + b * kKeys + p * page, a.v_exp + yp, page, bar);
+                            else
+                                tc::bulk_load(kexps + b * kKeys + p * page, a.k_exp + yp, page, &xfull[b]);
+                            tc::tma_load_2d(dst + p * page * D, map, bar, 0, yp);
                         } else {
 #pragma unroll
                             for (int half = 0; half < D / 64; ++half)
-                                tc::tma_load_2d(ring + b * C::kTile + half * 16384 + p * page * 128, map, &bf[b],
-                                                half * 64, yp);
+                                tc::tma_load_2d(dst + half * 16384 + p * page * 128, map, bar, half * 64, yp);
                         }
                     }
                     __syncwarp();
                 }
+                if (buf.v) ++iv;
+                else ++ik;
             }
         }
         if (!wait.ok) err_bits = kErrTimeoutProducer;
         // copies in flight land before the CTA ends
-        for (uint32_t i = it > N ? it - N : 0; lane == 0 && i < it; ++i)
-            tc::mbar_wait(&bf[i % N], (i / N) & 1, zero_flag, kTeardown);
+        if (lane == 0) {
+            for (uint32_t i = iv > N ? iv - N : 0; i < iv; ++i) tc::mbar_wait(&vf[i % N], (i / N) & 1, zero_flag, kTeardown);
+            for (uint32_t i = ik > NK ? ik - NK : 0; i < ik; ++i) {
+                // (an FP8 tile's phase also needs its scales, which an aborted CTA may not write: the
+                // exponents are the last of the tile's copies to be waited for then)
+                if (F8) tc::mbar_wait(&xfull[i % NK], (i / NK) & 1, zero_flag, kTeardown);
+                tc::mbar_wait(&kfull[i % NK], (i / NK) & 1, zero_flag, F8 && !wait.ok ? kAbortedTile : kTeardown);
+            }
+        }
         __syncwarp();
     } else if (warp < 11) {
         // ------------------------------------------------------------ MMA issuers, one a stream
@@ -557,32 +641,49 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const int g = warp - 9;
         if (g == 1 && lane == 0) attn_describe_join<kKeys>(a, plan);
         __syncwarp();
-        constexpr uint32_t idesc_s = tc::idesc_bf16(128, kKeys / C::kHalves), idesc_o = tc::idesc_bf16(128, D) | tc::kIdescTransposeB;
+        constexpr uint32_t idesc_s = F8 ? tc::idesc_e4m3(128, kKeys / C::kHalves) : tc::idesc_bf16(128, kKeys / C::kHalves);
+        constexpr uint32_t idesc_o = tc::idesc_bf16(128, D) | tc::kIdescTransposeB;
         const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128;
-        const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(sq + (C::kTwo ? g * C::kQ : 0)));
-        const uint64_t kd0 = tc::sdesc_k_sw128(tc::smem_addr(ring)), vd0 = tc::sdesc_mn_sw128(tc::smem_addr(ring), 16384);
+        auto sdesc = [](const void* p) {
+            return F8 && D == 64 ? tc::sdesc_k_sw64(tc::smem_addr(p)) : tc::sdesc_k_sw128(tc::smem_addr(p));
+        };
+        const uint64_t qd = sdesc(sq + (C::kTwo ? g * C::kQ : 0)), kd0 = sdesc(kring);
+        const uint64_t vd0 = tc::sdesc_mn_sw128(tc::smem_addr(vring), 16384);
         // Every buffer is waited for and released in order, the other stream's too: a parity names
         // a phase only as long as nobody skips one or falls two behind.
-        uint32_t it = 0, segs = 0, turns = 0;
-        auto ready = [&](uint32_t i) -> bool { return wait(&full[i % NB], (i / NB) & 1); };
-        auto pass = [&]() -> bool {  // a buffer of the other stream's
-            if (!ready(it)) return false;
-            if (lane == 0) tc::mbar_arrive(&empty[it % NB]);
-            ++it;
+        uint32_t ik = 0, iv = 0, segs = 0, turns = 0;
+        auto ready = [&](bool v) -> bool {
+            return v ? wait(&vfull[iv % NV], (iv / NV) & 1) : wait(&kfull[ik % NK], (ik / NK) & 1);
+        };
+        auto pass = [&](bool v) -> bool {  // a buffer of the other stream's
+            if (!ready(v)) return false;
+            if (lane == 0) tc::mbar_arrive(v ? &vempty[iv % NV] : &kempty[ik % NK]);
+            if (v) ++iv;
+            else ++ik;
             return true;
         };
-        auto scores = [&](uint32_t i, int half) {  // Q K^T of the keys in buffer i
-            const int b = i % NB;
-            const uint64_t kd = kd0 + b * (C::kTile >> 4) + half * 512;  // (descriptors count in 16 bytes)
+        auto scores = [&](int half) {  // Q K^T of half the keys of buffer ik
+            const int b = ik % NK;
+            // (descriptors count in 16 bytes)
+            const uint64_t kd = kd0 + b * (C::kKTile >> 4) + half * (F8 ? 4 * D : 512);
             tc::fence_after_sync();
             if (tc::elect_one()) {
+                if (F8) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int off = (k >> 2) * 1024 + (k & 3) * 2;
-                    tc::mma_bf16(t_s + half * 64, qd + off, kd + off, idesc_s, k > 0);
+                    for (int part = 0; part < 2; ++part)  // of the queries
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            tc::mma_e4m3(t_s + half * 64, qd + part * (128 * D / 16) + k * 2, kd + k * 2, idesc_s,
+                                         part > 0 || k > 0);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int off = (k >> 2) * 1024 + (k & 3) * 2;
+                        tc::mma_bf16(t_s + half * 64, qd + off, kd + off, idesc_s, k > 0);
+                    }
                 }
                 tc::mma_commit(&s_full[g * 2 + half]);
-                if (half == C::kHalves - 1) tc::mma_commit(&empty[b]);
+                if (half == C::kHalves - 1) tc::mma_commit(&kempty[b]);
             }
             __syncwarp();
         };
@@ -600,18 +701,17 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             for (int t = -kNext; t < n && wait.ok; ++t) {
                 const bool now = t >= 0, more = t + kNext < n;
                 if (!C::kTwo && ((t ^ g) & 1)) {
-                    if ((!now || pass()) && more) pass();
+                    if ((!now || pass(true)) && more) pass(false);
                     continue;
                 }
-                const uint32_t iv = it, ik = it + now;
-                const int b = iv % NB;
-                if (now && !ready(iv)) break;
+                const int b = iv % NV;
+                if (now && !ready(true)) break;
                 const int j0 = (s.tile + t) * kKeys, za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
                 // V's keys in steps of 16: those that some query sees, one step at least; the rows
                 // of the first and last step that none sees are zeroed (by both streams alike)
                 const int k0 = min(za >> 4, 7), k1 = max((zb + 15) >> 4, k0 + 1);
                 if (!F8 && now && ((za & 15) != 0 || (zb & 15) != 0 || zb <= 0)) {
-                    uint8_t* v = ring + b * C::kTile;
+                    uint8_t* v = vring + b * C::kTile;
 #pragma unroll 1
                     for (int i = lane; i < 2 * 16 * (D / 8); i += 32) {
                         const int r = (i >> 3) & 31, row = r < 16 ? k0 * 16 + r : k1 * 16 - 32 + r;
@@ -640,19 +740,19 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                                 }
                             if (C::kHalves > 1) tc::mma_commit(&pv_done[g]);
                             if (half == C::kHalves - 1) {
-                                tc::mma_commit(&empty[b]);
+                                tc::mma_commit(&vempty[b]);
                                 if (!more) tc::mma_commit(&o_full[g]);
                             }
                         }
                         __syncwarp();
                     }
                     if (more) {
-                        if (half == 0 && !ready(ik)) break;
-                        scores(ik, half);
+                        if (half == 0 && !ready(false)) break;
+                        scores(half);
                     }
                 }
-                if (now) ++turns;
-                it += now + more;
+                if (now) ++turns, ++iv;
+                if (more) ++ik;
             }
         }
         if (!wait.ok) err_bits = kErrTimeoutMma;
@@ -677,15 +777,30 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const int cw = warp - 11;
         constexpr int kStepRows = D == 128 ? 4 : 8, kStepsC = 16 / kStepRows;  // of a warp's 16 keys
         const int lr = lane >> 3, lc = lane & 7;
-        uint32_t it = 0;
+        uint32_t ik = 0, iv = 0;
         AttnWalk s = attn_begin<kKeys>(a, plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
             const int lo = attn_lo(a, s.L);
 #pragma unroll 1
-            for (int i = 0; i < 2 * s.tiles; ++i, ++it) {
-                const int tt = buffer_of<C::kTwo>(i, s.tiles).tile;
-                const int rb = it % NR, b = it % NB;
-                if (!wait.both(&rfull[rb], (it / NR) & 1, &empty[b], ((it / NB) & 1) ^ 1u)) break;
+            for (int i = 0; i < 2 * s.tiles; ++i) {
+                const Buffer buf = buffer_of<C::kTwo>(i, s.tiles);
+                if (!buf.v) {  // keys: their scales, by one warp
+                    if (static_cast<int>(ik & 7) == cw) {
+                        const int b = ik % NK;
+                        if (!wait(&xfull[b], (ik / NK) & 1)) break;
+                        const uint32_t w = reinterpret_cast<const uint32_t*>(kexps + b * kKeys)[lane];
+                        float4 f;
+                        f.x = exp_scale(w & 255), f.y = exp_scale(w >> 8 & 255), f.z = exp_scale(w >> 16 & 255), f.w = exp_scale(w >> 24);
+                        *reinterpret_cast<float4*>(kscale + (ik % NS) * kKeys + lane * 4) = f;
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&kfull[b]);
+                    }
+                    ++ik;
+                    continue;
+                }
+                const int tt = buf.tile, rb = iv % NR, b = iv % NV;
+                if (!wait.both(&rfull[rb], (iv / NR) & 1, &vempty[b], ((iv / NV) & 1) ^ 1u)) break;
+                ++iv;
                 const int j0 = (s.tile + tt) * kKeys;
                 const int za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
                 const bool partial = za > 0 || zb < kKeys;
@@ -700,7 +815,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     x[i] = *reinterpret_cast<const uint2*>(src + row_of(i) * D + half_of(i) * 64);
                     ex[i] = D == 128 && (i & 1) ? ex[i - 1] : se[row_of(i)];
                 }
-                uint8_t* dst = ring + b * C::kTile;
+                uint8_t* dst = vring + b * C::kTile;
 #pragma unroll
                 for (int i = 0; i < 2 * kStepsC; ++i) {
                     const uint32_t f1 = min(ex[i] + 120u, 254u);  // exponent field of the factor
@@ -731,7 +846,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tc::mbar_arrive(&full[b]);
+                    tc::mbar_arrive(&vfull[b]);
                     tc::mbar_arrive(&rempty[rb]);
                 }
             }

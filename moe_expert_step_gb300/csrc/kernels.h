@@ -176,7 +176,7 @@ int validate_dims(const moestep_dims* d);  // MOESTEP_OK or the code every entry
 int device_ok(int* sms);                   // current device is sm_103; *sms = its SM count
 // 2D tensor of 2-byte (bf16) or 1-byte elements, cols contiguous; boxes of box_rows x box_cols
 int encode_tile_map(CUtensorMap* m, int elem_bytes, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
-                    uint32_t box_rows, bool swizzle128);
+                    uint32_t box_rows, int swizzle);  // swizzle: 128, 64 or 0 bytes
 unsigned long long wait_timeout_ns();      // limit of bounded waits (moestep_set_wait_timeout_ns)
 
 // ------------------------------------------------------------------ profiling hooks (api.cu)
