@@ -186,63 +186,85 @@ constexpr int kJoinThreads = 256;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, int ctas) {
-    __shared__ int s_list[kAttnMaxCtas];  // CTAs that describe a join
-    __shared__ int s_n;
+    __shared__ int4 s_list[kAttnMaxCtas];  // the joins that there are
+    __shared__ int s_cnt[8];
     __shared__ float s_f[8][kAttnMaxCtas];
     __shared__ float s_o[8][D];
+    constexpr int W = D / 32, kBatch = 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    if (warp == 0) {
-        int n = 0;
-        for (int i0 = 0; i0 < ctas; i0 += 32) {
-            const bool on = i0 + lane < ctas && __ldcg(&a.joins[i0 + lane].x) >= 0;
-            const unsigned b = __ballot_sync(0xffffffffu, on);
-            if (on) s_list[n + __popc(b & ((1u << lane) - 1))] = i0 + lane;
-            n += __popc(b);
+    int found = 0;
+    for (int i0 = 0; i0 < ctas; i0 += kJoinThreads) {  // (once or twice)
+        int4 j = make_int4(-1, 0, 0, 0);
+        if (i0 + threadIdx.x < ctas) j = __ldcg(&a.joins[i0 + threadIdx.x]);
+        const unsigned b = __ballot_sync(0xffffffffu, j.x >= 0);
+        __syncthreads();
+        if (lane == 0) s_cnt[warp] = __popc(b);
+        __syncthreads();
+        int at = found + __popc(b & ((1u << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) at += s_cnt[w];
+            found += s_cnt[w];
         }
-        if (lane == 0) s_n = n;
+        if (j.x >= 0) s_list[at] = j;
     }
     __syncthreads();
-    const int rows = min(a.slot_rows, a.rows), work = s_n * rows;
+    const int rows = min(a.slot_rows, a.rows), work = found * rows;
     int wpr = 8;  // warps per row
     while (wpr > 1 && work * wpr > static_cast<int>(gridDim.x) * 8) wpr >>= 1;
     const int team = warp / wpr, part = warp % wpr, teams = 8 / wpr;
     for (int w0 = blockIdx.x * teams; w0 < work; w0 += gridDim.x * teams) {  // the same for the whole block
         const int w = w0 + team, seg = w / rows, rr = w - seg * rows;
         int4 j = make_int4(-1, 0, 0, 0);
-        if (w < work) j = __ldcg(&a.joins[s_list[seg]]);
+        if (w < work) j = s_list[seg];
         const int h = j.y / a.row_tiles, row0 = (j.y - h * a.row_tiles) * a.slot_rows;
         const bool on = j.x >= 0 && row0 + rr < a.rows;
-        const int c0 = j.z >> 1, n = j.w - c0 + 1;
+        const int c0 = j.z >> 1, n = on ? j.w - c0 + 1 : 0;
         auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? j.z : 2 * (c0 + i)) * a.slot_rows + rr; };
-        float m = -INFINITY, l = 0.f;
-        constexpr int W = D / 32;
-        float acc[W] = {};
-        if (on) {
-            for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(&a.part_ml[slot(i)]).x);
-            m = warp_max(m);
-            const float ms = m == -INFINITY ? 0.f : m;
-            for (int i = lane; i < n; i += 32) {
-                const float2 ml = __ldcg(&a.part_ml[slot(i)]);
-                const float f = exp2f(ml.x - ms);
-                l += ml.y * f;
-                s_f[warp][i] = f;
+        auto load = [&](int i, float (&x)[W]) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) x[k] = 0.f;
+            if (i >= n) return;
+            const float* p = a.part_o + slot(i) * D + lane * W;
+            if constexpr (W == 4) {
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(p));
+                x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+            } else {
+                const float2 y = __ldcg(reinterpret_cast<const float2*>(p));
+                x[0] = y.x, x[1] = y.y;
             }
-            l = warp_sum(l);
-            __syncwarp();
-#pragma unroll 8
-            for (int i = part; i < n; i += wpr) {
-                const float* p = a.part_o + slot(i) * D + lane * W;
-                const float f = s_f[warp][i];
-                if constexpr (W == 4) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
-                    acc[0] += f * x.x, acc[1] += f * x.y, acc[2] += f * x.z, acc[3] += f * x.w;
-                } else {
-                    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
-                    acc[0] += f * x.x, acc[1] += f * x.y;
+        };
+        float x[kBatch][W];  // the first parts are on their way while the statistics are joined
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) load(part + u * wpr, x[u]);
+        float m = -INFINITY, l = 0.f;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(&a.part_ml[slot(i)]).x);
+        m = warp_max(m);
+        const float ms = m == -INFINITY ? 0.f : m;
+        for (int i = lane; i < n; i += 32) {
+            const float2 ml = __ldcg(&a.part_ml[slot(i)]);
+            const float f = exp2f(ml.x - ms);
+            l += ml.y * f;
+            s_f[warp][i] = f;
+        }
+        l = warp_sum(l);
+        __syncwarp();
+        float acc[W] = {};
+        for (int i = part;;) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (i + u * wpr < n) {
+                    const float f = s_f[warp][i + u * wpr];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) acc[k] += f * x[u][k];
                 }
             }
+            i += kBatch * wpr;
+            if (i >= n) break;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) load(i + u * wpr, x[u]);
         }
         if (wpr > 1) {
 #pragma unroll
@@ -276,9 +298,9 @@ cudaError_t launch_f32(const AttnArgs& a, int grid, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_join(const AttnArgs& a, int ctas, int sms, cudaStream_t s) {
-    // at most ctas - 1 segments are shared; eight blocks an SM are resident at once
+    // four blocks an SM are resident at once
     const long long work = 1ll * ctas * (a.slot_rows < a.rows ? a.slot_rows : a.rows);
-    const int grid = work < 8ll * sms ? static_cast<int>(work) : 8 * sms;
+    const int grid = work < 4ll * sms ? static_cast<int>(work) : 4 * sms;
     return launch_pdl(attn_join_kernel<T, D>, dim3(grid), dim3(kJoinThreads), 0, s, a, ctas);
 }
 
@@ -379,12 +401,13 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     a.page_log2 = kd->page == 16 ? 4 : kd->page == 32 ? 5 : kd->page == 64 ? 6 : 7;
     a.max_pages = kd->max_pages;
     a.n_pages = kd->n_pages;
+    const bool f32 = kd->dtype == MOESTEP_F32, f8 = kd->dtype == MOESTEP_FP8;
     a.causal = causal != 0;
+    a.even = !f32 && L.slot_rows == 256 ? 4 : 0;
     // a window as long as the cache hides nothing (and stays out of 32-bit overflow)
     a.window = window >= kd->max_pages * kd->page ? 0 : window;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.timeout_ns = wait_timeout_ns();
-    const bool f32 = kd->dtype == MOESTEP_F32, f8 = kd->dtype == MOESTEP_FP8;
     const int want = f32 ? 2 * sms : sms, grid = want < max_ctas(*kd) ? want : max_ctas(*kd);
     CUtensorMap km, vm;
     if (!f32) {

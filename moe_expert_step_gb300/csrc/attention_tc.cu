@@ -20,7 +20,7 @@
 // memory by the softmax warps, which is rare after the first tiles.
 //
 // Warps: 0-7 softmax (two warpgroups), 8 TMA producer, 9-10 MMA issuers (one lane each, a
-// stream each), and with FP8 11-18 converters (E4M3 code * 2^exp -> bf16, exact, into the swizzled operand buffers).
+// stream each), and with FP8 from 11 converters (E4M3 code * 2^exp -> bf16, exact, into the swizzled operand buffers).
 // Keys outside [lo, L) of the request reach no result: their scores are replaced by -inf, and
 // their V rows, which a zero weight would still multiply (NaN), are zeroed in shared memory.
 // Every wait is bounded (timeout -> error word, orderly teardown).
@@ -48,7 +48,12 @@ struct Cfg {
     static constexpr int kCols = kKeys / kRep;            // keys of a tile that a lane handles
     static constexpr int kHalves = kRep == 1 ? 2 : 1;     // turns in which a tile's keys pass through a stream
     static constexpr int kWide = kCols / kHalves;         // scores of a lane and turn: 32 or 64
-    static constexpr int kThreads = F8 ? 608 : 352;
+    static constexpr int kConv = F8 ? 8 : 0;              // converter warps
+    // FP8: 20 warps (one idle) of 96 registers a thread, 61440 in all, redistributed: 256 softmax threads
+    // x 136 (64 scores in registers) + 384 others x 64 = 59392
+    static constexpr int kThreads = F8 ? 640 : 352;
+    static constexpr int kSoftRegs = 136, kOtherRegs = 64;
+    static_assert(!F8 || 256 * kSoftRegs + (kThreads - 256) * kOtherRegs <= kThreads * 96, "registers");
     static constexpr int kTile = kKeys * D * 2;           // bytes of a bf16 operand tile
     static constexpr int kKTile = F8 ? kKeys * D : kTile; // of keys, as they are multiplied
     static constexpr int kRaw = kKeys * D;                // of FP8 values
@@ -56,9 +61,9 @@ struct Cfg {
     // query tile(s); with one row tile also the merge buffer, once the segment's scores are done
     static constexpr int kFront = kTwo ? 2 * kQ : 32768;
     static constexpr int kMul = 128 / D;
-    static constexpr int kNK = (F8 ? (kTwo ? 3 : 4) : 3) * kMul;             // key tiles
-    static constexpr int kNV = (F8 ? 2 : kTwo ? 2 : 3) * kMul;               // value tiles
-    static constexpr int kNR = F8 ? (kTwo ? 2 : 3) * kMul : 0;               // FP8 value tiles
+    static constexpr int kNK = 3 * kMul;                                     // key tiles
+    static constexpr int kNV = (kTwo ? 2 : 3) * kMul;                        // value tiles
+    static constexpr int kNR = F8 ? 2 * kMul : 0;                            // FP8 value tiles
     static constexpr int kNS = F8 ? kNK + 2 : 0;  // key tiles' scales: a turn's are read while the tiles two ahead land
     static constexpr int kMisc = 1024 + (F8 ? 1024 + (kNK + kNR) * kKeys + kNS * kKeys * 4 : 0);
     static constexpr int kSmem = 1024 + kFront + kNK * kKTile + kNV * kTile + kNR * kRaw + kMisc;
@@ -178,12 +183,12 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             if (F8) tc::mbar_init(&xfull[i], 1);
         }
         for (int i = 0; i < NV; ++i) {
-            tc::mbar_init(&vfull[i], F8 ? 8 : 1);
+            tc::mbar_init(&vfull[i], F8 ? C::kConv : 1);
             tc::mbar_init(&vempty[i], 2);
         }
         for (int i = 0; i < C::kNR; ++i) {
             tc::mbar_init(&rfull[i], 1);
-            tc::mbar_init(&rempty[i], 8);
+            tc::mbar_init(&rempty[i], C::kConv);
         }
         for (int g = 0; g < 2; ++g) {
             for (int q = 0; q < C::kHalves; ++q) {
@@ -221,6 +226,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax and output
+        if (F8) tc::more_registers<C::kSoftRegs>();
         const int g = warp >> 2, w = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
         const uint32_t t_s = tmem + lanes + g * 128, t_o = tmem + lanes + 256 + g * 128;
@@ -256,18 +262,22 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     }
                 }
                 __syncwarp();
+                // (a loop over one piece of code, the loaded pieces moved up: unrolled, its instructions
+                // alone took 7 us to arrive)
+#pragma unroll 1
+                for (int m = m0; m < 128; m += kStep) {
+                    const uint4 piece16 = x[0];
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int m = m0 + b * kStep;
+                    for (int b = 0; b + 1 < kBatch; ++b) x[b] = x[b + 1];
                     if (!F8) {
-                        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = x[b];
+                        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = piece16;
                         continue;
                     }
                     // A row times a power of two that brings it to at most 448, as the sum of two E4M3
                     // parts: the first takes the leading 4 bits of a bf16's 8, the second the rest,
                     // exactly but for elements 2000 times below the row's largest (error
                     // below 2^-19 of that).  An infinite row gives NaN scores.
-                    const uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+                    const uint32_t w[4] = {piece16.x, piece16.y, piece16.z, piece16.w};
                     float amax = 0.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -325,10 +335,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 const int c0 = col0 + half * 64;
                 const int lo = see.x - (t * kKeys + c0), hi = see.y - (t * kKeys + c0);
                 const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < C::kWide);
-                // scores held in registers between the two passes (with FP8 the converters' registers
-                // leave room for 32)
-                constexpr bool kKeep = C::kWide == 32 || !F8;
-                constexpr int kHold = kKeep ? C::kWide : 32;
+                constexpr int kHold = C::kWide;  // scores held in registers between the two passes
                 float v[kHold];
                 float mx = -INFINITY;
                 auto fetch = [&](int c) {  // kHold of the lane's scores, the hidden ones replaced
@@ -348,12 +355,9 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         for (int i = 0; i < kHold; ++i) v[i] = (c + i >= lo && c + i < hi) ? v[i] : -INFINITY;
                     }
                 };
-#pragma unroll 1
-                for (int c = 0; c < C::kWide; c += kHold) {
-                    fetch(c);
+                fetch(0);
 #pragma unroll
-                    for (int i = 0; i < kHold; i += 2) mx = fmaxf(mx, fmaxf(v[i], v[i + 1]));
-                }
+                for (int i = 0; i < kHold; i += 2) mx = fmaxf(mx, fmaxf(v[i], v[i + 1]));
                 mx *= scl;
                 const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
                 if (__any_sync(0xffffffffu, move)) {
@@ -380,21 +384,17 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 const float ms = m == -INFINITY ? 0.f : m;
                 if (C::kTwo && g == 0 && turn == 0 && lane == 0) tc::mbar_arrive(go);
                 const float2 c2 = make_float2(scl, scl), m2 = make_float2(-ms, -ms);
-#pragma unroll 1
-                for (int c = 0; c < C::kWide; c += kHold) {
-                    if (!kKeep) fetch(c);
 #pragma unroll
-                    for (int j = 0; j < kHold; j += 32) {
-                        uint32_t p[16];
+                for (int j = 0; j < kHold; j += 32) {
+                    uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float2 x = tc::fma2(make_float2(v[j + 2 * i], v[j + 2 * i + 1]), c2, m2);
-                            x = make_float2(tc::exp2_fast(x.x), tc::exp2_fast(x.y));
-                            l2 = tc::add2(l2, x);
-                            p[i] = tc::pack_bf16(x.x, x.y);
-                        }
-                        tc::tmem_st16_async((C::kRep == 1 ? t_x : t_s + col0 / 2) + (c + j) / 2, p);
+                    for (int i = 0; i < 16; ++i) {
+                        float2 x = tc::fma2(make_float2(v[j + 2 * i], v[j + 2 * i + 1]), c2, m2);
+                        x = make_float2(tc::exp2_fast(x.x), tc::exp2_fast(x.y));
+                        l2 = tc::add2(l2, x);
+                        p[i] = tc::pack_bf16(x.x, x.y);
                     }
+                    tc::tmem_st16_async((C::kRep == 1 ? t_x : t_s + col0 / 2) + j / 2, p);
                 }
                 if (C::kRep > 1) {  // the other copies' keys (after the lane's own scores have been read)
                     const uint32_t z[16] = {};
@@ -549,7 +549,9 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             }
         }
         if (!wait.ok) err_bits = kErrTimeoutEpilogue;
-    } else if (warp == 8) {
+    } else {
+    if (F8) tc::fewer_registers<C::kOtherRegs>();
+    if (warp == 8) {
         // ------------------------------------------------------------ TMA producer
         uint64_t* const vf = F8 ? rfull : vfull;
         uint64_t* const ve = F8 ? rempty : vempty;
@@ -762,7 +764,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             tc::mbar_wait(fin, 0, zero_flag, kTeardown);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 19) {
         // ------------------------------------------------------------ FP8 converters
         // Eight lanes take 64 codes of a key, 8 each, and write the 16-byte piece of the 128-byte
         // swizzled bf16 tile that holds them; each lane does that twice a step (D = 128: the key's
@@ -785,7 +787,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             for (int i = 0; i < 2 * s.tiles; ++i) {
                 const Buffer buf = buffer_of<C::kTwo>(i, s.tiles);
                 if (!buf.v) {  // keys: their scales, by one warp
-                    if (static_cast<int>(ik & 7) == cw) {
+                    if (static_cast<int>(ik % (F8 ? C::kConv : 1)) == cw) {
                         const int b = ik % NK;
                         if (!wait(&xfull[b], (ik / NK) & 1)) break;
                         const uint32_t w = reinterpret_cast<const uint32_t*>(kexps + b * kKeys)[lane];
@@ -804,9 +806,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 const int j0 = (s.tile + tt) * kKeys;
                 const int za = max(lo - j0, 0), zb = min(s.L - j0, kKeys);
                 const bool partial = za > 0 || zb < kKeys;
+#pragma unroll 1
+                for (int base = cw * 16; base < kKeys; base += (F8 ? C::kConv : 1) * 16) {
                 uint2 x[2 * kStepsC];
                 uint32_t ex[2 * kStepsC];
-                auto row_of = [&](int i) { return cw * 16 + (i >> 1) * kStepRows + lr + (D == 128 ? 0 : 4 * (i & 1)); };
+                auto row_of = [&](int i) { return base + (i >> 1) * kStepRows + lr + (D == 128 ? 0 : 4 * (i & 1)); };
                 auto half_of = [&](int i) { return D == 128 ? (i ^ lr) & 1 : 0; };
                 const uint8_t* src = raw + rb * C::kRaw + lc * 8;
                 const uint8_t* se = exps + rb * kKeys;
@@ -843,6 +847,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     *reinterpret_cast<uint4*>(dst + half_of(i) * 16384 + row * 128 + ((lc ^ (row & 7)) << 4)) =
                         make_uint4(y[0], y[1], y[2], y[3]);
                 }
+                }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -852,6 +857,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             }
         }
         if (!wait.ok) err_bits = kErrTimeoutProducer;
+    }
     }
     if (err_bits) {
         *abort_flag = 1;

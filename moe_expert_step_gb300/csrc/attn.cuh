@@ -45,6 +45,7 @@ struct AttnArgs {
     int slot_rows;
     int page_log2, max_pages, n_pages;
     int causal, window;
+    int even;          // largest share (units a CTA) that is divided evenly
     float scale_log2;  // scale * log2(e): the kernels take exponentials to base 2
     unsigned long long timeout_ns;
 };
@@ -77,10 +78,16 @@ __device__ __forceinline__ int2 attn_tiles(const AttnArgs& a, int L) {  // first
     return make_int2(t0, max(1, (L + KT - 1) / KT - t0));
 }
 
-// The division: of W units over A CTAs the first W % A take one more than the rest.
+// The division: of W units over A CTAs the first W % A take one more than the rest.  With few units
+// a CTA (`even`), as many CTAs as have the same largest share: fewer parts to join for the same time.
 struct AttnShare {
     int A, base, extra;
-    __device__ __forceinline__ AttnShare(int W, int grid) : A(min(W, grid)), base(W / A), extra(W - base * A) {}
+    __device__ __forceinline__ AttnShare(int W, int grid, int even) : A(min(W, grid)) {
+        const int most = (W + A - 1) / A;
+        if (most <= even) A = (W + most - 1) / most;
+        base = W / A;
+        extra = W - base * A;
+    }
     __device__ __forceinline__ int first(int c) const { return c * base + min(c, extra); }  // of CTA c
     __device__ __forceinline__ int owner(int u) const {                                     // of unit u
         const int cut = extra * (base + 1);
@@ -123,7 +130,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int* sm) {
         W += sm[w];
     }
     incl += before;
-    const AttnShare sh(W, gridDim.x);
+    const AttnShare sh(W, gridDim.x, a.even);
     AttnPlan p;
     p.W = W;
     const int c = blockIdx.x;
@@ -155,7 +162,7 @@ __device__ __forceinline__ void attn_describe_join(const AttnArgs& a, const Attn
     if (p.count > 0) {
         const int nt = attn_tiles<KT>(a, attn_len(a, p.begin_r)).y, seg = p.begin_o / nt, t = p.begin_o - seg * nt;
         if (t > 0) {
-            const AttnShare sh(p.W, gridDim.x);
+            const AttnShare sh(p.W, gridDim.x, a.even);
             const int start = p.first - t, c0 = sh.owner(start);
             // the segment is the first one of CTA c0 (its slot 0) or not (slot 1)
             if (c0 == c - 1) j = make_int4(p.begin_r, seg, 2 * c0 + (sh.first(c0) != start), sh.owner(start + nt - 1));
