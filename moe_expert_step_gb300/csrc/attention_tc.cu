@@ -19,8 +19,8 @@
 // than 8 (a factor 256, harmless in fp32 sums and bf16 weights): O is then rescaled in tensor
 // memory by the softmax warps, which is rare after the first tiles.
 //
-// Warps: 0-7 softmax (two warpgroups), 8 TMA producer, 9-10 MMA issuers (one lane each, a
-// stream each), and with FP8 from 11 converters (E4M3 code * 2^exp -> bf16, exact, into the swizzled operand buffers).
+// Warps: 0-7 softmax (two warpgroups), 8 and 11 TMA producers (keys, values), 9-10 MMA
+// issuers (a stream each), and with FP8 12-19 converters (E4M3 code * 2^exp -> bf16, exact, into the swizzled operand buffers).
 // Keys outside [lo, L) of the request reach no result: their scores are replaced by -inf, and
 // their V rows, which a zero weight would still multiply (NaN), are zeroed in shared memory.
 // Every wait is bounded (timeout -> error word, orderly teardown).
@@ -49,9 +49,9 @@ struct Cfg {
     static constexpr int kHalves = kRep == 1 ? 2 : 1;     // turns in which a tile's keys pass through a stream
     static constexpr int kWide = kCols / kHalves;         // scores of a lane and turn: 32 or 64
     static constexpr int kConv = F8 ? 8 : 0;              // converter warps
-    // FP8: 20 warps (one idle) of 96 registers a thread, 61440 in all, redistributed: 256 softmax threads
+    // FP8: 20 warps of 96 registers a thread, 61440 in all, redistributed: 256 softmax threads
     // x 136 (64 scores in registers) + 384 others x 64 = 59392
-    static constexpr int kThreads = F8 ? 640 : 352;
+    static constexpr int kThreads = F8 ? 640 : 384;
     static constexpr int kSoftRegs = 136, kOtherRegs = 64;
     static_assert(!F8 || 256 * kSoftRegs + (kThreads - 256) * kOtherRegs <= kThreads * 96, "registers");
     static constexpr int kTile = kKeys * D * 2;           // bytes of a bf16 operand tile
@@ -551,12 +551,17 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         if (!wait.ok) err_bits = kErrTimeoutEpilogue;
     } else {
     if (F8) tc::fewer_registers<C::kOtherRegs>();
-    if (warp == 8) {
-        // ------------------------------------------------------------ TMA producer
-        uint64_t* const vf = F8 ? rfull : vfull;
-        uint64_t* const ve = F8 ? rempty : vempty;
-        constexpr int N = F8 ? NR : NV;
-        uint32_t ik = 0, iv = 0;
+    if (warp == 8 || warp == 11) {
+        // ------------------------------------------------------------ TMA producers: keys, values
+        const bool v = warp == 11;
+        uint64_t* const bf = !v ? kfull : F8 ? rfull : vfull;
+        uint64_t* const be = !v ? kempty : F8 ? rempty : vempty;
+        const CUtensorMap* map = v ? &vmap : &kmap;
+        uint8_t* const base = !v ? kring : F8 ? raw : vring;
+        const int bytes = !v ? C::kKTile : F8 ? C::kRaw : C::kTile, N = v ? (F8 ? NR : NV) : NK;
+        const uint8_t* const ex = v ? a.v_exp : a.k_exp;
+        int b = 0;              // buffer
+        uint32_t it = 0, ph = 0;  // buffers so far, times round the ring
         const int page = 1 << a.page_log2, pages = kKeys >> a.page_log2;
         AttnWalk s = attn_begin<kKeys>(a, plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
@@ -570,68 +575,59 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 const int pg = at + lane;
                 return pg >= pg_lo && pg < pg_end ? __ldg(&tab[pg]) : -2;
             };
-            int chunk = pg0, ids_last = -2, ids = table(chunk), ids_next = table(chunk + 32);
+            int chunk = pg0, ids = table(chunk), ids_next = table(chunk + 32);
 #pragma unroll 1
-            for (int i = 0; i < 2 * s.tiles; ++i) {
-                const Buffer buf = buffer_of<C::kTwo>(i, s.tiles);
-                // lane l: page l of the tile.  The keys' tiles ascend; the values' follow at most
-                // two tiles behind, so they are in these 32 pages or the last.
-                const int at = pg0 + buf.tile * pages;
+            for (int at = pg0; at < pg0 + s.tiles * pages; at += pages, ++it) {
                 if (at >= chunk + 32) {
                     chunk += 32;
-                    ids_last = ids;
                     ids = ids_next;
                     ids_next = table(chunk + 32);
                 }
-                const int id = __shfl_sync(0xffffffffu, at < chunk ? ids_last : ids, (at - chunk + lane) & 31);
-                const int b = buf.v ? iv % N : ik % NK;
-                if (!(buf.v ? wait(&ve[b], ((iv / N) & 1) ^ 1u) : wait(&kempty[b], ((ik / NK) & 1) ^ 1u))) break;
+                // lane l: page l of the tile, -2 for one that is not loaded
+                const int id = __shfl_sync(0xffffffffu, ids, (at - chunk + lane) & 31);
                 const bool here = lane < pages && id != -2;
                 const bool good = here && static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages);
                 if (here && !good) record_error(a.err, kErrBadInput);
                 const unsigned on = __ballot_sync(0xffffffffu, good);
                 const int y = good ? (id * a.Hkv + h) << a.page_log2 : 0;
                 const int keys = __popc(on) * page;
-                uint64_t* bar = buf.v ? &vf[b] : &kfull[b];
+                if (!wait(&be[b], ph ^ 1u)) break;
+                uint64_t* ebar = F8 && !v ? &xfull[b] : &bf[b];  // what the exponents' copies report to
                 if (lane == 0) {
-                    if (F8 && !buf.v) tc::mbar_arrive_expect_tx(&xfull[b], keys);
-                    tc::mbar_arrive_expect_tx(bar, keys * (F8 ? D + buf.v : 2 * D));
+                    if (F8 && !v) tc::mbar_arrive_expect_tx(ebar, keys);
+                    tc::mbar_arrive_expect_tx(&bf[b], keys * (F8 ? D + v : 2 * D));
                 }
                 __syncwarp();
-                const CUtensorMap* map = buf.v ? &vmap : &kmap;
-                uint8_t* dst = !buf.v ? kring + b * C::kKTile : F8 ? raw + b * C::kRaw : vring + b * C::kTile;
+                uint8_t* dst = base + b * bytes;
+                uint8_t* edst = (v ? exps : kexps) + b * kKeys;
 #pragma unroll 1
                 for (int p = 0; p < pages; ++p) {
                     const int yp = __shfl_sync(0xffffffffu, y, p);
                     if (!(on >> p & 1)) continue;
                     if (tc::elect_one()) {
                         if (F8) {
-                            if (buf.v)
-                                tc::bulk_load(exps + b * kKeys + p * page, a.v_exp + yp, page, bar);
-                            else
-                                tc::bulk_load(kexps + b * kKeys + p * page, a.k_exp + yp, page, &xfull[b]);
-                            tc::tma_load_2d(dst + p * page * D, map, bar, 0, yp);
+                            tc::tma_load_2d(dst + p * page * D, map, &bf[b], 0, yp);
+                            tc::bulk_load(edst + p * page, ex + yp, page, ebar);
                         } else {
 #pragma unroll
                             for (int half = 0; half < D / 64; ++half)
-                                tc::tma_load_2d(dst + half * 16384 + p * page * 128, map, bar, half * 64, yp);
+                                tc::tma_load_2d(dst + half * 16384 + p * page * 128, map, &bf[b], half * 64, yp);
                         }
                     }
                     __syncwarp();
                 }
-                if (buf.v) ++iv;
-                else ++ik;
+                if (++b == N) b = 0, ph ^= 1u;
             }
         }
         if (!wait.ok) err_bits = kErrTimeoutProducer;
         // copies in flight land before the CTA ends
         if (lane == 0) {
-            for (uint32_t i = iv > N ? iv - N : 0; i < iv; ++i) tc::mbar_wait(&vf[i % N], (i / N) & 1, zero_flag, kTeardown);
-            for (uint32_t i = ik > NK ? ik - NK : 0; i < ik; ++i) {
-                // (an FP8 tile's phase also needs its scales, which an aborted CTA may not write: the
-                // exponents are the last of the tile's copies to be waited for then)
-                if (F8) tc::mbar_wait(&xfull[i % NK], (i / NK) & 1, zero_flag, kTeardown);
-                tc::mbar_wait(&kfull[i % NK], (i / NK) & 1, zero_flag, F8 && !wait.ok ? kAbortedTile : kTeardown);
+            for (uint32_t i = it > N ? it - N : 0; i < it; ++i) {
+                const int w = i % N;
+                const uint32_t parity = (i / N) & 1;
+                // (a phase of FP8 keys also needs their scales, which an aborted CTA may not write)
+                if (F8 && !v) tc::mbar_wait(&xfull[w], parity, zero_flag, kTeardown);
+                tc::mbar_wait(&bf[w], parity, zero_flag, F8 && !v && !wait.ok ? kAbortedTile : kTeardown);
             }
         }
         __syncwarp();
@@ -764,7 +760,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             tc::mbar_wait(fin, 0, zero_flag, kTeardown);
         }
         __syncwarp();
-    } else if (warp < 19) {
+    } else {
         // ------------------------------------------------------------ FP8 converters
         // Eight lanes take 64 codes of a key, 8 each, and write the 16-byte piece of the 128-byte
         // swizzled bf16 tile that holds them; each lane does that twice a step (D = 128: the key's
@@ -776,7 +772,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         // are placed as bytes 0 and 2, then 1 and 3, which is the column order 0, 2, 1, 3.  The
         // conversion instruction would share its unit with the exponentials (2300 cycles a
         // tile instead of ~1000); NaN codes, which the placement does not keep, are rare and patched.
-        const int cw = warp - 11;
+        const int cw = warp - 12;
         constexpr int kStepRows = D == 128 ? 4 : 8, kStepsC = 16 / kStepRows;  // of a warp's 16 keys
         const int lr = lane >> 3, lc = lane & 7;
         uint32_t ik = 0, iv = 0;
