@@ -103,7 +103,7 @@ struct Waits {
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
         if (ok) {
             int r = 1;
-            if ((threadIdx.x & 31) == 0) r = tc::mbar_poll(bar, parity, abort, limit);
+            if ((threadIdx.x & 31) == 0) r = tc::mbar_wait_cycles(bar, parity, abort, limit);
             ok = __shfl_sync(0xffffffffu, r, 0) != 0;
             __syncwarp();
         }
@@ -114,7 +114,7 @@ struct Waits {
         if (ok) {
             const int l = threadIdx.x & 31;
             int r = 1;
-            if (l < 2) r = tc::mbar_poll(l ? bar1 : bar0, l ? parity1 : parity0, abort, limit);
+            if (l < 2) r = tc::mbar_wait_cycles(l ? bar1 : bar0, l ? parity1 : parity0, abort, limit);
             ok = __all_sync(0xffffffffu, r) != 0;
             __syncwarp();
         }
@@ -262,13 +262,19 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     }
                 }
                 __syncwarp();
-                // (a loop over one piece of code, the loaded pieces moved up: unrolled, its instructions
-                // alone took 7 us to arrive)
+                // (four pieces of code in a loop, the loaded pieces moved up: unrolled in full, the
+                // instructions alone took 7 us to arrive)
 #pragma unroll 1
-                for (int m = m0; m < 128; m += kStep) {
-                    const uint4 piece16 = x[0];
+                for (int mb = m0; mb < 128; mb += 4 * kStep) {
+                    uint4 y[4];
 #pragma unroll
-                    for (int b = 0; b + 1 < kBatch; ++b) x[b] = x[b + 1];
+                    for (int u = 0; u < 4; ++u) y[u] = x[u];
+#pragma unroll
+                    for (int b = 0; b + 4 < kBatch; ++b) x[b] = x[b + 4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int m = mb + u * kStep;
+                    const uint4 piece16 = y[u];
                     if (!F8) {
                         *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = piece16;
                         continue;
@@ -310,6 +316,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     uint8_t* d = dst + m * D + (piece << 4) + (c & 1) * 8;
                     *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2*>(d + 128 * D) = make_uint2(lo[0], lo[1]);
+                }
                 }
                 tc::fence_proxy_async_smem();
                 tc::fence_before_sync();

@@ -18,17 +18,15 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lead
     d |= static_cast<uint64_t>(2) << 61;
     return d;
 }
-// mbar_wait by polling, its limit in SM clock cycles.  The blocking probe (try_wait) returned up to
-// 850 cycles after the phase was complete, longer than most of these waits; one lane's polls
-// take an issue slot every ~50 cycles.
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, long long limit) {
+// mbar_wait with its limit in SM clock cycles (reading the global timer before every probe costs
+// more than most of these waits).  The probes block: polling warps took issue slots from the
+// softmax and made the FP8 launch a fifth slower.
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t* bar, uint32_t parity, volatile int* abort, long long limit) {
     if (mbar_test_wait(bar, parity)) return true;
     if (limit <= 0) return false;
     const long long t0 = clock64();
     for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_test_wait(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort || clock64() - t0 >= limit) return false;
     }
 }
