@@ -146,8 +146,12 @@ def _p(t):
 
 
 def _s(stream):
-    import torch
+    """cudaStream_t of a torch stream (None: the current one), or of an integer handle."""
     if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone: no Stream object
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -309,18 +313,18 @@ def kv_workspace(kd: KvDims, R: int, n_q: int, device="cuda", stream=None):
 
 def _rows(t, heads: int, kd: KvDims, what: str) -> int:
     """Distance between the rows of t [tokens, heads, D], which may be part of a wider row."""
-    st = t.stride()
-    if (len(st) != 3 or st[2] != 1 or (heads > 1 and st[1] != kd.D) or t.shape[1] != heads or t.shape[2] != kd.D
+    st, shape = t.stride(), t.shape
+    if (len(st) != 3 or st[2] != 1 or (heads > 1 and st[1] != kd.D) or shape[1] != heads or shape[2] != kd.D
             or t.element_size() != (4 if kd.dtype == F32 else 2)):
         raise MoeStepError(EINVAL, f"{what} must be [tokens, {heads}, {kd.D}] in the activations' type, heads dense")
     if not t.is_cuda:
         raise MoeStepError(EINVAL, f"{what} must be on the GPU")
-    return st[0] if t.shape[0] > 1 else max(st[0], heads * kd.D)
+    return st[0] if shape[0] > 1 else max(st[0], heads * kd.D)
 
 
 def _dense(t, shape, size: int, what: str) -> None:
     """t is a contiguous GPU tensor of the shape, `size` bytes an element."""
-    if tuple(t.shape) != shape or t.element_size() != size or not t.is_contiguous():
+    if t.shape != shape or t.element_size() != size or not t.is_contiguous():
         raise MoeStepError(EINVAL, f"{what} must be contiguous, of shape {list(shape)} and {size} bytes an element")
     if not t.is_cuda:
         raise MoeStepError(EINVAL, f"{what} must be on the GPU")

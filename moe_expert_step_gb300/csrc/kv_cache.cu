@@ -12,6 +12,8 @@
 #include "kv.h"
 #include "launch.cuh"
 
+#include <type_traits>
+
 namespace moestep {
 namespace {
 
@@ -26,20 +28,46 @@ struct CopyArgs {
     uint8_t* ve;
     const int32_t* table;
     int n, Hkv, page_log2, n_pages, max_pages;
-    long long tokens;
+    long long vectors;  // tokens * 2 * Hkv
     int* err;
 };
 
-// Place of a token's vector of one head: its row index (vectors of D elements from the
-// pool's start), -1 for a token that is not stored, -2 for a bad position or page.
-__device__ __forceinline__ long long place(const CopyArgs& a, long long t, int h) {
-    const int p = __ldg(&a.pos[t]);
+// A thread handles 16 consecutive elements of kPer vectors; D / 16 lanes share a vector, and
+// consecutive vectors are a token's key heads, then its value heads, so a warp reads and
+// writes whole lines.  A block takes 2 * 256 / (D / 16) vectors: their tokens and requests are
+// found with one wide division a block and narrow ones after it.
+constexpr int kPer = 2;
+
+struct Vector {
+    long long t;  // token
+    int r;        // its request
+    int h;
+    bool v, on;
+};
+
+template <int L>
+__device__ __forceinline__ Vector vector_of(const CopyArgs& a, long long t0, unsigned rem, int r0, unsigned tl0, int q,
+                                            long long first) {
+    const unsigned local = q * (256 / L) + threadIdx.x / L, per = 2 * a.Hkv;
+    const unsigned j = rem + local, dt = j / per, w = j - dt * per, tl = tl0 + dt, dr = tl / a.n;
+    Vector x;
+    x.t = t0 + dt;
+    x.r = r0 + static_cast<int>(dr);
+    x.v = w >= static_cast<unsigned>(a.Hkv);
+    x.h = static_cast<int>(x.v ? w - a.Hkv : w);
+    x.on = first + local < a.vectors;
+    return x;
+}
+
+// Place of a token's vector: its row index (vectors of D elements from the pool's start), -1
+// for a token that is not stored, -2 for a bad position or page.
+__device__ __forceinline__ long long place(const CopyArgs& a, int p, const Vector& x) {
     if (p < 0) return -1;
     const int pg = p >> a.page_log2;
     if (pg >= a.max_pages) return -2;
-    const int id = __ldg(&a.table[t / a.n * a.max_pages + pg]);
+    const int id = __ldg(&a.table[static_cast<long long>(x.r) * a.max_pages + pg]);
     if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_pages)) return -2;
-    return ((static_cast<long long>(id) * a.Hkv + h) << a.page_log2) + (p & ((1 << a.page_log2) - 1));
+    return ((static_cast<long long>(id) * a.Hkv + x.h) << a.page_log2) + (p & ((1 << a.page_log2) - 1));
 }
 
 // e of a vector whose largest finite magnitude (or infinity) is amax >= 0
@@ -66,77 +94,76 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t w) {
     return __half22float2(*reinterpret_cast<__half2*>(&r));
 }
 
-// Eight consecutive elements of a vector a thread: D / 8 lanes share a vector, and
-// consecutive lane groups are the heads of one token's row, so a warp reads whole lines.
-// `a` works on item = (token, k or v, head, lane); kPer items a thread keep enough loads in flight.
-constexpr int kPer = 4;
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<bf16>(const bf16* p, float (&x)[8]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
+// 16 elements as they are loaded: 2 (bf16) or 4 (fp32) 16-byte pieces
+template <int DT>
+struct Sixteen {
+    static constexpr int N = DT == MOESTEP_F32 ? 4 : 2;
+    uint4 p[N];
+};
 
 template <int DT, int D>
 __global__ void __launch_bounds__(256) kv_write_kernel(const CopyArgs a) {
     pdl_trigger();
     pdl_wait();
     using T = typename std::conditional<DT == MOESTEP_F32, float, bf16>::type;
-    constexpr int L = D / 8;
-    const long long items = a.tokens * 2 * a.Hkv * L;
-    const long long base = static_cast<long long>(blockIdx.x) * (256 * kPer) + threadIdx.x;
+    using S = Sixteen<DT>;
+    constexpr int L = D / 16;
+    const long long first = static_cast<long long>(blockIdx.x) * (256 / L * kPer);
+    const long long t0 = first / (2 * a.Hkv);
+    const unsigned rem = static_cast<unsigned>(first - t0 * (2 * a.Hkv));
+    const int r0 = static_cast<int>(t0 / a.n);
+    const unsigned tl0 = static_cast<unsigned>(t0 - static_cast<long long>(r0) * a.n);
+    const int lane = threadIdx.x % L;
+    Vector vec[kPer];
+    int pos[kPer];
+    S in[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {  // the tokens' rows do not wait for their places
+        vec[q] = vector_of<L>(a, t0, rem, r0, tl0, q, first);
+        pos[q] = -1;
+        if (vec[q].on) {
+            pos[q] = __ldg(&a.pos[vec[q].t]);
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const T*>(vec[q].v ? a.v : a.k) + vec[q].t * a.ld + vec[q].h * D + lane * 16);
+#pragma unroll
+            for (int i = 0; i < S::N; ++i) in[q].p[i] = __ldg(src + i);
+        }
+    }
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-        const long long it = base + q * 256;
-        const bool on = it < items;  // whole warps' lane groups agree: items is a multiple of L
-        const int lane = static_cast<int>(it % L);
-        const long long vec = it / L;
-        const int h = static_cast<int>(vec % a.Hkv);
-        const long long tv = vec / a.Hkv;
-        const int isv = static_cast<int>(tv & 1);
-        const long long t = tv >> 1;
-        long long row = -1;
-        if (on) row = place(a, t, h);
+        const long long row = vec[q].on ? place(a, pos[q], vec[q]) : -1;
         if (row == -2 && lane == 0) record_error(a.err, kErrBadInput);
-        const T* src = static_cast<const T*>(isv ? a.v : a.k) + t * a.ld + h * D + lane * 8;
+        void* cache = vec[q].v ? a.vc : a.kc;
         if (DT != MOESTEP_FP8) {
             if (row < 0) continue;
-            const uint4* s = reinterpret_cast<const uint4*>(src);
-            uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(isv ? a.vc : a.kc) + row * D + lane * 8);
-            d[0] = __ldg(s);
-            if (DT == MOESTEP_F32) d[1] = __ldg(s + 1);
+            uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(cache) + row * D + lane * 16);
+#pragma unroll
+            for (int i = 0; i < S::N; ++i) d[i] = in[q].p[i];
             continue;
         }
-        float x[8] = {};
-        if (row >= 0) load8<T>(src, x);
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 u = in[q].p[i / 4];
+            const uint32_t w = vec[q].on ? (i % 4 == 0 ? u.x : i % 4 == 1 ? u.y : i % 4 == 2 ? u.z : u.w) : 0u;
+            x[2 * i] = __uint_as_float(w << 16);
+            x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+        }
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf passes over NaN
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf passes over NaN
 #pragma unroll
         for (int o = L / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (row < 0) continue;
         const int e = kv_exponent(amax);
         const float s = pow2f(-e);
-        uint32_t w[2];
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
             w[i] = to_e4m3x2(x[4 * i] * s, x[4 * i + 1] * s) |
                    static_cast<uint32_t>(to_e4m3x2(x[4 * i + 2] * s, x[4 * i + 3] * s)) << 16;
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(isv ? a.vc : a.kc) + row * D + lane * 8) =
-            make_uint2(w[0], w[1]);
-        if (lane == 0) (isv ? a.ve : a.ke)[row] = static_cast<uint8_t>(e + 127);
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(cache) + row * D + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (lane == 0) (vec[q].v ? a.ve : a.ke)[row] = static_cast<uint8_t>(e + 127);
     }
 }
 
@@ -145,58 +172,78 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const CopyArgs a) {
     pdl_trigger();
     pdl_wait();
     using T = typename std::conditional<DT == MOESTEP_F32, float, bf16>::type;
-    constexpr int L = D / 8;
-    const long long items = a.tokens * 2 * a.Hkv * L;
-    const long long base = static_cast<long long>(blockIdx.x) * (256 * kPer) + threadIdx.x;
+    using S = Sixteen<DT>;
+    constexpr int L = D / 16;
+    const long long first = static_cast<long long>(blockIdx.x) * (256 / L * kPer);
+    const long long t0 = first / (2 * a.Hkv);
+    const unsigned rem = static_cast<unsigned>(first - t0 * (2 * a.Hkv));
+    const int r0 = static_cast<int>(t0 / a.n);
+    const unsigned tl0 = static_cast<unsigned>(t0 - static_cast<long long>(r0) * a.n);
+    const int lane = threadIdx.x % L;
+    Vector vec[kPer];
+    long long row[kPer];
+    int pos[kPer];
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-        const long long it = base + q * 256;
-        if (it >= items) continue;
-        const int lane = static_cast<int>(it % L);
-        const long long vec = it / L;
-        const int h = static_cast<int>(vec % a.Hkv);
-        const long long tv = vec / a.Hkv;
-        const int isv = static_cast<int>(tv & 1);
-        const long long t = tv >> 1;
-        const long long row = place(a, t, h);
-        if (row == -2 && lane == 0) record_error(a.err, kErrBadInput);
-        uint4 o[2] = {};
-        if (row >= 0) {
-            if (DT != MOESTEP_FP8) {
-                const uint4* s =
-                    reinterpret_cast<const uint4*>(static_cast<const T*>(isv ? a.vc : a.kc) + row * D + lane * 8);
-                o[0] = __ldg(s);
-                if (DT == MOESTEP_F32) o[1] = __ldg(s + 1);
-            } else {
-                const uint2 w = __ldg(
-                    reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(isv ? a.vc : a.kc) + row * D + lane * 8));
-                // 2^(exp - 127) in two factors: the byte of a corrupted cache may name any power
-                const int e = __ldg(&(isv ? a.ve : a.ke)[row]) - 127, e1 = e >> 1;
-                const float s1 = pow2f(e1), s2 = pow2f(e - e1);
-                uint32_t r[4];
+        vec[q] = vector_of<L>(a, t0, rem, r0, tl0, q, first);
+        pos[q] = vec[q].on ? __ldg(&a.pos[vec[q].t]) : -1;
+    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint16_t c = static_cast<uint16_t>((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
-                    const float2 f = from_e4m3x2(c);
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s1 * s2, f.y * s1 * s2);
-                    r[i] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                o[0] = make_uint4(r[0], r[1], r[2], r[3]);
-            }
+    for (int q = 0; q < kPer; ++q) {
+        row[q] = place(a, pos[q], vec[q]);
+        if (row[q] == -2 && lane == 0) record_error(a.err, kErrBadInput);
+    }
+    S o[kPer];
+    uint4 codes[kPer];
+    int ex[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {  // all loads before the first use
+        const void* cache = vec[q].v ? a.vc : a.kc;
+#pragma unroll
+        for (int i = 0; i < S::N; ++i) o[q].p[i] = make_uint4(0, 0, 0, 0);
+        codes[q] = make_uint4(0, 0, 0, 0);
+        ex[q] = 127;
+        if (row[q] < 0) continue;
+        if (DT == MOESTEP_FP8) {
+            codes[q] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + row[q] * D + lane * 16));
+            ex[q] = __ldg(&(vec[q].v ? a.ve : a.ke)[row[q]]);
+        } else {
+            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(cache) + row[q] * D + lane * 16);
+#pragma unroll
+            for (int i = 0; i < S::N; ++i) o[q].p[i] = __ldg(s + i);
         }
-        uint4* d = reinterpret_cast<uint4*>(const_cast<T*>(static_cast<const T*>(isv ? a.v : a.k)) + t * a.ld + h * D +
-                                            lane * 8);
-        d[0] = o[0];
-        if (DT == MOESTEP_F32) d[1] = o[1];
+    }
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        if (!vec[q].on) continue;
+        if (DT == MOESTEP_FP8) {
+            // 2^(exp - 127) in two factors: the byte of a corrupted cache may name any power
+            const int e = ex[q] - 127, e1 = e >> 1;
+            const float s1 = pow2f(e1), s2 = pow2f(e - e1);
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t c4 = i / 2 == 0 ? codes[q].x : i / 2 == 1 ? codes[q].y : i / 2 == 2 ? codes[q].z : codes[q].w;
+                const float2 f = from_e4m3x2(static_cast<uint16_t>(c4 >> (16 * (i & 1))));
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s1 * s2, f.y * s1 * s2);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            o[q].p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            o[q].p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        uint4* d = reinterpret_cast<uint4*>(const_cast<T*>(static_cast<const T*>(vec[q].v ? a.v : a.k)) +
+                                            vec[q].t * a.ld + vec[q].h * D + lane * 16);
+#pragma unroll
+        for (int i = 0; i < S::N; ++i) d[i] = o[q].p[i];
     }
 }
 
 template <int DT, int D>
 cudaError_t launch_copy(bool write, const CopyArgs& a, cudaStream_t s) {
-    const long long items = a.tokens * 2 * a.Hkv * (D / 8);
-    const long long ctas = (items + 256 * kPer - 1) / (256 * kPer);
-    return write ? launch_pdl(kv_write_kernel<DT, D>, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, s, a)
-                 : launch_pdl(kv_read_kernel<DT, D>, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, s, a);
+    constexpr int per_block = 256 / (D / 16) * kPer;
+    const dim3 grid(static_cast<unsigned>((a.vectors + per_block - 1) / per_block));
+    return write ? launch_pdl(kv_write_kernel<DT, D>, grid, dim3(256), 0, s, a)
+                 : launch_pdl(kv_read_kernel<DT, D>, grid, dim3(256), 0, s, a);
 }
 
 int copy_call(bool write, const moestep_kv_dims* kd, int R, int n, const void* k, const void* v, long long ld,
@@ -209,7 +256,8 @@ int copy_call(bool write, const moestep_kv_dims* kd, int R, int n, const void* k
     if ((rc = check_kv_rows(k, ld, width, kd->dtype)) != MOESTEP_OK) return rc;
     if ((rc = check_kv_rows(v, ld, width, kd->dtype)) != MOESTEP_OK) return rc;
     const long long tokens = 1ll * R * n;
-    if (tokens > (1ll << 31) - 1 || tokens * 2 * width / 8 > (1ll << 40)) return MOESTEP_EUNSUPPORTED;
+    // (one block handles at least 64 vectors)
+    if (tokens > (1ll << 31) - 1 || tokens * kd->Hkv > (1ll << 35)) return MOESTEP_EUNSUPPORTED;
     if ((rc = check_kv_ws(ws, ws_bytes, kKvHeader)) != MOESTEP_OK) return rc;
     if ((rc = device_ok(nullptr)) != MOESTEP_OK) return rc;
     CopyArgs a{};
@@ -227,7 +275,7 @@ int copy_call(bool write, const moestep_kv_dims* kd, int R, int n, const void* k
     a.page_log2 = kd->page == 16 ? 4 : kd->page == 32 ? 5 : kd->page == 64 ? 6 : 7;
     a.n_pages = kd->n_pages;
     a.max_pages = kd->max_pages;
-    a.tokens = tokens;
+    a.vectors = tokens * 2 * kd->Hkv;
     a.err = static_cast<int*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_begin(8, s);

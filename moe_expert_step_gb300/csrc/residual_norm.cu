@@ -1,8 +1,7 @@
 // The gated residual update after a block and the norm before the next one, one pass:
 //   h' = h + s * g * (w_post * y * rsqrt(mean(y^2) + eps)),   x = w_pre * h' * rsqrt(mean(h'^2) + eps)
-// One CTA a token.  A token's y and h are read once, held in registers through both
-// reductions, and h' and x are written once: 12 to 16 bytes an element, memory-bound.
-#include "combine.cuh"
+// A token's y and h are read once, held in registers through both reductions, and h' and x are
+// written once: 12 to 16 bytes an element, memory-bound.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv.h"
@@ -24,91 +23,168 @@ struct NormArgs {
     const void* w_pre;
     void* x;
     float eps;
-    int H, P;
+    int H, P, T;
 };
 
+// Eight consecutive columns, as loaded
 template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
+struct Eight;
 template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
 template <>
-__device__ __forceinline__ float4 load4<bf16>(const bf16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
+struct Eight<bf16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const bf16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Columns c = 4 (tid + 256 i), i < N: N = ceil(H / 1024)
-template <typename TY, typename TX, int N>
-__global__ void __launch_bounds__(256) residual_norm_kernel(const NormArgs a) {
-    __shared__ float red[9];
+constexpr int kNormThreads = 128;
+
+// Sum over the W warps of a row (W = 1, or the whole block of 4)
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+    v = warp_sum(v);
+    if (W == 1) return v;
+    __syncthreads();  // the last sum has been read
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// A row on W warps: lane i of warp w holds columns 8 (i + 32 (w + W j)) .. + 7, j < N.
+template <typename TY, typename TX, int W, int N>
+__global__ void __launch_bounds__(kNormThreads) residual_norm_kernel(const NormArgs a) {
+    __shared__ float red[4];
     pdl_trigger();
     pdl_wait();
-    const size_t row = static_cast<size_t>(blockIdx.x) * a.H;
-    const TY* y = static_cast<const TY*>(a.y) + row;
-    float4 yv[N], hv[N];
-    float ss = 0.f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = W == 1 ? blockIdx.x * 4 + warp : blockIdx.x;
+    if (t >= a.T) return;  // (W = 1 only: no barrier follows)
+    const size_t row = static_cast<size_t>(t) * a.H;
+    const int c0 = 8 * (lane + (W == 1 ? 0 : 32 * warp));
+    Eight<TY> yv[N];
+    float h[N][8];
+    // y and h of the whole row in flight at once
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 4 * (threadIdx.x + 256 * i);
-        yv[i] = hv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < N; ++j) {
+        const int c = c0 + 256 * W * j;
+        if (c < a.H) yv[j].load(static_cast<const TY*>(a.y) + row + c);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int c = c0 + 256 * W * j;
+        Eight<float> e;
         if (c < a.H) {
-            yv[i] = load4<TY>(y + c);
-            hv[i] = load4<float>(a.h_in + row + c);
+            e.load(a.h_in + row + c);
+            e.get(h[j]);
         }
     }
-    float ry = 1.f;
+    float ry = 1.f, ss = 0.f;
     if (a.w_post) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            ss += yv[i].x * yv[i].x + yv[i].y * yv[i].y + yv[i].z * yv[i].z + yv[i].w * yv[i].w;
-        ry = 1.0f / sqrtf(group_sum_256(ss, red) / a.H + a.eps);
+        for (int j = 0; j < N; ++j) {
+            if (c0 + 256 * W * j >= a.H) continue;
+            float y[8];
+            yv[j].get(y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += y[i] * y[i];
+        }
+        ry = 1.0f / sqrtf(row_sum<W>(ss, red) / a.H + a.eps);
     }
-    const float* g = a.gate ? a.gate + (blockIdx.x / a.P) * a.gate_ld : nullptr;
+    const float* g = a.gate ? a.gate + (t / a.P) * a.gate_ld : nullptr;
     ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 4 * (threadIdx.x + 256 * i);
+    for (int j = 0; j < N; ++j) {
+        const int c = c0 + 256 * W * j;
         if (c >= a.H) continue;
-        float4 v = yv[i];
+        float y[8], w[8];
+        yv[j].get(y);
         if (a.w_post) {
-            const float4 w = load4<TX>(static_cast<const TX*>(a.w_post) + c);
-            v = make_float4(v.x * ry * w.x, v.y * ry * w.y, v.z * ry * w.z, v.w * ry * w.w);
+            Eight<TX> e;
+            e.load(static_cast<const TX*>(a.w_post) + c);
+            e.get(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = y[i] * ry * w[i];
         }
         if (g) {
-            const float4 w = load4<float>(g + c);
-            v = make_float4(v.x * w.x, v.y * w.y, v.z * w.z, v.w * w.w);
+            Eight<float> e;
+            e.load(g + c);
+            e.get(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= w[i];
         }
-        float4 h = hv[i];
-        h = make_float4(h.x + a.res_scale * v.x, h.y + a.res_scale * v.y, h.z + a.res_scale * v.z,
-                        h.w + a.res_scale * v.w);
-        hv[i] = h;
-        ss += h.x * h.x + h.y * h.y + h.z * h.z + h.w * h.w;
-        *reinterpret_cast<float4*>(a.h_out + row + c) = h;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h[j][i] += a.res_scale * y[i];
+            ss += h[j][i] * h[j][i];
+        }
+        store8(a.h_out + row + c, h[j]);
     }
     if (a.x == nullptr) return;
-    const float rh = 1.0f / sqrtf(group_sum_256(ss, red) / a.H + a.eps);
-    TX* x = static_cast<TX*>(a.x) + row;
+    const float rh = 1.0f / sqrtf(row_sum<W>(ss, red) / a.H + a.eps);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 4 * (threadIdx.x + 256 * i);
+    for (int j = 0; j < N; ++j) {
+        const int c = c0 + 256 * W * j;
         if (c >= a.H) continue;
-        const float4 w = a.w_pre ? load4<TX>(static_cast<const TX*>(a.w_pre) + c) : make_float4(1.f, 1.f, 1.f, 1.f);
-        const float4 h = hv[i];
-        store4<TX>(x + c, make_float4(h.x * rh * w.x, h.y * rh * w.y, h.z * rh * w.z, h.w * rh * w.w));
+        float w[8];
+        if (a.w_pre) {
+            Eight<TX> e;
+            e.load(static_cast<const TX*>(a.w_pre) + c);
+            e.get(w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] *= h[j][i] * rh;
+        store8(static_cast<TX*>(a.x) + row + c, w);
     }
 }
 
 template <typename TY, typename TX>
-cudaError_t launch_norm(int T, const NormArgs& a, cudaStream_t s) {
-    const dim3 grid(T), block(256);
-    switch ((a.H + 1023) / 1024) {
-        case 1: return launch_pdl(residual_norm_kernel<TY, TX, 1>, grid, block, 0, s, a);
-        case 2: return launch_pdl(residual_norm_kernel<TY, TX, 2>, grid, block, 0, s, a);
-        case 3:
-        case 4: return launch_pdl(residual_norm_kernel<TY, TX, 4>, grid, block, 0, s, a);
-        default: return launch_pdl(residual_norm_kernel<TY, TX, 7>, grid, block, 0, s, a);
+cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
+    // One warp a row where there are rows enough to fill the machine and a row fits its registers;
+    // else four (8192 tokens x 2048: see the file's head; 32 tokens: shorter rows a lane)
+    const dim3 block(kNormThreads);
+    if (a.H <= 2048 && a.T >= 8 * sms) {
+        const dim3 grid((a.T + 3) / 4);
+        if (a.H <= 512) return launch_pdl(residual_norm_kernel<TY, TX, 1, 2>, grid, block, 0, s, a);
+        if (a.H <= 1024) return launch_pdl(residual_norm_kernel<TY, TX, 1, 4>, grid, block, 0, s, a);
+        return launch_pdl(residual_norm_kernel<TY, TX, 1, 8>, grid, block, 0, s, a);
     }
+    const dim3 grid(a.T);
+    if (a.H <= 2048) return launch_pdl(residual_norm_kernel<TY, TX, 4, 2>, grid, block, 0, s, a);
+    if (a.H <= 4096) return launch_pdl(residual_norm_kernel<TY, TX, 4, 4>, grid, block, 0, s, a);
+    return launch_pdl(residual_norm_kernel<TY, TX, 4, 8>, grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -128,16 +204,17 @@ extern "C" int block_residual_norm(const moestep_dims* dims, int T, const void* 
                           static_cast<const void*>(h_out), w_pre, static_cast<const void*>(x)})
         if (!kv_aligned16(p)) return MOESTEP_EALIGN;
     if (gate && gate_ld % 4) return MOESTEP_EALIGN;
-    if (dims->H > 7168) return MOESTEP_EUNSUPPORTED;
-    if ((rc = device_ok(nullptr)) != MOESTEP_OK) return rc;
-    NormArgs a{y, w_post, gate, gate_ld, res_scale, h_in, h_out, w_pre, x, eps, dims->H, dims->P};
+    if (dims->H > 8192) return MOESTEP_EUNSUPPORTED;
+    int sms = 0;
+    if ((rc = device_ok(&sms)) != MOESTEP_OK) return rc;
+    NormArgs a{y, w_post, gate, gate_ld, res_scale, h_in, h_out, w_pre, x, eps, dims->H, dims->P, T};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_begin(8, s);
     cudaError_t e;
     if (dims->dtype == MOESTEP_F32)
-        e = y_dtype == MOESTEP_F32 ? launch_norm<float, float>(T, a, s) : launch_norm<bf16, float>(T, a, s);
+        e = y_dtype == MOESTEP_F32 ? launch_norm<float, float>(a, sms, s) : launch_norm<bf16, float>(a, sms, s);
     else
-        e = y_dtype == MOESTEP_F32 ? launch_norm<float, bf16>(T, a, s) : launch_norm<bf16, bf16>(T, a, s);
+        e = y_dtype == MOESTEP_F32 ? launch_norm<float, bf16>(a, sms, s) : launch_norm<bf16, bf16>(a, sms, s);
     prof_end(8, s);
     if (e != cudaSuccess) {
         set_last_cuda(static_cast<int>(e));
