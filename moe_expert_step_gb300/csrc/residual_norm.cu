@@ -1,7 +1,9 @@
 // The gated residual update after a block and the norm before the next one, one pass:
 //   h' = h + s * g * (w_post * y * rsqrt(mean(y^2) + eps)),   x = w_pre * h' * rsqrt(mean(h'^2) + eps)
 // A token's y and h are read once, held in registers through both reductions, and h' and x are
-// written once: 12 to 16 bytes an element, memory-bound.
+// written once: 12 to 16 bytes an element, memory-bound.  Four warps a row up to H = 2048 (8192
+// tokens x 2048, bf16 y: 38.1 us, 5.3 TB/s; eight warps 39.7, two 41.2, one warp a row without
+// barriers 52: too few rows in flight), eight above, 8 columns a lane at a time.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv.h"
@@ -67,30 +69,27 @@ __device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kNormThreads = 128;
-
-// Sum over the W warps of a row (W = 1, or the whole block of 4)
+// Sum over the W warps of a row
 template <int W>
 __device__ __forceinline__ float row_sum(float v, float* red) {
     v = warp_sum(v);
-    if (W == 1) return v;
     __syncthreads();  // the last sum has been read
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) t += red[w];
+    return t;
 }
 
-// A row on W warps: lane i of warp w holds columns 8 (i + 32 (w + W j)) .. + 7, j < N.
+// A row on the W warps of a block: lane i of warp w holds columns 8 (i + 32 (w + W j)) .. + 7, j < N.
 template <typename TY, typename TX, int W, int N>
-__global__ void __launch_bounds__(kNormThreads) residual_norm_kernel(const NormArgs a) {
-    __shared__ float red[4];
+__global__ void __launch_bounds__(32 * W) residual_norm_kernel(const NormArgs a) {
+    __shared__ float red[W];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = W == 1 ? blockIdx.x * 4 + warp : blockIdx.x;
-    if (t >= a.T) return;  // (W = 1 only: no barrier follows)
+    const int t = blockIdx.x, c0 = 8 * threadIdx.x;
     const size_t row = static_cast<size_t>(t) * a.H;
-    const int c0 = 8 * (lane + (W == 1 ? 0 : 32 * warp));
     Eight<TY> yv[N];
     float h[N][8];
     // y and h of the whole row in flight at once
@@ -171,20 +170,12 @@ __global__ void __launch_bounds__(kNormThreads) residual_norm_kernel(const NormA
 }
 
 template <typename TY, typename TX>
-cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
-    // One warp a row where there are rows enough to fill the machine and a row fits its registers;
-    // else four (8192 tokens x 2048: see the file's head; 32 tokens: shorter rows a lane)
-    const dim3 block(kNormThreads);
-    if (a.H <= 2048 && a.T >= 8 * sms) {
-        const dim3 grid((a.T + 3) / 4);
-        if (a.H <= 512) return launch_pdl(residual_norm_kernel<TY, TX, 1, 2>, grid, block, 0, s, a);
-        if (a.H <= 1024) return launch_pdl(residual_norm_kernel<TY, TX, 1, 4>, grid, block, 0, s, a);
-        return launch_pdl(residual_norm_kernel<TY, TX, 1, 8>, grid, block, 0, s, a);
-    }
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     const dim3 grid(a.T);
-    if (a.H <= 2048) return launch_pdl(residual_norm_kernel<TY, TX, 4, 2>, grid, block, 0, s, a);
-    if (a.H <= 4096) return launch_pdl(residual_norm_kernel<TY, TX, 4, 4>, grid, block, 0, s, a);
-    return launch_pdl(residual_norm_kernel<TY, TX, 4, 8>, grid, block, 0, s, a);
+    if (a.H <= 1024) return launch_pdl(residual_norm_kernel<TY, TX, 4, 1>, grid, dim3(128), 0, s, a);
+    if (a.H <= 2048) return launch_pdl(residual_norm_kernel<TY, TX, 4, 2>, grid, dim3(128), 0, s, a);
+    if (a.H <= 4096) return launch_pdl(residual_norm_kernel<TY, TX, 8, 2>, grid, dim3(256), 0, s, a);
+    return launch_pdl(residual_norm_kernel<TY, TX, 8, 4>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -205,16 +196,15 @@ extern "C" int block_residual_norm(const moestep_dims* dims, int T, const void* 
         if (!kv_aligned16(p)) return MOESTEP_EALIGN;
     if (gate && gate_ld % 4) return MOESTEP_EALIGN;
     if (dims->H > 8192) return MOESTEP_EUNSUPPORTED;
-    int sms = 0;
-    if ((rc = device_ok(&sms)) != MOESTEP_OK) return rc;
+    if ((rc = device_ok(nullptr)) != MOESTEP_OK) return rc;
     NormArgs a{y, w_post, gate, gate_ld, res_scale, h_in, h_out, w_pre, x, eps, dims->H, dims->P, T};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_begin(8, s);
     cudaError_t e;
     if (dims->dtype == MOESTEP_F32)
-        e = y_dtype == MOESTEP_F32 ? launch_norm<float, float>(a, sms, s) : launch_norm<bf16, float>(a, sms, s);
+        e = y_dtype == MOESTEP_F32 ? launch_norm<float, float>(a, s) : launch_norm<bf16, float>(a, s);
     else
-        e = y_dtype == MOESTEP_F32 ? launch_norm<float, bf16>(a, sms, s) : launch_norm<bf16, bf16>(a, sms, s);
+        e = y_dtype == MOESTEP_F32 ? launch_norm<float, bf16>(a, s) : launch_norm<bf16, bf16>(a, s);
     prof_end(8, s);
     if (e != cudaSuccess) {
         set_last_cuda(static_cast<int>(e));

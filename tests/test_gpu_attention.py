@@ -258,3 +258,66 @@ def test_offsets_past_32_bits():
         ms.block_attention(kd, 1, q, n, c, outs[-1], ws, 0.09)
     torch.cuda.synchronize()
     assert ms.read_device_error(ws) == ms.OK and torch.equal(*outs) and torch.isfinite(outs[0].float()).all()
+
+
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.FP8])
+@pytest.mark.parametrize("shape", [([700, 40, 0], 1, 2, 4, 128, 32), ([900, 300], 32, 1, 8, 128, 64),
+                                   ([500], 16, 1, 4, 64, 16), ([400], 32, 1, 4, 64, 128)])
+def test_wait_timeout_is_reported_and_recovered(dtype, shape):
+    """A limit of zero makes the kernel's bounded waits give up; it drains what it issued, reports,
+    and the next call is right."""
+    s = Setup(dtype, *shape, seed=12)
+    good, _ = s.run()
+    torch.cuda.synchronize()
+    try:
+        ms.set_wait_timeout_ns(0)
+        s.run()
+        assert ms.read_device_error(s.ws) == ms.ETIMEOUT
+    finally:
+        ms.set_wait_timeout_ns(2_000_000_000)
+    out, ls = s.run()
+    assert torch.equal(out, good)
+    s.check(out, ls)
+
+
+@pytest.mark.parametrize("dtype", KIND)
+def test_nan_where_it_is_seen(dtype):
+    """NaN in a visible key or value reaches its own head's rows and no others; an infinite query
+    its own row."""
+    s = Setup(dtype, [300, 77], 2, 2, 2, 64, 16, seed=13)
+    good, _ = s.run()
+    tab = s.table.cpu().numpy()
+    for pool in s.pools:                                   # one of the two at a time
+        raw = pool.view(torch.uint8) if dtype == ms.FP8 else pool
+        at = (int(tab[0, 200 // 16]), 1, 200 % 16, 5)      # request 0, key-value head 1
+        old = raw[at].clone()
+        raw[at] = 0x7F if dtype == ms.FP8 else float("nan")
+        out, _ = s.run()
+        raw[at] = old
+        bad = torch.isnan(out.float()).any(-1).cpu().numpy()
+        assert bad[:2, 2:].all() and not bad[:2, :2].any() and not bad[2:].any()
+        assert torch.equal(out[2:], good[2:]) and torch.equal(out[:2, :2], good[:2, :2])
+    s.q[1, 3, 7] = float("inf")
+    out, _ = s.run()
+    bad = torch.isnan(out.float()).any(-1).cpu().numpy()
+    assert bad[1, 3] and bad.sum() == 1
+
+
+@pytest.mark.parametrize("exps", [(-90, -80), (100, 110), (-3, 20)])
+def test_fp8_scales_far_from_one(exps):
+    """Exponents below and above what one bf16 factor holds: keys and queries scaled so that the
+    scores stay moderate, values anywhere."""
+    s = Setup(ms.FP8, [400, 33], 3, 1, 2, 128, 32, seed=14)
+    g = np.random.default_rng(15)
+    ek, ev = s.cache._tensors[3], s.cache._tensors[4]
+    tab = s.table.cpu().numpy()
+    dv = g.integers(exps[0], exps[1] + 1, 2)
+    for r, L in enumerate(s.lengths):
+        for j in range(L):
+            i = (int(tab[r, j // 32]), 0, j % 32)
+            ev[i] = int(ev[i]) + int(dv[r])
+            ek[i] = int(ek[i]) + 20
+        s.v[r] = s.v[r].astype(np.float64) * 2.0 ** int(dv[r])
+        s.k[r] = s.k[r].astype(np.float64) * 2.0 ** 20
+    s.q = (s.q.float() * 2.0 ** -20).bfloat16()
+    s.check(*s.run())
