@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
     constexpr int CW = D / 32;             // output columns of a thread
     AttnWalk w = attn_begin<kKT>(a, plan);
     while (attn_next<kKT>(a, w)) {
-        const int h = w.seg / a.row_tiles, row0 = (w.seg - h * a.row_tiles) * kRT;
+        const int h = w.h, row0 = w.rt * kRT;
         const int nrows = min(kRT, a.rows - row0);
         __syncthreads();
         for (int i = tid; i < kRT * D; i += kSimpleThreads) {

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         auto sync8 = [&]() { tc::named_bar_sync(1, 256); };
         AttnWalk s = attn_begin<kKeys>(a, plan);
         while (attn_next<kKeys>(a, s)) {
-            const int h = s.seg / a.row_tiles, row0 = (s.seg - h * a.row_tiles) * C::kRows;
+            const int h = s.h, row0 = s.rt * C::kRows;
             const int nrows = min(C::kRows, a.rows - row0);
             {   // query rows into the swizzled operand tile(s), copies for lanes that repeat rows
                 constexpr int kChunks = D / 8, NT = C::kTwo ? 128 : 256, kBatch = 128 * kChunks / NT;
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const int page = 1 << a.page_log2, pages = kKeys >> a.page_log2;
         AttnWalk s = attn_begin<kKeys>(a, plan);
         while (wait.ok && attn_next<kKeys>(a, s)) {
-            const int h = s.seg / a.row_tiles, lo = attn_lo(a, s.L);
+            const int h = s.h, lo = attn_lo(a, s.L);
             const int32_t* tab = a.table + static_cast<long long>(s.r) * a.max_pages;
             // Page numbers come 32 at a time, a lane each, the next 32 while these are used: a
             // table read behind the copies in flight takes as long as they do.
@@ -823,32 +823,45 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     ex[i] = D == 128 && (i & 1) ? ex[i - 1] : se[row_of(i)];
                 }
                 uint8_t* dst = vring + b * C::kTile;
+                auto put = [&](int i, const uint32_t (&y)[4]) {
+                    const int row = row_of(i);
+                    const bool in = !partial || (row >= za && row < zb);
+                    *reinterpret_cast<uint4*>(dst + half_of(i) * 16384 + row * 128 + ((lc ^ (row & 7)) << 4)) =
+                        in ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(0, 0, 0, 0);
+                };
+                uint32_t odd = 0;  // bit 7 of a byte: a NaN code among them; bit 0: a factor beyond bf16
 #pragma unroll
                 for (int i = 0; i < 2 * kStepsC; ++i) {
-                    const uint32_t f1 = min(ex[i] + 120u, 254u);  // exponent field of the factor
-                    const uint32_t s1 = f1 * 0x00800080u;
-                    uint32_t y[4], nan = 0;
+                    const uint32_t s1 = min(ex[i] + 120u, 254u) * 0x00800080u;  // exponent field of the factor
+                    uint32_t y[4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const uint32_t w = k ? x[i].y : x[i].x;
                         y[2 * k] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), s1);
                         y[2 * k + 1] = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s1);
-                        nan |= (w & 0x7f7f7f7fu) + 0x01010101u;  // bit 7 of a NaN code's byte
+                        odd |= ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                     }
-                    if ((nan & 0x80808080u) | (ex[i] > 134u)) {
-                        const uint32_t f2 = ex[i] > 134u ? ex[i] - 134u + 127u : 127u;
+                    odd |= ex[i] > 134u;
+                    put(i, y);
+                }
+                if (odd) {  // again, with the patches
+#pragma unroll 1
+                    for (int i = 0; i < 2 * kStepsC; ++i) {
+                        const uint2 xi = *reinterpret_cast<const uint2*>(src + row_of(i) * D + half_of(i) * 64);
+                        const uint32_t e = se[row_of(i)];
+                        const uint32_t s1 = min(e + 120u, 254u) * 0x00800080u, s2 = (e > 134u ? e - 7u : 127u) * 0x00800080u;
+                        uint32_t y[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t w = (k < 2 ? x[i].x : x[i].y) >> (8 * (k & 1));
-                            y[k] = mul_bf16x2(y[k], f2 * 0x00800080u);
-                            if ((w & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
-                            if ((w & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
+                            const uint32_t w = k < 2 ? xi.x : xi.y, c = w >> (8 * (k & 1));
+                            const uint32_t t = k & 1 ? (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u)
+                                                     : ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
+                            y[k] = mul_bf16x2(mul_bf16x2(t, s1), s2);
+                            if ((c & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
+                            if ((c & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
                         }
+                        put(i, y);
                     }
-                    const int row = row_of(i);
-                    if (partial && (row < za || row >= zb)) y[0] = y[1] = y[2] = y[3] = 0;
-                    *reinterpret_cast<uint4*>(dst + half_of(i) * 16384 + row * 128 + ((lc ^ (row & 7)) << 4)) =
-                        make_uint4(y[0], y[1], y[2], y[3]);
                 }
                 }
                 tc::fence_proxy_async_smem();

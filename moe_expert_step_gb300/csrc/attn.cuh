@@ -173,9 +173,10 @@ __device__ __forceinline__ void attn_describe_join(const AttnArgs& a, const Attn
 
 // A CTA's walk over its segments.
 struct AttnWalk {
-    int r, left, k;         // request, units left, segments done
-    int L, t0, nt, seg;     // of the current segment: length, first key tile, key tiles, head * row tiles + row tile
-    int tile, tiles;        // its first key tile here and how many
+    int r, left, k;     // request, units left, segments done
+    int h, rt;          // head and row tile of the current segment
+    int L, t0, nt;      // its length, first key tile, key tiles
+    int tile, tiles;    // its first key tile here and how many
     bool whole;
 };
 template <int KT>
@@ -189,8 +190,10 @@ __device__ __forceinline__ AttnWalk attn_begin(const AttnArgs& a, const AttnPlan
         const int2 t = attn_tiles<KT>(a, w.L);
         w.t0 = t.x;
         w.nt = t.y;
-        w.seg = p.begin_o / t.y;
-        w.tile = t.x + (p.begin_o - w.seg * t.y);
+        const int seg = p.begin_o / t.y;
+        w.tile = t.x + (p.begin_o - seg * t.y);
+        w.h = seg / a.row_tiles;
+        w.rt = seg - w.h * a.row_tiles;
     }
     return w;
 }
@@ -198,19 +201,20 @@ template <int KT>
 __device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnWalk& w) {
     if (w.k >= 0) {
         w.left -= w.tiles;
-        ++w.seg;
-        if (w.left > 0 && w.seg == a.Hkv * a.row_tiles) {
-            w.seg = 0;
-            w.L = attn_len(a, ++w.r);
-            const int2 t = attn_tiles<KT>(a, w.L);
-            w.t0 = t.x;
-            w.nt = t.y;
+        if (++w.rt == a.row_tiles) {
+            w.rt = 0;
+            if (++w.h == a.Hkv && w.left > 0) {
+                w.h = 0;
+                w.L = attn_len(a, ++w.r);
+                const int2 t = attn_tiles<KT>(a, w.L);
+                w.t0 = t.x;
+                w.nt = t.y;
+            }
         }
         w.tile = w.t0;
     }
     if (w.left <= 0) return false;
-    const int rest = w.t0 + w.nt - w.tile;
-    w.tiles = min(rest, w.left);
+    w.tiles = min(w.t0 + w.nt - w.tile, w.left);
     w.whole = w.tiles == w.nt;
     ++w.k;
     return true;
