@@ -313,6 +313,13 @@ int row_tile(const moestep_kv_dims& d, int n_q) {
 }
 int max_ctas(const moestep_kv_dims& d) { return d.dtype == MOESTEP_F32 ? kAttnMaxCtas : kAttnMaxCtasTc; }
 
+// Empty units of a segment of 256 rows (see attn.cuh): beginning one takes 12 (bf16) to 17 us (FP8),
+// a key tile 2 to 2.7
+#ifndef AHEAD
+#define AHEAD 6
+#endif
+constexpr int kAhead = AHEAD;
+
 struct KvLayout {
     size_t joins, ml, o, total;
     int slot_rows;
@@ -341,7 +348,7 @@ int check_attn(const moestep_kv_dims* kd, int R, int n_q) {
     if (n_q > 1024 || R > (1 << 20)) return MOESTEP_EUNSUPPORTED;
     // units and rows are counted in 31 bits
     const long long row_tiles = (1ll * n_q * (kd->Hq / kd->Hkv) + kRT - 1) / kRT;
-    const long long tiles = (1ll * kd->max_pages * kd->page + kKT - 1) / kKT;
+    const long long tiles = (1ll * kd->max_pages * kd->page + kKT - 1) / kKT + kAhead;
     if (tiles * kd->Hkv > ((1ll << 31) - 1) / row_tiles / R) return MOESTEP_EUNSUPPORTED;
     if (1ll * R * n_q > ((1ll << 31) - 1) / kd->Hq) return MOESTEP_EUNSUPPORTED;
     return MOESTEP_OK;
@@ -404,6 +411,7 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     const bool f32 = kd->dtype == MOESTEP_F32, f8 = kd->dtype == MOESTEP_FP8;
     a.causal = causal != 0;
     a.even = !f32 && L.slot_rows == 256 ? 4 : 0;
+    a.ahead = f32 ? 0 : L.slot_rows == 256 ? kAhead : 4;
     // a window as long as the cache hides nothing (and stays out of 32-bit overflow)
     a.window = window >= kd->max_pages * kd->page ? 0 : window;
     a.scale_log2 = scale * 1.4426950408889634f;

@@ -8,7 +8,11 @@
 // CTA works the division out from kv_len itself (a block-wide scan over the requests; an
 // empty request counts one unit, whose only effect is to write its empty rows).
 //
-// The units of one (request, head, row tile) are a segment.  A segment inside one CTA is
+// The units of one (request, head, row tile) are a segment.  Beginning a segment inside a CTA costs
+// about as much as some units (the last one is written out, queries are staged, the pipeline fills
+// again), so each segment counts that many empty units (`ahead`) before its first key tile: CTAs in
+// which segments end and begin get fewer tiles.
+//  A segment inside one CTA is
 // written out directly; of one that CTAs share, each leaves its rows' (m, l, o) in a slot of
 // the workspace (a CTA has at most two such: the one it begins in and the one it ends in) and
 // the join launch adds them up in CTA order, so the result does not depend on timing.
@@ -46,6 +50,7 @@ struct AttnArgs {
     int page_log2, max_pages, n_pages;
     int causal, window;
     int even;          // largest share (units a CTA) that is divided evenly
+    int ahead;         // empty units of a segment
     float scale_log2;  // scale * log2(e): the kernels take exponentials to base 2
     unsigned long long timeout_ns;
 };
@@ -113,7 +118,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int* sm) {
     for (int r = r0; r < r1; ++r) {
         const int L = attn_len(a, r);
         if (blockIdx.x == 0 && L != __ldg(&a.kv_len[r])) record_error(a.err, kErrBadInput);
-        mine += attn_tiles<KT>(a, L).y * heads;
+        mine += (a.ahead + attn_tiles<KT>(a, L).y) * heads;
     }
     int incl = mine;  // block-wide inclusive scan
 #pragma unroll
@@ -139,7 +144,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int* sm) {
     if (p.count > 0 && p.first >= incl - mine && p.first < incl) {
         int at = incl - mine;
         for (int r = r0; r < r1; ++r) {
-            const int n = attn_tiles<KT>(a, attn_len(a, r)).y * heads;
+            const int n = (a.ahead + attn_tiles<KT>(a, attn_len(a, r)).y) * heads;
             if (p.first < at + n) {
                 sm[32] = r;
                 sm[33] = p.first - at;
@@ -160,12 +165,12 @@ __device__ __forceinline__ void attn_describe_join(const AttnArgs& a, const Attn
     int4 j = make_int4(-1, 0, 0, 0);
     const int c = blockIdx.x;
     if (p.count > 0) {
-        const int nt = attn_tiles<KT>(a, attn_len(a, p.begin_r)).y, seg = p.begin_o / nt, t = p.begin_o - seg * nt;
-        if (t > 0) {
+        const int n = a.ahead + attn_tiles<KT>(a, attn_len(a, p.begin_r)).y, seg = p.begin_o / n, o = p.begin_o - seg * n;
+        if (o > a.ahead) {
             const AttnShare sh(p.W, gridDim.x, a.even);
-            const int start = p.first - t, c0 = sh.owner(start);
+            const int start = p.first - o, c0 = sh.owner(start + a.ahead);  // who has the first key tile
             // the segment is the first one of CTA c0 (its slot 0) or not (slot 1)
-            if (c0 == c - 1) j = make_int4(p.begin_r, seg, 2 * c0 + (sh.first(c0) != start), sh.owner(start + nt - 1));
+            if (c0 == c - 1) j = make_int4(p.begin_r, seg, 2 * c0 + (sh.first(c0) < start), sh.owner(start + n - 1));
         }
     }
     a.joins[c] = j;
@@ -190,8 +195,9 @@ __device__ __forceinline__ AttnWalk attn_begin(const AttnArgs& a, const AttnPlan
         const int2 t = attn_tiles<KT>(a, w.L);
         w.t0 = t.x;
         w.nt = t.y;
-        const int seg = p.begin_o / t.y;
-        w.tile = t.x + (p.begin_o - seg * t.y);
+        const int seg = p.begin_o / (a.ahead + t.y), o = p.begin_o - seg * (a.ahead + t.y);
+        w.tile = t.x + max(o - a.ahead, 0);
+        w.left -= min(max(a.ahead - o, 0), w.left);
         w.h = seg / a.row_tiles;
         w.rt = seg - w.h * a.row_tiles;
     }
@@ -200,7 +206,7 @@ __device__ __forceinline__ AttnWalk attn_begin(const AttnArgs& a, const AttnPlan
 template <int KT>
 __device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnWalk& w) {
     if (w.k >= 0) {
-        w.left -= w.tiles;
+        w.left -= w.tiles + a.ahead;
         if (++w.rt == a.row_tiles) {
             w.rt = 0;
             if (++w.h == a.Hkv && w.left > 0) {
