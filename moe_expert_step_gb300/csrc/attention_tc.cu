@@ -62,8 +62,8 @@ struct Cfg {
     static constexpr int kFront = kTwo ? 2 * kQ : 32768;
     static constexpr int kMul = 128 / D;
     static constexpr int kNK = 3 * kMul;                                     // key tiles
-    static constexpr int kNV = (kTwo ? 2 : 3) * kMul;                        // value tiles
-    static constexpr int kNR = F8 ? 2 * kMul : 0;                            // FP8 value tiles
+    static constexpr int kNV = (kTwo || F8 ? 2 : 3) * kMul;                        // value tiles
+    static constexpr int kNR = F8 ? (kTwo ? 2 : 4) * kMul : 0;                            // FP8 value tiles
     static constexpr int kNS = F8 ? kNK + 2 : 0;  // key tiles' scales: a turn's are read while the tiles two ahead land
     static constexpr int kMisc = 1024 + (F8 ? 1024 + (kNK + kNR) * kKeys + kNS * kKeys * 4 : 0);
     static constexpr int kSmem = 1024 + kFront + kNK * kKTile + kNV * kTile + kNR * kRaw + kMisc;
