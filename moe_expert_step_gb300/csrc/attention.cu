@@ -15,16 +15,16 @@ namespace {
 // Tiles of 16 query rows and 64 keys, 128 threads.  Each thread computes a 2 x 4 block of the
 // tile's scores, the 16 rows' statistics are kept by 8 lanes each, and each thread accumulates
 // 4 rows x (D / 32) columns of the output.
-constexpr int kRT = 16, kKT = 64, kSimpleThreads = 128;
+constexpr int kRT = 16, kKT = 64, kF32Threads = 128;
 template <int D>
-constexpr int simple_smem() {
+constexpr int f32_smem() {
     return (kRT * D + 2 * kKT * (D + 4) + kRT * (kKT + 4) + 3 * kRT) * 4;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kF32Threads) attn_f32_kernel(const AttnArgs a) {
     extern __shared__ float smf[];
-    __shared__ int plan_sm[40];
+    __shared__ int plan_sm[40], s_row[kKT];
     float* sq = smf;                       // [16][D]
     float* sk = sq + kRT * D;              // [64][D + 4]
     float* sv = sk + kKT * (D + 4);        // [64][D + 4]
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x;
-    const AttnPlan plan = attn_plan<kKT, kSimpleThreads>(a, plan_sm);
+    const AttnPlan plan = attn_plan<kKT, kF32Threads>(a, plan_sm);
     if (tid == 0) attn_describe_join<kKT>(a, plan);
     constexpr int CW = D / 32;             // output columns of a thread
     AttnWalk w = attn_begin<kKT>(a, plan);
@@ -43,15 +43,17 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
         const int h = w.h, row0 = w.rt * kRT;
         const int nrows = min(kRT, a.rows - row0);
         __syncthreads();
-        for (int i = tid; i < kRT * D; i += kSimpleThreads) {
-            const int rr = i / D, d = i - rr * D, row = row0 + rr;
-            float x = 0.f;
+#pragma unroll 4
+        for (int i = tid; i < kRT * (D / 4); i += kF32Threads) {
+            const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4)), row = row0 + rr;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (rr < nrows) {
                 const int qi = attn_query(a, row), g = row - qi * a.G;
-                x = static_cast<const float*>(a.q)[(static_cast<long long>(w.r) * a.n_q + qi) * a.q_ld +
-                                                   (h * a.G + g) * D + d];
+                x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                                          (static_cast<long long>(w.r) * a.n_q + qi) * a.q_ld +
+                                                          (h * a.G + g) * D + d));
             }
-            sq[i] = x;
+            *reinterpret_cast<float4*>(sq + rr * D + d) = x;
         }
         if (tid < kRT) {
             s_m[tid] = -INFINITY;
@@ -62,23 +64,39 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_f32_kernel(const AttnArgs
         const int lo = attn_lo(a, w.L);
         for (int t = w.tile; t < w.tile + w.tiles; ++t) {
             const int j0 = t * kKT;
-            __syncthreads();
-            for (int i = tid; i < kKT * (D / 4); i += kSimpleThreads) {
-                const int key = i / (D / 4), d = 4 * (i - key * (D / 4)), j = j0 + key;
-                float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+            if (tid < kKT) {  // each key's row in the pool, -1: not to be read
+                const int j = j0 + tid;
+                int row = -1;
                 if (j >= lo && j < w.L) {
                     const int id = __ldg(&a.table[static_cast<long long>(w.r) * a.max_pages + (j >> a.page_log2)]);
-                    if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_pages)) {
+                    if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages))
+                        row = ((id * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+                    else
                         record_error(a.err, kErrBadInput);
-                    } else {
-                        const long long row = ((static_cast<long long>(id) * a.Hkv + h) << a.page_log2) +
-                                              (j & ((1 << a.page_log2) - 1));
-                        kx = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + row * D + d);
-                        vx = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + row * D + d);
+                }
+                s_row[tid] = row;
+            }
+            __syncthreads();
+            constexpr int kPiece = D / 4, kBatch = 8;  // pieces of a row; loads of a thread in flight, twice
+#pragma unroll 1
+            for (int i0 = 0; i0 < kKT * kPiece; i0 += kBatch * kF32Threads) {
+                float4 kx[kBatch], vx[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = i0 + u * kF32Threads + tid, key = i / kPiece, row = s_row[key];
+                    kx[u] = vx[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (row >= 0) {
+                        const long long at = static_cast<long long>(row) * D + 4 * (i - key * kPiece);
+                        kx[u] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + at));
+                        vx[u] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + at));
                     }
                 }
-                *reinterpret_cast<float4*>(sk + key * (D + 4) + d) = kx;
-                *reinterpret_cast<float4*>(sv + key * (D + 4) + d) = vx;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = i0 + u * kF32Threads + tid, key = i / kPiece, d = 4 * (i - key * kPiece);
+                    *reinterpret_cast<float4*>(sk + key * (D + 4) + d) = kx[u];
+                    *reinterpret_cast<float4*>(sv + key * (D + 4) + d) = vx[u];
+                }
             }
             __syncthreads();
             {   // scores: rows 2 sr, 2 sr + 1; keys sc + 16 j
@@ -291,15 +309,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
 template <int D>
 cudaError_t launch_f32(const AttnArgs& a, int grid, cudaStream_t s) {
     static int done[64] = {};
-    cudaError_t e = ensure_smem(attn_f32_kernel<D>, simple_smem<D>(), done);
+    cudaError_t e = ensure_smem(attn_f32_kernel<D>, f32_smem<D>(), done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_f32_kernel<D>, dim3(grid), dim3(kSimpleThreads), simple_smem<D>(), s, a);
+    return launch_pdl(attn_f32_kernel<D>, dim3(grid), dim3(kF32Threads), f32_smem<D>(), s, a);
 }
 
 template <typename T, int D>
 cudaError_t launch_join(const AttnArgs& a, int ctas, int sms, cudaStream_t s) {
-    // (measured: 8 blocks an SM, as many as there are warps for; 4 a little slower, 2 by 5 us where 256 rows are joined)
-    const long long work = 1ll * ctas * (a.slot_rows < a.rows ? a.slot_rows : a.rows);
+    // A block can take one row on its eight warps; no more are shared than there are segments, or
+    // boundaries between CTAs.  (At most 8 blocks an SM, as many as its warps: 4 are a little slower, 2 by
+    // 5 us where 256 rows are joined.)
+    const long long segments = 1ll * a.R * a.Hkv * a.row_tiles;
+    const long long work = (segments < ctas ? segments : ctas) * (a.slot_rows < a.rows ? a.slot_rows : a.rows);
     const int grid = work < 8ll * sms ? static_cast<int>(work) : 8 * sms;
     return launch_pdl(attn_join_kernel<T, D>, dim3(grid), dim3(kJoinThreads), 0, s, a, ctas);
 }
