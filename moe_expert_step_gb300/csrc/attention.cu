@@ -206,7 +206,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, int ctas) {
     __shared__ int4 s_list[kAttnMaxCtas];  // the joins that there are
     __shared__ int s_cnt[8];
-    __shared__ float s_f[8][kAttnMaxCtas];
+    __shared__ float s_f[8][(kAttnMaxCtas + 31) / 32 * 32];
     __shared__ float s_o[8][D];
     constexpr int W = D / 32, kBatch = 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -257,15 +257,24 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
         float x[kBatch][W];  // the first parts are on their way while the statistics are joined
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) load(part + u * wpr, x[u]);
+        constexpr int kStats = (kAttnMaxCtas + 31) / 32;
+        float2 ml[kStats];
         float m = -INFINITY, l = 0.f;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(&a.part_ml[slot(i)]).x);
+#pragma unroll
+        for (int u = 0; u < kStats; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.f);
+            if (lane + 32 * u < n) ml[u] = __ldcg(&a.part_ml[slot(lane + 32 * u)]);
+        }
+#pragma unroll
+        for (int u = 0; u < kStats; ++u) m = fmaxf(m, ml[u].x);
         m = warp_max(m);
         const float ms = m == -INFINITY ? 0.f : m;
-        for (int i = lane; i < n; i += 32) {
-            const float2 ml = __ldcg(&a.part_ml[slot(i)]);
-            const float f = exp2f(ml.x - ms);
-            l += ml.y * f;
-            s_f[warp][i] = f;
+#pragma unroll
+        for (int u = 0; u < kStats; ++u) {
+            if (32 * u >= n) break;
+            const float f = exp2f(ml[u].x - ms);
+            l += ml[u].y * f;
+            s_f[warp][lane + 32 * u] = f;
         }
         l = warp_sum(l);
         __syncwarp();
