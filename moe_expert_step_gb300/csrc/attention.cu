@@ -14,7 +14,9 @@ namespace {
 // ---------------------------------------------------------------------------- CUDA cores
 // Tiles of 16 query rows and 64 keys, 128 threads.  Each thread computes a 2 x 4 block of the
 // tile's scores, the 16 rows' statistics are kept by 8 lanes each, and each thread accumulates
-// 4 rows x (D / 32) columns of the output.
+// 4 rows x (D / 32) columns of the output.  A tile's loads are in flight together, eight pieces a
+// thread of keys and of values.  3 requests of 7 tokens, window 500, 8 heads of 64 over 4: 14 us,
+// the latency of a tile, of starting up and of the join (0.5 us of bytes).
 constexpr int kRT = 16, kKT = 64, kF32Threads = 128;
 template <int D>
 constexpr int f32_smem() {
@@ -326,8 +328,8 @@ cudaError_t launch_f32(const AttnArgs& a, int grid, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t launch_join(const AttnArgs& a, int ctas, int sms, cudaStream_t s) {
     // A block can take one row on its eight warps; no more are shared than there are segments, or
-    // boundaries between CTAs.  (At most 8 blocks an SM, as many as its warps: 4 are a little slower, 2 by
-    // 5 us where 256 rows are joined.)
+    // boundaries between CTAs.  (At most 8 blocks an SM, as many as its warps allow: 4 are a little
+    // slower, 2 by 5 us where 256 rows are joined.)
     const long long segments = 1ll * a.R * a.Hkv * a.row_tiles;
     const long long work = (segments < ctas ? segments : ctas) * (a.slot_rows < a.rows ? a.slot_rows : a.rows);
     const int grid = work < 8ll * sms ? static_cast<int>(work) : 8 * sms;
@@ -343,12 +345,10 @@ int row_tile(const moestep_kv_dims& d, int n_q) {
 }
 int max_ctas(const moestep_kv_dims& d) { return d.dtype == MOESTEP_F32 ? kAttnMaxCtas : kAttnMaxCtasTc; }
 
-// Empty units of a segment of 256 rows (see attn.cuh): beginning one takes 12 (bf16) to 17 us (FP8),
-// a key tile 2 to 2.7
-#ifndef AHEAD
-#define AHEAD 6
-#endif
-constexpr int kAhead = AHEAD;
+// Empty units of a segment (see attn.cuh) of 256 rows and of fewer.  Beginning one inside a CTA takes
+// 12 (bf16) to 17 us (FP8) with 256 rows, a key tile 2 to 2.7.  Against no empty units: 16 blocks of
+// 32 tokens, up to 32768 FP8 positions, 156 -> 131 us, 16 ragged single tokens 33 -> 26 us.
+constexpr int kAhead = 6, kAheadFew = 4;
 
 struct KvLayout {
     size_t joins, ml, o, total;
@@ -441,7 +441,7 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     const bool f32 = kd->dtype == MOESTEP_F32, f8 = kd->dtype == MOESTEP_FP8;
     a.causal = causal != 0;
     a.even = !f32 && L.slot_rows == 256 ? 4 : 0;
-    a.ahead = f32 ? 0 : L.slot_rows == 256 ? kAhead : 4;
+    a.ahead = f32 ? 0 : L.slot_rows == 256 ? kAhead : kAheadFew;
     // a window as long as the cache hides nothing (and stays out of 32-bit overflow)
     a.window = window >= kd->max_pages * kd->page ? 0 : window;
     a.scale_log2 = scale * 1.4426950408889634f;

@@ -6,10 +6,13 @@
 // the MMA's M = 128: S = Q K^T into tensor memory, P = 2^(S c - m) written back over S as
 // bf16, O += P V with P read from tensor memory.
 //
-// Two streams run through each CTA, each with a softmax warpgroup, its S / P (128 columns) and its O
-// (D columns), so that one stream's MMAs run under the other's exponentials:
+// Two streams run through each CTA, each with a softmax warpgroup, its S / P (128 columns) and
+// its O (D columns), so that one stream's MMAs run under the other's exponentials:
 //   more than 128 rows: the streams are two row tiles of 128 on the same keys;
 //   else:               they take alternate key tiles of the same rows, each with its own (m, l, O).
+// Where a lane has a whole row of the tile (65 rows and more) the tile passes in two halves of 64
+// keys: the scores of the next tile's half are issued as soon as this half's weights have been
+// multiplied, so a stream's MMAs also run under its own exponentials.
 // Few rows would leave most of the 128 lanes idle and one lane with 128 exponentials a tile, so
 // 32 (64) rows are held four (two) times, and warp w of a warpgroup computes only its quarter
 // (half) of the tile's keys, the rest of its lanes' P being zero: each such copy is one more
@@ -19,11 +22,27 @@
 // than 8 (a factor 256, harmless in fp32 sums and bf16 weights): O is then rescaled in tensor
 // memory by the softmax warps, which is rare after the first tiles.
 //
-// Warps: 0-7 softmax (two warpgroups), 8 and 11 TMA producers (keys, values), 9-10 MMA
-// issuers (a stream each), and with FP8 12-19 converters (E4M3 code * 2^exp -> bf16, exact, into the swizzled operand buffers).
+// FP8 cache.  Keys are multiplied as they are stored: a query row is scaled by a power of two and
+// split into two E4M3 parts (4 significant bits each, the 8 of a bf16: see the staging), S is the
+// sum of both parts' products, and the keys' powers of two come in with the softmax's scale.
+// That halves the keys' way through shared memory and needs no conversion of them.  Weights have
+// no such split, so values are turned into bf16 (code * 2^exp, exact) by eight converter warps.
+//
+// Warps: 0-7 softmax (two warpgroups), 8 and 11 TMA producers (keys, values), 9-10 MMA issuers (a
+// stream each), with FP8 12-19 converters.
 // Keys outside [lo, L) of the request reach no result: their scores are replaced by -inf, and
 // their V rows, which a zero weight would still multiply (NaN), are zeroed in shared memory.
 // Every wait is bounded (timeout -> error word, orderly teardown).
+//
+// What bounds it, measured with the join launch (16 query heads of 128 over 2, cold caches; in
+// brackets the copy rate's time for the keys and values): single tokens of 16 ragged requests, up
+// to 8192 positions, 26 us (12.1): starting up 4 us, the beginnings of two segments, eight tiles
+// and the join; tensor pipe 21 % busy.  One token at 131072 FP8 positions 38 us (10.0): 13 tiles
+// of 3000 cycles, issue slots 54 %.  32 tokens at 16384 positions 25 us (2.5): one beginning, two
+// tiles, 128 KB of parts a CTA and their join.  16 such blocks, up to 32768 FP8 positions, 131 us
+// (24.9; 43.6 by operations at the bf16 rate): 34 tiles of two row tiles, 4500 to 5000 cycles
+// each, issue slots 60 %, tensor pipe 32 %: exponentials, conversions and staging share the issue
+// slots.
 #include "attn.cuh"
 #include "attn_tc.cuh"
 #include "common.cuh"
@@ -70,8 +89,6 @@ struct Cfg {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// The FP8 converters leave every four columns of the values in the order 0, 2, 1, 3 (see there):
-// the output's columns are put back.
 // 2^(exp - 127) of an exponent byte
 __device__ __forceinline__ float exp_scale(uint32_t e) {
     return e > 0 ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);
@@ -81,6 +98,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// 32 columns of the output.  The FP8 converters leave every four columns of the values in the order
+// 0, 2, 1, 3 (see there): they are put back.
 template <bool F8>
 __device__ __forceinline__ void load_output(uint32_t taddr, float* x) {
     tc::tmem_ld32(taddr, x);
@@ -272,51 +291,52 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
 #pragma unroll
                     for (int b = 0; b + 4 < kBatch; ++b) x[b] = x[b + 4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int m = mb + u * kStep;
-                    const uint4 piece16 = y[u];
-                    if (!F8) {
-                        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = piece16;
-                        continue;
-                    }
-                    // A row times a power of two that brings it to at most 448, as the sum of two E4M3
-                    // parts: the first takes the leading 4 bits of a bf16's 8, the second the rest,
-                    // exactly but for elements 2000 times below the row's largest (error
-                    // below 2^-19 of that).  An infinite row gives NaN scores.
-                    const uint32_t w[4] = {piece16.x, piece16.y, piece16.z, piece16.w};
-                    float amax = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-#pragma unroll
-                    for (int o = kChunks / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    const uint32_t bits = __float_as_uint(amax);
-                    int e = static_cast<int>(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u);  // 448 = 0.875 * 2^9
-                    e = min(max(e, -100), 119);
-                    const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    if (c == 0)
-                        qscale[(C::kTwo ? g * 128 : 0) + m] = bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                                                                  : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                    uint32_t hi[2], lo[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t p[2], q[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float y0 = __uint_as_float(w[2 * i + j] << 16) * s, y1 = __uint_as_float(w[2 * i + j] & 0xffff0000u) * s;
-                            p[j] = tc::to_e4m3x2(y0, y1);
-                            const uint32_t h2 = tc::e4m3x2_to_f16x2(p[j], 0);
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                            q[j] = tc::to_e4m3x2(y0 - f.x, y1 - f.y);
+                    for (int u = 0; u < 4; ++u) {
+                        const int m = mb + u * kStep;
+                        const uint4 piece16 = y[u];
+                        if (!F8) {
+                            *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = piece16;
+                            continue;
                         }
-                        hi[i] = p[0] | p[1] << 16;
-                        lo[i] = q[0] | q[1] << 16;
+                        // A row times a power of two that brings it to at most 448, as the sum of two E4M3
+                        // parts: the first takes the leading 4 bits of a bf16's 8, the second the rest.
+                        // Exact for elements of 1/4 and more; below that the second's smallest step,
+                        // 2^-9, leaves an error of at most 2^-10, against a largest element above
+                        // 224: 2^-17 of it.  An infinite row gives NaN scores.
+                        const uint32_t w[4] = {piece16.x, piece16.y, piece16.z, piece16.w};
+                        float amax = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+#pragma unroll
+                        for (int o = kChunks / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        const uint32_t bits = __float_as_uint(amax);
+                        int e = static_cast<int>(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u);  // 448 = 0.875 * 2^9
+                        e = min(max(e, -100), 119);
+                        const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        if (c == 0)
+                            qscale[(C::kTwo ? g * 128 : 0) + m] = bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                                                                      : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t p[2], q[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float y0 = __uint_as_float(w[2 * i + j] << 16) * s, y1 = __uint_as_float(w[2 * i + j] & 0xffff0000u) * s;
+                                p[j] = tc::to_e4m3x2(y0, y1);
+                                const uint32_t h2 = tc::e4m3x2_to_f16x2(p[j], 0);
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                                q[j] = tc::to_e4m3x2(y0 - f.x, y1 - f.y);
+                            }
+                            hi[i] = p[0] | p[1] << 16;
+                            lo[i] = q[0] | q[1] << 16;
+                        }
+                        const int piece = D == 128 ? (c >> 1) ^ (m & 7) : (c >> 1) ^ ((m >> 1) & 3);  // TMA's swizzles
+                        uint8_t* d = dst + m * D + (piece << 4) + (c & 1) * 8;
+                        *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2*>(d + 128 * D) = make_uint2(lo[0], lo[1]);
                     }
-                    const int piece = D == 128 ? (c >> 1) ^ (m & 7) : (c >> 1) ^ ((m >> 1) & 3);  // TMA's swizzles
-                    uint8_t* d = dst + m * D + (piece << 4) + (c & 1) * 8;
-                    *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2*>(d + 128 * D) = make_uint2(lo[0], lo[1]);
-                }
                 }
                 tc::fence_proxy_async_smem();
                 tc::fence_before_sync();
@@ -334,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             kt0 += s.tiles;
             for (int t = first; t < s.tile + s.tiles; t += step, ++tiles_g, kt += step)
 #pragma unroll 1
-            for (int half = 0; half < C::kHalves; ++half, ++turn) {
+            for (int half = 0; half < C::kHalves; ++half, ++turn) {  // (both loops' body)
                 wait(&s_full[g * 2 + half], tiles_g & 1);
                 tc::fence_after_sync();
                 if (F8 && turn == 0) scl = a.scale_log2 * qscale[C::kTwo ? lrow : w * 32 + lane];
@@ -811,58 +831,58 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 const bool partial = za > 0 || zb < kKeys;
 #pragma unroll 1
                 for (int base = cw * 16; base < kKeys; base += (F8 ? C::kConv : 1) * 16) {
-                uint2 x[2 * kStepsC];
-                uint32_t ex[2 * kStepsC];
-                auto row_of = [&](int i) { return base + (i >> 1) * kStepRows + lr + (D == 128 ? 0 : 4 * (i & 1)); };
-                auto half_of = [&](int i) { return D == 128 ? (i ^ lr) & 1 : 0; };
-                const uint8_t* src = raw + rb * C::kRaw + lc * 8;
-                const uint8_t* se = exps + rb * kKeys;
+                    uint2 x[2 * kStepsC];
+                    uint32_t ex[2 * kStepsC];
+                    auto row_of = [&](int i) { return base + (i >> 1) * kStepRows + lr + (D == 128 ? 0 : 4 * (i & 1)); };
+                    auto half_of = [&](int i) { return D == 128 ? (i ^ lr) & 1 : 0; };
+                    const uint8_t* src = raw + rb * C::kRaw + lc * 8;
+                    const uint8_t* se = exps + rb * kKeys;
 #pragma unroll
-                for (int i = 0; i < 2 * kStepsC; ++i) {
-                    x[i] = *reinterpret_cast<const uint2*>(src + row_of(i) * D + half_of(i) * 64);
-                    ex[i] = D == 128 && (i & 1) ? ex[i - 1] : se[row_of(i)];
-                }
-                uint8_t* dst = vring + b * C::kTile;
-                auto put = [&](int i, const uint32_t (&y)[4]) {
-                    const int row = row_of(i);
-                    const bool in = !partial || (row >= za && row < zb);
-                    *reinterpret_cast<uint4*>(dst + half_of(i) * 16384 + row * 128 + ((lc ^ (row & 7)) << 4)) =
-                        in ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(0, 0, 0, 0);
-                };
-                uint32_t odd = 0;  // bit 7 of a byte: a NaN code among them; bit 0: a factor beyond bf16
-#pragma unroll
-                for (int i = 0; i < 2 * kStepsC; ++i) {
-                    const uint32_t s1 = min(ex[i] + 120u, 254u) * 0x00800080u;  // exponent field of the factor
-                    uint32_t y[4];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t w = k ? x[i].y : x[i].x;
-                        y[2 * k] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), s1);
-                        y[2 * k + 1] = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s1);
-                        odd |= ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                    }
-                    odd |= ex[i] > 134u;
-                    put(i, y);
-                }
-                if (odd) {  // again, with the patches
-#pragma unroll 1
                     for (int i = 0; i < 2 * kStepsC; ++i) {
-                        const uint2 xi = *reinterpret_cast<const uint2*>(src + row_of(i) * D + half_of(i) * 64);
-                        const uint32_t e = se[row_of(i)];
-                        const uint32_t s1 = min(e + 120u, 254u) * 0x00800080u, s2 = (e > 134u ? e - 7u : 127u) * 0x00800080u;
+                        x[i] = *reinterpret_cast<const uint2*>(src + row_of(i) * D + half_of(i) * 64);
+                        ex[i] = D == 128 && (i & 1) ? ex[i - 1] : se[row_of(i)];
+                    }
+                    uint8_t* dst = vring + b * C::kTile;
+                    auto put = [&](int i, const uint32_t (&y)[4]) {
+                        const int row = row_of(i);
+                        const bool in = !partial || (row >= za && row < zb);
+                        *reinterpret_cast<uint4*>(dst + half_of(i) * 16384 + row * 128 + ((lc ^ (row & 7)) << 4)) =
+                            in ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(0, 0, 0, 0);
+                    };
+                    uint32_t odd = 0;  // bit 7 of a byte: a NaN code among them; bit 0: a factor beyond bf16
+#pragma unroll
+                    for (int i = 0; i < 2 * kStepsC; ++i) {
+                        const uint32_t s1 = min(ex[i] + 120u, 254u) * 0x00800080u;  // exponent field of the factor
                         uint32_t y[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t w = k < 2 ? xi.x : xi.y, c = w >> (8 * (k & 1));
-                            const uint32_t t = k & 1 ? (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u)
-                                                     : ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
-                            y[k] = mul_bf16x2(mul_bf16x2(t, s1), s2);
-                            if ((c & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
-                            if ((c & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t w = k ? x[i].y : x[i].x;
+                            y[2 * k] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u), s1);
+                            y[2 * k + 1] = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s1);
+                            odd |= ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                         }
+                        odd |= ex[i] > 134u;
                         put(i, y);
                     }
-                }
+                    if (odd) {  // again, with the patches
+#pragma unroll 1
+                        for (int i = 0; i < 2 * kStepsC; ++i) {
+                            const uint2 xi = *reinterpret_cast<const uint2*>(src + row_of(i) * D + half_of(i) * 64);
+                            const uint32_t e = se[row_of(i)];
+                            const uint32_t s1 = min(e + 120u, 254u) * 0x00800080u, s2 = (e > 134u ? e - 7u : 127u) * 0x00800080u;
+                            uint32_t y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t w = k < 2 ? xi.x : xi.y, c = w >> (8 * (k & 1));
+                                const uint32_t t = k & 1 ? (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u)
+                                                         : ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
+                                y[k] = mul_bf16x2(mul_bf16x2(t, s1), s2);
+                                if ((c & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
+                                if ((c & 0x7f0000u) == 0x7f0000u) y[k] |= 0x7fff0000u;
+                            }
+                            put(i, y);
+                        }
+                    }
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();

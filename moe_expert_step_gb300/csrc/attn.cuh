@@ -2,20 +2,21 @@
 // the rows a query sees.
 //
 // The work is a list of units: one tile of keys for one tile of query rows of one
-// (request, key-value head).  Units are numbered request by request, then head, then row tile, then key
-// tile, and every CTA takes the same number of them in a row (one more or less): it streams as
-// many key tiles as any other whatever the requests' lengths are.  The lengths are on the device, so every
-// CTA works the division out from kv_len itself (a block-wide scan over the requests; an
-// empty request counts one unit, whose only effect is to write its empty rows).
+// (request, key-value head).  Units are numbered request by request, then head, then row tile,
+// then key tile, and every CTA takes the same number of them in a row (one more or less): it
+// streams as many key tiles as any other whatever the requests' lengths are.  The lengths are on
+// the device, so every CTA works the division out from kv_len itself (a block-wide scan over the
+// requests; an empty request counts one unit, whose only effect is to write its empty rows).
 //
 // The units of one (request, head, row tile) are a segment.  Beginning a segment inside a CTA costs
 // about as much as some units (the last one is written out, queries are staged, the pipeline fills
 // again), so each segment counts that many empty units (`ahead`) before its first key tile: CTAs in
 // which segments end and begin get fewer tiles.
-//  A segment inside one CTA is
-// written out directly; of one that CTAs share, each leaves its rows' (m, l, o) in a slot of
-// the workspace (a CTA has at most two such: the one it begins in and the one it ends in) and
-// the join launch adds them up in CTA order, so the result does not depend on timing.
+//
+// A segment inside one CTA is written out directly; of one that CTAs share, each leaves its rows'
+// (m, l, o) in a slot of the workspace (a CTA has at most two such: the one it begins in and the
+// one it ends in) and the join launch adds them up in CTA order, so the result does not depend on
+// timing.
 #pragma once
 #include <cuda.h>
 
@@ -44,7 +45,7 @@ struct AttnArgs {
     int* err;
     int R, n_q, Hq, Hkv, G;
     uint32_t g_magic;  // ceil(2^32 / G); 0 for G = 1
-    int rows;        // n_q * G: query rows of one (request, key-value head)
+    int rows;          // n_q * G: query rows of one (request, key-value head)
     int row_tiles;
     int slot_rows;
     int page_log2, max_pages, n_pages;
@@ -66,7 +67,7 @@ __device__ __forceinline__ int attn_query(const AttnArgs& a, int row) {
     return a.g_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.g_magic)) : row;
 }
 
-// Positions [lo, hi) that some query of the request sees
+// First position that some query of the request sees (the last is L - 1)
 __device__ __forceinline__ int attn_lo(const AttnArgs& a, int L) {
     return a.window > 0 ? max(0, L - a.n_q - a.window + 1) : 0;
 }
