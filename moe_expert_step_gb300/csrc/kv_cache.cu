@@ -28,18 +28,22 @@ struct CopyArgs {
     uint8_t* ve;
     const int32_t* table;
     int n, Hkv, page_log2, n_pages, max_pages;
-    long long vectors;  // tokens * 2 * Hkv
+    uint32_t per_magic, n_magic;  // ceil(2^32 / divisor) of 2 * Hkv and, where n is in [2, 65000], of n
+    long long vectors;            // tokens * 2 * Hkv
     int* err;
 };
 
 // A thread handles 16 consecutive elements of kPer vectors; D / 16 lanes share a vector, and
 // consecutive vectors are a token's key heads, then its value heads, so a warp reads and
 // writes whole lines.  A block takes 2 * 256 / (D / 16) vectors: their tokens and requests are
-// found with 32-bit divisions, a wide one only in a launch of more than 2^32 vectors.
+// found with 32-bit divisions (a wide one only in a launch of more than 2^32 vectors) and from
+// there on with multiplications by reciprocals: j < 2048 + 64, tl < n + 33, so both are exact.
 // Both kernels are copies, bound by memory: 32768 tokens of 8 heads of 128 (134 MB of bf16 on
-// one side, 69 MB of codes on the other) are written in 37.4 us and read back in 38.5 us, 5.4
-// and 5.2 TB/s.  Four vectors a thread take 40.1 / 39.6 us (fewer blocks, a longer tail), one
-// takes 37.9 / 40.8 us and a read of 512 tokens 6.6 us against 6.0 us (too few loads in flight).
+// one side, 69 MB of codes on the other) are written in 35.0 us and read back in 36.3 us, 5.8
+// and 5.6 TB/s.  Four vectors a thread take 3 and 1 us longer (fewer blocks, a longer tail), one
+// 0.5 and 2 us and a read of 777 tokens 6.6 us against 6.0 us (too few loads in flight).  Six
+// resident blocks for the write (40 registers) against five 35.0 : 36.0 us, eight for the read
+// (32 registers) against six 36.3 : 40.2 us.
 constexpr int kPer = 2;
 
 struct Vector {
@@ -58,7 +62,8 @@ template <int L>
 __device__ __forceinline__ Vector vector_of(const CopyArgs& a, unsigned t0, unsigned rem, unsigned r0, unsigned tl0, int q,
                                             long long first) {
     const unsigned local = q * (256 / L) + threadIdx.x / L, per = 2 * a.Hkv;
-    const unsigned j = rem + local, dt = j / per, w = j - dt * per, tl = tl0 + dt, dr = tl / a.n;
+    const unsigned j = rem + local, dt = __umulhi(j, a.per_magic), w = j - dt * per, tl = tl0 + dt;
+    const unsigned dr = a.n_magic ? __umulhi(tl, a.n_magic) : a.n == 1 ? tl : tl >= static_cast<unsigned>(a.n);
     Vector x;
     x.t = static_cast<long long>(t0) + dt;
     x.r = static_cast<int>(r0 + dr);
@@ -111,7 +116,7 @@ struct Sixteen {
 };
 
 template <int DT, int D>
-__global__ void __launch_bounds__(256) kv_write_kernel(const CopyArgs a) {
+__global__ void __launch_bounds__(256, DT == MOESTEP_F32 ? 4 : 6) kv_write_kernel(const CopyArgs a) {
     pdl_trigger();
     pdl_wait();
     using T = typename std::conditional<DT == MOESTEP_F32, float, bf16>::type;
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const CopyArgs a) {
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(256) kv_read_kernel(const CopyArgs a) {
+__global__ void __launch_bounds__(256, DT == MOESTEP_F32 ? 4 : 8) kv_read_kernel(const CopyArgs a) {
     pdl_trigger();
     pdl_wait();
     using T = typename std::conditional<DT == MOESTEP_F32, float, bf16>::type;
@@ -280,6 +285,8 @@ int copy_call(bool write, const moestep_kv_dims* kd, int R, int n, const void* k
     a.page_log2 = kd->page == 16 ? 4 : kd->page == 32 ? 5 : kd->page == 64 ? 6 : 7;
     a.n_pages = kd->n_pages;
     a.max_pages = kd->max_pages;
+    a.per_magic = static_cast<uint32_t>(((1ull << 32) + 2 * kd->Hkv - 1) / (2 * kd->Hkv));
+    a.n_magic = n >= 2 && n <= 65000 ? static_cast<uint32_t>(((1ull << 32) + n - 1) / n) : 0;
     a.vectors = tokens * 2 * kd->Hkv;
     a.err = static_cast<int*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
