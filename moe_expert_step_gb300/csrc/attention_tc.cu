@@ -56,6 +56,7 @@ namespace {
 constexpr int kKeys = 128;                        // keys of a tile
 constexpr uint64_t kTeardown = 1000000000ull;     // limit for draining copies and MMAs in flight
 constexpr uint64_t kAbortedTile = 1000000ull;     // for FP8 key tiles whose scales an aborted CTA did not write
+constexpr int kStagger = 4;                       // key tiles of a share whose streams are put out of step
 constexpr float kSlack = 8.f;                     // how far a tile's maximum may pass m
 
 // MODE 0, 1, 2: row tiles of 32, 64, 128 (one tile, streams on alternate keys); 3: of 256 (two tiles)
@@ -80,9 +81,9 @@ struct Cfg {
     // query tile(s); with one row tile also the merge buffer, once the segment's scores are done
     static constexpr int kFront = kTwo ? 2 * kQ : 32768;
     static constexpr int kMul = 128 / D;
-    static constexpr int kNK = 3 * kMul;                                     // key tiles
-    static constexpr int kNV = (kTwo || F8 ? 2 : 3) * kMul;                        // value tiles
-    static constexpr int kNR = F8 ? (kTwo ? 2 : 4) * kMul : 0;                            // FP8 value tiles
+    static constexpr int kNK = 3 * kMul;                               // key tiles
+    static constexpr int kNV = (kTwo || F8 ? 2 : 3) * kMul;            // value tiles
+    static constexpr int kNR = F8 ? (kTwo ? 2 : 4) * kMul : 0;         // FP8 value tiles as stored
     static constexpr int kNS = F8 ? kNK + 2 : 0;  // key tiles' scales: a turn's are read while the tiles two ahead land
     static constexpr int kMisc = 1024 + (F8 ? 1024 + (kNK + kNR) * kKeys + kNS * kKeys * 4 : 0);
     static constexpr int kSmem = 1024 + kFront + kNK * kKTile + kNV * kTile + kNR * kRaw + kMisc;
@@ -662,7 +663,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         // ------------------------------------------------------------ MMA issuers, one a stream
         // With two row tiles the second stream's first scores wait until the first stream's weights
         // are under way, so that one's MMAs run under the other's exponentials: in step with each
-        // other both waited for both.
+        // other both waited for both.  (Not in a short share, which would only end later by that
+        // much: 32 tokens at 16384 positions, two tiles a CTA, 26.8 -> 25.6 us.)
         const int g = warp - 9;
         if (g == 1 && lane == 0) attn_describe_join<kKeys>(a, plan);
         __syncwarp();
@@ -716,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         while (wait.ok && attn_next<kKeys>(a, s)) {
             const int lo = attn_lo(a, s.L), n = s.tiles;
             if (!wait(q_full, segs & 1)) break;
-            if (C::kTwo && g == 1 && !wait(go, segs & 1)) break;
+                        if (C::kTwo && g == 1 && n >= kStagger && !wait(go, segs & 1)) break;
             ++segs;
             constexpr int kNext = C::kTwo ? 1 : 2;  // from one of the stream's key tiles to the next
             uint32_t begun = 0;

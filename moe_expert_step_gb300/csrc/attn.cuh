@@ -107,6 +107,7 @@ struct AttnPlan {
     int first;    // the CTA's first unit
     int begin_r;  // that unit's request
     int begin_o;  // and its number within the request
+    int begin_L;  // and the request's length
     int count;    // the CTA's units
 };
 
@@ -145,10 +146,13 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int* sm) {
     if (p.count > 0 && p.first >= incl - mine && p.first < incl) {
         int at = incl - mine;
         for (int r = r0; r < r1; ++r) {
-            const int n = (a.ahead + attn_tiles<KT>(a, attn_len(a, r)).y) * heads;
+            const int L = attn_len(a, r);
+            const int2 t = attn_tiles<KT>(a, L);
+            const int n = (a.ahead + t.y) * heads;
             if (p.first < at + n) {
                 sm[32] = r;
                 sm[33] = p.first - at;
+                sm[34] = L;
                 break;
             }
             at += n;
@@ -157,6 +161,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int* sm) {
     __syncthreads();
     p.begin_r = p.count > 0 ? sm[32] : 0;
     p.begin_o = p.count > 0 ? sm[33] : 0;
+    p.begin_L = p.count > 0 ? sm[34] : 0;
     return p;
 }
 
@@ -166,7 +171,7 @@ __device__ __forceinline__ void attn_describe_join(const AttnArgs& a, const Attn
     int4 j = make_int4(-1, 0, 0, 0);
     const int c = blockIdx.x;
     if (p.count > 0) {
-        const int n = a.ahead + attn_tiles<KT>(a, attn_len(a, p.begin_r)).y, seg = p.begin_o / n, o = p.begin_o - seg * n;
+        const int n = a.ahead + attn_tiles<KT>(a, p.begin_L).y, seg = p.begin_o / n, o = p.begin_o - seg * n;
         if (o > a.ahead) {
             const AttnShare sh(p.W, gridDim.x, a.even);
             const int start = p.first - o, c0 = sh.owner(start + a.ahead);  // who has the first key tile
@@ -192,7 +197,7 @@ __device__ __forceinline__ AttnWalk attn_begin(const AttnArgs& a, const AttnPlan
     w.left = p.count;
     w.k = -1;
     if (p.count > 0) {
-        w.L = attn_len(a, w.r);
+        w.L = p.begin_L;
         const int2 t = attn_tiles<KT>(a, w.L);
         w.t0 = t.x;
         w.nt = t.y;
