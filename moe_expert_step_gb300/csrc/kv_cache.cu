@@ -33,17 +33,18 @@ struct CopyArgs {
     int* err;
 };
 
-// A thread handles 16 consecutive elements of kPer vectors; D / 16 lanes share a vector, and
+// A thread handles 16 elements of kPer vectors; D / 16 lanes share a vector, and
 // consecutive vectors are a token's key heads, then its value heads, so a warp reads and
 // writes whole lines.  A block takes 2 * 256 / (D / 16) vectors: their tokens and requests are
 // found with 32-bit divisions (a wide one only in a launch of more than 2^32 vectors) and from
 // there on with multiplications by reciprocals: j < 2048 + 64, tl < n + 33, so both are exact.
 // Both kernels are copies, bound by memory: 32768 tokens of 8 heads of 128 (134 MB of bf16 on
-// one side, 69 MB of codes on the other) are written in 35.0 us and read back in 36.3 us, 5.8
-// and 5.6 TB/s.  Four vectors a thread take 3 and 1 us longer (fewer blocks, a longer tail), one
+// one side, 69 MB of codes on the other) are written in 34.7 us and read back in 33.8 us, 5.8
+// and 6.0 TB/s.  Four vectors a thread take 3 and 1 us longer (fewer blocks, a longer tail), one
 // 0.5 and 2 us and a read of 777 tokens 6.6 us against 6.0 us (too few loads in flight).  Six
 // resident blocks for the write (40 registers) against five 35.0 : 36.0 us, eight for the read
-// (32 registers) against six 36.3 : 40.2 us.
+// (32 registers) against six 36.3 : 40.2 us (then with 16 consecutive elements a thread, whose
+// stores of half sectors cost 2.5 us).
 constexpr int kPer = 2;
 
 struct Vector {
@@ -108,7 +109,8 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t w) {
     return __half22float2(*reinterpret_cast<__half2*>(&r));
 }
 
-// 16 elements as they are loaded: 2 (bf16) or 4 (fp32) 16-byte pieces
+// 16 elements as they are loaded: 2 (bf16) or 4 (fp32) 16-byte pieces, D / N elements apart, so that
+// the lanes of a vector read and write whole sectors together
 template <int DT>
 struct Sixteen {
     static constexpr int N = DT == MOESTEP_F32 ? 4 : 2;
@@ -136,9 +138,9 @@ __global__ void __launch_bounds__(256, DT == MOESTEP_F32 ? 4 : 6) kv_write_kerne
         if (vec[q].on) {
             pos[q] = __ldg(&a.pos[vec[q].t]);
             const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const T*>(vec[q].v ? a.v : a.k) + vec[q].t * a.ld + vec[q].h * D + lane * 16);
+                static_cast<const T*>(vec[q].v ? a.v : a.k) + vec[q].t * a.ld + vec[q].h * D) + lane;
 #pragma unroll
-            for (int i = 0; i < S::N; ++i) in[q].p[i] = __ldg(src + i);
+            for (int i = 0; i < S::N; ++i) in[q].p[i] = __ldg(src + i * L);
         }
     }
 #pragma unroll
@@ -148,9 +150,9 @@ __global__ void __launch_bounds__(256, DT == MOESTEP_F32 ? 4 : 6) kv_write_kerne
         void* cache = vec[q].v ? a.vc : a.kc;
         if (DT != MOESTEP_FP8) {
             if (row < 0) continue;
-            uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(cache) + row * D + lane * 16);
+            uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(cache) + row * D) + lane;
 #pragma unroll
-            for (int i = 0; i < S::N; ++i) d[i] = in[q].p[i];
+            for (int i = 0; i < S::N; ++i) d[i * L] = in[q].p[i];
             continue;
         }
         float x[16];
@@ -174,7 +176,9 @@ __global__ void __launch_bounds__(256, DT == MOESTEP_F32 ? 4 : 6) kv_write_kerne
         for (int i = 0; i < 4; ++i)
             w[i] = to_e4m3x2(x[4 * i] * s, x[4 * i + 1] * s) |
                    static_cast<uint32_t>(to_e4m3x2(x[4 * i + 2] * s, x[4 * i + 3] * s)) << 16;
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(cache) + row * D + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        uint2* d = reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D) + lane;
+        d[0] = make_uint2(w[0], w[1]);
+        d[L] = make_uint2(w[2], w[3]);
         if (lane == 0) (vec[q].v ? a.ve : a.ke)[row] = static_cast<uint8_t>(e + 127);
     }
 }
@@ -215,12 +219,14 @@ __global__ void __launch_bounds__(256, DT == MOESTEP_F32 ? 4 : 8) kv_read_kernel
         ex[q] = 127;
         if (row[q] < 0) continue;
         if (DT == MOESTEP_FP8) {
-            codes[q] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + row[q] * D + lane * 16));
+            const uint2* s = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + row[q] * D) + lane;
+            const uint2 lo = __ldg(s), hi = __ldg(s + L);
+            codes[q] = make_uint4(lo.x, lo.y, hi.x, hi.y);
             ex[q] = __ldg(&(vec[q].v ? a.ve : a.ke)[row[q]]);
         } else {
-            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(cache) + row[q] * D + lane * 16);
+            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(cache) + row[q] * D) + lane;
 #pragma unroll
-            for (int i = 0; i < S::N; ++i) o[q].p[i] = __ldg(s + i);
+            for (int i = 0; i < S::N; ++i) o[q].p[i] = __ldg(s + i * L);
         }
     }
 #pragma unroll
@@ -242,9 +248,9 @@ __global__ void __launch_bounds__(256, DT == MOESTEP_F32 ? 4 : 8) kv_read_kernel
             o[q].p[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
         uint4* d = reinterpret_cast<uint4*>(const_cast<T*>(static_cast<const T*>(vec[q].v ? a.v : a.k)) +
-                                            vec[q].t * a.ld + vec[q].h * D + lane * 16);
+                                            vec[q].t * a.ld + vec[q].h * D) + lane;
 #pragma unroll
-        for (int i = 0; i < S::N; ++i) d[i] = o[q].p[i];
+        for (int i = 0; i < S::N; ++i) d[i * L] = o[q].p[i];
     }
 }
 
