@@ -285,6 +285,9 @@ class KvDims:
         c = KvDimsC(self.Hq, self.Hkv, self.D, self.page, self.n_pages, self.max_pages, self.dtype)
         object.__setattr__(self, "_c", ctypes.byref(c))  # kept: single-token calls are short
 
+    def __reduce__(self):  # (a reference into a C struct cannot be copied or pickled)
+        return KvDims, (self.Hq, self.Hkv, self.D, self.page, self.n_pages, self.max_pages, self.dtype)
+
 
 def kv_cache(k, v, table, k_exp=None, v_exp=None) -> KvCache:
     """Device pointers of one paged cache: k, v [n_pages, Hkv, page, D], table [R, max_pages] int32, and with
@@ -311,21 +314,31 @@ def kv_workspace(kd: KvDims, R: int, n_q: int, device="cuda", stream=None):
     return ws
 
 
+_ACT = {}  # torch types of the activations of each dtype and of the integers (torch is imported late)
+
+
+def _types() -> dict:
+    if not _ACT:
+        import torch
+        _ACT.update({BF16: torch.bfloat16, FP8: torch.bfloat16, F32: torch.float32, "int": torch.int32})
+    return _ACT
+
+
 def _rows(t, heads: int, kd: KvDims, what: str) -> int:
     """Distance between the rows of t [tokens, heads, D], which may be part of a wider row."""
     st, shape = t.stride(), t.shape
     if (len(st) != 3 or st[2] != 1 or (heads > 1 and st[1] != kd.D) or shape[1] != heads or shape[2] != kd.D
-            or t.element_size() != (4 if kd.dtype == F32 else 2)):
+            or t.dtype is not _types().get(kd.dtype)):
         raise MoeStepError(EINVAL, f"{what} must be [tokens, {heads}, {kd.D}] in the activations' type, heads dense")
     if not t.is_cuda:
         raise MoeStepError(EINVAL, f"{what} must be on the GPU")
     return st[0] if shape[0] > 1 else max(st[0], heads * kd.D)
 
 
-def _dense(t, shape, size: int, what: str) -> None:
-    """t is a contiguous GPU tensor of the shape, `size` bytes an element."""
-    if t.shape != shape or t.element_size() != size or not t.is_contiguous():
-        raise MoeStepError(EINVAL, f"{what} must be contiguous, of shape {list(shape)} and {size} bytes an element")
+def _dense(t, shape, dtype, what: str) -> None:
+    """t is a contiguous GPU tensor of the shape and type."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise MoeStepError(EINVAL, f"{what} must be contiguous, of shape {list(shape)} and type {dtype}")
     if not t.is_cuda:
         raise MoeStepError(EINVAL, f"{what} must be on the GPU")
 
@@ -334,7 +347,7 @@ def kv_cache_write(kd: KvDims, R: int, k, v, pos, cache: KvCache, ws, stream=Non
     """Store the keys and values k, v [R * n, Hkv, D] (rows may be parts of wider rows) at positions
     pos [R, n] int32; a negative position is not stored."""
     n = pos.shape[1]
-    _dense(pos, (R, n), 4, "kv_cache_write: pos")
+    _dense(pos, (R, n), _types()["int"], "kv_cache_write: pos")
     ld = _rows(k, kd.Hkv, kd, "kv_cache_write: k")
     if _rows(v, kd.Hkv, kd, "kv_cache_write: v") != ld or k.shape[0] != R * n or v.shape[0] != R * n:
         raise MoeStepError(EINVAL, "kv_cache_write: k and v must have R * n rows, equally far apart")
@@ -345,10 +358,10 @@ def kv_cache_write(kd: KvDims, R: int, k, v, pos, cache: KvCache, ws, stream=Non
 def kv_cache_read(kd: KvDims, R: int, pos, cache: KvCache, k, v, ws, stream=None) -> None:
     """Read the cached vectors at positions pos [R, n] back into k, v [R * n, Hkv, D] (zeros where negative)."""
     n = pos.shape[1]
-    _dense(pos, (R, n), 4, "kv_cache_read: pos")
-    size = 4 if kd.dtype == F32 else 2
-    _dense(k, (R * n, kd.Hkv, kd.D), size, "kv_cache_read: k")
-    _dense(v, (R * n, kd.Hkv, kd.D), size, "kv_cache_read: v")
+    _dense(pos, (R, n), _types()["int"], "kv_cache_read: pos")
+    act = _types().get(kd.dtype)
+    _dense(k, (R * n, kd.Hkv, kd.D), act, "kv_cache_read: k")
+    _dense(v, (R * n, kd.Hkv, kd.D), act, "kv_cache_read: v")
     _check(lib().kv_cache_read(kd._c, R, n, pos.data_ptr(), cache, k.data_ptr(), v.data_ptr(), ws.data_ptr(),
                                ws.numel(), _s(stream)), "kv_cache_read")
 
@@ -360,12 +373,12 @@ def block_attention(kd: KvDims, R: int, q, kv_len, cache: KvCache, out, ws, scal
     T = q.shape[0]
     n_q = T // R if R > 0 else 0
     ld = _rows(q, kd.Hq, kd, "block_attention: q")
-    _dense(out, (R * n_q, kd.Hq, kd.D), 4 if kd.dtype == F32 else 2, "block_attention: out")
-    _dense(kv_len, (R,), 4, "block_attention: kv_len")
+    _dense(out, (R * n_q, kd.Hq, kd.D), _types().get(kd.dtype), "block_attention: out")
+    _dense(kv_len, (R,), _types()["int"], "block_attention: kv_len")
     if R * n_q != T:
         raise MoeStepError(EINVAL, "block_attention: q must have R * n_q rows")
     if lse is not None:
-        _dense(lse, (T, kd.Hq), 4, "block_attention: lse")
+        _dense(lse, (T, kd.Hq), _types()[F32], "block_attention: lse")
     _check(lib().block_attention(kd._c, R, n_q, q.data_ptr(), ld, kv_len.data_ptr(), cache, scale, int(causal),
                                  int(window), out.data_ptr(), _p(lse), ws.data_ptr(), ws.numel(), _s(stream)),
            "block_attention")
@@ -375,26 +388,27 @@ def block_residual_norm(d: ModelDims, y, h_in, h_out, x, w_pre=None, w_post=None
                         eps: float = 1e-6, stream=None) -> None:
     """h_out = h_in + res_scale * gate * (w_post * y / rms(y)); x = w_pre * h_out / rms(h_out).  y [T, H] fp32 or
     bf16; gate fp32 [H], or [requests, H] with one row for each d.P tokens; see block_residual_norm in moestep.h."""
-    T = y.shape[0]
-    shape = (T, d.H)
-    size, act = y.element_size(), 4 if d.dtype == F32 else 2
-    if size not in (2, 4):
+    T, H = y.shape[0], d.H
+    shape, types = (T, H), _types()
+    f32, act = types[F32], types.get(d.dtype)
+    if y.dtype is not f32 and y.dtype is not types[BF16]:
         raise MoeStepError(EINVAL, "block_residual_norm: y must be bf16 or fp32")
-    _dense(y, shape, size, "block_residual_norm: y")
-    _dense(h_in, shape, 4, "block_residual_norm: h_in")
-    _dense(h_out, shape, 4, "block_residual_norm: h_out")
+    _dense(y, shape, y.dtype, "block_residual_norm: y")
+    _dense(h_in, shape, f32, "block_residual_norm: h_in")
+    _dense(h_out, shape, f32, "block_residual_norm: h_out")
     if x is not None:
         _dense(x, shape, act, "block_residual_norm: x")
     for w in (w_pre, w_post):
         if w is not None:
-            _dense(w, (d.H,), act, "block_residual_norm: w_pre, w_post")
+            _dense(w, (H,), act, "block_residual_norm: w_pre, w_post")
     gate_ld = 0
     if gate is not None:
-        if (gate.shape[-1] != d.H or gate.stride(-1) != 1 or gate.element_size() != 4 or not gate.is_cuda
-                or gate.dim() > 2 or (gate.dim() == 2 and gate.shape[0] < -(-T // d.P))):
+        rows, st = gate.shape, gate.stride()
+        if (len(rows) not in (1, 2) or rows[-1] != H or st[-1] != 1 or gate.dtype is not f32 or not gate.is_cuda
+                or (len(rows) == 2 and rows[0] * d.P < T)):
             raise MoeStepError(EINVAL, "block_residual_norm: gate must be fp32 on the GPU, [H] or [requests, H]")
-        gate_ld = gate.stride(0) if gate.dim() == 2 and gate.shape[0] > 1 else 0
-    _check(lib().block_residual_norm(ctypes.byref(d.c()), T, y.data_ptr(), F32 if size == 4 else BF16, _p(w_post),
+        gate_ld = st[0] if len(rows) == 2 and rows[0] > 1 else 0
+    _check(lib().block_residual_norm(ctypes.byref(d.c()), T, y.data_ptr(), F32 if y.dtype is f32 else BF16, _p(w_post),
                                      _p(gate), gate_ld, res_scale, h_in.data_ptr(), h_out.data_ptr(), _p(w_pre),
                                      _p(x), eps, _s(stream)), "block_residual_norm")
 

@@ -142,3 +142,33 @@ def test_binding_refuses_shapes(L):
     y, h = torch.zeros(3, 2048), torch.zeros(3, 1024)
     refused("y must be", ms.block_residual_norm, d, y.double(), y, y, None)
     refused("y must be contiguous", ms.block_residual_norm, d, h, h, h, None)
+
+
+@pytest.mark.parametrize("what,dtype", [("q", torch.float16), ("q", torch.int16), ("out", torch.float16),
+                                        ("kv_len", torch.float32), ("lse", torch.int32)])
+def test_binding_refuses_types_of_the_right_size(L, what, dtype):
+    kd = ms.KvDims(**GOOD)
+    t = dict(q=torch.zeros(4, 16, 128, dtype=torch.bfloat16), kv_len=torch.zeros(4, dtype=torch.int32),
+             out=torch.zeros(4, 16, 128, dtype=torch.bfloat16), lse=torch.zeros(4, 16))
+    t[what] = t[what].to(dtype)
+    with pytest.raises(ms.MoeStepError) as e:
+        ms.block_attention(kd, 4, t["q"], t["kv_len"], cache(), t["out"], torch.zeros(512, dtype=torch.uint8), 1.0,
+                           lse=t["lse"])
+    assert e.value.code == ms.EINVAL
+
+
+def test_binding_refuses_other_types_in_the_norm(L):
+    d = ms.ModelDims(H=256, E=8, k=2, I=64, Is=64, V=128)
+    h = torch.zeros(2, 256)
+    for y, x in ((h.half(), None), (h, h.half()), (h, h)):
+        with pytest.raises(ms.MoeStepError) as e:
+            ms.block_residual_norm(d, y, h, h, x)
+        assert e.value.code == ms.EINVAL
+
+
+def test_dims_can_be_copied():
+    import copy
+    import pickle
+    kd = ms.KvDims(**GOOD)
+    for other in (copy.deepcopy(kd), pickle.loads(pickle.dumps(kd))):
+        assert other == kd and other is not kd and other._c is not kd._c
