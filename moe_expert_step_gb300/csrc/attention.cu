@@ -15,7 +15,8 @@ namespace {
 // Tiles of 16 query rows and 64 keys, 128 threads.  Each thread computes a 2 x 4 block of the
 // tile's scores, the 16 rows' statistics are kept by 8 lanes each, and each thread accumulates
 // 4 rows x (D / 32) columns of the output.  A tile's loads are in flight together, eight pieces a
-// thread of keys and of values.  3 requests of 7 tokens, window 500, 8 heads of 64 over 4: 14 us,
+// thread of keys and of values, the next tile's page numbers too.  3 requests of 7 tokens, window
+// 500, 8 heads of 64 over 4: 17 us,
 // the latency of a tile, of starting up and of the join (0.5 us of bytes).
 constexpr int kRT = 16, kKT = 64, kF32Threads = 128;
 template <int D>
@@ -44,40 +45,50 @@ __global__ void __launch_bounds__(kF32Threads) attn_f32_kernel(const AttnArgs a)
     while (attn_next<kKT>(a, w)) {
         const int h = w.h, row0 = w.rt * kRT;
         const int nrows = min(kRT, a.rows - row0);
-        __syncthreads();
-#pragma unroll 4
-        for (int i = tid; i < kRT * (D / 4); i += kF32Threads) {
-            const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4)), row = row0 + rr;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        // the queries and the first tile's pages are on their way together
+        constexpr int kQ = kRT * (D / 4) / kF32Threads;  // pieces of a thread
+        float4 qx[kQ];
+#pragma unroll
+        for (int u = 0; u < kQ; ++u) {
+            const int i = tid + u * kF32Threads, rr = i / (D / 4), d = 4 * (i - rr * (D / 4)), row = row0 + rr;
+            qx[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (rr < nrows) {
                 const int qi = attn_query(a, row), g = row - qi * a.G;
-                x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
-                                                          (static_cast<long long>(w.r) * a.n_q + qi) * a.q_ld +
-                                                          (h * a.G + g) * D + d));
+                qx[u] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                                              (static_cast<long long>(w.r) * a.n_q + qi) * a.q_ld +
+                                                              (h * a.G + g) * D + d));
             }
-            *reinterpret_cast<float4*>(sq + rr * D + d) = x;
         }
+        const int lo = attn_lo(a, w.L);
+        auto page_of = [&](int t) {  // of key tid of a tile, -1: not to be read
+            const int j = t * kKT + tid;
+            return tid < kKT && j >= lo && j < w.L
+                       ? __ldg(&a.table[static_cast<long long>(w.r) * a.max_pages + (j >> a.page_log2)]) : -1;
+        };
+        int page = page_of(w.tile);
+        __syncthreads();  // the segment before is done with the queries
+#pragma unroll
+        for (int u = 0; u < kQ; ++u) *reinterpret_cast<float4*>(sq + 4 * (tid + u * kF32Threads)) = qx[u];
         if (tid < kRT) {
             s_m[tid] = -INFINITY;
             s_l[tid] = 0.f;
         }
         float acc[4][CW] = {};
         const int vr = tid >> 5, vc = tid & 31;  // output: rows 4 vr .., columns vc + 32 j
-        const int lo = attn_lo(a, w.L);
         for (int t = w.tile; t < w.tile + w.tiles; ++t) {
             const int j0 = t * kKT;
             if (tid < kKT) {  // each key's row in the pool, -1: not to be read
                 const int j = j0 + tid;
                 int row = -1;
                 if (j >= lo && j < w.L) {
-                    const int id = __ldg(&a.table[static_cast<long long>(w.r) * a.max_pages + (j >> a.page_log2)]);
-                    if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages))
-                        row = ((id * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+                    if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages))
+                        row = ((page * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
                     else
                         record_error(a.err, kErrBadInput);
                 }
                 s_row[tid] = row;
             }
+            if (t + 1 < w.tile + w.tiles) page = page_of(t + 1);
             __syncthreads();
             constexpr int kPiece = D / 4, kBatch = 8;  // pieces of a row; loads of a thread in flight, twice
 #pragma unroll 1
@@ -104,6 +115,7 @@ __global__ void __launch_bounds__(kF32Threads) attn_f32_kernel(const AttnArgs a)
             {   // scores: rows 2 sr, 2 sr + 1; keys sc + 16 j
                 const int sr = tid >> 4, sc = tid & 15;
                 float s[2][4] = {};
+#pragma unroll 4
                 for (int d = 0; d < D; d += 4) {
                     const float4 q0 = *reinterpret_cast<const float4*>(sq + (2 * sr) * D + d);
                     const float4 q1 = *reinterpret_cast<const float4*>(sq + (2 * sr + 1) * D + d);
@@ -159,6 +171,7 @@ __global__ void __launch_bounds__(kF32Threads) attn_f32_kernel(const AttnArgs a)
 #pragma unroll
                 for (int c = 0; c < CW; ++c) acc[i][c] *= f;
             }
+#pragma unroll 4
             for (int key = 0; key < kKT; key += 4) {
                 float4 p[4];
 #pragma unroll
