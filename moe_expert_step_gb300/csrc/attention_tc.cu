@@ -38,7 +38,7 @@
 // brackets the copy rate's time for the keys and values): single tokens of 16 ragged requests, up
 // to 8192 positions, 26 us (12.1): starting up 4 us, the beginnings of two segments, eight tiles
 // and the join; tensor pipe 21 % busy.  One token at 131072 FP8 positions 38 us (10.0): 13 tiles
-// of 3000 cycles, issue slots 54 %.  32 tokens at 16384 positions 25 us (2.5): one beginning, two
+// of 2700 cycles, issue slots 54 %.  32 tokens at 16384 positions 25 us (2.5): one beginning, two
 // tiles, 128 KB of parts a CTA and their join.  16 such blocks, up to 32768 FP8 positions, 131 us
 // (24.9; 43.6 by operations at the bf16 rate): 34 tiles of two row tiles, 4500 to 5000 cycles
 // each, issue slots 60 %, tensor pipe 32 %: exponentials, conversions and staging share the issue
