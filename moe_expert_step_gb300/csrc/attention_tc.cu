@@ -282,6 +282,9 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                     }
                 }
                 __syncwarp();
+                // Two row tiles: the segment before left through the query tile, a part a warp, and
+                // these rows go to all parts.  (One row tile: the merge ended with a barrier.)
+                if (C::kTwo && s.k > 0) tc::named_bar_sync(2 + g, 128);
                 // (four pieces of code in a loop, the loaded pieces moved up: unrolled in full, the
                 // instructions alone took 7 us to arrive)
 #pragma unroll 1
