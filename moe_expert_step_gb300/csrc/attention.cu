@@ -260,7 +260,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
 #pragma unroll
             for (int k = 0; k < W; ++k) x[k] = 0.f;
             if (i >= n) return;
-            const float* p = a.part_o + slot(i) * D + lane * W;
+            const float* p = a.part_o;
+            if (a.slot_rows == 256) {  // halves of the columns, each row's 16-byte pieces swizzled (attention_tc.cu)
+                const int col = lane * W, half = col / (D / 2), piece = (col - half * (D / 2)) / 4;
+                const size_t s = static_cast<size_t>(i == 0 ? j.z : 2 * (c0 + i));
+                p += ((s * 2 + half) * 256 + rr) * (D / 2) + ((piece ^ (rr & 7)) << 2) + (col & 3);
+            } else {
+                p += slot(i) * D + lane * W;
+            }
             if constexpr (W == 4) {
                 const float4 y = __ldcg(reinterpret_cast<const float4*>(p));
                 x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;

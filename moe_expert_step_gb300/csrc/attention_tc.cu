@@ -39,7 +39,7 @@
 // to 8192 positions, 26 us (12.1): starting up 4 us, the beginnings of two segments, eight tiles
 // and the join; tensor pipe 21 % busy.  One token at 131072 FP8 positions 38 us (10.0): 13 tiles
 // of 2700 cycles, issue slots 54 %.  32 tokens at 16384 positions 25 us (2.5): one beginning, two
-// tiles, 128 KB of parts a CTA and their join.  16 such blocks, up to 32768 FP8 positions, 131 us
+// tiles, 128 KB of parts a CTA and their join.  16 such blocks, up to 32768 FP8 positions, 129 us
 // (24.9; 43.6 by operations at the bf16 rate): 34 tiles of two row tiles, 4500 to 5000 cycles
 // each, issue slots 60 %, tensor pipe 32 %: exponentials, conversions and staging share the issue
 // slots.
@@ -485,17 +485,24 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                                     make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                         }
                     }
+                    if (!s.whole) {  // as it stands, swizzle and all: one copy for the join to unravel
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tc::bulk_store(a.part_o + ((static_cast<size_t>(slot) * 2 + half) * 256 + wrow0) * (D / 2),
+                                           mine, kPart);
+                            tc::bulk_stores_read();
+                        }
+                        __syncwarp();
+                        continue;
+                    }
                     __syncwarp();
 #pragma unroll 4
                     for (int i = 0; i < 32; i += kRowsAtOnce) {
                         const int rr = i + sr;
                         if (rr >= wrows) continue;
-                        const uint4 x = *reinterpret_cast<const uint4*>(mine + rr * D * 2 + ((sc ^ (rr & 7)) << 4));
-                        if (s.whole)
-                            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + where(wrow0 + rr) * D + sc * 8) = x;
-                        else
-                            *reinterpret_cast<uint4*>(a.part_o + (static_cast<size_t>(slot) * a.slot_rows + wrow0 + rr) * D +
-                                                      half * (D / 2) + sc * 4) = x;
+                        *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + where(wrow0 + rr) * D + sc * 8) =
+                            *reinterpret_cast<const uint4*>(mine + rr * D * 2 + ((sc ^ (rr & 7)) << 4));
                     }
                 }
                 __syncwarp();
@@ -579,6 +586,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 }
             }
         }
+        if (C::kTwo && lane == 0) tc::bulk_stores_done();
         if (!wait.ok) err_bits = kErrTimeoutEpilogue;
     } else {
     if (F8) tc::fewer_registers<C::kOtherRegs>();

@@ -39,7 +39,7 @@ struct AttnArgs {
     const uint8_t* v_exp;
     void* out;
     float* lse;
-    float* part_o;    // [2 * CTAs][slot_rows][D]
+    float* part_o;    // [2 * CTAs][slot_rows][D]; slot_rows = 256: [2 * CTAs][2][256][D / 2], swizzled
     float2* part_ml;  // [2 * CTAs][slot_rows]: maximum (times scale * log2 e), sum
     int4* joins;      // [CTAs]: {request or -1, head * row tiles + row tile, first CTA's slot, last CTA}
     int* err;
