@@ -822,8 +822,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < 2 * s.tiles; ++i) {
                 const Buffer buf = buffer_of<C::kTwo>(i, s.tiles);
-                if (!buf.v) {  // keys: their scales, by one warp
-                    if (static_cast<int>(ik % (F8 ? C::kConv : 1)) == cw) {
+                // Keys: their scales, by one warp, always the same for a buffer: a warp that left out a
+                // phase of xfull could take the one before for the one it waits for.
+                static_assert(!F8 || NK <= C::kConv, "a converter warp for each key buffer");
+                if (!buf.v) {
+                    if (static_cast<int>(ik % NK) == cw) {
                         const int b = ik % NK;
                         if (!wait(&xfull[b], (ik / NK) & 1)) break;
                         const uint32_t w = reinterpret_cast<const uint32_t*>(kexps + b * kKeys)[lane];

@@ -212,6 +212,21 @@ def test_repeats_and_streams(dtype):
     assert torch.equal(o4, out)
 
 
+@pytest.mark.parametrize("n_q", [1, 17])
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.FP8])
+def test_many_one_tile_segments_of_a_cta(dtype, n_q):
+    """Several requests of one key tile each in a row on every CTA: each role goes from segment to
+    segment with the others up to a ring of buffers ahead."""
+    lengths = [n_q + (7 * r) % 23 for r in range(400 if n_q == 1 else 200)]
+    s = Setup(dtype, lengths, n_q, Hkv=2, G=8, D=128, page=16, seed=3)
+    out, ls = s.run()
+    s.check(out, ls)
+    for _ in range(20):
+        o2, l2 = s.run()
+        assert torch.equal(o2, out) and torch.equal(l2, ls)
+
+
+
 @pytest.mark.parametrize("dtype", KIND)
 def test_many_requests(dtype):
     """More requests than threads of a block: the division of the work scans them in runs."""
