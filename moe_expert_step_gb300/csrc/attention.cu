@@ -16,7 +16,7 @@ namespace {
 // tile's scores, the 16 rows' statistics are kept by 8 lanes each, and each thread accumulates
 // 4 rows x (D / 32) columns of the output.  A tile's loads are in flight together, eight pieces a
 // thread of keys and of values, the next tile's page numbers too.  3 requests of 7 tokens, window
-// 500, 8 heads of 64 over 4: 17 us, the latency of a tile, of starting up and of the join (0.5 us
+// 500, 8 heads of 64 over 4: 14 to 17 us, the latency of a tile, of starting up and of the join (0.5 us
 // of bytes).
 constexpr int kRT = 16, kKT = 64, kF32Threads = 128;
 template <int D>
