@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         const int lrow = C::kTwo ? g * 128 + w * 32 + lane               // row within the row tile
                                  : (w * 32 + lane) & (C::kRows - 1);
         const int col0 = part * C::kCols;
-        uint32_t tiles_g = 0, turns_g = 0, segs_g = 0, kt0 = 0;
+        uint32_t tiles_g = 0, turns_g = 0, segs = 0, kt0 = 0;
         // The eight warps meet at a hardware barrier between the steps of a merge.  They pass it
         // equally often whatever happens: after a wait that gave up they go through the rest of
         // their segments without waiting (their results are then unspecified).
@@ -440,11 +440,9 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             }
             turns_g += turn;
             const float l = l2.x + l2.y;
-            if (turn > 0) {
-                wait(&o_full[g], segs_g & 1);
-                ++segs_g;
-                tc::fence_after_sync();
-            }
+            wait(&o_full[g], segs & 1);
+            ++segs;
+            tc::fence_after_sync();
             const int slot = 2 * blockIdx.x + (s.k > 0);
             // row `rr` of the row tile: where it goes
             auto where = [&](int rr) {
@@ -729,8 +727,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
         while (wait.ok && attn_next<kKeys>(a, s)) {
             const int lo = attn_lo(a, s.L), n = s.tiles;
             if (!wait(q_full, segs & 1)) break;
-                        if (C::kTwo && g == 1 && n >= kStagger && !wait(go, segs & 1)) break;
+            if (C::kTwo && g == 1 && n >= kStagger && !wait(go, segs & 1)) break;
             ++segs;
+            // A stream without a tile here reports at once: the softmax warps stage the next segment's
+            // queries only once both issuers have taken these (q_full's parity names one of two phases).
+            if (!C::kTwo && g >= n && lane == 0) tc::mbar_arrive(&o_full[g]);
             constexpr int kNext = C::kTwo ? 1 : 2;  // from one of the stream's key tiles to the next
             uint32_t begun = 0;
             // t = -kNext ..: the values of tile t, and the scores of the stream's next tile, each
