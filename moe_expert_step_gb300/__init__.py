@@ -67,6 +67,7 @@ class KvDimsC(ctypes.Structure):
 
 class KvCache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp", "table")]
+    _holds = None  # of the tensors (kv_cache): type, Hkv, page, D, max_pages
 
 
 _LIB = None
@@ -284,20 +285,46 @@ class KvDims:
     def __post_init__(self):
         c = KvDimsC(self.Hq, self.Hkv, self.D, self.page, self.n_pages, self.max_pages, self.dtype)
         object.__setattr__(self, "_c", ctypes.byref(c))  # kept: single-token calls are short
+        object.__setattr__(self, "_holds", (self.dtype, self.Hkv, self.page, self.D, self.max_pages))
 
     def __reduce__(self):  # (a reference into a C struct cannot be copied or pickled)
         return KvDims, (self.Hq, self.Hkv, self.D, self.page, self.n_pages, self.max_pages, self.dtype)
 
 
 def kv_cache(k, v, table, k_exp=None, v_exp=None) -> KvCache:
-    """Device pointers of one paged cache: k, v [n_pages, Hkv, page, D], table [R, max_pages] int32, and with
-    MOESTEP_FP8 k_exp, v_exp [n_pages, Hkv, page] uint8.  The struct keeps the tensors alive."""
-    for t in (k, v, table, k_exp, v_exp):
+    """Device pointers of one paged cache: k, v [n_pages, Hkv, page, D] in bf16, fp32 or, for MOESTEP_FP8, E4M3 codes
+    (or their bytes), table [R, max_pages] int32, and with MOESTEP_FP8 k_exp, v_exp [n_pages, Hkv, page] uint8.  The
+    struct keeps the tensors alive; each call compares them with its dims and R (a pool may have more pages, a table
+    more rows than a call names)."""
+    import torch
+    tensors = (k, v, table, k_exp, v_exp)
+    for t in tensors:
         if t is not None and not t.is_contiguous():
             raise MoeStepError(EINVAL, "kv_cache: tensors must be contiguous")
+    kind = {torch.bfloat16: BF16, torch.float32: F32, torch.float8_e4m3fn: FP8, torch.uint8: FP8}.get(k.dtype)
+    if kind is None or k.dim() != 4 or v.dtype is not k.dtype or v.shape != k.shape:
+        raise MoeStepError(EINVAL, "kv_cache: k and v must be [n_pages, Hkv, page, D], bf16, fp32 or E4M3, and alike")
+    if table.dim() != 2 or table.dtype is not torch.int32:
+        raise MoeStepError(EINVAL, "kv_cache: table must be [R, max_pages] int32")
+    for e in (k_exp, v_exp) if kind == FP8 else ():
+        if e is None or e.dtype is not torch.uint8 or e.shape != k.shape[:3]:
+            raise MoeStepError(EINVAL, "kv_cache: k_exp and v_exp must be [n_pages, Hkv, page] uint8")
+    if not all(t is None or t.is_cuda for t in tensors):
+        raise MoeStepError(EINVAL, "kv_cache: tensors must be on the GPU")
     c = KvCache(_p(k), _p(v), _p(k_exp), _p(v_exp), _p(table))
-    c._tensors = (k, v, table, k_exp, v_exp)
+    c._tensors = tensors
+    c._holds = (kind, *k.shape[1:], table.shape[1])
+    c._n_pages, c._rows = k.shape[0], table.shape[0]
     return c
+
+
+def _fits(cache: KvCache, kd: KvDims, R: int, ws, what: str) -> None:
+    """The cache holds what kd and R say (a struct of raw pointers is taken as it is), the workspace is on the GPU."""
+    holds = cache._holds
+    if holds is not None and (holds != kd._holds or cache._n_pages < kd.n_pages or cache._rows < R):
+        raise MoeStepError(EINVAL, f"{what}: the cache does not have the type, the pages or the table of {kd}, R = {R}")
+    if not ws.is_cuda:
+        raise MoeStepError(EINVAL, f"{what}: ws must be on the GPU")
 
 
 def kv_workspace_size(kd: KvDims, R: int, n_q: int) -> int:
@@ -351,6 +378,7 @@ def kv_cache_write(kd: KvDims, R: int, k, v, pos, cache: KvCache, ws, stream=Non
     ld = _rows(k, kd.Hkv, kd, "kv_cache_write: k")
     if _rows(v, kd.Hkv, kd, "kv_cache_write: v") != ld or k.shape[0] != R * n or v.shape[0] != R * n:
         raise MoeStepError(EINVAL, "kv_cache_write: k and v must have R * n rows, equally far apart")
+    _fits(cache, kd, R, ws, "kv_cache_write")
     _check(lib().kv_cache_write(kd._c, R, n, k.data_ptr(), v.data_ptr(), ld, pos.data_ptr(), cache, ws.data_ptr(),
                                 ws.numel(), _s(stream)), "kv_cache_write")
 
@@ -362,6 +390,7 @@ def kv_cache_read(kd: KvDims, R: int, pos, cache: KvCache, k, v, ws, stream=None
     act = _types().get(kd.dtype)
     _dense(k, (R * n, kd.Hkv, kd.D), act, "kv_cache_read: k")
     _dense(v, (R * n, kd.Hkv, kd.D), act, "kv_cache_read: v")
+    _fits(cache, kd, R, ws, "kv_cache_read")
     _check(lib().kv_cache_read(kd._c, R, n, pos.data_ptr(), cache, k.data_ptr(), v.data_ptr(), ws.data_ptr(),
                                ws.numel(), _s(stream)), "kv_cache_read")
 
@@ -379,6 +408,7 @@ def block_attention(kd: KvDims, R: int, q, kv_len, cache: KvCache, out, ws, scal
         raise MoeStepError(EINVAL, "block_attention: q must have R * n_q rows")
     if lse is not None:
         _dense(lse, (T, kd.Hq), _types()[F32], "block_attention: lse")
+    _fits(cache, kd, R, ws, "block_attention")
     _check(lib().block_attention(kd._c, R, n_q, q.data_ptr(), ld, kv_len.data_ptr(), cache, scale, int(causal),
                                  int(window), out.data_ptr(), _p(lse), ws.data_ptr(), ws.numel(), _s(stream)),
            "block_attention")
