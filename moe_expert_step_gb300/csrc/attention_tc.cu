@@ -90,9 +90,14 @@ struct Cfg {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// 2^(exp - 127) of an exponent byte
-__device__ __forceinline__ float exp_scale(uint32_t e) {
-    return e > 0 ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);
+// FP8 scores.  A product of codes is below 2^25 (D 448^2) and the keys' powers of two go up to 2^119, so
+// the keys' factor is 2^(exp - 127) * 2^-17, finite wherever the score is, and the row's is 2^17 times the
+// query's power.  Of a power above kBigQuery, which would take that factor past fp32's range, the rest
+// comes in by a multiplication beside the masking of a partial tile (16 blocks of 32 tokens, up to 32768
+// positions, 129.1 -> 129.8 us; as a branch of its own 134 to 137 us).
+constexpr float kKeyShift = 0x1p17f, kBigQuery = 0x1p32f;
+__device__ __forceinline__ float key_scale(uint32_t e) {  // of an exponent byte
+    return __uint_as_float(e > 17 ? (e - 17) << 23 : 1u << (e + 5));
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
     uint8_t* vring = sq + C::kFront;
     uint8_t* kring = vring + NV * C::kTile;
     uint8_t* raw = kring + NK * C::kKTile;
-    float* kscale = reinterpret_cast<float*>(raw + C::kNR * C::kRaw);        // FP8 [NS][128]: 2^(exp - 127) of keys
+    float* kscale = reinterpret_cast<float*>(raw + C::kNR * C::kRaw);        // FP8 [NS][128]: factors of keys
     float* qscale = kscale + C::kNS * kKeys;                                 // FP8 [256]: powers of two of query rows
     uint8_t* kexps = reinterpret_cast<uint8_t*>(qscale + (F8 ? 256 : 0));    // FP8 [NK][128]
     uint8_t* exps = kexps + (F8 ? NK * kKeys : 0);                           // FP8 [NR][128] of values
@@ -361,11 +366,15 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             for (int half = 0; half < C::kHalves; ++half, ++turn) {  // (both loops' body)
                 wait(&s_full[g * 2 + half], tiles_g & 1);
                 tc::fence_after_sync();
-                if (F8 && turn == 0) scl = a.scale_log2 * qscale[C::kTwo ? lrow : w * 32 + lane];
+                if (F8 && turn == 0) {
+                    const float q = qscale[C::kTwo ? lrow : w * 32 + lane];
+                    scl = a.scale_log2 * ((q > kBigQuery ? kBigQuery : q) * kKeyShift);
+                }
                 const uint32_t t_x = t_s + half * 64;  // this turn's scores, then its weights
                 const int c0 = col0 + half * 64;
                 const int lo = see.x - (t * kKeys + c0), hi = see.y - (t * kKeys + c0);
-                const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < C::kWide);
+                const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < C::kWide ||  // or a big query's row
+                                                                (F8 && scl >= a.scale_log2 * (kBigQuery * kKeyShift)));
                 constexpr int kHold = C::kWide;  // scores held in registers between the two passes
                 float v[kHold];
                 float mx = -INFINITY;
@@ -382,6 +391,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         }
                     }
                     if (masked) {
+                        if (F8) {
+                            const float q = qscale[C::kTwo ? lrow : w * 32 + lane], x = q > kBigQuery ? q * (1.f / kBigQuery) : 1.f;
+#pragma unroll
+                            for (int i = 0; i < kHold; i += 2) {
+                                const float2 y = tc::mul2(make_float2(v[i], v[i + 1]), make_float2(x, x));
+                                v[i] = y.x, v[i + 1] = y.y;
+                            }
+                        }
 #pragma unroll
                         for (int i = 0; i < kHold; ++i) v[i] = (c + i >= lo && c + i < hi) ? v[i] : -INFINITY;
                     }
@@ -832,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         if (!wait(&xfull[b], (ik / NK) & 1)) break;
                         const uint32_t w = reinterpret_cast<const uint32_t*>(kexps + b * kKeys)[lane];
                         float4 f;
-                        f.x = exp_scale(w & 255), f.y = exp_scale(w >> 8 & 255), f.z = exp_scale(w >> 16 & 255), f.w = exp_scale(w >> 24);
+                        f.x = key_scale(w & 255), f.y = key_scale(w >> 8 & 255), f.z = key_scale(w >> 16 & 255), f.w = key_scale(w >> 24);
                         *reinterpret_cast<float4*>(kscale + (ik % NS) * kKeys + lane * 4) = f;
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(&kfull[b]);
