@@ -465,6 +465,11 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     // a window as long as the cache hides nothing (and stays out of 32-bit overflow)
     a.window = window >= kd->max_pages * kd->page ? 0 : window;
     a.scale_log2 = scale * 1.4426950408889634f;
+    if (f8) {
+        int e = 0;
+        a.key_mul = std::frexp(a.scale_log2, &e);
+        a.scale_log2 = std::ldexp(1.f, e);
+    }
     a.timeout_ns = wait_timeout_ns();
     const int want = f32 ? 2 * sms : sms, grid = want < max_ctas(*kd) ? want : max_ctas(*kd);
     CUtensorMap km, vm;

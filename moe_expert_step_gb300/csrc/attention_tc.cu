@@ -99,6 +99,19 @@ constexpr float kKeyShift = 0x1p17f, kBigQuery = 0x1p32f;
 __device__ __forceinline__ float key_scale(uint32_t e) {  // of an exponent byte
     return __uint_as_float(e > 17 ? (e - 17) << 23 : 1u << (e + 5));
 }
+// Scores beyond 2^30.  Fp32 holds multiples of 64 of them, so their softmax is one key's (or some equal
+// ones'), and weights are 2^(S c - m), a fused product: with c of 24 bits it is off a maximum m that was
+// rounded by up to half a step of it, which from 2^31 on takes the largest weight itself out of range.
+// FP8: c is a power of two (the scale's mantissa is in the keys' factors), so that m is exact.  bf16: such
+// a row's scores are counted in a unit that brings the maximum down to 2^30, a power of two that leaves
+// neighbouring scores 32 apart.
+__device__ __forceinline__ float unit_of(float top) {
+    const uint32_t e = __float_as_uint(top) >> 23 & 255;
+    return e > 127 + 30 && e < 255 ? __uint_as_float((2 * 127 + 30 - e) << 23) : 1.f;
+}
+__device__ __forceinline__ float ratio_pow2(float a, float b) {  // of two floats with the same mantissa
+    return __uint_as_float(__float_as_uint(a) - __float_as_uint(b) + (127u << 23));
+}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -354,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
             }
             const int2 see = attn_sees(a, s.L, attn_query(a, row0 + min(lrow, nrows - 1)));
             if (F8) __syncwarp();
-            float scl = a.scale_log2;  // of this row's scores; FP8: read once the queries are staged
+            float scl = a.scale_log2;  // of this row's scores; FP8: read once the queries are staged; bf16: see unit_of
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
             const int step = C::kTwo ? 1 : 2, first = s.tile + (C::kTwo ? 0 : g);
@@ -409,8 +422,17 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 mx *= scl;
                 const bool move = mx > m + kSlack || (m == -INFINITY && mx > m);
                 if (__any_sync(0xffffffffu, move)) {
+                    if (!F8 && move) {  // in units of 1, then of this maximum
+                        const float up = ratio_pow2(a.scale_log2, scl);
+                        m *= up, mx *= up;
+                    }
                     const float f = move ? tc::exp2_fast(m - mx) : 1.f;  // 0 from m = -inf
                     if (move) m = mx;
+                    if (!F8 && move) {
+                        const float unit = unit_of(m);
+                        scl = a.scale_log2 * unit;
+                        m *= unit;
+                    }
                     l2 = make_float2(l2.x * f, l2.y * f);
                     if (turn > 0) {
                         if (C::kHalves > 1) {  // the half before is multiplied meanwhile
@@ -456,6 +478,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                 if (lane == 0) tc::mbar_arrive(&p_full[g * 2 + half]);
             }
             turns_g += turn;
+            if (!F8) m *= ratio_pow2(a.scale_log2, scl);
             const float l = l2.x + l2.y;
             wait(&o_full[g], segs & 1);
             ++segs;
@@ -849,7 +872,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         if (!wait(&xfull[b], (ik / NK) & 1)) break;
                         const uint32_t w = reinterpret_cast<const uint32_t*>(kexps + b * kKeys)[lane];
                         float4 f;
-                        f.x = key_scale(w & 255), f.y = key_scale(w >> 8 & 255), f.z = key_scale(w >> 16 & 255), f.w = key_scale(w >> 24);
+                        f.x = key_scale(w & 255) * a.key_mul, f.y = key_scale(w >> 8 & 255) * a.key_mul;
+                        f.z = key_scale(w >> 16 & 255) * a.key_mul, f.w = key_scale(w >> 24) * a.key_mul;
                         *reinterpret_cast<float4*>(kscale + (ik % NS) * kKeys + lane * 4) = f;
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(&kfull[b]);

@@ -53,6 +53,7 @@ struct AttnArgs {
     int even;          // largest share (units a CTA) that is divided evenly
     int ahead;         // empty units of a segment
     float scale_log2;  // scale * log2(e): the kernels take exponentials to base 2
+    float key_mul;     // FP8: scale_log2 is a power of two, this the rest of scale * log2(e) (1/2 .. 1)
     unsigned long long timeout_ns;
 };
 

@@ -2,6 +2,7 @@
 can express, against the float64 oracle with the bounds of test_gpu_attention.py: powers of two change
 neither the relative errors nor the weights, as long as the scale takes them back."""
 import pytest
+import torch
 
 import moe_expert_step_gb300 as ms
 from tests.test_gpu_attention import Setup
@@ -29,4 +30,14 @@ def scaled(keys, queries, n_q, D, seed=30):
 def test_large_and_small_keys(keys, queries, n_q, D):
     """Row tiles of 32, 64, 128 and 256; exponents from -100 to 119, queries from 2^-84 to 2^120."""
     s = scaled(keys, queries, n_q, D)
+    s.check(*s.run())
+
+
+@pytest.mark.parametrize("n_q", [3, 20, 50, 80])
+def test_large_queries_beside_ordinary_ones(n_q):
+    """Rows of one tile whose powers of two lie 80 apart."""
+    s = scaled(-60, 0, n_q, 128)
+    s.scale *= 2.0 ** -40
+    f = torch.tensor([2.0 ** (40 * (i % 3)) for i in range(s.q.shape[0])], dtype=torch.float64, device="cuda")
+    s.q = (s.q.double() * f[:, None, None]).bfloat16()
     s.check(*s.run())
