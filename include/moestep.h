@@ -328,8 +328,8 @@ int kv_cache_read(const moestep_kv_dims* kd, int R, int n, const int32_t* pos, c
  * Products accumulate in fp32; the softmax weights are rounded to bf16 before they
  * multiply V, except with MOESTEP_F32.  MOESTEP_FP8: a query row enters as the sum of two
  * E4M3 values an element times a power of two, exact but for elements below 1/896 of the
- * row's largest, which are off by at most 2^-17 of that; an infinite or NaN query makes its
- * row NaN.  Results do not depend on timing, only on the arguments and the device. */
+ * row's largest, which are off by at most 2^-17 of that (or 2^-136); an infinite or NaN query
+ * makes its row NaN.  Results do not depend on timing, only on the arguments and the device. */
 int block_attention(const moestep_kv_dims* kd, int R, int n_q, const void* q, long long q_ld,
                     const int32_t* kv_len, const moestep_kv_cache* cache, float scale, int causal, int window,
                     void* out, float* lse, void* ws, size_t ws_bytes, void* stream);

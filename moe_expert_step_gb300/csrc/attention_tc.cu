@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         // parts: the first takes the leading 4 bits of a bf16's 8, the second the rest.
                         // Exact for elements of 1/4 and more; below that the second's smallest step,
                         // 2^-9, leaves an error of at most 2^-10, against a largest element above
-                        // 224: 2^-17 of it.  An infinite row gives NaN scores.
+                        // 224: 2^-17 of it (in rows below 2^-117, which no normal power brings there, 2^-136).
+                        // An infinite row gives NaN scores.
                         const uint32_t w[4] = {piece16.x, piece16.y, piece16.z, piece16.w};
                         float amax = 0.f;
 #pragma unroll
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
                         for (int o = kChunks / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                         const uint32_t bits = __float_as_uint(amax);
                         int e = static_cast<int>(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u);  // 448 = 0.875 * 2^9
-                        e = min(max(e, -100), 119);
+                        e = min(max(e, -126), 119);
                         const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                         if (c == 0)
                             qscale[(C::kTwo ? g * 128 : 0) + m] = bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)

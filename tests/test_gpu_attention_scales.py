@@ -41,3 +41,12 @@ def test_large_queries_beside_ordinary_ones(n_q):
     f = torch.tensor([2.0 ** (40 * (i % 3)) for i in range(s.q.shape[0])], dtype=torch.float64, device="cuda")
     s.q = (s.q.double() * f[:, None, None]).bfloat16()
     s.check(*s.run())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_q", [3, 20, 50, 80])
+@pytest.mark.parametrize("keys,queries", [(96, -96), (112, -112), (118, -115)])
+def test_tiny_queries(keys, queries, n_q, D):
+    """Queries down to 2^-115 keep their bits."""
+    s = scaled(keys, queries, n_q, D, seed=31)
+    s.check(*s.run())
