@@ -410,7 +410,7 @@ def block_attention(kd: KvDims, R: int, q, kv_len, cache: KvCache, out, ws, scal
         _dense(lse, (T, kd.Hq), _types()[F32], "block_attention: lse")
     _fits(cache, kd, R, ws, "block_attention")
     _check(lib().block_attention(kd._c, R, n_q, q.data_ptr(), ld, kv_len.data_ptr(), cache, scale, int(causal),
-                                 int(window), out.data_ptr(), _p(lse), ws.data_ptr(), ws.numel(), _s(stream)),
+                                 min(int(window), 0x7fffffff), out.data_ptr(), _p(lse), ws.data_ptr(), ws.numel(), _s(stream)),
            "block_attention")
 
 

@@ -423,6 +423,8 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     int rc = check_attn(kd, R, n_q);
     if (rc != MOESTEP_OK) return rc;
     if (!kv_len || !out || window < 0 || !std::isfinite(scale) || !(scale > 0.f)) return MOESTEP_EINVAL;
+    if (window >= kd->max_pages * kd->page) window = 0;  // a window as long as the cache hides nothing
+    if (window > (1ll << 31) - 1 - n_q) return MOESTEP_EUNSUPPORTED;  // (positions less a window stay in 32 bits)
     if ((rc = check_kv_cache(kd, cache)) != MOESTEP_OK) return rc;
     if ((rc = check_kv_rows(q, q_ld, 1ll * kd->Hq * kd->D, kd->dtype)) != MOESTEP_OK) return rc;
     if (!kv_aligned16(out)) return MOESTEP_EALIGN;
@@ -462,8 +464,7 @@ extern "C" int block_attention(const moestep_kv_dims* kd, int R, int n_q, const 
     a.causal = causal != 0;
     a.even = !f32 && L.slot_rows == 256 ? 4 : 0;
     a.ahead = f32 ? 0 : L.slot_rows == 256 ? kAhead : kAheadFew;
-    // a window as long as the cache hides nothing (and stays out of 32-bit overflow)
-    a.window = window >= kd->max_pages * kd->page ? 0 : window;
+    a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
     if (f8) {
         int e = 0;

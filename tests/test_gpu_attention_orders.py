@@ -21,3 +21,27 @@ def test_segments_that_one_stream_has_no_tile_of(dtype, n_q, D):
     for _ in range(20):
         o2, l2 = s.run()
         assert torch.equal(o2, out) and torch.equal(l2, ls)
+
+
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.F32, ms.FP8])
+def test_windows_about_as_long_as_32_bits(dtype):
+    """A window longer than the request hides nothing, up to the longest that the longest page table allows and
+    beyond it."""
+    n_q, max_pages = 512, (1 << 27) - 16
+    s = Setup(dtype, [600], n_q, 1, 1, 64, 16, seed=22)
+    table = torch.empty((1, max_pages), dtype=torch.int32, device="cuda")
+    table[:, :s.table.shape[1]] = s.table
+    s.kd = ms.KvDims(Hq=1, Hkv=1, D=64, page=16, n_pages=s.kd.n_pages, max_pages=max_pages, dtype=dtype)
+    s.cache = ms.kv_cache(*s.pools, table, *s.cache._tensors[3:])
+    for n in (600, 10):
+        s.len.fill_(n)
+        s.window = 0
+        want = s.run(True)
+        for s.window in (1 << 30, 2 ** 31 - 1 - n_q, 16 * max_pages, 2 ** 31 - 1, 2 ** 31, 2 ** 40):
+            out, ls = s.run(True)
+            assert torch.equal(out, want[0]) and torch.equal(ls, want[1]), (n, s.window)
+        for s.window in (2 ** 31 - n_q, 16 * max_pages - 1):  # shorter than the table's positions
+            with pytest.raises(ms.MoeStepError) as e:
+                s.run(True)
+            assert e.value.code == ms.EUNSUPPORTED
+    assert ms.read_device_error(s.ws) == ms.OK

@@ -103,3 +103,14 @@ def test_the_comparison_itself():
     for more in (0, 1):
         c._holds, c._n_pages, c._rows = good[:5], N + more, R + more
         ms._fits(c, kd, R, Ws, "call")
+
+
+@pytest.mark.parametrize("window,n_q,code", [(2 ** 31 - 257, 300, ms.EUNSUPPORTED), (2 ** 31 - 300, 300, ms.EUNSUPPORTED),
+                                             (2 ** 31 - 301, 300, None), (2 ** 31 - 256, 300, None),
+                                             (2 ** 31 - 1, 300, None), (2 ** 31 - 257, 256, None)])
+def test_windows_that_pass_32_bits(window, n_q, code):
+    """At the C entry, with a workspace too small: what is not refused for the window is refused for that."""
+    kd = ms.KvDims(Hq=1, Hkv=1, D=D, page=16, n_pages=N, max_pages=(1 << 27) - 16)
+    c = ms.KvCache(1 << 20, 1 << 20, None, None, 1 << 20)
+    got = ms.lib().block_attention(kd._c, 1, n_q, 1 << 20, D, 1 << 20, c, 1.0, 0, window, 1 << 20, None, 1 << 20, 512, None)
+    assert got == (ms.EWORKSPACE if code is None else code)
