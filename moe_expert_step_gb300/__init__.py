@@ -359,7 +359,7 @@ def _rows(t, heads: int, kd: KvDims, what: str) -> int:
         raise MoeStepError(EINVAL, f"{what} must be [tokens, {heads}, {kd.D}] in the activations' type, heads dense")
     if not t.is_cuda:
         raise MoeStepError(EINVAL, f"{what} must be on the GPU")
-    return st[0] if shape[0] > 1 else max(st[0], heads * kd.D)
+    return st[0] if shape[0] > 1 else heads * kd.D  # (of one row: any)
 
 
 def _dense(t, shape, dtype, what: str) -> None:

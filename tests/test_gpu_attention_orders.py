@@ -45,3 +45,27 @@ def test_windows_about_as_long_as_32_bits(dtype):
                 s.run(True)
             assert e.value.code == ms.EUNSUPPORTED
     assert ms.read_device_error(s.ws) == ms.OK
+
+
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.F32, ms.FP8])
+def test_one_row_has_no_stride(dtype):
+    """A single token's keys, values and queries are taken from rows of different and odd widths."""
+    kd = ms.KvDims(Hq=4, Hkv=2, D=64, page=16, n_pages=1, max_pages=1, dtype=dtype)
+    act = torch.float32 if dtype == ms.F32 else torch.bfloat16
+    store = {ms.BF16: torch.bfloat16, ms.F32: torch.float32, ms.FP8: torch.float8_e4m3fn}[dtype]
+    results = []
+    for k_ld, v_ld, q_ld in ((128, 128, 256), (1024, 128, 259), (131, 2000, 777), (1, 1, 1)):
+        pools = [torch.zeros((1, 2, 16, 64), device="cuda").to(store) for _ in "kv"]
+        exps = [torch.zeros((1, 2, 16), dtype=torch.uint8, device="cuda") if dtype == ms.FP8 else None for _ in "kv"]
+        cache = ms.kv_cache(*pools, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), *exps)
+        ws = ms.kv_workspace(kd, 1, 1)
+        g = torch.Generator(device="cuda").manual_seed(1)
+        new = lambda h, ld: torch.randn(h * 64, generator=g, device="cuda").to(act).as_strided((1, h, 64), (ld, 64, 1))  # noqa: E731
+        k, v, q, out = new(2, k_ld), new(2, v_ld), new(4, q_ld), torch.empty((1, 4, 64), dtype=act, device="cuda")
+        ms.kv_cache_write(kd, 1, k, v, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), cache, ws)
+        ms.block_attention(kd, 1, q, torch.ones(1, dtype=torch.int32, device="cuda"), cache, out, ws, 0.1)
+        assert ms.read_device_error(ws) == ms.OK
+        results.append((pools[0].float(), pools[1].float(), out))
+    for r in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(r, results[0]))
+    assert torch.equal(results[0][2][0, :2], results[0][2][0, 1:2].expand(2, 64))  # one key: its value
