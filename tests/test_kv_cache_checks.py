@@ -114,3 +114,66 @@ def test_windows_that_pass_32_bits(window, n_q, code):
     c = ms.KvCache(1 << 20, 1 << 20, None, None, 1 << 20)
     got = ms.lib().block_attention(kd._c, 1, n_q, 1 << 20, D, 1 << 20, c, 1.0, 0, window, 1 << 20, None, 1 << 20, 512, None)
     assert got == (ms.EWORKSPACE if code is None else code)
+
+
+ATTENTION = [("q", torch.float16, "q must be"), ("q", torch.int16, "q must be"), ("q", torch.float64, "q must be"),
+             ("out", torch.float16, "out must be"), ("out", torch.int16, "out must be"),
+             ("n", torch.float32, "kv_len must be"), ("n", torch.int64, "kv_len must be"),
+             ("lse", torch.int32, "lse must be"), ("lse", torch.bfloat16, "lse must be")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.F32, ms.FP8])
+def test_attention_takes_no_other_type(dtype):
+    """One argument at a time, the others as they should be."""
+    c = Calls(dtype)
+    c.all()[2]()
+    for name, other, match in ATTENTION:
+        c = Calls(dtype)
+        setattr(c, name, getattr(c, name).to(other))
+        refused([c.all()[2]], f"block_attention: {match}")
+    for name in ("q", "out", "n", "lse"):
+        c = Calls(dtype)
+        setattr(c, name, getattr(c, name).cpu())
+        refused([c.all()[2]], "must be on the GPU")
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.F32, ms.FP8])
+def test_copies_take_no_other_type(dtype):
+    for name, other in (("k", torch.float16), ("v", torch.float16), ("k", torch.int32), ("pos", torch.int64),
+                        ("pos", torch.float32)):
+        c = Calls(dtype)
+        setattr(c, name, getattr(c, name).to(other))
+        refused(c.all()[:2], f"{name} must be")
+        c = Calls(dtype)
+        setattr(c, name, getattr(c, name).cpu())
+        refused(c.all()[:2], "must be on the GPU")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.F32])
+def test_the_norm_takes_no_other_type(dtype):
+    d = ms.ModelDims(H=256, E=8, k=2, I=64, Is=64, V=128, dtype=dtype)
+    act = torch.float32 if dtype == ms.F32 else torch.bfloat16
+
+    def call(**kw):
+        z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+        a = dict(y=z(2, 256), h_in=z(2, 256), h_out=z(2, 256), x=z(2, 256, t=act), w_pre=z(256, t=act),
+                 w_post=z(256, t=act), gate=z(256))
+        for name, f in kw.items():
+            a[name] = f(a[name])
+        ms.block_residual_norm(d, **a)
+
+    call()
+    torch.cuda.synchronize()
+    half = lambda t: t.half()  # noqa: E731
+    wrong = torch.bfloat16 if dtype == ms.F32 else torch.float32
+    for name in ("y", "h_in", "h_out", "x", "w_pre", "w_post", "gate"):
+        refused([lambda: call(**{name: half})], f"{name}.* must be")
+        refused([lambda: call(**{name: lambda t: t.cpu()})], "on the GPU")
+    for name in ("x", "w_pre", "w_post"):
+        refused([lambda: call(**{name: lambda t: t.to(wrong)})], f"{name}.* must be")
+    for name in ("h_in", "h_out", "gate"):
+        refused([lambda: call(**{name: lambda t: t.bfloat16()})], f"{name}.* must be")
