@@ -69,3 +69,26 @@ def test_one_row_has_no_stride(dtype):
     for r in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(r, results[0]))
     assert torch.equal(results[0][2][0, :2], results[0][2][0, 1:2].expand(2, 64))  # one key: its value
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("window", [1, 40, 70, 128, 300])
+@pytest.mark.parametrize("n_q,D", [(20, 64), (20, 128), (50, 64), (50, 128), (80, 64), (80, 128), (150, 128), (200, 64)])
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.F32, ms.FP8])
+def test_windows_over_every_row_tile(dtype, n_q, D, window, causal):
+    """Row tiles of 64, 128 and 256 and two of 256; windows that begin in either half of a key tile."""
+    s = Setup(dtype, [400, 17, 0, 139], n_q, 1, 2, D, 32, window=window, seed=23)
+    s.check(*s.run(causal), causal)
+
+
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 128), (False, 50)])
+@pytest.mark.parametrize("lengths,n_q,G,D", [([700, 130], 130, 4, 128), ([515, 1, 300], 260, 2, 128), ([1024], 1024, 1, 128),
+                                             ([1500], 1024, 2, 64), ([777], 513, 3, 128)])
+@pytest.mark.parametrize("dtype", [ms.BF16, ms.F32, ms.FP8])
+def test_prompts(dtype, lengths, n_q, G, D, causal, window):
+    """Up to 1024 new tokens and eight row tiles, whole and shared by CTAs."""
+    s = Setup(dtype, lengths, n_q, 1, G, D, 64, window=window, seed=24)
+    out, ls = s.run(causal)
+    s.check(out, ls, causal)
+    o2, l2 = s.run(causal)
+    assert torch.equal(out, o2) and torch.equal(ls, l2)
