@@ -347,10 +347,10 @@ __global__ void __launch_bounds__(Cfg<D, MODE, F8>::kThreads, 1)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const float y0 = __uint_as_float(w[2 * i + j] << 16) * s, y1 = __uint_as_float(w[2 * i + j] & 0xffff0000u) * s;
-                                p[j] = tc::to_e4m3x2(y0, y1);
+                                p[j] = to_e4m3x2(y0, y1);
                                 const uint32_t h2 = tc::e4m3x2_to_f16x2(p[j], 0);
                                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                                q[j] = tc::to_e4m3x2(y0 - f.x, y1 - f.y);
+                                q[j] = to_e4m3x2(y0 - f.x, y1 - f.y);
                             }
                             hi[i] = p[0] | p[1] << 16;
                             lo[i] = q[0] | q[1] << 16;

@@ -90,6 +90,13 @@ __device__ __forceinline__ bool wait_at_least(const int* p, int v, uint64_t limi
     }
 }
 
+// Two values to E4M3, nearest even, saturating; `lo` in the low byte
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Merge of softmax partials (m = max logit, a = its lowest index, s = sum exp(l - m)).
 struct SoftmaxPartial {
     float m;

@@ -37,7 +37,8 @@ struct CopyArgs {
 // consecutive vectors are a token's key heads, then its value heads, so a warp reads and
 // writes whole lines.  A block takes 2 * 256 / (D / 16) vectors: their tokens and requests are
 // found with 32-bit divisions (a wide one only in a launch of more than 2^32 vectors) and from
-// there on with multiplications by reciprocals: j < 2048 + 64, tl < n + 33, so both are exact.
+// there on with multiplications by reciprocals, which give x / d exactly while x (d - 1) < 2^32: j < 2 Hkv + 128
+// (2176 at most), tl < n + 64 (a block has 128 vectors where D = 64, two at least to a token).
 // Both kernels are copies, bound by memory: 32768 tokens of 8 heads of 128 (134 MB of bf16 on
 // one side, 69 MB of codes on the other) are written in 34.7 us and read back in 33.8 us, 5.8
 // and 6.0 TB/s.  Four vectors a thread take 3 and 1 us longer (fewer blocks, a longer tail), one
@@ -98,11 +99,6 @@ __device__ __forceinline__ int kv_exponent(float amax) {
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-__device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ float2 from_e4m3x2(uint16_t w) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
@@ -174,8 +170,7 @@ __global__ void __launch_bounds__(256, DT == MOESTEP_F32 ? 4 : 6) kv_write_kerne
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = to_e4m3x2(x[4 * i] * s, x[4 * i + 1] * s) |
-                   static_cast<uint32_t>(to_e4m3x2(x[4 * i + 2] * s, x[4 * i + 3] * s)) << 16;
+            w[i] = to_e4m3x2(x[4 * i] * s, x[4 * i + 1] * s) | to_e4m3x2(x[4 * i + 2] * s, x[4 * i + 3] * s) << 16;
         uint2* d = reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D) + lane;
         d[0] = make_uint2(w[0], w[1]);
         d[L] = make_uint2(w[2], w[3]);
