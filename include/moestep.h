@@ -325,7 +325,8 @@ int kv_cache_read(const moestep_kv_dims* kd, int R, int n, const int32_t* pos, c
  *   q [R*n_q][Hq][D], rows q_ld elements apart (q_ld >= Hq*D; rows 16-byte aligned)
  *   kv_len [R] int32 in [0, max_pages * page] (others are clamped, MOESTEP_EDEVINPUT)
  *   out [R*n_q][Hq][D]; lse [R*n_q][Hq] fp32 (may be NULL); scale > 0; n_q <= 1024;
- *   window + n_q < 2^31 where the window is shorter than max_pages * page
+ *   window + n_q < 2^31 where the window is shorter than max_pages * page; out and lse overlap
+ *   neither q nor the cache
  * Products accumulate in fp32; the softmax weights are rounded to bf16 before they
  * multiply V, except with MOESTEP_F32.  MOESTEP_FP8: a query row enters as the sum of two
  * E4M3 values an element times a power of two, exact but for elements below 1/896 of the

@@ -15,7 +15,7 @@ namespace {
 // Tiles of 16 query rows and 64 keys, 128 threads.  Each thread computes a 2 x 4 block of the
 // tile's scores, the 16 rows' statistics are kept by 8 lanes each, and each thread accumulates
 // 4 rows x (D / 32) columns of the output.  A tile's loads are in flight together, eight pieces a
-// thread of keys and of values, the next tile's page numbers too.  3 requests of 7 tokens, window
+// thread of keys and of values, the next tile's page numbers too (D = 128: 40 bytes spilled).  3 requests of 7 tokens, window
 // 500, 8 heads of 64 over 4: 14 to 17 us, the latency of a tile, of starting up and of the join (0.5 us
 // of bytes).
 constexpr int kRT = 16, kKT = 64, kF32Threads = 128;
@@ -367,7 +367,8 @@ int max_ctas(const moestep_kv_dims& d) { return d.dtype == MOESTEP_F32 ? kAttnMa
 
 // Empty units of a segment (see attn.cuh) of 256 rows and of fewer.  Beginning one inside a CTA takes
 // 12 (bf16) to 17 us (FP8) with 256 rows, a key tile 2 to 2.7.  Against no empty units: 16 blocks of
-// 32 tokens, up to 32768 FP8 positions, 156 -> 131 us, 16 ragged single tokens 33 -> 26 us.
+// 32 tokens, up to 32768 FP8 positions, 156 -> 131 us, 16 ragged single tokens 33 -> 26 us.  (Measured with
+// heads of 128 and row tiles of 32 and 256; the others, and heads of 64, whose tiles cost less, take the same.)
 constexpr int kAhead = 6, kAheadFew = 4;
 
 struct KvLayout {

@@ -20,7 +20,10 @@
 //
 // The maximum m that the weights refer to moves only when a tile's maximum exceeds it by more
 // than 8 (a factor 256, harmless in fp32 sums and bf16 weights): O is then rescaled in tensor
-// memory by the softmax warps, which is rare after the first tiles.
+// memory by the softmax warps, which is rare after the first tiles (a known method).
+//
+// Weights are rounded to bf16 for P V, by 2^-8 at most, because that is the MMA's type; their sum l is of
+// the unrounded ones.  S, m, l and O are fp32.
 //
 // FP8 cache.  Keys are multiplied as they are stored: a query row is scaled by a power of two and
 // split into two E4M3 parts (4 significant bits each, the 8 of a bf16: see the staging), S is the
@@ -37,12 +40,14 @@
 // What bounds it, measured with the join launch (16 query heads of 128 over 2, cold caches; in
 // brackets the copy rate's time for the keys and values): single tokens of 16 ragged requests, up
 // to 8192 positions, 26 us (12.1): starting up 4 us, the beginnings of two segments, eight tiles
-// and the join; tensor pipe 21 % busy.  One token at 131072 FP8 positions 38 us (10.0): 13 tiles
+// and the join; tensor pipe 21 % busy.  One token at 131072 FP8 positions 37 us (10.0): 13 tiles
 // of 2700 cycles, issue slots 54 %.  32 tokens at 16384 positions 25 us (2.5): one beginning, two
-// tiles, 128 KB of parts a CTA and their join.  16 such blocks, up to 32768 FP8 positions, 129 us
+// tiles, 128 KB of parts a CTA and their join.  16 such blocks, up to 32768 FP8 positions, 130 us
 // (24.9; 43.6 by operations at the bf16 rate): 34 tiles of two row tiles, 4500 to 5000 cycles
 // each, issue slots 60 %, tensor pipe 32 %: exponentials, conversions and staging share the issue
-// slots.
+// slots.  (The compiler has 96 registers for all FP8 roles, what 640 threads leave at launch, and with
+// heads of 128 spills 150 to 250 bytes.  By how it allocates them the batch takes 130 or 132 to 137 us, so
+// what is added beside the softmax's loop is measured, not only counted.)
 #include "attn.cuh"
 #include "attn_tc.cuh"
 #include "common.cuh"
@@ -56,7 +61,7 @@ namespace {
 constexpr int kKeys = 128;                        // keys of a tile
 constexpr uint64_t kTeardown = 1000000000ull;     // limit for draining copies and MMAs in flight
 constexpr uint64_t kAbortedTile = 1000000ull;     // for FP8 key tiles whose scales an aborted CTA did not write
-constexpr int kStagger = 4;                       // key tiles of a share whose streams are put out of step
+constexpr int kStagger = 4;                       // key tiles of a share whose streams are put out of step (measured: D = 128)
 constexpr float kSlack = 8.f;                     // how far a tile's maximum may pass m
 
 // MODE 0, 1, 2: row tiles of 32, 64, 128 (one tile, streams on alternate keys); 3: of 256 (two tiles)
@@ -94,7 +99,8 @@ struct Cfg {
 // the keys' factor is 2^(exp - 127) * 2^-17, finite wherever the score is, and the row's is 2^17 times the
 // query's power.  Of a power above kBigQuery, which would take that factor past fp32's range, the rest
 // comes in by a multiplication beside the masking of a partial tile (16 blocks of 32 tokens, up to 32768
-// positions, 129.1 -> 129.8 us; as a branch of its own 134 to 137 us).
+// positions, 129.1 -> 129.8 us; as a branch of its own 134 to 137 us).  The scale's mantissa is among the
+// keys' factors too: see unit_of.
 constexpr float kKeyShift = 0x1p17f, kBigQuery = 0x1p32f;
 __device__ __forceinline__ float key_scale(uint32_t e) {  // of an exponent byte
     return __uint_as_float(e > 17 ? (e - 17) << 23 : 1u << (e + 5));

@@ -6,12 +6,17 @@
 // then key tile, and every CTA takes the same number of them in a row (one more or less): it
 // streams as many key tiles as any other whatever the requests' lengths are.  The lengths are on
 // the device, so every CTA works the division out from kv_len itself (a block-wide scan over the
-// requests; an empty request counts one unit, whose only effect is to write its empty rows).
+// requests; an empty request counts one key tile, whose only effect is to write its empty rows).
 //
 // The units of one (request, head, row tile) are a segment.  Beginning a segment inside a CTA costs
 // about as much as some units (the last one is written out, queries are staged, the pipeline fills
 // again), so each segment counts that many empty units (`ahead`) before its first key tile: CTAs in
 // which segments end and begin get fewer tiles.
+//
+// Every row tile goes through all key tiles that some query of its request sees, also those that none of its
+// own does.  With one row tile (32 tokens of 16 heads over 2) that is nothing; of a causal prompt in several it
+// is up to half of the work, with a window much shorter than the prompt more: 1024 tokens, 8 row tiles,
+// 39 us, with a window of 128, for which 2 or 3 of each row tile's 8 key tiles would do, 39 us too.
 //
 // A segment inside one CTA is written out directly; of one that CTAs share, each leaves its rows'
 // (m, l, o) in a slot of the workspace (a CTA has at most two such: the one it begins in and the
