@@ -351,6 +351,90 @@ int block_residual_norm(const moestep_dims* dims, int T, const void* y, int y_dt
                         const float* gate, long long gate_ld, float res_scale, const float* h_in, float* h_out,
                         const void* w_pre, void* x, float eps, void* stream);
 
+/* Gives the next tokens of R requests their pages and positions, on the GPU.  Request r has
+ * kv_len[r] cached positions and gets n_new[r] <= n more, or gives up its last -n_new[r]
+ * (all of them when it ends).  Free pages stand in a ring: head[1] of them, the first at
+ * ring[head[0]], going round at n_pages.  In the order of the requests, those that grow into new pages
+ * take them from the front, as long as the pages asked for so far, refused ones' included, are
+ * at most head[1]; pages given up in the call go to the ring's end and are not taken in it.  A
+ * request that is refused, or whose positions would pass max_pages * page, stays as it was.
+ *   kv_len, n_new [R] int32, -kv_len[r] <= n_new[r] <= n
+ *   ring [n_pages] int32 (in/out); head [2] int32; head_out [2] (may be head)
+ *   table [R][max_pages] int32 (in/out): entries of new pages are written; those of pages given
+ *   up keep their old values
+ *   new_len [R] (not kv_len or n_new): kv_len + n_new, or kv_len of a request that was refused
+ *   pos [R][n]: positions kv_len[r] .. of the new tokens, -1 behind them, as kv_cache_write takes them
+ *   slots [R][n] (may be NULL): page * dims.page + place in the page of each, -1 behind them
+ * Lengths, counts or pages out of range are recorded (MOESTEP_EDEVINPUT) and not followed: such a request
+ * is refused, a page out of range enters the table as -1, pages beyond the ring's n_pages are dropped. */
+int kv_cache_plan(const moestep_kv_dims* kd, int R, int n, const int32_t* kv_len, const int32_t* n_new, int32_t* ring,
+                  const int32_t* head, int32_t* head_out, int32_t* table, int32_t* new_len, int32_t* pos,
+                  int32_t* slots, void* ws, size_t ws_bytes, void* stream);
+
+/* Frequencies of rotary positions: pair i of rot / 2 turns f_i = base^(-2 i / rot) radians a position.
+ * For contexts longer than the `original` one, f is replaced by f s + (f / factor) (1 - s):
+ *   MOESTEP_ROTARY_PLAIN       s = 1 (factor, original, low, high are not used)
+ *   MOESTEP_ROTARY_LINEAR      s = 0 (all positions are divided by the factor)
+ *   MOESTEP_ROTARY_ROTATIONS   s = (original f / 2 pi - low) / (high - low), within [0, 1]: pairs of
+ *                              `high` turns and more within the original context keep their frequency
+ *   MOESTEP_ROTARY_DIMENSIONS  s = 1 - (i - a) / (b - a), within [0, 1], a and b the indexes of the pairs that
+ *                              turn `high` and `low` times, rounded down and up, within [0, rot - 1]
+ * freq [rot / 2] uint64 (device): the fraction of a turn a position, times 2^64.  A program may fill
+ * it with frequencies of its own.  base > 1, rot even and at most 4096, 0 < low < high. */
+#define MOESTEP_ROTARY_PLAIN 0
+#define MOESTEP_ROTARY_LINEAR 1
+#define MOESTEP_ROTARY_ROTATIONS 2
+#define MOESTEP_ROTARY_DIMENSIONS 3
+int rotary_frequencies(int rot, double base, int scaling, double factor, double original, double low, double high,
+                       uint64_t* freq, void* stream);
+
+/* Turns the first rot of the D elements of every query and key head by its token's position:
+ *   (x0, x1) -> mscale * (x0 cos t - x1 sin t, x1 cos t + x0 sin t),  t = pos * f_i,
+ * for the pairs (x_i, x_{i + rot/2}), with pairs != 0 (x_{2i}, x_{2i+1}); the other elements are copied.
+ * The angle is reduced exactly at any position; one rounding to the element type.
+ *   q [R*n][Hq][D], k [R*n][Hkv][D], rows *_ld elements apart (either may be NULL, with its output)
+ *   pos [R][n] int32; rows of a negative position are left as they were
+ *   q_out, k_out: may be q and k themselves, with the same row distance, else apart from both
+ * Rows aligned to 16 bytes and rot / 2 (pairs: rot) a multiple of 8 (fp32: 4) are the fast case; others work. */
+int block_rotary(const moestep_kv_dims* kd, int R, int n, const void* q, long long q_ld, const void* k, long long k_ld,
+                 const int32_t* pos, const uint64_t* freq, int rot, int pairs, float mscale, void* q_out,
+                 long long qo_ld, void* k_out, long long ko_ld, void* stream);
+
+/* The gated delta rule: a token mixer whose history is one matrix a head instead of a cache.
+ * Supported: Dk and Dv 64 or 128, Hv a multiple of Hk, Hv <= 1024; dtype MOESTEP_BF16 or MOESTEP_F32 is that of
+ * queries, keys, values and outputs (states are fp32 always). */
+typedef struct {
+    int Hk;      /* heads of queries and keys; value head i uses head i / (Hv / Hk) */
+    int Hv;      /* heads of values, states and outputs */
+    int Dk;      /* size of a query or key */
+    int Dv;      /* size of a value */
+    int n_slots; /* states in the pool */
+    int dtype;   /* MOESTEP_BF16 or MOESTEP_F32 */
+} moestep_delta_dims;
+
+/* Bytes of workspace for block_delta_rule with R requests of up to n tokens. */
+int moestep_delta_workspace_size(const moestep_delta_dims* dd, int R, int n, size_t* bytes);
+
+/* For each request, its tokens in order, and each value head:
+ *   S <- e^g S + beta k (v - e^g S^T k)^T,   out = scale * S^T q
+ *   q, k [R*n][Hk][Dk], v [R*n][Hv][Dv], rows *_ld elements apart (16-byte aligned)
+ *   qk_eps > 0: q and k are divided by sqrt(|.|^2 + qk_eps) first; 0: taken as they are
+ *   g, beta [R*n][Hv] fp32; g <= 0 is the logarithm of the decay (-inf: the history is dropped)
+ *   length [R] int32 in [0, n]: tokens of each request (NULL: n); rows of out behind them are left as they were
+ *   slot [R] int32: the request's state (NULL: slot r); negative: the request is skipped.  Slots of a call that
+ *   writes states must differ
+ *   fresh [R] uint8: non-zero, the request begins with S = 0, whatever its slot holds (NULL: none does)
+ *   state [n_slots][Hv][Dv][Dk] fp32 (S transposed); state_out: where the states after the tokens go, in the
+ *   same slots; may be state itself, NULL: not wanted (a block that is not resolved yet leaves its history)
+ *   out [R*n][Hv][Dv]
+ * Lengths and slots out of range are recorded (MOESTEP_EDEVINPUT) and the request is skipped.  Sums and states
+ * are fp32; results do not depend on timing.  A non-finite value may reach every output of its head's request
+ * from 63 tokens before its own on. */
+int block_delta_rule(const moestep_delta_dims* dd, int R, int n, const void* q, long long q_ld, const void* k,
+                     long long k_ld, const void* v, long long v_ld, const float* g, const float* beta,
+                     const int32_t* length, const int32_t* slot, const uint8_t* fresh, const float* state,
+                     float* state_out, float scale, float qk_eps, void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronously reads and clears the workspace's device error word (host *word:
  * 0 or a MOESTEP_E* code).  Waits for `stream`. */
 int moestep_read_device_error(void* ws, size_t ws_bytes, void* stream, int* word);

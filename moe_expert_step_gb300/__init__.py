@@ -17,6 +17,8 @@ BF16 = 0
 F32 = 1
 FP8 = 2
 
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_ROTATIONS, ROTARY_DIMENSIONS = 0, 1, 2, 3
+
 OK = 0
 EINVAL = -1
 EWORKSPACE = -2
@@ -37,6 +39,7 @@ EXPORTS = [
     "moestep_set_wait_timeout_ns", "moestep_set_route_fusion", "moestep_route_fusion", "moestep_launch_count",
     "moe_block_route_noalloc",
     "moestep_kv_workspace_size", "kv_cache_write", "kv_cache_read", "block_attention", "block_residual_norm",
+    "kv_cache_plan", "rotary_frequencies", "block_rotary", "moestep_delta_workspace_size", "block_delta_rule",
 ]
 
 
@@ -70,6 +73,10 @@ class KvCache(ctypes.Structure):
     _holds = None  # of the tensors (kv_cache): type, Hkv, page, D, max_pages
 
 
+class DeltaDimsC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("Hk", "Hv", "Dk", "Dv", "n_slots", "dtype")]
+
+
 _LIB = None
 
 
@@ -87,6 +94,7 @@ def lib():
         vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
         D = ctypes.POINTER(Dims)
         ll, KD, KC = ctypes.c_longlong, ctypes.POINTER(KvDimsC), ctypes.POINTER(KvCache)
+        f64, DD = ctypes.c_double, ctypes.POINTER(DeltaDimsC)
         sig = {
             "moestep_workspace_size": [D, i, ctypes.POINTER(sz)],
             "moestep_workspace_init": [vp, sz, vp],
@@ -115,6 +123,11 @@ def lib():
             "kv_cache_read": [KD, i, i, vp, KC, vp, vp, vp, sz, vp],
             "block_attention": [KD, i, i, vp, ll, vp, KC, f, i, i, vp, vp, vp, sz, vp],
             "block_residual_norm": [D, i, vp, i, vp, vp, ll, f, vp, vp, vp, vp, f, vp],
+            "kv_cache_plan": [KD, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+            "rotary_frequencies": [i, f64, i, f64, f64, f64, f64, vp, vp],
+            "block_rotary": [KD, i, i, vp, ll, vp, ll, vp, vp, i, i, f, vp, ll, vp, ll, vp],
+            "moestep_delta_workspace_size": [DD, i, i, ctypes.POINTER(sz)],
+            "block_delta_rule": [DD, i, i, vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, vp, vp, vp, f, f, vp, vp, sz, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -347,7 +360,8 @@ _ACT = {}  # torch types of the activations of each dtype and of the integers (t
 def _types() -> dict:
     if not _ACT:
         import torch
-        _ACT.update({BF16: torch.bfloat16, FP8: torch.bfloat16, F32: torch.float32, "int": torch.int32})
+        _ACT.update({BF16: torch.bfloat16, FP8: torch.bfloat16, F32: torch.float32, "int": torch.int32, "turn": torch.int64,
+                     "byte": torch.uint8})
     return _ACT
 
 
@@ -441,6 +455,157 @@ def block_residual_norm(d: ModelDims, y, h_in, h_out, x, w_pre=None, w_post=None
     _check(lib().block_residual_norm(ctypes.byref(d.c()), T, y.data_ptr(), F32 if y.dtype is f32 else BF16, _p(w_post),
                                      _p(gate), gate_ld, res_scale, h_in.data_ptr(), h_out.data_ptr(), _p(w_pre),
                                      _p(x), eps, _s(stream)), "block_residual_norm")
+
+
+# ------------------------------------------------------------------------------ pages, positions, the delta rule
+
+
+def kv_cache_plan(kd: KvDims, R: int, kv_len, n_new, ring, head, head_out, table, new_len, pos, ws, slots=None,
+                  stream=None) -> None:
+    """Give R requests pages and positions for n_new [R] more tokens each (negative: the last -n_new go): pages from
+    the ring of free ones [n_pages] with head [2] = (first, count), or back to it; the tables [R, max_pages] are
+    extended, pos [R, n] (-1 behind the new tokens), slots [R, n] and new_len [R] are written.  All int32; see
+    kv_cache_plan in moestep.h."""
+    n, i32 = pos.shape[-1], _types()["int"]
+    for t, shape, what in ((kv_len, (R,), "kv_len"), (n_new, (R,), "n_new"), (new_len, (R,), "new_len"),
+                           (ring, (kd.n_pages,), "ring"), (head, (2,), "head"), (head_out, (2,), "head_out"),
+                           (pos, (R, n), "pos")):
+        _dense(t, shape, i32, "kv_cache_plan: " + what)
+    if table.dim() != 2 or table.shape[0] < R:
+        raise MoeStepError(EINVAL, "kv_cache_plan: table must have a row a request")
+    _dense(table, (table.shape[0], kd.max_pages), i32, "kv_cache_plan: table")
+    if slots is not None:
+        _dense(slots, (R, n), i32, "kv_cache_plan: slots")
+    _on_gpu(ws, "kv_cache_plan")
+    _check(lib().kv_cache_plan(kd._c, R, n, kv_len.data_ptr(), n_new.data_ptr(), ring.data_ptr(), head.data_ptr(),
+                               head_out.data_ptr(), table.data_ptr(), new_len.data_ptr(), pos.data_ptr(), _p(slots),
+                               ws.data_ptr(), ws.numel(), _s(stream)), "kv_cache_plan")
+
+
+def _on_gpu(ws, what: str) -> None:
+    if not ws.is_cuda or not ws.is_contiguous() or ws.element_size() != 1:
+        raise MoeStepError(EINVAL, f"{what}: ws must be bytes on the GPU")
+
+
+def rotary_frequencies(rot: int, base: float, scaling: int = ROTARY_PLAIN, factor: float = 1.0, original: float = 1.0,
+                       low: float = 1.0, high: float = 2.0, device="cuda", stream=None):
+    """Table for block_rotary, [rot / 2] int64 holding the bits of uint64: the fraction of a turn that each pair makes
+    a position, times 2^64.  Pairs turn base^(-2 i / rot) radians, or less where that is scaled for a context longer
+    than the `original` one (ROTARY_*); see rotary_frequencies in moestep.h."""
+    import torch
+    if int(rot) != rot or rot <= 0 or rot % 2:
+        raise MoeStepError(EINVAL, "rotary_frequencies: rot must be even and positive")
+    freq = torch.empty(int(rot) // 2, dtype=torch.int64, device=device)
+    _check(lib().rotary_frequencies(int(rot), base, scaling, factor, original, low, high, freq.data_ptr(), _s(stream)),
+           "rotary_frequencies")
+    return freq
+
+
+def _rotary_rows(x, heads: int, kd: KvDims, T: int, what: str):
+    """Pointer and row distance of x [T, heads, D] (None: absent)."""
+    if x is None:
+        return None, 0
+    ld = _rows(x, heads, kd, what)
+    if x.shape[0] != T:
+        raise MoeStepError(EINVAL, f"{what} must have a row a position")
+    return x.data_ptr(), ld
+
+
+def block_rotary(kd: KvDims, q, k, pos, freq, q_out, k_out, interleaved: bool = False, mscale: float = 1.0,
+                 stream=None) -> None:
+    """Turn the first 2 * len(freq) of the D elements of q [R * n, Hq, D] and k [R * n, Hkv, D] (either may be None;
+    rows may be parts of wider rows) by the positions pos [R, n] (negative: the row is left) into q_out, k_out,
+    which may be q and k themselves.  freq: of rotary_frequencies; pairs are halves of the rotated part apart, or
+    neighbours where interleaved; see block_rotary in moestep.h."""
+    types = _types()
+    if pos.dim() != 2:
+        raise MoeStepError(EINVAL, "block_rotary: pos must be [R, n]")
+    R, n = pos.shape
+    _dense(pos, (R, n), types["int"], "block_rotary: pos")
+    _dense(freq, freq.shape, types["turn"], "block_rotary: freq")
+    qp, q_ld = _rotary_rows(q, kd.Hq, kd, R * n, "block_rotary: q")
+    kp, k_ld = _rotary_rows(k, kd.Hkv, kd, R * n, "block_rotary: k")
+    qo, qo_ld = _rotary_rows(q_out, kd.Hq, kd, R * n, "block_rotary: q_out")
+    ko, ko_ld = _rotary_rows(k_out, kd.Hkv, kd, R * n, "block_rotary: k_out")
+    _check(lib().block_rotary(kd._c, R, n, qp, q_ld, kp, k_ld, pos.data_ptr(), freq.data_ptr(), 2 * freq.numel(),
+                              int(interleaved), mscale, qo, qo_ld, ko, ko_ld, _s(stream)), "block_rotary")
+
+
+@dataclass(frozen=True)
+class DeltaDims:
+    """Shape of a layer of the gated delta rule and of its pool of states (moestep_delta_dims)."""
+    Hk: int
+    Hv: int
+    Dk: int
+    Dv: int
+    n_slots: int
+    dtype: int = BF16
+
+    def __post_init__(self):
+        c = DeltaDimsC(self.Hk, self.Hv, self.Dk, self.Dv, self.n_slots, self.dtype)
+        object.__setattr__(self, "_c", ctypes.byref(c))
+
+    def __reduce__(self):
+        return DeltaDims, (self.Hk, self.Hv, self.Dk, self.Dv, self.n_slots, self.dtype)
+
+
+def delta_workspace_size(dd: DeltaDims, R: int, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().moestep_delta_workspace_size(dd._c, R, n, ctypes.byref(out)), "moestep_delta_workspace_size")
+    return out.value
+
+
+def delta_workspace(dd: DeltaDims, R: int, n: int, device="cuda", stream=None):
+    """Allocate (through torch) and initialise a workspace for block_delta_rule."""
+    import torch
+    ws = torch.empty(delta_workspace_size(dd, R, n), dtype=torch.uint8, device=device)
+    workspace_init(ws, stream)
+    return ws
+
+
+def _head_rows(t, T: int, heads: int, D: int, dtype, what: str) -> int:
+    """Distance between the rows of t [T, heads, D], which may be part of a wider row."""
+    st, shape = t.stride(), t.shape
+    if (len(st) != 3 or shape[0] != T or shape[1] != heads or shape[2] != D or st[2] != 1
+            or (heads > 1 and st[1] != D) or t.dtype is not dtype):
+        raise MoeStepError(EINVAL, f"{what} must be [{T}, {heads}, {D}] in the activations' type, heads dense")
+    if not t.is_cuda:
+        raise MoeStepError(EINVAL, f"{what} must be on the GPU")
+    return st[0] if T > 1 else heads * D
+
+
+def block_delta_rule(dd: DeltaDims, R: int, q, k, v, g, beta, state, out, ws, state_out=None, slot=None, length=None,
+                     fresh=None, scale: float = 1.0, qk_eps: float = 0.0, stream=None) -> None:
+    """The gated delta rule over the tokens of R requests: q, k [R * n, Hk, Dk] and v [R * n, Hv, Dv] (rows may be
+    parts of wider rows), g (logarithm of the decay) and beta [R * n, Hv] fp32, state [n_slots, Hv, Dv, Dk] fp32 with
+    the request's slot [R], out [R * n, Hv, Dv].  state_out: where the new states go (state itself, or None: not
+    wanted); length [R]: tokens of each; fresh [R] uint8: begin from nothing; see block_delta_rule in moestep.h."""
+    T, types = q.shape[0], _types()
+    n = T // R if R > 0 else 0
+    if R * n != T:
+        raise MoeStepError(EINVAL, "block_delta_rule: q must have R * n rows")
+    act = types.get(dd.dtype) if dd.dtype != FP8 else None
+    q_ld = _head_rows(q, T, dd.Hk, dd.Dk, act, "block_delta_rule: q")
+    k_ld = _head_rows(k, T, dd.Hk, dd.Dk, act, "block_delta_rule: k")
+    v_ld = _head_rows(v, T, dd.Hv, dd.Dv, act, "block_delta_rule: v")
+    f32, pool = types[F32], (dd.n_slots, dd.Hv, dd.Dv, dd.Dk)
+    _dense(g, (T, dd.Hv), f32, "block_delta_rule: g")
+    _dense(beta, (T, dd.Hv), f32, "block_delta_rule: beta")
+    _dense(state, pool, f32, "block_delta_rule: state")
+    _dense(out, (T, dd.Hv, dd.Dv), act, "block_delta_rule: out")
+    if state_out is not None:
+        _dense(state_out, pool, f32, "block_delta_rule: state_out")
+    if slot is not None:
+        _dense(slot, (R,), types["int"], "block_delta_rule: slot")
+    if length is not None:
+        _dense(length, (R,), types["int"], "block_delta_rule: length")
+    if fresh is not None:
+        _dense(fresh, (R,), types["byte"], "block_delta_rule: fresh")
+    _on_gpu(ws, "block_delta_rule")
+    _check(lib().block_delta_rule(dd._c, R, n, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                                  g.data_ptr(), beta.data_ptr(), _p(length), _p(slot), _p(fresh), state.data_ptr(),
+                                  _p(state_out), scale, qk_eps, out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                  _s(stream)), "block_delta_rule")
 
 
 def read_device_error(ws, stream=None) -> int:

@@ -1,0 +1,313 @@
+// Pages and positions of a batch's next tokens, given out on the GPU: requests take pages from
+// the front of a ring of free pages or return them to its end, their page tables are extended,
+// and every new token gets its position and its slot in the pool.
+//
+// A first-in-first-out ring, not a stack: pages taken are read from [first, first + count) and
+// pages returned are written from first + count on, places that never meet while the pool's pages
+// are distinct, so blocks need no order among themselves.  Where a request's pages begin in
+// the ring is a sum over the requests before it.  Every block adds those up by itself (a few
+// loads a thread from L2 for the batches of serving) instead of waiting for a launch that does.
+// The header is written by the block that finishes last, so it may be updated in place.
+#include "common.cuh"
+#include "kernels.h"
+#include "kv.h"
+#include "launch.cuh"
+
+namespace moestep {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTicket = 64;  // word of the workspace's header that counts finished blocks
+
+struct PlanArgs {
+    const int32_t* kv_len;
+    const int32_t* n_new;
+    int32_t* ring;
+    const int32_t* head;
+    int32_t* head_out;
+    int32_t* table;
+    int32_t* new_len;
+    int32_t* pos;
+    int32_t* slots;
+    int* err;
+    int* ticket;
+    int R, n, page_log2, n_pages, max_pages;
+    int rows;      // requests of a block
+    int segments;  // or, where that is 1, blocks of a request
+    int wide;      // pos and slots can be written four at a time
+};
+
+// What a request asks for
+struct Ask {
+    int len, m, held, need;
+    bool bad, fits;
+    __device__ __forceinline__ int grow() const { return fits ? max(need - held, 0) : 0; }
+    __device__ __forceinline__ int drop() const { return max(held - need, 0); }
+};
+__device__ __forceinline__ Ask ask_of(const PlanArgs& a, int r) {
+    Ask q;
+    q.len = __ldg(&a.kv_len[r]);
+    q.m = __ldg(&a.n_new[r]);
+    const int cap = a.max_pages << a.page_log2, up = (1 << a.page_log2) - 1;
+    q.bad = q.len < 0 || q.len > cap || q.m > a.n || q.m < -q.len;
+    if (q.bad) q.m = 0;
+    const int len = q.bad ? 0 : q.len;
+    q.held = (len + up) >> a.page_log2;
+    q.fits = !q.bad && q.m <= cap - len;
+    q.need = q.fits ? (len + q.m + up) >> a.page_log2 : q.held;
+    return q;
+}
+
+struct Sums {
+    long long grow, drop;
+};
+
+// Sums over the block, in all threads; `sm` is free again after the call's second barrier
+__device__ __forceinline__ Sums block_sums(Sums v, Sums* sm) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        v.grow += __shfl_xor_sync(0xffffffffu, v.grow, o);
+        v.drop += __shfl_xor_sync(0xffffffffu, v.drop, o);
+    }
+    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = sm[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) v.grow += sm[w].grow, v.drop += sm[w].drop;
+    __syncthreads();
+    return v;
+}
+
+// Sums over the threads before this one
+__device__ __forceinline__ Sums block_before(Sums v, Sums* sm) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    Sums run = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long g = __shfl_up_sync(0xffffffffu, run.grow, o), d = __shfl_up_sync(0xffffffffu, run.drop, o);
+        if (lane >= o) run.grow += g, run.drop += d;
+    }
+    if (lane == 31) sm[warp] = run;
+    __syncthreads();
+    Sums out{run.grow - v.grow, run.drop - v.drop};
+    for (int w = 0; w < warp; ++w) out.grow += sm[w].grow, out.drop += sm[w].drop;
+    __syncthreads();
+    return out;
+}
+
+__device__ __forceinline__ Sums sums_of(const PlanArgs& a, int first, int last) {
+    Sums s{0, 0};
+    for (int r = first + threadIdx.x; r < last; r += kThreads) {
+        const Ask q = ask_of(a, r);
+        s.grow += q.grow();
+        s.drop += q.drop();
+    }
+    return s;
+}
+
+struct Row {
+    int len, m, held, need;
+    long long take, back;  // pages that the requests before it take and return
+    bool served;
+};
+
+__global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
+    __shared__ Sums sm[kThreads / 32];
+    __shared__ Row rows[kThreads];
+    __shared__ bool last;
+    pdl_trigger();
+    pdl_wait();
+    int first = a.head[0], count = a.head[1];  // (written below by the last block, after every block has read them)
+    const bool broken = static_cast<unsigned>(first) >= static_cast<unsigned>(a.n_pages) ||
+                        static_cast<unsigned>(count) > static_cast<unsigned>(a.n_pages);
+    if (broken) first = 0, count = 0;
+    if (broken && threadIdx.x == 0) record_error(a.err, kErrBadInput);
+
+    const int r0 = blockIdx.x / a.segments * a.rows, segment = blockIdx.x % a.segments;
+    const int n_rows = min(a.rows, a.R - r0);
+    const Sums before = block_sums(sums_of(a, 0, r0), sm);
+    {
+        Ask q{};
+        Sums mine{0, 0};
+        const bool on = threadIdx.x < n_rows;
+        if (on) {
+            q = ask_of(a, r0 + threadIdx.x);
+            mine = Sums{q.grow(), q.drop()};
+        }
+        const Sums ahead = block_before(mine, sm);
+        if (on) {
+            Row w{q.len, q.m, q.held, q.need, before.grow + ahead.grow, before.drop + ahead.drop, false};
+            w.served = q.fits && (mine.grow == 0 || w.take + mine.grow <= count);
+            if (broken) w.served = q.fits && q.need == q.held;
+            if (!w.served) w.m = 0, w.need = w.held;
+            rows[threadIdx.x] = w;
+            if (segment == 0) {
+                if (q.bad) record_error(a.err, kErrBadInput);
+                a.new_len[r0 + threadIdx.x] = q.len + w.m;
+            }
+        }
+    }
+    __syncthreads();
+
+    const long long ring = a.n_pages;
+    auto page_at = [&](const Row& w, int i) {  // table entry i >= held of a served request
+        const int id = a.ring[(first + w.take + (i - w.held)) % ring];
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages)) return id;
+        record_error(a.err, kErrBadInput);
+        return -1;
+    };
+    const int step = a.segments * kThreads;
+    for (int j = 0; j < n_rows; ++j) {  // table entries that are new, pages that go back
+        const Row& w = rows[j];
+        int32_t* table = a.table + static_cast<long long>(r0 + j) * a.max_pages;
+        const int t0 = segment * kThreads + threadIdx.x;
+        for (int i = w.held + t0; i < w.need; i += step) table[i] = page_at(w, i);
+        for (int i = w.need + t0; i < w.held; i += step) {
+            const long long o = count + w.back + (i - w.need);
+            const int id = table[i];
+            if (o < ring) a.ring[(first + o) % ring] = id;  // (else more pages than the pool has)
+            if (o >= ring || static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_pages))
+                record_error(a.err, kErrBadInput);
+        }
+    }
+
+    const int mask = (1 << a.page_log2) - 1;
+    auto place = [&](const Row& w, const int32_t* table, int i, int& p, int& slot) {
+        p = slot = -1;
+        if (i >= w.m) return;
+        p = w.len + i;
+        const int pg = p >> a.page_log2;
+        const int id = pg < w.held ? __ldcg(&table[pg]) : page_at(w, pg);
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages))
+            slot = (id << a.page_log2) + (p & mask);
+        else
+            record_error(a.err, kErrBadInput);
+    };
+    if (a.wide) {
+        const int quads = a.n / 4, total = n_rows * quads;
+        for (int k = segment * kThreads + threadIdx.x; k < total; k += step) {
+            const int j = k / quads, i = 4 * (k - j * quads);
+            const Row& w = rows[j];
+            const long long at = static_cast<long long>(r0 + j) * a.n + i;
+            const int32_t* table = a.table + static_cast<long long>(r0 + j) * a.max_pages;
+            int4 p, s;
+            place(w, table, i, p.x, s.x);
+            place(w, table, i + 1, p.y, s.y);
+            place(w, table, i + 2, p.z, s.z);
+            place(w, table, i + 3, p.w, s.w);
+            *reinterpret_cast<int4*>(a.pos + at) = p;
+            if (a.slots) *reinterpret_cast<int4*>(a.slots + at) = s;
+        }
+    } else {
+        const long long total = static_cast<long long>(n_rows) * a.n;
+        for (long long k = segment * kThreads + threadIdx.x; k < total; k += step) {
+            const int j = static_cast<int>(k / a.n), i = static_cast<int>(k - static_cast<long long>(j) * a.n);
+            int p, s;
+            place(rows[j], a.table + static_cast<long long>(r0 + j) * a.max_pages, i, p, s);
+            const long long at = static_cast<long long>(r0) * a.n + k;
+            a.pos[at] = p;
+            if (a.slots) a.slots[at] = s;
+        }
+    }
+
+    // the header, by the block that ends last (the ticket wraps to 0 for the next call)
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last = true;
+        if (gridDim.x > 1) {
+            __threadfence();
+            last = atomicInc(reinterpret_cast<unsigned*>(a.ticket), gridDim.x - 1) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!last) return;
+    Sums run{0, 0};
+    long long taken = 0;
+    for (int r = 0; r < a.R; r += kThreads) {
+        Sums mine{0, 0};
+        if (r + threadIdx.x < a.R) {
+            const Ask q = ask_of(a, r + threadIdx.x);
+            mine = Sums{q.grow(), q.drop()};
+        }
+        const Sums ahead = block_before(mine, sm);
+        const long long upto = run.grow + ahead.grow + mine.grow;
+        if (mine.grow > 0 && upto <= count) taken = upto;
+        const Sums all = block_sums(mine, sm);
+        run.grow += all.grow;
+        run.drop += all.drop;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
+    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32].grow = taken;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / 32; ++w) taken = max(taken, sm[w].grow);
+        if (broken) {
+            a.head_out[0] = a.head[0];
+            a.head_out[1] = a.head[1];
+        } else {
+            const long long most = ring - count;  // what did not fit was not written
+            a.head_out[0] = static_cast<int>((first + taken) % ring);
+            a.head_out[1] = static_cast<int>(count - taken + min(run.drop, most));
+        }
+    }
+}
+
+}  // namespace
+}  // namespace moestep
+
+extern "C" int kv_cache_plan(const moestep_kv_dims* kd, int R, int n, const int32_t* kv_len, const int32_t* n_new,
+                             int32_t* ring, const int32_t* head, int32_t* head_out, int32_t* table, int32_t* new_len,
+                             int32_t* pos, int32_t* slots, void* ws, size_t ws_bytes, void* stream) {
+    using namespace moestep;
+    int rc = check_kv_dims(kd);
+    if (rc != MOESTEP_OK) return rc;
+    if (R <= 0 || n <= 0) return MOESTEP_EINVAL;
+    if (!kv_len || !n_new || !ring || !head || !head_out || !table || !new_len || !pos) return MOESTEP_EINVAL;
+    // blocks read every request's lengths while others write theirs
+    if (new_len == kv_len || new_len == n_new) return MOESTEP_EINVAL;
+    for (const void* p : {static_cast<const void*>(kv_len), static_cast<const void*>(n_new),
+                          static_cast<const void*>(ring), static_cast<const void*>(head),
+                          static_cast<const void*>(head_out), static_cast<const void*>(table),
+                          static_cast<const void*>(new_len), static_cast<const void*>(pos),
+                          static_cast<const void*>(slots)})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return MOESTEP_EALIGN;
+    if (R > (1 << 20)) return MOESTEP_EUNSUPPORTED;
+    if ((rc = check_kv_ws(ws, ws_bytes, kKvHeader)) != MOESTEP_OK) return rc;
+    if ((rc = device_ok(nullptr)) != MOESTEP_OK) return rc;
+    PlanArgs a{};
+    a.kv_len = kv_len;
+    a.n_new = n_new;
+    a.ring = ring;
+    a.head = head;
+    a.head_out = head_out;
+    a.table = table;
+    a.new_len = new_len;
+    a.pos = pos;
+    a.slots = slots;
+    a.err = static_cast<int*>(ws);
+    a.ticket = static_cast<int*>(ws) + kTicket;
+    a.R = R;
+    a.n = n;
+    a.page_log2 = kd->page == 16 ? 4 : kd->page == 32 ? 5 : kd->page == 64 ? 6 : 7;
+    a.n_pages = kd->n_pages;
+    a.max_pages = kd->max_pages;
+    a.wide = n % 4 == 0 && kv_aligned16(pos) && (!slots || kv_aligned16(slots));
+    // a block writes about 4096 positions
+    constexpr int kEntries = 4096;
+    a.rows = n >= kEntries ? 1 : kEntries / n < kThreads ? kEntries / n : kThreads;
+    if (a.rows > R) a.rows = R;
+    a.segments = a.rows > 1 ? 1 : (n + kEntries - 1) / kEntries;
+    const long long grid = 1ll * ((R + a.rows - 1) / a.rows) * a.segments;
+    if (grid > (1ll << 31) - 1) return MOESTEP_EUNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    prof_begin(8, s);
+    const cudaError_t e = launch_pdl(kv_plan_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
+    prof_end(8, s);
+    if (e != cudaSuccess) {
+        set_last_cuda(static_cast<int>(e));
+        return MOESTEP_ECUDA;
+    }
+    count_launch();
+    return MOESTEP_OK;
+}
