@@ -149,7 +149,7 @@ int check_delta(const moestep_delta_dims* dd, int R, int n) {
     if (rc != MOESTEP_OK) return rc;
     if (R <= 0 || n <= 0) return MOESTEP_EINVAL;
     if (1ll * R * dd->Hv > (1 << 24)) return MOESTEP_EUNSUPPORTED;
-    if (1ll * R * n > (1ll << 31) - 1) return MOESTEP_EUNSUPPORTED;
+    if (1ll * R * n > (1ll << 31) - 1 || (1ll * R * n + 64ll * R) * dd->Hk > 64 * ((1ll << 31) - 1)) return MOESTEP_EUNSUPPORTED;
     return MOESTEP_OK;
 }
 
@@ -198,7 +198,8 @@ extern "C" int block_delta_rule(const moestep_delta_dims* dd, int R, int n, cons
                       dd->Dk,    dd->Dv,    dd->n_slots, scale, qk_eps,    wait_timeout_ns()};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_begin(8, s);
-    const cudaError_t e = launch_delta_recurrent(a, dd->dtype, s);
+    const cudaError_t e = delta_chunked(*dd, R, n) ? launch_delta_chunks(a, static_cast<char*>(ws) + kKvHeader, sms, s)
+                                                   : launch_delta_recurrent(a, dd->dtype, s);
     prof_end(8, s);
     if (e != cudaSuccess) {
         set_last_cuda(static_cast<int>(e));
@@ -207,8 +208,3 @@ extern "C" int block_delta_rule(const moestep_delta_dims* dd, int R, int n, cons
     count_launch();
     return MOESTEP_OK;
 }
-
-namespace moestep {
-bool delta_chunked(const moestep_delta_dims&, int, int) { return false; }
-size_t delta_chunk_bytes(const moestep_delta_dims&, int, int) { return 0; }
-}  // namespace moestep
