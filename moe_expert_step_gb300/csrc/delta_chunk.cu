@@ -33,11 +33,11 @@ namespace moestep {
 namespace {
 
 constexpr int C = 64;             // tokens of a chunk
-constexpr int kSquare = C * C * 2;  // bytes of a 64 x 64 f16 tile
-constexpr int kVec = 2048;        // bytes of a chunk's factors
-constexpr int kHeadBytes = 3 * kSquare + kVec;  // X high, X low, P, factors of one value head
-// factors of a token (float [8][64])
-enum { kA, kBeta, kB, kD, kTau, kPi, kGamma };
+// X and P are lower triangular: of their 16 x 16 blocks (f16, 512 bytes) the ten on and below the diagonal are kept, row by row
+constexpr int kTri = 10 * 512;
+constexpr int kHeadBytes = 3 * kTri + 6 * C * 4;  // X high, X low, P, factors of one value head
+// factors of a token, [6][64] floats
+enum { kA, kBeta, kB, kD, kPi, kGamma };
 
 template <int DK>
 struct Tile {
@@ -110,17 +110,129 @@ __device__ __forceinline__ float quad_max(float x) {
 // byte offset of 16-byte piece c of row r in a tile of 128-byte rows
 __device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
+// the same of row r of block (bi, bj) of a lower triangle; of one without its diagonal
+__device__ __forceinline__ int tri(int bi, int bj, int r, int c) {
+    return (bi * (bi + 1) / 2 + bj) * 512 + r * 32 + ((c ^ (r >> 2 & 1)) << 4);
+}
+__device__ __forceinline__ int below(int bi, int bj, int r, int c) { return tri(bi - 1, bj, r, c); }
+
 // ---------------------------------------------------------------- first launch: X and P of every chunk
-// A block has one chunk of one key head, four warps with 16 tokens each for the products k.k and q.k.  The inverse of
-// I + A of a value head is 64 columns that 64 threads find by elimination, each holding its column in registers.
+// A block has one chunk of one key head, four warps with 16 tokens each for the products k.k and q.k.
+//
+// Rows of keys are brought to [1, 2) by a power of two and their norms left out: with c_i the factor between key and row,
+// the system is solved for U' = c U, whose matrix A'_ij = beta_i c_i^2 e^(G_i - G_j) k_i.k_j has entries of the size of 1
+// whatever the keys' scale (up to 23 for normalised ones, as long as beta |k|^2 <= 2 without).
+//
+// X = (I + A')^-1 of a value head by a pair of warps: the 16 x 16 blocks on the diagonal by elimination in fp32, a column
+// a thread; then blocks of 32 and of 64 from X_BA = -X_B A_BA X_A, on tensor cores with operands of two f16
+// numbers.  Computed transposed, (X_A^T A_BA^T) X_B^T, the first product is the second one's A operand in place.
+// (64 steps of elimination in registers, unrolled, ran at the speed of their instruction fetches and took 208 us for
+// 8192 tokens of 32 heads; in loops of 16 rows 150 us.)
 template <int DK>
 struct PrepSmem {
-    alignas(128) char k[Tile<DK>::kBytes];
-    char q[Tile<DK>::kBytes];
-    float at[2][C][C + 4];  // A transposed, then X, of two value heads
-    float ck[C], cq[C];     // factors of the keys and queries
+    struct Blocks {
+        char ahi[6 * 512], alo[6 * 512];  // A' below its diagonal blocks
+        float at[4][16][20];              // the diagonal blocks, transposed
+    };
+    union {
+        struct {
+            alignas(128) char k[Tile<DK>::kBytes];  // K and Q as they go to global memory
+            char q[Tile<DK>::kBytes];
+        };
+        Blocks blocks[2];  // of two value heads, once the products of k and q are taken
+    };
+    alignas(128) char x[2][kHeadBytes];  // X high, X low, P, factors, as they go to global memory
+    float ck[C], cq[C];                  // factors of the keys and queries
     float ghi[2][C], glo[2][C], beta[2][C];
 };
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(tc::smem_addr(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_fast(float x) {  // (2^-22 of the value; to 0 below 2^-126)
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// d += a b for operands of two f16 numbers (the product of the low ones is below the others' error)
+__device__ __forceinline__ void mma3(float (&d)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint32_t b0, uint32_t b1,
+                                     uint32_t l0, uint32_t l1) {
+    mma(d, hi, b0, b1);
+    mma(d, lo, b0, b1);
+    mma(d, hi, l0, l1);
+}
+
+// Block [n0, n0 + 16 NB) x [m0, m0 + 16) of X, below the diagonal, from the finished blocks: X_A is rows and columns
+// from ma on, X_B from n0 on, both of 16 NB; m0 is one of X_A's column blocks.
+template <int NB>
+__device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t ah, uint32_t al, int ma, int m0, int n0) {
+    const int lane = threadIdx.x % 32, lr = lane & 7, lm = lane >> 3;
+    float d[2 * NB][4];
+#pragma unroll
+    for (int t = 0; t < 2 * NB; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[t][e] = 0.f;
+    // T^T [m][n] = sum_k X_A[k][m] A_BA[n][k]: rows k before m0 are zero
+#pragma unroll
+    for (int kb = 0; kb < NB; ++kb) {
+        const int k0 = ma + 16 * kb;
+        if (k0 < m0) continue;
+        uint32_t a[4], l[4];
+        const int at = tri(k0 / 16, m0 / 16, (lm >> 1) * 8 + lr, lm & 1);
+        ldsm4_t(a, xh + at);
+        ldsm4_t(l, xl + at);
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
+            uint32_t b[4], bl[4];
+            const int bt = below(n0 / 16 + t, k0 / 16, (lm >> 1) * 8 + lr, lm & 1);
+            ldsm4(b, ah + bt);
+            ldsm4(bl, al + bt);
+            mma3(d[2 * t], a, l, b[0], b[1], bl[0], bl[1]);
+            mma3(d[2 * t + 1], a, l, b[2], b[3], bl[2], bl[3]);
+        }
+    }
+    // X_BA^T [m][n] = - sum_k T^T[m][k] X_B[n][k]
+    float y[2 * NB][4];
+#pragma unroll
+    for (int t = 0; t < 2 * NB; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[t][e] = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < NB; ++kb) {
+        uint32_t a[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            split(-d[2 * kb + j][0], -d[2 * kb + j][1], a[2 * j], l[2 * j]);
+            split(-d[2 * kb + j][2], -d[2 * kb + j][3], a[2 * j + 1], l[2 * j + 1]);
+        }
+#pragma unroll
+        for (int t = kb; t < NB; ++t) {
+            uint32_t b[4], bl[4];
+            const int bt = tri(n0 / 16 + t, n0 / 16 + kb, (lm >> 1) * 8 + lr, lm & 1);
+            ldsm4(b, xh + bt);
+            ldsm4(bl, xl + bt);
+            mma3(y[2 * t], a, l, b[0], b[1], bl[0], bl[1]);
+            mma3(y[2 * t + 1], a, l, b[2], b[3], bl[2], bl[3]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NB; ++t) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) split(y[2 * t + j][2 * h], y[2 * t + j][2 * h + 1], hi[2 * j + h], lo[2 * j + h]);
+        const int at = tri(n0 / 16 + t, m0 / 16, (lm >> 1) * 8 + lr, lm & 1);
+        stsm4_t(xh + at, hi[0], hi[1], hi[2], hi[3]);
+        stsm4_t(xl + at, lo[0], lo[1], lo[2], lo[3]);
+    }
+}
 
 template <int DK>
 __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, const Scratch w) {
@@ -128,7 +240,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
     PrepSmem<DK>& sm = *reinterpret_cast<PrepSmem<DK>*>(raw);
     pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, pair = warp / 2;
     const int hk = blockIdx.x % a.Hk, chunk = blockIdx.x / a.Hk % w.chunks, r = blockIdx.x / a.Hk / w.chunks;
     int tokens, slot;
     if (!delta_request(a, r, false, tokens, slot)) return;
@@ -136,44 +248,68 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
     if (m <= 0) return;
     const long long tok0 = 1ll * r * a.n + chunk * C;
     const long long unit = 1ll * r * w.chunks + chunk;
+    const int group = a.Hv / a.Hk;
 
     // keys and queries: f16 after a power of two a row, DK / 8 lanes a row
-    constexpr int L = DK / 8, RPW = 32 / L;
-    char* to = w.qk + (unit * a.Hk + hk) * 2 * Tile<DK>::kBytes;
+    constexpr int L = DK / 8, RPW = 32 / L, ROWS = 16 / RPW;
     const int sub = lane % L;
-#pragma unroll 4
-    for (int i = 0; i < 16 / RPW * 2; ++i) {
-        const bool query = i >= 16 / RPW;
-        const int t = warp * 16 + (i % (16 / RPW)) * RPW + lane / L;
-        const bf16* p = static_cast<const bf16*>(query ? a.q : a.k) + (tok0 + t) * (query ? a.q_ld : a.k_ld) + hk * DK + 8 * sub;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (t < m) x = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-        float f[8], most = 0.f;
+    uint4 in[2][ROWS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = __uint_as_float(xs[j] << 16);
-            f[2 * j + 1] = __uint_as_float(xs[j] & 0xffff0000u);
-            most = fmaxf(most, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
+    for (int i = 0; i < ROWS; ++i) {
+        const int t = warp * 16 + i * RPW + lane / L;
+        in[0][i] = in[1][i] = make_uint4(0, 0, 0, 0);
+        if (t < m) {
+            in[0][i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.k) + (tok0 + t) * a.k_ld + hk * DK + 8 * sub));
+            in[1][i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (tok0 + t) * a.q_ld + hk * DK + 8 * sub));
         }
-#pragma unroll
-        for (int o = L / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const float up = scale_to(most, 0), down = 1.f / up;
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f[j] *= up;
-            ss += f[j] * f[j];
-        }
-#pragma unroll
-        for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (sub == 0) (query ? sm.cq : sm.ck)[t] = a.eps > 0.f ? 1.f / sqrtf(ss + a.eps * up * up) : down;
-        const uint4 y = make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
-        const int at = sub / 8 * (C * 128) + swz(t, sub % 8);
-        *reinterpret_cast<uint4*>((query ? sm.q : sm.k) + at) = y;
-        *reinterpret_cast<uint4*>(to + (query ? Tile<DK>::kBytes : 0) + at) = y;
     }
+    float gs[2], be[2];  // of the first two value heads, by an even warp each: tokens 2 lane and 2 lane + 1
+    auto load_gates = [&](int v) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const bool on = v < group && t < m;
+            gs[i] = on ? a.g[(tok0 + t) * a.Hv + hk * group + v] : 0.f;
+            be[i] = on ? a.beta[(tok0 + t) * a.Hv + hk * group + v] : 0.f;
+        }
+    };
+    if (warp % 2 == 0) load_gates(pair);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int t = warp * 16 + i * RPW + lane / L;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const uint32_t xs[4] = {in[which][i].x, in[which][i].y, in[which][i].z, in[which][i].w};
+            float f[8], most = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[2 * j] = __uint_as_float(xs[j] << 16);
+                f[2 * j + 1] = __uint_as_float(xs[j] & 0xffff0000u);
+                most = fmaxf(most, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
+            }
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const float up = scale_to(most, 0);
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                f[j] *= up;
+                ss += f[j] * f[j];
+            }
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (sub == 0)
+                (which ? sm.cq : sm.ck)[t] = ss == 0.f ? 0.f : a.eps > 0.f ? 1.f / sqrtf(ss + a.eps * up * up) : 1.f / up;
+            *reinterpret_cast<uint4*>((which ? sm.q : sm.k) + sub / 8 * (C * 128) + swz(t, sub % 8)) =
+                make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+        }
+    }
+    tc::fence_proxy_async_smem();
     __syncthreads();
+    if (tid == 0) {
+        bulk_store(w.qk + (unit * a.Hk + hk) * 2 * Tile<DK>::kBytes, sm.k, 2 * Tile<DK>::kBytes);
+        bulk_commit();
+    }
 
     // k.k and q.k of this warp's 16 tokens with the tokens up to them
     float kk[8][4], qk[8][4];
@@ -183,7 +319,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
         for (int e = 0; e < 4; ++e) kk[t][e] = qk[t][e] = 0.f;
     const uint32_t ks = tc::smem_addr(sm.k), qs = tc::smem_addr(sm.q);
     const int lr = lane & 7, lm = lane >> 3;  // row within a matrix, matrix of ldmatrix.x4
-#pragma unroll
+#pragma unroll 2
     for (int kt = 0; kt < DK / 16; ++kt) {
         const int base = kt / 4 * (C * 128), c = kt % 4 * 2;
         uint32_t ak[4], aq[4];
@@ -202,25 +338,20 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
         }
     }
 
-    const int group = a.Hv / a.Hk, g4 = lane / 4, q4 = lane % 4;
+    const int g4 = lane / 4, q4 = lane % 4;
+#pragma unroll 1
     for (int v0 = 0; v0 < group; v0 += 2) {  // two value heads at a time, a pair of warps each
-        const int pair = warp / 2, hv = hk * group + v0 + pair;
         const bool on = v0 + pair < group;
-        char* head = w.heads + (unit * a.Hv + hv) * kHeadBytes;
-        float* vec = reinterpret_cast<float*>(head + 3 * kSquare);
-        if (v0) __syncthreads();  // at[] is free
+        if (tid == 0) bulk_wait_read();  // K and Q, or x[], have been read: their places are free
+        if (v0) {
+            __syncthreads();
+            if (warp % 2 == 0) load_gates(v0 + pair);
+        }
         if (on && warp % 2 == 0) {
-            // sums of g, in 64 bits: lane holds tokens 2 lane and 2 lane + 1
-            double s[2];
-            float be[2];
+            float* vec = reinterpret_cast<float*>(sm.x[pair] + 3 * kTri);
+            double s[2];  // sums of g in 64 bits, to base 2
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                float g = t < m ? a.g[(tok0 + t) * a.Hv + hv] : 0.f;
-                if (g < -200.f) g = -200.f;  // e^-200 is 0 in fp32 as well
-                s[i] = g;
-                be[i] = t < m ? a.beta[(tok0 + t) * a.Hv + hv] : 0.f;
-            }
+            for (int i = 0; i < 2; ++i) s[i] = (gs[i] < -200.f ? -200.f : gs[i]) * 1.4426950408889634;  // (e^-200 is 0 as well)
             const double mine = s[0] + s[1];
             double run = mine;
 #pragma unroll
@@ -237,95 +368,105 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
                 const float hi = static_cast<float>(s[i]);
                 sm.ghi[pair][t] = hi;
                 sm.glo[pair][t] = static_cast<float>(s[i] - hi);
-                sm.beta[pair][t] = be[i];
-                const float since = expf(hi), left = expf(static_cast<float>(all - s[i]));
-                vec[kA * C + t] = since * sm.ck[t];
-                vec[kBeta * C + t] = be[i];
-                vec[kB * C + t] = since * sm.cq[t] * a.scale;
-                vec[kD * C + t] = left * sm.ck[t];
+                const float ck = sm.ck[t], cq = sm.cq[t] * a.scale, since = exp2f(hi);
+                sm.beta[pair][t] = be[i] * ck * ck;
+                vec[kA * C + t] = since * ck;
+                vec[kBeta * C + t] = be[i] * ck;
+                vec[kB * C + t] = since * cq;
+                vec[kPi * C + t] = cq;
+                vec[kD * C + t] = exp2f(static_cast<float>(all - s[i]));
             }
-            if (lane == 0) vec[kGamma * C] = expf(static_cast<float>(all));
+            if (lane == 0) vec[kGamma * C] = exp2f(static_cast<float>(all));
         }
         __syncthreads();
-        // A (transposed) and P of both heads, from every warp's products
-#pragma unroll
+        // A' and P of both heads, from every warp's products
+#pragma unroll 1
         for (int p = 0; p < 2; ++p) {
-            if (v0 + p >= group) continue;
-            char* ph = w.heads + (unit * a.Hv + hk * group + v0 + p) * kHeadBytes;
+            if (v0 + p >= group) break;
+            char* const ps = sm.x[p] + 2 * kTri;
+            typename PrepSmem<DK>::Blocks& bl = sm.blocks[p];
+            const int i0 = warp * 16 + g4;
+            const float gh[2] = {sm.ghi[p][i0], sm.ghi[p][i0 + 8]}, gl[2] = {sm.glo[p][i0], sm.glo[p][i0 + 8]};
+            const float bc[2] = {sm.beta[p][i0], sm.beta[p][i0 + 8]};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // rows g4 and g4 + 8 of the warp's 16
-                const int i = warp * 16 + h * 8 + g4;
-                const float gh = sm.ghi[p][i], gl = sm.glo[p][i], bc = sm.beta[p][i] * sm.ck[i], qc = sm.cq[i] * a.scale;
-                float pv[16], most = 0.f;
+            for (int t = 0; t < 8; ++t) {
+                if (t / 2 > warp) continue;
+                const float2 jh = *reinterpret_cast<const float2*>(&sm.ghi[p][8 * t + 2 * q4]);
+                const float2 jl = *reinterpret_cast<const float2*>(&sm.glo[p][8 * t + 2 * q4]);
+                const bool diagonal = t / 2 == warp;
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = 8 * t + 2 * q4 + e;
-                        float x = 0.f;
-                        if (t / 2 <= warp && j <= i) {
-                            const float decay = expf((gh - sm.ghi[p][j]) + (gl - sm.glo[p][j])) * sm.ck[j];
-                            x = decay * qc * qk[t][2 * h + e];
-                            if (j < i) sm.at[p][j][i] = decay * bc * kk[t][2 * h + e];
-                        }
-                        pv[2 * t + e] = x;
-                        most = fmaxf(most, fabsf(x));
+                for (int h = 0; h < 2; ++h) {
+                    const int i = i0 + 8 * h, j = 8 * t + 2 * q4;
+                    float e0 = exp2_fast((gh[h] - jh.x) + (gl[h] - jl.x)), e1 = exp2_fast((gh[h] - jh.y) + (gl[h] - jl.y));
+                    if (diagonal) {
+                        if (j > i) e0 = 0.f;
+                        if (j + 1 > i) e1 = 0.f;
+                        // the elements on and above the diagonal are not looked at
+                        bl.at[warp][j % 16][i % 16] = e0 * bc[h] * kk[t][2 * h];
+                        bl.at[warp][j % 16 + 1][i % 16] = e1 * bc[h] * kk[t][2 * h + 1];
+                    } else {
+                        uint32_t hi, lo;
+                        split(e0 * bc[h] * kk[t][2 * h], e1 * bc[h] * kk[t][2 * h + 1], hi, lo);
+                        *reinterpret_cast<uint32_t*>(bl.ahi + below(warp, t / 2, g4 + 8 * h, t % 2) + 4 * q4) = hi;
+                        *reinterpret_cast<uint32_t*>(bl.alo + below(warp, t / 2, g4 + 8 * h, t % 2) + 4 * q4) = lo;
                     }
-                const float up = scale_to(quad_max(most), 0);
-                if (q4 == 0) reinterpret_cast<float*>(ph + 3 * kSquare)[kPi * C + i] = 1.f / up;
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    *reinterpret_cast<uint32_t*>(ph + 2 * kSquare + swz(i, t) + 4 * q4) = pack(pv[2 * t] * up, pv[2 * t + 1] * up);
+                    // (a factor of zero, not a product with what may be inf, above the diagonal)
+                    const float p0 = diagonal && j > i ? 0.f : e0 * qk[t][2 * h], p1 = diagonal && j + 1 > i ? 0.f : e1 * qk[t][2 * h + 1];
+                    *reinterpret_cast<uint32_t*>(ps + tri(warp, t / 2, g4 + 8 * h, t % 2) + 4 * q4) = pack(p0, p1);
+                }
             }
         }
+        tc::fence_proxy_async_smem();
         __syncthreads();
         if (on) {
-            // column c of X: x_i = (i == c) - sum_{j < i} A_ij x_j, every x_j taken off the later rows as it is final
-            const int c = warp % 2 * 32 + lane;
-            float x[C];
+            char* const xp = sm.x[pair];
+            {  // diagonal blocks: column c of block b, an elimination in registers
+                const int c = warp % 2 * 32 + lane, b = c / 16;
+                const float(*at)[20] = sm.blocks[pair].at[b];
+                float x[16];
 #pragma unroll
-            for (int i = 0; i < C; ++i) x[i] = i == c ? 1.f : 0.f;
-            const float(*at)[C + 4] = sm.at[pair];
-            if (warp % 2 == 0) {
+                for (int i = 0; i < 16; ++i) x[i] = i == c % 16 ? 1.f : 0.f;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 15; ++j)
 #pragma unroll
-                    for (int i = j + 1; i < C; ++i) x[i] -= at[j][i] * x[j];
+                    for (int i = j + 1; i < 16; ++i) x[i] -= at[j][i] * x[j];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int o = tri(b, b, i, c % 16 / 8) + 2 * (c % 8);
+                    const __half hi = __float2half_rn(x[i]);
+                    *reinterpret_cast<__half*>(xp + o) = hi;
+                    *reinterpret_cast<__half*>(xp + kTri + o) = __float2half_rn(x[i] - __half2float(hi));
+                }
             }
-#pragma unroll
-            for (int j = 32; j < C - 1; ++j)
-#pragma unroll
-                for (int i = j + 1; i < C; ++i) x[i] -= at[j][i] * x[j];
+            const uint32_t xh = tc::smem_addr(xp), xl = xh + kTri;
+            const uint32_t ah = tc::smem_addr(sm.blocks[pair].ahi), al = tc::smem_addr(sm.blocks[pair].alo);
+            const int w2 = warp % 2;
+            __syncwarp();
+            merge_blocks<1>(xh, xl, ah, al, 32 * w2, 32 * w2, 32 * w2 + 16);
             tc::named_bar_sync(1 + pair, 64);
-#pragma unroll
-            for (int i = 0; i < C; ++i) sm.at[pair][i][c] = x[i];
+            merge_blocks<2>(xh, xl, ah, al, 0, 16 * w2, 32);
+            tc::fence_proxy_async_smem();
             tc::named_bar_sync(1 + pair, 64);
-            const int i = c;  // now a row each
-            float most = 0.f;
-#pragma unroll
-            for (int j = 0; j < C; j += 4) {
-                const float4 y = *reinterpret_cast<const float4*>(&sm.at[pair][i][j]);
-                most = fmaxf(fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y))), fmaxf(fabsf(y.z), fabsf(y.w)));
-            }
-            const float up = scale_to(most, 10);
-            vec[kTau * C + i] = 1.f / up;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float4 y = *reinterpret_cast<const float4*>(&sm.at[pair][i][8 * j]);
-                const float4 z = *reinterpret_cast<const float4*>(&sm.at[pair][i][8 * j + 4]);
-                uint4 hi, lo;
-                split(y.x * up, y.y * up, hi.x, lo.x);
-                split(y.z * up, y.w * up, hi.y, lo.y);
-                split(z.x * up, z.y * up, hi.z, lo.z);
-                split(z.z * up, z.w * up, hi.w, lo.w);
-                *reinterpret_cast<uint4*>(head + swz(i, j)) = hi;
-                *reinterpret_cast<uint4*>(head + kSquare + swz(i, j)) = lo;
-            }
+        }
+        if (group - v0 > 1) __syncthreads();  // (thread 0 stores both heads)
+        if (tid == 0) {
+            for (int p = 0; p < 2 && v0 + p < group; ++p)
+                bulk_store(w.heads + (unit * a.Hv + hk * group + v0 + p) * kHeadBytes, sm.x[p], kHeadBytes);
+            bulk_commit();
         }
     }
+    if (tid == 0) bulk_wait();
 }
 
 // ---------------------------------------------------------------- second launch: the states' walk
+// A slice of 16 rows of the transposed state is walked by two warps.  Warp p keeps columns [DK / 2 p, DK / 2 (p + 1)) of
+// the rows and takes tokens [32 p, 32 p + 32) of R, U and O; the operands that the other one needs (its half of the
+// state, R of the first tokens, U') pass through shared memory as f16 pairs in the A operand's layout, each
+// half with row scales of its own, so that nothing has to be agreed on before.
+//
+// Bound: a warp's dependent chain of about 1100 instructions a chunk, 200 of them MMAs at 8 cycles, while there are fewer
+// than two warps a scheduler; with more, the rate of mma.sync (1024 multiplications a cycle and multiprocessor; 400
+// MMAs a slice and chunk).
 template <int DK, int W>
 struct WalkSmem {
     static constexpr int kStages = 2;
@@ -335,23 +476,33 @@ struct WalkSmem {
         char head[kHeadBytes];
     };
     alignas(128) Stage st[kStages];
-    char v[W][2][C * 32];  // a warp's 16 columns of the values, then of the outputs
+    struct Pass {                      // from warp p of a slice to the other
+        uint4 s[2][DK / 32][2][32];    // [p][k step][high, low][lane]
+        uint4 d[2][2][2][32];          // U' e^(G_C - G)
+        uint4 r[2][2][32];             // R of the first 32 tokens
+        uint4 u[2][32];                // U' of the first 32 tokens (high)
+        float ds[2][16], dd[2][16], dr[16], du[16];  // factors of their rows
+    } pass[W];
+    char v[2 * W][2][32 * 32];  // a warp's 32 tokens of 16 values, then of outputs
     uint64_t full[kStages], empty[kStages];
     int abort;
 };
 
 template <int DK, int W>
-__global__ void __launch_bounds__(32 * W, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
+__global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
     extern __shared__ __align__(128) char raw[];
     using Smem = WalkSmem<DK, W>;
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     constexpr int NS = Smem::kStages;
+    constexpr int NK = DK / 32;  // k steps of 16 of a half of the state's columns
     constexpr uint32_t kQk = 2 * Tile<DK>::kBytes;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g4 = lane / 4, q4 = lane % 4;
+    const int mine = warp / 2, p = warp % 2;  // slice of the block, part of it
+    typename Smem::Pass& ps = sm.pass[mine];
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             tc::mbar_init(&sm.full[i], 1);
-            tc::mbar_init(&sm.empty[i], W);
+            tc::mbar_init(&sm.empty[i], 2 * W);
         }
         sm.abort = 0;
         tc::fence_mbar_init();
@@ -364,7 +515,7 @@ __global__ void __launch_bounds__(32 * W, 1) delta_walk_kernel(const DeltaArgs a
     if (!delta_request(a, r, tid == 0 && slice == 0 && hv == 0, tokens, slot)) return;
     __syncthreads();
     const int hk = hv / (a.Hv / a.Hk), n_chunks = (tokens + C - 1) / C;
-    const int row0 = (slice * W + warp) * 16;  // first of the warp's rows
+    const int row0 = (slice * W + mine) * 16;  // first of the slice's rows
     const long long tok0 = 1ll * r * a.n, unit0 = 1ll * r * w.chunks;
 
     auto fetch = [&](int c) {  // by one thread: chunk c into its stage
@@ -376,13 +527,13 @@ __global__ void __launch_bounds__(32 * W, 1) delta_walk_kernel(const DeltaArgs a
     };
     const uint32_t vs = tc::smem_addr(sm.v[warp]);
     auto at_v = [&](int t, int c) { return t * 32 + ((c ^ (t >> 2 & 1)) << 4); };
-    auto fetch_v = [&](int c) {  // a warp's 16 columns of the values, zeros behind the request's tokens
-        const bf16* p = static_cast<const bf16*>(a.v) + hv * a.Dv + row0;
+    auto fetch_v = [&](int c) {  // the warp's values, zeros behind the request's tokens
+        const bf16* vp = static_cast<const bf16*>(a.v) + hv * a.Dv + row0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = i * 16 + lane / 2, tok = c * C + t;
+        for (int i = 0; i < 2; ++i) {
+            const int t = i * 16 + lane / 2, tok = c * C + 32 * p + t;
             const bool on = tok < tokens;
-            cp16(vs + (c & 1) * (C * 32) + at_v(t, lane & 1), p + (tok0 + (on ? tok : 0)) * a.v_ld + 8 * (lane & 1), on);
+            cp16(vs + (c & 1) * 1024 + at_v(t, lane & 1), vp + (tok0 + (on ? tok : 0)) * a.v_ld + 8 * (lane & 1), on);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -390,12 +541,12 @@ __global__ void __launch_bounds__(32 * W, 1) delta_walk_kernel(const DeltaArgs a
         for (int c = 0; c < NS && c < n_chunks; ++c) fetch(c);
     if (n_chunks > 0) fetch_v(0);
 
-    // rows g4 and g4 + 8 of the transposed state, columns 8 t + 2 q4 + {0, 1}; times sigma of the row
-    float S[DK / 8][4], sigma[2] = {1.f, 1.f};
-    const long long state0 = ((1ll * slot * a.Hv + hv) * a.Dv + row0 + g4) * DK + 2 * q4;
+    // rows g4 and g4 + 8 of the slice, columns DK / 2 p + 8 t + 2 q4 + {0, 1}
+    float S[DK / 16][4];
+    const long long state0 = ((1ll * slot * a.Hv + hv) * a.Dv + row0 + g4) * DK + p * (DK / 2) + 2 * q4;
     const bool fresh = a.fresh && a.fresh[r];
 #pragma unroll
-    for (int t = 0; t < DK / 8; ++t) {
+    for (int t = 0; t < DK / 16; ++t) {
         float2 x = make_float2(0.f, 0.f), y = x;
         if (!fresh) {
             x = *reinterpret_cast<const float2*>(a.state + state0 + 8 * t);
@@ -405,12 +556,15 @@ __global__ void __launch_bounds__(32 * W, 1) delta_walk_kernel(const DeltaArgs a
     }
 
     const int lr = lane & 7, lm = lane >> 3;
+    const int bar_id = 1 + mine;
     bool ok = true;
     int c = 0;
+#pragma unroll 1
     for (; c < n_chunks; ++c) {
         const int st = c % NS;
+        // both warps of a slice leave together: the second of them sees a wait that ran out behind the next barrier
         ok = tc::mbar_wait(&sm.full[st], (c / NS) & 1, &sm.abort, a.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = tc::named_bar_and(bar_id, 64, ok);
         if (!ok) break;
         if (c + 1 < n_chunks) {
             fetch_v(c + 1);
@@ -421,211 +575,276 @@ __global__ void __launch_bounds__(32 * W, 1) delta_walk_kernel(const DeltaArgs a
         __syncwarp();
         typename Smem::Stage& s = sm.st[st];
         const uint32_t ks = tc::smem_addr(s.k), qs = tc::smem_addr(s.q), xs = tc::smem_addr(s.head);
-        const float* vec = reinterpret_cast<const float*>(s.head + 3 * kSquare);
-        const uint32_t vc = vs + (c & 1) * (C * 32);
+        const float* vec = reinterpret_cast<const float*>(s.head + 3 * kTri) + 32 * p + 2 * q4;  // of this warp's tokens
+        const uint32_t vc = vs + (c & 1) * 1024;
 
-        // S0 K^T (pairs of f16) and S0 Q^T (one f16)
-        float most[2] = {0.f, 0.f};
+        // S0 K^T (pairs of f16) and S0 Q^T (one f16) of the warp's tokens: first with its own columns of S0, then
+        // with the other's
+        float most[2] = {0.f, 0.f}, up[2], own[2], other[2];
 #pragma unroll
-        for (int t = 0; t < DK / 8; ++t) {
+        for (int t = 0; t < DK / 16; ++t) {
             most[0] = fmaxf(most[0], fmaxf(fabsf(S[t][0]), fabsf(S[t][1])));
             most[1] = fmaxf(most[1], fmaxf(fabsf(S[t][2]), fabsf(S[t][3])));
         }
-        float up[2], down[2];  // S is brought to 2^12 by `up`; products are brought back by `down`
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            most[h] = quad_max(most[h]);
-            up[h] = scale_to(most[h], 12);
-            down[h] = 1.f / up[h] * sigma[h];
-            most[h] *= sigma[h];
+            up[h] = scale_to(quad_max(most[h]), 12);
+            own[h] = 1.f / up[h];
+            if (q4 == 0) ps.ds[p][g4 + 8 * h] = own[h];
         }
-        float sk[8][4], sq[8][4];
+        float sk[4][4], sq[4][4], zk[4][4], zq[4][4];
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sk[t][e] = sq[t][e] = 0.f;
+            for (int e = 0; e < 4; ++e) sk[t][e] = sq[t][e] = zk[t][e] = zq[t][e] = 0.f;
+        auto half_product = [&](const uint32_t(&hi)[4], const uint32_t(&lo)[4], int kt, float(&k4)[4][4], float(&q4x)[4][4]) {
+            const int base = kt / 4 * (C * 128), cc = kt % 4 * 2;
 #pragma unroll
-        for (int kt = 0; kt < DK / 16; ++kt) {
+            for (int t2 = 0; t2 < 2; ++t2) {
+                uint32_t b[4];
+                const int off = base + swz(32 * p + t2 * 16 + (lm >> 1) * 8 + lr, cc + (lm & 1));
+                ldsm4(b, ks + off);
+                mma(k4[2 * t2], hi, b[0], b[1]);
+                mma(k4[2 * t2 + 1], hi, b[2], b[3]);
+                mma(k4[2 * t2], lo, b[0], b[1]);
+                mma(k4[2 * t2 + 1], lo, b[2], b[3]);
+                ldsm4(b, qs + off);
+                mma(q4x[2 * t2], hi, b[0], b[1]);
+                mma(q4x[2 * t2 + 1], hi, b[2], b[3]);
+            }
+        };
+#pragma unroll
+        for (int kt = 0; kt < NK; ++kt) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 split(S[2 * kt + j][0] * up[0], S[2 * kt + j][1] * up[0], hi[2 * j], lo[2 * j]);
                 split(S[2 * kt + j][2] * up[1], S[2 * kt + j][3] * up[1], hi[2 * j + 1], lo[2 * j + 1]);
             }
-            const int base = kt / 4 * (C * 128), cc = kt % 4 * 2;
-#pragma unroll
-            for (int t2 = 0; t2 < 4; ++t2) {
-                uint32_t b[4];
-                const int off = base + swz(t2 * 16 + (lm >> 1) * 8 + lr, cc + (lm & 1));
-                ldsm4(b, ks + off);
-                mma(sk[2 * t2], hi, b[0], b[1]);
-                mma(sk[2 * t2 + 1], hi, b[2], b[3]);
-                mma(sk[2 * t2], lo, b[0], b[1]);
-                mma(sk[2 * t2 + 1], lo, b[2], b[3]);
-                ldsm4(b, qs + off);
-                mma(sq[2 * t2], hi, b[0], b[1]);
-                mma(sq[2 * t2 + 1], hi, b[2], b[3]);
-            }
+            ps.s[p][kt][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            ps.s[p][kt][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            half_product(hi, lo, p * NK + kt, sk, sq);
         }
-        // R = beta (v - e^G S0 k), in place of S0 K^T
+        tc::named_bar_sync(bar_id, 64);
+        other[0] = ps.ds[1 - p][g4], other[1] = ps.ds[1 - p][g4 + 8];
+#pragma unroll
+        for (int kt = 0; kt < NK; ++kt) {
+            const uint4 x = ps.s[1 - p][kt][0][lane], y = ps.s[1 - p][kt][1][lane];
+            const uint32_t hi[4] = {x.x, x.y, x.z, x.w}, lo[4] = {y.x, y.y, y.z, y.w};
+            half_product(hi, lo, (1 - p) * NK + kt, zk, zq);
+        }
+        // R = beta c (v - e^G c S0 k), in place of S0 K^T
         float rmost[2] = {0.f, 0.f};
 #pragma unroll
-        for (int t2 = 0; t2 < 4; ++t2) {
+        for (int t2 = 0; t2 < 2; ++t2) {
             uint32_t vv[4];  // tokens 16 t2 ..: columns 0-7, 8-15; tokens 16 t2 + 8 ..: the same
             ldsm4_t(vv, vc + at_v(t2 * 16 + (lm >> 1) * 8 + lr, lm & 1));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = 2 * t2 + j;
-                const float2 av = *reinterpret_cast<const float2*>(vec + kA * C + 8 * t + 2 * q4);
-                const float2 be = *reinterpret_cast<const float2*>(vec + kBeta * C + 8 * t + 2 * q4);
+                const float2 av = *reinterpret_cast<const float2*>(vec + kA * C + 8 * t);
+                const float2 be = *reinterpret_cast<const float2*>(vec + kBeta * C + 8 * t);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t x = vv[2 * j + h];
                     float& r0 = sk[t][2 * h];
                     float& r1 = sk[t][2 * h + 1];
-                    r0 = be.x * (__uint_as_float(x << 16) - av.x * (r0 * down[h]));
-                    r1 = be.y * (__uint_as_float(x & 0xffff0000u) - av.y * (r1 * down[h]));
+                    r0 = be.x * (__uint_as_float(x << 16) - av.x * (r0 * own[h] + zk[t][2 * h] * other[h]));
+                    r1 = be.y * (__uint_as_float(x & 0xffff0000u) - av.y * (r1 * own[h] + zk[t][2 * h + 1] * other[h]));
                     rmost[h] = fmaxf(rmost[h], fmaxf(fabsf(r0), fabsf(r1)));
+                    sq[t][2 * h] = sq[t][2 * h] * own[h] + zq[t][2 * h] * other[h];
+                    sq[t][2 * h + 1] = sq[t][2 * h + 1] * own[h] + zq[t][2 * h + 1] * other[h];
                 }
             }
         }
-        // U = X R
-        float rup[2];
+        // U' = X R: of the warp's own tokens, and for the later tokens of the first ones
+        float rup[2], rdown[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) rup[h] = scale_to(quad_max(rmost[h]), 12);
-        float u[8][4];
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                split(sk[2 * kt + j][0] * rup[0], sk[2 * kt + j][1] * rup[0], hi[2 * j], lo[2 * j]);
-                split(sk[2 * kt + j][2] * rup[1], sk[2 * kt + j][3] * rup[1], hi[2 * j + 1], lo[2 * j + 1]);
-            }
-#pragma unroll
-            for (int t2 = kt; t2 < 4; ++t2) {  // X is lower triangular
-                uint32_t b[4], bl[4];
-                const int off = swz(t2 * 16 + (lm >> 1) * 8 + lr, kt * 2 + (lm & 1));
-                ldsm4(b, xs + off);
-                ldsm4(bl, xs + kSquare + off);
-                mma(u[2 * t2], hi, b[0], b[1]);
-                mma(u[2 * t2 + 1], hi, b[2], b[3]);
-                mma(u[2 * t2], lo, b[0], b[1]);
-                mma(u[2 * t2 + 1], lo, b[2], b[3]);
-                mma(u[2 * t2], hi, bl[0], bl[1]);
-                mma(u[2 * t2 + 1], hi, bl[2], bl[3]);
-            }
+        for (int h = 0; h < 2; ++h) {
+            rup[h] = scale_to(quad_max(rmost[h]), 12);
+            rdown[h] = 1.f / rup[h];
+            if (p == 0 && q4 == 0) ps.dr[g4 + 8 * h] = rdown[h];
         }
-        float umost[2] = {0.f, 0.f}, dmost[2] = {0.f, 0.f};
+        float u[4][4], z[4][4];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const float2 tau = *reinterpret_cast<const float2*>(vec + kTau * C + 8 * t + 2 * q4);
-            const float2 dd = *reinterpret_cast<const float2*>(vec + kD * C + 8 * t + 2 * q4);
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[t][e] = z[t][e] = 0.f;
+        auto x_product = [&](const uint32_t(&hi)[4], const uint32_t(&lo)[4], int kt, int t2, float(&d)[4][4]) {
+            uint32_t b[4], bl[4];
+            const int off = tri(2 * p + t2, kt, (lm >> 1) * 8 + lr, lm & 1);
+            ldsm4(b, xs + off);
+            ldsm4(bl, xs + kTri + off);
+            mma3(d[2 * t2], hi, lo, b[0], b[1], bl[0], bl[1]);
+            mma3(d[2 * t2 + 1], hi, lo, b[2], b[3], bl[2], bl[3]);
+        };
+        {
+            uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    split(sk[2 * kt + j][0] * rup[0], sk[2 * kt + j][1] * rup[0], hi[kt][2 * j], lo[kt][2 * j]);
+                    split(sk[2 * kt + j][2] * rup[1], sk[2 * kt + j][3] * rup[1], hi[kt][2 * j + 1], lo[kt][2 * j + 1]);
+                }
+                if (p == 0) {
+                    ps.r[kt][0][lane] = make_uint4(hi[kt][0], hi[kt][1], hi[kt][2], hi[kt][3]);
+                    ps.r[kt][1][lane] = make_uint4(lo[kt][0], lo[kt][1], lo[kt][2], lo[kt][3]);
+                }
+            }
+            if (p == 0) tc::named_bar_sync(bar_id, 64);
+            x_product(hi[0], lo[0], 2 * p, 0, u);
+            x_product(hi[0], lo[0], 2 * p, 1, u);
+            x_product(hi[1], lo[1], 2 * p + 1, 1, u);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[t][e] *= rdown[e / 2];
+        if (p == 1) {
+            tc::named_bar_sync(bar_id, 64);
+            const float f[2] = {ps.dr[g4], ps.dr[g4 + 8]};
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                const uint4 x = ps.r[kt][0][lane], y = ps.r[kt][1][lane];
+                const uint32_t hi[4] = {x.x, x.y, x.z, x.w}, lo[4] = {y.x, y.y, y.z, y.w};
+                x_product(hi, lo, kt, 0, z);
+                x_product(hi, lo, kt, 1, z);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[t][e] += z[t][e] * f[e / 2];
+        }
+        // U' and U' e^(G_C - G), each brought to 2^12
+        float umost[2] = {0.f, 0.f}, dmost[2] = {0.f, 0.f}, dx[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float2 left = *reinterpret_cast<const float2*>(vec + kD * C + 8 * t);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float back = 1.f / rup[h];
-                float& u0 = u[t][2 * h];
-                float& u1 = u[t][2 * h + 1];
-                u0 *= tau.x * back;
-                u1 *= tau.y * back;
-                umost[h] = fmaxf(umost[h], fmaxf(fabsf(u0), fabsf(u1)));
-                dmost[h] = fmaxf(dmost[h], fmaxf(fabsf(u0 * dd.x), fabsf(u1 * dd.y)));
+                dx[t][2 * h] = u[t][2 * h] * left.x;
+                dx[t][2 * h + 1] = u[t][2 * h + 1] * left.y;
+                umost[h] = fmaxf(umost[h], fmaxf(fabsf(u[t][2 * h]), fabsf(u[t][2 * h + 1])));
+                dmost[h] = fmaxf(dmost[h], fmaxf(fabsf(dx[t][2 * h]), fabsf(dx[t][2 * h + 1])));
             }
         }
-        // O = e^G scale S0 Q^T + U P^T
-        float uup[2];
+        float uup[2], udown[2], dup[2], ddown[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) uup[h] = scale_to(quad_max(umost[h]), 12);
-        float o[8][4];
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t hi[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                hi[2 * j] = pack(u[2 * kt + j][0] * uup[0], u[2 * kt + j][1] * uup[0]);
-                hi[2 * j + 1] = pack(u[2 * kt + j][2] * uup[1], u[2 * kt + j][3] * uup[1]);
-            }
-#pragma unroll
-            for (int t2 = kt; t2 < 4; ++t2) {
-                uint32_t b[4];
-                ldsm4(b, xs + 2 * kSquare + swz(t2 * 16 + (lm >> 1) * 8 + lr, kt * 2 + (lm & 1)));
-                mma(o[2 * t2], hi, b[0], b[1]);
-                mma(o[2 * t2 + 1], hi, b[2], b[3]);
+        for (int h = 0; h < 2; ++h) {
+            uup[h] = scale_to(quad_max(umost[h]), 12);
+            dup[h] = scale_to(quad_max(dmost[h]), 12);
+            udown[h] = 1.f / uup[h];
+            ddown[h] = 1.f / dup[h];
+            if (q4 == 0) {
+                ps.dd[p][g4 + 8 * h] = ddown[h];
+                if (p == 0) ps.du[g4 + 8 * h] = udown[h];
             }
         }
-        __syncwarp();  // the values have been read: their place takes the outputs
+        uint32_t dhi[2][4], dlo[2][4], uh[2][4];
 #pragma unroll
-        for (int t2 = 0; t2 < 4; ++t2) {
-            uint32_t y[4];
+        for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = 2 * kt + j;
+                    split(dx[t][2 * h] * dup[h], dx[t][2 * h + 1] * dup[h], dhi[kt][2 * j + h], dlo[kt][2 * j + h]);
+                    uh[kt][2 * j + h] = pack(u[t][2 * h] * uup[h], u[t][2 * h + 1] * uup[h]);
+                }
+            ps.d[p][kt][0][lane] = make_uint4(dhi[kt][0], dhi[kt][1], dhi[kt][2], dhi[kt][3]);
+            ps.d[p][kt][1][lane] = make_uint4(dlo[kt][0], dlo[kt][1], dlo[kt][2], dlo[kt][3]);
+            if (p == 0) ps.u[kt][lane] = make_uint4(uh[kt][0], uh[kt][1], uh[kt][2], uh[kt][3]);
+        }
+        tc::named_bar_sync(bar_id, 64);
+        // S = e^G_C S0 + U' e^(G_C - G) K on the warp's columns (sums of their own, added in fp32: an MMA cuts off what it
+        // adds to a large accumulator)
+        {
+            const float gamma = *(reinterpret_cast<const float*>(s.head + 3 * kTri) + kGamma * C);
+            const float f[2] = {ps.dd[1 - p][g4], ps.dd[1 - p][g4 + 8]};
+            uint32_t ehi[2][4], elo[2][4];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                const uint4 x = ps.d[1 - p][kt][0][lane], y = ps.d[1 - p][kt][1][lane];
+                ehi[kt][0] = x.x, ehi[kt][1] = x.y, ehi[kt][2] = x.z, ehi[kt][3] = x.w;
+                elo[kt][0] = y.x, elo[kt][1] = y.y, elo[kt][2] = y.z, elo[kt][3] = y.w;
+            }
+#pragma unroll
+            for (int t2 = 0; t2 < DK / 32; ++t2) {
+                float d[2][2][4];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) (&d[0][0][0])[i] = 0.f;
+                const int col = p * (DK / 32) + t2;  // of 16 columns of K
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) {
+                    uint32_t b[4];
+                    const int cb = ks + col / 4 * (C * 128), cp = col % 4 * 2 + (lm >> 1), rw = kt * 16 + (lm & 1) * 8 + lr;
+                    ldsm4_t(b, cb + swz(32 * p + rw, cp));
+                    mma(d[0][0], dhi[kt], b[0], b[1]);
+                    mma(d[0][1], dhi[kt], b[2], b[3]);
+                    mma(d[0][0], dlo[kt], b[0], b[1]);
+                    mma(d[0][1], dlo[kt], b[2], b[3]);
+                    ldsm4_t(b, cb + swz(32 * (1 - p) + rw, cp));
+                    mma(d[1][0], ehi[kt], b[0], b[1]);
+                    mma(d[1][1], ehi[kt], b[2], b[3]);
+                    mma(d[1][0], elo[kt], b[0], b[1]);
+                    mma(d[1][1], elo[kt], b[2], b[3]);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float& x = S[2 * t2 + j][e];
+                        x = x * gamma + (d[0][j][e] * ddown[e / 2] + d[1][j][e] * f[e / 2]);
+                    }
+            }
+        }
+        // O = e^G scale S0 Q^T + U' P^T
+        float o[4][4], y[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][e] = y[t][e] = 0.f;
+        auto p_product = [&](const uint32_t(&hi)[4], int kt, int t2, float(&d)[4][4]) {
+            uint32_t b[4];
+            ldsm4(b, xs + 2 * kTri + tri(2 * p + t2, kt, (lm >> 1) * 8 + lr, lm & 1));
+            mma(d[2 * t2], hi, b[0], b[1]);
+            mma(d[2 * t2 + 1], hi, b[2], b[3]);
+        };
+        p_product(uh[0], 2 * p, 0, o);
+        p_product(uh[0], 2 * p, 1, o);
+        p_product(uh[1], 2 * p + 1, 1, o);
+        float uf[2] = {0.f, 0.f};
+        if (p == 1) {
+            uf[0] = ps.du[g4], uf[1] = ps.du[g4 + 8];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                const uint4 x = ps.u[kt][lane];
+                const uint32_t hi[4] = {x.x, x.y, x.z, x.w};
+                p_product(hi, kt, 0, y);
+                p_product(hi, kt, 1, y);
+            }
+        }
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2) {  // the values have been read: their place takes the outputs
+            uint32_t x[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = 2 * t2 + j;
-                const float2 b = *reinterpret_cast<const float2*>(vec + kB * C + 8 * t + 2 * q4);
-                const float2 pi = *reinterpret_cast<const float2*>(vec + kPi * C + 8 * t + 2 * q4);
+                const float2 b = *reinterpret_cast<const float2*>(vec + kB * C + 8 * t);
+                const float2 pi = *reinterpret_cast<const float2*>(vec + kPi * C + 8 * t);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float back = 1.f / uup[h];
-                    const __nv_bfloat162 x =
-                        __floats2bfloat162_rn(b.x * (sq[t][2 * h] * down[h]) + pi.x * (o[t][2 * h] * back),
-                                              b.y * (sq[t][2 * h + 1] * down[h]) + pi.y * (o[t][2 * h + 1] * back));
-                    y[2 * j + h] = *reinterpret_cast<const uint32_t*>(&x);
+                    const float o0 = o[t][2 * h] * udown[h] + y[t][2 * h] * uf[h], o1 = o[t][2 * h + 1] * udown[h] + y[t][2 * h + 1] * uf[h];
+                    const __nv_bfloat162 both = __floats2bfloat162_rn(b.x * sq[t][2 * h] + pi.x * o0, b.y * sq[t][2 * h + 1] + pi.y * o1);
+                    x[2 * j + h] = *reinterpret_cast<const uint32_t*>(&both);
                 }
             }
-            stsm4_t(vc + at_v(t2 * 16 + (lm >> 1) * 8 + lr, lm & 1), y[0], y[1], y[2], y[3]);
-        }
-        __syncwarp();
-        {
-            bf16* p = static_cast<bf16*>(a.out) + hv * a.Dv + row0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = i * 16 + lane / 2, tok = c * C + t;
-                if (tok < tokens)
-                    *reinterpret_cast<uint4*>(p + (tok0 + tok) * a.Hv * a.Dv + 8 * (lane & 1)) =
-                        *reinterpret_cast<const uint4*>(sm.v[warp][c & 1] + at_v(t, lane & 1));
-            }
-        }
-        __syncwarp();  // read before the next values are fetched into it
-        // S = e^G_C S0 + U' K, U' = e^(G_C - G) U; S and U' share the row's new power of two
-        const float gamma = vec[kGamma * C];
-        float dup[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            dup[h] = scale_to(fmaxf(quad_max(dmost[h]), most[h] * gamma * 0x1p-8f), 12);
-            const float f = gamma * sigma[h] * dup[h];
-            sigma[h] = 1.f / dup[h];
-#pragma unroll
-            for (int t = 0; t < DK / 8; ++t) S[t][2 * h] *= f, S[t][2 * h + 1] *= f;
-        }
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 dd = *reinterpret_cast<const float2*>(vec + kD * C + 8 * (2 * kt + j) + 2 * q4);
-                split(u[2 * kt + j][0] * dd.x * dup[0], u[2 * kt + j][1] * dd.y * dup[0], hi[2 * j], lo[2 * j]);
-                split(u[2 * kt + j][2] * dd.x * dup[1], u[2 * kt + j][3] * dd.y * dup[1], hi[2 * j + 1], lo[2 * j + 1]);
-            }
-#pragma unroll
-            for (int t2 = 0; t2 < DK / 16; ++t2) {
-                uint32_t b[4];
-                ldsm4_t(b, ks + t2 / 4 * (C * 128) + swz(kt * 16 + (lm & 1) * 8 + lr, t2 % 4 * 2 + (lm >> 1)));
-                mma(S[2 * t2], hi, b[0], b[1]);
-                mma(S[2 * t2 + 1], hi, b[2], b[3]);
-                mma(S[2 * t2], lo, b[0], b[1]);
-                mma(S[2 * t2 + 1], lo, b[2], b[3]);
-            }
+            stsm4_t(vc + at_v(t2 * 16 + (lm >> 1) * 8 + lr, lm & 1), x[0], x[1], x[2], x[3]);
         }
         // the stage is free for chunk c + NS
+        __syncwarp();
         if (c + NS < n_chunks) {
-            __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
             if (tid == 0) {
                 if (tc::mbar_wait(&sm.empty[st], (c / NS) & 1, &sm.abort, a.timeout_ns))
@@ -634,6 +853,17 @@ __global__ void __launch_bounds__(32 * W, 1) delta_walk_kernel(const DeltaArgs a
                     *const_cast<volatile int*>(&sm.abort) = 1;  // every warp leaves at its next wait
             }
         }
+        {
+            bf16* op = static_cast<bf16*>(a.out) + hv * a.Dv + row0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = i * 16 + lane / 2, tok = c * C + 32 * p + t;
+                if (tok < tokens)
+                    *reinterpret_cast<uint4*>(op + (tok0 + tok) * a.Hv * a.Dv + 8 * (lane & 1)) =
+                        *reinterpret_cast<const uint4*>(sm.v[warp][c & 1] + at_v(t, lane & 1));
+            }
+        }
+        __syncwarp();  // read before the values after the next are fetched into it
     }
     if (!ok) {  // a wait ran out: record it, let the copies that were issued land, leave the state as it was
         if (lane == 0) {
@@ -650,9 +880,9 @@ __global__ void __launch_bounds__(32 * W, 1) delta_walk_kernel(const DeltaArgs a
     }
     if (!a.state_out) return;
 #pragma unroll
-    for (int t = 0; t < DK / 8; ++t) {
-        *reinterpret_cast<float2*>(a.state_out + state0 + 8 * t) = make_float2(S[t][0] * sigma[0], S[t][1] * sigma[0]);
-        *reinterpret_cast<float2*>(a.state_out + state0 + 8 * DK + 8 * t) = make_float2(S[t][2] * sigma[1], S[t][3] * sigma[1]);
+    for (int t = 0; t < DK / 16; ++t) {
+        *reinterpret_cast<float2*>(a.state_out + state0 + 8 * t) = make_float2(S[t][0], S[t][1]);
+        *reinterpret_cast<float2*>(a.state_out + state0 + 8 * DK + 8 * t) = make_float2(S[t][2], S[t][3]);
     }
 }
 
@@ -671,7 +901,7 @@ cudaError_t launch_walk(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
     cudaError_t e = ensure_smem(delta_walk_kernel<DK, W>, sizeof(WalkSmem<DK, W>), done);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.R * a.Hv * (a.Dv / (16 * W))));
-    return launch_pdl(delta_walk_kernel<DK, W>, grid, dim3(32 * W), sizeof(WalkSmem<DK, W>), s, a, w);
+    return launch_pdl(delta_walk_kernel<DK, W>, grid, dim3(64 * W), sizeof(WalkSmem<DK, W>), s, a, w);
 }
 
 template <int DK>
