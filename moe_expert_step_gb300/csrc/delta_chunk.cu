@@ -29,6 +29,8 @@
 #include "launch.cuh"
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace moestep {
 namespace {
 
@@ -69,12 +71,27 @@ __device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, u
                  : "memory");
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
         "%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the first product of a sum
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+        "%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+template <bool FIRST>
+__device__ __forceinline__ void mma_(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (FIRST)
+        mma0(d, a, b0, b1);
+    else
+        mma(d, a, b0, b1);
+}
+__device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(tc::smem_addr(bar))
@@ -102,19 +119,28 @@ __device__ __forceinline__ float scale_to(float most, int to) {
     if (most == 0.f || e == 255) return 1.f;
     return pow2(min(max(to + 127 - e, -126), 126));
 }
+// 1 / x of a power of two, |exponent| <= 126
+__device__ __forceinline__ float inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+// x^-1/2, rsqrtf and a step of Newton's iteration (the compiler's 1 / sqrtf takes two subroutines)
+__device__ __forceinline__ float inverse_root(float x) {
+    const float y = rsqrtf(x);
+    return x < 3e38f ? y * (1.5f - 0.5f * x * y * y) : 0.f;
+}
 __device__ __forceinline__ float quad_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
-// byte offset of 16-byte piece c of row r in a tile of 128-byte rows
-__device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-
-// the same of row r of block (bi, bj) of a lower triangle; of one without its diagonal
-__device__ __forceinline__ int tri(int bi, int bj, int r, int c) {
-    return (bi * (bi + 1) / 2 + bj) * 512 + r * 32 + ((c ^ (r >> 2 & 1)) << 4);
-}
-__device__ __forceinline__ int below(int bi, int bj, int r, int c) { return tri(bi - 1, bj, r, c); }
+// Every tile is made of 16 x 16 blocks of 512 bytes, rows of 32 bytes whose two halves change places in every second group
+// of four rows, so that the eight rows of a matrix fall into different banks.  An ldmatrix address is then the lane's
+// place in a block, found once, plus a constant.
+__device__ __forceinline__ int in_block(int r, int c) { return r * 32 + ((c ^ (r >> 2 & 1)) << 4); }  // 16-byte half c of row r
+__device__ __forceinline__ constexpr int tri(int bi, int bj) { return (bi * (bi + 1) / 2 + bj) * 512; }  // of a lower triangle
+__device__ __forceinline__ constexpr int below(int bi, int bj) { return tri(bi - 1, bj); }  // of one without its diagonal
+// lanes' places for ldmatrix.x4: with the 8 x 8 matrices in the order of the rows (B operands; outputs transposed), and
+// in the order of the columns (A operands; B operands transposed)
+__device__ __forceinline__ int by_rows(int lane) { return in_block((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1); }
+__device__ __forceinline__ int by_cols(int lane) { return in_block((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4); }
 
 // ---------------------------------------------------------------- first launch: X and P of every chunk
 // A block has one chunk of one key head, four warps with 16 tokens each for the products k.k and q.k.
@@ -160,41 +186,42 @@ __device__ __forceinline__ float exp2_fast(float x) {  // (2^-22 of the value; t
     return y;
 }
 
-// d += a b for operands of two f16 numbers (the product of the low ones is below the others' error)
-__device__ __forceinline__ void mma3(float (&d)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint32_t b0, uint32_t b1,
-                                     uint32_t l0, uint32_t l1) {
-    mma(d, hi, b0, b1);
-    mma(d, lo, b0, b1);
-    mma(d, hi, l0, l1);
+// d += a b for operands of two f16 numbers (the product of the low ones is below the others' error), two tiles at a time
+template <bool FIRST>
+__device__ __forceinline__ void mma3(float (&d0)[4], float (&d1)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                     const uint32_t (&b)[4], const uint32_t (&bl)[4]) {
+    mma_<FIRST>(d0, hi, b[0], b[1]);
+    mma_<FIRST>(d1, hi, b[2], b[3]);
+    mma(d0, lo, b[0], b[1]);
+    mma(d1, lo, b[2], b[3]);
+    mma(d0, hi, bl[0], bl[1]);
+    mma(d1, hi, bl[2], bl[3]);
 }
 
-// Block [n0, n0 + 16 NB) x [m0, m0 + 16) of X, below the diagonal, from the finished blocks: X_A is rows and columns
-// from ma on, X_B from n0 on, both of 16 NB; m0 is one of X_A's column blocks.
+// Blocks [bn, bn + NB) x m of X, below the diagonal, from the finished ones: X_A is block rows and columns from ma on,
+// X_B from bn on, NB each; m is one of X_A's block columns.
 template <int NB>
-__device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t ah, uint32_t al, int ma, int m0, int n0) {
-    const int lane = threadIdx.x % 32, lr = lane & 7, lm = lane >> 3;
+__device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t ah, uint32_t al, int ma, int m, int bn) {
+    const int lane = threadIdx.x % 32, rows = by_rows(lane), cols = in_block((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1);
     float d[2 * NB][4];
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[t][e] = 0.f;
-    // T^T [m][n] = sum_k X_A[k][m] A_BA[n][k]: rows k before m0 are zero
+    // T^T [m][n] = sum_k X_A[k][m] A_BA[n][k]: block rows k before m are zero
 #pragma unroll
     for (int kb = 0; kb < NB; ++kb) {
-        const int k0 = ma + 16 * kb;
-        if (k0 < m0) continue;
+        const int k = ma + kb;
+        if (k < m) continue;
         uint32_t a[4], l[4];
-        const int at = tri(k0 / 16, m0 / 16, (lm >> 1) * 8 + lr, lm & 1);
-        ldsm4_t(a, xh + at);
-        ldsm4_t(l, xl + at);
+        ldsm4_t(a, xh + tri(k, m) + cols);
+        ldsm4_t(l, xl + tri(k, m) + cols);
 #pragma unroll
         for (int t = 0; t < NB; ++t) {
             uint32_t b[4], bl[4];
-            const int bt = below(n0 / 16 + t, k0 / 16, (lm >> 1) * 8 + lr, lm & 1);
-            ldsm4(b, ah + bt);
-            ldsm4(bl, al + bt);
-            mma3(d[2 * t], a, l, b[0], b[1], bl[0], bl[1]);
-            mma3(d[2 * t + 1], a, l, b[2], b[3], bl[2], bl[3]);
+            ldsm4(b, ah + below(bn + t, k) + rows);
+            ldsm4(bl, al + below(bn + t, k) + rows);
+            mma3<false>(d[2 * t], d[2 * t + 1], a, l, b, bl);
         }
     }
     // X_BA^T [m][n] = - sum_k T^T[m][k] X_B[n][k]
@@ -214,11 +241,9 @@ __device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t 
 #pragma unroll
         for (int t = kb; t < NB; ++t) {
             uint32_t b[4], bl[4];
-            const int bt = tri(n0 / 16 + t, n0 / 16 + kb, (lm >> 1) * 8 + lr, lm & 1);
-            ldsm4(b, xh + bt);
-            ldsm4(bl, xl + bt);
-            mma3(y[2 * t], a, l, b[0], b[1], bl[0], bl[1]);
-            mma3(y[2 * t + 1], a, l, b[2], b[3], bl[2], bl[3]);
+            ldsm4(b, xh + tri(bn + t, bn + kb) + rows);
+            ldsm4(bl, xl + tri(bn + t, bn + kb) + rows);
+            mma3<false>(y[2 * t], y[2 * t + 1], a, l, b, bl);
         }
     }
 #pragma unroll
@@ -228,9 +253,8 @@ __device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t 
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) split(y[2 * t + j][2 * h], y[2 * t + j][2 * h + 1], hi[2 * j + h], lo[2 * j + h]);
-        const int at = tri(n0 / 16 + t, m0 / 16, (lm >> 1) * 8 + lr, lm & 1);
-        stsm4_t(xh + at, hi[0], hi[1], hi[2], hi[3]);
-        stsm4_t(xl + at, lo[0], lo[1], lo[2], lo[3]);
+        stsm4_t(xh + tri(bn + t, m) + rows, hi[0], hi[1], hi[2], hi[3]);
+        stsm4_t(xl + tri(bn + t, m) + rows, lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
@@ -299,8 +323,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 #pragma unroll
             for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             if (sub == 0)
-                (which ? sm.cq : sm.ck)[t] = ss == 0.f ? 0.f : a.eps > 0.f ? 1.f / sqrtf(ss + a.eps * up * up) : 1.f / up;
-            *reinterpret_cast<uint4*>((which ? sm.q : sm.k) + sub / 8 * (C * 128) + swz(t, sub % 8)) =
+                (which ? sm.cq : sm.ck)[t] = ss == 0.f ? 0.f : a.eps > 0.f ? inverse_root(ss + a.eps * up * up) : inverse(up);
+            *reinterpret_cast<uint4*>((which ? sm.q : sm.k) + (t / 16 * (DK / 16) + sub / 2) * 512 + in_block(t % 16, sub % 2)) =
                 make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
         }
     }
@@ -318,19 +342,17 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) kk[t][e] = qk[t][e] = 0.f;
     const uint32_t ks = tc::smem_addr(sm.k), qs = tc::smem_addr(sm.q);
-    const int lr = lane & 7, lm = lane >> 3;  // row within a matrix, matrix of ldmatrix.x4
+    const int rows = by_rows(lane), cols = by_cols(lane);
 #pragma unroll 2
     for (int kt = 0; kt < DK / 16; ++kt) {
-        const int base = kt / 4 * (C * 128), c = kt % 4 * 2;
         uint32_t ak[4], aq[4];
-        const int arow = warp * 16 + (lm & 1) * 8 + lr, acol = c + (lm >> 1);
-        ldsm4(ak, ks + base + swz(arow, acol));
-        ldsm4(aq, qs + base + swz(arow, acol));
+        ldsm4(ak, ks + (warp * (DK / 16) + kt) * 512 + cols);
+        ldsm4(aq, qs + (warp * (DK / 16) + kt) * 512 + cols);
 #pragma unroll
         for (int t2 = 0; t2 < 4; ++t2) {
             if (t2 > warp) continue;
             uint32_t b[4];
-            ldsm4(b, ks + base + swz(t2 * 16 + (lm >> 1) * 8 + lr, c + (lm & 1)));
+            ldsm4(b, ks + (t2 * (DK / 16) + kt) * 512 + rows);
             mma(kk[2 * t2], ak, b[0], b[1]);
             mma(kk[2 * t2 + 1], ak, b[2], b[3]);
             mma(qk[2 * t2], aq, b[0], b[1]);
@@ -407,12 +429,12 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
                     } else {
                         uint32_t hi, lo;
                         split(e0 * bc[h] * kk[t][2 * h], e1 * bc[h] * kk[t][2 * h + 1], hi, lo);
-                        *reinterpret_cast<uint32_t*>(bl.ahi + below(warp, t / 2, g4 + 8 * h, t % 2) + 4 * q4) = hi;
-                        *reinterpret_cast<uint32_t*>(bl.alo + below(warp, t / 2, g4 + 8 * h, t % 2) + 4 * q4) = lo;
+                        *reinterpret_cast<uint32_t*>(bl.ahi + below(warp, t / 2) + in_block(g4 + 8 * h, t % 2) + 4 * q4) = hi;
+                        *reinterpret_cast<uint32_t*>(bl.alo + below(warp, t / 2) + in_block(g4 + 8 * h, t % 2) + 4 * q4) = lo;
                     }
                     // (a factor of zero, not a product with what may be inf, above the diagonal)
                     const float p0 = diagonal && j > i ? 0.f : e0 * qk[t][2 * h], p1 = diagonal && j + 1 > i ? 0.f : e1 * qk[t][2 * h + 1];
-                    *reinterpret_cast<uint32_t*>(ps + tri(warp, t / 2, g4 + 8 * h, t % 2) + 4 * q4) = pack(p0, p1);
+                    *reinterpret_cast<uint32_t*>(ps + tri(warp, t / 2) + in_block(g4 + 8 * h, t % 2) + 4 * q4) = pack(p0, p1);
                 }
             }
         }
@@ -432,7 +454,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
                     for (int i = j + 1; i < 16; ++i) x[i] -= at[j][i] * x[j];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int o = tri(b, b, i, c % 16 / 8) + 2 * (c % 8);
+                    const int o = tri(b, b) + in_block(i, c % 16 / 8) + 2 * (c % 8);
                     const __half hi = __float2half_rn(x[i]);
                     *reinterpret_cast<__half*>(xp + o) = hi;
                     *reinterpret_cast<__half*>(xp + kTri + o) = __float2half_rn(x[i] - __half2float(hi));
@@ -442,9 +464,9 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
             const uint32_t ah = tc::smem_addr(sm.blocks[pair].ahi), al = tc::smem_addr(sm.blocks[pair].alo);
             const int w2 = warp % 2;
             __syncwarp();
-            merge_blocks<1>(xh, xl, ah, al, 32 * w2, 32 * w2, 32 * w2 + 16);
+            merge_blocks<1>(xh, xl, ah, al, 2 * w2, 2 * w2, 2 * w2 + 1);
             tc::named_bar_sync(1 + pair, 64);
-            merge_blocks<2>(xh, xl, ah, al, 0, 16 * w2, 32);
+            merge_blocks<2>(xh, xl, ah, al, 0, w2, 2);
             tc::fence_proxy_async_smem();
             tc::named_bar_sync(1 + pair, 64);
         }
@@ -526,14 +548,13 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         bulk_load(tc::smem_addr(s.head), w.heads + ((unit0 + c) * a.Hv + hv) * kHeadBytes, kHeadBytes, bar);
     };
     const uint32_t vs = tc::smem_addr(sm.v[warp]);
-    auto at_v = [&](int t, int c) { return t * 32 + ((c ^ (t >> 2 & 1)) << 4); };
     auto fetch_v = [&](int c) {  // the warp's values, zeros behind the request's tokens
         const bf16* vp = static_cast<const bf16*>(a.v) + hv * a.Dv + row0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = i * 16 + lane / 2, tok = c * C + 32 * p + t;
             const bool on = tok < tokens;
-            cp16(vs + (c & 1) * 1024 + at_v(t, lane & 1), vp + (tok0 + (on ? tok : 0)) * a.v_ld + 8 * (lane & 1), on);
+            cp16(vs + (c & 1) * 1024 + i * 512 + in_block(lane / 2, lane & 1), vp + (tok0 + (on ? tok : 0)) * a.v_ld + 8 * (lane & 1), on);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -555,17 +576,19 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         S[t][0] = x.x, S[t][1] = x.y, S[t][2] = y.x, S[t][3] = y.y;
     }
 
-    const int lr = lane & 7, lm = lane >> 3;
-    const int bar_id = 1 + mine;
+    const int rows = by_rows(lane), cols = by_cols(lane);
+    // Barriers of the slice's warps.  A: both halves of S0 are there, and later U' of the first tokens (the second warp
+    // waits for it before it reports at C, so the first cannot be at A again before it has passed); B: R of the first
+    // tokens; C: U' of the later ones.
+    const int bar_a = 1 + 3 * mine, bar_b = bar_a + 1, bar_c = bar_a + 2;
     bool ok = true;
-    int c = 0;
+    int issued = min(NS, n_chunks);
 #pragma unroll 1
-    for (; c < n_chunks; ++c) {
+    for (int c = 0; c < n_chunks; ++c) {
         const int st = c % NS;
-        // both warps of a slice leave together: the second of them sees a wait that ran out behind the next barrier
-        ok = tc::mbar_wait(&sm.full[st], (c / NS) & 1, &sm.abort, a.timeout_ns);
-        ok = tc::named_bar_and(bar_id, 64, ok);
-        if (!ok) break;
+        // (after a wait that ran out the other waits end at once and no more is fetched: the walk goes on, bounded, over
+        // whatever stands in the tiles, so that nobody is left at a barrier, and nothing of it becomes the state)
+        ok = tc::mbar_wait(&sm.full[st], (c / NS) & 1, &sm.abort, a.timeout_ns) && ok;
         if (c + 1 < n_chunks) {
             fetch_v(c + 1);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -574,7 +597,8 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         }
         __syncwarp();
         typename Smem::Stage& s = sm.st[st];
-        const uint32_t ks = tc::smem_addr(s.k), qs = tc::smem_addr(s.q), xs = tc::smem_addr(s.head);
+        constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
+        const uint32_t kr = tc::smem_addr(s.k) + 2 * p * KB + rows, xr = tc::smem_addr(s.head) + rows;
         const float* vec = reinterpret_cast<const float*>(s.head + 3 * kTri) + 32 * p + 2 * q4;  // of this warp's tokens
         const uint32_t vc = vs + (c & 1) * 1024;
 
@@ -589,30 +613,34 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             up[h] = scale_to(quad_max(most[h]), 12);
-            own[h] = 1.f / up[h];
+            own[h] = inverse(up[h]);
             if (q4 == 0) ps.ds[p][g4 + 8 * h] = own[h];
         }
         float sk[4][4], sq[4][4], zk[4][4], zq[4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sk[t][e] = sq[t][e] = zk[t][e] = zq[t][e] = 0.f;
-        auto half_product = [&](const uint32_t(&hi)[4], const uint32_t(&lo)[4], int kt, float(&k4)[4][4], float(&q4x)[4][4]) {
-            const int base = kt / 4 * (C * 128), cc = kt % 4 * 2;
-#pragma unroll
-            for (int t2 = 0; t2 < 2; ++t2) {
-                uint32_t b[4];
-                const int off = base + swz(32 * p + t2 * 16 + (lm >> 1) * 8 + lr, cc + (lm & 1));
-                ldsm4(b, ks + off);
-                mma(k4[2 * t2], hi, b[0], b[1]);
-                mma(k4[2 * t2 + 1], hi, b[2], b[3]);
-                mma(k4[2 * t2], lo, b[0], b[1]);
-                mma(k4[2 * t2 + 1], lo, b[2], b[3]);
-                ldsm4(b, qs + off);
-                mma(q4x[2 * t2], hi, b[0], b[1]);
-                mma(q4x[2 * t2 + 1], hi, b[2], b[3]);
-            }
+        auto half_product = [&](auto first, const uint32_t(&hi)[4], const uint32_t(&lo)[4], uint32_t kb, float(&x)[4][4],
+                                float(&y)[4][4]) {
+            constexpr bool F = decltype(first)::value;
+            uint32_t b0[4], b1[4], c0[4], c1[4];
+            ldsm4(b0, kb);
+            ldsm4(b1, kb + KB);
+            ldsm4(c0, kb + Tile<DK>::kBytes);
+            ldsm4(c1, kb + Tile<DK>::kBytes + KB);
+            mma_<F>(x[0], hi, b0[0], b0[1]);
+            mma_<F>(x[1], hi, b0[2], b0[3]);
+            mma_<F>(x[2], hi, b1[0], b1[1]);
+            mma_<F>(x[3], hi, b1[2], b1[3]);
+            mma_<F>(y[0], hi, c0[0], c0[1]);
+            mma_<F>(y[1], hi, c0[2], c0[3]);
+            mma_<F>(y[2], hi, c1[0], c1[1]);
+            mma_<F>(y[3], hi, c1[2], c1[3]);
+            mma(x[0], lo, b0[0], b0[1]);
+            mma(x[1], lo, b0[2], b0[3]);
+            mma(x[2], lo, b1[0], b1[1]);
+            mma(x[3], lo, b1[2], b1[3]);
         };
+        const std::true_type first{};
+        const std::false_type then{};
+        const uint32_t k_own = kr + p * (NK * 512), k_other = kr + (1 - p) * (NK * 512);
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
             uint32_t hi[4], lo[4];
@@ -623,22 +651,28 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
             }
             ps.s[p][kt][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             ps.s[p][kt][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            half_product(hi, lo, p * NK + kt, sk, sq);
+            if (kt == 0)
+                half_product(first, hi, lo, k_own + kt * 512, sk, sq);
+            else
+                half_product(then, hi, lo, k_own + kt * 512, sk, sq);
         }
-        tc::named_bar_sync(bar_id, 64);
+        tc::named_bar_sync(bar_a, 64);
         other[0] = ps.ds[1 - p][g4], other[1] = ps.ds[1 - p][g4 + 8];
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
             const uint4 x = ps.s[1 - p][kt][0][lane], y = ps.s[1 - p][kt][1][lane];
             const uint32_t hi[4] = {x.x, x.y, x.z, x.w}, lo[4] = {y.x, y.y, y.z, y.w};
-            half_product(hi, lo, (1 - p) * NK + kt, zk, zq);
+            if (kt == 0)
+                half_product(first, hi, lo, k_other + kt * 512, zk, zq);
+            else
+                half_product(then, hi, lo, k_other + kt * 512, zk, zq);
         }
         // R = beta c (v - e^G c S0 k), in place of S0 K^T
         float rmost[2] = {0.f, 0.f};
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
             uint32_t vv[4];  // tokens 16 t2 ..: columns 0-7, 8-15; tokens 16 t2 + 8 ..: the same
-            ldsm4_t(vv, vc + at_v(t2 * 16 + (lm >> 1) * 8 + lr, lm & 1));
+            ldsm4_t(vv, vc + t2 * 512 + rows);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = 2 * t2 + j;
@@ -652,8 +686,6 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
                     r0 = be.x * (__uint_as_float(x << 16) - av.x * (r0 * own[h] + zk[t][2 * h] * other[h]));
                     r1 = be.y * (__uint_as_float(x & 0xffff0000u) - av.y * (r1 * own[h] + zk[t][2 * h + 1] * other[h]));
                     rmost[h] = fmaxf(rmost[h], fmaxf(fabsf(r0), fabsf(r1)));
-                    sq[t][2 * h] = sq[t][2 * h] * own[h] + zq[t][2 * h] * other[h];
-                    sq[t][2 * h + 1] = sq[t][2 * h + 1] * own[h] + zq[t][2 * h + 1] * other[h];
                 }
             }
         }
@@ -662,22 +694,10 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             rup[h] = scale_to(quad_max(rmost[h]), 12);
-            rdown[h] = 1.f / rup[h];
+            rdown[h] = inverse(rup[h]);
             if (p == 0 && q4 == 0) ps.dr[g4 + 8 * h] = rdown[h];
         }
-        float u[4][4], z[4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[t][e] = z[t][e] = 0.f;
-        auto x_product = [&](const uint32_t(&hi)[4], const uint32_t(&lo)[4], int kt, int t2, float(&d)[4][4]) {
-            uint32_t b[4], bl[4];
-            const int off = tri(2 * p + t2, kt, (lm >> 1) * 8 + lr, lm & 1);
-            ldsm4(b, xs + off);
-            ldsm4(bl, xs + kTri + off);
-            mma3(d[2 * t2], hi, lo, b[0], b[1], bl[0], bl[1]);
-            mma3(d[2 * t2 + 1], hi, lo, b[2], b[3], bl[2], bl[3]);
-        };
+        float u[4][4];
         {
             uint32_t hi[2][4], lo[2][4];
 #pragma unroll
@@ -692,25 +712,43 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
                     ps.r[kt][1][lane] = make_uint4(lo[kt][0], lo[kt][1], lo[kt][2], lo[kt][3]);
                 }
             }
-            if (p == 0) tc::named_bar_sync(bar_id, 64);
-            x_product(hi[0], lo[0], 2 * p, 0, u);
-            x_product(hi[0], lo[0], 2 * p, 1, u);
-            x_product(hi[1], lo[1], 2 * p + 1, 1, u);
+            if (p == 0) bar_arrive(bar_b, 64);
+            const uint32_t x0 = xr + (p ? tri(2, 2) : tri(0, 0)), x1 = xr + (p ? tri(3, 2) : tri(1, 0));
+            uint32_t b0[4], l0[4], b1[4], l1[4], b2[4], l2[4];
+            ldsm4(b0, x0);
+            ldsm4(l0, x0 + kTri);
+            ldsm4(b1, x1);
+            ldsm4(l1, x1 + kTri);
+            ldsm4(b2, x1 + 512);
+            ldsm4(l2, x1 + 512 + kTri);
+            mma3<true>(u[0], u[1], hi[0], lo[0], b0, l0);
+            mma3<true>(u[2], u[3], hi[0], lo[0], b1, l1);
+            mma3<false>(u[2], u[3], hi[1], lo[1], b2, l2);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) u[t][e] *= rdown[e / 2];
         if (p == 1) {
-            tc::named_bar_sync(bar_id, 64);
+            float z[4][4];
+            uint32_t b0[4], l0[4], b1[4], l1[4], b2[4], l2[4], b3[4], l3[4];
+            ldsm4(b0, xr + tri(2, 0));
+            ldsm4(l0, xr + tri(2, 0) + kTri);
+            ldsm4(b1, xr + tri(3, 0));
+            ldsm4(l1, xr + tri(3, 0) + kTri);
+            ldsm4(b2, xr + tri(2, 1));
+            ldsm4(l2, xr + tri(2, 1) + kTri);
+            ldsm4(b3, xr + tri(3, 1));
+            ldsm4(l3, xr + tri(3, 1) + kTri);
+            tc::named_bar_sync(bar_b, 64);
             const float f[2] = {ps.dr[g4], ps.dr[g4 + 8]};
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-                const uint4 x = ps.r[kt][0][lane], y = ps.r[kt][1][lane];
-                const uint32_t hi[4] = {x.x, x.y, x.z, x.w}, lo[4] = {y.x, y.y, y.z, y.w};
-                x_product(hi, lo, kt, 0, z);
-                x_product(hi, lo, kt, 1, z);
-            }
+            const uint4 h0 = ps.r[0][0][lane], g0 = ps.r[0][1][lane], h1 = ps.r[1][0][lane], g1 = ps.r[1][1][lane];
+            const uint32_t hi0[4] = {h0.x, h0.y, h0.z, h0.w}, lo0[4] = {g0.x, g0.y, g0.z, g0.w};
+            const uint32_t hi1[4] = {h1.x, h1.y, h1.z, h1.w}, lo1[4] = {g1.x, g1.y, g1.z, g1.w};
+            mma3<true>(z[0], z[1], hi0, lo0, b0, l0);
+            mma3<true>(z[2], z[3], hi0, lo0, b1, l1);
+            mma3<false>(z[0], z[1], hi1, lo1, b2, l2);
+            mma3<false>(z[2], z[3], hi1, lo1, b3, l3);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -734,8 +772,8 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         for (int h = 0; h < 2; ++h) {
             uup[h] = scale_to(quad_max(umost[h]), 12);
             dup[h] = scale_to(quad_max(dmost[h]), 12);
-            udown[h] = 1.f / uup[h];
-            ddown[h] = 1.f / dup[h];
+            udown[h] = inverse(uup[h]);
+            ddown[h] = inverse(dup[h]);
             if (q4 == 0) {
                 ps.dd[p][g4 + 8 * h] = ddown[h];
                 if (p == 0) ps.du[g4 + 8 * h] = udown[h];
@@ -756,74 +794,90 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
             ps.d[p][kt][1][lane] = make_uint4(dlo[kt][0], dlo[kt][1], dlo[kt][2], dlo[kt][3]);
             if (p == 0) ps.u[kt][lane] = make_uint4(uh[kt][0], uh[kt][1], uh[kt][2], uh[kt][3]);
         }
-        tc::named_bar_sync(bar_id, 64);
-        // S = e^G_C S0 + U' e^(G_C - G) K on the warp's columns (sums of their own, added in fp32: an MMA cuts off what it
-        // adds to a large accumulator)
+        if (p == 0) {
+            bar_arrive(bar_a, 64);
+        } else {
+            tc::named_bar_sync(bar_a, 64);
+            bar_arrive(bar_c, 64);
+        }
+        // S = e^G_C S0 + U' e^(G_C - G) K on the warp's columns, with its own tokens and then with the other's (sums of
+        // their own, added in fp32: an MMA cuts off what it adds to a large accumulator)
+        float d[DK / 16][4];
+        auto state_product = [&](const uint32_t(&hi)[2][4], const uint32_t(&lo)[2][4], int half) {
+            const uint32_t kc = tc::smem_addr(s.k) + half * (2 * KB) + p * (NK * 512) + cols;
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int t2 = 0; t2 < NK; t2 += 2) {
+                    uint32_t b0[4], b1[4];
+                    ldsm4_t(b0, kc + kt * KB + t2 * 512);
+                    ldsm4_t(b1, kc + kt * KB + t2 * 512 + 512);
+                    if (kt == 0) {
+                        mma0(d[2 * t2], hi[kt], b0[0], b0[1]);
+                        mma0(d[2 * t2 + 1], hi[kt], b0[2], b0[3]);
+                        mma0(d[2 * t2 + 2], hi[kt], b1[0], b1[1]);
+                        mma0(d[2 * t2 + 3], hi[kt], b1[2], b1[3]);
+                    } else {
+                        mma(d[2 * t2], hi[kt], b0[0], b0[1]);
+                        mma(d[2 * t2 + 1], hi[kt], b0[2], b0[3]);
+                        mma(d[2 * t2 + 2], hi[kt], b1[0], b1[1]);
+                        mma(d[2 * t2 + 3], hi[kt], b1[2], b1[3]);
+                    }
+                    mma(d[2 * t2], lo[kt], b0[0], b0[1]);
+                    mma(d[2 * t2 + 1], lo[kt], b0[2], b0[3]);
+                    mma(d[2 * t2 + 2], lo[kt], b1[0], b1[1]);
+                    mma(d[2 * t2 + 3], lo[kt], b1[2], b1[3]);
+                }
+        };
+        state_product(dhi, dlo, p);
         {
             const float gamma = *(reinterpret_cast<const float*>(s.head + 3 * kTri) + kGamma * C);
-            const float f[2] = {ps.dd[1 - p][g4], ps.dd[1 - p][g4 + 8]};
-            uint32_t ehi[2][4], elo[2][4];
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-                const uint4 x = ps.d[1 - p][kt][0][lane], y = ps.d[1 - p][kt][1][lane];
-                ehi[kt][0] = x.x, ehi[kt][1] = x.y, ehi[kt][2] = x.z, ehi[kt][3] = x.w;
-                elo[kt][0] = y.x, elo[kt][1] = y.y, elo[kt][2] = y.z, elo[kt][3] = y.w;
-            }
+            for (int t = 0; t < DK / 16; ++t)
 #pragma unroll
-            for (int t2 = 0; t2 < DK / 32; ++t2) {
-                float d[2][2][4];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) (&d[0][0][0])[i] = 0.f;
-                const int col = p * (DK / 32) + t2;  // of 16 columns of K
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt) {
-                    uint32_t b[4];
-                    const int cb = ks + col / 4 * (C * 128), cp = col % 4 * 2 + (lm >> 1), rw = kt * 16 + (lm & 1) * 8 + lr;
-                    ldsm4_t(b, cb + swz(32 * p + rw, cp));
-                    mma(d[0][0], dhi[kt], b[0], b[1]);
-                    mma(d[0][1], dhi[kt], b[2], b[3]);
-                    mma(d[0][0], dlo[kt], b[0], b[1]);
-                    mma(d[0][1], dlo[kt], b[2], b[3]);
-                    ldsm4_t(b, cb + swz(32 * (1 - p) + rw, cp));
-                    mma(d[1][0], ehi[kt], b[0], b[1]);
-                    mma(d[1][1], ehi[kt], b[2], b[3]);
-                    mma(d[1][0], elo[kt], b[0], b[1]);
-                    mma(d[1][1], elo[kt], b[2], b[3]);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float& x = S[2 * t2 + j][e];
-                        x = x * gamma + (d[0][j][e] * ddown[e / 2] + d[1][j][e] * f[e / 2]);
-                    }
-            }
+                for (int e = 0; e < 4; ++e) S[t][e] = S[t][e] * gamma + d[t][e] * ddown[e / 2];
         }
         // O = e^G scale S0 Q^T + U' P^T
-        float o[4][4], y[4][4];
+        float o[4][4];
+        {
+            const uint32_t x0 = xr + 2 * kTri + (p ? tri(2, 2) : tri(0, 0)), x1 = xr + 2 * kTri + (p ? tri(3, 2) : tri(1, 0));
+            uint32_t b0[4], b1[4], b2[4];
+            ldsm4(b0, x0);
+            ldsm4(b1, x1);
+            ldsm4(b2, x1 + 512);
+            mma0(o[0], uh[0], b0[0], b0[1]);
+            mma0(o[1], uh[0], b0[2], b0[3]);
+            mma0(o[2], uh[0], b1[0], b1[1]);
+            mma0(o[3], uh[0], b1[2], b1[3]);
+            mma(o[2], uh[1], b2[0], b2[1]);
+            mma(o[3], uh[1], b2[2], b2[3]);
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][e] = y[t][e] = 0.f;
-        auto p_product = [&](const uint32_t(&hi)[4], int kt, int t2, float(&d)[4][4]) {
-            uint32_t b[4];
-            ldsm4(b, xs + 2 * kTri + tri(2 * p + t2, kt, (lm >> 1) * 8 + lr, lm & 1));
-            mma(d[2 * t2], hi, b[0], b[1]);
-            mma(d[2 * t2 + 1], hi, b[2], b[3]);
-        };
-        p_product(uh[0], 2 * p, 0, o);
-        p_product(uh[0], 2 * p, 1, o);
-        p_product(uh[1], 2 * p + 1, 1, o);
-        float uf[2] = {0.f, 0.f};
+            for (int e = 0; e < 4; ++e) o[t][e] *= udown[e / 2];
         if (p == 1) {
-            uf[0] = ps.du[g4], uf[1] = ps.du[g4 + 8];
+            float y[4][4];
+            uint32_t b0[4], b1[4], b2[4], b3[4];
+            ldsm4(b0, xr + 2 * kTri + tri(2, 0));
+            ldsm4(b1, xr + 2 * kTri + tri(3, 0));
+            ldsm4(b2, xr + 2 * kTri + tri(2, 1));
+            ldsm4(b3, xr + 2 * kTri + tri(3, 1));
+            const float f[2] = {ps.du[g4], ps.du[g4 + 8]};
+            const uint4 h0 = ps.u[0][lane], h1 = ps.u[1][lane];
+            const uint32_t a0[4] = {h0.x, h0.y, h0.z, h0.w}, a1[4] = {h1.x, h1.y, h1.z, h1.w};
+            mma0(y[0], a0, b0[0], b0[1]);
+            mma0(y[1], a0, b0[2], b0[3]);
+            mma0(y[2], a0, b1[0], b1[1]);
+            mma0(y[3], a0, b1[2], b1[3]);
+            mma(y[0], a1, b2[0], b2[1]);
+            mma(y[1], a1, b2[2], b2[3]);
+            mma(y[2], a1, b3[0], b3[1]);
+            mma(y[3], a1, b3[2], b3[3]);
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-                const uint4 x = ps.u[kt][lane];
-                const uint32_t hi[4] = {x.x, x.y, x.z, x.w};
-                p_product(hi, kt, 0, y);
-                p_product(hi, kt, 1, y);
-            }
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][e] += y[t][e] * f[e / 2];
         }
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {  // the values have been read: their place takes the outputs
@@ -835,24 +889,15 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
                 const float2 pi = *reinterpret_cast<const float2*>(vec + kPi * C + 8 * t);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float o0 = o[t][2 * h] * udown[h] + y[t][2 * h] * uf[h], o1 = o[t][2 * h + 1] * udown[h] + y[t][2 * h + 1] * uf[h];
-                    const __nv_bfloat162 both = __floats2bfloat162_rn(b.x * sq[t][2 * h] + pi.x * o0, b.y * sq[t][2 * h + 1] + pi.y * o1);
+                    const float q0 = sq[t][2 * h] * own[h] + zq[t][2 * h] * other[h];
+                    const float q1 = sq[t][2 * h + 1] * own[h] + zq[t][2 * h + 1] * other[h];
+                    const __nv_bfloat162 both = __floats2bfloat162_rn(b.x * q0 + pi.x * o[t][2 * h], b.y * q1 + pi.y * o[t][2 * h + 1]);
                     x[2 * j + h] = *reinterpret_cast<const uint32_t*>(&both);
                 }
             }
-            stsm4_t(vc + at_v(t2 * 16 + (lm >> 1) * 8 + lr, lm & 1), x[0], x[1], x[2], x[3]);
+            stsm4_t(vc + t2 * 512 + rows, x[0], x[1], x[2], x[3]);
         }
-        // the stage is free for chunk c + NS
         __syncwarp();
-        if (c + NS < n_chunks) {
-            if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
-            if (tid == 0) {
-                if (tc::mbar_wait(&sm.empty[st], (c / NS) & 1, &sm.abort, a.timeout_ns))
-                    fetch(c + NS);
-                else
-                    *const_cast<volatile int*>(&sm.abort) = 1;  // every warp leaves at its next wait
-            }
-        }
         {
             bf16* op = static_cast<bf16*>(a.out) + hv * a.Dv + row0;
 #pragma unroll
@@ -860,11 +905,41 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
                 const int t = i * 16 + lane / 2, tok = c * C + 32 * p + t;
                 if (tok < tokens)
                     *reinterpret_cast<uint4*>(op + (tok0 + tok) * a.Hv * a.Dv + 8 * (lane & 1)) =
-                        *reinterpret_cast<const uint4*>(sm.v[warp][c & 1] + at_v(t, lane & 1));
+                        *reinterpret_cast<const uint4*>(sm.v[warp][c & 1] + i * 512 + in_block(lane / 2, lane & 1));
             }
         }
-        __syncwarp();  // read before the values after the next are fetched into it
+        // the other warp's tokens
+        if (p == 0) tc::named_bar_sync(bar_c, 64);
+        {
+            const float f[2] = {ps.dd[1 - p][g4], ps.dd[1 - p][g4 + 8]};
+            uint32_t ehi[2][4], elo[2][4];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                const uint4 x = ps.d[1 - p][kt][0][lane], y = ps.d[1 - p][kt][1][lane];
+                ehi[kt][0] = x.x, ehi[kt][1] = x.y, ehi[kt][2] = x.z, ehi[kt][3] = x.w;
+                elo[kt][0] = y.x, elo[kt][1] = y.y, elo[kt][2] = y.z, elo[kt][3] = y.w;
+            }
+            state_product(ehi, elo, 1 - p);
+#pragma unroll
+            for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[t][e] += d[t][e] * f[e / 2];
+        }
+        // the stage is free for chunk c + NS
+        if (c + NS < n_chunks) {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
+            if (tid == 0) {
+                ok = ok && tc::mbar_wait(&sm.empty[st], (c / NS) & 1, &sm.abort, a.timeout_ns);
+                if (ok)
+                    fetch(issued++);
+                else
+                    *const_cast<volatile int*>(&sm.abort) = 1;
+            }
+        }
+        __syncwarp();
     }
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) {  // a wait ran out: record it, let the copies that were issued land, leave the state as it was
         if (lane == 0) {
             *const_cast<volatile int*>(&sm.abort) = 1;
@@ -873,7 +948,7 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (tid == 0) {
             int zero = 0;
-            for (int i = c; i < c + NS && i < n_chunks; ++i)
+            for (int i = max(0, issued - NS); i < issued; ++i)
                 tc::mbar_wait(&sm.full[i % NS], (i / NS) & 1, &zero, 1000000000ull);
         }
         return;
