@@ -105,12 +105,14 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float2 unpack(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 // two values as the sum of two f16 pairs
 __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
     hi = pack(x, y);
-    const float2 h = unpack(hi);
-    lo = pack(x - h.x, y - h.y);
+    float lx, ly;  // x - hi
+    asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tfma.rn.f32.f16 %0, p, %5, %3;\n\tfma.rn.f32.f16 %1, q, %5, %4;\n\t}"
+        : "=f"(lx), "=f"(ly)
+        : "r"(hi), "f"(x), "f"(y), "h"(static_cast<unsigned short>(0xbc00)));  // -1
+    lo = pack(lx, ly);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // |e| <= 126
 // a power of two that brings `most` to [2^to, 2^(to+1)); 1 for zeros and what is not finite
@@ -482,49 +484,59 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 
 // ---------------------------------------------------------------- second launch: the states' walk
 // A slice of 16 rows of the transposed state is walked by two warps.  Warp p keeps columns [DK / 2 p, DK / 2 (p + 1)) of
-// the rows and takes tokens [32 p, 32 p + 32) of R, U and O; the operands that the other one needs (its half of the
+// the rows and takes tokens [32 p, 32 p + 32) of R and U; the operands that the other one needs (its half of the
 // state, R of the first tokens, U') pass through shared memory as f16 pairs in the A operand's layout, each
-// half with row scales of its own, so that nothing has to be agreed on before.
+// half with row scales of its own, so that nothing has to be agreed on before.  The outputs are no part of the chain of
+// states: a third warp makes them from the same operands, up to a chunk later, and also fetches the tiles.
 //
-// Bound: a warp's dependent chain of about 1100 instructions a chunk, 200 of them MMAs at 8 cycles, while there are fewer
-// than two warps a scheduler; with more, the rate of mma.sync (1024 multiplications a cycle and multiprocessor; 400
-// MMAs a slice and chunk).
+// Bound: a warp's dependent chain of instructions (170 of them MMAs at 8 cycles), while there are fewer than two or three
+// warps a scheduler; with more, the rate of mma.sync (1024 multiplications a cycle and multiprocessor; 400 MMAs a
+// slice and chunk).
 template <int DK, int W>
 struct WalkSmem {
-    static constexpr int kStages = 2;
+    static constexpr int kStages = W <= 2 ? 3 : 2;
     struct Stage {
         char k[Tile<DK>::kBytes];
         char q[Tile<DK>::kBytes];
         char head[kHeadBytes];
     };
     alignas(128) Stage st[kStages];
-    struct Pass {                      // from warp p of a slice to the other
-        uint4 s[2][DK / 32][2][32];    // [p][k step][high, low][lane]
-        uint4 d[2][2][2][32];          // U' e^(G_C - G)
-        uint4 r[2][2][32];             // R of the first 32 tokens
-        uint4 u[2][32];                // U' of the first 32 tokens (high)
-        float ds[2][16], dd[2][16], dr[16], du[16];  // factors of their rows
+    struct Pass {                    // of a slice, from warp p to the others
+        uint4 s[2][2][DK / 32][32];  // [chunk % 2][p][k step][lane]: S0, high
+        uint4 sl[2][DK / 32][32];    // low
+        uint4 u[2][2][2][32];        // [chunk % 2][p][k step][lane]: U', high
+        uint4 d[2][2][2][32];        // [p][k step][high, low][lane]: U' e^(G_C - G)
+        uint4 r[2][2][32];           // R of the first 32 tokens
+        float ds[2][2][16], du[2][2][16], dd[2][16], dr[16];  // factors of their rows
     } pass[W];
-    char v[2 * W][2][32 * 32];  // a warp's 32 tokens of 16 values, then of outputs
+    char v[2 * W][2][32 * 32];  // a warp's 32 tokens of 16 values
+    char o[W][C * 32];          // 64 tokens of 16 outputs
     uint64_t full[kStages], empty[kStages];
-    int abort;
+    uint64_t given[W][2], taken[W][2];  // S0 and U' of chunk % 2 for the third warp
+    int abort, request;
 };
 
 template <int DK, int W>
-__global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
+__global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
     extern __shared__ __align__(128) char raw[];
     using Smem = WalkSmem<DK, W>;
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     constexpr int NS = Smem::kStages;
     constexpr int NK = DK / 32;  // k steps of 16 of a half of the state's columns
     constexpr uint32_t kQk = 2 * Tile<DK>::kBytes;
+    constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g4 = lane / 4, q4 = lane % 4;
-    const int mine = warp / 2, p = warp % 2;  // slice of the block, part of it
+    const bool outputs = warp >= 2 * W;
+    const int mine = outputs ? warp - 2 * W : warp / 2, p = warp % 2;  // slice of the block, part of it
     typename Smem::Pass& ps = sm.pass[mine];
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             tc::mbar_init(&sm.full[i], 1);
-            tc::mbar_init(&sm.empty[i], 2 * W);
+            tc::mbar_init(&sm.empty[i], 3 * W);
+        }
+        for (int i = 0; i < 2 * W; ++i) {
+            tc::mbar_init(&sm.given[0][i], 2);
+            tc::mbar_init(&sm.taken[0][i], 1);
         }
         sm.abort = 0;
         tc::fence_mbar_init();
@@ -532,21 +544,168 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
     pdl_trigger();
     pdl_wait();
     const int slices = a.Dv / (16 * W);
-    const int slice = blockIdx.x % slices, hv = blockIdx.x / slices % a.Hv, r = blockIdx.x / slices / a.Hv;
+    const int slice = blockIdx.x % slices, hv = blockIdx.x / slices % a.Hv;
+    int r = blockIdx.x / slices / a.Hv;
+    if (a.length && a.R <= 64) {  // long requests first, so that none begins when the others end
+        if (tid < a.R) {
+            const int len = __ldg(&a.length[tid]);
+            int rank = 0;
+            for (int j = 0; j < a.R; ++j) {
+                const int other = __ldg(&a.length[j]);
+                rank += other > len || (other == len && j < tid);
+            }
+            if (rank == r) sm.request = tid;
+        }
+        __syncthreads();
+        r = sm.request;
+    }
     int tokens, slot;
     if (!delta_request(a, r, tid == 0 && slice == 0 && hv == 0, tokens, slot)) return;
     __syncthreads();
     const int hk = hv / (a.Hv / a.Hk), n_chunks = (tokens + C - 1) / C;
     const int row0 = (slice * W + mine) * 16;  // first of the slice's rows
     const long long tok0 = 1ll * r * a.n, unit0 = 1ll * r * w.chunks;
-
-    auto fetch = [&](int c) {  // by one thread: chunk c into its stage
-        typename Smem::Stage& s = sm.st[c % NS];
-        uint64_t* bar = &sm.full[c % NS];
-        tc::mbar_arrive_expect_tx(bar, kQk + kHeadBytes);
-        bulk_load(tc::smem_addr(s.k), w.qk + ((unit0 + c) * a.Hk + hk) * kQk, kQk, bar);
-        bulk_load(tc::smem_addr(s.head), w.heads + ((unit0 + c) * a.Hv + hv) * kHeadBytes, kHeadBytes, bar);
+    const int rows = by_rows(lane), cols = by_cols(lane);
+    // (after a wait that ran out the other waits end at once and no more is fetched: the walk goes on, bounded, over
+    // whatever stands in the tiles, so that nobody is left at a barrier, and the error is recorded)
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) {
+        if (tc::mbar_wait(bar, phase & 1, &sm.abort, a.timeout_ns)) return;
+        ok = false;
+        *const_cast<volatile int*>(&sm.abort) = 1;
     };
+
+    if (outputs) {
+        const bool fetches = mine == 0 && lane == 0;
+        int issued = 0;
+        auto fetch = [&]() {  // the next chunk into its stage
+            typename Smem::Stage& s = sm.st[issued % NS];
+            uint64_t* bar = &sm.full[issued % NS];
+            tc::mbar_arrive_expect_tx(bar, kQk + kHeadBytes);
+            bulk_load(tc::smem_addr(s.k), w.qk + ((unit0 + issued) * a.Hk + hk) * kQk, kQk, bar);
+            bulk_load(tc::smem_addr(s.head), w.heads + ((unit0 + issued) * a.Hv + hv) * kHeadBytes, kHeadBytes, bar);
+            ++issued;
+        };
+        if (fetches)
+            while (issued < NS && issued < n_chunks) fetch();
+        const uint32_t os = tc::smem_addr(sm.o[mine]);
+#pragma unroll 1
+        for (int c = 0; c < n_chunks; ++c) {
+            const int st = c % NS, cb = c & 1;
+            wait(&sm.given[mine][cb], c >> 1);  // (after the tiles' barrier in time, but that one has to be seen here too)
+            wait(&sm.full[st], c / NS);
+            __syncwarp();
+            typename Smem::Stage& s = sm.st[st];
+            const uint32_t qr = tc::smem_addr(s.q) + rows, pr = tc::smem_addr(s.head) + 2 * kTri + rows;
+            const float* vec = reinterpret_cast<const float*>(s.head + 3 * kTri) + 2 * q4;
+            // S0 Q^T, with the columns of each half of S0 and their scale
+            float o[8][4];
+            {
+                float x[8][4];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int kt = 0; kt < NK; ++kt) {
+                        const uint4 y = ps.s[cb][half][kt][lane];
+                        const uint32_t hi[4] = {y.x, y.y, y.z, y.w};
+                        uint32_t b[4][4];
+#pragma unroll
+                        for (int t2 = 0; t2 < 4; ++t2) ldsm4(b[t2], qr + t2 * KB + (half * NK + kt) * 512);
+#pragma unroll
+                        for (int t2 = 0; t2 < 4; ++t2) {
+                            if (kt == 0) {
+                                mma0(x[2 * t2], hi, b[t2][0], b[t2][1]);
+                                mma0(x[2 * t2 + 1], hi, b[t2][2], b[t2][3]);
+                            } else {
+                                mma(x[2 * t2], hi, b[t2][0], b[t2][1]);
+                                mma(x[2 * t2 + 1], hi, b[t2][2], b[t2][3]);
+                            }
+                        }
+                    }
+                    const float f[2] = {ps.ds[cb][half][g4], ps.ds[cb][half][g4 + 8]};
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[t][e] = half ? o[t][e] + x[t][e] * f[e / 2] : x[t][e] * f[e / 2];
+                }
+            }
+            // + P U', scaled by the token's factors
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 b = *reinterpret_cast<const float2*>(vec + kB * C + 8 * t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][e] *= e % 2 ? b.y : b.x;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float x[8][4];
+                const uint4 y0 = ps.u[cb][half][0][lane], y1 = ps.u[cb][half][1][lane];
+                const uint32_t u0[4] = {y0.x, y0.y, y0.z, y0.w}, u1[4] = {y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                for (int t2 = 2 * half; t2 < 4; ++t2) {
+                    uint32_t b[4];
+                    ldsm4(b, pr + tri(t2, 2 * half));
+                    mma0(x[2 * t2], u0, b[0], b[1]);
+                    mma0(x[2 * t2 + 1], u0, b[2], b[3]);
+                }
+#pragma unroll
+                for (int t2 = 2 * half + 1; t2 < 4; ++t2) {
+                    uint32_t b[4];
+                    ldsm4(b, pr + tri(t2, 2 * half + 1));
+                    mma(x[2 * t2], u1, b[0], b[1]);
+                    mma(x[2 * t2 + 1], u1, b[2], b[3]);
+                }
+                const float f[2] = {ps.du[cb][half][g4], ps.du[cb][half][g4 + 8]};
+#pragma unroll
+                for (int t = 4 * half; t < 8; ++t) {
+                    const float2 pi = *reinterpret_cast<const float2*>(vec + kPi * C + 8 * t);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][e] += (e % 2 ? pi.y : pi.x) * (x[t][e] * f[e / 2]);
+                }
+            }
+            __syncwarp();  // S0, U' and the tiles have been read
+            if (lane == 0) {
+                tc::mbar_arrive(&sm.empty[st]);  // (in this order: whoever sees S0 and U' taken may be at the tiles' next phase)
+                tc::mbar_arrive(&sm.taken[mine][cb]);
+            }
+#pragma unroll
+            for (int t2 = 0; t2 < 4; ++t2) {
+                uint32_t x[4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const __nv_bfloat162 both = __floats2bfloat162_rn(o[2 * t2 + j][2 * h], o[2 * t2 + j][2 * h + 1]);
+                        x[2 * j + h] = *reinterpret_cast<const uint32_t*>(&both);
+                    }
+                stsm4_t(os + t2 * 512 + rows, x[0], x[1], x[2], x[3]);
+            }
+            __syncwarp();
+            bf16* op = static_cast<bf16*>(a.out) + hv * a.Dv + row0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = c * C + i * 16 + lane / 2;
+                if (tok < tokens)
+                    *reinterpret_cast<uint4*>(op + (tok0 + tok) * a.Hv * a.Dv + 8 * (lane & 1)) =
+                        *reinterpret_cast<const uint4*>(sm.o[mine] + i * 512 + in_block(lane / 2, lane & 1));
+            }
+            if (fetches && issued < n_chunks) {  // the stage that chunk c has left
+                wait(&sm.empty[st], c / NS);
+                if (ok && !*const_cast<volatile int*>(&sm.abort)) fetch();
+            }
+            __syncwarp();
+        }
+        if (!__all_sync(0xffffffffu, ok)) {  // a wait ran out: record it and let the copies that were issued land
+            if (lane == 0) record_error(a.err, kErrTimeoutEpilogue);
+            if (fetches) {
+                int zero = 0;
+                for (int i = max(0, issued - NS); i < issued; ++i)
+                    tc::mbar_wait(&sm.full[i % NS], (i / NS) & 1, &zero, 1000000000ull);
+            }
+        }
+        return;
+    }
+
     const uint32_t vs = tc::smem_addr(sm.v[warp]);
     auto fetch_v = [&](int c) {  // the warp's values, zeros behind the request's tokens
         const bf16* vp = static_cast<const bf16*>(a.v) + hv * a.Dv + row0;
@@ -558,8 +717,6 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    if (tid == 0)
-        for (int c = 0; c < NS && c < n_chunks; ++c) fetch(c);
     if (n_chunks > 0) fetch_v(0);
 
     // rows g4 and g4 + 8 of the slice, columns DK / 2 p + 8 t + 2 q4 + {0, 1}
@@ -576,19 +733,15 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         S[t][0] = x.x, S[t][1] = x.y, S[t][2] = y.x, S[t][3] = y.y;
     }
 
-    const int rows = by_rows(lane), cols = by_cols(lane);
     // Barriers of the slice's warps.  A: both halves of S0 are there, and later U' of the first tokens (the second warp
-    // waits for it before it reports at C, so the first cannot be at A again before it has passed); B: R of the first
-    // tokens; C: U' of the later ones.
+    // waits for it before it reports at C, so that the first cannot be at A again before it has passed); B: R of the
+    // first tokens; C: U' of the later ones.
     const int bar_a = 1 + 3 * mine, bar_b = bar_a + 1, bar_c = bar_a + 2;
-    bool ok = true;
-    int issued = min(NS, n_chunks);
 #pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
-        const int st = c % NS;
-        // (after a wait that ran out the other waits end at once and no more is fetched: the walk goes on, bounded, over
-        // whatever stands in the tiles, so that nobody is left at a barrier, and nothing of it becomes the state)
-        ok = tc::mbar_wait(&sm.full[st], (c / NS) & 1, &sm.abort, a.timeout_ns) && ok;
+        const int st = c % NS, cb = c & 1;
+        wait(&sm.full[st], c / NS);
+        if (c >= 2) wait(&sm.taken[mine][cb], (c >> 1) - 1);
         if (c + 1 < n_chunks) {
             fetch_v(c + 1);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -597,13 +750,11 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         }
         __syncwarp();
         typename Smem::Stage& s = sm.st[st];
-        constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
         const uint32_t kr = tc::smem_addr(s.k) + 2 * p * KB + rows, xr = tc::smem_addr(s.head) + rows;
         const float* vec = reinterpret_cast<const float*>(s.head + 3 * kTri) + 32 * p + 2 * q4;  // of this warp's tokens
         const uint32_t vc = vs + (c & 1) * 1024;
 
-        // S0 K^T (pairs of f16) and S0 Q^T (one f16) of the warp's tokens: first with its own columns of S0, then
-        // with the other's
+        // S0 K^T of the warp's tokens: first with its own columns of S0, then with the other's
         float most[2] = {0.f, 0.f}, up[2], own[2], other[2];
 #pragma unroll
         for (int t = 0; t < DK / 16; ++t) {
@@ -614,25 +765,18 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
         for (int h = 0; h < 2; ++h) {
             up[h] = scale_to(quad_max(most[h]), 12);
             own[h] = inverse(up[h]);
-            if (q4 == 0) ps.ds[p][g4 + 8 * h] = own[h];
+            if (q4 == 0) ps.ds[cb][p][g4 + 8 * h] = own[h];
         }
-        float sk[4][4], sq[4][4], zk[4][4], zq[4][4];
-        auto half_product = [&](auto first, const uint32_t(&hi)[4], const uint32_t(&lo)[4], uint32_t kb, float(&x)[4][4],
-                                float(&y)[4][4]) {
+        float sk[4][4], zk[4][4];
+        auto half_product = [&](auto first, const uint32_t(&hi)[4], const uint32_t(&lo)[4], uint32_t kb, float(&x)[4][4]) {
             constexpr bool F = decltype(first)::value;
-            uint32_t b0[4], b1[4], c0[4], c1[4];
+            uint32_t b0[4], b1[4];
             ldsm4(b0, kb);
             ldsm4(b1, kb + KB);
-            ldsm4(c0, kb + Tile<DK>::kBytes);
-            ldsm4(c1, kb + Tile<DK>::kBytes + KB);
             mma_<F>(x[0], hi, b0[0], b0[1]);
             mma_<F>(x[1], hi, b0[2], b0[3]);
             mma_<F>(x[2], hi, b1[0], b1[1]);
             mma_<F>(x[3], hi, b1[2], b1[3]);
-            mma_<F>(y[0], hi, c0[0], c0[1]);
-            mma_<F>(y[1], hi, c0[2], c0[3]);
-            mma_<F>(y[2], hi, c1[0], c1[1]);
-            mma_<F>(y[3], hi, c1[2], c1[3]);
             mma(x[0], lo, b0[0], b0[1]);
             mma(x[1], lo, b0[2], b0[3]);
             mma(x[2], lo, b1[0], b1[1]);
@@ -649,23 +793,23 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
                 split(S[2 * kt + j][0] * up[0], S[2 * kt + j][1] * up[0], hi[2 * j], lo[2 * j]);
                 split(S[2 * kt + j][2] * up[1], S[2 * kt + j][3] * up[1], hi[2 * j + 1], lo[2 * j + 1]);
             }
-            ps.s[p][kt][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            ps.s[p][kt][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            ps.s[cb][p][kt][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            ps.sl[p][kt][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (kt == 0)
-                half_product(first, hi, lo, k_own + kt * 512, sk, sq);
+                half_product(first, hi, lo, k_own + kt * 512, sk);
             else
-                half_product(then, hi, lo, k_own + kt * 512, sk, sq);
+                half_product(then, hi, lo, k_own + kt * 512, sk);
         }
         tc::named_bar_sync(bar_a, 64);
-        other[0] = ps.ds[1 - p][g4], other[1] = ps.ds[1 - p][g4 + 8];
+        other[0] = ps.ds[cb][1 - p][g4], other[1] = ps.ds[cb][1 - p][g4 + 8];
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
-            const uint4 x = ps.s[1 - p][kt][0][lane], y = ps.s[1 - p][kt][1][lane];
+            const uint4 x = ps.s[cb][1 - p][kt][lane], y = ps.sl[1 - p][kt][lane];
             const uint32_t hi[4] = {x.x, x.y, x.z, x.w}, lo[4] = {y.x, y.y, y.z, y.w};
             if (kt == 0)
-                half_product(first, hi, lo, k_other + kt * 512, zk, zq);
+                half_product(first, hi, lo, k_other + kt * 512, zk);
             else
-                half_product(then, hi, lo, k_other + kt * 512, zk, zq);
+                half_product(then, hi, lo, k_other + kt * 512, zk);
         }
         // R = beta c (v - e^G c S0 k), in place of S0 K^T
         float rmost[2] = {0.f, 0.f};
@@ -767,32 +911,32 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
                 dmost[h] = fmaxf(dmost[h], fmaxf(fabsf(dx[t][2 * h]), fabsf(dx[t][2 * h + 1])));
             }
         }
-        float uup[2], udown[2], dup[2], ddown[2];
+        float uup[2], dup[2], ddown[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uup[h] = scale_to(quad_max(umost[h]), 12);
             dup[h] = scale_to(quad_max(dmost[h]), 12);
-            udown[h] = inverse(uup[h]);
             ddown[h] = inverse(dup[h]);
             if (q4 == 0) {
                 ps.dd[p][g4 + 8 * h] = ddown[h];
-                if (p == 0) ps.du[g4 + 8 * h] = udown[h];
+                ps.du[cb][p][g4 + 8 * h] = inverse(uup[h]);
             }
         }
-        uint32_t dhi[2][4], dlo[2][4], uh[2][4];
+        uint32_t dhi[2][4], dlo[2][4];
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
+            uint32_t uh[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int t = 2 * kt + j;
                     split(dx[t][2 * h] * dup[h], dx[t][2 * h + 1] * dup[h], dhi[kt][2 * j + h], dlo[kt][2 * j + h]);
-                    uh[kt][2 * j + h] = pack(u[t][2 * h] * uup[h], u[t][2 * h + 1] * uup[h]);
+                    uh[2 * j + h] = pack(u[t][2 * h] * uup[h], u[t][2 * h + 1] * uup[h]);
                 }
             ps.d[p][kt][0][lane] = make_uint4(dhi[kt][0], dhi[kt][1], dhi[kt][2], dhi[kt][3]);
             ps.d[p][kt][1][lane] = make_uint4(dlo[kt][0], dlo[kt][1], dlo[kt][2], dlo[kt][3]);
-            if (p == 0) ps.u[kt][lane] = make_uint4(uh[kt][0], uh[kt][1], uh[kt][2], uh[kt][3]);
+            ps.u[cb][p][kt][lane] = make_uint4(uh[0], uh[1], uh[2], uh[3]);
         }
         if (p == 0) {
             bar_arrive(bar_a, 64);
@@ -800,6 +944,8 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
             tc::named_bar_sync(bar_a, 64);
             bar_arrive(bar_c, 64);
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.given[mine][cb]);
         // S = e^G_C S0 + U' e^(G_C - G) K on the warp's columns, with its own tokens and then with the other's (sums of
         // their own, added in fp32: an MMA cuts off what it adds to a large accumulator)
         float d[DK / 16][4];
@@ -837,77 +983,6 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
 #pragma unroll
                 for (int e = 0; e < 4; ++e) S[t][e] = S[t][e] * gamma + d[t][e] * ddown[e / 2];
         }
-        // O = e^G scale S0 Q^T + U' P^T
-        float o[4][4];
-        {
-            const uint32_t x0 = xr + 2 * kTri + (p ? tri(2, 2) : tri(0, 0)), x1 = xr + 2 * kTri + (p ? tri(3, 2) : tri(1, 0));
-            uint32_t b0[4], b1[4], b2[4];
-            ldsm4(b0, x0);
-            ldsm4(b1, x1);
-            ldsm4(b2, x1 + 512);
-            mma0(o[0], uh[0], b0[0], b0[1]);
-            mma0(o[1], uh[0], b0[2], b0[3]);
-            mma0(o[2], uh[0], b1[0], b1[1]);
-            mma0(o[3], uh[0], b1[2], b1[3]);
-            mma(o[2], uh[1], b2[0], b2[1]);
-            mma(o[3], uh[1], b2[2], b2[3]);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][e] *= udown[e / 2];
-        if (p == 1) {
-            float y[4][4];
-            uint32_t b0[4], b1[4], b2[4], b3[4];
-            ldsm4(b0, xr + 2 * kTri + tri(2, 0));
-            ldsm4(b1, xr + 2 * kTri + tri(3, 0));
-            ldsm4(b2, xr + 2 * kTri + tri(2, 1));
-            ldsm4(b3, xr + 2 * kTri + tri(3, 1));
-            const float f[2] = {ps.du[g4], ps.du[g4 + 8]};
-            const uint4 h0 = ps.u[0][lane], h1 = ps.u[1][lane];
-            const uint32_t a0[4] = {h0.x, h0.y, h0.z, h0.w}, a1[4] = {h1.x, h1.y, h1.z, h1.w};
-            mma0(y[0], a0, b0[0], b0[1]);
-            mma0(y[1], a0, b0[2], b0[3]);
-            mma0(y[2], a0, b1[0], b1[1]);
-            mma0(y[3], a0, b1[2], b1[3]);
-            mma(y[0], a1, b2[0], b2[1]);
-            mma(y[1], a1, b2[2], b2[3]);
-            mma(y[2], a1, b3[0], b3[1]);
-            mma(y[3], a1, b3[2], b3[3]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[t][e] += y[t][e] * f[e / 2];
-        }
-#pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2) {  // the values have been read: their place takes the outputs
-            uint32_t x[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int t = 2 * t2 + j;
-                const float2 b = *reinterpret_cast<const float2*>(vec + kB * C + 8 * t);
-                const float2 pi = *reinterpret_cast<const float2*>(vec + kPi * C + 8 * t);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float q0 = sq[t][2 * h] * own[h] + zq[t][2 * h] * other[h];
-                    const float q1 = sq[t][2 * h + 1] * own[h] + zq[t][2 * h + 1] * other[h];
-                    const __nv_bfloat162 both = __floats2bfloat162_rn(b.x * q0 + pi.x * o[t][2 * h], b.y * q1 + pi.y * o[t][2 * h + 1]);
-                    x[2 * j + h] = *reinterpret_cast<const uint32_t*>(&both);
-                }
-            }
-            stsm4_t(vc + t2 * 512 + rows, x[0], x[1], x[2], x[3]);
-        }
-        __syncwarp();
-        {
-            bf16* op = static_cast<bf16*>(a.out) + hv * a.Dv + row0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = i * 16 + lane / 2, tok = c * C + 32 * p + t;
-                if (tok < tokens)
-                    *reinterpret_cast<uint4*>(op + (tok0 + tok) * a.Hv * a.Dv + 8 * (lane & 1)) =
-                        *reinterpret_cast<const uint4*>(sm.v[warp][c & 1] + i * 512 + in_block(lane / 2, lane & 1));
-            }
-        }
         // the other warp's tokens
         if (p == 0) tc::named_bar_sync(bar_c, 64);
         {
@@ -925,32 +1000,12 @@ __global__ void __launch_bounds__(64 * W, 1) delta_walk_kernel(const DeltaArgs a
 #pragma unroll
                 for (int e = 0; e < 4; ++e) S[t][e] += d[t][e] * f[e / 2];
         }
-        // the stage is free for chunk c + NS
-        if (c + NS < n_chunks) {
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
-            if (tid == 0) {
-                ok = ok && tc::mbar_wait(&sm.empty[st], (c / NS) & 1, &sm.abort, a.timeout_ns);
-                if (ok)
-                    fetch(issued++);
-                else
-                    *const_cast<volatile int*>(&sm.abort) = 1;
-            }
-        }
         __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
     }
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) {  // a wait ran out: record it, let the copies that were issued land, leave the state as it was
-        if (lane == 0) {
-            *const_cast<volatile int*>(&sm.abort) = 1;
-            record_error(a.err, kErrTimeoutMma);
-        }
+    if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) record_error(a.err, kErrTimeoutMma);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (tid == 0) {
-            int zero = 0;
-            for (int i = max(0, issued - NS); i < issued; ++i)
-                tc::mbar_wait(&sm.full[i % NS], (i / NS) & 1, &zero, 1000000000ull);
-        }
         return;
     }
     if (!a.state_out) return;
@@ -972,11 +1027,12 @@ cudaError_t launch_prep(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
 
 template <int DK, int W>
 cudaError_t launch_walk(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
+    static_assert(sizeof(WalkSmem<DK, W>) <= 227 * 1024);
     static int done[64];
     cudaError_t e = ensure_smem(delta_walk_kernel<DK, W>, sizeof(WalkSmem<DK, W>), done);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.R * a.Hv * (a.Dv / (16 * W))));
-    return launch_pdl(delta_walk_kernel<DK, W>, grid, dim3(64 * W), sizeof(WalkSmem<DK, W>), s, a, w);
+    return launch_pdl(delta_walk_kernel<DK, W>, grid, dim3(96 * W), sizeof(WalkSmem<DK, W>), s, a, w);
 }
 
 template <int DK>
