@@ -182,6 +182,21 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// A number as the sum of two floats, of which the high one is the nearest float: about 2^-46 of the larger term is lost a sum
+struct Sum {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum sum_of(float a, float b) {  // a b
+    const float p = a * b;
+    return Sum{p, fmaf(a, b, -p)};
+}
+__device__ __forceinline__ Sum operator+(const Sum& a, const Sum& b) {
+    const float s = a.hi + b.hi, v = s - a.hi;
+    const float e = (a.hi - (s - v)) + (b.hi - v) + (a.lo + b.lo);
+    const float h = s + e;
+    return Sum{h, e - (h - s)};
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {  // (2^-22 of the value; to 0 below 2^-126)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -276,17 +291,22 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
     const long long unit = 1ll * r * w.chunks + chunk;
     const int group = a.Hv / a.Hk;
 
-    // keys and queries: f16 after a power of two a row, DK / 8 lanes a row
-    constexpr int L = DK / 8, RPW = 32 / L, ROWS = 16 / RPW;
-    const int sub = lane % L;
-    uint4 in[2][ROWS];
+    // keys and queries: f16 after a power of two a row, four lanes a row
+    constexpr int PIECES = DK / 32;  // 16-byte pieces of a lane: 64 bytes of a row together
+    const int sub = lane % 4;
+    uint4 in[2][2][PIECES];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int t = warp * 16 + i * RPW + lane / L;
-        in[0][i] = in[1][i] = make_uint4(0, 0, 0, 0);
-        if (t < m) {
-            in[0][i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.k) + (tok0 + t) * a.k_ld + hk * DK + 8 * sub));
-            in[1][i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (tok0 + t) * a.q_ld + hk * DK + 8 * sub));
+    for (int i = 0; i < 2; ++i) {
+        const int t = warp * 16 + i * 8 + lane / 4;
+        const bf16* kp = static_cast<const bf16*>(a.k) + (tok0 + t) * a.k_ld + hk * DK + 8 * sub;
+        const bf16* qp = static_cast<const bf16*>(a.q) + (tok0 + t) * a.q_ld + hk * DK + 8 * sub;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            in[0][i][j] = in[1][i][j] = make_uint4(0, 0, 0, 0);
+            if (t < m) {
+                in[0][i][j] = __ldg(reinterpret_cast<const uint4*>(kp + 32 * j));
+                in[1][i][j] = __ldg(reinterpret_cast<const uint4*>(qp + 32 * j));
+            }
         }
     }
     float gs[2], be[2];  // of the first two value heads, by an even warp each: tokens 2 lane and 2 lane + 1
@@ -301,35 +321,38 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
     };
     if (warp % 2 == 0) load_gates(pair);
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int t = warp * 16 + i * RPW + lane / L;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            const uint32_t xs[4] = {in[which][i].x, in[which][i].y, in[which][i].z, in[which][i].w};
-            float f[8], most = 0.f;
+            const int t = warp * 16 + i * 8 + lane / 4;
+            float f[8 * PIECES], most = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[2 * j] = __uint_as_float(xs[j] << 16);
-                f[2 * j + 1] = __uint_as_float(xs[j] & 0xffff0000u);
-                most = fmaxf(most, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
+            for (int j = 0; j < PIECES; ++j) {
+                const uint32_t xs[4] = {in[which][i][j].x, in[which][i][j].y, in[which][i][j].z, in[which][i][j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[8 * j + 2 * e] = __uint_as_float(xs[e] << 16);
+                    f[8 * j + 2 * e + 1] = __uint_as_float(xs[e] & 0xffff0000u);
+                    most = fmaxf(most, fmaxf(fabsf(f[8 * j + 2 * e]), fabsf(f[8 * j + 2 * e + 1])));
+                }
             }
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const float up = scale_to(most, 0);
+            const float up = scale_to(quad_max(most), 0);
             float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 8 * PIECES; ++j) {
                 f[j] *= up;
                 ss += f[j] * f[j];
             }
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
             if (sub == 0)
                 (which ? sm.cq : sm.ck)[t] = ss == 0.f ? 0.f : a.eps > 0.f ? inverse_root(ss + a.eps * up * up) : inverse(up);
-            *reinterpret_cast<uint4*>((which ? sm.q : sm.k) + (t / 16 * (DK / 16) + sub / 2) * 512 + in_block(t % 16, sub % 2)) =
-                make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j)
+                *reinterpret_cast<uint4*>((which ? sm.q : sm.k) + (t / 16 * (DK / 16) + 2 * j + sub / 2) * 512 + in_block(t % 16, sub % 2)) =
+                    make_uint4(pack(f[8 * j], f[8 * j + 1]), pack(f[8 * j + 2], f[8 * j + 3]), pack(f[8 * j + 4], f[8 * j + 5]),
+                               pack(f[8 * j + 6], f[8 * j + 7]));
         }
-    }
     tc::fence_proxy_async_smem();
     __syncthreads();
     if (tid == 0) {
@@ -373,34 +396,40 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
         }
         if (on && warp % 2 == 0) {
             float* vec = reinterpret_cast<float*>(sm.x[pair] + 3 * kTri);
-            double s[2];  // sums of g in 64 bits, to base 2
+            Sum s[2];  // sums of g, to base 2
 #pragma unroll
-            for (int i = 0; i < 2; ++i) s[i] = (gs[i] < -200.f ? -200.f : gs[i]) * 1.4426950408889634;  // (e^-200 is 0 as well)
-            const double mine = s[0] + s[1];
-            double run = mine;
+            for (int i = 0; i < 2; ++i) {
+                const float g = gs[i] < -200.f ? -200.f : gs[i];  // (e^-200 is 0 as well)
+                s[i] = sum_of(g, 1.4426950408889634f);
+                s[i].lo = fmaf(g, 1.925963033500811e-8f, s[i].lo);  // log2(e) = 1.44269502162933 + 1.9259630335e-8
+            }
+            const Sum mine = s[0] + s[1];
+            Sum run = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += x;
+                const Sum x{__shfl_up_sync(0xffffffffu, run.hi, o), __shfl_up_sync(0xffffffffu, run.lo, o)};
+                if (lane >= o) run = x + run;
             }
-            const double all = __shfl_sync(0xffffffffu, run, 31);
-            s[0] = run - mine + s[0];
+            const Sum all{__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
+            Sum before{__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+            if (lane == 0) before = Sum{0.f, 0.f};
+            s[0] = before + s[0];
             s[1] = run;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
-                const float hi = static_cast<float>(s[i]);
+                const float hi = s[i].hi;
                 sm.ghi[pair][t] = hi;
-                sm.glo[pair][t] = static_cast<float>(s[i] - hi);
-                const float ck = sm.ck[t], cq = sm.cq[t] * a.scale, since = exp2f(hi);
+                sm.glo[pair][t] = s[i].lo;
+                const float ck = sm.ck[t], cq = sm.cq[t] * a.scale, since = exp2f(hi + s[i].lo);
                 sm.beta[pair][t] = be[i] * ck * ck;
                 vec[kA * C + t] = since * ck;
                 vec[kBeta * C + t] = be[i] * ck;
                 vec[kB * C + t] = since * cq;
                 vec[kPi * C + t] = cq;
-                vec[kD * C + t] = exp2f(static_cast<float>(all - s[i]));
+                vec[kD * C + t] = exp2f((all.hi - hi) + (all.lo - s[i].lo));
             }
-            if (lane == 0) vec[kGamma * C] = exp2f(static_cast<float>(all));
+            if (lane == 0) vec[kGamma * C] = exp2f(all.hi + all.lo);
         }
         __syncthreads();
         // A' and P of both heads, from every warp's products
