@@ -37,9 +37,10 @@ namespace {
 constexpr int C = 64;             // tokens of a chunk
 // X and P are lower triangular: of their 16 x 16 blocks (f16, 512 bytes) the ten on and below the diagonal are kept, row by row
 constexpr int kTri = 10 * 512;
-constexpr int kHeadBytes = 3 * kTri + 6 * C * 4;  // X high, X low, P, factors of one value head
-// factors of a token, [6][64] floats
-enum { kA, kBeta, kB, kD, kPi, kGamma };
+// What a chunk of one value head has: X high, X low and factors for the states, P and factors for the outputs
+enum { kA, kBeta, kD, kGamma };  // [4][64] floats
+enum { kB, kPi };                // [2][64] floats
+constexpr int kXBytes = 2 * kTri + 4 * C * 4, kPBytes = kTri + 2 * C * 4, kHeadBytes = kXBytes + kPBytes;
 
 template <int DK>
 struct Tile {
@@ -395,7 +396,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
             if (warp % 2 == 0) load_gates(v0 + pair);
         }
         if (on && warp % 2 == 0) {
-            float* vec = reinterpret_cast<float*>(sm.x[pair] + 3 * kTri);
+            float* vec = reinterpret_cast<float*>(sm.x[pair] + 2 * kTri);
+            float* out = reinterpret_cast<float*>(sm.x[pair] + kXBytes + kTri);
             Sum s[2];  // sums of g, to base 2
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -425,8 +427,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
                 sm.beta[pair][t] = be[i] * ck * ck;
                 vec[kA * C + t] = since * ck;
                 vec[kBeta * C + t] = be[i] * ck;
-                vec[kB * C + t] = since * cq;
-                vec[kPi * C + t] = cq;
+                out[kB * C + t] = since * cq;
+                out[kPi * C + t] = cq;
                 vec[kD * C + t] = exp2f((all.hi - hi) + (all.lo - s[i].lo));
             }
             if (lane == 0) vec[kGamma * C] = exp2f(all.hi + all.lo);
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
             if (v0 + p >= group) break;
-            char* const ps = sm.x[p] + 2 * kTri;
+            char* const ps = sm.x[p] + kXBytes;
             typename PrepSmem<DK>::Blocks& bl = sm.blocks[p];
             const int i0 = warp * 16 + g4;
             const float gh[2] = {sm.ghi[p][i0], sm.ghi[p][i0 + 8]}, gl[2] = {sm.glo[p][i0], sm.glo[p][i0 + 8]};
@@ -524,12 +526,16 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 template <int DK, int W>
 struct WalkSmem {
     static constexpr int kStages = W <= 2 ? 3 : 2;
-    struct Stage {
+    struct ForStates {
         char k[Tile<DK>::kBytes];
-        char q[Tile<DK>::kBytes];
-        char head[kHeadBytes];
+        char x[kXBytes];
     };
-    alignas(128) Stage st[kStages];
+    struct ForOutputs {
+        char q[Tile<DK>::kBytes];
+        char p[kPBytes];
+    };
+    alignas(128) ForStates x[kStages];
+    ForOutputs q[2];
     struct Pass {                    // of a slice, from warp p to the others
         uint4 s[2][2][DK / 32][32];  // [chunk % 2][p][k step][lane]: S0, high
         uint4 sl[2][DK / 32][32];    // low
@@ -540,28 +546,36 @@ struct WalkSmem {
     } pass[W];
     char v[2 * W][2][32 * 32];  // a warp's 32 tokens of 16 values
     char o[W][C * 32];          // 64 tokens of 16 outputs
-    uint64_t full[kStages], empty[kStages];
+    uint64_t x_full[kStages], x_empty[kStages], q_full[2], q_empty[2];
     uint64_t given[W][2], taken[W][2];  // S0 and U' of chunk % 2 for the third warp
     int abort, request;
 };
 
+// Warps of a block: two a slice, then those of the outputs; with two slices an idle one between these, so that each shares
+// its scheduler (warp modulo 4) with the lighter warp of another slice
+template <int W>
+constexpr int kWalkWarps = 3 * W + (W == 2);
+
 template <int DK, int W>
-__global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
+__global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
     extern __shared__ __align__(128) char raw[];
     using Smem = WalkSmem<DK, W>;
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     constexpr int NS = Smem::kStages;
     constexpr int NK = DK / 32;  // k steps of 16 of a half of the state's columns
-    constexpr uint32_t kQk = 2 * Tile<DK>::kBytes;
     constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g4 = lane / 4, q4 = lane % 4;
     const bool outputs = warp >= 2 * W;
-    const int mine = outputs ? warp - 2 * W : warp / 2, p = warp % 2;  // slice of the block, part of it
+    const int mine = !outputs ? warp / 2 : W == 2 ? (warp - 4) / 2 : warp - 2 * W, p = warp % 2;  // slice of the block, part of it
     typename Smem::Pass& ps = sm.pass[mine];
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            tc::mbar_init(&sm.full[i], 1);
-            tc::mbar_init(&sm.empty[i], 3 * W);
+            tc::mbar_init(&sm.x_full[i], 1);
+            tc::mbar_init(&sm.x_empty[i], 2 * W);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sm.q_full[i], 1);
+            tc::mbar_init(&sm.q_empty[i], W);
         }
         for (int i = 0; i < 2 * W; ++i) {
             tc::mbar_init(&sm.given[0][i], 2);
@@ -604,29 +618,37 @@ __global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a
         *const_cast<volatile int*>(&sm.abort) = 1;
     };
 
+    // tiles: those of the states are fetched by the first warp, those of the outputs by the first of these.  A stage is
+    // filled again in the middle of the next chunk, when nobody uses it any more, so that no wait costs anything.
+    int issued = 0;
+    auto keys = [&](int c) { return w.qk + ((unit0 + c) * a.Hk + hk) * 2 * Tile<DK>::kBytes; };
+    auto head = [&](int c) { return w.heads + ((unit0 + c) * a.Hv + hv) * kHeadBytes; };
+
     if (outputs) {
+        if (W == 2 && p) return;
         const bool fetches = mine == 0 && lane == 0;
-        int issued = 0;
-        auto fetch = [&]() {  // the next chunk into its stage
-            typename Smem::Stage& s = sm.st[issued % NS];
-            uint64_t* bar = &sm.full[issued % NS];
-            tc::mbar_arrive_expect_tx(bar, kQk + kHeadBytes);
-            bulk_load(tc::smem_addr(s.k), w.qk + ((unit0 + issued) * a.Hk + hk) * kQk, kQk, bar);
-            bulk_load(tc::smem_addr(s.head), w.heads + ((unit0 + issued) * a.Hv + hv) * kHeadBytes, kHeadBytes, bar);
+        auto fetch = [&]() {
+            const int st = issued & 1;
+            if (issued >= 2) wait(&sm.q_empty[st], (issued >> 1) - 1);
+            if (!ok) return;
+            tc::mbar_arrive_expect_tx(&sm.q_full[st], Tile<DK>::kBytes + kPBytes);
+            bulk_load(tc::smem_addr(sm.q[st].q), keys(issued) + Tile<DK>::kBytes, Tile<DK>::kBytes, &sm.q_full[st]);
+            bulk_load(tc::smem_addr(sm.q[st].p), head(issued) + kXBytes, kPBytes, &sm.q_full[st]);
             ++issued;
         };
-        if (fetches)
-            while (issued < NS && issued < n_chunks) fetch();
+        if (fetches && n_chunks) fetch();
         const uint32_t os = tc::smem_addr(sm.o[mine]);
 #pragma unroll 1
         for (int c = 0; c < n_chunks; ++c) {
-            const int st = c % NS, cb = c & 1;
-            wait(&sm.given[mine][cb], c >> 1);  // (after the tiles' barrier in time, but that one has to be seen here too)
-            wait(&sm.full[st], c / NS);
+            const int cb = c & 1;
+            if (fetches && ok && issued < n_chunks) fetch();
             __syncwarp();
-            typename Smem::Stage& s = sm.st[st];
-            const uint32_t qr = tc::smem_addr(s.q) + rows, pr = tc::smem_addr(s.head) + 2 * kTri + rows;
-            const float* vec = reinterpret_cast<const float*>(s.head + 3 * kTri) + 2 * q4;
+            wait(&sm.q_full[cb], c >> 1);
+            wait(&sm.given[mine][cb], c >> 1);
+            __syncwarp();
+            typename Smem::ForOutputs& s = sm.q[cb];
+            const uint32_t qr = tc::smem_addr(s.q) + rows, pr = tc::smem_addr(s.p) + rows;
+            const float* vec = reinterpret_cast<const float*>(s.p + kTri) + 2 * q4;
             // S0 Q^T, with the columns of each half of S0 and their scale
             float o[8][4];
             {
@@ -694,8 +716,8 @@ __global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a
             }
             __syncwarp();  // S0, U' and the tiles have been read
             if (lane == 0) {
-                tc::mbar_arrive(&sm.empty[st]);  // (in this order: whoever sees S0 and U' taken may be at the tiles' next phase)
                 tc::mbar_arrive(&sm.taken[mine][cb]);
+                tc::mbar_arrive(&sm.q_empty[cb]);
             }
 #pragma unroll
             for (int t2 = 0; t2 < 4; ++t2) {
@@ -718,22 +740,30 @@ __global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a
                     *reinterpret_cast<uint4*>(op + (tok0 + tok) * a.Hv * a.Dv + 8 * (lane & 1)) =
                         *reinterpret_cast<const uint4*>(sm.o[mine] + i * 512 + in_block(lane / 2, lane & 1));
             }
-            if (fetches && issued < n_chunks) {  // the stage that chunk c has left
-                wait(&sm.empty[st], c / NS);
-                if (ok && !*const_cast<volatile int*>(&sm.abort)) fetch();
-            }
             __syncwarp();
         }
         if (!__all_sync(0xffffffffu, ok)) {  // a wait ran out: record it and let the copies that were issued land
             if (lane == 0) record_error(a.err, kErrTimeoutEpilogue);
             if (fetches) {
                 int zero = 0;
-                for (int i = max(0, issued - NS); i < issued; ++i)
-                    tc::mbar_wait(&sm.full[i % NS], (i / NS) & 1, &zero, 1000000000ull);
+                for (int i = max(0, issued - 2); i < issued; ++i)
+                    tc::mbar_wait(&sm.q_full[i & 1], (i >> 1) & 1, &zero, 1000000000ull);
             }
         }
         return;
     }
+
+    auto fetch = [&]() {
+        const int st = issued % NS;
+        if (issued >= NS) wait(&sm.x_empty[st], issued / NS - 1);
+        if (!ok) return;
+        tc::mbar_arrive_expect_tx(&sm.x_full[st], Tile<DK>::kBytes + kXBytes);
+        bulk_load(tc::smem_addr(sm.x[st].k), keys(issued), Tile<DK>::kBytes, &sm.x_full[st]);
+        bulk_load(tc::smem_addr(sm.x[st].x), head(issued), kXBytes, &sm.x_full[st]);
+        ++issued;
+    };
+    if (tid == 0)
+        while (issued < NS - 1 && issued < n_chunks) fetch();
 
     const uint32_t vs = tc::smem_addr(sm.v[warp]);
     auto fetch_v = [&](int c) {  // the warp's values, zeros behind the request's tokens
@@ -769,7 +799,7 @@ __global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a
 #pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
         const int st = c % NS, cb = c & 1;
-        wait(&sm.full[st], c / NS);
+        wait(&sm.x_full[st], c / NS);
         if (c >= 2) wait(&sm.taken[mine][cb], (c >> 1) - 1);
         if (c + 1 < n_chunks) {
             fetch_v(c + 1);
@@ -778,9 +808,9 @@ __global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         __syncwarp();
-        typename Smem::Stage& s = sm.st[st];
-        const uint32_t kr = tc::smem_addr(s.k) + 2 * p * KB + rows, xr = tc::smem_addr(s.head) + rows;
-        const float* vec = reinterpret_cast<const float*>(s.head + 3 * kTri) + 32 * p + 2 * q4;  // of this warp's tokens
+        typename Smem::ForStates& s = sm.x[st];
+        const uint32_t kr = tc::smem_addr(s.k) + 2 * p * KB + rows, xr = tc::smem_addr(s.x) + rows;
+        const float* vec = reinterpret_cast<const float*>(s.x + 2 * kTri) + 32 * p + 2 * q4;  // of this warp's tokens
         const uint32_t vc = vs + (c & 1) * 1024;
 
         // S0 K^T of the warp's tokens: first with its own columns of S0, then with the other's
@@ -830,6 +860,8 @@ __global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a
                 half_product(then, hi, lo, k_own + kt * 512, sk);
         }
         tc::named_bar_sync(bar_a, 64);
+        if (tid == 0 && ok && issued < n_chunks) fetch();
+        __syncwarp();
         other[0] = ps.ds[cb][1 - p][g4], other[1] = ps.ds[cb][1 - p][g4 + 8];
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
@@ -1006,7 +1038,7 @@ __global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a
         };
         state_product(dhi, dlo, p);
         {
-            const float gamma = *(reinterpret_cast<const float*>(s.head + 3 * kTri) + kGamma * C);
+            const float gamma = *(reinterpret_cast<const float*>(s.x + 2 * kTri) + kGamma * C);
 #pragma unroll
             for (int t = 0; t < DK / 16; ++t)
 #pragma unroll
@@ -1030,11 +1062,16 @@ __global__ void __launch_bounds__(96 * W, 1) delta_walk_kernel(const DeltaArgs a
                 for (int e = 0; e < 4; ++e) S[t][e] += d[t][e] * f[e / 2];
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
+        if (lane == 0) tc::mbar_arrive(&sm.x_empty[st]);
     }
     if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) record_error(a.err, kErrTimeoutMma);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (tid == 0) {
+            int zero = 0;
+            for (int i = max(0, issued - NS); i < issued; ++i)
+                tc::mbar_wait(&sm.x_full[i % NS], (i / NS) & 1, &zero, 1000000000ull);
+        }
         return;
     }
     if (!a.state_out) return;
@@ -1061,7 +1098,7 @@ cudaError_t launch_walk(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
     cudaError_t e = ensure_smem(delta_walk_kernel<DK, W>, sizeof(WalkSmem<DK, W>), done);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.R * a.Hv * (a.Dv / (16 * W))));
-    return launch_pdl(delta_walk_kernel<DK, W>, grid, dim3(96 * W), sizeof(WalkSmem<DK, W>), s, a, w);
+    return launch_pdl(delta_walk_kernel<DK, W>, grid, dim3(32 * kWalkWarps<W>), sizeof(WalkSmem<DK, W>), s, a, w);
 }
 
 template <int DK>
