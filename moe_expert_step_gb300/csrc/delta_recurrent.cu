@@ -25,17 +25,43 @@
 namespace moestep {
 namespace {
 
-constexpr int kTokens = 16;  // staged at a time
 constexpr int kWarps = 4;
 
-// NR: rows of a lane group (a warp has 4 NR rows, a block kWarps * 4 NR)
-template <typename T, int DK, int NR>
+// N pieces of four elements, 32 apart
+template <typename T, int N>
+__device__ __forceinline__ void load_row(const T* p, float (&x)[N][4]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 y = __ldg(reinterpret_cast<const float4*>(p + 32 * j));
+            x[j][0] = y.x, x[j][1] = y.y, x[j][2] = y.z, x[j][3] = y.w;
+        } else {
+            const uint2 y = __ldg(reinterpret_cast<const uint2*>(p + 32 * j));
+            x[j][0] = __uint_as_float(y.x << 16), x[j][1] = __uint_as_float(y.x & 0xffff0000u);
+            x[j][2] = __uint_as_float(y.y << 16), x[j][3] = __uint_as_float(y.y & 0xffff0000u);
+        }
+    }
+}
+
+// One token of a head for the lane group of a row: everything that does not depend on the state
+template <typename T, int DK>
+struct Staged {
+    static constexpr int kTokens = 16;  // at a time
+    float k[kTokens][DK], q[kTokens][DK];
+    float gate[kTokens], rate[kTokens], kq[kTokens];
+};
+
+__device__ __forceinline__ float inverse_norm(float ss, float eps) { return eps > 0.f ? 1.0f / sqrtf(ss + eps) : 1.f; }
+
+// NR: rows of a lane group (a warp has 4 NR rows, a block kWarps * 4 NR); ONE: a token a request, nothing is staged and each
+// warp forms the token's sums itself
+template <typename T, int DK, int NR, bool ONE>
 __global__ void __launch_bounds__(32 * kWarps) delta_recurrent_kernel(const DeltaArgs a) {
     constexpr int N = DK / 32;             // 16-byte pieces of a lane's share of a row
     constexpr int ROWS = kWarps * 4 * NR;  // rows of a block
-    __shared__ float ks[kTokens][DK], qs[kTokens][DK];
-    __shared__ float vs[kTokens][ROWS];
-    __shared__ float gate[kTokens], rate[kTokens], kq[kTokens];
+    using Stage = Staged<T, DK>;
+    __shared__ Stage sm[ONE ? 1 : 2];
+    __shared__ float vs[ONE ? 1 : 2][Stage::kTokens][ROWS];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane % 8;
@@ -43,8 +69,13 @@ __global__ void __launch_bounds__(32 * kWarps) delta_recurrent_kernel(const Delt
     const int slice = blockIdx.x % slices, hv = blockIdx.x / slices % a.Hv, r = blockIdx.x / slices / a.Hv;
     int tokens, slot;
     if (!delta_request(a, r, threadIdx.x == 0 && slice == 0 && hv == 0, tokens, slot)) return;
-    const int row0 = slice * ROWS + warp * 4 * NR + lane / 8;  // + 4 i
-    const long long state0 = (1ll * slot * a.Hv + hv) * a.Dv * DK + 4 * sub;
+    const int hk = hv / (a.Hv / a.Hk);
+    const long long tok0 = 1ll * r * a.n;
+    const T* const kp = static_cast<const T*>(a.k) + tok0 * a.k_ld + hk * DK;
+    const T* const qp = static_cast<const T*>(a.q) + tok0 * a.q_ld + hk * DK;
+    const T* const vp = static_cast<const T*>(a.v) + tok0 * a.v_ld + hv * a.Dv + slice * ROWS;
+    const int row = warp * 4 * NR + lane / 8;  // + 4 i, of the block's
+    const long long state0 = ((1ll * slot * a.Hv + hv) * a.Dv + slice * ROWS + row) * DK + 4 * sub;
     float S[NR][N][4];
     const bool fresh = a.fresh && a.fresh[r];
 #pragma unroll
@@ -52,81 +83,137 @@ __global__ void __launch_bounds__(32 * kWarps) delta_recurrent_kernel(const Delt
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!fresh) x = *reinterpret_cast<const float4*>(a.state + state0 + 1ll * (row0 + 4 * i) * DK + 32 * j);
+            if (!fresh) x = *reinterpret_cast<const float4*>(a.state + state0 + 4 * i * DK + 32 * j);
             S[i][j][0] = x.x, S[i][j][1] = x.y, S[i][j][2] = x.z, S[i][j][3] = x.w;
         }
-    const int hk = hv / (a.Hv / a.Hk);
-    for (int t0 = 0; t0 < tokens; t0 += kTokens) {
-        const int m = min(kTokens, tokens - t0);
-        if (t0) __syncthreads();
-        for (int t = warp; t < m; t += kWarps) {  // a warp stages a token
-            const long long tok = 1ll * r * a.n + t0 + t;
-            const T* kp = static_cast<const T*>(a.k) + tok * a.k_ld + hk * DK;
-            const T* qp = static_cast<const T*>(a.q) + tok * a.q_ld + hk * DK;
-            float kk[DK / 32], qq[DK / 32], sk = 0.f, sq = 0.f, c = 0.f;
+    T* const out = static_cast<T*>(a.out) + (tok0 * a.Hv + hv) * a.Dv + slice * ROWS + row;
+    // a token of the lane group's rows, from its key and query and their scalars
+    auto step = [&](const float(&kk)[N][4], const float(&qq)[N][4], float al, float be, float c, const float(&v)[NR], T* o) {
+        float p[NR], s[NR];
 #pragma unroll
-            for (int j = 0; j < DK / 32; ++j) {
-                kk[j] = to_f32(kp[lane + 32 * j]);
-                qq[j] = to_f32(qp[lane + 32 * j]);
-                sk += kk[j] * kk[j];
-                sq += qq[j] * qq[j];
-                c += kk[j] * qq[j];
-            }
-            sk = warp_sum(sk);
-            sq = warp_sum(sq);
-            c = warp_sum(c);
-            const float rk = a.eps > 0.f ? 1.0f / sqrtf(sk + a.eps) : 1.f, rq = a.eps > 0.f ? 1.0f / sqrtf(sq + a.eps) : 1.f;
+        for (int i = 0; i < NR; ++i) {
+            p[i] = s[i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < DK / 32; ++j) {
-                ks[t][lane + 32 * j] = kk[j] * rk;
-                qs[t][lane + 32 * j] = qq[j] * rq;
-            }
-            if (lane == 0) {
-                gate[t] = expf(a.g[tok * a.Hv + hv]);
-                rate[t] = a.beta[tok * a.Hv + hv];
-                kq[t] = c * rk * rq;
-            }
-            for (int j = lane; j < ROWS; j += 32)
-                vs[t][j] = to_f32(static_cast<const T*>(a.v)[tok * a.v_ld + hv * a.Dv + slice * ROWS + j]);
-        }
-        __syncthreads();
-        for (int t = 0; t < m; ++t) {
-            float p[NR], s[NR];
+            for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int i = 0; i < NR; ++i) p[i] = s[i] = 0.f;
-            float kk[N][4];
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float4 x = *reinterpret_cast<const float4*>(&ks[t][32 * j + 4 * sub]);
-                const float4 y = *reinterpret_cast<const float4*>(&qs[t][32 * j + 4 * sub]);
-                kk[j][0] = x.x, kk[j][1] = x.y, kk[j][2] = x.z, kk[j][3] = x.w;
-                const float qq[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int i = 0; i < NR; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[i] += S[i][j][e] * kk[j][e];
-                        s[i] += S[i][j][e] * qq[e];
-                    }
-            }
-#pragma unroll
-            for (int o = 4; o; o >>= 1)
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    p[i] += __shfl_xor_sync(0xffffffffu, p[i], o);
-                    s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+                for (int e = 0; e < 4; ++e) {
+                    p[i] += S[i][j][e] * kk[j][e];
+                    s[i] += S[i][j][e] * qq[j][e];
                 }
-            const float al = gate[t], be = rate[t], c = kq[t];
-            T* out = static_cast<T*>(a.out) + ((1ll * r * a.n + t0 + t) * a.Hv + hv) * a.Dv + row0;
+        }
+#pragma unroll
+        for (int m = 4; m; m >>= 1)
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                const float u = be * (vs[t][warp * 4 * NR + lane / 8 + 4 * i] - al * p[i]);
-                if (sub == 0) out[4 * i] = from_f32<T>(a.scale * (al * s[i] + u * c));
+                p[i] += __shfl_xor_sync(0xffffffffu, p[i], m);
+                s[i] += __shfl_xor_sync(0xffffffffu, s[i], m);
+            }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const float u = be * (v[i] - al * p[i]);
+            if (sub == 0) o[4 * i] = from_f32<T>(a.scale * (al * s[i] + u * c));
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[i][j][e] = al * S[i][j][e] + u * kk[j][e];
+        }
+    };
+    if constexpr (ONE) {
+        if (tokens > 0) {
+            float kk[N][4], qq[N][4], sk = 0.f, sq = 0.f, c = 0.f, v[NR];
+            load_row<T, N>(kp + 4 * sub, kk);
+            load_row<T, N>(qp + 4 * sub, qq);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) v[i] = to_f32(vp[row + 4 * i]);
+            const float al = expf(a.g[tok0 * a.Hv + hv]), be = a.beta[tok0 * a.Hv + hv];
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sk += kk[j][e] * kk[j][e];
+                    sq += qq[j][e] * qq[j][e];
+                    c += kk[j][e] * qq[j][e];
+                }
+#pragma unroll
+            for (int m = 4; m; m >>= 1) {
+                sk += __shfl_xor_sync(0xffffffffu, sk, m);
+                sq += __shfl_xor_sync(0xffffffffu, sq, m);
+                c += __shfl_xor_sync(0xffffffffu, c, m);
+            }
+            const float rk = inverse_norm(sk, a.eps), rq = inverse_norm(sq, a.eps);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kk[j][e] *= rk, qq[j][e] *= rq;
+            step(kk, qq, al, be, c * rk * rq, v, out);
+        }
+    } else {
+        // a warp stages four tokens of kTokens, eight lanes each; the next ones while these are computed
+        auto stage = [&](int t0, int which) {
+            Stage& s = sm[which];
+            const int t = warp * 4 + lane / 8;
+            if (t0 + t < tokens) {
+                float kk[N][4], qq[N][4], sk = 0.f, sq = 0.f, c = 0.f;
+                load_row<T, N>(kp + (t0 + t) * a.k_ld + 4 * sub, kk);
+                load_row<T, N>(qp + (t0 + t) * a.q_ld + 4 * sub, qq);
+                float v[ROWS / 8];
+#pragma unroll
+                for (int i = 0; i < ROWS / 8; ++i) v[i] = to_f32(vp[(t0 + t) * a.v_ld + sub + 8 * i]);
+                const float g = a.g[(tok0 + t0 + t) * a.Hv + hv], be = a.beta[(tok0 + t0 + t) * a.Hv + hv];
 #pragma unroll
                 for (int j = 0; j < N; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) S[i][j][e] = al * S[i][j][e] + u * kk[j][e];
+                    for (int e = 0; e < 4; ++e) {
+                        sk += kk[j][e] * kk[j][e];
+                        sq += qq[j][e] * qq[j][e];
+                        c += kk[j][e] * qq[j][e];
+                    }
+                const unsigned group = 0xffu << (lane & 24);
+#pragma unroll
+                for (int m = 4; m; m >>= 1) {
+                    sk += __shfl_xor_sync(group, sk, m);
+                    sq += __shfl_xor_sync(group, sq, m);
+                    c += __shfl_xor_sync(group, c, m);
+                }
+                const float rk = inverse_norm(sk, a.eps), rq = inverse_norm(sq, a.eps);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    *reinterpret_cast<float4*>(&s.k[t][32 * j + 4 * sub]) =
+                        make_float4(kk[j][0] * rk, kk[j][1] * rk, kk[j][2] * rk, kk[j][3] * rk);
+                    *reinterpret_cast<float4*>(&s.q[t][32 * j + 4 * sub]) =
+                        make_float4(qq[j][0] * rq, qq[j][1] * rq, qq[j][2] * rq, qq[j][3] * rq);
+                }
+#pragma unroll
+                for (int i = 0; i < ROWS / 8; ++i) vs[which][t][sub + 8 * i] = v[i];
+                if (sub == 0) {
+                    s.gate[t] = expf(g);
+                    s.rate[t] = be;
+                    s.kq[t] = c * rk * rq;
+                }
             }
+        };
+        stage(0, 0);
+        __syncthreads();
+#pragma unroll 1
+        for (int t0 = 0; t0 < tokens; t0 += Stage::kTokens) {
+            const int which = t0 / Stage::kTokens & 1, m = min(Stage::kTokens, tokens - t0);
+            const Stage& s = sm[which];
+            if (t0 + Stage::kTokens < tokens) stage(t0 + Stage::kTokens, which ^ 1);
+#pragma unroll 1
+            for (int t = 0; t < m; ++t) {
+                float kk[N][4], qq[N][4], v[NR];
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float4 x = *reinterpret_cast<const float4*>(&s.k[t][32 * j + 4 * sub]);
+                    const float4 y = *reinterpret_cast<const float4*>(&s.q[t][32 * j + 4 * sub]);
+                    kk[j][0] = x.x, kk[j][1] = x.y, kk[j][2] = x.z, kk[j][3] = x.w;
+                    qq[j][0] = y.x, qq[j][1] = y.y, qq[j][2] = y.z, qq[j][3] = y.w;
+                }
+#pragma unroll
+                for (int i = 0; i < NR; ++i) v[i] = vs[which][t][row + 4 * i];
+                step(kk, qq, s.gate[t], s.rate[t], s.kq[t], v, out + static_cast<long long>(t0 + t) * a.Hv * a.Dv);
+            }
+            __syncthreads();
         }
     }
     if (!a.state_out) return;
@@ -134,14 +221,21 @@ __global__ void __launch_bounds__(32 * kWarps) delta_recurrent_kernel(const Delt
     for (int i = 0; i < NR; ++i)
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            *reinterpret_cast<float4*>(a.state_out + state0 + 1ll * (row0 + 4 * i) * DK + 32 * j) =
-                make_float4(S[i][j][0], S[i][j][1], S[i][j][2], S[i][j][3]);
+            *reinterpret_cast<float4*>(a.state_out + state0 + 4 * i * DK + 32 * j) = make_float4(S[i][j][0], S[i][j][1], S[i][j][2], S[i][j][3]);
+}
+
+template <typename T, int DK, int NR, bool ONE>
+cudaError_t launch_rows(const DeltaArgs& a, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(1ll * a.R * a.Hv * (a.Dv / (kWarps * 4 * NR))));
+    return launch_pdl(delta_recurrent_kernel<T, DK, NR, ONE>, grid, dim3(32 * kWarps), 0, s, a);
 }
 
 template <typename T, int DK>
-cudaError_t launch_rows(const DeltaArgs& a, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(1ll * a.R * a.Hv * (a.Dv / (kWarps * 8))));
-    return launch_pdl(delta_recurrent_kernel<T, DK, 2>, grid, dim3(32 * kWarps), 0, s, a);
+cudaError_t launch_dk(const DeltaArgs& a, cudaStream_t s) {
+    if (a.n == 1) return launch_rows<T, DK, 2, true>(a, s);
+    // with few rows, a lane group for every row: the chain of a token is shorter
+    if (1ll * a.R * a.Hv * a.Dv <= 16384) return launch_rows<T, DK, 1, false>(a, s);
+    return launch_rows<T, DK, 2, false>(a, s);
 }
 
 int check_delta(const moestep_delta_dims* dd, int R, int n) {
@@ -156,8 +250,8 @@ int check_delta(const moestep_delta_dims* dd, int R, int n) {
 }  // namespace
 
 cudaError_t launch_delta_recurrent(const DeltaArgs& a, int dtype, cudaStream_t s) {
-    if (dtype == MOESTEP_F32) return a.Dk == 128 ? launch_rows<float, 128>(a, s) : launch_rows<float, 64>(a, s);
-    return a.Dk == 128 ? launch_rows<bf16, 128>(a, s) : launch_rows<bf16, 64>(a, s);
+    if (dtype == MOESTEP_F32) return a.Dk == 128 ? launch_dk<float, 128>(a, s) : launch_dk<float, 64>(a, s);
+    return a.Dk == 128 ? launch_dk<bf16, 128>(a, s) : launch_dk<bf16, 64>(a, s);
 }
 
 }  // namespace moestep
