@@ -159,20 +159,23 @@ __device__ __forceinline__ int by_cols(int lane) { return in_block((lane >> 3 & 
 // 8192 tokens of 32 heads; in loops of 16 rows 150 us.)
 template <int DK>
 struct PrepSmem {
-    struct Blocks {
-        char ahi[6 * 512], alo[6 * 512];  // A' below its diagonal blocks
-        float at[4][16][20];              // the diagonal blocks, transposed
-    };
     union {
         struct {
             alignas(128) char k[Tile<DK>::kBytes];  // K and Q as they go to global memory
             char q[Tile<DK>::kBytes];
         };
-        Blocks blocks[2];  // of two value heads, once the products of k and q are taken
+        // then of two value heads: X high, X low, factors, P, factors, as they go to global memory.  Before X is there,
+        // its place has the tokens' sums of g and beta c^2.
+        char x[2][kHeadBytes];
     };
-    alignas(128) char x[2][kHeadBytes];  // X high, X low, P, factors, as they go to global memory
-    float ck[C], cq[C];                  // factors of the keys and queries
-    float ghi[2][C], glo[2][C], beta[2][C];
+    struct Blocks {
+        char ahi[6 * 512], alo[6 * 512];  // A' below its diagonal blocks
+        float at[4][16][16];              // the diagonal blocks, transposed
+    } blocks[2];
+    float ck[C], cq[C];  // factors of the keys and queries
+};
+struct Gates {  // in x
+    float ghi[C], glo[C], beta[C];
 };
 
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
@@ -277,22 +280,25 @@ __device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t 
 }
 
 template <int DK>
-__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, const Scratch w) {
+__global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, const Scratch w) {
     extern __shared__ __align__(128) char raw[];
     PrepSmem<DK>& sm = *reinterpret_cast<PrepSmem<DK>*>(raw);
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, pair = warp / 2;
     const int hk = blockIdx.x % a.Hk, chunk = blockIdx.x / a.Hk % w.chunks, r = blockIdx.x / a.Hk / w.chunks;
-    int tokens, slot;
-    if (!delta_request(a, r, false, tokens, slot)) return;
-    const int m = min(C, tokens - chunk * C);
-    if (m <= 0) return;
     const long long tok0 = 1ll * r * a.n + chunk * C;
+    // A first chunk's rows are on their way before it is known how many are tokens (they are the request's memory in any
+    // case); later ones, of which ragged batches have many without a token, wait for it.
+    int tokens = a.n, slot = 0;
+    if (chunk && !delta_request(a, r, false, tokens, slot)) return;
+    const int there = tokens - chunk * C;
+    if (there <= 0) return;
     const long long unit = 1ll * r * w.chunks + chunk;
     const int group = a.Hv / a.Hk;
 
     // keys and queries: f16 after a power of two a row, four lanes a row
+    constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
     constexpr int PIECES = DK / 32;  // 16-byte pieces of a lane: 64 bytes of a row together
     const int sub = lane % 4;
     uint4 in[2][2][PIECES];
@@ -304,12 +310,15 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 #pragma unroll
         for (int j = 0; j < PIECES; ++j) {
             in[0][i][j] = in[1][i][j] = make_uint4(0, 0, 0, 0);
-            if (t < m) {
+            if (t < there) {
                 in[0][i][j] = __ldg(reinterpret_cast<const uint4*>(kp + 32 * j));
                 in[1][i][j] = __ldg(reinterpret_cast<const uint4*>(qp + 32 * j));
             }
         }
     }
+    if (!chunk && !delta_request(a, r, false, tokens, slot)) return;
+    const int m = min(C, tokens - chunk * C);
+    if (m <= 0) return;
     float gs[2], be[2];  // of the first two value heads, by an even warp each: tokens 2 lane and 2 lane + 1
     auto load_gates = [&](int v) {
 #pragma unroll
@@ -329,6 +338,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
             float f[8 * PIECES], most = 0.f;
 #pragma unroll
             for (int j = 0; j < PIECES; ++j) {
+                if (t >= m) in[which][i][j] = make_uint4(0, 0, 0, 0);
                 const uint32_t xs[4] = {in[which][i][j].x, in[which][i][j].y, in[which][i][j].z, in[which][i][j].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -361,28 +371,33 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
         bulk_commit();
     }
 
-    // k.k and q.k of this warp's 16 tokens with the tokens up to them
+    // k.k and q.k of this warp's tokens with the tokens up to them: eight tokens from the front and eight from the back, so
+    // that every warp has as many pairs
+    const int front = warp, back = 7 - warp;  // in eights
     float kk[8][4], qk[8][4];
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) kk[t][e] = qk[t][e] = 0.f;
     const uint32_t ks = tc::smem_addr(sm.k), qs = tc::smem_addr(sm.q);
-    const int rows = by_rows(lane), cols = by_cols(lane);
+    {
+        const int eight = lane >> 3 & 1 ? back : front;
+        const int own = eight / 2 * KB + in_block(eight % 2 * 8 + (lane & 7), lane >> 4), rows = by_rows(lane);
 #pragma unroll 2
-    for (int kt = 0; kt < DK / 16; ++kt) {
-        uint32_t ak[4], aq[4];
-        ldsm4(ak, ks + (warp * (DK / 16) + kt) * 512 + cols);
-        ldsm4(aq, qs + (warp * (DK / 16) + kt) * 512 + cols);
+        for (int kt = 0; kt < DK / 16; ++kt) {
+            uint32_t ak[4], aq[4];
+            ldsm4(ak, ks + kt * 512 + own);
+            ldsm4(aq, qs + kt * 512 + own);
 #pragma unroll
-        for (int t2 = 0; t2 < 4; ++t2) {
-            if (t2 > warp) continue;
-            uint32_t b[4];
-            ldsm4(b, ks + (t2 * (DK / 16) + kt) * 512 + rows);
-            mma(kk[2 * t2], ak, b[0], b[1]);
-            mma(kk[2 * t2 + 1], ak, b[2], b[3]);
-            mma(qk[2 * t2], aq, b[0], b[1]);
-            mma(qk[2 * t2 + 1], aq, b[2], b[3]);
+            for (int t2 = 0; t2 < 4; ++t2) {
+                if (2 * t2 > back) continue;
+                uint32_t b[4];
+                ldsm4(b, ks + t2 * KB + kt * 512 + rows);
+                mma(kk[2 * t2], ak, b[0], b[1]);
+                mma(kk[2 * t2 + 1], ak, b[2], b[3]);
+                mma(qk[2 * t2], aq, b[0], b[1]);
+                mma(qk[2 * t2 + 1], aq, b[2], b[3]);
+            }
         }
     }
 
@@ -390,12 +405,11 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 #pragma unroll 1
     for (int v0 = 0; v0 < group; v0 += 2) {  // two value heads at a time, a pair of warps each
         const bool on = v0 + pair < group;
-        if (tid == 0) bulk_wait_read();  // K and Q, or x[], have been read: their places are free
-        if (v0) {
-            __syncthreads();
-            if (warp % 2 == 0) load_gates(v0 + pair);
-        }
+        if (tid == 0) bulk_wait_read();
+        __syncthreads();  // K and Q, or x[], have been read: their place is free
+        if (v0 && warp % 2 == 0) load_gates(v0 + pair);
         if (on && warp % 2 == 0) {
+            Gates& gates = *reinterpret_cast<Gates*>(sm.x[pair]);
             float* vec = reinterpret_cast<float*>(sm.x[pair] + 2 * kTri);
             float* out = reinterpret_cast<float*>(sm.x[pair] + kXBytes + kTri);
             Sum s[2];  // sums of g, to base 2
@@ -421,10 +435,10 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 const float hi = s[i].hi;
-                sm.ghi[pair][t] = hi;
-                sm.glo[pair][t] = s[i].lo;
+                gates.ghi[t] = hi;
+                gates.glo[t] = s[i].lo;
                 const float ck = sm.ck[t], cq = sm.cq[t] * a.scale, since = exp2f(hi + s[i].lo);
-                sm.beta[pair][t] = be[i] * ck * ck;
+                gates.beta[t] = be[i] * ck * ck;
                 vec[kA * C + t] = since * ck;
                 vec[kBeta * C + t] = be[i] * ck;
                 out[kB * C + t] = since * cq;
@@ -440,34 +454,35 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
             if (v0 + p >= group) break;
             char* const ps = sm.x[p] + kXBytes;
             typename PrepSmem<DK>::Blocks& bl = sm.blocks[p];
-            const int i0 = warp * 16 + g4;
-            const float gh[2] = {sm.ghi[p][i0], sm.ghi[p][i0 + 8]}, gl[2] = {sm.glo[p][i0], sm.glo[p][i0 + 8]};
-            const float bc[2] = {sm.beta[p][i0], sm.beta[p][i0 + 8]};
+            const Gates& gates = *reinterpret_cast<const Gates*>(sm.x[p]);
+            const int i0[2] = {8 * front + g4, 8 * back + g4};
+            const float gh[2] = {gates.ghi[i0[0]], gates.ghi[i0[1]]}, gl[2] = {gates.glo[i0[0]], gates.glo[i0[1]]};
+            const float bc[2] = {gates.beta[i0[0]], gates.beta[i0[1]]};
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                if (t / 2 > warp) continue;
-                const float2 jh = *reinterpret_cast<const float2*>(&sm.ghi[p][8 * t + 2 * q4]);
-                const float2 jl = *reinterpret_cast<const float2*>(&sm.glo[p][8 * t + 2 * q4]);
-                const bool diagonal = t / 2 == warp;
+                if (t > (back | 1)) continue;
+                const float2 jh = *reinterpret_cast<const float2*>(&gates.ghi[8 * t + 2 * q4]);
+                const float2 jl = *reinterpret_cast<const float2*>(&gates.glo[8 * t + 2 * q4]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int i = i0 + 8 * h, j = 8 * t + 2 * q4;
-                    float e0 = exp2_fast((gh[h] - jh.x) + (gl[h] - jl.x)), e1 = exp2_fast((gh[h] - jh.y) + (gl[h] - jl.y));
-                    if (diagonal) {
-                        if (j > i) e0 = 0.f;
-                        if (j + 1 > i) e1 = 0.f;
-                        // the elements on and above the diagonal are not looked at
-                        bl.at[warp][j % 16][i % 16] = e0 * bc[h] * kk[t][2 * h];
-                        bl.at[warp][j % 16 + 1][i % 16] = e1 * bc[h] * kk[t][2 * h + 1];
+                    const int eight = h ? back : front;
+                    if (t > (eight | 1)) continue;
+                    const int i = i0[h], j = 8 * t + 2 * q4, at = in_block(eight % 2 * 8 + g4, t % 2) + 4 * q4;
+                    const float e0 = exp2_fast((gh[h] - jh.x) + (gl[h] - jl.x)), e1 = exp2_fast((gh[h] - jh.y) + (gl[h] - jl.y));
+                    const float a0 = e0 * bc[h] * kk[t][2 * h], a1 = e1 * bc[h] * kk[t][2 * h + 1];
+                    float p0 = e0 * qk[t][2 * h], p1 = e1 * qk[t][2 * h + 1];
+                    if (t / 2 == eight / 2) {  // (the elements of A' on and above the diagonal are not looked at)
+                        bl.at[t / 2][j % 16][i % 16] = a0;
+                        bl.at[t / 2][j % 16 + 1][i % 16] = a1;
+                        if (j > i) p0 = 0.f;
+                        if (j + 1 > i) p1 = 0.f;
                     } else {
                         uint32_t hi, lo;
-                        split(e0 * bc[h] * kk[t][2 * h], e1 * bc[h] * kk[t][2 * h + 1], hi, lo);
-                        *reinterpret_cast<uint32_t*>(bl.ahi + below(warp, t / 2) + in_block(g4 + 8 * h, t % 2) + 4 * q4) = hi;
-                        *reinterpret_cast<uint32_t*>(bl.alo + below(warp, t / 2) + in_block(g4 + 8 * h, t % 2) + 4 * q4) = lo;
+                        split(a0, a1, hi, lo);
+                        *reinterpret_cast<uint32_t*>(bl.ahi + below(eight / 2, t / 2) + at) = hi;
+                        *reinterpret_cast<uint32_t*>(bl.alo + below(eight / 2, t / 2) + at) = lo;
                     }
-                    // (a factor of zero, not a product with what may be inf, above the diagonal)
-                    const float p0 = diagonal && j > i ? 0.f : e0 * qk[t][2 * h], p1 = diagonal && j + 1 > i ? 0.f : e1 * qk[t][2 * h + 1];
-                    *reinterpret_cast<uint32_t*>(ps + tri(warp, t / 2) + in_block(g4 + 8 * h, t % 2) + 4 * q4) = pack(p0, p1);
+                    *reinterpret_cast<uint32_t*>(ps + tri(eight / 2, t / 2) + at) = pack(p0, p1);
                 }
             }
         }
@@ -477,7 +492,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
             char* const xp = sm.x[pair];
             {  // diagonal blocks: column c of block b, an elimination in registers
                 const int c = warp % 2 * 32 + lane, b = c / 16;
-                const float(*at)[20] = sm.blocks[pair].at[b];
+                const float(*at)[16] = sm.blocks[pair].at[b];
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = i == c % 16 ? 1.f : 0.f;
@@ -523,9 +538,9 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 // Bound: a warp's dependent chain of instructions (170 of them MMAs at 8 cycles), while there are fewer than two or three
 // warps a scheduler; with more, the rate of mma.sync (1024 multiplications a cycle and multiprocessor; 400 MMAs a
 // slice and chunk).
-template <int DK, int W>
+template <int DK, int W, int NS>
 struct WalkSmem {
-    static constexpr int kStages = W <= 2 ? 3 : 2;
+    static constexpr int QS = NS == 1 ? 1 : 2;
     struct ForStates {
         char k[Tile<DK>::kBytes];
         char x[kXBytes];
@@ -534,8 +549,8 @@ struct WalkSmem {
         char q[Tile<DK>::kBytes];
         char p[kPBytes];
     };
-    alignas(128) ForStates x[kStages];
-    ForOutputs q[2];
+    alignas(128) ForStates x[NS];
+    ForOutputs q[QS];
     struct Pass {                    // of a slice, from warp p to the others
         uint4 s[2][2][DK / 32][32];  // [chunk % 2][p][k step][lane]: S0, high
         uint4 sl[2][DK / 32][32];    // low
@@ -546,7 +561,7 @@ struct WalkSmem {
     } pass[W];
     char v[2 * W][2][32 * 32];  // a warp's 32 tokens of 16 values
     char o[W][C * 32];          // 64 tokens of 16 outputs
-    uint64_t x_full[kStages], x_empty[kStages], q_full[2], q_empty[2];
+    uint64_t x_full[NS], x_empty[NS], q_full[QS], q_empty[QS];
     uint64_t given[W][2], taken[W][2];  // S0 and U' of chunk % 2 for the third warp
     int abort, request;
 };
@@ -556,12 +571,12 @@ struct WalkSmem {
 template <int W>
 constexpr int kWalkWarps = 3 * W + (W == 2);
 
-template <int DK, int W>
-__global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
+template <int DK, int W, int NS, int CTAS>
+__global__ void __launch_bounds__(32 * kWalkWarps<W>, CTAS) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
     extern __shared__ __align__(128) char raw[];
-    using Smem = WalkSmem<DK, W>;
+    using Smem = WalkSmem<DK, W, NS>;
     Smem& sm = *reinterpret_cast<Smem*>(raw);
-    constexpr int NS = Smem::kStages;
+    constexpr int QS = Smem::QS;
     constexpr int NK = DK / 32;  // k steps of 16 of a half of the state's columns
     constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g4 = lane / 4, q4 = lane % 4;
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             tc::mbar_init(&sm.x_full[i], 1);
             tc::mbar_init(&sm.x_empty[i], 2 * W);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < QS; ++i) {
             tc::mbar_init(&sm.q_full[i], 1);
             tc::mbar_init(&sm.q_empty[i], W);
         }
@@ -628,8 +643,8 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         if (W == 2 && p) return;
         const bool fetches = mine == 0 && lane == 0;
         auto fetch = [&]() {
-            const int st = issued & 1;
-            if (issued >= 2) wait(&sm.q_empty[st], (issued >> 1) - 1);
+            const int st = issued % QS;
+            if (issued >= QS) wait(&sm.q_empty[st], issued / QS - 1);
             if (!ok) return;
             tc::mbar_arrive_expect_tx(&sm.q_full[st], Tile<DK>::kBytes + kPBytes);
             bulk_load(tc::smem_addr(sm.q[st].q), keys(issued) + Tile<DK>::kBytes, Tile<DK>::kBytes, &sm.q_full[st]);
@@ -643,10 +658,10 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             const int cb = c & 1;
             if (fetches && ok && issued < n_chunks) fetch();
             __syncwarp();
-            wait(&sm.q_full[cb], c >> 1);
+            wait(&sm.q_full[c % QS], c / QS);
             wait(&sm.given[mine][cb], c >> 1);
             __syncwarp();
-            typename Smem::ForOutputs& s = sm.q[cb];
+            typename Smem::ForOutputs& s = sm.q[c % QS];
             const uint32_t qr = tc::smem_addr(s.q) + rows, pr = tc::smem_addr(s.p) + rows;
             const float* vec = reinterpret_cast<const float*>(s.p + kTri) + 2 * q4;
             // S0 Q^T, with the columns of each half of S0 and their scale
@@ -717,7 +732,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             __syncwarp();  // S0, U' and the tiles have been read
             if (lane == 0) {
                 tc::mbar_arrive(&sm.taken[mine][cb]);
-                tc::mbar_arrive(&sm.q_empty[cb]);
+                tc::mbar_arrive(&sm.q_empty[c % QS]);
             }
 #pragma unroll
             for (int t2 = 0; t2 < 4; ++t2) {
@@ -746,8 +761,8 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             if (lane == 0) record_error(a.err, kErrTimeoutEpilogue);
             if (fetches) {
                 int zero = 0;
-                for (int i = max(0, issued - 2); i < issued; ++i)
-                    tc::mbar_wait(&sm.q_full[i & 1], (i >> 1) & 1, &zero, 1000000000ull);
+                for (int i = max(0, issued - QS); i < issued; ++i)
+                    tc::mbar_wait(&sm.q_full[i % QS], (i / QS) & 1, &zero, 1000000000ull);
             }
         }
         return;
@@ -763,7 +778,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         ++issued;
     };
     if (tid == 0)
-        while (issued < NS - 1 && issued < n_chunks) fetch();
+        while (issued < (NS == 1 ? 1 : NS - 1) && issued < n_chunks) fetch();  // (one stage: one chunk)
 
     const uint32_t vs = tc::smem_addr(sm.v[warp]);
     auto fetch_v = [&](int c) {  // the warp's values, zeros behind the request's tokens
@@ -1091,14 +1106,15 @@ cudaError_t launch_prep(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
     return launch_pdl(delta_prep_kernel<DK>, grid, dim3(128), sizeof(PrepSmem<DK>), s, a, w);
 }
 
-template <int DK, int W>
+template <int DK, int W, int NS, int CTAS>
 cudaError_t launch_walk(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
-    static_assert(sizeof(WalkSmem<DK, W>) <= 227 * 1024);
+    constexpr size_t bytes = sizeof(WalkSmem<DK, W, NS>);
+    static_assert(CTAS * (bytes + 1024) <= 228 * 1024);
     static int done[64];
-    cudaError_t e = ensure_smem(delta_walk_kernel<DK, W>, sizeof(WalkSmem<DK, W>), done);
+    cudaError_t e = ensure_smem(delta_walk_kernel<DK, W, NS, CTAS>, bytes, done);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.R * a.Hv * (a.Dv / (16 * W))));
-    return launch_pdl(delta_walk_kernel<DK, W>, grid, dim3(32 * kWalkWarps<W>), sizeof(WalkSmem<DK, W>), s, a, w);
+    return launch_pdl(delta_walk_kernel<DK, W, NS, CTAS>, grid, dim3(32 * kWalkWarps<W>), bytes, s, a, w);
 }
 
 template <int DK>
@@ -1106,17 +1122,20 @@ cudaError_t launch_chunks(const DeltaArgs& a, const Scratch& w, int sms, cudaStr
     cudaError_t e = launch_prep<DK>(a, w, s);
     if (e != cudaSuccess) return e;
     count_launch();
-    // as few warps a block as keep the multiprocessors busy: a block's tiles are shared by its warps
+    // As few slices a block as keep the multiprocessors busy: a block's tiles are shared by its slices.
     const long long slices = 1ll * a.R * a.Hv * (a.Dv / 16);
-    if (slices <= 2ll * sms) return launch_walk<DK, 2>(a, w, s);
-    return launch_walk<DK, 4>(a, w, s);
+    if (slices <= 2ll * sms) return launch_walk<DK, 2, 3, 1>(a, w, s);
+    return launch_walk<DK, 4, 2, 1>(a, w, s);
 }
 
 size_t qk_bytes(const moestep_delta_dims& d, long long units) { return static_cast<size_t>(units) * d.Hk * 2 * C * d.Dk * 2; }
 
 }  // namespace
 
-bool delta_chunked(const moestep_delta_dims& d, int R, int n) { return d.dtype == MOESTEP_BF16 && n >= 64; }
+// From 32 tokens on the two launches are faster than the recurrence, whatever the number of requests (us, 16 and 32 heads of
+// 128, one request: 24 tokens 13.1 against 11.3, 32 tokens 13.1 : 14.1, 64 tokens 13.4 : 25.8; 16 requests: 24 tokens 51 : 55,
+// 32 tokens 51 : 72).
+bool delta_chunked(const moestep_delta_dims& d, int R, int n) { return d.dtype == MOESTEP_BF16 && n >= 32; }
 
 size_t delta_chunk_bytes(const moestep_delta_dims& d, int R, int n) {
     if (!delta_chunked(d, R, n)) return 0;
