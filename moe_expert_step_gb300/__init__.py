@@ -466,14 +466,18 @@ def kv_cache_plan(kd: KvDims, R: int, kv_len, n_new, ring, head, head_out, table
     the ring of free ones [n_pages] with head [2] = (first, count), or back to it; the tables [R, max_pages] are
     extended, pos [R, n] (-1 behind the new tokens), slots [R, n] and new_len [R] are written.  All int32; see
     kv_cache_plan in moestep.h."""
-    n, i32 = pos.shape[-1], _types()["int"]
-    for t, shape, what in ((kv_len, (R,), "kv_len"), (n_new, (R,), "n_new"), (new_len, (R,), "new_len"),
-                           (ring, (kd.n_pages,), "ring"), (head, (2,), "head"), (head_out, (2,), "head_out"),
-                           (pos, (R, n), "pos")):
-        _dense(t, shape, i32, "kv_cache_plan: " + what)
-    if table.dim() != 2 or table.shape[0] < R:
+    n, i32, requests = pos.shape[-1], _types()["int"], (R,)
+    _dense(kv_len, requests, i32, "kv_cache_plan: kv_len")
+    _dense(n_new, requests, i32, "kv_cache_plan: n_new")
+    _dense(new_len, requests, i32, "kv_cache_plan: new_len")
+    _dense(ring, (kd.n_pages,), i32, "kv_cache_plan: ring")
+    _dense(head, (2,), i32, "kv_cache_plan: head")
+    _dense(head_out, (2,), i32, "kv_cache_plan: head_out")
+    _dense(pos, (R, n), i32, "kv_cache_plan: pos")
+    rows = table.shape[0]
+    _dense(table, (rows, kd.max_pages), i32, "kv_cache_plan: table")
+    if rows < R:
         raise MoeStepError(EINVAL, "kv_cache_plan: table must have a row a request")
-    _dense(table, (table.shape[0], kd.max_pages), i32, "kv_cache_plan: table")
     if slots is not None:
         _dense(slots, (R, n), i32, "kv_cache_plan: slots")
     _on_gpu(ws, "kv_cache_plan")
@@ -501,16 +505,6 @@ def rotary_frequencies(rot: int, base: float, scaling: int = ROTARY_PLAIN, facto
     return freq
 
 
-def _rotary_rows(x, heads: int, kd: KvDims, T: int, what: str):
-    """Pointer and row distance of x [T, heads, D] (None: absent)."""
-    if x is None:
-        return None, 0
-    ld = _rows(x, heads, kd, what)
-    if x.shape[0] != T:
-        raise MoeStepError(EINVAL, f"{what} must have a row a position")
-    return x.data_ptr(), ld
-
-
 def block_rotary(kd: KvDims, q, k, pos, freq, q_out, k_out, interleaved: bool = False, mscale: float = 1.0,
                  stream=None) -> None:
     """Turn the first 2 * len(freq) of the D elements of q [R * n, Hq, D] and k [R * n, Hkv, D] (either may be None;
@@ -518,17 +512,18 @@ def block_rotary(kd: KvDims, q, k, pos, freq, q_out, k_out, interleaved: bool = 
     which may be q and k themselves.  freq: of rotary_frequencies; pairs are halves of the rotated part apart, or
     neighbours where interleaved; see block_rotary in moestep.h."""
     types = _types()
-    if pos.dim() != 2:
-        raise MoeStepError(EINVAL, "block_rotary: pos must be [R, n]")
-    R, n = pos.shape
-    _dense(pos, (R, n), types["int"], "block_rotary: pos")
+    if pos.dim() != 2 or freq.dim() != 1:
+        raise MoeStepError(EINVAL, "block_rotary: pos must be [R, n], freq [rot / 2]")
+    R, n = shape = pos.shape
+    _dense(pos, shape, types["int"], "block_rotary: pos")
     _dense(freq, freq.shape, types["turn"], "block_rotary: freq")
-    qp, q_ld = _rotary_rows(q, kd.Hq, kd, R * n, "block_rotary: q")
-    kp, k_ld = _rotary_rows(k, kd.Hkv, kd, R * n, "block_rotary: k")
-    qo, qo_ld = _rotary_rows(q_out, kd.Hq, kd, R * n, "block_rotary: q_out")
-    ko, ko_ld = _rotary_rows(k_out, kd.Hkv, kd, R * n, "block_rotary: k_out")
-    _check(lib().block_rotary(kd._c, R, n, qp, q_ld, kp, k_ld, pos.data_ptr(), freq.data_ptr(), 2 * freq.numel(),
-                              int(interleaved), mscale, qo, qo_ld, ko, ko_ld, _s(stream)), "block_rotary")
+    T, act = R * n, types.get(kd.dtype)
+    q_ld = 0 if q is None else _head_rows(q, T, kd.Hq, kd.D, act, "block_rotary: q")
+    k_ld = 0 if k is None else _head_rows(k, T, kd.Hkv, kd.D, act, "block_rotary: k")
+    qo_ld = 0 if q_out is None else _head_rows(q_out, T, kd.Hq, kd.D, act, "block_rotary: q_out")
+    ko_ld = 0 if k_out is None else _head_rows(k_out, T, kd.Hkv, kd.D, act, "block_rotary: k_out")
+    _check(lib().block_rotary(kd._c, R, n, _p(q), q_ld, _p(k), k_ld, pos.data_ptr(), freq.data_ptr(), 2 * freq.shape[0],
+                              int(interleaved), mscale, _p(q_out), qo_ld, _p(k_out), ko_ld, _s(stream)), "block_rotary")
 
 
 @dataclass(frozen=True)
@@ -565,13 +560,12 @@ def delta_workspace(dd: DeltaDims, R: int, n: int, device="cuda", stream=None):
 
 def _head_rows(t, T: int, heads: int, D: int, dtype, what: str) -> int:
     """Distance between the rows of t [T, heads, D], which may be part of a wider row."""
-    st, shape = t.stride(), t.shape
-    if (len(st) != 3 or shape[0] != T or shape[1] != heads or shape[2] != D or st[2] != 1
-            or (heads > 1 and st[1] != D) or t.dtype is not dtype):
-        raise MoeStepError(EINVAL, f"{what} must be [{T}, {heads}, {D}] in the activations' type, heads dense")
-    if not t.is_cuda:
-        raise MoeStepError(EINVAL, f"{what} must be on the GPU")
-    return st[0] if T > 1 else heads * D
+    if t.shape != (T, heads, D) or t.dtype is not dtype or not t.is_cuda:
+        raise MoeStepError(EINVAL, f"{what} must be [{T}, {heads}, {D}] in the activations' type, on the GPU")
+    ld, head, one = t.stride()
+    if one != 1 or (head != D and heads > 1):
+        raise MoeStepError(EINVAL, f"{what}: heads and their elements must be dense")
+    return ld if T > 1 else heads * D
 
 
 def block_delta_rule(dd: DeltaDims, R: int, q, k, v, g, beta, state, out, ws, state_out=None, slot=None, length=None,

@@ -7,7 +7,8 @@
 // are distinct, so blocks need no order among themselves.  Where a request's pages begin in
 // the ring is a sum over the requests before it.  Every block adds those up by itself (a few
 // loads a thread from L2 for the batches of serving) instead of waiting for a launch that does.
-// The header is written by the block that finishes last, so it may be updated in place.
+// The header is written by one block: the last that has read it where it is updated in place (a ticket tells),
+// else any.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv.h"
@@ -17,7 +18,7 @@ namespace moestep {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTicket = 64;  // word of the workspace's header that counts finished blocks
+constexpr int kTicket = 64;  // word of the workspace's header that counts the blocks that have read the ring's header
 
 struct PlanArgs {
     const int32_t* kv_len;
@@ -35,6 +36,7 @@ struct PlanArgs {
     int rows;      // requests of a block
     int segments;  // or, where that is 1, blocks of a request
     int wide;      // pos and slots can be written four at a time
+    int in_place;  // head_out is head
 };
 
 // What a request asks for
@@ -114,10 +116,10 @@ struct Row {
 __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
     __shared__ Sums sm[kThreads / 32];
     __shared__ Row rows[kThreads];
-    __shared__ bool last;
+    __shared__ bool writes;
     pdl_trigger();
     pdl_wait();
-    int first = a.head[0], count = a.head[1];  // (written below by the last block, after every block has read them)
+    int first = a.head[0], count = a.head[1];
     const bool broken = static_cast<unsigned>(first) >= static_cast<unsigned>(a.n_pages) ||
                         static_cast<unsigned>(count) > static_cast<unsigned>(a.n_pages);
     if (broken) first = 0, count = 0;
@@ -126,6 +128,14 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
     const int r0 = blockIdx.x / a.segments * a.rows, segment = blockIdx.x % a.segments;
     const int n_rows = min(a.rows, a.R - r0);
     const Sums before = block_sums(sums_of(a, 0, r0), sm);
+    // (behind the barriers of block_sums: every thread has read the header; the ticket wraps to 0 for the next call)
+    if (threadIdx.x == 0) {
+        writes = blockIdx.x == gridDim.x - 1;
+        if (a.in_place && gridDim.x > 1) {
+            __threadfence();
+            writes = atomicInc(reinterpret_cast<unsigned*>(a.ticket), gridDim.x - 1) == gridDim.x - 1;
+        }
+    }
     {
         Ask q{};
         Sums mine{0, 0};
@@ -149,9 +159,10 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
     }
     __syncthreads();
 
-    const long long ring = a.n_pages;
+    const unsigned ring = a.n_pages;
+    auto around = [&](unsigned i) { return i >= ring ? i - ring : i; };  // (i < 2 n_pages < 2^32)
     auto page_at = [&](const Row& w, int i) {  // table entry i >= held of a served request
-        const int id = a.ring[(first + w.take + (i - w.held)) % ring];
+        const int id = a.ring[around(first + static_cast<unsigned>(w.take) + (i - w.held))];
         if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages)) return id;
         record_error(a.err, kErrBadInput);
         return -1;
@@ -163,38 +174,41 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
         const int t0 = segment * kThreads + threadIdx.x;
         for (int i = w.held + t0; i < w.need; i += step) table[i] = page_at(w, i);
         for (int i = w.need + t0; i < w.held; i += step) {
-            const long long o = count + w.back + (i - w.need);
+            const long long o = count + w.back + (i - w.need);  // (w.back may be a broken table's)
             const int id = table[i];
-            if (o < ring) a.ring[(first + o) % ring] = id;  // (else more pages than the pool has)
+            if (o < ring) a.ring[around(first + static_cast<unsigned>(o))] = id;  // (else more pages than the pool has)
             if (o >= ring || static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_pages))
                 record_error(a.err, kErrBadInput);
         }
     }
 
     const int mask = (1 << a.page_log2) - 1;
-    auto place = [&](const Row& w, const int32_t* table, int i, int& p, int& slot) {
-        p = slot = -1;
-        if (i >= w.m) return;
-        p = w.len + i;
+    auto page_of = [&](const Row& w, const int32_t* table, int p) {  // first slot of the page of position p
         const int pg = p >> a.page_log2;
         const int id = pg < w.held ? __ldcg(&table[pg]) : page_at(w, pg);
-        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages))
-            slot = (id << a.page_log2) + (p & mask);
-        else
-            record_error(a.err, kErrBadInput);
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_pages)) return id << a.page_log2;
+        record_error(a.err, kErrBadInput);
+        return -1;
     };
+    auto slot_at = [&](int page, int p) { return page < 0 ? -1 : page + (p & mask); };
     if (a.wide) {
         const int quads = a.n / 4, total = n_rows * quads;
+#pragma unroll 4
         for (int k = segment * kThreads + threadIdx.x; k < total; k += step) {
-            const int j = k / quads, i = 4 * (k - j * quads);
+            const int j = a.rows > 1 ? k / quads : 0, i = 4 * (k - j * quads);
             const Row& w = rows[j];
             const long long at = static_cast<long long>(r0 + j) * a.n + i;
-            const int32_t* table = a.table + static_cast<long long>(r0 + j) * a.max_pages;
-            int4 p, s;
-            place(w, table, i, p.x, s.x);
-            place(w, table, i + 1, p.y, s.y);
-            place(w, table, i + 2, p.z, s.z);
-            place(w, table, i + 3, p.w, s.w);
+            int4 p = make_int4(-1, -1, -1, -1), s = p;
+            if (i < w.m) {
+                const int32_t* table = a.table + static_cast<long long>(r0 + j) * a.max_pages;
+                const int p0 = w.len + i, p3 = w.len + min(i + 3, w.m - 1);
+                const int page = page_of(w, table, p0), after = p3 >> a.page_log2 == p0 >> a.page_log2 ? page : page_of(w, table, p3);
+                auto slot = [&](int q) { return slot_at(q >> a.page_log2 == p0 >> a.page_log2 ? page : after, q); };
+                p.x = p0, s.x = slot(p0);
+                if (i + 1 < w.m) p.y = p0 + 1, s.y = slot(p0 + 1);
+                if (i + 2 < w.m) p.z = p0 + 2, s.z = slot(p0 + 2);
+                if (i + 3 < w.m) p.w = p0 + 3, s.w = slot(p0 + 3);
+            }
             *reinterpret_cast<int4*>(a.pos + at) = p;
             if (a.slots) *reinterpret_cast<int4*>(a.slots + at) = s;
         }
@@ -202,25 +216,18 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
         const long long total = static_cast<long long>(n_rows) * a.n;
         for (long long k = segment * kThreads + threadIdx.x; k < total; k += step) {
             const int j = static_cast<int>(k / a.n), i = static_cast<int>(k - static_cast<long long>(j) * a.n);
-            int p, s;
-            place(rows[j], a.table + static_cast<long long>(r0 + j) * a.max_pages, i, p, s);
+            const Row& w = rows[j];
+            const int p = i < w.m ? w.len + i : -1;
+            const int s = p < 0 ? -1 : slot_at(page_of(w, a.table + static_cast<long long>(r0 + j) * a.max_pages, p), p);
             const long long at = static_cast<long long>(r0) * a.n + k;
             a.pos[at] = p;
             if (a.slots) a.slots[at] = s;
         }
     }
 
-    // the header, by the block that ends last (the ticket wraps to 0 for the next call)
+    // the header
+    if (!writes) return;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        last = true;
-        if (gridDim.x > 1) {
-            __threadfence();
-            last = atomicInc(reinterpret_cast<unsigned*>(a.ticket), gridDim.x - 1) == gridDim.x - 1;
-        }
-    }
-    __syncthreads();
-    if (!last) return;
     Sums run{0, 0};
     long long taken = 0;
     for (int r = 0; r < a.R; r += kThreads) {
@@ -246,8 +253,8 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
             a.head_out[0] = a.head[0];
             a.head_out[1] = a.head[1];
         } else {
-            const long long most = ring - count;  // what did not fit was not written
-            a.head_out[0] = static_cast<int>((first + taken) % ring);
+            const long long most = static_cast<long long>(ring) - count;  // what did not fit was not written
+            a.head_out[0] = static_cast<int>(around(first + static_cast<unsigned>(taken)));
             a.head_out[1] = static_cast<int>(count - taken + min(run.drop, most));
         }
     }
@@ -292,6 +299,7 @@ extern "C" int kv_cache_plan(const moestep_kv_dims* kd, int R, int n, const int3
     a.page_log2 = kd->page == 16 ? 4 : kd->page == 32 ? 5 : kd->page == 64 ? 6 : 7;
     a.n_pages = kd->n_pages;
     a.max_pages = kd->max_pages;
+    a.in_place = head_out == head;
     a.wide = n % 4 == 0 && kv_aligned16(pos) && (!slots || kv_aligned16(slots));
     // a block writes about 4096 positions
     constexpr int kEntries = 4096;

@@ -34,6 +34,8 @@ struct RotaryArgs {
     float mscale;
 };
 
+constexpr int kHeads = 4;  // of a thread, at most
+
 // V elements of a 16-byte piece, or one
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Piece {
@@ -84,37 +86,45 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
     } else {
         lo = hi = a.rot + (item - a.turned) * V;
     }
+    // every load before the first store, which may go to the same rows
     const int heads = a.Hq + a.Hkv;
-#pragma unroll 4
-    for (int h = group; h < heads; h += a.groups) {
+    Piece<T, V> x[kHeads], y[kHeads];
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+        const int h = group + u * a.groups;
+        if (h >= heads) break;
         const bool key = h >= a.Hq;
-        const int hh = key ? h - a.Hq : h;
-        const T* src = static_cast<const T*>(key ? a.k : a.q) + t * (key ? a.k_ld : a.q_ld) + hh * a.D;
-        T* dst = static_cast<T*>(key ? a.k_out : a.q_out) + t * (key ? a.ko_ld : a.qo_ld) + hh * a.D;
-        Piece<T, V> x, y;
-        x.load(src + lo);
+        const T* src = static_cast<const T*>(key ? a.k : a.q) + t * (key ? a.k_ld : a.q_ld) + (key ? h - a.Hq : h) * a.D;
+        x[u].load(src + lo);
+        if (!(PAIRS && V > 1) && turned) y[u].load(src + hi);
+    }
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+        const int h = group + u * a.groups;
+        if (h >= heads) break;
+        const bool key = h >= a.Hq;
+        T* dst = static_cast<T*>(key ? a.k_out : a.q_out) + t * (key ? a.ko_ld : a.qo_ld) + (key ? h - a.Hq : h) * a.D;
         if (!turned) {
-            if (src != dst) x.store(dst + lo);
+            x[u].store(dst + lo);  // (of a row turned in place: what stands there)
             continue;
         }
         if constexpr (PAIRS && V > 1) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float u = to_f32(x.v[2 * i]), w = to_f32(x.v[2 * i + 1]);
-                x.v[2 * i] = from_f32<T>(u * cs[i] - w * sn[i]);
-                x.v[2 * i + 1] = from_f32<T>(w * cs[i] + u * sn[i]);
+                const float f = to_f32(x[u].v[2 * i]), g = to_f32(x[u].v[2 * i + 1]);
+                x[u].v[2 * i] = from_f32<T>(f * cs[i] - g * sn[i]);
+                x[u].v[2 * i + 1] = from_f32<T>(g * cs[i] + f * sn[i]);
             }
-            x.store(dst + lo);
+            x[u].store(dst + lo);
         } else {
-            y.load(src + hi);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float u = to_f32(x.v[i]), w = to_f32(y.v[i]);
-                x.v[i] = from_f32<T>(u * cs[i] - w * sn[i]);
-                y.v[i] = from_f32<T>(w * cs[i] + u * sn[i]);
+                const float f = to_f32(x[u].v[i]), g = to_f32(y[u].v[i]);
+                x[u].v[i] = from_f32<T>(f * cs[i] - g * sn[i]);
+                y[u].v[i] = from_f32<T>(g * cs[i] + f * sn[i]);
             }
-            x.store(dst + lo);
-            y.store(dst + hi);
+            x[u].store(dst + lo);
+            y[u].store(dst + hi);
         }
     }
 }
@@ -125,8 +135,8 @@ cudaError_t launch_rotary(RotaryArgs a, bool pairs, int sms, cudaStream_t s) {
     a.turned = pairs ? a.rot / (V == 1 ? 2 : V) : a.rot / 2 / V;
     const bool copies = (a.Hq && (a.q != a.q_out)) || (a.Hkv && (a.k != a.k_out));
     a.items = a.turned + (copies ? (a.D - a.rot) / V : 0);
-    // four heads a thread share its sines; where that leaves multiprocessors idle, fewer
-    a.groups = (heads + 3) / 4;
+    // kHeads heads a thread share its sines; where that leaves multiprocessors idle, fewer
+    a.groups = (heads + kHeads - 1) / kHeads;
     while (a.groups < heads && a.tokens * a.items * a.groups < 4ll * sms * 256) a.groups = a.groups * 2 < heads ? a.groups * 2 : heads;
     const long long blocks = (a.tokens * a.items * a.groups + 255) / 256;
     if (blocks > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
