@@ -7,7 +7,11 @@ the LowConfidence commit.  While a block is being resolved its keys and values a
 round, at the same positions; a resolved block is passed once more, so that the cache holds the
 committed tokens', and the next block follows it.
 
-    python examples/block_decoder.py [--fp8-cache] [--requests 2] [--prefix 100] [--blocks 2]
+    python examples/block_decoder.py [--fp8-cache] [--requests 2] [--prefix 100] [--blocks 2] [--hybrid]
+
+With --hybrid the cache's pages are given out on the GPU as blocks begin (kv_cache_plan), queries and keys carry
+rotary positions (block_rotary), and every second layer has the gated delta rule in the attention's place
+(block_delta_rule): its history is read while a block is being resolved, and takes the block in once it is.
 """
 from __future__ import annotations
 
@@ -76,22 +80,35 @@ class BlockDecoder:
         self.accept, self.n_committed = torch.zeros(T, dtype=torch.uint8, device="cuda"), i32(R)
         self.kv_len = i32(R)
 
-    def forward(self, record=None) -> None:
+    def places(self):
+        """Positions [R, P] of the block's tokens, and what each request has with them."""
+        return self.kv_len[:, None] + torch.arange(self.d.P, dtype=torch.int32, device="cuda"), self.kv_len + self.d.P
+
+    def mixer(self, i: int, L: Layer, pos, seen):
+        """The token mixer of layer i over self.x: [T, H]."""
+        kd = self.kd
+        qkv = (self.x @ L.Wqkv.t()).view(self.T, kd.Hq + 2 * kd.Hkv, kd.D)
+        q, k, v = qkv[:, :kd.Hq], qkv[:, kd.Hq:kd.Hq + kd.Hkv], qkv[:, kd.Hq + kd.Hkv:]
+        self.rotate(q, k, pos)
+        ms.kv_cache_write(kd, self.R, k, v, pos, L.cache, self.kv_ws)
+        ms.block_attention(kd, self.R, q, seen, L.cache, self.att, self.kv_ws, kd.D ** -0.5)
+        return self.att.view(self.T, -1) @ L.Wo.t()
+
+    def rotate(self, q, k, pos) -> None:
+        """(Positions come with the embeddings here.)"""
+
+    def forward(self, record=None, resolved: bool = False) -> None:
         """One pass of the block through the layers; its positions are kv_len .. kv_len + P - 1."""
-        d, kd, R = self.d, self.kd, self.R
-        pos = self.kv_len[:, None] + torch.arange(d.P, dtype=torch.int32, device="cuda")
-        seen = self.kv_len + d.P
+        d, R = self.d, self.R
+        self.resolved = resolved
+        pos, seen = self.places()
         ids = torch.where(self.masked.bool(), self.mask_id, self.tokens)
         ms.block_residual_norm(d, self.emb[ids.long()], self.pos_emb.repeat(R, 1), self.h, self.x,
                                w_pre=self.layers[0].attn_in)
         for i, L in enumerate(self.layers):
             if record is not None:
                 record.append(dict(h=self.h.clone(), x=self.x.clone()))
-            qkv = (self.x @ L.Wqkv.t()).view(self.T, kd.Hq + 2 * kd.Hkv, kd.D)
-            q, k, v = qkv[:, :kd.Hq], qkv[:, kd.Hq:kd.Hq + kd.Hkv], qkv[:, kd.Hq + kd.Hkv:]
-            ms.kv_cache_write(kd, R, k, v, pos, L.cache, self.kv_ws)
-            ms.block_attention(kd, R, q, seen, L.cache, self.att, self.kv_ws, kd.D ** -0.5)
-            ms.block_residual_norm(d, self.att.view(self.T, -1) @ L.Wo.t(), self.h, self.h, self.x, w_pre=L.moe_in,
+            ms.block_residual_norm(d, self.mixer(i, L, pos, seen), self.h, self.h, self.x, w_pre=L.moe_in,
                                    w_post=L.attn_out, gate=self.gate)
             if record is not None:
                 record[-1] |= dict(h_mid=self.h.clone(), x_mid=self.x.clone())
@@ -104,6 +121,7 @@ class BlockDecoder:
 
     def decode_block(self, threshold: float = 0.95, logit_scale: float = 1.0) -> int:
         """Resolve one block; returns the rounds it took.  The tokens are in self.tokens."""
+        self.begin()
         self.masked.fill_(1)
         rounds = 0
         while rounds < self.d.P and bool(self.masked.any()):
@@ -111,15 +129,83 @@ class BlockDecoder:
             ms.lm_head_commit(self.d, self.R, self.x, self.Wlm, threshold, self.tokens, self.masked, self.choice,
                               self.conf, self.accept, self.n_committed, self.ws, logit_scale=logit_scale)
             rounds += 1
-        self.forward()  # the committed tokens' keys and values stay
+        self.forward(resolved=True)  # the committed tokens' keys and values stay
         self.kv_len += self.d.P
         return rounds
+
+    def begin(self) -> None:
+        """(The pages of all blocks are dealt out in advance here.)"""
 
     def check(self) -> None:
         for ws in (self.ws, self.kv_ws):
             word = ms.read_device_error(ws)
             if word != ms.OK:
                 raise ms.MoeStepError(word, "device error word")
+
+
+class HybridDecoder(BlockDecoder):
+    """Pages as they are needed, rotary positions in half of every head, and in every second layer the gated delta rule."""
+
+    def __init__(self, d: ms.ModelDims, kd: ms.KvDims, R: int, n_layers: int, seed: int = 0, top_p: float = 0.9):
+        super().__init__(d, kd, R, n_layers, seed, top_p)
+        g = torch.Generator(device="cuda").manual_seed(seed + 2)
+        f32 = dict(dtype=torch.float32, device="cuda")
+        self.dd = dd = ms.DeltaDims(Hk=2, Hv=4, Dk=64, Dv=64, n_slots=R)
+        self.widths = (dd.Hk * dd.Dk, dd.Hk * dd.Dk, dd.Hv * dd.Dv, dd.Hv, dd.Hv)  # queries, keys, values, decays, rates
+        w = lambda *s: (0.02 * torch.randn(s, generator=g, device="cuda")).bfloat16()  # noqa: E731
+        self.delta = {i: dict(Win=w(sum(self.widths), d.H), Wout=w(d.H, dd.Hv * dd.Dv),
+                              rate=torch.exp(torch.randn(dd.Hv, generator=g, device="cuda") - 3),
+                              state=torch.zeros((R, dd.Hv, dd.Dv, dd.Dk), **f32)) for i in range(0, n_layers, 2)}
+        self.delta_ws = ms.delta_workspace(dd, R, d.P)
+        self.mixed = torch.empty((self.T, dd.Hv, dd.Dv), dtype=torch.bfloat16, device="cuda")
+        self.freq = ms.rotary_frequencies(kd.D // 2, 1e4)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        self.table.fill_(-1)
+        self.ring = torch.randperm(kd.n_pages, generator=g, device="cuda").to(torch.int32)  # every page is free
+        self.head = torch.tensor([0, kd.n_pages], **i32)
+        self.pos, self.seen = torch.empty((R, d.P), **i32), torch.zeros(R, **i32)
+
+    def plan(self, n_new) -> None:
+        ms.kv_cache_plan(self.kd, self.R, self.kv_len, n_new, self.ring, self.head, self.head, self.table, self.seen, self.pos,
+                         self.kv_ws)
+
+    def begin(self) -> None:
+        self.plan(torch.full_like(self.kv_len, self.d.P))
+
+    def end(self) -> None:
+        """Every request ends: its pages go back, its slots may be taken by others."""
+        self.plan(-self.kv_len)
+        self.kv_len.zero_()
+
+    def places(self):
+        return self.pos, self.seen
+
+    def rotate(self, q, k, pos) -> None:
+        ms.block_rotary(self.kd, q, k, pos, self.freq, q, k)
+
+    def mixer(self, i: int, L: Layer, pos, seen):
+        if i not in self.delta:
+            return super().mixer(i, L, pos, seen)
+        dd, M = self.dd, self.delta[i]
+        q, k, v, a, b = (self.x @ M["Win"].t()).split(self.widths, 1)
+        decay = -M["rate"] * torch.nn.functional.softplus(a.float())
+        ms.block_delta_rule(dd, self.R, q.unflatten(1, (dd.Hk, dd.Dk)), k.unflatten(1, (dd.Hk, dd.Dk)),
+                            v.unflatten(1, (dd.Hv, dd.Dv)), decay, torch.sigmoid(b.float()), M["state"], self.mixed,
+                            self.delta_ws, state_out=M["state"] if self.resolved else None, scale=dd.Dk ** -0.5, qk_eps=1e-6)
+        return self.mixed.view(self.T, -1) @ M["Wout"].t()
+
+    def check(self) -> None:
+        super().check()
+        word = ms.read_device_error(self.delta_ws)
+        if word != ms.OK:
+            raise ms.MoeStepError(word, "device error word")
+
+
+def hybrid(R: int, blocks: int, fp8: bool, P: int = 32, seed: int = 0, layers: int = 4) -> HybridDecoder:
+    d = ms.ModelDims(H=512, E=32, k=4, I=128, Is=128, V=4096, P=P)
+    pages = -(-(blocks * P) // 16)
+    kd = ms.KvDims(Hq=8, Hkv=2, D=64, page=16, n_pages=R * pages + 1, max_pages=pages, dtype=ms.FP8 if fp8 else ms.BF16)
+    return HybridDecoder(d, kd, R, layers, seed)
 
 
 def small(R: int, prefix: int, blocks: int, fp8: bool, P: int = 32, seed: int = 0, layers: int = 2) -> BlockDecoder:
@@ -144,8 +230,9 @@ def main() -> None:
     ap.add_argument("--requests", type=int, default=2)
     ap.add_argument("--prefix", type=int, default=100)
     ap.add_argument("--blocks", type=int, default=2)
+    ap.add_argument("--hybrid", action="store_true")
     a = ap.parse_args()
-    m = small(a.requests, a.prefix, a.blocks, a.fp8_cache)
+    m = hybrid(a.requests, a.blocks, a.fp8_cache) if a.hybrid else small(a.requests, a.prefix, a.blocks, a.fp8_cache)
     for b in range(a.blocks):
         rounds = m.decode_block(logit_scale=8.0)
         m.check()

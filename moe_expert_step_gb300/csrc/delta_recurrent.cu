@@ -243,7 +243,7 @@ int check_delta(const moestep_delta_dims* dd, int R, int n) {
     if (rc != MOESTEP_OK) return rc;
     if (R <= 0 || n <= 0) return MOESTEP_EINVAL;
     if (1ll * R * dd->Hv > (1 << 24)) return MOESTEP_EUNSUPPORTED;
-    if (1ll * R * n > (1ll << 31) - 1 || (1ll * R * n + 64ll * R) * dd->Hk > 64 * ((1ll << 31) - 1)) return MOESTEP_EUNSUPPORTED;
+    if (n > (1 << 30) || 1ll * R * n > (1ll << 31) - 1 || (1ll * R * n + 64ll * R) * dd->Hk > 64 * ((1ll << 31) - 1)) return MOESTEP_EUNSUPPORTED;
     return MOESTEP_OK;
 }
 

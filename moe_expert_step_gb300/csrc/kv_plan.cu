@@ -305,7 +305,7 @@ extern "C" int kv_cache_plan(const moestep_kv_dims* kd, int R, int n, const int3
     constexpr int kEntries = 4096;
     a.rows = n >= kEntries ? 1 : kEntries / n < kThreads ? kEntries / n : kThreads;
     if (a.rows > R) a.rows = R;
-    a.segments = a.rows > 1 ? 1 : (n + kEntries - 1) / kEntries;
+    a.segments = a.rows > 1 ? 1 : static_cast<int>((n + kEntries - 1ll) / kEntries);
     const long long grid = 1ll * ((R + a.rows - 1) / a.rows) * a.segments;
     if (grid > (1ll << 31) - 1) return MOESTEP_EUNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -232,6 +232,8 @@ extern "C" int block_rotary(const moestep_kv_dims* kd, int R, int n, const void*
     if (k && (rc = check_rotary_rows(k_out, ko_ld, wk, kd->dtype)) != MOESTEP_OK) return rc;
     if ((q && q == q_out && q_ld != qo_ld) || (k && k == k_out && k_ld != ko_ld)) return MOESTEP_EINVAL;
     if (reinterpret_cast<uintptr_t>(pos) & 3u || reinterpret_cast<uintptr_t>(freq) & 7u) return MOESTEP_EALIGN;
+    // (a thread an element and head at most)
+    if (1ll * R * n > ((1ll << 31) - 1) * 256 / (1ll * kd->D * (kd->Hq + kd->Hkv))) return MOESTEP_EUNSUPPORTED;
     int sms = 0;
     if ((rc = device_ok(&sms)) != MOESTEP_OK) return rc;
     RotaryArgs a{};
@@ -257,8 +259,6 @@ extern "C" int block_rotary(const moestep_kv_dims* kd, int R, int n, const void*
     for (const void* p : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)}) wide = wide && kv_aligned16(p);
     if (q) wide = wide && q_ld % v == 0 && qo_ld % v == 0;
     if (k) wide = wide && k_ld % v == 0 && ko_ld % v == 0;
-    const long long most = ((1ll << 31) - 1) * 256 / (1ll * kd->D * (kd->Hq + kd->Hkv));
-    if (a.tokens > most) return MOESTEP_EUNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_begin(8, s);
     cudaError_t e;

@@ -220,3 +220,63 @@ def test_pieces_of_a_sequence(dtype):
     assert at == n
     end, s["state"] = s["state"], start
     check(dd, 1, s, torch.cat(outs), end, scale=0.1)
+
+
+def test_wait_timeout_is_reported_and_recovered():
+    """Waits that run out end the walk with an error; the next call is right."""
+    dd = ms.DeltaDims(Hk=2, Hv=4, Dk=128, Dv=128, n_slots=3)
+    s = make(dd, 3, 200, 61)
+    ws, to = ms.delta_workspace(dd, 3, 200), torch.empty_like(s["state"])
+    good, word = call(dd, 3, s, ws=ws, state_out=to)
+    first = to.clone()
+    assert word == ms.OK
+    try:
+        ms.set_wait_timeout_ns(0)
+        _, word = call(dd, 3, s, ws=ws, state_out=to)
+        assert word == ms.ETIMEOUT
+    finally:
+        ms.set_wait_timeout_ns(2_000_000_000)
+    again, word = call(dd, 3, s, ws=ws, state_out=to)
+    assert word == ms.OK and torch.equal(good, again) and torch.equal(first, to)
+
+
+@pytest.mark.parametrize("R,Hk,Hv", [(1, 1, 2), (5, 2, 6), (40, 4, 4)])
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+def test_longer(R, Hk, Hv, Dk, Dv):
+    """Several chunks, ragged, few and many slices of the states a multiprocessor, groups of one to three value heads."""
+    dd = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=R)
+    n = 330 if R < 40 else 140
+    s = make(dd, R, n, 70 + R)
+    length = torch.tensor([n - (37 * r) % n for r in range(R)], dtype=torch.int32, device="cuda")
+    to = torch.full_like(s["state"], 3.0)
+    out, word = call(dd, R, s, state_out=to, length=length, scale=Dk ** -0.5)
+    assert word == ms.OK
+    if R == 40:  # the oracle on a few of them, the others against calls of their own
+        for r in (0, 17, 39):
+            part = {k: (v[r:r + 1] if k == "state" else v[r * n:(r + 1) * n]) for k, v in s.items()}
+            check(ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=1), 1, part, out[r * n:(r + 1) * n], to[r:r + 1],
+                  length=length[r:r + 1], scale=Dk ** -0.5)
+        for r in range(R):
+            one = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=1)
+            part = {k: (v[r:r + 1] if k == "state" else v[r * n:(r + 1) * n]) for k, v in s.items()}
+            alone = torch.empty_like(part["state"])
+            o, _ = call(one, 1, part, state_out=alone, length=length[r:r + 1], scale=Dk ** -0.5)
+            assert torch.equal(o, out[r * n:(r + 1) * n]) and torch.equal(alone[0], to[r])
+    else:
+        check(dd, R, s, out, to, length=length, scale=Dk ** -0.5)
+
+
+@pytest.mark.parametrize("n", [6, 100])
+def test_magnitudes(n):
+    """Values, states, queries and keys of very different sizes: powers of two of each change nothing but the result's."""
+    dd = ms.DeltaDims(Hk=1, Hv=2, Dk=64, Dv=64, n_slots=1)
+    s = make(dd, 1, n, 81)
+    to = torch.empty_like(s["state"])
+    out, _ = call(dd, 1, s, state_out=to, qk_eps=1e-30)
+    for v, k, q in ((2.0 ** 60, 1.0, 1.0), (2.0 ** -60, 1.0, 1.0), (1.0, 2.0 ** 30, 2.0 ** -30), (1.0, 2.0 ** -30, 2.0 ** 40)):
+        t = dict(s, v=s["v"] * v, state=s["state"] * v, k=s["k"] * k, q=s["q"] * q)
+        to2 = torch.empty_like(to)
+        out2, word = call(dd, 1, t, state_out=to2, qk_eps=1e-30)
+        assert word == ms.OK
+        assert (out2.double() / v - out.double()).abs().max() <= 2.0 ** -8 * out.double().abs().max()
+        assert ((to2.double() / v - to.double()).norm() / to.double().norm()) <= 2.0 ** -17
