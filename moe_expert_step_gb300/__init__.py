@@ -159,12 +159,19 @@ def _p(t):
     return t.data_ptr()
 
 
+_CURRENT = None  # torch's functions for the current device and the handle of its current stream, once CUDA is up
+
+
 def _s(stream):
     """cudaStream_t of a torch stream (None: the current one), or of an integer handle."""
+    global _CURRENT
     if stream is None:
+        if _CURRENT is not None:
+            return _CURRENT[1](_CURRENT[0]())
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone: no Stream object
         if raw is not None and torch.cuda.is_initialized():
+            _CURRENT = torch._C._cuda_getDevice, raw
             return raw(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -481,9 +488,11 @@ def kv_cache_plan(kd: KvDims, R: int, kv_len, n_new, ring, head, head_out, table
     if slots is not None:
         _dense(slots, (R, n), i32, "kv_cache_plan: slots")
     _on_gpu(ws, "kv_cache_plan")
-    _check(lib().kv_cache_plan(kd._c, R, n, kv_len.data_ptr(), n_new.data_ptr(), ring.data_ptr(), head.data_ptr(),
-                               head_out.data_ptr(), table.data_ptr(), new_len.data_ptr(), pos.data_ptr(), _p(slots),
-                               ws.data_ptr(), ws.numel(), _s(stream)), "kv_cache_plan")
+    rc = lib().kv_cache_plan(kd._c, R, n, kv_len.data_ptr(), n_new.data_ptr(), ring.data_ptr(), head.data_ptr(),
+                             head_out.data_ptr(), table.data_ptr(), new_len.data_ptr(), pos.data_ptr(), _p(slots),
+                             ws.data_ptr(), ws.numel(), _s(stream))
+    if rc:
+        _check(rc, "kv_cache_plan")
 
 
 def _on_gpu(ws, what: str) -> None:
@@ -517,13 +526,22 @@ def block_rotary(kd: KvDims, q, k, pos, freq, q_out, k_out, interleaved: bool = 
     R, n = shape = pos.shape
     _dense(pos, shape, types["int"], "block_rotary: pos")
     _dense(freq, freq.shape, types["turn"], "block_rotary: freq")
-    T, act = R * n, types.get(kd.dtype)
-    q_ld = 0 if q is None else _head_rows(q, T, kd.Hq, kd.D, act, "block_rotary: q")
-    k_ld = 0 if k is None else _head_rows(k, T, kd.Hkv, kd.D, act, "block_rotary: k")
-    qo_ld = 0 if q_out is None else _head_rows(q_out, T, kd.Hq, kd.D, act, "block_rotary: q_out")
-    ko_ld = 0 if k_out is None else _head_rows(k_out, T, kd.Hkv, kd.D, act, "block_rotary: k_out")
-    _check(lib().block_rotary(kd._c, R, n, _p(q), q_ld, _p(k), k_ld, pos.data_ptr(), freq.data_ptr(), 2 * freq.shape[0],
-                              int(interleaved), mscale, _p(q_out), qo_ld, _p(k_out), ko_ld, _s(stream)), "block_rotary")
+    act, q_ld, k_ld, qo_ld, ko_ld = types.get(kd.dtype), 0, 0, 0, 0
+    qp = kp = qo = ko = None
+    if q is not None:
+        heads = (R * n, kd.Hq, kd.D)
+        qp, q_ld = q.data_ptr(), _head_rows(q, heads, act, "block_rotary: q")
+        if q_out is not None:
+            qo, qo_ld = q_out.data_ptr(), _head_rows(q_out, heads, act, "block_rotary: q_out")
+    if k is not None:
+        heads = (R * n, kd.Hkv, kd.D)
+        kp, k_ld = k.data_ptr(), _head_rows(k, heads, act, "block_rotary: k")
+        if k_out is not None:
+            ko, ko_ld = k_out.data_ptr(), _head_rows(k_out, heads, act, "block_rotary: k_out")
+    rc = lib().block_rotary(kd._c, R, n, qp, q_ld, kp, k_ld, pos.data_ptr(), freq.data_ptr(), 2 * freq.shape[0],
+                            interleaved, mscale, qo, qo_ld, ko, ko_ld, _s(stream))
+    if rc:
+        _check(rc, "block_rotary")
 
 
 @dataclass(frozen=True)
@@ -558,14 +576,14 @@ def delta_workspace(dd: DeltaDims, R: int, n: int, device="cuda", stream=None):
     return ws
 
 
-def _head_rows(t, T: int, heads: int, D: int, dtype, what: str) -> int:
-    """Distance between the rows of t [T, heads, D], which may be part of a wider row."""
-    if t.shape != (T, heads, D) or t.dtype is not dtype or not t.is_cuda:
-        raise MoeStepError(EINVAL, f"{what} must be [{T}, {heads}, {D}] in the activations' type, on the GPU")
+def _head_rows(t, shape, dtype, what: str) -> int:
+    """Distance between the rows of t [tokens, heads, D], which may be part of a wider row."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        raise MoeStepError(EINVAL, f"{what} must be {list(shape)} in the activations' type, on the GPU")
     ld, head, one = t.stride()
-    if one != 1 or (head != D and heads > 1):
+    if one != 1 or (head != shape[2] and shape[1] > 1):
         raise MoeStepError(EINVAL, f"{what}: heads and their elements must be dense")
-    return ld if T > 1 else heads * D
+    return ld if shape[0] > 1 else shape[1] * shape[2]
 
 
 def block_delta_rule(dd: DeltaDims, R: int, q, k, v, g, beta, state, out, ws, state_out=None, slot=None, length=None,
@@ -579,15 +597,16 @@ def block_delta_rule(dd: DeltaDims, R: int, q, k, v, g, beta, state, out, ws, st
     if R * n != T:
         raise MoeStepError(EINVAL, "block_delta_rule: q must have R * n rows")
     act = types.get(dd.dtype) if dd.dtype != FP8 else None
-    q_ld = _head_rows(q, T, dd.Hk, dd.Dk, act, "block_delta_rule: q")
-    k_ld = _head_rows(k, T, dd.Hk, dd.Dk, act, "block_delta_rule: k")
-    v_ld = _head_rows(v, T, dd.Hv, dd.Dv, act, "block_delta_rule: v")
+    keys, values, gates = (T, dd.Hk, dd.Dk), (T, dd.Hv, dd.Dv), (T, dd.Hv)
+    q_ld = _head_rows(q, keys, act, "block_delta_rule: q")
+    k_ld = _head_rows(k, keys, act, "block_delta_rule: k")
+    v_ld = _head_rows(v, values, act, "block_delta_rule: v")
     f32, pool = types[F32], (dd.n_slots, dd.Hv, dd.Dv, dd.Dk)
-    _dense(g, (T, dd.Hv), f32, "block_delta_rule: g")
-    _dense(beta, (T, dd.Hv), f32, "block_delta_rule: beta")
+    _dense(g, gates, f32, "block_delta_rule: g")
+    _dense(beta, gates, f32, "block_delta_rule: beta")
     _dense(state, pool, f32, "block_delta_rule: state")
-    _dense(out, (T, dd.Hv, dd.Dv), act, "block_delta_rule: out")
-    if state_out is not None:
+    _dense(out, values, act, "block_delta_rule: out")
+    if state_out is not None and state_out is not state:
         _dense(state_out, pool, f32, "block_delta_rule: state_out")
     if slot is not None:
         _dense(slot, (R,), types["int"], "block_delta_rule: slot")
@@ -596,10 +615,11 @@ def block_delta_rule(dd: DeltaDims, R: int, q, k, v, g, beta, state, out, ws, st
     if fresh is not None:
         _dense(fresh, (R,), types["byte"], "block_delta_rule: fresh")
     _on_gpu(ws, "block_delta_rule")
-    _check(lib().block_delta_rule(dd._c, R, n, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
-                                  g.data_ptr(), beta.data_ptr(), _p(length), _p(slot), _p(fresh), state.data_ptr(),
-                                  _p(state_out), scale, qk_eps, out.data_ptr(), ws.data_ptr(), ws.numel(),
-                                  _s(stream)), "block_delta_rule")
+    rc = lib().block_delta_rule(dd._c, R, n, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, g.data_ptr(),
+                                beta.data_ptr(), _p(length), _p(slot), _p(fresh), state.data_ptr(), _p(state_out), scale,
+                                qk_eps, out.data_ptr(), ws.data_ptr(), ws.numel(), _s(stream))
+    if rc:
+        _check(rc, "block_delta_rule")
 
 
 def read_device_error(ws, stream=None) -> int:
