@@ -1122,8 +1122,11 @@ cudaError_t launch_chunks(const DeltaArgs& a, const Scratch& w, int sms, cudaStr
     cudaError_t e = launch_prep<DK>(a, w, s);
     if (e != cudaSuccess) return e;
     count_launch();
-    // As few slices a block as keep the multiprocessors busy: a block's tiles are shared by its slices.
+    // As few slices a block as leave no multiprocessor a second block (blocks of more share their tiles, but also the chain
+    // of a chunk gets longer).  us for 1000 tokens with 1 / 2 / 4 slices a block: 128 slices 41 / 48 / 65, 256 slices
+    // 73 / 52 / 68, 384 slices of 500 tokens 59 / 51 / 40.
     const long long slices = 1ll * a.R * a.Hv * (a.Dv / 16);
+    if (slices <= sms) return launch_walk<DK, 1, 3, 1>(a, w, s);
     if (slices <= 2ll * sms) return launch_walk<DK, 2, 3, 1>(a, w, s);
     return launch_walk<DK, 4, 2, 1>(a, w, s);
 }
