@@ -362,7 +362,8 @@ int block_residual_norm(const moestep_dims* dims, int T, const void* y, int y_dt
  *   ring [n_pages] int32 (in/out); head [2] int32; head_out [2] (may be head)
  *   table [R][max_pages] int32 (in/out): entries of new pages are written; those of pages given
  *   up keep their old values
- *   new_len [R] (not kv_len or n_new): kv_len + n_new, or kv_len of a request that was refused
+ *   new_len [R] (not kv_len or n_new): kv_len + n_new, or kv_len of a request that was refused; the
+ *   next call's kv_len (planned again without it, the same positions would take new pages)
  *   pos [R][n]: positions kv_len[r] .. of the new tokens, -1 behind them, as kv_cache_write takes them
  *   slots [R][n] (may be NULL): page * dims.page + place in the page of each, -1 behind them
  * Lengths, counts or pages out of range are recorded (MOESTEP_EDEVINPUT) and not followed: such a request
@@ -418,7 +419,7 @@ int moestep_delta_workspace_size(const moestep_delta_dims* dd, int R, int n, siz
 /* For each request, its tokens in order, and each value head:
  *   S <- e^g S + beta k (v - e^g S^T k)^T,   out = scale * S^T q
  *   q, k [R*n][Hk][Dk], v [R*n][Hv][Dv], rows *_ld elements apart (16-byte aligned)
- *   qk_eps > 0: q and k are divided by sqrt(|.|^2 + qk_eps) first; 0: taken as they are
+ *   qk_eps > 0: q and k are divided by sqrt(|.|^2 + qk_eps) first (|.| below 2^63); 0: taken as they are
  *   g, beta [R*n][Hv] fp32; g <= 0 is the logarithm of the decay (-inf: the history is dropped)
  *   length [R] int32 in [0, n]: tokens of each request (NULL: n); rows of out behind them are left as they were
  *   slot [R] int32: the request's state (NULL: slot r); negative: the request is skipped.  Slots of a call that
@@ -429,7 +430,8 @@ int moestep_delta_workspace_size(const moestep_delta_dims* dd, int R, int n, siz
  *   out [R*n][Hv][Dv]
  * Lengths and slots out of range are recorded (MOESTEP_EDEVINPUT) and the request is skipped.  Sums and states
  * are fp32; results do not depend on timing.  A non-finite value may reach every output of its head's request
- * from 63 tokens before its own on. */
+ * from 63 tokens before its own on.  Where beta |k|^2 passes 2 the recurrence has no bound of its own; with MOESTEP_BF16 and
+ * n >= 32 what it grows by within 64 tokens has to stay below 2^15. */
 int block_delta_rule(const moestep_delta_dims* dd, int R, int n, const void* q, long long q_ld, const void* k,
                      long long k_ld, const void* v, long long v_ld, const float* g, const float* beta,
                      const int32_t* length, const int32_t* slot, const uint8_t* fresh, const float* state,

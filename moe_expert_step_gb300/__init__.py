@@ -521,8 +521,8 @@ def block_rotary(kd: KvDims, q, k, pos, freq, q_out, k_out, interleaved: bool = 
     which may be q and k themselves.  freq: of rotary_frequencies; pairs are halves of the rotated part apart, or
     neighbours where interleaved; see block_rotary in moestep.h."""
     types = _types()
-    if pos.dim() != 2 or freq.dim() != 1:
-        raise MoeStepError(EINVAL, "block_rotary: pos must be [R, n], freq [rot / 2]")
+    if pos.dim() != 2 or freq.dim() != 1 or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise MoeStepError(EINVAL, "block_rotary: pos must be [R, n], freq [rot / 2]; q and k come with their outputs")
     R, n = shape = pos.shape
     _dense(pos, shape, types["int"], "block_rotary: pos")
     _dense(freq, freq.shape, types["turn"], "block_rotary: freq")
@@ -531,13 +531,11 @@ def block_rotary(kd: KvDims, q, k, pos, freq, q_out, k_out, interleaved: bool = 
     if q is not None:
         heads = (R * n, kd.Hq, kd.D)
         qp, q_ld = q.data_ptr(), _head_rows(q, heads, act, "block_rotary: q")
-        if q_out is not None:
-            qo, qo_ld = q_out.data_ptr(), _head_rows(q_out, heads, act, "block_rotary: q_out")
+        qo, qo_ld = q_out.data_ptr(), _head_rows(q_out, heads, act, "block_rotary: q_out")
     if k is not None:
         heads = (R * n, kd.Hkv, kd.D)
         kp, k_ld = k.data_ptr(), _head_rows(k, heads, act, "block_rotary: k")
-        if k_out is not None:
-            ko, ko_ld = k_out.data_ptr(), _head_rows(k_out, heads, act, "block_rotary: k_out")
+        ko, ko_ld = k_out.data_ptr(), _head_rows(k_out, heads, act, "block_rotary: k_out")
     rc = lib().block_rotary(kd._c, R, n, qp, q_ld, kp, k_ld, pos.data_ptr(), freq.data_ptr(), 2 * freq.shape[0],
                             interleaved, mscale, qo, qo_ld, ko, ko_ld, _s(stream))
     if rc:

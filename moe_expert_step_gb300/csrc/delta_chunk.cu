@@ -11,11 +11,16 @@
 //   S = e^G_C S0 + sum_j e^(G_C - G_j) U_j k_j^T
 //
 // Two launches.  The first, parallel over (chunk, key head), has no states in it: it makes X and P.  The second walks
-// the chunks of each (request, head) in order.  Its unit is a warp with 16 rows of the transposed state (16 of the
-// Dv columns): rows need nothing from one another, so warps never meet.  All its products have those 16 rows
-// as the MMA's M, so that each accumulator is the next product's A operand as it stands in the registers:
-// S0 -> S0 K^T -> R -> R X^T = U -> U P^T and U K, without shared memory or lane exchanges in between; the B
-// operands (K, Q, X, P) are shared-memory tiles that the first launch has laid out swizzled, brought by bulk copies.
+// the chunks of each (request, head) in order.  Its unit is a slice of 16 rows of the transposed state (16 of the Dv
+// columns): rows need nothing from one another.  All its products have those 16 rows as the MMA's M, so that an
+// accumulator is the next product's A operand as it stands in the registers, S0 -> S0 K^T -> R -> R X^T = U -> U P^T and
+// U K; the B operands (K, Q, X, P) are tiles that the first launch has laid out for ldmatrix, brought by bulk copies.
+// (mma.sync, not tcgen05: a slice's chain of products with 64 columns would be bound by the issue of its MMAs, 67 cycles or
+// more each, and pass through tensor memory at every link.  For one prompt's 256 slices on 152 multiprocessors
+// the chain is what counts; with hundreds of heads tcgen05 would have the higher rate.)
+//
+// 8192 tokens of 16 and 32 heads of 128: 55 and 291 us (349 together; 206 MB that have to be moved, 30 us); 8 requests of up
+// to 4096 tokens: 135 and 433 us (517 MB, 76 us).
 //
 // Accuracy.  States and sums are fp32.  An fp32 operand enters as the sum of two f16 numbers after a power of two that
 // brings its row's largest element to 2^12: 22 bits, and 2^-37 of the row's largest for small elements.  Queries and
@@ -34,7 +39,7 @@
 namespace moestep {
 namespace {
 
-constexpr int C = 64;             // tokens of a chunk
+constexpr int C = 64;  // tokens of a chunk
 // X and P are lower triangular: of their 16 x 16 blocks (f16, 512 bytes) the ten on and below the diagonal are kept, row by row
 constexpr int kTri = 10 * 512;
 // What a chunk of one value head has: X high, X low and factors for the states, P and factors for the outputs
@@ -44,7 +49,7 @@ constexpr int kXBytes = 2 * kTri + 4 * C * 4, kPBytes = kTri + 2 * C * 4, kHeadB
 
 template <int DK>
 struct Tile {
-    static constexpr int kBytes = C * DK * 2;  // K or Q of a chunk: DK / 64 tiles of [64 tokens][64]
+    static constexpr int kBytes = C * DK * 2;  // K or Q of a chunk
 };
 
 struct Scratch {
@@ -140,13 +145,14 @@ __device__ __forceinline__ float quad_max(float x) {
 __device__ __forceinline__ int in_block(int r, int c) { return r * 32 + ((c ^ (r >> 2 & 1)) << 4); }  // 16-byte half c of row r
 __device__ __forceinline__ constexpr int tri(int bi, int bj) { return (bi * (bi + 1) / 2 + bj) * 512; }  // of a lower triangle
 __device__ __forceinline__ constexpr int below(int bi, int bj) { return tri(bi - 1, bj); }  // of one without its diagonal
-// lanes' places for ldmatrix.x4: with the 8 x 8 matrices in the order of the rows (B operands; outputs transposed), and
+// lanes' places for ldmatrix.x4: with the 8 x 8 matrices in the order of the rows (B operands; A operands transposed), and
 // in the order of the columns (A operands; B operands transposed)
 __device__ __forceinline__ int by_rows(int lane) { return in_block((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1); }
 __device__ __forceinline__ int by_cols(int lane) { return in_block((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4); }
 
 // ---------------------------------------------------------------- first launch: X and P of every chunk
-// A block has one chunk of one key head, four warps with 16 tokens each for the products k.k and q.k.
+// A block has one chunk of one key head, four warps with 16 tokens each for the products k.k and q.k.  Bound by latency: 38 %
+// of the issue slots and 2.5 to 3.2 TB/s with four blocks a multiprocessor.
 //
 // Rows of keys are brought to [1, 2) by a power of two and their norms left out: with c_i the factor between key and row,
 // the system is solved for U' = c U, whose matrix A'_ij = beta_i c_i^2 e^(G_i - G_j) k_i.k_j has entries of the size of 1
@@ -155,8 +161,8 @@ __device__ __forceinline__ int by_cols(int lane) { return in_block((lane >> 3 & 
 // X = (I + A')^-1 of a value head by a pair of warps: the 16 x 16 blocks on the diagonal by elimination in fp32, a column
 // a thread; then blocks of 32 and of 64 from X_BA = -X_B A_BA X_A, on tensor cores with operands of two f16
 // numbers.  Computed transposed, (X_A^T A_BA^T) X_B^T, the first product is the second one's A operand in place.
-// (64 steps of elimination in registers, unrolled, ran at the speed of their instruction fetches and took 208 us for
-// 8192 tokens of 32 heads; in loops of 16 rows 150 us.)
+// (64 steps of elimination in registers, unrolled, ran at the speed of their instruction fetches: 208 us for 8192 tokens
+// of 32 heads; in loops of 16 rows 150 us; by blocks 91 us, now 55 us.)
 template <int DK>
 struct PrepSmem {
     union {
@@ -223,7 +229,7 @@ __device__ __forceinline__ void mma3(float (&d0)[4], float (&d1)[4], const uint3
 // X_B from bn on, NB each; m is one of X_A's block columns.
 template <int NB>
 __device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t ah, uint32_t al, int ma, int m, int bn) {
-    const int lane = threadIdx.x % 32, rows = by_rows(lane), cols = in_block((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1);
+    const int lane = threadIdx.x % 32, rows = by_rows(lane);
     float d[2 * NB][4];
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t)
@@ -235,8 +241,8 @@ __device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t 
         const int k = ma + kb;
         if (k < m) continue;
         uint32_t a[4], l[4];
-        ldsm4_t(a, xh + tri(k, m) + cols);
-        ldsm4_t(l, xl + tri(k, m) + cols);
+        ldsm4_t(a, xh + tri(k, m) + rows);
+        ldsm4_t(l, xl + tri(k, m) + rows);
 #pragma unroll
         for (int t = 0; t < NB; ++t) {
             uint32_t b[4], bl[4];
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
 
     // keys and queries: f16 after a power of two a row, four lanes a row
     constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
-    constexpr int PIECES = DK / 32;  // 16-byte pieces of a lane: 64 bytes of a row together
+    constexpr int PIECES = DK / 32;    // 16-byte pieces of a lane: 64 bytes of a row together
     const int sub = lane % 4;
     uint4 in[2][2][PIECES];
 #pragma unroll
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
             for (int i = 0; i < 2; ++i) {
                 const float g = gs[i] < -200.f ? -200.f : gs[i];  // (e^-200 is 0 as well)
                 s[i] = sum_of(g, 1.4426950408889634f);
-                s[i].lo = fmaf(g, 1.925963033500811e-8f, s[i].lo);  // log2(e) = 1.44269502162933 + 1.9259630335e-8
+                s[i].lo = fmaf(g, 1.925963033500811e-8f, s[i].lo);  // log2(e) = 1.4426950216293335 + 1.92596299e-8
             }
             const Sum mine = s[0] + s[1];
             Sum run = mine;
@@ -533,14 +539,17 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
 // the rows and takes tokens [32 p, 32 p + 32) of R and U; the operands that the other one needs (its half of the
 // state, R of the first tokens, U') pass through shared memory as f16 pairs in the A operand's layout, each
 // half with row scales of its own, so that nothing has to be agreed on before.  The outputs are no part of the chain of
-// states: a third warp makes them from the same operands, up to a chunk later, and also fetches the tiles.
+// states: a third warp makes them from the same operands, up to a chunk later.
 //
-// Bound: a warp's dependent chain of instructions (170 of them MMAs at 8 cycles), while there are fewer than two or three
-// warps a scheduler; with more, the rate of mma.sync (1024 multiplications a cycle and multiprocessor; 400 MMAs a
-// slice and chunk).
+// Bound: with one slice a multiprocessor the chain, 3500 cycles a chunk (170 MMAs at 8 cycles a warp, the rest is the latency
+// of scales, splits and exchanges between them); with two 4400 (the third warps share the schedulers); with four 6400,
+// shared memory at 72 % (ldmatrix half of it) and the tensor pipe at 50 %.
+// Slower: one warp a slice (448 us for the 8192 tokens); four warps a slice, a quarter of columns and tokens each (333); the
+// products of neighbouring chunks' keys from the first launch, which take the states off the chain but cost a quarter
+// more MMAs (273, and 13 us more in the first launch; 648 for the batch).
 template <int DK, int W, int NS>
 struct WalkSmem {
-    static constexpr int QS = NS == 1 ? 1 : 2;
+    static constexpr int QS = 2;
     struct ForStates {
         char k[Tile<DK>::kBytes];
         char x[kXBytes];
@@ -571,13 +580,13 @@ struct WalkSmem {
 template <int W>
 constexpr int kWalkWarps = 3 * W + (W == 2);
 
-template <int DK, int W, int NS, int CTAS>
-__global__ void __launch_bounds__(32 * kWalkWarps<W>, CTAS) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
+template <int DK, int W, int NS>
+__global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
     extern __shared__ __align__(128) char raw[];
     using Smem = WalkSmem<DK, W, NS>;
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     constexpr int QS = Smem::QS;
-    constexpr int NK = DK / 32;  // k steps of 16 of a half of the state's columns
+    constexpr int NK = DK / 32;        // k steps of 16 of a half of the state's columns
     constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g4 = lane / 4, q4 = lane % 4;
     const bool outputs = warp >= 2 * W;
@@ -778,7 +787,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, CTAS) delta_walk_kernel(co
         ++issued;
     };
     if (tid == 0)
-        while (issued < (NS == 1 ? 1 : NS - 1) && issued < n_chunks) fetch();  // (one stage: one chunk)
+        while (issued < NS - 1 && issued < n_chunks) fetch();
 
     const uint32_t vs = tc::smem_addr(sm.v[warp]);
     auto fetch_v = [&](int c) {  // the warp's values, zeros behind the request's tokens
@@ -1106,15 +1115,15 @@ cudaError_t launch_prep(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
     return launch_pdl(delta_prep_kernel<DK>, grid, dim3(128), sizeof(PrepSmem<DK>), s, a, w);
 }
 
-template <int DK, int W, int NS, int CTAS>
+template <int DK, int W, int NS>
 cudaError_t launch_walk(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
     constexpr size_t bytes = sizeof(WalkSmem<DK, W, NS>);
-    static_assert(CTAS * (bytes + 1024) <= 228 * 1024);
+    static_assert(bytes <= 227 * 1024);
     static int done[64];
-    cudaError_t e = ensure_smem(delta_walk_kernel<DK, W, NS, CTAS>, bytes, done);
+    cudaError_t e = ensure_smem(delta_walk_kernel<DK, W, NS>, bytes, done);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.R * a.Hv * (a.Dv / (16 * W))));
-    return launch_pdl(delta_walk_kernel<DK, W, NS, CTAS>, grid, dim3(32 * kWalkWarps<W>), bytes, s, a, w);
+    return launch_pdl(delta_walk_kernel<DK, W, NS>, grid, dim3(32 * kWalkWarps<W>), bytes, s, a, w);
 }
 
 template <int DK>
@@ -1126,9 +1135,9 @@ cudaError_t launch_chunks(const DeltaArgs& a, const Scratch& w, int sms, cudaStr
     // of a chunk gets longer).  us for 1000 tokens with 1 / 2 / 4 slices a block: 128 slices 41 / 48 / 65, 256 slices
     // 73 / 52 / 68, 384 slices of 500 tokens 59 / 51 / 40.
     const long long slices = 1ll * a.R * a.Hv * (a.Dv / 16);
-    if (slices <= sms) return launch_walk<DK, 1, 3, 1>(a, w, s);
-    if (slices <= 2ll * sms) return launch_walk<DK, 2, 3, 1>(a, w, s);
-    return launch_walk<DK, 4, 2, 1>(a, w, s);
+    if (slices <= sms) return launch_walk<DK, 1, 3>(a, w, s);
+    if (slices <= 2ll * sms) return launch_walk<DK, 2, 3>(a, w, s);
+    return launch_walk<DK, 4, 2>(a, w, s);
 }
 
 size_t qk_bytes(const moestep_delta_dims& d, long long units) { return static_cast<size_t>(units) * d.Hk * 2 * C * d.Dk * 2; }

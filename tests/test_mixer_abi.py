@@ -156,7 +156,7 @@ def test_rotary_binding_on_the_gpu():
         for a in ((bad, k, pos, freq, q, k), (q, k, pos, freq, bad, k)):
             with pytest.raises(ms.MoeStepError, match="q"):
                 ms.block_rotary(kd, *a)
-    for a in ((q, None, pos, freq, None, None), (q, k, pos, freq, q, None), (q, k, pos, ms.rotary_frequencies(130, 1e4), q, k),
+    for a in ((q, None, pos, freq, None, None), (q, k, pos, freq, q, None), (q, None, pos, freq, q, k), (None, k, pos, freq, q, k), (q, k, pos, ms.rotary_frequencies(130, 1e4), q, k),
               (q, k, pos, freq.float(), q, k)):
         with pytest.raises(ms.MoeStepError):
             ms.block_rotary(kd, *a)
