@@ -9,6 +9,11 @@
 // loads a thread from L2 for the batches of serving) instead of waiting for a launch that does.
 // The header is written by one block: the last that has read it where it is updated in place (a ticket tells),
 // else any.
+//
+// Bound by latency: header, lengths, sums, ring or table, slots are reads that depend on one another.  One request of 32
+// new tokens takes 7 us on the device and the call of it 8; 256 requests of up to 4096 tokens (8.7 MB of positions and
+// slots, 1.3 us at the copy rate) 8 us.  Divisions by the page size (a shift instead) and a header written by the last
+// block only (by any, where it is not updated in place) cost the larger one 3.4 us.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv.h"
