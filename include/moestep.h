@@ -429,7 +429,8 @@ int moestep_delta_workspace_size(const moestep_delta_dims* dd, int R, int n, siz
  *   same slots; may be state itself, NULL: not wanted (a block that is not resolved yet leaves its history)
  *   out [R*n][Hv][Dv]
  * Lengths and slots out of range are recorded (MOESTEP_EDEVINPUT) and the request is skipped.  Sums and states
- * are fp32; results do not depend on timing.  A non-finite value may reach every output of its head's request
+ * are fp32; results do not depend on timing (but the last bits of a request's may differ between calls of few and of
+ * many heads, which are walked in other ways).  A non-finite value may reach every output of its head's request
  * from 63 tokens before its own on.  Where beta |k|^2 passes 2 the recurrence has no bound of its own; with MOESTEP_BF16 and
  * n >= 32 what it grows by within 64 tokens has to stay below 2^15. */
 int block_delta_rule(const moestep_delta_dims* dd, int R, int n, const void* q, long long q_ld, const void* k,

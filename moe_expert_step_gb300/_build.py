@@ -10,7 +10,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmoestep.so")
 SOURCES = ["api.cu", "route.cu", "misc.cu", "expert_gemm.cu", "noalloc.cu", "kv_cache.cu",
-           "residual_norm.cu", "attention.cu", "attention_tc.cu", "kv_plan.cu", "rotary.cu", "delta_recurrent.cu", "delta_chunk.cu"]
+           "residual_norm.cu", "attention.cu", "attention_tc.cu", "kv_plan.cu", "rotary.cu", "delta_recurrent.cu", "delta_chunk.cu",
+           "delta_heads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -15,12 +15,11 @@
 // columns): rows need nothing from one another.  All its products have those 16 rows as the MMA's M, so that an
 // accumulator is the next product's A operand as it stands in the registers, S0 -> S0 K^T -> R -> R X^T = U -> U P^T and
 // U K; the B operands (K, Q, X, P) are tiles that the first launch has laid out for ldmatrix, brought by bulk copies.
-// (mma.sync, not tcgen05: a slice's chain of products with 64 columns would be bound by the issue of its MMAs, 67 cycles or
-// more each, and pass through tensor memory at every link.  For one prompt's 256 slices on 152 multiprocessors
-// the chain is what counts; with hundreds of heads tcgen05 would have the higher rate.)
+// (On mma.sync: with few heads the chain counts, and every link of it would pass through tensor memory on tcgen05.  Many heads
+// of 128 values are walked there, in delta_heads.cu.)
 //
-// 8192 tokens of 16 and 32 heads of 128: 55 and 291 us (349 together; 206 MB that have to be moved, 30 us); 8 requests of up
-// to 4096 tokens: 135 and 433 us (517 MB, 76 us).
+// 8192 tokens of 16 and 32 heads of 128: 60 and 290 us (350 together; 206 MB that have to be moved, 30 us); 8 requests of up
+// to 4096 tokens: 140 and 294 us (517 MB, 76 us).
 //
 // Accuracy.  States and sums are fp32.  An fp32 operand enters as the sum of two f16 numbers after a power of two that
 // brings its row's largest element to 2^12: 22 bits, and 2^-37 of the row's largest for small elements.  Queries and
@@ -29,7 +28,7 @@
 // for S0, U and P (2^-12, against the 2^-9 to which outputs are rounded).  Exponents of decays are differences of sums
 // held in two floats, so strong decays before a token do not blur the weak ones after it.
 #include "common.cuh"
-#include "delta.h"
+#include "delta_chunk.cuh"
 #include "kernels.h"
 #include "launch.cuh"
 #include "tc.cuh"
@@ -37,26 +36,8 @@
 #include <type_traits>
 
 namespace moestep {
+using namespace delta;
 namespace {
-
-constexpr int C = 64;  // tokens of a chunk
-// X and P are lower triangular: of their 16 x 16 blocks (f16, 512 bytes) the ten on and below the diagonal are kept, row by row
-constexpr int kTri = 10 * 512;
-// What a chunk of one value head has: X high, X low and factors for the states, P and factors for the outputs
-enum { kA, kBeta, kD, kGamma };  // [4][64] floats
-enum { kB, kPi };                // [2][64] floats
-constexpr int kXBytes = 2 * kTri + 4 * C * 4, kPBytes = kTri + 2 * C * 4, kHeadBytes = kXBytes + kPBytes;
-
-template <int DK>
-struct Tile {
-    static constexpr int kBytes = C * DK * 2;  // K or Q of a chunk
-};
-
-struct Scratch {
-    char* qk;     // [R][chunks][Hk][K tile, Q tile]
-    char* heads;  // [R][chunks][Hv][kHeadBytes]
-    int chunks;
-};
 
 // ---------------------------------------------------------------- PTX
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -98,37 +79,7 @@ __device__ __forceinline__ void mma_(float (&d)[4], const uint32_t (&a)[4], uint
         mma(d, a, b0, b1);
 }
 __device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(tc::smem_addr(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
 
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-// two values as the sum of two f16 pairs
-__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
-    hi = pack(x, y);
-    float lx, ly;  // x - hi
-    asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tfma.rn.f32.f16 %0, p, %5, %3;\n\tfma.rn.f32.f16 %1, q, %5, %4;\n\t}"
-        : "=f"(lx), "=f"(ly)
-        : "r"(hi), "f"(x), "f"(y), "h"(static_cast<unsigned short>(0xbc00)));  // -1
-    lo = pack(lx, ly);
-}
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // |e| <= 126
-// a power of two that brings `most` to [2^to, 2^(to+1)); 1 for zeros and what is not finite
-__device__ __forceinline__ float scale_to(float most, int to) {
-    const int e = static_cast<int>(__float_as_uint(most) >> 23);
-    if (most == 0.f || e == 255) return 1.f;
-    return pow2(min(max(to + 127 - e, -126), 126));
-}
-// 1 / x of a power of two, |exponent| <= 126
-__device__ __forceinline__ float inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
 // x^-1/2, rsqrtf and a step of Newton's iteration (the compiler's 1 / sqrtf takes two subroutines)
 __device__ __forceinline__ float inverse_root(float x) {
     const float y = rsqrtf(x);
@@ -139,16 +90,15 @@ __device__ __forceinline__ float quad_max(float x) {
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
-// Every tile is made of 16 x 16 blocks of 512 bytes, rows of 32 bytes whose two halves change places in every second group
-// of four rows, so that the eight rows of a matrix fall into different banks.  An ldmatrix address is then the lane's
-// place in a block, found once, plus a constant.
-__device__ __forceinline__ int in_block(int r, int c) { return r * 32 + ((c ^ (r >> 2 & 1)) << 4); }  // 16-byte half c of row r
-__device__ __forceinline__ constexpr int tri(int bi, int bj) { return (bi * (bi + 1) / 2 + bj) * 512; }  // of a lower triangle
-__device__ __forceinline__ constexpr int below(int bi, int bj) { return tri(bi - 1, bj); }  // of one without its diagonal
+__device__ __forceinline__ constexpr int below(int bi, int bj) { return (bi * (bi - 1) / 2 + bj) * 512; }  // of one without its diagonal
+// Values and outputs of a slice: 16 rows of 32 bytes, whose halves change places in every second group of four rows
+__device__ __forceinline__ int in_slice(int r, int c) { return r * 32 + ((c ^ (r >> 2 & 1)) << 4); }
 // lanes' places for ldmatrix.x4: with the 8 x 8 matrices in the order of the rows (B operands; A operands transposed), and
 // in the order of the columns (A operands; B operands transposed)
 __device__ __forceinline__ int by_rows(int lane) { return in_block((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1); }
-__device__ __forceinline__ int by_cols(int lane) { return in_block((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4); }
+__device__ __forceinline__ int slice_by_rows(int lane) { return in_slice((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1); }
+__device__ __forceinline__ int tile_by_rows(int lane) { return in_tile((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1); }
+__device__ __forceinline__ int tile_by_cols(int lane) { return in_tile((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4); }
 
 // ---------------------------------------------------------------- first launch: X and P of every chunk
 // A block has one chunk of one key head, four warps with 16 tokens each for the products k.k and q.k.  Bound by latency: 38 %
@@ -183,14 +133,6 @@ struct PrepSmem {
 struct Gates {  // in x
     float ghi[C], glo[C], beta[C];
 };
-
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(tc::smem_addr(src)), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // A number as the sum of two floats, of which the high one is the nearest float: about 2^-46 of the larger term is lost a sum
 struct Sum {
@@ -304,13 +246,12 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
     const int group = a.Hv / a.Hk;
 
     // keys and queries: f16 after a power of two a row, four lanes a row
-    constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
-    constexpr int PIECES = DK / 32;    // 16-byte pieces of a lane: 64 bytes of a row together
-    const int sub = lane % 4;
+    constexpr int PIECES = DK / 32;  // 16-byte pieces of a lane: 64 bytes of a row together
+    const int sub = (lane & 1) + (lane >> 4) * 2, row = lane >> 1 & 7;  // (a load's and a store's eight lanes: whole sectors, few conflicts)
     uint4 in[2][2][PIECES];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int t = warp * 16 + i * 8 + lane / 4;
+        const int t = warp * 16 + i * 8 + row;
         const bf16* kp = static_cast<const bf16*>(a.k) + (tok0 + t) * a.k_ld + hk * DK + 8 * sub;
         const bf16* qp = static_cast<const bf16*>(a.q) + (tok0 + t) * a.q_ld + hk * DK + 8 * sub;
 #pragma unroll
@@ -340,7 +281,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            const int t = warp * 16 + i * 8 + lane / 4;
+            const int t = warp * 16 + i * 8 + row;
             float f[8 * PIECES], most = 0.f;
 #pragma unroll
             for (int j = 0; j < PIECES; ++j) {
@@ -353,7 +294,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
                     most = fmaxf(most, fmaxf(fabsf(f[8 * j + 2 * e]), fabsf(f[8 * j + 2 * e + 1])));
                 }
             }
-            const float up = scale_to(quad_max(most), 0);
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            const float up = scale_to(fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16)), 0);
             float ss = 0.f;
 #pragma unroll
             for (int j = 0; j < 8 * PIECES; ++j) {
@@ -361,12 +303,12 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
                 ss += f[j] * f[j];
             }
             ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 16);
             if (sub == 0)
                 (which ? sm.cq : sm.ck)[t] = ss == 0.f ? 0.f : a.eps > 0.f ? inverse_root(ss + a.eps * up * up) : inverse(up);
 #pragma unroll
             for (int j = 0; j < PIECES; ++j)
-                *reinterpret_cast<uint4*>((which ? sm.q : sm.k) + (t / 16 * (DK / 16) + 2 * j + sub / 2) * 512 + in_block(t % 16, sub % 2)) =
+                *reinterpret_cast<uint4*>((which ? sm.q : sm.k) + in_tile(t, 4 * j + sub)) =
                     make_uint4(pack(f[8 * j], f[8 * j + 1]), pack(f[8 * j + 2], f[8 * j + 3]), pack(f[8 * j + 4], f[8 * j + 5]),
                                pack(f[8 * j + 6], f[8 * j + 7]));
         }
@@ -388,17 +330,17 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
     const uint32_t ks = tc::smem_addr(sm.k), qs = tc::smem_addr(sm.q);
     {
         const int eight = lane >> 3 & 1 ? back : front;
-        const int own = eight / 2 * KB + in_block(eight % 2 * 8 + (lane & 7), lane >> 4), rows = by_rows(lane);
+        const int own = in_tile(8 * eight + (lane & 7), lane >> 4), rows = tile_by_rows(lane);
 #pragma unroll 2
         for (int kt = 0; kt < DK / 16; ++kt) {
             uint32_t ak[4], aq[4];
-            ldsm4(ak, ks + kt * 512 + own);
-            ldsm4(aq, qs + kt * 512 + own);
+            ldsm4(ak, ks + kt * kCols16 + own);
+            ldsm4(aq, qs + kt * kCols16 + own);
 #pragma unroll
             for (int t2 = 0; t2 < 4; ++t2) {
                 if (2 * t2 > back) continue;
                 uint32_t b[4];
-                ldsm4(b, ks + t2 * KB + kt * 512 + rows);
+                ldsm4(b, ks + t2 * kRows16 + kt * kCols16 + rows);
                 mma(kk[2 * t2], ak, b[0], b[1]);
                 mma(kk[2 * t2 + 1], ak, b[2], b[3]);
                 mma(qk[2 * t2], aq, b[0], b[1]);
@@ -447,7 +389,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
                 gates.beta[t] = be[i] * ck * ck;
                 vec[kA * C + t] = since * ck;
                 vec[kBeta * C + t] = be[i] * ck;
-                out[kB * C + t] = since * cq;
+                out[kSince * C + t] = since;
                 out[kPi * C + t] = cq;
                 vec[kD * C + t] = exp2f((all.hi - hi) + (all.lo - s[i].lo));
             }
@@ -587,7 +529,6 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     constexpr int QS = Smem::QS;
     constexpr int NK = DK / 32;        // k steps of 16 of a half of the state's columns
-    constexpr int KB = DK / 16 * 512;  // bytes of 16 tokens of K
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g4 = lane / 4, q4 = lane % 4;
     const bool outputs = warp >= 2 * W;
     const int mine = !outputs ? warp / 2 : W == 2 ? (warp - 4) / 2 : warp - 2 * W, p = warp % 2;  // slice of the block, part of it
@@ -613,26 +554,14 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
     const int slices = a.Dv / (16 * W);
     const int slice = blockIdx.x % slices, hv = blockIdx.x / slices % a.Hv;
     int r = blockIdx.x / slices / a.Hv;
-    if (a.length && a.R <= 64) {  // long requests first, so that none begins when the others end
-        if (tid < a.R) {
-            const int len = __ldg(&a.length[tid]);
-            int rank = 0;
-            for (int j = 0; j < a.R; ++j) {
-                const int other = __ldg(&a.length[j]);
-                rank += other > len || (other == len && j < tid);
-            }
-            if (rank == r) sm.request = tid;
-        }
-        __syncthreads();
-        r = sm.request;
-    }
+    r = longest_first(a, r, &sm.request);
     int tokens, slot;
     if (!delta_request(a, r, tid == 0 && slice == 0 && hv == 0, tokens, slot)) return;
     __syncthreads();
     const int hk = hv / (a.Hv / a.Hk), n_chunks = (tokens + C - 1) / C;
     const int row0 = (slice * W + mine) * 16;  // first of the slice's rows
     const long long tok0 = 1ll * r * a.n, unit0 = 1ll * r * w.chunks;
-    const int rows = by_rows(lane), cols = by_cols(lane);
+    const int rows = by_rows(lane), slice_rows = slice_by_rows(lane), tile_rows = tile_by_rows(lane), tile_cols = tile_by_cols(lane);
     // (after a wait that ran out the other waits end at once and no more is fetched: the walk goes on, bounded, over
     // whatever stands in the tiles, so that nobody is left at a barrier, and the error is recorded)
     bool ok = true;
@@ -671,7 +600,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             wait(&sm.given[mine][cb], c >> 1);
             __syncwarp();
             typename Smem::ForOutputs& s = sm.q[c % QS];
-            const uint32_t qr = tc::smem_addr(s.q) + rows, pr = tc::smem_addr(s.p) + rows;
+            const uint32_t qr = tc::smem_addr(s.q) + tile_rows, pr = tc::smem_addr(s.p) + rows;
             const float* vec = reinterpret_cast<const float*>(s.p + kTri) + 2 * q4;
             // S0 Q^T, with the columns of each half of S0 and their scale
             float o[8][4];
@@ -685,7 +614,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                         const uint32_t hi[4] = {y.x, y.y, y.z, y.w};
                         uint32_t b[4][4];
 #pragma unroll
-                        for (int t2 = 0; t2 < 4; ++t2) ldsm4(b[t2], qr + t2 * KB + (half * NK + kt) * 512);
+                        for (int t2 = 0; t2 < 4; ++t2) ldsm4(b[t2], qr + t2 * kRows16 + (half * NK + kt) * kCols16);
 #pragma unroll
                         for (int t2 = 0; t2 < 4; ++t2) {
                             if (kt == 0) {
@@ -704,10 +633,10 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                         for (int e = 0; e < 4; ++e) o[t][e] = half ? o[t][e] + x[t][e] * f[e / 2] : x[t][e] * f[e / 2];
                 }
             }
-            // + P U', scaled by the token's factors
+            // e^G of that, + P U', scaled by the token's factor
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                const float2 b = *reinterpret_cast<const float2*>(vec + kB * C + 8 * t);
+                const float2 b = *reinterpret_cast<const float2*>(vec + kSince * C + 8 * t);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][e] *= e % 2 ? b.y : b.x;
             }
@@ -732,11 +661,15 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                 }
                 const float f[2] = {ps.du[cb][half][g4], ps.du[cb][half][g4 + 8]};
 #pragma unroll
-                for (int t = 4 * half; t < 8; ++t) {
-                    const float2 pi = *reinterpret_cast<const float2*>(vec + kPi * C + 8 * t);
+                for (int t = 4 * half; t < 8; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[t][e] += (e % 2 ? pi.y : pi.x) * (x[t][e] * f[e / 2]);
-                }
+                    for (int e = 0; e < 4; ++e) o[t][e] += x[t][e] * f[e / 2];
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 pi = *reinterpret_cast<const float2*>(vec + kPi * C + 8 * t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][e] *= e % 2 ? pi.y : pi.x;
             }
             __syncwarp();  // S0, U' and the tiles have been read
             if (lane == 0) {
@@ -753,7 +686,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                         const __nv_bfloat162 both = __floats2bfloat162_rn(o[2 * t2 + j][2 * h], o[2 * t2 + j][2 * h + 1]);
                         x[2 * j + h] = *reinterpret_cast<const uint32_t*>(&both);
                     }
-                stsm4_t(os + t2 * 512 + rows, x[0], x[1], x[2], x[3]);
+                stsm4_t(os + t2 * 512 + slice_rows, x[0], x[1], x[2], x[3]);
             }
             __syncwarp();
             bf16* op = static_cast<bf16*>(a.out) + hv * a.Dv + row0;
@@ -762,7 +695,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                 const int tok = c * C + i * 16 + lane / 2;
                 if (tok < tokens)
                     *reinterpret_cast<uint4*>(op + (tok0 + tok) * a.Hv * a.Dv + 8 * (lane & 1)) =
-                        *reinterpret_cast<const uint4*>(sm.o[mine] + i * 512 + in_block(lane / 2, lane & 1));
+                        *reinterpret_cast<const uint4*>(sm.o[mine] + i * 512 + in_slice(lane / 2, lane & 1));
             }
             __syncwarp();
         }
@@ -796,7 +729,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         for (int i = 0; i < 2; ++i) {
             const int t = i * 16 + lane / 2, tok = c * C + 32 * p + t;
             const bool on = tok < tokens;
-            cp16(vs + (c & 1) * 1024 + i * 512 + in_block(lane / 2, lane & 1), vp + (tok0 + (on ? tok : 0)) * a.v_ld + 8 * (lane & 1), on);
+            cp16(vs + (c & 1) * 1024 + i * 512 + in_slice(lane / 2, lane & 1), vp + (tok0 + (on ? tok : 0)) * a.v_ld + 8 * (lane & 1), on);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -833,7 +766,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         }
         __syncwarp();
         typename Smem::ForStates& s = sm.x[st];
-        const uint32_t kr = tc::smem_addr(s.k) + 2 * p * KB + rows, xr = tc::smem_addr(s.x) + rows;
+        const uint32_t kr = tc::smem_addr(s.k) + 2 * p * kRows16 + tile_rows, xr = tc::smem_addr(s.x) + rows;
         const float* vec = reinterpret_cast<const float*>(s.x + 2 * kTri) + 32 * p + 2 * q4;  // of this warp's tokens
         const uint32_t vc = vs + (c & 1) * 1024;
 
@@ -855,7 +788,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             constexpr bool F = decltype(first)::value;
             uint32_t b0[4], b1[4];
             ldsm4(b0, kb);
-            ldsm4(b1, kb + KB);
+            ldsm4(b1, kb + kRows16);
             mma_<F>(x[0], hi, b0[0], b0[1]);
             mma_<F>(x[1], hi, b0[2], b0[3]);
             mma_<F>(x[2], hi, b1[0], b1[1]);
@@ -867,7 +800,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         };
         const std::true_type first{};
         const std::false_type then{};
-        const uint32_t k_own = kr + p * (NK * 512), k_other = kr + (1 - p) * (NK * 512);
+        const uint32_t k_own = kr + p * (NK * kCols16), k_other = kr + (1 - p) * (NK * kCols16);
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
             uint32_t hi[4], lo[4];
@@ -879,9 +812,9 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             ps.s[cb][p][kt][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             ps.sl[p][kt][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (kt == 0)
-                half_product(first, hi, lo, k_own + kt * 512, sk);
+                half_product(first, hi, lo, k_own + kt * kCols16, sk);
             else
-                half_product(then, hi, lo, k_own + kt * 512, sk);
+                half_product(then, hi, lo, k_own + kt * kCols16, sk);
         }
         tc::named_bar_sync(bar_a, 64);
         if (tid == 0 && ok && issued < n_chunks) fetch();
@@ -892,16 +825,16 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             const uint4 x = ps.s[cb][1 - p][kt][lane], y = ps.sl[1 - p][kt][lane];
             const uint32_t hi[4] = {x.x, x.y, x.z, x.w}, lo[4] = {y.x, y.y, y.z, y.w};
             if (kt == 0)
-                half_product(first, hi, lo, k_other + kt * 512, zk);
+                half_product(first, hi, lo, k_other + kt * kCols16, zk);
             else
-                half_product(then, hi, lo, k_other + kt * 512, zk);
+                half_product(then, hi, lo, k_other + kt * kCols16, zk);
         }
         // R = beta c (v - e^G c S0 k), in place of S0 K^T
         float rmost[2] = {0.f, 0.f};
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
             uint32_t vv[4];  // tokens 16 t2 ..: columns 0-7, 8-15; tokens 16 t2 + 8 ..: the same
-            ldsm4_t(vv, vc + t2 * 512 + rows);
+            ldsm4_t(vv, vc + t2 * 512 + slice_rows);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = 2 * t2 + j;
@@ -942,14 +875,14 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                 }
             }
             if (p == 0) bar_arrive(bar_b, 64);
-            const uint32_t x0 = xr + (p ? tri(2, 2) : tri(0, 0)), x1 = xr + (p ? tri(3, 2) : tri(1, 0));
+            const uint32_t x0 = xr + (p ? tri(2, 2) : tri(0, 0)), x1 = xr + (p ? tri(3, 2) : tri(1, 0)), x2 = xr + (p ? tri(3, 3) : tri(1, 1));
             uint32_t b0[4], l0[4], b1[4], l1[4], b2[4], l2[4];
             ldsm4(b0, x0);
             ldsm4(l0, x0 + kTri);
             ldsm4(b1, x1);
             ldsm4(l1, x1 + kTri);
-            ldsm4(b2, x1 + 512);
-            ldsm4(l2, x1 + 512 + kTri);
+            ldsm4(b2, x2);
+            ldsm4(l2, x2 + kTri);
             mma3<true>(u[0], u[1], hi[0], lo[0], b0, l0);
             mma3<true>(u[2], u[3], hi[0], lo[0], b1, l1);
             mma3<false>(u[2], u[3], hi[1], lo[1], b2, l2);
@@ -1035,14 +968,14 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         // their own, added in fp32: an MMA cuts off what it adds to a large accumulator)
         float d[DK / 16][4];
         auto state_product = [&](const uint32_t(&hi)[2][4], const uint32_t(&lo)[2][4], int half) {
-            const uint32_t kc = tc::smem_addr(s.k) + half * (2 * KB) + p * (NK * 512) + cols;
+            const uint32_t kc = tc::smem_addr(s.k) + half * (2 * kRows16) + p * (NK * kCols16) + tile_cols;
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
                 for (int t2 = 0; t2 < NK; t2 += 2) {
                     uint32_t b0[4], b1[4];
-                    ldsm4_t(b0, kc + kt * KB + t2 * 512);
-                    ldsm4_t(b1, kc + kt * KB + t2 * 512 + 512);
+                    ldsm4_t(b0, kc + kt * kRows16 + t2 * kCols16);
+                    ldsm4_t(b1, kc + kt * kRows16 + (t2 + 1) * kCols16);
                     if (kt == 0) {
                         mma0(d[2 * t2], hi[kt], b0[0], b0[1]);
                         mma0(d[2 * t2 + 1], hi[kt], b0[2], b0[3]);
@@ -1134,9 +1067,12 @@ cudaError_t launch_chunks(const DeltaArgs& a, const Scratch& w, int sms, cudaStr
     // As few slices a block as leave no multiprocessor a second block (blocks of more share their tiles, but also the chain
     // of a chunk gets longer).  us for 1000 tokens with 1 / 2 / 4 slices a block: 128 slices 41 / 48 / 65, 256 slices
     // 73 / 52 / 68, 384 slices of 500 tokens 59 / 51 / 40.
+    // Where that fills the multiprocessors more than once and there is more than one chunk, whole heads on tcgen05 are faster
+    // (1000 tokens, 512 slices 89 against 76, 768 slices 100 : 140, 1024 slices 104 : 145).
     const long long slices = 1ll * a.R * a.Hv * (a.Dv / 16);
     if (slices <= sms) return launch_walk<DK, 1, 3>(a, w, s);
     if (slices <= 2ll * sms) return launch_walk<DK, 2, 3>(a, w, s);
+    if (a.Dv == 128 && a.n > C && slices > 4ll * sms) return launch_delta_heads(a, w, s);
     return launch_walk<DK, 4, 2>(a, w, s);
 }
 
