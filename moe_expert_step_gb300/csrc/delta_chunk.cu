@@ -227,7 +227,8 @@ __device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t 
     }
 }
 
-template <int DK>
+// BRIEF: at most 32 tokens a request, whose products are half as many rows and columns
+template <int DK, bool BRIEF>
 __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, const Scratch w) {
     extern __shared__ __align__(128) char raw[];
     PrepSmem<DK>& sm = *reinterpret_cast<PrepSmem<DK>*>(raw);
@@ -247,11 +248,12 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
 
     // keys and queries: f16 after a power of two a row, four lanes a row
     constexpr int PIECES = DK / 32;  // 16-byte pieces of a lane: 64 bytes of a row together
+    constexpr int EIGHTS = BRIEF ? 1 : 2;  // of a warp's tokens
     const int sub = (lane & 1) + (lane >> 4) * 2, row = lane >> 1 & 7;  // (a load's and a store's eight lanes: whole sectors, few conflicts)
-    uint4 in[2][2][PIECES];
+    uint4 in[2][EIGHTS][PIECES];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int t = warp * 16 + i * 8 + row;
+    for (int i = 0; i < EIGHTS; ++i) {
+        const int t = (warp * EIGHTS + i) * 8 + row;
         const bf16* kp = static_cast<const bf16*>(a.k) + (tok0 + t) * a.k_ld + hk * DK + 8 * sub;
         const bf16* qp = static_cast<const bf16*>(a.q) + (tok0 + t) * a.q_ld + hk * DK + 8 * sub;
 #pragma unroll
@@ -278,10 +280,10 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
     };
     if (warp % 2 == 0) load_gates(pair);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < EIGHTS; ++i)
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            const int t = warp * 16 + i * 8 + row;
+            const int t = (warp * EIGHTS + i) * 8 + row;
             float f[8 * PIECES], most = 0.f;
 #pragma unroll
             for (int j = 0; j < PIECES; ++j) {
@@ -320,11 +322,13 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
     }
 
     // k.k and q.k of this warp's tokens with the tokens up to them: eight tokens from the front and eight from the back, so
-    // that every warp has as many pairs
-    const int front = warp, back = 7 - warp;  // in eights
-    float kk[8][4], qk[8][4];
+    // that every warp has as many pairs (BRIEF: k.k by the first two warps, q.k by the others)
+    const int front = BRIEF ? warp % 2 : warp, back = (BRIEF ? 3 : 7) - front;  // in eights
+    constexpr int COLS = BRIEF ? 4 : 8;                                        // eights of tokens
+    const bool of_keys = !BRIEF || warp < 2, of_queries = !BRIEF || warp >= 2;
+    float kk[COLS][4], qk[COLS][4];
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int t = 0; t < COLS; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) kk[t][e] = qk[t][e] = 0.f;
     const uint32_t ks = tc::smem_addr(sm.k), qs = tc::smem_addr(sm.q);
@@ -334,17 +338,21 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
 #pragma unroll 2
         for (int kt = 0; kt < DK / 16; ++kt) {
             uint32_t ak[4], aq[4];
-            ldsm4(ak, ks + kt * kCols16 + own);
-            ldsm4(aq, qs + kt * kCols16 + own);
+            if (of_keys) ldsm4(ak, ks + kt * kCols16 + own);
+            if (of_queries) ldsm4(aq, qs + kt * kCols16 + own);
 #pragma unroll
-            for (int t2 = 0; t2 < 4; ++t2) {
+            for (int t2 = 0; t2 < COLS / 2; ++t2) {
                 if (2 * t2 > back) continue;
                 uint32_t b[4];
                 ldsm4(b, ks + t2 * kRows16 + kt * kCols16 + rows);
-                mma(kk[2 * t2], ak, b[0], b[1]);
-                mma(kk[2 * t2 + 1], ak, b[2], b[3]);
-                mma(qk[2 * t2], aq, b[0], b[1]);
-                mma(qk[2 * t2 + 1], aq, b[2], b[3]);
+                if (of_keys) {
+                    mma(kk[2 * t2], ak, b[0], b[1]);
+                    mma(kk[2 * t2 + 1], ak, b[2], b[3]);
+                }
+                if (of_queries) {
+                    mma(qk[2 * t2], aq, b[0], b[1]);
+                    mma(qk[2 * t2 + 1], aq, b[2], b[3]);
+                }
             }
         }
     }
@@ -407,7 +415,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
             const float gh[2] = {gates.ghi[i0[0]], gates.ghi[i0[1]]}, gl[2] = {gates.glo[i0[0]], gates.glo[i0[1]]};
             const float bc[2] = {gates.beta[i0[0]], gates.beta[i0[1]]};
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
+            for (int t = 0; t < COLS; ++t) {
                 if (t > (back | 1)) continue;
                 const float2 jh = *reinterpret_cast<const float2*>(&gates.ghi[8 * t + 2 * q4]);
                 const float2 jl = *reinterpret_cast<const float2*>(&gates.glo[8 * t + 2 * q4]);
@@ -420,23 +428,25 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
                     const float a0 = e0 * bc[h] * kk[t][2 * h], a1 = e1 * bc[h] * kk[t][2 * h + 1];
                     float p0 = e0 * qk[t][2 * h], p1 = e1 * qk[t][2 * h + 1];
                     if (t / 2 == eight / 2) {  // (the elements of A' on and above the diagonal are not looked at)
-                        bl.at[t / 2][j % 16][i % 16] = a0;
-                        bl.at[t / 2][j % 16 + 1][i % 16] = a1;
+                        if (of_keys) {
+                            bl.at[t / 2][j % 16][i % 16] = a0;
+                            bl.at[t / 2][j % 16 + 1][i % 16] = a1;
+                        }
                         if (j > i) p0 = 0.f;
                         if (j + 1 > i) p1 = 0.f;
-                    } else {
+                    } else if (of_keys) {
                         uint32_t hi, lo;
                         split(a0, a1, hi, lo);
                         *reinterpret_cast<uint32_t*>(bl.ahi + below(eight / 2, t / 2) + at) = hi;
                         *reinterpret_cast<uint32_t*>(bl.alo + below(eight / 2, t / 2) + at) = lo;
                     }
-                    *reinterpret_cast<uint32_t*>(ps + tri(eight / 2, t / 2) + at) = pack(p0, p1);
+                    if (of_queries) *reinterpret_cast<uint32_t*>(ps + tri(eight / 2, t / 2) + at) = pack(p0, p1);
                 }
             }
         }
         tc::fence_proxy_async_smem();
         __syncthreads();
-        if (on) {
+        if (on && (!BRIEF || warp % 2 == 0)) {
             char* const xp = sm.x[pair];
             {  // diagonal blocks: column c of block b, an elimination in registers
                 const int c = warp % 2 * 32 + lane, b = c / 16;
@@ -461,10 +471,12 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
             const int w2 = warp % 2;
             __syncwarp();
             merge_blocks<1>(xh, xl, ah, al, 2 * w2, 2 * w2, 2 * w2 + 1);
-            tc::named_bar_sync(1 + pair, 64);
-            merge_blocks<2>(xh, xl, ah, al, 0, w2, 2);
+            if constexpr (!BRIEF) {
+                tc::named_bar_sync(1 + pair, 64);
+                merge_blocks<2>(xh, xl, ah, al, 0, w2, 2);
+            }
             tc::fence_proxy_async_smem();
-            tc::named_bar_sync(1 + pair, 64);
+            if constexpr (!BRIEF) tc::named_bar_sync(1 + pair, 64);
         }
         if (group - v0 > 1) __syncthreads();  // (thread 0 stores both heads)
         if (tid == 0) {
@@ -489,9 +501,9 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
 // Slower: one warp a slice (448 us for the 8192 tokens); four warps a slice, a quarter of columns and tokens each (333); the
 // products of neighbouring chunks' keys from the first launch, which take the states off the chain but cost a quarter
 // more MMAs (273, and 13 us more in the first launch; 648 for the batch).
-template <int DK, int W, int NS>
+template <int DK, int W, int NS, int TT>
 struct WalkSmem {
-    static constexpr int QS = 2;
+    static constexpr int QS = NS == 1 ? 1 : 2;
     struct ForStates {
         char k[Tile<DK>::kBytes];
         char x[kXBytes];
@@ -502,16 +514,16 @@ struct WalkSmem {
     };
     alignas(128) ForStates x[NS];
     ForOutputs q[QS];
-    struct Pass {                    // of a slice, from warp p to the others
-        uint4 s[2][2][DK / 32][32];  // [chunk % 2][p][k step][lane]: S0, high
-        uint4 sl[2][DK / 32][32];    // low
-        uint4 u[2][2][2][32];        // [chunk % 2][p][k step][lane]: U', high
-        uint4 d[2][2][2][32];        // [p][k step][high, low][lane]: U' e^(G_C - G)
-        uint4 r[2][2][32];           // R of the first 32 tokens
-        float ds[2][2][16], du[2][2][16], dd[2][16], dr[16];  // factors of their rows
+    struct Pass {                     // of a slice, from warp p to the others
+        uint4 s[QS][2][DK / 32][32];  // [chunk % 2][p][k step][lane]: S0, high
+        uint4 sl[2][DK / 32][32];     // low
+        uint4 u[QS][2][TT][32];       // [chunk % 2][p][k step][lane]: U', high
+        uint4 d[2][TT][2][32];        // [p][k step][high, low][lane]: U' e^(G_C - G)
+        uint4 r[TT][2][32];           // R of the first tokens
+        float ds[QS][2][16], du[QS][2][16], dd[2][16], dr[16];  // factors of their rows
     } pass[W];
-    char v[2 * W][2][32 * 32];  // a warp's 32 tokens of 16 values
-    char o[W][C * 32];          // 64 tokens of 16 outputs
+    char v[2 * W][QS][TT * 16 * 32];  // a warp's tokens of 16 values
+    char o[W][2 * TT * 16 * 32];      // the chunk's tokens of 16 outputs
     uint64_t x_full[NS], x_empty[NS], q_full[QS], q_empty[QS];
     uint64_t given[W][2], taken[W][2];  // S0 and U' of chunk % 2 for the third warp
     int abort, request;
@@ -522,10 +534,11 @@ struct WalkSmem {
 template <int W>
 constexpr int kWalkWarps = 3 * W + (W == 2);
 
-template <int DK, int W, int NS>
-__global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
+// TT: sixteens of tokens of each of the two warps.  2; or 1, for at most 32 tokens a request, with tiles for one chunk (NS = 1)
+template <int DK, int W, int NS, int TT>
+__global__ void __launch_bounds__(32 * kWalkWarps<W>, TT == 1 ? 2 : 1) delta_walk_kernel(const DeltaArgs a, const Scratch w) {
     extern __shared__ __align__(128) char raw[];
-    using Smem = WalkSmem<DK, W, NS>;
+    using Smem = WalkSmem<DK, W, NS, TT>;
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     constexpr int QS = Smem::QS;
     constexpr int NK = DK / 32;        // k steps of 16 of a half of the state's columns
@@ -603,20 +616,20 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             const uint32_t qr = tc::smem_addr(s.q) + tile_rows, pr = tc::smem_addr(s.p) + rows;
             const float* vec = reinterpret_cast<const float*>(s.p + kTri) + 2 * q4;
             // S0 Q^T, with the columns of each half of S0 and their scale
-            float o[8][4];
+            float o[4 * TT][4];
             {
-                float x[8][4];
+                float x[4 * TT][4];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
 #pragma unroll
                     for (int kt = 0; kt < NK; ++kt) {
                         const uint4 y = ps.s[cb][half][kt][lane];
                         const uint32_t hi[4] = {y.x, y.y, y.z, y.w};
-                        uint32_t b[4][4];
+                        uint32_t b[2 * TT][4];
 #pragma unroll
-                        for (int t2 = 0; t2 < 4; ++t2) ldsm4(b[t2], qr + t2 * kRows16 + (half * NK + kt) * kCols16);
+                        for (int t2 = 0; t2 < 2 * TT; ++t2) ldsm4(b[t2], qr + t2 * kRows16 + (half * NK + kt) * kCols16);
 #pragma unroll
-                        for (int t2 = 0; t2 < 4; ++t2) {
+                        for (int t2 = 0; t2 < 2 * TT; ++t2) {
                             if (kt == 0) {
                                 mma0(x[2 * t2], hi, b[t2][0], b[t2][1]);
                                 mma0(x[2 * t2 + 1], hi, b[t2][2], b[t2][3]);
@@ -628,45 +641,46 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                     }
                     const float f[2] = {ps.ds[cb][half][g4], ps.ds[cb][half][g4 + 8]};
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
+                    for (int t = 0; t < 4 * TT; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[t][e] = half ? o[t][e] + x[t][e] * f[e / 2] : x[t][e] * f[e / 2];
                 }
             }
             // e^G of that, + P U', scaled by the token's factor
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
+            for (int t = 0; t < 4 * TT; ++t) {
                 const float2 b = *reinterpret_cast<const float2*>(vec + kSince * C + 8 * t);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][e] *= e % 2 ? b.y : b.x;
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float x[8][4];
-                const uint4 y0 = ps.u[cb][half][0][lane], y1 = ps.u[cb][half][1][lane];
-                const uint32_t u0[4] = {y0.x, y0.y, y0.z, y0.w}, u1[4] = {y1.x, y1.y, y1.z, y1.w};
+                float x[4 * TT][4];
 #pragma unroll
-                for (int t2 = 2 * half; t2 < 4; ++t2) {
-                    uint32_t b[4];
-                    ldsm4(b, pr + tri(t2, 2 * half));
-                    mma0(x[2 * t2], u0, b[0], b[1]);
-                    mma0(x[2 * t2 + 1], u0, b[2], b[3]);
-                }
+                for (int kt = 0; kt < TT; ++kt) {
+                    const uint4 y = ps.u[cb][half][kt][lane];
+                    const uint32_t uh[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int t2 = 2 * half + 1; t2 < 4; ++t2) {
-                    uint32_t b[4];
-                    ldsm4(b, pr + tri(t2, 2 * half + 1));
-                    mma(x[2 * t2], u1, b[0], b[1]);
-                    mma(x[2 * t2 + 1], u1, b[2], b[3]);
+                    for (int t2 = TT * half + kt; t2 < 2 * TT; ++t2) {
+                        uint32_t b[4];
+                        ldsm4(b, pr + tri(t2, TT * half + kt));
+                        if (kt == 0) {
+                            mma0(x[2 * t2], uh, b[0], b[1]);
+                            mma0(x[2 * t2 + 1], uh, b[2], b[3]);
+                        } else {
+                            mma(x[2 * t2], uh, b[0], b[1]);
+                            mma(x[2 * t2 + 1], uh, b[2], b[3]);
+                        }
+                    }
                 }
                 const float f[2] = {ps.du[cb][half][g4], ps.du[cb][half][g4 + 8]};
 #pragma unroll
-                for (int t = 4 * half; t < 8; ++t)
+                for (int t = 2 * TT * half; t < 4 * TT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[t][e] += x[t][e] * f[e / 2];
             }
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
+            for (int t = 0; t < 4 * TT; ++t) {
                 const float2 pi = *reinterpret_cast<const float2*>(vec + kPi * C + 8 * t);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][e] *= e % 2 ? pi.y : pi.x;
@@ -677,7 +691,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                 tc::mbar_arrive(&sm.q_empty[c % QS]);
             }
 #pragma unroll
-            for (int t2 = 0; t2 < 4; ++t2) {
+            for (int t2 = 0; t2 < 2 * TT; ++t2) {
                 uint32_t x[4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -691,7 +705,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             __syncwarp();
             bf16* op = static_cast<bf16*>(a.out) + hv * a.Dv + row0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2 * TT; ++i) {
                 const int tok = c * C + i * 16 + lane / 2;
                 if (tok < tokens)
                     *reinterpret_cast<uint4*>(op + (tok0 + tok) * a.Hv * a.Dv + 8 * (lane & 1)) =
@@ -720,16 +734,16 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         ++issued;
     };
     if (tid == 0)
-        while (issued < NS - 1 && issued < n_chunks) fetch();
+        while (issued < (NS == 1 ? 1 : NS - 1) && issued < n_chunks) fetch();
 
     const uint32_t vs = tc::smem_addr(sm.v[warp]);
     auto fetch_v = [&](int c) {  // the warp's values, zeros behind the request's tokens
         const bf16* vp = static_cast<const bf16*>(a.v) + hv * a.Dv + row0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = i * 16 + lane / 2, tok = c * C + 32 * p + t;
+        for (int i = 0; i < TT; ++i) {
+            const int t = i * 16 + lane / 2, tok = c * C + 16 * TT * p + t;
             const bool on = tok < tokens;
-            cp16(vs + (c & 1) * 1024 + i * 512 + in_slice(lane / 2, lane & 1), vp + (tok0 + (on ? tok : 0)) * a.v_ld + 8 * (lane & 1), on);
+            cp16(vs + (c & 1) * (TT * 512) + i * 512 + in_slice(lane / 2, lane & 1), vp + (tok0 + (on ? tok : 0)) * a.v_ld + 8 * (lane & 1), on);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -766,9 +780,9 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         }
         __syncwarp();
         typename Smem::ForStates& s = sm.x[st];
-        const uint32_t kr = tc::smem_addr(s.k) + 2 * p * kRows16 + tile_rows, xr = tc::smem_addr(s.x) + rows;
-        const float* vec = reinterpret_cast<const float*>(s.x + 2 * kTri) + 32 * p + 2 * q4;  // of this warp's tokens
-        const uint32_t vc = vs + (c & 1) * 1024;
+        const uint32_t kr = tc::smem_addr(s.k) + TT * p * kRows16 + tile_rows, xr = tc::smem_addr(s.x) + rows;
+        const float* vec = reinterpret_cast<const float*>(s.x + 2 * kTri) + 16 * TT * p + 2 * q4;  // of this warp's tokens
+        const uint32_t vc = vs + (c & 1) * (TT * 512);
 
         // S0 K^T of the warp's tokens: first with its own columns of S0, then with the other's
         float most[2] = {0.f, 0.f}, up[2], own[2], other[2];
@@ -783,20 +797,22 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             own[h] = inverse(up[h]);
             if (q4 == 0) ps.ds[cb][p][g4 + 8 * h] = own[h];
         }
-        float sk[4][4], zk[4][4];
-        auto half_product = [&](auto first, const uint32_t(&hi)[4], const uint32_t(&lo)[4], uint32_t kb, float(&x)[4][4]) {
+        float sk[2 * TT][4], zk[2 * TT][4];
+        auto half_product = [&](auto first, const uint32_t(&hi)[4], const uint32_t(&lo)[4], uint32_t kb, float(&x)[2 * TT][4]) {
             constexpr bool F = decltype(first)::value;
-            uint32_t b0[4], b1[4];
-            ldsm4(b0, kb);
-            ldsm4(b1, kb + kRows16);
-            mma_<F>(x[0], hi, b0[0], b0[1]);
-            mma_<F>(x[1], hi, b0[2], b0[3]);
-            mma_<F>(x[2], hi, b1[0], b1[1]);
-            mma_<F>(x[3], hi, b1[2], b1[3]);
-            mma(x[0], lo, b0[0], b0[1]);
-            mma(x[1], lo, b0[2], b0[3]);
-            mma(x[2], lo, b1[0], b1[1]);
-            mma(x[3], lo, b1[2], b1[3]);
+            uint32_t b[TT][4];
+#pragma unroll
+            for (int t2 = 0; t2 < TT; ++t2) ldsm4(b[t2], kb + t2 * kRows16);
+#pragma unroll
+            for (int t2 = 0; t2 < TT; ++t2) {
+                mma_<F>(x[2 * t2], hi, b[t2][0], b[t2][1]);
+                mma_<F>(x[2 * t2 + 1], hi, b[t2][2], b[t2][3]);
+            }
+#pragma unroll
+            for (int t2 = 0; t2 < TT; ++t2) {
+                mma(x[2 * t2], lo, b[t2][0], b[t2][1]);
+                mma(x[2 * t2 + 1], lo, b[t2][2], b[t2][3]);
+            }
         };
         const std::true_type first{};
         const std::false_type then{};
@@ -832,7 +848,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         // R = beta c (v - e^G c S0 k), in place of S0 K^T
         float rmost[2] = {0.f, 0.f};
 #pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2) {
+        for (int t2 = 0; t2 < TT; ++t2) {
             uint32_t vv[4];  // tokens 16 t2 ..: columns 0-7, 8-15; tokens 16 t2 + 8 ..: the same
             ldsm4_t(vv, vc + t2 * 512 + slice_rows);
 #pragma unroll
@@ -859,11 +875,11 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             rdown[h] = inverse(rup[h]);
             if (p == 0 && q4 == 0) ps.dr[g4 + 8 * h] = rdown[h];
         }
-        float u[4][4];
+        float u[2 * TT][4];
         {
-            uint32_t hi[2][4], lo[2][4];
+            uint32_t hi[TT][4], lo[TT][4];
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
+            for (int kt = 0; kt < TT; ++kt) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     split(sk[2 * kt + j][0] * rup[0], sk[2 * kt + j][1] * rup[0], hi[kt][2 * j], lo[kt][2 * j]);
@@ -875,51 +891,62 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                 }
             }
             if (p == 0) bar_arrive(bar_b, 64);
-            const uint32_t x0 = xr + (p ? tri(2, 2) : tri(0, 0)), x1 = xr + (p ? tri(3, 2) : tri(1, 0)), x2 = xr + (p ? tri(3, 3) : tri(1, 1));
-            uint32_t b0[4], l0[4], b1[4], l1[4], b2[4], l2[4];
-            ldsm4(b0, x0);
-            ldsm4(l0, x0 + kTri);
-            ldsm4(b1, x1);
-            ldsm4(l1, x1 + kTri);
-            ldsm4(b2, x2);
-            ldsm4(l2, x2 + kTri);
-            mma3<true>(u[0], u[1], hi[0], lo[0], b0, l0);
-            mma3<true>(u[2], u[3], hi[0], lo[0], b1, l1);
-            mma3<false>(u[2], u[3], hi[1], lo[1], b2, l2);
+            uint32_t b[TT][TT][4], l[TT][TT][4];
+#pragma unroll
+            for (int t2 = 0; t2 < TT; ++t2)
+#pragma unroll
+                for (int kt = 0; kt <= t2; ++kt) {
+                    const uint32_t x = xr + (p ? tri(TT + t2, TT + kt) : tri(t2, kt));
+                    ldsm4(b[t2][kt], x);
+                    ldsm4(l[t2][kt], x + kTri);
+                }
+#pragma unroll
+            for (int kt = 0; kt < TT; ++kt)
+#pragma unroll
+                for (int t2 = kt; t2 < TT; ++t2) {
+                    if (kt == 0)
+                        mma3<true>(u[2 * t2], u[2 * t2 + 1], hi[kt], lo[kt], b[t2][kt], l[t2][kt]);
+                    else
+                        mma3<false>(u[2 * t2], u[2 * t2 + 1], hi[kt], lo[kt], b[t2][kt], l[t2][kt]);
+                }
         }
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 2 * TT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) u[t][e] *= rdown[e / 2];
         if (p == 1) {
-            float z[4][4];
-            uint32_t b0[4], l0[4], b1[4], l1[4], b2[4], l2[4], b3[4], l3[4];
-            ldsm4(b0, xr + tri(2, 0));
-            ldsm4(l0, xr + tri(2, 0) + kTri);
-            ldsm4(b1, xr + tri(3, 0));
-            ldsm4(l1, xr + tri(3, 0) + kTri);
-            ldsm4(b2, xr + tri(2, 1));
-            ldsm4(l2, xr + tri(2, 1) + kTri);
-            ldsm4(b3, xr + tri(3, 1));
-            ldsm4(l3, xr + tri(3, 1) + kTri);
+            float z[2 * TT][4];
+            uint32_t b[TT][TT][4], l[TT][TT][4];
+#pragma unroll
+            for (int t2 = 0; t2 < TT; ++t2)
+#pragma unroll
+                for (int kt = 0; kt < TT; ++kt) {
+                    ldsm4(b[t2][kt], xr + tri(TT + t2, kt));
+                    ldsm4(l[t2][kt], xr + tri(TT + t2, kt) + kTri);
+                }
             tc::named_bar_sync(bar_b, 64);
             const float f[2] = {ps.dr[g4], ps.dr[g4 + 8]};
-            const uint4 h0 = ps.r[0][0][lane], g0 = ps.r[0][1][lane], h1 = ps.r[1][0][lane], g1 = ps.r[1][1][lane];
-            const uint32_t hi0[4] = {h0.x, h0.y, h0.z, h0.w}, lo0[4] = {g0.x, g0.y, g0.z, g0.w};
-            const uint32_t hi1[4] = {h1.x, h1.y, h1.z, h1.w}, lo1[4] = {g1.x, g1.y, g1.z, g1.w};
-            mma3<true>(z[0], z[1], hi0, lo0, b0, l0);
-            mma3<true>(z[2], z[3], hi0, lo0, b1, l1);
-            mma3<false>(z[0], z[1], hi1, lo1, b2, l2);
-            mma3<false>(z[2], z[3], hi1, lo1, b3, l3);
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int kt = 0; kt < TT; ++kt) {
+                const uint4 x = ps.r[kt][0][lane], y = ps.r[kt][1][lane];
+                const uint32_t hi[4] = {x.x, x.y, x.z, x.w}, lo[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int t2 = 0; t2 < TT; ++t2) {
+                    if (kt == 0)
+                        mma3<true>(z[2 * t2], z[2 * t2 + 1], hi, lo, b[t2][kt], l[t2][kt]);
+                    else
+                        mma3<false>(z[2 * t2], z[2 * t2 + 1], hi, lo, b[t2][kt], l[t2][kt]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 2 * TT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) u[t][e] += z[t][e] * f[e / 2];
         }
         // U' and U' e^(G_C - G), each brought to 2^12
-        float umost[2] = {0.f, 0.f}, dmost[2] = {0.f, 0.f}, dx[4][4];
+        float umost[2] = {0.f, 0.f}, dmost[2] = {0.f, 0.f}, dx[2 * TT][4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 2 * TT; ++t) {
             const float2 left = *reinterpret_cast<const float2*>(vec + kD * C + 8 * t);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -940,9 +967,9 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
                 ps.du[cb][p][g4 + 8 * h] = inverse(uup[h]);
             }
         }
-        uint32_t dhi[2][4], dlo[2][4];
+        uint32_t dhi[TT][4], dlo[TT][4];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
+        for (int kt = 0; kt < TT; ++kt) {
             uint32_t uh[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -956,6 +983,11 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
             ps.d[p][kt][1][lane] = make_uint4(dlo[kt][0], dlo[kt][1], dlo[kt][2], dlo[kt][3]);
             ps.u[cb][p][kt][lane] = make_uint4(uh[0], uh[1], uh[2], uh[3]);
         }
+        if (!a.state_out && c + 1 == n_chunks) {  // the states behind the last chunk are not wanted
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.given[mine][cb]);
+            break;
+        }
         if (p == 0) {
             bar_arrive(bar_a, 64);
         } else {
@@ -967,10 +999,10 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         // S = e^G_C S0 + U' e^(G_C - G) K on the warp's columns, with its own tokens and then with the other's (sums of
         // their own, added in fp32: an MMA cuts off what it adds to a large accumulator)
         float d[DK / 16][4];
-        auto state_product = [&](const uint32_t(&hi)[2][4], const uint32_t(&lo)[2][4], int half) {
-            const uint32_t kc = tc::smem_addr(s.k) + half * (2 * kRows16) + p * (NK * kCols16) + tile_cols;
+        auto state_product = [&](const uint32_t(&hi)[TT][4], const uint32_t(&lo)[TT][4], int half) {
+            const uint32_t kc = tc::smem_addr(s.k) + half * (TT * kRows16) + p * (NK * kCols16) + tile_cols;
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
+            for (int kt = 0; kt < TT; ++kt)
 #pragma unroll
                 for (int t2 = 0; t2 < NK; t2 += 2) {
                     uint32_t b0[4], b1[4];
@@ -1005,9 +1037,9 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
         if (p == 0) tc::named_bar_sync(bar_c, 64);
         {
             const float f[2] = {ps.dd[1 - p][g4], ps.dd[1 - p][g4 + 8]};
-            uint32_t ehi[2][4], elo[2][4];
+            uint32_t ehi[TT][4], elo[TT][4];
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
+            for (int kt = 0; kt < TT; ++kt) {
                 const uint4 x = ps.d[1 - p][kt][0][lane], y = ps.d[1 - p][kt][1][lane];
                 ehi[kt][0] = x.x, ehi[kt][1] = x.y, ehi[kt][2] = x.z, ehi[kt][3] = x.w;
                 elo[kt][0] = y.x, elo[kt][1] = y.y, elo[kt][2] = y.z, elo[kt][3] = y.w;
@@ -1039,51 +1071,60 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, 1) delta_walk_kernel(const
     }
 }
 
-template <int DK>
+template <int DK, bool BRIEF>
 cudaError_t launch_prep(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
     static int done[64];
-    cudaError_t e = ensure_smem(delta_prep_kernel<DK>, sizeof(PrepSmem<DK>), done);
+    cudaError_t e = ensure_smem(delta_prep_kernel<DK, BRIEF>, sizeof(PrepSmem<DK>), done);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(1ll * a.R * w.chunks * a.Hk));
-    return launch_pdl(delta_prep_kernel<DK>, grid, dim3(128), sizeof(PrepSmem<DK>), s, a, w);
+    return launch_pdl(delta_prep_kernel<DK, BRIEF>, grid, dim3(128), sizeof(PrepSmem<DK>), s, a, w);
 }
 
-template <int DK, int W, int NS>
+template <int DK, int W, int NS, int TT>
 cudaError_t launch_walk(const DeltaArgs& a, const Scratch& w, cudaStream_t s) {
-    constexpr size_t bytes = sizeof(WalkSmem<DK, W, NS>);
-    static_assert(bytes <= 227 * 1024);
+    constexpr size_t bytes = sizeof(WalkSmem<DK, W, NS, TT>);
+    static_assert(bytes <= (TT == 1 ? 113 : 227) * 1024);
     static int done[64];
-    cudaError_t e = ensure_smem(delta_walk_kernel<DK, W, NS>, bytes, done);
+    cudaError_t e = ensure_smem(delta_walk_kernel<DK, W, NS, TT>, bytes, done);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.R * a.Hv * (a.Dv / (16 * W))));
-    return launch_pdl(delta_walk_kernel<DK, W, NS>, grid, dim3(32 * kWalkWarps<W>), bytes, s, a, w);
+    return launch_pdl(delta_walk_kernel<DK, W, NS, TT>, grid, dim3(32 * kWalkWarps<W>), bytes, s, a, w);
 }
 
 template <int DK>
 cudaError_t launch_chunks(const DeltaArgs& a, const Scratch& w, int sms, cudaStream_t s) {
-    cudaError_t e = launch_prep<DK>(a, w, s);
+    const bool brief = a.n <= 32;
+    cudaError_t e = brief ? launch_prep<DK, true>(a, w, s) : launch_prep<DK, false>(a, w, s);
     if (e != cudaSuccess) return e;
     count_launch();
     // As few slices a block as leave no multiprocessor a second block (blocks of more share their tiles, but also the chain
     // of a chunk gets longer).  us for 1000 tokens with 1 / 2 / 4 slices a block: 128 slices 41 / 48 / 65, 256 slices
-    // 73 / 52 / 68, 384 slices of 500 tokens 59 / 51 / 40.
-    // Where that fills the multiprocessors more than once and there is more than one chunk, whole heads on tcgen05 are faster
-    // (1000 tokens, 512 slices 89 against 76, 768 slices 100 : 140, 1024 slices 104 : 145).
+    // 73 / 52 / 68, 384 slices of 500 tokens 59 / 51 / 40.  Where four fill the multiprocessors more than once and there is more
+    // than one chunk, whole heads on tcgen05 are faster (1000 tokens, 512 slices 89 against 76, 768 slices 100 : 140, 1024
+    // slices 104 : 145).
     const long long slices = 1ll * a.R * a.Hv * (a.Dv / 16);
-    if (slices <= sms) return launch_walk<DK, 1, 3>(a, w, s);
-    if (slices <= 2ll * sms) return launch_walk<DK, 2, 3>(a, w, s);
+    // One chunk in halves of 16 tokens leaves room for two blocks a multiprocessor (us for 32 tokens with 1 / 2 / 4 slices a
+    // block: 256 slices 11.4 / 11.5 / 12.4, 512 slices 14.0 / 13.1 / 15.0, 1024 slices 21.6 / 18.9 / 16.6).
+    if (brief) {
+        if (slices <= 2ll * sms) return launch_walk<DK, 1, 1, 1>(a, w, s);
+        if (slices <= 4ll * sms) return launch_walk<DK, 2, 1, 1>(a, w, s);
+        return launch_walk<DK, 4, 1, 1>(a, w, s);
+    }
+    if (slices <= sms) return launch_walk<DK, 1, 3, 2>(a, w, s);
+    if (slices <= 2ll * sms) return launch_walk<DK, 2, 3, 2>(a, w, s);
     if (a.Dv == 128 && a.n > C && slices > 4ll * sms) return launch_delta_heads(a, w, s);
-    return launch_walk<DK, 4, 2>(a, w, s);
+    return launch_walk<DK, 4, 2, 2>(a, w, s);
 }
 
 size_t qk_bytes(const moestep_delta_dims& d, long long units) { return static_cast<size_t>(units) * d.Hk * 2 * C * d.Dk * 2; }
 
 }  // namespace
 
-// From 32 tokens on the two launches are faster than the recurrence, whatever the number of requests (us, 16 and 32 heads of
-// 128, one request: 24 tokens 13.1 against 11.3, 32 tokens 13.1 : 14.1, 64 tokens 13.4 : 25.8; 16 requests: 24 tokens 51 : 55,
-// 32 tokens 51 : 72).
-bool delta_chunked(const moestep_delta_dims& d, int R, int n) { return d.dtype == MOESTEP_BF16 && n >= 32; }
+// From 24 tokens on the two launches are faster than the recurrence but for one request or few small heads, which they hardly
+// slow down (us against the recurrence's with 20 / 24 / 28 tokens; 16 and 32 heads of 128: one request 11.2 : 9.6 / 11.2 : 10.6 /
+// 11.3 : 11.9, 4 requests 15.2 : 18.1 / 15.2 : 20.8 / 15.4 : 23.8, 16 requests 40.7 : 50.3 / 41.1 : 57.9 / 41.6 : 66.1; 2 and 4
+// heads of 64, one request 7.4 : 5.8 / 7.4 : 6.3 / 7.4 : 7.0).
+bool delta_chunked(const moestep_delta_dims& d, int R, int n) { return d.dtype == MOESTEP_BF16 && n >= 24; }
 
 size_t delta_chunk_bytes(const moestep_delta_dims& d, int R, int n) {
     if (!delta_chunked(d, R, n)) return 0;

@@ -284,6 +284,67 @@ def test_magnitudes(n):
         assert ((to2.double() / v - to.double()).norm() / to.double().norm()) <= 2.0 ** -17
 
 
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+@pytest.mark.parametrize("R,Hk,Hv", [(3, 1, 1), (24, 1, 3), (60, 2, 2)])
+@pytest.mark.parametrize("n", [24, 31, 32])
+def test_blocks(n, R, Hk, Hv, Dk, Dv):
+    """One short chunk; few and many slices of the states a multiprocessor; ragged, idle and new requests, NaN behind a
+    request's tokens; the history read only, written elsewhere, in place."""
+    dd = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=R + 1)
+    s = make(dd, R, n, 900 + n + R, extra=16)
+    length = torch.tensor([[n, 0, 1, 15, 16, 17, n - 1, n // 2][r % 8] for r in range(R)], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(n)
+    slot = torch.randperm(R + 1, generator=g)[:R].to(torch.int32).cuda()
+    slot[R // 2] = -1
+    fresh = (torch.rand(R, generator=g) < 0.3).to(torch.uint8).cuda()
+    for r in range(R):
+        if fresh[r] and slot[r] >= 0:
+            s["state"][int(slot[r])] = float("nan")
+        for x in ("q", "k", "v", "g", "beta"):
+            s[x][r * n + int(length[r]):(r + 1) * n] = float("nan")
+    clean = {k: v.nan_to_num(0.0) for k, v in s.items()}
+    kw = dict(slot=slot, length=length, fresh=fresh, scale=Dk ** -0.5)
+    out, word = call(dd, R, s, **kw)
+    assert word == ms.OK
+    check(dd, R, clean, out, None, **kw)
+    to = torch.full_like(s["state"], 3.0)
+    out2, word = call(dd, R, s, state_out=to, **kw)
+    assert word == ms.OK and torch.equal(out, out2)
+    check(dd, R, clean, out, to, **kw)
+    idle = [i for i in range(R + 1) if i not in slot.tolist()]
+    assert (to[idle] == 3.0).all()
+    out3, word = call(dd, R, s, state_out=s["state"], **kw)
+    assert word == ms.OK and torch.equal(out, out3)
+    used = [int(i) for i in slot if i >= 0]
+    assert torch.equal(s["state"][used], to[used])
+
+
+def test_blocks_are_their_sequence():
+    """Blocks of 32 and of 24 in place end where one call over all of their tokens does; a block that is read only changes
+    nothing; a wait that runs out is reported."""
+    dd = ms.DeltaDims(Hk=1, Hv=2, Dk=128, Dv=128, n_slots=1)
+    s = make(dd, 1, 120, 46)
+    start, outs, at = s["state"].clone(), [], 0
+    for m in (32, 24, 32, 32):
+        part = {k: (v if k == "state" else v[at:at + m]) for k, v in s.items()}
+        before = s["state"].clone()
+        seen, word = call(dd, 1, part, scale=0.1)
+        assert word == ms.OK and torch.equal(before, s["state"])
+        out, word = call(dd, 1, part, state_out=s["state"], scale=0.1)
+        assert word == ms.OK and torch.equal(seen, out)
+        outs.append(out)
+        at += m
+    assert at == 120
+    try:
+        ms.set_wait_timeout_ns(0)
+        _, word = call(dd, 1, {k: (v if k == "state" else v[:32]) for k, v in s.items()}, state_out=torch.empty_like(start))
+        assert word == ms.ETIMEOUT
+    finally:
+        ms.set_wait_timeout_ns(2_000_000_000)
+    end, s["state"] = s["state"], start
+    check(dd, 1, s, torch.cat(outs), end, scale=0.1)
+
+
 def many(R, Hk, Hv, Dk, n, seed, **kw):
     """More heads of 128 values than half the multiprocessors, more than one chunk: walked a head a block."""
     dd = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=128, n_slots=R + 2)
