@@ -476,7 +476,10 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
                 merge_blocks<2>(xh, xl, ah, al, 0, w2, 2);
             }
             tc::fence_proxy_async_smem();
-            if constexpr (!BRIEF) tc::named_bar_sync(1 + pair, 64);
+            if constexpr (BRIEF)
+                __syncwarp();
+            else
+                tc::named_bar_sync(1 + pair, 64);
         }
         if (group - v0 > 1) __syncthreads();  // (thread 0 stores both heads)
         if (tid == 0) {

@@ -9,9 +9,9 @@
 // are the first launch's tiles: 8 x 8 matrices at constant distances, so that K is an operand both ways and the
 // columns of a lower triangle are operands of 64, 48, 32 and 16 rows without their zeros.
 //
-// Bound: the chain, 7200 cycles a chunk.  An MMA with its left operand in tensor memory takes 64 cycles whatever its N, and 28 of
-// the 48 are on the chain (S0 K^T 1050 cycles, U' 1050, the state's 770); the threads' part is 3500 issue slots of a
-// scheduler.  Against the walk of slices of 16 rows with mma.sync (four slices a block; us with both launches, 16 / 32 heads of
+// Bound: the chain, 7200 cycles a chunk.  An MMA with its left operand in tensor memory takes 64 cycles whatever its N, and 40 of
+// the 48 are on the chain (S0 K^T 1050 cycles, U' 1050, the outputs' and the state's 770); the threads' part is 3500 issue
+// slots of a scheduler.  Against the walk of slices of 16 rows with mma.sync (four slices a block; us with both launches, 16 / 32 heads of
 // 128): 4 requests of 1000 tokens 104 : 145, 8 requests 199 : 281, 16 requests 387 : 499, 8 ragged ones of up to 4096 tokens
 // 434 : 569; but 2 requests of 1000 tokens 89 : 76, and with one chunk the same or more (4 requests of 64 tokens 27 : 24).
 // Slower: two threads a row and two blocks a multiprocessor (514), a warp of its own for the MMAs (518, 96 registers a thread
