@@ -227,6 +227,9 @@ __device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t 
     }
 }
 
+// 2^x of a chunk's decay; close to 1 it multiplies the state in every chunk, and exp2f's errors of one direction add up
+__device__ __forceinline__ float chunk_decay(float x) { return x > -0.25f ? 1.f + expm1f(x * 0.6931471805599453f) : exp2f(x); }
+
 // BRIEF: at most 32 tokens a request, whose products are half as many rows and columns
 template <int DK, bool BRIEF>
 __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, const Scratch w) {
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
                 out[kPi * C + t] = cq;
                 vec[kD * C + t] = exp2f((all.hi - hi) + (all.lo - s[i].lo));
             }
-            if (lane == 0) vec[kGamma * C] = exp2f(all.hi + all.lo);
+            if (lane == 0) vec[kGamma * C] = chunk_decay(all.hi + all.lo);
         }
         __syncthreads();
         // A' and P of both heads, from every warp's products

@@ -59,6 +59,10 @@ struct Staged {
 
 __device__ __forceinline__ float inverse_norm(float ss, float eps) { return eps > 0.f ? 1.0f / sqrtf(ss + eps) : 1.f; }
 
+// e^g.  Decays close to 1 multiply the state hundreds of times, where an error of a whole step in the same direction adds up
+// (expf: 500 tokens of g around -2e-4 leave states 2e-6 off, so 3e-7); below, expf's relative error is what counts.
+__device__ __forceinline__ float decay(float g) { return g > -0.25f ? 1.f + expm1f(g) : expf(g); }
+
 // ONE: a token a request, nothing is staged and each warp forms the token's sums itself
 template <typename T, int DK, bool ONE>
 __global__ void __launch_bounds__(32 * kWarps) delta_recurrent_kernel(const DeltaArgs a) {
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(32 * kWarps) delta_recurrent_kernel(const Delt
             load_row<T, N>(qp + 4 * sub, qq);
 #pragma unroll
             for (int i = 0; i < NR; ++i) v[i] = to_f32(vp[row + 4 * i]);
-            const float al = expf(a.g[tok0 * a.Hv + hv]), be = a.beta[tok0 * a.Hv + hv];
+            const float al = decay(a.g[tok0 * a.Hv + hv]), be = a.beta[tok0 * a.Hv + hv];
 #pragma unroll
             for (int j = 0; j < N; ++j)
 #pragma unroll
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(32 * kWarps) delta_recurrent_kernel(const Delt
 #pragma unroll
                 for (int i = 0; i < ROWS / 8; ++i) vs[which][t][sub + 8 * i] = v[i];
                 if (sub == 0) {
-                    s.gate[t] = expf(g);
+                    s.gate[t] = decay(g);
                     s.rate[t] = be;
                     s.kq[t] = c * rk * rq;
                 }

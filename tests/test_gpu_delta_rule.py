@@ -451,3 +451,27 @@ def test_many_heads_streams_graphs_and_timeouts():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(a, out) and torch.equal(first[:R], to[:R])
+
+
+@pytest.mark.parametrize("dtype,step", [(ms.F32, 3000), (ms.F32, 1), (ms.BF16, 3000), (ms.BF16, 1), (ms.BF16, 32)])
+def test_slow_decays_do_not_drift(dtype, step):
+    """Thousands of decays close to 1, in one call, in blocks and token by token: the state is multiplied by each, and the
+    errors of their roundings must not all point the same way.  With beta = 0 it ends as its start times e^(sum of g).  A
+    factor and a product are each off by 2^-25 of a value at most (values in [1/2, 1)) or 2^-24 in all, uniformly, so with a
+    standard deviation of 2^-24 / sqrt(3) a token; six of them after n tokens are allowed."""
+    n = 3000 if step != 32 else 3008
+    dd = ms.DeltaDims(Hk=1, Hv=2, Dk=64, Dv=64, n_slots=1, dtype=dtype)
+    s = make(dd, 1, n, 7)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    s["g"] = -2e-4 * torch.exp(0.5 * torch.randn((n, 2), generator=g, device="cuda"))
+    s["beta"].zero_()
+    start, ws = s["state"].clone(), ms.delta_workspace(dd, 1, step)
+    out = torch.empty((step, 2, 64), device="cuda", dtype=s["q"].dtype)
+    for t in range(0, n, step):
+        ms.block_delta_rule(dd, 1, s["q"][t:t + step], s["k"][t:t + step], s["v"][t:t + step], s["g"][t:t + step],
+                            s["beta"][t:t + step], s["state"], out, ws, state_out=s["state"], qk_eps=1e-6)
+    torch.cuda.synchronize()
+    assert ms.read_device_error(ws) == ms.OK
+    want = start.double() * torch.exp(s["g"].double().sum(0))[None, :, None, None]
+    off = ((s["state"].double() - want).norm(dim=-1) / want.norm(dim=-1)).max()
+    assert off <= 6 * n ** 0.5 * 2.0 ** -24 / 3 ** 0.5, float(off)
