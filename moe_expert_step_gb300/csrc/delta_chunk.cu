@@ -227,8 +227,8 @@ __device__ __forceinline__ void merge_blocks(uint32_t xh, uint32_t xl, uint32_t 
     }
 }
 
-// 2^x of a chunk's decay; close to 1 it multiplies the state in every chunk, and exp2f's errors of one direction add up
-__device__ __forceinline__ float chunk_decay(float x) { return x > -0.25f ? 1.f + expm1f(x * 0.6931471805599453f) : exp2f(x); }
+// 2^x of a chunk's decay
+__device__ __forceinline__ float chunk_decay(float x) { return fabsf(x) < 0.25f ? 1.f + grown(x * 0.6931471805599453f) : exp2f(x); }
 
 // BRIEF: at most 32 tokens a request, whose products are half as many rows and columns
 template <int DK, bool BRIEF>

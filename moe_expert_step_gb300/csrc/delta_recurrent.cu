@@ -59,9 +59,7 @@ struct Staged {
 
 __device__ __forceinline__ float inverse_norm(float ss, float eps) { return eps > 0.f ? 1.0f / sqrtf(ss + eps) : 1.f; }
 
-// e^g.  Decays close to 1 multiply the state hundreds of times, where an error of a whole step in the same direction adds up
-// (expf: 500 tokens of g around -2e-4 leave states 2e-6 off, so 3e-7); below, expf's relative error is what counts.
-__device__ __forceinline__ float decay(float g) { return g > -0.25f ? 1.f + expm1f(g) : expf(g); }
+__device__ __forceinline__ float decay(float g) { return fabsf(g) < 0.25f ? 1.f + grown(g) : expf(g); }
 
 // ONE: a token a request, nothing is staged and each warp forms the token's sums itself
 template <typename T, int DK, bool ONE>
