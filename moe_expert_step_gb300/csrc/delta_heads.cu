@@ -9,6 +9,10 @@
 // are the first launch's tiles: 8 x 8 matrices at constant distances, so that K is an operand both ways and the
 // columns of a lower triangle are operands of 64, 48, 32 and 16 rows without their zeros.
 //
+// MMAs that are in flight together are ordered only among those of one accumulator and one shape.  So products of 64, 48, 32 and
+// 16 tokens have accumulators of their own, which the threads add up, and none is written to columns that another one in flight
+// reads or writes.
+//
 // Bound: the chain, 7200 cycles a chunk.  An MMA with its left operand in tensor memory takes 64 cycles whatever its N, and 40 of
 // the 48 are on the chain (S0 K^T 1050 cycles, U' 1050, the outputs' and the state's 770); the threads' part is 3500 issue
 // slots of a scheduler.  Against the walk of slices of 16 rows with mma.sync (four slices a block; us with both launches, 16 / 32 heads of
@@ -28,11 +32,15 @@ namespace {
 
 constexpr int kDv = 128, kParts = 4, kThreads = kParts * kDv;  // kParts threads share a row of the state
 // Places in tensor memory, 64 columns each (lane = row of the state), and what they hold in the course of a chunk
-constexpr uint32_t kS = 0;    // S0, high parts; e^G S0 Q^T, to which P U' is added
-constexpr uint32_t kL = 64;   // S0, low parts; U'; U' e^(G_C - G), high and low parts (32 columns each)
-constexpr uint32_t kR = 128;  // S0 K^T; R, high and low parts (32 each); U' (32); what is added to the state (DK columns)
-constexpr uint32_t kO = 192;  // S0 Q^T
-constexpr uint32_t kColumns = 256;
+constexpr uint32_t kS = 0;     // S0, high parts; e^G S0 Q^T, to which the products with U' of the first 16 tokens are added
+constexpr uint32_t kL = 64;    // S0, low parts; U' from R of the first 16; U' e^(G_C - G), high and low parts (32 columns each)
+constexpr uint32_t kR = 128;   // S0 K^T; R, high and low parts (32 each); U' (32)
+constexpr uint32_t kO = 192;   // S0 Q^T
+constexpr uint32_t kM = 256;   // (96 columns) U' from R of the later sixteens; P U' with U' of these
+constexpr uint32_t kT = 352;   // (DK columns) what is added to the state
+constexpr uint32_t kColumns = 512;
+// Columns of the products with tokens 16 kt .. 16 kt + 15, kt > 0, which reach the tokens from 16 kt on
+__device__ __forceinline__ constexpr uint32_t later(int kt) { return kM + (kt > 1 ? 48 : 0) + (kt > 2 ? 32 : 0); }
 
 template <int DK>
 struct HeadSmem {
@@ -90,6 +98,45 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
           "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr)
         : "memory");
+}
+
+// The same of two places at once
+__device__ __forceinline__ void tmem_ld16_two(uint32_t a, uint32_t b, float* v, float* w) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%32];\n\ttcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31}, [%33];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(w[0]), "=f"(w[1]),
+          "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]), "=f"(w[6]), "=f"(w[7]), "=f"(w[8]), "=f"(w[9]), "=f"(w[10]),
+          "=f"(w[11]), "=f"(w[12]), "=f"(w[13]), "=f"(w[14]), "=f"(w[15])
+        : "r"(a), "r"(b)
+        : "memory");
+}
+
+// The sums of a product over the sixteens of tokens up to `part`, at the tokens of that sixteen: `first` is where the
+// first sixteen's stands, `lanes` this warp's lanes
+__device__ __forceinline__ void tmem_sum16(uint32_t lanes, uint32_t first, int part, float* v) {
+    float w[16];
+    auto add = [&]() {
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float2 s = tc::add2(make_float2(v[i], v[i + 1]), make_float2(w[i], w[i + 1]));
+            v[i] = s.x, v[i + 1] = s.y;
+        }
+    };
+    if (part == 0) {
+        tmem_ld16(lanes + first, v);
+        return;
+    }
+    tmem_ld16_two(lanes + first + 16 * part, lanes + later(1) + 16 * (part - 1), v, w);
+    add();
+    if (part == 1) return;
+    tmem_ld16(lanes + later(2) + 16 * (part - 2), w);
+    add();
+    if (part == 2) return;
+    tmem_ld16(lanes + later(3), w);
+    add();
 }
 
 template <int DK>
@@ -337,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_heads_kernel(const DeltaArg
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt) {
                     const uint64_t b = plain_desc(x_at + tri(kt, kt), 128, 256), l = plain_desc(x_at + kTri + tri(kt, kt), 128, 256);
-                    const uint32_t idesc = tc::idesc_f16(128, 64 - 16 * kt), d = tmem + kL + 16 * kt;
-                    tc::mma_f16_tmem_a(d, tmem + kR + 8 * kt, b, idesc, kt > 0);
+                    const uint32_t idesc = tc::idesc_f16(128, 64 - 16 * kt), d = tmem + (kt ? later(kt) : kL);
+                    tc::mma_f16_tmem_a(d, tmem + kR + 8 * kt, b, idesc, 0);
                     tc::mma_f16_tmem_a(d, tmem + kR + 32 + 8 * kt, b, idesc, 1);
                     tc::mma_f16_tmem_a(d, tmem + kR + 8 * kt, l, idesc, 1);
                 }
@@ -352,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_heads_kernel(const DeltaArg
             float u[T];
             wait(&sm.done[kNew], c);
             tc::fence_after_sync();
-            tmem_ld16(mine + kL + T * part, u);
+            tmem_sum16(mine, kL, part, u);
             float umost = 0.f, dmost = 0.f;
 #pragma unroll
             for (int t = 0; t < T; t += 4) {
@@ -424,16 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_heads_kernel(const DeltaArg
                 const uint32_t p_at = here(sm.p);
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt)
-                    tc::mma_f16_tmem_a(tmem + kS + 16 * kt, tmem + kR + 8 * kt, plain_desc(p_at + tri(kt, kt), 128, 256),
-                                       tc::idesc_f16(128, 64 - 16 * kt), 1);
+                    tc::mma_f16_tmem_a(tmem + (kt ? later(kt) : kS), tmem + kR + 8 * kt, plain_desc(p_at + tri(kt, kt), 128, 256),
+                                       tc::idesc_f16(128, 64 - 16 * kt), kt == 0);
                 tc::mma_commit(&sm.done[kOutputs]);
-                // (into U's place as well, behind the products that read it)
                 const uint32_t k_at = here(sm.k[c & 1]), idesc = tc::idesc_f16(128, DK) | tc::kIdescTransposeB;
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt) {
                     const uint64_t b = plain_desc(k_at + kt * kRows16, 128, 1024);
-                    tc::mma_f16_tmem_a(tmem + kR, tmem + kL + 8 * kt, b, idesc, kt > 0);
-                    tc::mma_f16_tmem_a(tmem + kR, tmem + kL + 32 + 8 * kt, b, idesc, 1);
+                    tc::mma_f16_tmem_a(tmem + kT, tmem + kL + 8 * kt, b, idesc, kt > 0);
+                    tc::mma_f16_tmem_a(tmem + kT, tmem + kL + 32 + 8 * kt, b, idesc, 1);
                 }
                 tc::mma_commit(&sm.done[kState]);
             }
@@ -443,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_heads_kernel(const DeltaArg
             wait(&sm.done[kOutputs], c);
             tc::fence_after_sync();
             float o[T];
-            tmem_ld16(mine + kS + T * part, o);
+            tmem_sum16(mine, kS, part, o);
             char* op = sm.o + T * part * 2 * kDv + 2 * row;
 #pragma unroll
             for (int t = 0; t < T; t += 4) {
@@ -472,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_heads_kernel(const DeltaArg
 #pragma unroll
             for (int i = 0; i < N; i += 16) {
                 float d[16];
-                tmem_ld16(mine + kR + part * N + i, d);
+                tmem_ld16(mine + kT + part * N + i, d);
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                     const float2 y = tc::fma2(pair_of(S + i + j), make_float2(gamma, gamma), mul2(pair_of(d + j), step));
