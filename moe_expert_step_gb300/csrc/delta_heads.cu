@@ -156,7 +156,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_heads_kernel(const DeltaArg
         sm.abort = 0;
         tc::fence_mbar_init();
     }
-    pdl_trigger();
     pdl_wait();
     const int hv = blockIdx.x % a.Hv, r = longest_first(a, blockIdx.x / a.Hv, &sm.request);
     int tokens, slot;
@@ -172,6 +171,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_heads_kernel(const DeltaArg
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    // The next kernel may start once every block has its tensor memory: one that takes its own before it waits for this
+    // kernel would otherwise keep a block from it for good.
+    pdl_trigger();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     const uint32_t mine = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);  // this warp's lanes
     const int n_chunks = (tokens + C - 1) / C;
