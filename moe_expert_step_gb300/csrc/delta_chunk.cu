@@ -85,6 +85,12 @@ __device__ __forceinline__ float inverse_root(float x) {
     const float y = rsqrtf(x);
     return x < 3e38f ? y * (1.5f - 0.5f * x * y * y) : 0.f;
 }
+// Factor that divides a row by sqrt(|x|^2 + eps), of elements that are `up` times the row's, their squares' sum ss: (ss +
+// eps up^2)^-1/2.  ss is 2^9 at most, so for rows so small that eps up^2 leaves fp32's range eps is all that counts.
+__device__ __forceinline__ float inverse_norm(float ss, float eps, float up) {
+    const float more = eps * up * up;
+    return more < 1e38f ? inverse_root(ss + more) : inverse_root(eps) * inverse(up);
+}
 __device__ __forceinline__ float quad_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaArgs a, c
             ss += __shfl_xor_sync(0xffffffffu, ss, 1);
             ss += __shfl_xor_sync(0xffffffffu, ss, 16);
             if (sub == 0)
-                (which ? sm.cq : sm.ck)[t] = ss == 0.f ? 0.f : a.eps > 0.f ? inverse_root(ss + a.eps * up * up) : inverse(up);
+                (which ? sm.cq : sm.ck)[t] = ss == 0.f ? 0.f : a.eps > 0.f ? inverse_norm(ss, a.eps, up) : inverse(up);
 #pragma unroll
             for (int j = 0; j < PIECES; ++j)
                 *reinterpret_cast<uint4*>((which ? sm.q : sm.k) + in_tile(t, 4 * j + sub)) =
