@@ -588,8 +588,10 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, TT == 1 ? 2 : 1) delta_wal
     const long long tok0 = 1ll * r * a.n, unit0 = 1ll * r * w.chunks;
     const int rows = by_rows(lane), slice_rows = slice_by_rows(lane), tile_rows = tile_by_rows(lane), tile_cols = tile_by_cols(lane);
     // (after a wait that ran out the other waits end at once and no more is fetched: the walk goes on, bounded, over
-    // whatever stands in the tiles, so that nobody is left at a barrier, and the error is recorded)
+    // whatever stands in the tiles, so that nobody is left at a barrier, the error is recorded and no state is stored: the
+    // warps of the states learn at a barrier, which those of the outputs only pass, whether all of the block's waits ended well)
     bool ok = true;
+    constexpr int kBarEnd = 13, kEnd = 3 * W * 32;
     auto wait = [&](uint64_t* bar, int phase) {
         if (tc::mbar_wait(bar, phase & 1, &sm.abort, a.timeout_ns)) return;
         ok = false;
@@ -624,6 +626,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, TT == 1 ? 2 : 1) delta_wal
             wait(&sm.q_full[c % QS], c / QS);
             wait(&sm.given[mine][cb], c >> 1);
             __syncwarp();
+            if (a.state_out && c + 1 == n_chunks) bar_arrive(kBarEnd, kEnd);  // (the last wait is over)
             typename Smem::ForOutputs& s = sm.q[c % QS];
             const uint32_t qr = tc::smem_addr(s.q) + tile_rows, pr = tc::smem_addr(s.p) + rows;
             const float* vec = reinterpret_cast<const float*>(s.p + kTri) + 2 * q4;
@@ -1073,9 +1076,12 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, TT == 1 ? 2 : 1) delta_wal
             for (int i = max(0, issued - NS); i < issued; ++i)
                 tc::mbar_wait(&sm.x_full[i % NS], (i / NS) & 1, &zero, 1000000000ull);
         }
-        return;
     }
     if (!a.state_out) return;
+    if (n_chunks) {
+        tc::named_bar_sync(kBarEnd, kEnd);
+        if (*const_cast<volatile int*>(&sm.abort)) return;
+    }
 #pragma unroll
     for (int t = 0; t < DK / 16; ++t) {
         *reinterpret_cast<float2*>(a.state_out + state0 + 8 * t) = make_float2(S[t][0], S[t][1]);

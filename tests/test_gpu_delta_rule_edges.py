@@ -20,3 +20,35 @@ def test_tiny_keys_and_queries(dtype, n, k_exp, q_exp):
     out, word = call(dd, 2, s, state_out=to, fresh=fresh)
     assert word == ms.OK
     check(dd, 2, s, out, to, fresh=fresh)
+
+
+# (requests, heads of keys, of values, Dk, Dv, tokens): one, two and four slices of 16 rows a block of several chunks, of one
+# short one, and whole heads
+WALKS = [(3, 2, 4, 128, 128, 200), (6, 2, 4, 128, 128, 200), (24, 2, 4, 64, 64, 130), (3, 2, 4, 128, 128, 32),
+         (12, 2, 4, 128, 128, 32), (40, 2, 4, 128, 128, 32), (40, 2, 4, 128, 128, 140)]
+
+
+@pytest.mark.parametrize("R,Hk,Hv,Dk,Dv,n", WALKS)
+def test_a_state_is_left_or_right_after_a_timeout(R, Hk, Hv, Dk, Dv, n):
+    """In place, with waits that run out at once: what a block of the walk did not finish it does not store, so each 16 rows of
+    a state are either what they were or what they should become."""
+    dd = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=R)
+    s = make(dd, R, n, 61)
+    start, ws = s["state"].clone(), ms.delta_workspace(dd, R, n)
+    right = torch.empty_like(start)
+    _, word = call(dd, R, s, ws=ws, state_out=right)
+    assert word == ms.OK
+    for _ in range(5):
+        s["state"].copy_(start)
+        try:
+            ms.set_wait_timeout_ns(0)
+            _, word = call(dd, R, s, ws=ws, state_out=s["state"])
+        finally:
+            ms.set_wait_timeout_ns(2_000_000_000)
+        assert word == ms.ETIMEOUT
+        cut = lambda t: t.view(R, Hv, Dv // 16, 16 * Dk)  # noqa: E731
+        left, done = ((cut(s["state"]) == cut(x)).all(-1) for x in (start, right))
+        assert (left | done).all(), int((~(left | done)).sum())
+    s["state"].copy_(start)
+    _, word = call(dd, R, s, ws=ws, state_out=s["state"])
+    assert word == ms.OK and torch.equal(s["state"], right)
