@@ -130,11 +130,15 @@ class BlockDecoder:
                               self.conf, self.accept, self.n_committed, self.ws, logit_scale=logit_scale)
             rounds += 1
         self.forward(resolved=True)  # the committed tokens' keys and values stay
-        self.kv_len += self.d.P
+        self.advance()
         return rounds
 
     def begin(self) -> None:
         """(The pages of all blocks are dealt out in advance here.)"""
+
+    def advance(self) -> None:
+        """The block's positions count as cached from here on."""
+        self.kv_len += self.d.P
 
     def check(self) -> None:
         for ws in (self.ws, self.kv_ws):
@@ -170,12 +174,23 @@ class HybridDecoder(BlockDecoder):
                          self.kv_ws)
 
     def begin(self) -> None:
+        """Pages and positions for a block of every request; where one of them is refused, those of the others go back."""
         self.plan(torch.full_like(self.kv_len, self.d.P))
+        self.fresh = (self.kv_len == 0).to(torch.uint8)  # requests that begin, whatever their slots' states hold
+        if bool((self.seen != self.kv_len + self.d.P).any()):
+            start = self.kv_len.clone()
+            self.advance()
+            self.plan(start - self.kv_len)
+            self.advance()
+            raise ms.MoeStepError(ms.EINVAL, "decode_block: no pages left for every request's block")
+
+    def advance(self) -> None:
+        self.kv_len.copy_(self.seen)
 
     def end(self) -> None:
         """Every request ends: its pages go back, its slots may be taken by others."""
         self.plan(-self.kv_len)
-        self.kv_len.zero_()
+        self.advance()
 
     def places(self):
         return self.pos, self.seen
@@ -191,7 +206,8 @@ class HybridDecoder(BlockDecoder):
         decay = -M["rate"] * torch.nn.functional.softplus(a.float())
         ms.block_delta_rule(dd, self.R, q.unflatten(1, (dd.Hk, dd.Dk)), k.unflatten(1, (dd.Hk, dd.Dk)),
                             v.unflatten(1, (dd.Hv, dd.Dv)), decay, torch.sigmoid(b.float()), M["state"], self.mixed,
-                            self.delta_ws, state_out=M["state"] if self.resolved else None, scale=dd.Dk ** -0.5, qk_eps=1e-6)
+                            self.delta_ws, state_out=M["state"] if self.resolved else None, fresh=self.fresh,
+                            scale=dd.Dk ** -0.5, qk_eps=1e-6)
         return self.mixed.view(self.T, -1) @ M["Wout"].t()
 
     def check(self) -> None:
