@@ -7,7 +7,7 @@ the LowConfidence commit.  While a block is being resolved its keys and values a
 round, at the same positions; a resolved block is passed once more, so that the cache holds the
 committed tokens', and the next block follows it.
 
-    python examples/block_decoder.py [--fp8-cache] [--requests 2] [--prefix 100] [--blocks 2] [--hybrid]
+    python examples/block_decoder.py [--fp8-cache] [--requests 2] [--blocks 2] [--prefix 100 | --hybrid]
 
 With --hybrid the cache's pages are given out on the GPU as blocks begin (kv_cache_plan), queries and keys carry
 rotary positions (block_rotary), and every second layer has the gated delta rule in the attention's place
@@ -244,11 +244,14 @@ def main() -> None:
     ap = argparse.ArgumentParser()
     ap.add_argument("--fp8-cache", action="store_true")
     ap.add_argument("--requests", type=int, default=2)
-    ap.add_argument("--prefix", type=int, default=100)
+    ap.add_argument("--prefix", type=int, help="cached positions of random keys and values before the first block (100)")
     ap.add_argument("--blocks", type=int, default=2)
     ap.add_argument("--hybrid", action="store_true")
     a = ap.parse_args()
-    m = hybrid(a.requests, a.blocks, a.fp8_cache) if a.hybrid else small(a.requests, a.prefix, a.blocks, a.fp8_cache)
+    if a.hybrid and a.prefix is not None:
+        ap.error("--prefix writes keys and values only: a --hybrid decoder begins without one")
+    prefix = 100 if a.prefix is None else a.prefix
+    m = hybrid(a.requests, a.blocks, a.fp8_cache) if a.hybrid else small(a.requests, prefix, a.blocks, a.fp8_cache)
     for b in range(a.blocks):
         rounds = m.decode_block(logit_scale=8.0)
         m.check()
