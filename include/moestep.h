@@ -292,8 +292,8 @@ typedef struct {
     const int32_t* table;
 } moestep_kv_cache;
 
-/* Bytes of workspace for the three cache calls below with R requests of n_q query
- * tokens each (kv_cache_write and kv_cache_read need only its 512-byte header, for
+/* Bytes of workspace for kv_cache_write, kv_cache_read, block_attention and kv_cache_plan with
+ * R requests of n_q query tokens each (all but block_attention need only its 512-byte header, for
  * the error word, whatever R and n are).  moestep_workspace_init() prepares it. */
 int moestep_kv_workspace_size(const moestep_kv_dims* kd, int R, int n_q, size_t* bytes);
 
@@ -367,7 +367,9 @@ int block_residual_norm(const moestep_dims* dims, int T, const void* y, int y_dt
  *   pos [R][n]: positions kv_len[r] .. of the new tokens, -1 behind them, as kv_cache_write takes them
  *   slots [R][n] (may be NULL): page * dims.page + place in the page of each, -1 behind them
  * Lengths, counts or pages out of range are recorded (MOESTEP_EDEVINPUT) and not followed: such a request
- * is refused, a page out of range enters the table as -1, pages beyond the ring's n_pages are dropped. */
+ * is refused, a page out of range enters the table as -1, pages beyond the ring's n_pages are dropped.
+ *   ws: the 512-byte header of any workspace, initialised: with head_out == head the call counts in it who has read
+ *   the header, and leaves the count at 0 */
 int kv_cache_plan(const moestep_kv_dims* kd, int R, int n, const int32_t* kv_len, const int32_t* n_new, int32_t* ring,
                   const int32_t* head, int32_t* head_out, int32_t* table, int32_t* new_len, int32_t* pos,
                   int32_t* slots, void* ws, size_t ws_bytes, void* stream);

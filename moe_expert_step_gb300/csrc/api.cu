@@ -79,7 +79,7 @@ Layout make_layout(const moestep_dims& d, int R) {
         o = align_up(o + (bytes ? bytes : 1), 256);
         return at;
     };
-    L.hdr = take(256);  // int[0]: error word, int[8..15]: where a wait timed out, int[32..34]: expert work plan
+    L.hdr = take(256);  // int[0]: error word, int[8..15]: where a wait timed out, int[32..34]: expert work plan, int[48]: kv_cache_plan
     // router groups, coreset, commit per request, plan flag (zeroed at the start of every call)
     L.counters_bytes = sizeof(int) * (L.route_groups + 1 + R + 1);
     L.counters = take(L.counters_bytes);

@@ -23,7 +23,7 @@ namespace moestep {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTicket = 64;  // word of the workspace's header that counts the blocks that have read the ring's header
+constexpr int kTicket = 48;  // word of the workspace that counts the blocks that have read the ring's header (no other call's)
 
 struct PlanArgs {
     const int32_t* kv_len;
