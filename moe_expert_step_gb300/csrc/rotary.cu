@@ -5,7 +5,8 @@
 // of the turn's fraction (position 10^6 at one radian a position: 0.06 radians off).  So a
 // frequency is held as its fraction of a turn a position in 64-bit fixed point, 2^64 a turn:
 // position * frequency modulo 2^64 is the fraction of the turn exactly, two integer
-// multiplications, and its upper 32 bits (2^-33 turns off at most) go to sincospif.
+// multiplications.  Its upper 32 bits (2^-32 turns off at most), as a float of half-turns (another 2^-26 turns, 1.6 units of
+// 2^-24 radians), go to sincospif.
 //
 // The kernel is a copy bound by memory.  A thread takes one 16-byte piece of the pairs of one
 // token, computes its sines and cosines once, and turns that piece of several heads with them (four
