@@ -1,8 +1,10 @@
 """block_delta_rule at its edges."""
+import numpy as np
 import pytest
 import torch
 
 import moe_expert_step_gb300 as ms
+from oracle import token_mixer as om
 from tests.test_gpu_delta_rule import call, check, make
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +54,89 @@ def test_a_state_is_left_or_right_after_a_timeout(R, Hk, Hv, Dk, Dv, n):
     s["state"].copy_(start)
     _, word = call(dd, R, s, ws=ws, state_out=s["state"])
     assert word == ms.OK and torch.equal(s["state"], right)
+
+
+@pytest.mark.parametrize("Hk,Hv,Dk,Dv", [(1, 2, 64, 64), (2, 2, 128, 128), (1, 3, 128, 64), (2, 4, 64, 128)])
+@pytest.mark.parametrize("R,n", [(1, 1), (3, 1), (2, 2), (5, 5), (1, 16), (2, 17), (3, 23)])
+def test_tokens_in_bf16_are_held_to_the_bound_of_fp32(Hk, Hv, Dk, Dv, R, n):
+    """Up to 23 tokens a call bf16 goes token by token in fp32: 40 units of 2^-24 a token and the output's own rounding, without
+    the f16 numbers of the chunked form."""
+    dd = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=R)
+    assert ms.delta_workspace_size(dd, R, n) == 512  # (no tiles: not in chunks)
+    s = make(dd, R, n, 40 * n + R, extra=8)
+    to = torch.empty_like(s["state"])
+    out, word = call(dd, R, s, state_out=to, scale=Dk ** -0.5)
+    assert word == ms.OK
+    check(dd, R, s, out, to, scale=Dk ** -0.5, chunks=False)
+
+
+@pytest.mark.parametrize("R,Hk,Hv,Dk,Dv,n", [(1, 1, 2, 64, 64, 4001), (1, 1, 1, 128, 128, 2500), (40, 1, 2, 64, 128, 900)])
+def test_long_calls(R, Hk, Hv, Dk, Dv, n):
+    """Thousands of tokens with decays and rates as they come, against the recurrence token by token.  (The long ones of a
+    ragged batch; many heads of 128 values are walked a head a block.)"""
+    dd = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=R)
+    s = make(dd, R, n, 900 + R, decay=0.5)
+    length = torch.tensor([n - (211 * r) % n for r in range(R)], dtype=torch.int32, device="cuda")
+    to = torch.empty_like(s["state"])
+    out, word = call(dd, R, s, state_out=to, length=length, scale=Dk ** -0.5)
+    assert word == ms.OK
+    one = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=1)
+    for r in range(0, R, 7):
+        part = {k: (v[r:r + 1] if k == "state" else v[r * n:(r + 1) * n]) for k, v in s.items()}
+        check(one, 1, part, out[r * n:(r + 1) * n], to[r:r + 1], length=length[r:r + 1], scale=Dk ** -0.5)
+
+
+@pytest.mark.parametrize("R,Hk,Hv,Dk,Dv,n", [(3, 2, 4, 128, 128, 200), (40, 2, 4, 128, 128, 200), (3, 2, 4, 64, 64, 32)])
+@pytest.mark.parametrize("what", ["q", "k", "v", "g", "beta"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_what_a_non_finite_value_reaches(R, Hk, Hv, Dk, Dv, n, what, value):
+    """In chunks it may reach its head's outputs from the beginning of its chunk of 64 tokens on and its head's state; nothing
+    before that, no other head, no other request."""
+    if what == "g" and value < 0:
+        pytest.skip("a history that is dropped is finite")
+    dd = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=R)
+    s = make(dd, R, n, 17)
+    clean_to, to = torch.empty_like(s["state"]), torch.empty_like(s["state"])
+    clean, word = call(dd, R, s, state_out=clean_to)
+    assert word == ms.OK
+    r, t, head = R // 2, min(n - 1, 70), 1
+    bad = dict(s, **{what: s[what].clone()})
+    bad[what].view(R, n, *s[what].shape[1:])[r, t, head].view(-1)[0] = value
+    out, word = call(dd, R, bad, state_out=to)
+    assert word == ms.OK
+    heads = [head] if what in ("v", "g", "beta") else [2 * head, 2 * head + 1]
+    same = (out == clean).view(R, n, Hv, Dv).all(-1)
+    reached = torch.zeros((R, n, Hv), dtype=torch.bool, device="cuda")
+    reached[r, t // 64 * 64:, heads] = True
+    assert same[~reached].all()
+    states = (to == clean_to).flatten(2).all(-1)
+    reached = torch.zeros((R, Hv), dtype=torch.bool, device="cuda")
+    if what != "q":
+        reached[r, heads] = True
+    assert states[~reached].all()
+    for h in heads:  # and its own token's output shows it
+        assert not out.view(R, n, Hv, Dv)[r, t, h].isfinite().all()
+
+
+@pytest.mark.parametrize("n,start", [(32, 0), (32, 9), (64, 0), (64, 25), (150, 70)])
+def test_a_rule_that_grows_within_its_limit(n, start):
+    """14 tokens of one key with beta |k|^2 = 3: each doubles what the one before wrote, 2^14 in all, just below the limit of
+    the chunked form; the others have beta = 0.  Operands are pairs of f16 numbers, off by 2^-22, and a row of the inverse
+    has entries of alternating signs that add up to 2^14 with the last: at most three roundings of 28 products of the size of
+    the result, 2^-22 * 3 * 28 < 2^-15, and 2^-14 of the state's norm is allowed."""
+    dd = ms.DeltaDims(Hk=1, Hv=1, Dk=64, Dv=64, n_slots=1)
+    s = make(dd, 1, n, 5)
+    s["k"] = torch.full_like(s["k"], 0.25)  # |k|^2 = 4
+    s["beta"] = torch.zeros_like(s["beta"])
+    s["beta"][start:start + 14] = 0.75
+    s["g"] = torch.zeros_like(s["g"])
+    to = torch.empty_like(s["state"])
+    out, word = call(dd, 1, s, state_out=to, qk_eps=0.0)
+    assert word == ms.OK
+    x = {k: v.double().cpu().numpy() for k, v in s.items()}
+    want, S, _ = om.delta_rule(x["q"], x["k"], x["v"], x["g"], x["beta"], x["state"][0], 1.0, 0.0)
+    assert np.linalg.norm(S) > 2.0 ** 13 * np.linalg.norm(x["state"][0]) / 16
+    off = np.linalg.norm(to[0].double().cpu().numpy() - S) / np.linalg.norm(S)
+    assert off <= 2.0 ** -14, off
+    off = np.linalg.norm(out.double().cpu().numpy() - want) / np.linalg.norm(want)
+    assert off <= 2.0 ** -8 + 2.0 ** -11, off
