@@ -467,27 +467,42 @@ def block_residual_norm(d: ModelDims, y, h_in, h_out, x, w_pre=None, w_post=None
 # ------------------------------------------------------------------------------ pages, positions, the delta rule
 
 
+def _device() -> int:
+    """The current device: launches go to it, so a call's tensors have to be there.  (0 before CUDA is up: none are.)"""
+    if _CURRENT is not None:
+        return _CURRENT[0]()
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+
+
+def _here(t, shape, dtype, what: str, device: int) -> None:
+    """t is contiguous, of the shape and type, on the GPU of that index."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _dense(t, shape, dtype, what)
+        raise MoeStepError(EINVAL, f"{what} must be on the current device")
+
+
 def kv_cache_plan(kd: KvDims, R: int, kv_len, n_new, ring, head, head_out, table, new_len, pos, ws, slots=None,
                   stream=None) -> None:
     """Give R requests pages and positions for n_new [R] more tokens each (negative: the last -n_new go): pages from
     the ring of free ones [n_pages] with head [2] = (first, count), or back to it; the tables [R, max_pages] are
     extended, pos [R, n] (-1 behind the new tokens), slots [R, n] and new_len [R] are written.  All int32; see
     kv_cache_plan in moestep.h."""
-    n, i32, requests = pos.shape[-1], _types()["int"], (R,)
-    _dense(kv_len, requests, i32, "kv_cache_plan: kv_len")
-    _dense(n_new, requests, i32, "kv_cache_plan: n_new")
-    _dense(new_len, requests, i32, "kv_cache_plan: new_len")
-    _dense(ring, (kd.n_pages,), i32, "kv_cache_plan: ring")
-    _dense(head, (2,), i32, "kv_cache_plan: head")
-    _dense(head_out, (2,), i32, "kv_cache_plan: head_out")
-    _dense(pos, (R, n), i32, "kv_cache_plan: pos")
+    n, i32, requests, dev = pos.shape[-1], _types()["int"], (R,), _device()
+    _here(kv_len, requests, i32, "kv_cache_plan: kv_len", dev)
+    _here(n_new, requests, i32, "kv_cache_plan: n_new", dev)
+    _here(new_len, requests, i32, "kv_cache_plan: new_len", dev)
+    _here(ring, (kd.n_pages,), i32, "kv_cache_plan: ring", dev)
+    _here(head, (2,), i32, "kv_cache_plan: head", dev)
+    _here(head_out, (2,), i32, "kv_cache_plan: head_out", dev)
+    _here(pos, (R, n), i32, "kv_cache_plan: pos", dev)
     rows = table.shape[0]
-    _dense(table, (rows, kd.max_pages), i32, "kv_cache_plan: table")
+    _here(table, (rows, kd.max_pages), i32, "kv_cache_plan: table", dev)
     if rows < R:
         raise MoeStepError(EINVAL, "kv_cache_plan: table must have a row a request")
     if slots is not None:
-        _dense(slots, (R, n), i32, "kv_cache_plan: slots")
-    _on_gpu(ws, "kv_cache_plan")
+        _here(slots, (R, n), i32, "kv_cache_plan: slots", dev)
+    _on_gpu(ws, "kv_cache_plan", dev)
     rc = lib().kv_cache_plan(kd._c, R, n, kv_len.data_ptr(), n_new.data_ptr(), ring.data_ptr(), head.data_ptr(),
                              head_out.data_ptr(), table.data_ptr(), new_len.data_ptr(), pos.data_ptr(), _p(slots),
                              ws.data_ptr(), ws.numel(), _s(stream))
@@ -495,9 +510,9 @@ def kv_cache_plan(kd: KvDims, R: int, kv_len, n_new, ring, head, head_out, table
         _check(rc, "kv_cache_plan")
 
 
-def _on_gpu(ws, what: str) -> None:
-    if not ws.is_cuda or not ws.is_contiguous() or ws.element_size() != 1:
-        raise MoeStepError(EINVAL, f"{what}: ws must be bytes on the GPU")
+def _on_gpu(ws, what: str, device: int) -> None:
+    if ws.get_device() != device or not ws.is_contiguous() or ws.element_size() != 1:
+        raise MoeStepError(EINVAL, f"{what}: ws must be bytes on the GPU, the current device")
 
 
 def rotary_frequencies(rot: int, base: float, scaling: int = ROTARY_PLAIN, factor: float = 1.0, original: float = 1.0,
@@ -509,6 +524,8 @@ def rotary_frequencies(rot: int, base: float, scaling: int = ROTARY_PLAIN, facto
     if int(rot) != rot or rot <= 0 or rot % 2:
         raise MoeStepError(EINVAL, "rotary_frequencies: rot must be even and positive")
     freq = torch.empty(int(rot) // 2, dtype=torch.int64, device=device)
+    if freq.get_device() != _device():
+        raise MoeStepError(EINVAL, "rotary_frequencies: device must be the current one")
     _check(lib().rotary_frequencies(int(rot), base, scaling, factor, original, low, high, freq.data_ptr(), _s(stream)),
            "rotary_frequencies")
     return freq
@@ -520,22 +537,22 @@ def block_rotary(kd: KvDims, q, k, pos, freq, q_out, k_out, interleaved: bool = 
     rows may be parts of wider rows) by the positions pos [R, n] (negative: the row is left) into q_out, k_out,
     which may be q and k themselves.  freq: of rotary_frequencies; pairs are halves of the rotated part apart, or
     neighbours where interleaved; see block_rotary in moestep.h."""
-    types = _types()
+    types, dev = _types(), _device()
     if pos.dim() != 2 or freq.dim() != 1 or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise MoeStepError(EINVAL, "block_rotary: pos must be [R, n], freq [rot / 2]; q and k come with their outputs")
     R, n = shape = pos.shape
-    _dense(pos, shape, types["int"], "block_rotary: pos")
-    _dense(freq, freq.shape, types["turn"], "block_rotary: freq")
+    _here(pos, shape, types["int"], "block_rotary: pos", dev)
+    _here(freq, freq.shape, types["turn"], "block_rotary: freq", dev)
     act, q_ld, k_ld, qo_ld, ko_ld = types.get(kd.dtype), 0, 0, 0, 0
     qp = kp = qo = ko = None
     if q is not None:
         heads = (R * n, kd.Hq, kd.D)
-        qp, q_ld = q.data_ptr(), _head_rows(q, heads, act, "block_rotary: q")
-        qo, qo_ld = q_out.data_ptr(), _head_rows(q_out, heads, act, "block_rotary: q_out")
+        qp, q_ld = q.data_ptr(), _head_rows(q, heads, act, "block_rotary: q", dev)
+        qo, qo_ld = q_out.data_ptr(), _head_rows(q_out, heads, act, "block_rotary: q_out", dev)
     if k is not None:
         heads = (R * n, kd.Hkv, kd.D)
-        kp, k_ld = k.data_ptr(), _head_rows(k, heads, act, "block_rotary: k")
-        ko, ko_ld = k_out.data_ptr(), _head_rows(k_out, heads, act, "block_rotary: k_out")
+        kp, k_ld = k.data_ptr(), _head_rows(k, heads, act, "block_rotary: k", dev)
+        ko, ko_ld = k_out.data_ptr(), _head_rows(k_out, heads, act, "block_rotary: k_out", dev)
     rc = lib().block_rotary(kd._c, R, n, qp, q_ld, kp, k_ld, pos.data_ptr(), freq.data_ptr(), 2 * freq.shape[0],
                             interleaved, mscale, qo, qo_ld, ko, ko_ld, _s(stream))
     if rc:
@@ -574,10 +591,10 @@ def delta_workspace(dd: DeltaDims, R: int, n: int, device="cuda", stream=None):
     return ws
 
 
-def _head_rows(t, shape, dtype, what: str) -> int:
+def _head_rows(t, shape, dtype, what: str, device: int) -> int:
     """Distance between the rows of t [tokens, heads, D], which may be part of a wider row."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
-        raise MoeStepError(EINVAL, f"{what} must be {list(shape)} in the activations' type, on the GPU")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise MoeStepError(EINVAL, f"{what} must be {list(shape)} in the activations' type, on the GPU, the current device")
     ld, head, one = t.stride()
     if one != 1 or (head != shape[2] and shape[1] > 1):
         raise MoeStepError(EINVAL, f"{what}: heads and their elements must be dense")
@@ -590,29 +607,29 @@ def block_delta_rule(dd: DeltaDims, R: int, q, k, v, g, beta, state, out, ws, st
     parts of wider rows), g (logarithm of the decay) and beta [R * n, Hv] fp32, state [n_slots, Hv, Dv, Dk] fp32 with
     the request's slot [R], out [R * n, Hv, Dv].  state_out: where the new states go (state itself, or None: not
     wanted); length [R]: tokens of each; fresh [R] uint8: begin from nothing; see block_delta_rule in moestep.h."""
-    T, types = q.shape[0], _types()
+    T, types, dev = q.shape[0], _types(), _device()
     n = T // R if R > 0 else 0
     if R * n != T:
         raise MoeStepError(EINVAL, "block_delta_rule: q must have R * n rows")
     act = types.get(dd.dtype) if dd.dtype != FP8 else None
     keys, values, gates = (T, dd.Hk, dd.Dk), (T, dd.Hv, dd.Dv), (T, dd.Hv)
-    q_ld = _head_rows(q, keys, act, "block_delta_rule: q")
-    k_ld = _head_rows(k, keys, act, "block_delta_rule: k")
-    v_ld = _head_rows(v, values, act, "block_delta_rule: v")
+    q_ld = _head_rows(q, keys, act, "block_delta_rule: q", dev)
+    k_ld = _head_rows(k, keys, act, "block_delta_rule: k", dev)
+    v_ld = _head_rows(v, values, act, "block_delta_rule: v", dev)
     f32, pool = types[F32], (dd.n_slots, dd.Hv, dd.Dv, dd.Dk)
-    _dense(g, gates, f32, "block_delta_rule: g")
-    _dense(beta, gates, f32, "block_delta_rule: beta")
-    _dense(state, pool, f32, "block_delta_rule: state")
-    _dense(out, values, act, "block_delta_rule: out")
+    _here(g, gates, f32, "block_delta_rule: g", dev)
+    _here(beta, gates, f32, "block_delta_rule: beta", dev)
+    _here(state, pool, f32, "block_delta_rule: state", dev)
+    _here(out, values, act, "block_delta_rule: out", dev)
     if state_out is not None and state_out is not state:
-        _dense(state_out, pool, f32, "block_delta_rule: state_out")
+        _here(state_out, pool, f32, "block_delta_rule: state_out", dev)
     if slot is not None:
-        _dense(slot, (R,), types["int"], "block_delta_rule: slot")
+        _here(slot, (R,), types["int"], "block_delta_rule: slot", dev)
     if length is not None:
-        _dense(length, (R,), types["int"], "block_delta_rule: length")
+        _here(length, (R,), types["int"], "block_delta_rule: length", dev)
     if fresh is not None:
-        _dense(fresh, (R,), types["byte"], "block_delta_rule: fresh")
-    _on_gpu(ws, "block_delta_rule")
+        _here(fresh, (R,), types["byte"], "block_delta_rule: fresh", dev)
+    _on_gpu(ws, "block_delta_rule", dev)
     rc = lib().block_delta_rule(dd._c, R, n, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, g.data_ptr(),
                                 beta.data_ptr(), _p(length), _p(slot), _p(fresh), state.data_ptr(), _p(state_out), scale,
                                 qk_eps, out.data_ptr(), ws.data_ptr(), ws.numel(), _s(stream))
