@@ -429,7 +429,7 @@ int moestep_delta_workspace_size(const moestep_delta_dims* dd, int R, int n, siz
  *   fresh [R] uint8: non-zero, the request begins with S = 0, whatever its slot holds (NULL: none does)
  *   state [n_slots][Hv][Dv][Dk] fp32 (S transposed); state_out: where the states after the tokens go, in the
  *   same slots; may be state itself, NULL: not wanted (a block that is not resolved yet leaves its history)
- *   out [R*n][Hv][Dv]
+ *   out [R*n][Hv][Dv]; overlaps neither q, k, v nor the states
  * Lengths and slots out of range are recorded (MOESTEP_EDEVINPUT) and the request is skipped.  Sums and states
  * are fp32; results do not depend on timing (but the last bits of a request's may differ between calls of few and of
  * many heads, which are walked in other ways).  A non-finite value may reach every output of its head's request

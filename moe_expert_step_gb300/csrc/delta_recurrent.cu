@@ -290,6 +290,8 @@ extern "C" int block_delta_rule(const moestep_delta_dims* dd, int R, int n, cons
                           static_cast<const void*>(slot)})
         if (reinterpret_cast<uintptr_t>(p) & 3u) return MOESTEP_EALIGN;
     if ((rc = check_kv_ws(ws, ws_bytes, kKvHeader + delta_chunk_bytes(*dd, R, n))) != MOESTEP_OK) return rc;
+    // blocks read all of a head's queries, keys and states while others write theirs
+    if (out == q || out == k || out == state || out == state_out) return MOESTEP_EINVAL;
     int sms = 0;
     if ((rc = device_ok(&sms)) != MOESTEP_OK) return rc;
     const DeltaArgs a{q,         k,         v,     q_ld,   k_ld,   v_ld,          g,     beta,   length, slot,
