@@ -18,8 +18,8 @@
 // (On mma.sync: with few heads the chain counts, and every link of it would pass through tensor memory on tcgen05.  Many heads
 // of 128 values are walked there, in delta_heads.cu.)
 //
-// 8192 tokens of 16 and 32 heads of 128: 60 and 290 us (350 together; 206 MB that have to be moved, 30 us); 8 requests of up
-// to 4096 tokens: 140 and 294 us (517 MB, 76 us).
+// 8192 tokens of 16 and 32 heads of 128: 60 and 296 us (354 together; 206 MB that have to be moved, 30 us); 8 requests of up
+// to 4096 tokens: 140 and 300 us (517 MB, 76 us).
 //
 // Accuracy.  States and sums are fp32.  An fp32 operand enters as the sum of two f16 numbers after a power of two that
 // brings its row's largest element to 2^12: 22 bits, and 2^-37 of the row's largest for small elements.  Queries and
@@ -80,7 +80,7 @@ __device__ __forceinline__ void mma_(float (&d)[4], const uint32_t (&a)[4], uint
 }
 __device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
-// x^-1/2, rsqrtf and a step of Newton's iteration (the compiler's 1 / sqrtf takes two subroutines)
+// x^-1/2, rsqrtf and a step of Newton's iteration (1 / sqrtf in its place: 16 blocks of 32 tokens 43.9 -> 44.2 us)
 __device__ __forceinline__ float inverse_root(float x) {
     const float y = rsqrtf(x);
     return x < 3e38f ? y * (1.5f - 0.5f * x * y * y) : 0.f;
@@ -118,7 +118,7 @@ __device__ __forceinline__ int tile_by_cols(int lane) { return in_tile((lane >> 
 // a thread; then blocks of 32 and of 64 from X_BA = -X_B A_BA X_A, on tensor cores with operands of two f16
 // numbers.  Computed transposed, (X_A^T A_BA^T) X_B^T, the first product is the second one's A operand in place.
 // (64 steps of elimination in registers, unrolled, ran at the speed of their instruction fetches: 208 us for 8192 tokens
-// of 32 heads; in loops of 16 rows 150 us; by blocks 91 us, now 55 us.)
+// of 32 heads; in loops of 16 rows 150 us; by blocks 91 us, now 60 us.)
 template <int DK>
 struct PrepSmem {
     union {
@@ -1118,8 +1118,8 @@ cudaError_t launch_chunks(const DeltaArgs& a, const Scratch& w, int sms, cudaStr
     // As few slices a block as leave no multiprocessor a second block (blocks of more share their tiles, but also the chain
     // of a chunk gets longer).  us for 1000 tokens with 1 / 2 / 4 slices a block: 128 slices 41 / 48 / 65, 256 slices
     // 73 / 52 / 68, 384 slices of 500 tokens 59 / 51 / 40.  Where four fill the multiprocessors more than once and there is more
-    // than one chunk, whole heads on tcgen05 are faster (1000 tokens, 512 slices 89 against 76, 768 slices 100 : 140, 1024
-    // slices 104 : 145).
+    // than one chunk, whole heads on tcgen05 are faster (1000 tokens, 512 slices 91 against 76, 768 slices 100 : 140, 1024
+    // slices 105 : 145).
     const long long slices = 1ll * a.R * a.Hv * (a.Dv / 16);
     // One chunk in halves of 16 tokens leaves room for two blocks a multiprocessor (us for 32 tokens with 1 / 2 / 4 slices a
     // block: 256 slices 11.4 / 11.5 / 12.4, 512 slices 14.0 / 13.1 / 15.0, 1024 slices 21.6 / 18.9 / 16.6).

@@ -13,13 +13,13 @@
 // 16 tokens have accumulators of their own, which the threads add up, and none is written to columns that another one in flight
 // reads or writes.
 //
-// Bound: the chain, 7200 cycles a chunk.  An MMA with its left operand in tensor memory takes 64 cycles whatever its N, and 40 of
+// Bound: the chain, 7350 cycles a chunk.  An MMA with its left operand in tensor memory takes 64 cycles whatever its N, and 40 of
 // the 48 are on the chain (S0 K^T 1050 cycles, U' 1050, the outputs' and the state's 770); the threads' part is 3500 issue
 // slots of a scheduler.  Against the walk of slices of 16 rows with mma.sync (four slices a block; us with both launches, 16 / 32 heads of
-// 128): 4 requests of 1000 tokens 104 : 145, 8 requests 199 : 281, 16 requests 387 : 499, 8 ragged ones of up to 4096 tokens
-// 434 : 569; but 2 requests of 1000 tokens 89 : 76, and with one chunk the same or more (4 requests of 64 tokens 27 : 24).
-// Slower: two threads a row and two blocks a multiprocessor (514), a warp of its own for the MMAs (518, 96 registers a thread
-// spill), accumulators of their own for the low parts, issued by other warps (457).
+// 128): 4 requests of 1000 tokens 105 : 145, 8 requests 200 : 282, 16 requests 390 : 501, 8 ragged ones of up to 4096 tokens
+// 440 : 580; but 2 requests of 1000 tokens 91 : 76, and with one chunk the same or more (4 requests of 64 tokens 26 : 23).
+// Slower (where these took 435): two threads a row and two blocks a multiprocessor (514), a warp of its own for the MMAs (518,
+// 96 registers a thread spill), accumulators of their own for the low parts, issued by other warps (457).
 #include "attn_tc.cuh"
 #include "common.cuh"
 #include "delta_chunk.cuh"

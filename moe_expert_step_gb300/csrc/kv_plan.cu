@@ -11,8 +11,8 @@
 // else any.
 //
 // Bound by latency: header, lengths, sums, ring or table, slots are reads that depend on one another.  One request of 32
-// new tokens takes 7 us on the device and the call of it 8; 256 requests of up to 4096 tokens (8.7 MB of positions and
-// slots, 1.3 us at the copy rate) 8 us.  Divisions by the page size (a shift instead) and a header written by the last
+// new tokens takes 7 us on the device and the call of it 8.6; 256 requests of up to 4096 tokens (8.7 MB of positions and
+// slots, 1.3 us at the copy rate) 8.6 us.  Divisions by the page size (a shift instead) and a header written by the last
 // block only (by any, where it is not updated in place) cost the larger one 3.4 us.
 #include "common.cuh"
 #include "kernels.h"
