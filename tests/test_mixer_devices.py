@@ -42,6 +42,9 @@ class Launched(Exception):
 
 
 class Library:
+    def moestep_error_string(self, code):
+        return b"refused"
+
     def __getattr__(self, name):
         def call(*a):
             raise Launched
