@@ -1076,6 +1076,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps<W>, TT == 1 ? 2 : 1) delta_wal
             for (int i = max(0, issued - NS); i < issued; ++i)
                 tc::mbar_wait(&sm.x_full[i % NS], (i / NS) & 1, &zero, 1000000000ull);
         }
+        __syncwarp();
     }
     if (!a.state_out) return;
     if (n_chunks) {
