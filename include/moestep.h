@@ -434,8 +434,10 @@ int moestep_delta_workspace_size(const moestep_delta_dims* dd, int R, int n, siz
  * are fp32; results do not depend on timing (but the last bits of a request's may differ between calls of few and of
  * many heads, which are walked in other ways).  A non-finite value may reach every output of its head's request
  * from 63 tokens before its own on.  Where beta |k|^2 passes 2 the recurrence has no bound of its own; with MOESTEP_BF16 and
- * n >= 24 what it grows by within 64 tokens has to stay below 2^15.  When a wait runs out (MOESTEP_ETIMEOUT) outputs are
- * unspecified, and each head's state is the new one or was not written, in part by rows. */
+ * n >= 24 what it grows by within 64 tokens has to stay below 2^15, and the new values of a row are off by 2^-22 of
+ * themselves or 2^-37 of the largest of 64 tokens': what is less than 2^-15 of that loses bits, also where a decay drops the
+ * larger.  When a wait runs out (MOESTEP_ETIMEOUT) outputs are unspecified, and each head's state is the new one or was not
+ * written, in part by rows. */
 int block_delta_rule(const moestep_delta_dims* dd, int R, int n, const void* q, long long q_ld, const void* k,
                      long long k_ld, const void* v, long long v_ld, const float* g, const float* beta,
                      const int32_t* length, const int32_t* slot, const uint8_t* fresh, const float* state,

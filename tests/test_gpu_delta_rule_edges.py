@@ -140,3 +140,49 @@ def test_a_rule_that_grows_within_its_limit(n, start):
     assert off <= 2.0 ** -14, off
     off = np.linalg.norm(out.double().cpu().numpy() - want) / np.linalg.norm(want)
     assert off <= 2.0 ** -8 + 2.0 ** -11, off
+
+
+@pytest.mark.parametrize("R,Hk,Hv,Dk,Dv,n", WALKS)
+@pytest.mark.parametrize("larger", ["history", "values"])
+def test_a_history_that_is_dropped_within_a_chunk(R, Hk, Hv, Dk, Dv, n, larger):
+    """A decay of -inf in the middle of 64 tokens (a sequence that ends, another one behind it), the first one's history or
+    values 2^12 times the second one's.  In chunks a row's new values are off by 2^-22 of themselves or 2^-37 of the largest
+    of 64 tokens, here 2^-25 of the second sequence's: within the bound of the norms."""
+    dd = ms.DeltaDims(Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, n_slots=R)
+    s = make(dd, R, n, 71)
+    at = torch.tensor([(r * n + 11 + 5 * r % (n - 20)) for r in range(R)], device="cuda")
+    s["g"][at] = float("-inf")
+    if larger == "history":
+        s["state"] *= 2.0 ** 12
+    else:
+        before = torch.arange(R * n, device="cuda") < at.repeat_interleave(n)
+        s["v"] = torch.where(before[:, None, None], s["v"] * 2.0 ** 12, s["v"])
+    to = torch.empty_like(s["state"])
+    out, word = call(dd, R, s, state_out=to, scale=Dk ** -0.5)
+    assert word == ms.OK
+    check(dd, R, s, out, to, scale=Dk ** -0.5)
+
+
+def test_whole_heads_and_attention_follow_each_other():
+    """Both take tensor memory, and each may start while the other's blocks still run: many in a row give what each gives alone."""
+    R, n, T = 40, 140, 32
+    dd = ms.DeltaDims(Hk=2, Hv=4, Dk=128, Dv=128, n_slots=R)
+    s = make(dd, R, n, 91)
+    kd = ms.KvDims(Hq=16, Hkv=2, D=128, page=64, n_pages=R * 8, max_pages=8)
+    z = lambda *shape: torch.randn(shape, device="cuda").bfloat16()  # noqa: E731
+    table = torch.arange(R * 8, dtype=torch.int32, device="cuda").view(R, 8)
+    cache, q = ms.kv_cache(z(R * 8, 2, 64, 128), z(R * 8, 2, 64, 128), table), z(R * T, 16, 128)
+    seen = torch.randint(T, 513, (R,), device="cuda").to(torch.int32)
+    kv_ws, ws = ms.kv_workspace(kd, R, T), ms.delta_workspace(dd, R, n)
+    want, word = call(dd, R, s, ws=ws)
+    assert word == ms.OK
+    att = torch.empty_like(q)
+    ms.block_attention(kd, R, q, seen, cache, att, kv_ws, 128 ** -0.5)
+    torch.cuda.synchronize()
+    outs = [(torch.zeros_like(want), torch.zeros_like(att)) for _ in range(30)]
+    for o, a in outs:
+        ms.block_delta_rule(dd, R, s["q"], s["k"], s["v"], s["g"], s["beta"], s["state"], o, ws, qk_eps=1e-6)
+        ms.block_attention(kd, R, q, seen, cache, a, kv_ws, 128 ** -0.5)
+    torch.cuda.synchronize()
+    assert ms.read_device_error(ws) == ms.OK and ms.read_device_error(kv_ws) == ms.OK
+    assert all(torch.equal(o, want) and torch.equal(a, att) for o, a in outs)
